@@ -572,7 +572,7 @@ def _own(s):
     if op == "fork":
         kda.kda_cache_free(s["dst"], s["table"], s["lens"], s["refs"])
         kda.kda_cache_fork(s["src"], s["dst"], s["k_cache"], s["v_cache"], s["table"], s["lens"], s["refs"])
-        kda.kda_cache_reserve(s["dst"], s["new_lens"], s["case"]["page"], s["table"], s["refs"])
+        kda.kda_cache_reserve(s["dst"], s["new_lens"], s["case"]["page"], s["table"], s["lens"], s["refs"])
         return {"table": s["table"], "lens": s["lens"], "refs": s["refs"], "k_cache": s["k_cache"],
                 "v_cache": s["v_cache"]}
     s["table"].copy_(s["table0"])
