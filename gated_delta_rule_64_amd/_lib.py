@@ -55,6 +55,27 @@ class KernelTime(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 48), ("launches", ctypes.c_int64), ("total_ms", ctypes.c_double)]
 
 
+_f32 = ctypes.c_float
+_POOLS = [_vp, _vp, _i32, _i32]  # k_cache, v_cache, num_pages, page_size
+_TABLE = [_vp, _i32, _i32]       # page_table, slots, max_pages
+_WORK = [_vp, _sz, _vp]          # workspace, its bytes, stream
+PROTOTYPES.update({
+    "kda_attn_prefill": (ctypes.c_int, [_i64, _i32, _i32, _i32, _i32, _vp, _i32, _i32, _f32] + [_vp] * 6 + [_vp]),
+    "kda_attn_backward_workspace_bytes": (_sz, [_i64] + [_i32] * 7),
+    "kda_attn_prefill_backward": (ctypes.c_int, [_i64, _i32, _i32, _i32, _i32, _vp, _i32, _i32, _f32] + [_vp] * 11 + _WORK),
+    "kda_attn_tree_workspace_bytes": (_sz, [_i32] * 7 + [_i64]),
+    "kda_attn_tree": (ctypes.c_int, [_i32] * 7 + [_f32] + [_vp] * 5 + _POOLS + _TABLE + [_vp] * 4 + _WORK),
+    "kda_cache_append": (ctypes.c_int, [_i64, _i32, _vp, _i64, _vp] + [_i32] * 4 + [_vp, _vp] + _POOLS + _TABLE +
+                         [_vp, _vp, _vp]),
+    "kda_cache_workspace_bytes": (_sz, [_i32] * 3),
+    "kda_cache_free": (ctypes.c_int, [_i32, _vp, _i32] + _TABLE + [_vp, _vp, _vp]),
+    "kda_cache_fork": (ctypes.c_int, [_i32, _vp, _vp] + [_i32] * 4 + _POOLS + _TABLE + [_vp] * 3 + _WORK),
+    "kda_cache_reserve": (ctypes.c_int, [_i32, _vp, _vp, _i32, _i32] + _TABLE + [_vp] * 3 + _WORK),
+    "kda_cache_compact": (ctypes.c_int, [_i32] * 4 + _POOLS + _TABLE + [_vp, _vp] + _WORK),
+    "kda_cache_copy": (ctypes.c_int, [_vp, _i64, _i32, _vp, _vp, _i32, _vp]),
+})
+
+
 PROTOTYPES["kda_profile_enable"] = (ctypes.c_int, [ctypes.c_int])
 PROTOTYPES["kda_profile_collect"] = (ctypes.c_int, [ctypes.POINTER(KernelTime), ctypes.c_int])
 PROTOTYPES["kda_probe_peak"] = (ctypes.c_int, [_i32, _i32, _i32, _vp, _i64, _vp, _vp])

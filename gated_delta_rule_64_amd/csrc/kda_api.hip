@@ -1,10 +1,13 @@
 // C ABI of libkda: argument validation, status codes and dispatch to the
 // kernels.  See include/kda.h for the contract of every entry point.
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
+#include <new>
 #include <vector>
 
 #include "kda.h"
@@ -34,22 +37,24 @@ int hip_fail(hipError_t e, const char* what) {
 bool valid_head_dim(int32_t d) { return d == 16 || d == 32 || d == 64 || d == 128; }
 bool valid_dtype(int32_t t) { return t == KDA_F32 || t == KDA_BF16; }
 size_t dsize(int32_t t) { return t == KDA_BF16 ? 2 : 4; }
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 struct Span {
     const char* name;
     const void* p;
     size_t bytes;
     bool writes;
+    size_t align = 16;
 };
 
 // Rejects NULL/misaligned pointers and any overlap that involves a written
 // buffer (read-only inputs may share memory with each other).
-int check_spans(const std::vector<Span>& v) {
+template <typename Spans>
+int check_spans(const Spans& v) {
     for (const Span& s : v) {
         if (s.bytes == 0) continue;
         if (s.p == nullptr) return fail(KDA_ERR_INVALID_ARGUMENT, "%s is NULL", s.name);
-        if (!aligned16(s.p)) return fail(KDA_ERR_INVALID_ARGUMENT, "%s is not 16-byte aligned", s.name);
+        if (reinterpret_cast<uintptr_t>(s.p) % s.align != 0)
+            return fail(KDA_ERR_INVALID_ARGUMENT, "%s is not %zu-byte aligned", s.name, s.align);
     }
     for (size_t i = 0; i < v.size(); ++i) {
         for (size_t j = i + 1; j < v.size(); ++j) {
@@ -657,6 +662,414 @@ int kda_prefill_layer_noalloc(int64_t T_tot, int32_t H, int32_t dk, int32_t dv, 
     return prefill_layer_impl(T_tot, H, dk, dv, cu_seqlens, N, x_dtype, q_in, k_in, v_in, w_q, w_k, w_v, g_alpha,
                               b_beta, conv_state, out_gate, initial_state, final_state, out, ws,
                               static_cast<size_t>(KDA_NOALLOC_SCRATCH_BYTES), stream, nullptr);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------- full attention, its cache
+
+namespace {
+
+// A call's buffers, in place: checking them allocates nothing and cannot throw.
+class SpanList {
+public:
+    SpanList() = default;
+    SpanList(std::initializer_list<Span> l) {
+        for (const Span& s : l) push_back(s);
+    }
+    void push_back(const Span& s) {
+        if (n_ < kMost) v_[n_++] = s;
+    }
+    Span& back() { return v_[n_ - 1]; }
+    const Span& operator[](size_t i) const { return v_[i]; }
+    size_t size() const { return n_; }
+    const Span* begin() const { return v_; }
+    const Span* end() const { return v_ + n_; }
+
+private:
+    static constexpr size_t kMost = 16;  // the longest list below has 13
+    Span v_[kMost];
+    size_t n_ = 0;
+};
+
+// Sizes and types that the attention calls share.
+int check_heads(int32_t H, int32_t Hkv, int32_t dk, int32_t dv, int32_t x_dtype, float scale) {
+    if (!valid_dtype(x_dtype)) return fail(KDA_ERR_INVALID_ARGUMENT, "x_dtype=%d is not KDA_F32 or KDA_BF16", x_dtype);
+    if (H < 1 || H > 65535) return fail(KDA_ERR_INVALID_ARGUMENT, "H=%d out of range [1, 65535]", H);
+    if (Hkv < 1 || H % Hkv != 0) return fail(KDA_ERR_INVALID_ARGUMENT, "Hkv=%d does not divide H=%d", Hkv, H);
+    if (!kda::attn_head_sizes(dk, dv))
+        return fail(KDA_ERR_UNSUPPORTED, "dk=%d, dv=%d: attention takes dk = dv = 16, 32, 64, 128 or dk = 192, dv = 128", dk, dv);
+    if (static_cast<int64_t>(H) * dk * static_cast<int64_t>(dsize(x_dtype)) >= (1 << 25))
+        return fail(KDA_ERR_UNSUPPORTED, "H=%d, dk=%d: a token's row of %zu bytes is not below 2^25", H, dk, H * dk * dsize(x_dtype));
+    if (!(scale > 0.f) || !(scale < INFINITY)) return fail(KDA_ERR_INVALID_ARGUMENT, "scale=%g is not positive and finite", static_cast<double>(scale));
+    return KDA_OK;
+}
+
+int check_packed(int64_t T, int32_t N, const int32_t* cu, int64_t per_tile) {
+    if (T < 0 || T >= (int64_t(1) << 31)) return fail(KDA_ERR_INVALID_ARGUMENT, "T_tot=%lld out of range [0, 2^31)", (long long)T);
+    if (N < 1) return fail(KDA_ERR_INVALID_ARGUMENT, "N=%d must be >= 1", N);
+    if (cu == nullptr && N != 1) return fail(KDA_ERR_INVALID_ARGUMENT, "cu_seqlens is NULL but N=%d", N);
+    if (kda::attn_tiles(T, N, 128) * per_tile >= (int64_t(1) << 31) || T * per_tile / 16 >= (int64_t(1) << 31))
+        return fail(KDA_ERR_UNSUPPORTED, "T_tot=%lld, N=%d, H=%lld: more than 2^31 workgroups", (long long)T, N, (long long)per_tile);
+    return KDA_OK;
+}
+
+// As debug_check_cu, for the calls that let the last sequence end before T.
+int debug_check_cu_within(const int32_t* cu, int32_t N, int64_t T, hipStream_t s) try {
+    const char* env = getenv("KDA_DEBUG_CHECK");
+    if (cu == nullptr || env == nullptr || strcmp(env, "1") != 0) return KDA_OK;
+    int32_t last = 0;
+    hipError_t e = hipMemcpyAsync(&last, cu + N, 4, hipMemcpyDeviceToHost, s);
+    if (e == hipSuccess) e = hipStreamSynchronize(s);
+    if (e != hipSuccess) return hip_fail(e, "copy of cu_seqlens for KDA_DEBUG_CHECK");
+    if (last > T) return fail(KDA_ERR_INVALID_ARGUMENT, "cu_seqlens[N]=%d is above T_tot=%lld", last, (long long)T);
+    return debug_check_cu(cu, N, last, s);
+} catch (const std::bad_alloc&) {
+    return fail(KDA_ERR_INVALID_ARGUMENT, "no host memory for KDA_DEBUG_CHECK of %d sequences", N);
+}
+
+// The cache's sizes, shared by the calls that take one.  token_sizes: the
+// call also needs its heads and type.
+int check_cache(int32_t num_pages, int32_t page_size, int32_t slots, int32_t max_pages, int& shift) {
+    if (num_pages < 1 || num_pages >= (1 << 24)) return fail(KDA_ERR_INVALID_ARGUMENT, "num_pages=%d out of range [1, 2^24)", num_pages);
+    shift = 0;
+    while ((1 << shift) < page_size && shift < 11) ++shift;
+    if (page_size < 16 || page_size > 1024 || (1 << shift) != page_size)
+        return fail(KDA_ERR_UNSUPPORTED, "page_size=%d is not a power of two in [16, 1024]", page_size);
+    if (slots < 0) return fail(KDA_ERR_INVALID_ARGUMENT, "slots=%d is negative", slots);
+    if (max_pages < 1 || max_pages >= (1 << 24)) return fail(KDA_ERR_INVALID_ARGUMENT, "max_pages=%d out of range [1, 2^24)", max_pages);
+    if ((static_cast<int64_t>(max_pages) << shift) >= (int64_t(1) << 31))
+        return fail(KDA_ERR_UNSUPPORTED, "max_pages=%d pages of %d tokens reach 2^31 tokens", max_pages, page_size);
+    return KDA_OK;
+}
+
+// Optional host-side check that no row is written twice, or read and written,
+// by one copy (synchronises the stream).
+int debug_check_copy(const int32_t* src, const int32_t* dst, int32_t n, int32_t rows, hipStream_t s) try {
+    const char* env = getenv("KDA_DEBUG_CHECK");
+    if (env == nullptr || strcmp(env, "1") != 0) return KDA_OK;
+    std::vector<int32_t> hs(static_cast<size_t>(n)), hd(static_cast<size_t>(n));
+    hipError_t e = hipMemcpyAsync(hs.data(), src, hs.size() * 4, hipMemcpyDeviceToHost, s);
+    if (e == hipSuccess) e = hipMemcpyAsync(hd.data(), dst, hd.size() * 4, hipMemcpyDeviceToHost, s);
+    if (e == hipSuccess) e = hipStreamSynchronize(s);
+    if (e != hipSuccess) return hip_fail(e, "copy of the row lists for KDA_DEBUG_CHECK");
+    std::vector<char> written(static_cast<size_t>(rows), 0);
+    auto acts = [&](int32_t i) { return hs[i] >= 0 && hs[i] < rows && hd[i] >= 0 && hd[i] < rows && hs[i] != hd[i]; };
+    for (int32_t i = 0; i < n; ++i) {
+        if (!acts(i)) continue;
+        if (written[hd[i]]) return fail(KDA_ERR_INVALID_ARGUMENT, "dst[%d] = %d is written twice", i, hd[i]);
+        written[hd[i]] = 1;
+    }
+    for (int32_t i = 0; i < n; ++i)
+        if (acts(i) && written[hs[i]]) return fail(KDA_ERR_INVALID_ARGUMENT, "src[%d] = %d is written by the same copy", i, hs[i]);
+    return KDA_OK;
+} catch (const std::bad_alloc&) {
+    return fail(KDA_ERR_INVALID_ARGUMENT, "no host memory for KDA_DEBUG_CHECK of %d rows", rows);
+}
+
+size_t table_bytes(int32_t slots, int32_t max_pages) { return static_cast<size_t>(slots) * max_pages * 4; }
+
+int check_workspace(const char* call, size_t have, size_t need, const void* p, SpanList& sp) {
+    if (have < need) return fail(KDA_ERR_WORKSPACE_TOO_SMALL, "%s: workspace_bytes=%zu < %zu needed", call, have, need);
+    if (need > 0 && (p == nullptr || (reinterpret_cast<uintptr_t>(p) & 255u) != 0))
+        return fail(KDA_ERR_INVALID_ARGUMENT, "workspace is NULL or not 256-byte aligned");
+    sp.push_back({"workspace", p, need, true});
+    return KDA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int kda_attn_prefill(int64_t T_tot, int32_t H, int32_t Hkv, int32_t dk, int32_t dv, const int32_t* cu_seqlens,
+                     int32_t N, int32_t x_dtype, float scale, const void* q, const void* k, const void* v,
+                     const void* out_gate, void* out, float* lse, void* stream) {
+    int st = check_heads(H, Hkv, dk, dv, x_dtype, scale);
+    if (st == KDA_OK) st = check_packed(T_tot, N, cu_seqlens, H);
+    if (st != KDA_OK) return st;
+    const size_t xs = dsize(x_dtype), T = static_cast<size_t>(T_tot);
+    const SpanList sp = {
+        {"q", q, T * H * dk * xs, false}, {"k", k, T * Hkv * dk * xs, false}, {"v", v, T * Hkv * dv * xs, false},
+        {"out_gate", out_gate, out_gate ? T * H * dv * xs : 0, false},
+        {"cu_seqlens", cu_seqlens, cu_seqlens ? (static_cast<size_t>(N) + 1) * 4 : 0, false, 4},
+        {"out", out, T * H * dv * xs, true}, {"lse", lse, lse ? T * H * 4 : 0, true, 4},
+    };
+    st = check_spans(sp);
+    if (st != KDA_OK) return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    st = debug_check_cu_within(cu_seqlens, N, T_tot, s);
+    if (st != KDA_OK) return st;
+    const kda::AttnArgs a{T_tot, H, Hkv, dk, dv, N, cu_seqlens, static_cast<kda::DT>(x_dtype), scale, q, k, v, out_gate, out, lse};
+    const hipError_t e = kda::launch_attn_prefill(a, s);
+    if (e != hipSuccess) return hip_fail(e, "attention prefill launch");
+    return ok();
+}
+
+size_t kda_attn_backward_workspace_bytes(int64_t T_tot, int32_t N, int32_t H, int32_t Hkv, int32_t dk, int32_t dv,
+                                         int32_t x_dtype, int32_t with_gate) {
+    if (T_tot < 0 || T_tot >= (int64_t(1) << 31) || N < 1 || H < 1 || H > 65535 || Hkv < 1 || H % Hkv != 0 ||
+        !kda::attn_head_sizes(dk, dv) || !valid_dtype(x_dtype))
+        return 0;
+    return kda::attn_backward_workspace_bytes(T_tot, N, H, Hkv, dk, dv, static_cast<kda::DT>(x_dtype), with_gate != 0);
+}
+
+int kda_attn_prefill_backward(int64_t T_tot, int32_t H, int32_t Hkv, int32_t dk, int32_t dv,
+                              const int32_t* cu_seqlens, int32_t N, int32_t x_dtype, float scale, const void* q,
+                              const void* k, const void* v, const void* out_gate, const void* out, const float* lse,
+                              const void* dy, void* grad_q, void* grad_k, void* grad_v, void* grad_out_gate,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+    int st = check_heads(H, Hkv, dk, dv, x_dtype, scale);
+    if (st == KDA_OK) st = check_packed(T_tot, N, cu_seqlens, H);
+    if (st != KDA_OK) return st;
+    if ((out_gate != nullptr) != (grad_out_gate != nullptr) && T_tot > 0)
+        return fail(KDA_ERR_INVALID_ARGUMENT, "grad_out_gate is required exactly when out_gate is given");
+    const size_t xs = dsize(x_dtype), T = static_cast<size_t>(T_tot);
+    SpanList sp = {
+        {"q", q, T * H * dk * xs, false}, {"k", k, T * Hkv * dk * xs, false}, {"v", v, T * Hkv * dv * xs, false},
+        {"out_gate", out_gate, out_gate ? T * H * dv * xs : 0, false}, {"out", out, T * H * dv * xs, false},
+        {"lse", lse, T * H * 4, false, 4}, {"dy", dy, T * H * dv * xs, false},
+        {"cu_seqlens", cu_seqlens, cu_seqlens ? (static_cast<size_t>(N) + 1) * 4 : 0, false, 4},
+        {"grad_q", grad_q, T * H * dk * xs, true}, {"grad_k", grad_k, T * Hkv * dk * xs, true},
+        {"grad_v", grad_v, T * Hkv * dv * xs, true}, {"grad_out_gate", grad_out_gate, grad_out_gate ? T * H * dv * xs : 0, true},
+    };
+    st = check_workspace("kda_attn_prefill_backward", workspace_bytes,
+                         kda_attn_backward_workspace_bytes(T_tot, N, H, Hkv, dk, dv, x_dtype, out_gate != nullptr), workspace, sp);
+    if (st == KDA_OK) st = check_spans(sp);
+    if (st != KDA_OK) return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    st = debug_check_cu_within(cu_seqlens, N, T_tot, s);
+    if (st != KDA_OK) return st;
+    kda::AttnBackwardArgs a{};
+    a.f = kda::AttnArgs{T_tot, H, Hkv, dk, dv, N, cu_seqlens, static_cast<kda::DT>(x_dtype), scale, q, k, v, out_gate,
+                        const_cast<void*>(out), const_cast<float*>(lse)};
+    a.dy = dy; a.dq = grad_q; a.dk = grad_k; a.dv = grad_v; a.dz = grad_out_gate; a.ws = workspace;
+    const hipError_t e = kda::launch_attn_prefill_backward(a, s);
+    if (e != hipSuccess) return hip_fail(e, "attention backward launch");
+    return ok();
+}
+
+size_t kda_attn_tree_workspace_bytes(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t dk, int32_t dv,
+                                     int32_t x_dtype, int64_t max_context) {
+    if (B < 0 || T < 0 || T > kda::kTreeMaxTokens || H < 1 || H > 65535 || Hkv < 1 || H % Hkv != 0 || max_context < 0 ||
+        max_context >= (int64_t(1) << 31) || !kda::attn_head_sizes(dk, dv) || !valid_dtype(x_dtype))
+        return 0;
+    return kda::attn_tree_workspace_bytes(B, T, H, Hkv, dk, dv, static_cast<kda::DT>(x_dtype), max_context);
+}
+
+int kda_attn_tree(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t dk, int32_t dv, int32_t x_dtype, float scale,
+                  const void* q, const void* k_new, const void* v_new, const int64_t* tree_mask, const void* out_gate,
+                  const void* k_cache, const void* v_cache, int32_t num_pages, int32_t page_size,
+                  const int32_t* page_table, int32_t slots, int32_t max_pages, const int32_t* lens,
+                  const int32_t* slot_indices, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                  void* stream) {
+    int st = check_heads(H, Hkv, dk, dv, x_dtype, scale);
+    int shift = 0;
+    if (st == KDA_OK) st = check_cache(num_pages, page_size, slots, max_pages, shift);
+    if (st != KDA_OK) return st;
+    if (B < 0) return fail(KDA_ERR_INVALID_ARGUMENT, "B=%d is negative", B);
+    if (T < 0 || T > kda::kTreeMaxTokens) return fail(KDA_ERR_INVALID_ARGUMENT, "T=%d out of range [0, %d]", T, kda::kTreeMaxTokens);
+    if (slot_indices == nullptr && B != slots && B > 0)
+        return fail(KDA_ERR_INVALID_ARGUMENT, "slot_indices is NULL but slots=%d is not B=%d", slots, B);
+    if (static_cast<int64_t>(B) * T * H >= (int64_t(1) << 30))
+        return fail(KDA_ERR_UNSUPPORTED, "B x T x H = %lld rows are not below 2^30", static_cast<long long>(B) * T * H);
+    const size_t xs = dsize(x_dtype), BT = static_cast<size_t>(B) * T;
+    const size_t page = static_cast<size_t>(num_pages) * Hkv * page_size;
+    const bool any = BT > 0;
+    SpanList sp = {
+        {"q", q, BT * H * dk * xs, false}, {"k_new", k_new, BT * Hkv * dk * xs, false}, {"v_new", v_new, BT * Hkv * dv * xs, false},
+        {"tree_mask", tree_mask, tree_mask ? BT * 8 : 0, false, 8}, {"out_gate", out_gate, out_gate ? BT * H * dv * xs : 0, false},
+        {"k_cache", k_cache, any ? page * dk * xs : 0, false}, {"v_cache", v_cache, any ? page * dv * xs : 0, false},
+        {"page_table", page_table, any ? table_bytes(slots, max_pages) : 0, false, 4},
+        {"lens", lens, any ? static_cast<size_t>(slots) * 4 : 0, false, 4},
+        {"slot_indices", slot_indices, slot_indices ? static_cast<size_t>(B) * 4 : 0, false, 4},
+        {"out", out, BT * H * dv * xs, true}, {"lse", lse, lse ? BT * H * 4 : 0, true, 4},
+    };
+    st = check_workspace("kda_attn_tree", workspace_bytes,
+                         kda_attn_tree_workspace_bytes(B, T, H, Hkv, dk, dv, x_dtype, static_cast<int64_t>(max_pages) << shift), workspace, sp);
+    if (st == KDA_OK) st = check_spans(sp);
+    if (st != KDA_OK) return st;
+    kda::TreeArgs a{B, T, H, Hkv, dk, dv, static_cast<kda::DT>(x_dtype), scale, q, k_new, v_new, out_gate, tree_mask,
+                    k_cache, v_cache, num_pages, shift, page_table, slots, max_pages, lens, slot_indices, out, lse, workspace};
+    const hipError_t e = kda::launch_attn_tree(a, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(e, "tree attention launch");
+    return ok();
+}
+
+}  // extern "C"
+
+namespace {
+
+// A call on pools and tables: sizes checked, pools and table in the overlap
+// check (the pools where the call has them).
+int cache_args(int32_t Hkv, int32_t dk, int32_t dv, int32_t x_dtype, void* k_cache, void* v_cache, int32_t num_pages,
+               int32_t page_size, int32_t* page_table, int32_t slots, int32_t max_pages, int32_t* lens, int32_t* refs,
+               SpanList& sp, kda::CacheArgs& a) {
+    int shift = 0;
+    int st = check_cache(num_pages, page_size, slots, max_pages, shift);
+    if (st != KDA_OK) return st;
+    if (Hkv < 1 || Hkv > 65535) return fail(KDA_ERR_INVALID_ARGUMENT, "Hkv=%d out of range [1, 65535]", Hkv);
+    if (!valid_dtype(x_dtype)) return fail(KDA_ERR_INVALID_ARGUMENT, "x_dtype=%d is not KDA_F32 or KDA_BF16", x_dtype);
+    if (!kda::attn_head_sizes(dk, dv))
+        return fail(KDA_ERR_UNSUPPORTED, "dk=%d, dv=%d: attention takes dk = dv = 16, 32, 64, 128 or dk = 192, dv = 128", dk, dv);
+    if (static_cast<int64_t>(Hkv) * dk * static_cast<int64_t>(dsize(x_dtype)) >= (1 << 25))
+        return fail(KDA_ERR_UNSUPPORTED, "Hkv=%d, dk=%d: a token's row of %zu bytes is not below 2^25", Hkv, dk, Hkv * dk * dsize(x_dtype));
+    const size_t rows = static_cast<size_t>(num_pages) * Hkv * page_size;
+    sp.push_back({"k_cache", k_cache, rows * dk * dsize(x_dtype), true});
+    sp.push_back({"v_cache", v_cache, rows * dv * dsize(x_dtype), true});
+    sp.push_back({"page_table", page_table, table_bytes(slots, max_pages), true, 4});
+    a = kda::CacheArgs{Hkv, dk, dv, num_pages, shift, slots, max_pages, static_cast<kda::DT>(x_dtype), k_cache, v_cache, page_table, lens, refs};
+    return KDA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int kda_cache_append(int64_t T_tot, int32_t N, const int32_t* cu_seqlens, int64_t src_rows, const int32_t* rows,
+                     int32_t Hkv, int32_t dk, int32_t dv, int32_t x_dtype, const void* k_new, const void* v_new,
+                     void* k_cache, void* v_cache, int32_t num_pages, int32_t page_size, const int32_t* page_table,
+                     int32_t slots, int32_t max_pages, const int32_t* lens, const int32_t* slot_indices, void* stream) {
+    if (T_tot < 0 || T_tot >= (int64_t(1) << 31)) return fail(KDA_ERR_INVALID_ARGUMENT, "T_tot=%lld out of range [0, 2^31)", (long long)T_tot);
+    if (N < 1) return fail(KDA_ERR_INVALID_ARGUMENT, "N=%d must be >= 1", N);
+    if (cu_seqlens == nullptr && N != 1) return fail(KDA_ERR_INVALID_ARGUMENT, "cu_seqlens is NULL but N=%d", N);
+    if (slot_indices == nullptr && slots < N)
+        return fail(KDA_ERR_INVALID_ARGUMENT, "slot_indices is NULL but slots=%d is below N=%d", slots, N);
+    if (src_rows < 0 || src_rows >= (int64_t(1) << 31)) return fail(KDA_ERR_INVALID_ARGUMENT, "src_rows=%lld out of range [0, 2^31)", (long long)src_rows);
+    if (rows == nullptr && src_rows < T_tot)
+        return fail(KDA_ERR_INVALID_ARGUMENT, "rows is NULL but src_rows=%lld is below T_tot=%lld", (long long)src_rows, (long long)T_tot);
+    SpanList sp;
+    kda::CacheArgs c;
+    int st = cache_args(Hkv, dk, dv, x_dtype, k_cache, v_cache, num_pages, page_size, const_cast<int32_t*>(page_table), slots,
+                        max_pages, const_cast<int32_t*>(lens), nullptr, sp, c);
+    if (st != KDA_OK) return st;
+    if (T_tot == 0) return ok();
+    const size_t xs = dsize(x_dtype);
+    sp.back().writes = false;  // the table is read
+    sp.push_back({"lens", lens, static_cast<size_t>(slots) * 4, false, 4});
+    sp.push_back({"k_new", k_new, static_cast<size_t>(src_rows) * Hkv * dk * xs, false});
+    sp.push_back({"v_new", v_new, static_cast<size_t>(src_rows) * Hkv * dv * xs, false});
+    sp.push_back({"cu_seqlens", cu_seqlens, cu_seqlens ? (static_cast<size_t>(N) + 1) * 4 : 0, false, 4});
+    sp.push_back({"rows", rows, rows ? static_cast<size_t>(T_tot) * 4 : 0, false, 4});
+    sp.push_back({"slot_indices", slot_indices, slot_indices ? static_cast<size_t>(N) * 4 : 0, false, 4});
+    st = check_spans(sp);
+    if (st != KDA_OK) return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    st = debug_check_cu_within(cu_seqlens, N, T_tot, s);
+    if (st != KDA_OK) return st;
+    const hipError_t e = kda::launch_cache_append(c, T_tot, N, cu_seqlens, src_rows, rows, k_new, v_new, slot_indices, s);
+    if (e != hipSuccess) return hip_fail(e, "cache append launch");
+    return ok();
+}
+
+size_t kda_cache_workspace_bytes(int32_t num_pages, int32_t slots, int32_t n) {
+    if (num_pages < 1 || num_pages >= (1 << 24) || slots < 0 || n < 0) return 0;
+    return kda::cache_workspace_bytes(num_pages, slots, n);
+}
+
+int kda_cache_free(int32_t n, const int32_t* slot_list, int32_t num_pages, int32_t* page_table, int32_t slots,
+                   int32_t max_pages, int32_t* lens, int32_t* refs, void* stream) {
+    int shift = 0;
+    int st = check_cache(num_pages, 16, slots, max_pages, shift);
+    if (st != KDA_OK) return st;
+    if (n < 0) return fail(KDA_ERR_INVALID_ARGUMENT, "n=%d is negative", n);
+    if (n == 0) return ok();
+    const SpanList sp = {
+        {"slot_list", slot_list, static_cast<size_t>(n) * 4, false, 4}, {"page_table", page_table, table_bytes(slots, max_pages), true, 4},
+        {"lens", lens, static_cast<size_t>(slots) * 4, true, 4}, {"refs", refs, static_cast<size_t>(num_pages) * 4, true, 4},
+    };
+    st = check_spans(sp);
+    if (st != KDA_OK) return st;
+    kda::CacheArgs c{};
+    c.pages = num_pages; c.slots = slots; c.max_pages = max_pages; c.table = page_table; c.lens = lens; c.refs = refs;
+    const hipError_t e = kda::launch_cache_free(c, n, slot_list, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(e, "cache free launch");
+    return ok();
+}
+
+int kda_cache_fork(int32_t n, const int32_t* src, const int32_t* dst, int32_t Hkv, int32_t dk, int32_t dv,
+                   int32_t x_dtype, void* k_cache, void* v_cache, int32_t num_pages, int32_t page_size,
+                   int32_t* page_table, int32_t slots, int32_t max_pages, int32_t* lens, int32_t* refs,
+                   int32_t* status, void* workspace, size_t workspace_bytes, void* stream) {
+    SpanList sp;
+    kda::CacheArgs c;
+    int st = cache_args(Hkv, dk, dv, x_dtype, k_cache, v_cache, num_pages, page_size, page_table, slots, max_pages, lens, refs, sp, c);
+    if (st != KDA_OK) return st;
+    if (n < 0) return fail(KDA_ERR_INVALID_ARGUMENT, "n=%d is negative", n);
+    if (n == 0) return ok();
+    sp.push_back({"lens", lens, static_cast<size_t>(slots) * 4, true, 4});
+    sp.push_back({"refs", refs, static_cast<size_t>(num_pages) * 4, true, 4});
+    sp.push_back({"src", src, static_cast<size_t>(n) * 4, false, 4});
+    sp.push_back({"dst", dst, static_cast<size_t>(n) * 4, false, 4});
+    sp.push_back({"status", status, status ? static_cast<size_t>(n) * 4 : 0, true, 4});
+    st = check_workspace("kda_cache_fork", workspace_bytes, kda_cache_workspace_bytes(num_pages, slots, n), workspace, sp);
+    if (st == KDA_OK) st = check_spans(sp);
+    if (st != KDA_OK) return st;
+    const hipError_t e = kda::launch_cache_fork(c, n, src, dst, status, workspace, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(e, "cache fork launch");
+    return ok();
+}
+
+int kda_cache_reserve(int32_t n, const int32_t* slot_list, const int32_t* new_lens, int32_t num_pages,
+                      int32_t page_size, int32_t* page_table, int32_t slots, int32_t max_pages, const int32_t* lens,
+                      int32_t* refs, int32_t* status, void* workspace, size_t workspace_bytes, void* stream) {
+    int shift = 0;
+    int st = check_cache(num_pages, page_size, slots, max_pages, shift);
+    if (st != KDA_OK) return st;
+    if (n < 0) return fail(KDA_ERR_INVALID_ARGUMENT, "n=%d is negative", n);
+    if (n == 0) return ok();
+    SpanList sp = {
+        {"slot_list", slot_list, static_cast<size_t>(n) * 4, false, 4}, {"new_lens", new_lens, static_cast<size_t>(n) * 4, false, 4},
+        {"page_table", page_table, table_bytes(slots, max_pages), true, 4}, {"lens", lens, static_cast<size_t>(slots) * 4, false, 4},
+        {"refs", refs, static_cast<size_t>(num_pages) * 4, true, 4}, {"status", status, status ? static_cast<size_t>(n) * 4 : 0, true, 4},
+    };
+    st = check_workspace("kda_cache_reserve", workspace_bytes, kda_cache_workspace_bytes(num_pages, slots, n), workspace, sp);
+    if (st == KDA_OK) st = check_spans(sp);
+    if (st != KDA_OK) return st;
+    kda::CacheArgs c{};
+    c.pages = num_pages; c.page_shift = shift; c.slots = slots; c.max_pages = max_pages;
+    c.table = page_table; c.lens = const_cast<int32_t*>(lens); c.refs = refs;
+    const hipError_t e = kda::launch_cache_reserve(c, n, slot_list, new_lens, status, workspace, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(e, "cache reserve launch");
+    return ok();
+}
+
+int kda_cache_compact(int32_t Hkv, int32_t dk, int32_t dv, int32_t x_dtype, void* k_cache, void* v_cache,
+                      int32_t num_pages, int32_t page_size, int32_t* page_table, int32_t slots, int32_t max_pages,
+                      int32_t* refs, int32_t* live, void* workspace, size_t workspace_bytes, void* stream) {
+    SpanList sp;
+    kda::CacheArgs c;
+    int st = cache_args(Hkv, dk, dv, x_dtype, k_cache, v_cache, num_pages, page_size, page_table, slots, max_pages, nullptr, refs, sp, c);
+    if (st != KDA_OK) return st;
+    sp.push_back({"refs", refs, static_cast<size_t>(num_pages) * 4, true, 4});
+    sp.push_back({"live", live, 4, true, 4});
+    st = check_workspace("kda_cache_compact", workspace_bytes, kda_cache_workspace_bytes(num_pages, slots, 0), workspace, sp);
+    if (st == KDA_OK) st = check_spans(sp);
+    if (st != KDA_OK) return st;
+    const hipError_t e = kda::launch_cache_compact(c, live, workspace, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(e, "cache compact launch");
+    return ok();
+}
+
+int kda_cache_copy(void* pool, int64_t row_bytes, int32_t rows, const int32_t* src, const int32_t* dst, int32_t n,
+                   void* stream) {
+    if (row_bytes < 0 || row_bytes % 16 != 0) return fail(KDA_ERR_INVALID_ARGUMENT, "row_bytes=%lld is not a multiple of 16", (long long)row_bytes);
+    if (rows < 0) return fail(KDA_ERR_INVALID_ARGUMENT, "rows=%d is negative", rows);
+    if (n < 0) return fail(KDA_ERR_INVALID_ARGUMENT, "n=%d is negative", n);
+    if (rows > 0 && row_bytes > (int64_t(1) << 46) / rows)
+        return fail(KDA_ERR_INVALID_ARGUMENT, "row_bytes=%lld x rows=%d is out of range", (long long)row_bytes, rows);
+    if (n == 0 || row_bytes == 0 || rows == 0) return ok();
+    const SpanList sp = {
+        {"pool", pool, static_cast<size_t>(row_bytes) * rows, true}, {"src", src, static_cast<size_t>(n) * 4, false, 4},
+        {"dst", dst, static_cast<size_t>(n) * 4, false, 4},
+    };
+    int st = check_spans(sp);
+    if (st != KDA_OK) return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    st = debug_check_copy(src, dst, n, rows, s);
+    if (st != KDA_OK) return st;
+    const hipError_t e = kda::launch_cache_copy(pool, row_bytes, rows, src, dst, n, s);
+    if (e != hipSuccess) return hip_fail(e, "cache copy launch");
+    return ok();
 }
 
 }  // extern "C"

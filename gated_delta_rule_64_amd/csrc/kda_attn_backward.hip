@@ -1,0 +1,370 @@
+// Gradients of the causal attention of kda_attn_prefill.hip.
+//
+// With do = dy * sigmoid(z), delta_i = sum_c dy_ic y_ic (= do_i . o_i) and
+// P_ij = e^(s_ij - lse_i):
+//   dv_j = sum_i P_ij do_i              dS_ij = scale P_ij (do_i . v_j - delta_i)
+//   dq_i = sum_j dS_ij k_j              dk_j  = sum_i dS_ij q_i
+//   dz   = dy * y * (1 - sigmoid(z))    (y sigmoid'(z) / sigmoid(z); no division)
+// i over the queries of every head that shares the key head.
+//
+// Three kernels: delta, dz and the gated do per row; dk and dv per tile of
+// keys, looping over the queries; dq per tile of queries, looping over the
+// keys.  The scores are formed in both, seven products for five, and in
+// exchange every sum is one workgroup's, in a fixed order: no atomics.
+#include "kda_attn_common.h"
+#include "kda_internal.h"
+#include "kda_profile.h"
+
+namespace kda {
+namespace {
+
+using namespace attn;
+
+constexpr int kThreads = 256;
+constexpr int kRows = 128;  // rows of a workgroup in either kernel, 32 a wave
+
+struct BwdK {
+    int64_t T;
+    int H, Hkv, N;
+    const int32_t* cu;
+    const void *q, *k, *v, *z, *out, *dy;
+    const float* lse;
+    void *dq, *dk, *dv, *dz;
+    float* delta;     // [T, H]
+    void* dog;        // [T, H, dv]: dy * sigmoid(z), or dy itself without a gate
+    float scale;
+};
+
+// One row (token, head) per 16 lanes.
+template <typename T, int DV>
+__global__ __launch_bounds__(kThreads) void attn_bwd_rows_kernel(BwdK a) {
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreads / 16) + (threadIdx.x >> 4);
+    const int c = threadIdx.x & 15;
+    const int64_t tokens = a.cu == nullptr ? a.T : min(static_cast<int64_t>(max(a.cu[a.N], 0)), a.T);
+    const bool there = row < tokens * a.H;  // rows behind the last sequence are left as they are
+    constexpr int kV = 4;
+    float sum = 0.f;
+    if (there) {
+        const int64_t at = row * DV;
+#pragma unroll
+        for (int ch = kV * c; ch < DV; ch += 16 * kV) {
+            float dy[kV], y[kV];
+            ld4(static_cast<const T*>(a.dy) + at + ch, dy);
+            ld4(static_cast<const T*>(a.out) + at + ch, y);
+#pragma unroll
+            for (int e = 0; e < kV; ++e) sum += dy[e] * y[e];
+            if (a.z != nullptr) {
+                float z[kV], g[kV];
+                ld4(static_cast<const T*>(a.z) + at + ch, z);
+#pragma unroll
+                for (int e = 0; e < kV; ++e) {
+                    const float sg = sigmoid_fast(z[e]);
+                    g[e] = dy[e] * sg;
+                    z[e] = dy[e] * y[e] * sigmoid_fast(-z[e]);  // 1 - sigmoid(z) without cancellation
+                }
+                st4(static_cast<T*>(a.dog) + at + ch, g);
+                st4(static_cast<T*>(a.dz) + at + ch, z);
+            }
+        }
+    }
+    sum = row_ror_add<1>(sum);
+    sum = row_ror_add<2>(sum);
+    sum = row_ror_add<4>(sum);
+    sum = row_ror_add<8>(sum);
+    if (there && c == 0) a.delta[row] = sum;
+}
+
+// Writes a transposed 32-column result (register 4 i + e: channel 8 i + 4 half
+// + e of tile `tile`) of this lane's row.
+template <typename T, int D, int kTiles>
+__device__ __forceinline__ void store_rows(T* row, const f32x16 (&acc)[kTiles], float f, int half) {
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+        for (int r4 = 0; r4 < 4; ++r4) {
+            const int ch = 32 * i + 8 * r4 + 4 * half;
+            if (ch >= D) continue;
+            float y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = acc[i][4 * r4 + e] * f;
+            st4(row + ch, y);
+        }
+}
+
+template <typename T, int DK, int DV>
+struct DqSizes {
+    static constexpr int kKeys = sizeof(T) == 4 && DK > 128 ? 32 : 64;
+    static constexpr int kKStride = DK * static_cast<int>(sizeof(T)) + kBothPad;
+    static constexpr int kVStride = DV * static_cast<int>(sizeof(T)) + kRowPad;
+    static constexpr int kLds = kKeys * (kKStride + kVStride) + kTrSlack;
+};
+
+template <typename T, int DK, int DV>
+__global__ __launch_bounds__(kThreads) void attn_bwd_dq_kernel(BwdK a) {
+    using Sz = DqSizes<T, DK, DV>;
+    constexpr int kKeys = Sz::kKeys, kSub = kKeys / 32;
+    constexpr int kQPieces = DK / (2 * Elem<T>::kPer16), kVPieces = DV / (2 * Elem<T>::kPer16);
+    constexpr int kKTiles = (DK + 31) / 32;
+    constexpr int kP = Elem<T>::kPieces;
+    extern __shared__ __align__(16) char smem[];
+    char* sK = smem;
+    char* sV = smem + kKeys * Sz::kKStride;
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int c = lane & 31, half = lane >> 5;
+    const int G = a.H / a.Hkv;
+    const int64_t rank = blockIdx.x / a.H;
+    const int slot = blockIdx.x % a.H;
+    const int kvh = slot % a.Hkv, h = kvh * G + slot / a.Hkv;
+    const Tile t = find_tile<kRows>(a.cu, a.N, a.T, rank);
+    if (!t.there) return;
+    const int q0 = t.level * kRows + wave * 32;
+    const int rows = min(32, t.len - q0);
+
+    const int q_row = a.H * DK * static_cast<int>(sizeof(T)), o_row = a.H * DV * static_cast<int>(sizeof(T));
+    const int k_row = a.Hkv * DK * static_cast<int>(sizeof(T)), v_row = a.Hkv * DV * static_cast<int>(sizeof(T));
+    u32x4 qf[kQPieces], of[kVPieces];
+    {
+        const auto qs = rows_of(static_cast<const T*>(a.q) + h * DK, t.start + q0, q_row, rows);
+        const auto os = rows_of(static_cast<const T*>(a.dog) + h * DV, t.start + q0, o_row, rows);
+#pragma unroll
+        for (int s = 0; s < kQPieces; ++s) qf[s] = buffer_load16(qs, c * q_row + (2 * s + half) * 16);
+#pragma unroll
+        for (int s = 0; s < kVPieces; ++s) of[s] = buffer_load16(os, c * o_row + (2 * s + half) * 16);
+    }
+    const int64_t at = (t.start + q0 + c) * a.H + h;
+    const float lse2 = c < rows ? a.lse[at] * kLog2e : 0.f;
+    const float delta = c < rows ? a.delta[at] : 0.f;
+    const float sc = a.scale * kLog2e;
+
+    f32x16 acc[kKTiles];
+#pragma unroll
+    for (int i = 0; i < kKTiles; ++i) acc[i] = f32x16{};
+    TileCopy<T, kKeys, DK, kBothPad, kThreads> ck;
+    TileCopy<T, kKeys, DV, kRowPad, kThreads> cv;
+    const int last = min(t.level * kRows + kRows, t.len);
+    const T* kbase = static_cast<const T*>(a.k) + kvh * DK;
+    const T* vbase = static_cast<const T*>(a.v) + kvh * DV;
+    auto fetch = [&](int j0) {
+        ck.load(rows_of(kbase, t.start + j0, k_row, min(kKeys, t.len - j0)), k_row, tid);
+        cv.load(rows_of(vbase, t.start + j0, v_row, min(kKeys, t.len - j0)), v_row, tid);
+    };
+    fetch(0);
+    for (int j0 = 0; j0 < last; j0 += kKeys) {
+        __syncthreads();
+        ck.store(sK, tid);
+        cv.store(sV, tid);
+        if (j0 + kKeys < last) fetch(j0 + kKeys);
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < kSub; ++u) {
+            const int k0 = j0 + 32 * u;
+            if (k0 > q0 + 31) break;
+            f32x16 s{}, dp{};
+            const char* krow = sK + (32 * u + c) * Sz::kKStride + half * 16;
+            const char* vrow = sV + (32 * u + c) * Sz::kVStride + half * 16;
+#pragma unroll
+            for (int p = 0; p < kQPieces; ++p) s = mma<T>(*reinterpret_cast<const u32x4*>(krow + p * 32), qf[p], s);
+#pragma unroll
+            for (int p = 0; p < kVPieces; ++p) dp = mma<T>(*reinterpret_cast<const u32x4*>(vrow + p * 32), of[p], dp);
+            const int most = q0 + c - k0 - 4 * half;
+            const bool diagonal = k0 + 31 > q0;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const float p = __builtin_amdgcn_exp2f(fmaf(s[r], sc, -lse2));
+                s[r] = diagonal && 8 * (r / 4) + r % 4 > most ? 0.f : p * (dp[r] - delta);
+            }
+#pragma unroll
+            for (int p = 0; p < kP; ++p) {
+                const u32x4 b = as_operand<T>(s, p);
+#pragma unroll
+                for (int i = 0; i < kKTiles; ++i)
+                    acc[i] = mma<T>(transposed<T, Sz::kKStride>(sK + 32 * u * Sz::kKStride, 32 * i, p, lane), b, acc[i]);
+            }
+        }
+    }
+    if (c < rows) store_rows<T, DK>(static_cast<T*>(a.dq) + at * DK, acc, a.scale, half);
+}
+
+template <typename T, int DK, int DV>
+struct DkvSizes {
+    static constexpr int kQ = 32;  // queries of a step
+    static constexpr int kQStride = DK * static_cast<int>(sizeof(T)) + kBothPad;
+    static constexpr int kOStride = DV * static_cast<int>(sizeof(T)) + kBothPad;
+    static constexpr int kStats = kQ * 2 * 4;  // lse and delta of the step's queries
+    static constexpr int kLds = kQ * (kQStride + kOStride) + kTrSlack + kStats;
+};
+
+template <typename T, int DK, int DV>
+__global__ __launch_bounds__(kThreads) void attn_bwd_dkv_kernel(BwdK a) {
+    using Sz = DkvSizes<T, DK, DV>;
+    constexpr int kQ = Sz::kQ;
+    constexpr int kKPieces = DK / (2 * Elem<T>::kPer16), kVPieces = DV / (2 * Elem<T>::kPer16);
+    constexpr int kKTiles = (DK + 31) / 32, kVTiles = (DV + 31) / 32;
+    constexpr int kP = Elem<T>::kPieces;
+    extern __shared__ __align__(16) char smem[];
+    float* sLse = reinterpret_cast<float*>(smem);
+    float* sDelta = sLse + kQ;
+    char* sQ = smem + Sz::kStats;
+    char* sO = sQ + kQ * Sz::kQStride;
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int c = lane & 31, half = lane >> 5;
+    const int G = a.H / a.Hkv;
+    const int64_t rank = blockIdx.x / a.Hkv;
+    const int kvh = blockIdx.x % a.Hkv;
+    const Tile t = find_tile<kRows>(a.cu, a.N, a.T, rank);
+    if (!t.there) return;
+    // the first keys of a sequence have the most queries: levels from the end
+    const int k_first = (t.tiles - 1 - t.level) * kRows;
+    const int k0 = k_first + wave * 32;
+    const int rows = min(32, t.len - k0);
+
+    const int q_row = a.H * DK * static_cast<int>(sizeof(T)), o_row = a.H * DV * static_cast<int>(sizeof(T));
+    const int k_row = a.Hkv * DK * static_cast<int>(sizeof(T)), v_row = a.Hkv * DV * static_cast<int>(sizeof(T));
+    // bf16: this wave's keys and values stay in registers.  fp32: they would
+    // not fit beside the sums, and each step, whose products take four times
+    // as many cycles per byte, reads them again from the caches.
+    constexpr bool kKeep = sizeof(T) == 2;
+    const auto ks = rows_of(static_cast<const T*>(a.k) + kvh * DK, t.start + k0, k_row, rows);
+    const auto vs = rows_of(static_cast<const T*>(a.v) + kvh * DV, t.start + k0, v_row, rows);
+    const int k_at = c * k_row + half * 16, v_at = c * v_row + half * 16;
+    u32x4 kf[kKeep ? kKPieces : 1], vf[kKeep ? kVPieces : 1];
+    if constexpr (kKeep) {
+#pragma unroll
+        for (int s = 0; s < kKPieces; ++s) kf[s] = buffer_load16(ks, k_at + s * 32);
+#pragma unroll
+        for (int s = 0; s < kVPieces; ++s) vf[s] = buffer_load16(vs, v_at + s * 32);
+    }
+    const float sc = a.scale * kLog2e;
+    f32x16 gk[kKTiles], gv[kVTiles];
+#pragma unroll
+    for (int i = 0; i < kKTiles; ++i) gk[i] = f32x16{};
+#pragma unroll
+    for (int i = 0; i < kVTiles; ++i) gv[i] = f32x16{};
+
+    TileCopy<T, kQ, DK, kBothPad, kThreads> cq;
+    TileCopy<T, kQ, DV, kBothPad, kThreads> co;
+    float stat = 0.f;
+    const int steps = (t.len - k_first + kQ - 1) / kQ;  // per head
+    auto fetch = [&](int n) {
+        const int h = kvh * G + n / steps, i0 = k_first + (n % steps) * kQ;
+        const int here = min(kQ, t.len - i0);
+        cq.load(rows_of(static_cast<const T*>(a.q) + h * DK, t.start + i0, q_row, here), q_row, tid);
+        co.load(rows_of(static_cast<const T*>(a.dog) + h * DV, t.start + i0, o_row, here), o_row, tid);
+        if (tid < 2 * kQ) {
+            // a row behind the sequence's end weighs nothing: e^(s - inf)
+            const int i = tid % kQ;
+            const int64_t at = (t.start + i0 + i) * a.H + h;
+            stat = tid < kQ ? (i < here ? a.lse[at] * kLog2e : INFINITY) : (i < here ? a.delta[at] : 0.f);
+        }
+    };
+    fetch(0);
+    for (int n = 0; n < steps * G; ++n) {
+        __syncthreads();
+        cq.store(sQ, tid);
+        co.store(sO, tid);
+        if (tid < 2 * kQ) sLse[tid] = stat;
+        if (n + 1 < steps * G) fetch(n + 1);
+        __syncthreads();
+        const int i0 = k_first + (n % steps) * kQ;
+        if (i0 + kQ - 1 < k0) continue;  // queries before this wave's keys
+        f32x16 s{}, dp{};
+        const char* qrow = sQ + c * Sz::kQStride + half * 16;
+        const char* orow = sO + c * Sz::kOStride + half * 16;
+#pragma unroll
+        for (int p = 0; p < kKPieces; ++p)
+            s = mma<T>(*reinterpret_cast<const u32x4*>(qrow + p * 32), kKeep ? kf[kKeep ? p : 0] : buffer_load16(ks, k_at + p * 32), s);
+#pragma unroll
+        for (int p = 0; p < kVPieces; ++p)
+            dp = mma<T>(*reinterpret_cast<const u32x4*>(orow + p * 32), kKeep ? vf[kKeep ? p : 0] : buffer_load16(vs, v_at + p * 32), dp);
+        // register r: query i0 + 8 (r / 4) + 4 half + r % 4; key k0 + c
+        const int least = k0 + c - i0 - 4 * half;
+        const bool diagonal = i0 < k0 + 31;
+#pragma unroll
+        for (int r4 = 0; r4 < 4; ++r4) {
+            const f32x4 ls = *reinterpret_cast<const f32x4*>(sLse + 8 * r4 + 4 * half);
+            const f32x4 de = *reinterpret_cast<const f32x4*>(sDelta + 8 * r4 + 4 * half);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int r = 4 * r4 + e;
+                float p = __builtin_amdgcn_exp2f(fmaf(s[r], sc, -ls[e]));
+                if (diagonal && 8 * r4 + e < least) p = 0.f;
+                s[r] = p;
+                dp[r] = p * (dp[r] - de[e]);
+            }
+        }
+#pragma unroll
+        for (int p = 0; p < kP; ++p) {
+            const u32x4 b = as_operand<T>(s, p), d = as_operand<T>(dp, p);
+#pragma unroll
+            for (int i = 0; i < kVTiles; ++i) gv[i] = mma<T>(transposed<T, Sz::kOStride>(sO, 32 * i, p, lane), b, gv[i]);
+#pragma unroll
+            for (int i = 0; i < kKTiles; ++i) gk[i] = mma<T>(transposed<T, Sz::kQStride>(sQ, 32 * i, p, lane), d, gk[i]);
+        }
+    }
+    if (c < rows) {
+        const int64_t at = (t.start + k0 + c) * a.Hkv + kvh;
+        store_rows<T, DK>(static_cast<T*>(a.dk) + at * DK, gk, a.scale, half);
+        store_rows<T, DV>(static_cast<T*>(a.dv) + at * DV, gv, 1.f, half);
+    }
+}
+
+size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+template <typename F>
+hipError_t allow_lds(F fn, int lds) {
+    if (lds <= 64 * 1024) return hipSuccess;
+    return hipFuncSetAttribute(reinterpret_cast<const void*>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+}
+
+template <typename T, int DK, int DV>
+hipError_t launch_bwd(const AttnBackwardArgs& a, hipStream_t s) {
+    const AttnArgs& f = a.f;
+    BwdK k{};
+    k.T = f.T; k.H = f.H; k.Hkv = f.Hkv; k.N = f.N; k.cu = f.cu;
+    k.q = f.q; k.k = f.k; k.v = f.v; k.z = f.z; k.out = f.out; k.dy = a.dy; k.lse = f.lse;
+    k.dq = a.dq; k.dk = a.dk; k.dv = a.dv; k.dz = a.dz; k.scale = f.scale;
+    char* ws = static_cast<char*>(a.ws);
+    k.delta = reinterpret_cast<float*>(ws);
+    ws += up256(static_cast<size_t>(f.T) * f.H * 4);
+    k.dog = f.z != nullptr ? static_cast<void*>(ws) : const_cast<void*>(a.dy);
+    hipError_t e = allow_lds(attn_bwd_dq_kernel<T, DK, DV>, DqSizes<T, DK, DV>::kLds);
+    if (e == hipSuccess) e = allow_lds(attn_bwd_dkv_kernel<T, DK, DV>, DkvSizes<T, DK, DV>::kLds);
+    if (e != hipSuccess) return e;
+    {
+        LaunchTimer timer("attn_bwd_rows", s);
+        const int64_t blocks = (f.T * f.H + kThreads / 16 - 1) / (kThreads / 16);
+        attn_bwd_rows_kernel<T, DV><<<dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, s>>>(k);
+    }
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int64_t tiles = attn_tiles(f.T, f.N, kRows);
+    {
+        LaunchTimer timer("attn_bwd_dkv", s);
+        attn_bwd_dkv_kernel<T, DK, DV><<<dim3(static_cast<unsigned>(tiles * f.Hkv)), dim3(kThreads), DkvSizes<T, DK, DV>::kLds, s>>>(k);
+    }
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    {
+        LaunchTimer timer("attn_bwd_dq", s);
+        attn_bwd_dq_kernel<T, DK, DV><<<dim3(static_cast<unsigned>(tiles * f.H)), dim3(kThreads), DqSizes<T, DK, DV>::kLds, s>>>(k);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+size_t attn_backward_workspace_bytes(int64_t T, int N, int H, int Hkv, int dk, int dv, DT x, bool gate) {
+    const size_t rows = static_cast<size_t>(T) * H;
+    return up256(rows * 4) + (gate ? up256(rows * dv * (x == DT::BF16 ? 2 : 4)) : 0);
+}
+
+hipError_t launch_attn_prefill_backward(const AttnBackwardArgs& a, hipStream_t s) {
+    if (a.f.T == 0) return hipSuccess;
+    return attn_dispatch(a.f.x, a.f.dk, a.f.dv, [&](auto t, auto dk, auto dv) {
+        return launch_bwd<typename decltype(t)::type, decltype(dk)::value, decltype(dv)::value>(a, s);
+    });
+}
+
+}  // namespace kda

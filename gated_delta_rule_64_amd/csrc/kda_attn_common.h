@@ -1,0 +1,270 @@
+// Device-side parts shared by the attention kernels (prefill, its gradients,
+// draft trees): the 32 x 32 matrix-core products for both element types, the
+// ragged tile search and the bounded row loads.
+//
+// Matrix-core layouts used throughout (lane l, half h = l / 32, c = l % 32):
+//   v_mfma_f32_32x32x16_bf16  A: row c, contraction 8 h .. 8 h + 7
+//                             B: column c, contraction 8 h .. 8 h + 7
+//   v_mfma_f32_32x32x2_f32    A: row c, contraction h;  B: column c, contraction h
+//   result (both)             column c, register r holds row 8 (r / 4) + 4 h + r % 4
+// A contraction index may be permuted as long as A and B agree, which is used
+// twice.  First, an operand row is read in 16-byte pieces, piece 2 s + h by
+// the lanes of half h: 8 bf16 (one product) or 4 floats (four products), the
+// same bytes for A and B.  Second, a result becomes the B operand of the next
+// product without leaving its registers: the rows that a lane holds are its
+// contraction indices, and the A operand is read in that order.
+#pragma once
+
+#include "kda_common.h"
+
+namespace kda {
+namespace attn {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kBufferDword3 = 0x00020000;  // raw buffer: byte offsets, reads past the end give 0
+
+// One 16-byte operand piece of A times one of B, added to a 32 x 32 result.
+template <typename T>
+__device__ __forceinline__ f32x16 mma(u32x4 a, u32x4 b, f32x16 c);
+template <>
+__device__ __forceinline__ f32x16 mma<bf16>(u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+template <>
+__device__ __forceinline__ f32x16 mma<float>(u32x4 a, u32x4 b, f32x16 c) {
+    const f32x4 x = __builtin_bit_cast(f32x4, a), y = __builtin_bit_cast(f32x4, b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_32x32x2f32(x[i], y[i], c, 0, 0, 0);
+    return c;
+}
+
+// Sizes that depend on the element type: elements in 16 bytes, and the pieces
+// into which the 32 rows of a result fall when it becomes an operand.
+template <typename T>
+struct Elem {
+    static constexpr int kSize = sizeof(T);
+    static constexpr int kPer16 = 16 / sizeof(T);
+    static constexpr int kPieces = 16 / kPer16;  // bf16: 2 (16 rows each), fp32: 4 (8 rows each)
+};
+
+// Piece p of a 32 x 32 result as a B operand: registers p * kPer16 ..
+template <typename T>
+__device__ __forceinline__ u32x4 as_operand(const f32x16& x, int p);
+template <>
+__device__ __forceinline__ u32x4 as_operand<bf16>(const f32x16& x, int p) {
+    u32x4 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = pack_bf16x2(x[8 * p + 2 * i], x[8 * p + 2 * i + 1]);
+    return r;
+}
+template <>
+__device__ __forceinline__ u32x4 as_operand<float>(const f32x16& x, int p) {
+    u32x4 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = __float_as_uint(x[4 * p + i]);
+    return r;
+}
+
+// The A operand that goes with as_operand(x, p): the transpose of a row-major
+// LDS tile [32 rows][stride elements], its 32 columns from `col` as operand
+// rows, contraction over the tile's rows in the order in which the lane's half
+// holds them (see above).  For bf16 two transposing LDS reads of four rows
+// each: in a group of 16 lanes, lane i names row r0 + (i >> 2) at column
+// col + 4 (i & 3) and receives column col + i of rows r0 .. r0 + 3.
+typedef short tr16_v4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ uint2 lds_read_tr(const char* p) {
+    const tr16_v4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) tr16_v4*)(p));
+    return __builtin_bit_cast(uint2, v);
+}
+template <typename T, int kStride>  // stride in bytes
+__device__ __forceinline__ u32x4 transposed(const char* tile, int col, int p, int lane);
+template <int kStride>
+struct TransposedOf {
+    static __device__ __forceinline__ u32x4 get(const bf16*, const char* tile, int col, int p, int lane) {
+        const int i = lane & 15, h = lane >> 5, g = (lane >> 4) & 1;
+        const char* at = tile + (16 * p + 4 * h + (i >> 2)) * kStride + (col + 16 * g + 4 * (i & 3)) * 2;
+        const uint2 a = lds_read_tr(at), b = lds_read_tr(at + 8 * kStride);
+        return u32x4{a.x, a.y, b.x, b.y};
+    }
+    static __device__ __forceinline__ u32x4 get(const float*, const char* tile, int col, int p, int lane) {
+        const char* at = tile + (8 * p + 4 * (lane >> 5)) * kStride + (col + (lane & 31)) * 4;
+        u32x4 r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = *reinterpret_cast<const uint32_t*>(at + i * kStride);
+        return r;
+    }
+};
+template <typename T, int kStride>
+__device__ __forceinline__ u32x4 transposed(const char* tile, int col, int p, int lane) {
+    return TransposedOf<kStride>::get(static_cast<const T*>(nullptr), tile, col, p, lane);
+}
+
+// Larger of the two halves' values (lanes l and l + 32)
+__device__ __forceinline__ float xor32_max(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+__device__ __forceinline__ u32x4 buffer_load16(__amdgpu_buffer_rsrc_t r, int offset) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, offset, 0, 0));
+}
+
+// A wave-uniform value in scalar registers.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int64_t uniform64(int64_t x) {
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<int>(x));
+    const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<int>(x >> 32));
+    return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+// Rows [first, first + rows) of a row-major matrix as a bounded buffer: reads
+// past the last row give 0, so rows behind a sequence's end (the next
+// sequence's, or memory that is not the tensor's) are never read.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const void* base, int64_t first, int64_t row_bytes, int rows) {
+    const char* p = static_cast<const char*>(base) + first * row_bytes;
+    const int64_t bytes = rows > 0 ? rows * row_bytes : 0;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), 0, static_cast<int>(bytes), kBufferDword3);
+}
+
+// One tile of a packed batch: rows [start + first, start + len) of the tensor
+// from its first row on, `first` a multiple of the tile height.
+struct Tile {
+    int64_t start;  // the sequence's first token
+    int len;        // its tokens
+    int level;      // tiles of the same sequence before this one
+    int tiles;      // tiles of the sequence
+    bool there;
+};
+
+// Sequence n's tokens, whatever cu holds: inside [0, T).
+__device__ __forceinline__ void seq_bounds(const int32_t* cu, int n, int64_t T, int64_t& start, int& len) {
+    if (cu == nullptr) {
+        start = 0;
+        len = static_cast<int>(T);
+        return;
+    }
+    int64_t a = cu[n], b = cu[n + 1];
+    a = a < 0 ? 0 : a > T ? T : a;
+    b = b < a ? a : b > T ? T : b;
+    start = a;
+    len = static_cast<int>(b - a);
+}
+
+__device__ __forceinline__ int wave_sum_int(int x) {
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) x += __shfl_xor(x, o);
+    return uniform(x);
+}
+
+// The rank-th tile of the batch, tiles ordered by falling level (in causal
+// attention a tile's work grows with its level, so the longest start first
+// and the short ones fill the end), sequences in order within a level.  With
+// ge(j) = sum over sequences of max(0, tiles_n - j), the tiles at level j or
+// above, the level is the largest j with ge(j) > rank: a binary search, each
+// step a sum over the sequences by the wave's lanes.  All 64 lanes call it.
+template <int kRows>
+__device__ __forceinline__ Tile find_tile(const int32_t* cu, int N, int64_t T, int64_t rank) {
+    Tile t;
+    const int lane = threadIdx.x & 63;
+    if (N == 1) {
+        seq_bounds(cu, 0, T, t.start, t.len);
+        t.len = uniform(t.len);
+        t.start = uniform64(t.start);
+        t.tiles = (t.len + kRows - 1) / kRows;
+        t.there = rank < t.tiles;
+        t.level = t.there ? t.tiles - 1 - static_cast<int>(rank) : 0;
+        return t;
+    }
+    auto tiles_of = [&](int n) {
+        if (n >= N) return 0;
+        int64_t start;
+        int len;
+        seq_bounds(cu, n, T, start, len);
+        return (len + kRows - 1) / kRows;
+    };
+    const int mine = tiles_of(lane);  // the first 64 sequences stay in a register
+    auto at_least = [&](int j) {      // tiles at level j or above (at most 2^31 / kRows + N)
+        int s = max(0, mine - j);
+        for (int n = 64 + lane; n < N; n += 64) s += max(0, tiles_of(n) - j);
+        return wave_sum_int(s);
+    };
+    t.there = rank < at_least(0);
+    t.start = 0;
+    t.len = t.level = t.tiles = 0;
+    if (!t.there) return t;
+    int lo = 0, hi = 1;  // at_least(lo) > rank
+    while (at_least(hi) > rank) {
+        lo = hi;
+        hi *= 2;
+    }
+    while (hi - lo > 1) {
+        const int mid = lo + (hi - lo) / 2;
+        if (at_least(mid) > rank) lo = mid; else hi = mid;
+    }
+    int left = static_cast<int>(rank) - at_least(lo + 1);  // which of the level's sequences
+    for (int n0 = 0; n0 < N; n0 += 64) {
+        const int tn = n0 == 0 ? mine : tiles_of(n0 + lane);
+        unsigned long long has = __ballot(tn > lo);
+        const int count = __popcll(has);
+        if (left >= count) {
+            left -= count;
+            continue;
+        }
+        for (; left > 0; --left) has &= has - 1;
+        const int n = uniform(n0 + __ffsll(static_cast<long long>(has)) - 1);
+        seq_bounds(cu, n, T, t.start, t.len);
+        t.len = uniform(t.len);
+        t.start = uniform64(t.start);
+        t.level = lo;
+        t.tiles = (t.len + kRows - 1) / kRows;
+        break;
+    }
+    return t;
+}
+
+// Copy of a tile [kRows][kCols] (rows of `row_bytes` in memory, kPad bytes of
+// padding behind each row in LDS) in two steps: load() puts this thread's
+// 16-byte pieces in flight, store() writes them to LDS.
+template <typename T, int kRows, int kCols, int kPad, int kThreads>
+struct TileCopy {
+    static constexpr int kRowPieces = kCols * static_cast<int>(sizeof(T)) / 16;
+    static constexpr int kPieces = kRows * kRowPieces;
+    static constexpr int kEach = (kPieces + kThreads - 1) / kThreads;
+    static constexpr int kStride = kCols * static_cast<int>(sizeof(T)) + kPad;
+    u32x4 r[kEach];
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t src, int row_bytes, int tid) {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int p = tid + i * kThreads;
+            if (kPieces % kThreads == 0 || p < kPieces)
+                r[i] = buffer_load16(src, (p / kRowPieces) * row_bytes + (p % kRowPieces) * 16);
+        }
+    }
+    __device__ __forceinline__ void store(char* dst, int tid) const {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int p = tid + i * kThreads;
+            if (kPieces % kThreads == 0 || p < kPieces)
+                *reinterpret_cast<u32x4*>(dst + (p / kRowPieces) * kStride + (p % kRowPieces) * 16) = r[i];
+        }
+    }
+};
+
+// LDS row padding in bytes.  Rows read as operand pieces (16 bytes a lane, 32
+// rows): 16 bytes, so that neighbouring rows start four banks apart.  Rows
+// read transposed (four rows of 64 bytes at once): such that four rows start
+// 16 banks apart.
+constexpr int kRowPad = 16;
+constexpr int tr_pad(int row_bytes) { return (256 + 64 - row_bytes % 128) % 128; }
+// both ways: a compromise, two rows share a bank in either read
+constexpr int kBothPad = 32;
+// bytes of LDS that a transposed read may touch behind a tile whose rows are
+// shorter than the 32 columns of an operand (the results are not used)
+constexpr int kTrSlack = 64;
+
+}  // namespace attn
+}  // namespace kda

@@ -1,0 +1,197 @@
+// Causal attention over packed prompts, grouped heads, optional output gate.
+//
+//   s_ij = scale q_i . k_j (j <= i, same sequence),  m_i = max_j s_ij,
+//   l_i = sum_j e^(s_ij - m_i),  o_i = (1 / l_i) sum_j e^(s_ij - m_i) v_j,
+//   y_i = o_i * sigmoid(z_i),    lse_i = m_i + log l_i
+//
+// One pass over the keys with the running maximum and sum.  The scores are
+// formed transposed, S^T = K Q^T, so that a lane holds one query's scores (its
+// softmax statistics need one exchange between the wave's halves, no shuffle
+// tree) and P^T is the B operand of O^T += V^T P^T as it stands in registers.
+#include "kda_attn_common.h"
+#include "kda_internal.h"
+#include "kda_profile.h"
+
+namespace kda {
+namespace {
+
+using namespace attn;
+
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+constexpr int kQ = 32 * kWaves;  // query rows of a workgroup, 32 a wave
+
+struct FwdK {
+    int64_t T;
+    int H, Hkv, N;
+    const int32_t* cu;
+    const void *q, *k, *v, *z;
+    void* out;
+    float* lse;
+    float scale;
+};
+
+template <typename T, int DK, int DV>
+struct FwdSizes {
+    static constexpr int kKeys = 64;  // keys of a tile
+    static constexpr int kKStride = DK * static_cast<int>(sizeof(T)) + kRowPad;
+    static constexpr int kVStride = DV * static_cast<int>(sizeof(T)) + tr_pad(DV * sizeof(T));
+    static constexpr int kLds = kKeys * (kKStride + kVStride) + kTrSlack;
+};
+
+template <typename T, int DK, int DV>
+__global__ __launch_bounds__(kThreads) void attn_fwd_kernel(FwdK a) {
+    using Sz = FwdSizes<T, DK, DV>;
+    constexpr int kKeys = Sz::kKeys, kSub = kKeys / 32;
+    constexpr int kQPieces = DK / (2 * Elem<T>::kPer16);  // operand pieces per lane of a query or key row
+    constexpr int kVTiles = (DV + 31) / 32;
+    constexpr int kP = Elem<T>::kPieces;
+    extern __shared__ __align__(16) char smem[];
+    char* sK = smem;
+    char* sV = smem + kKeys * Sz::kKStride;
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int c = lane & 31, half = lane >> 5;
+    const int G = a.H / a.Hkv;
+    const int64_t rank = blockIdx.x / a.H;
+    const int slot = blockIdx.x % a.H;
+    const int kvh = slot % a.Hkv, h = kvh * G + slot / a.Hkv;
+    const Tile t = find_tile<kQ>(a.cu, a.N, a.T, rank);
+    if (!t.there) return;
+    const int q0 = t.level * kQ + wave * 32;  // this wave's first row, in the sequence
+
+    const int q_row = a.H * DK * static_cast<int>(sizeof(T));
+    const int k_row = a.Hkv * DK * static_cast<int>(sizeof(T)), v_row = a.Hkv * DV * static_cast<int>(sizeof(T));
+    u32x4 qf[kQPieces];
+    {
+        const auto src = rows_of(static_cast<const T*>(a.q) + h * DK, t.start + q0, q_row, min(32, t.len - q0));
+#pragma unroll
+        for (int s = 0; s < kQPieces; ++s) qf[s] = buffer_load16(src, c * q_row + (2 * s + half) * 16);
+    }
+
+    const float sc = a.scale * kLog2e;
+    float m = -INFINITY, l = 0.f;  // m in units of raw scores
+    f32x16 acc[kVTiles];
+#pragma unroll
+    for (int i = 0; i < kVTiles; ++i) acc[i] = f32x16{};
+
+    TileCopy<T, kKeys, DK, kRowPad, kThreads> ck;
+    TileCopy<T, kKeys, DV, tr_pad(DV * sizeof(T)), kThreads> cv;
+    const int last = min(t.level * kQ + kQ, t.len);  // keys [0, last) are attended by some row
+    const T* kbase = static_cast<const T*>(a.k) + kvh * DK;
+    const T* vbase = static_cast<const T*>(a.v) + kvh * DV;
+    auto fetch = [&](int j0) {
+        ck.load(rows_of(kbase, t.start + j0, k_row, min(kKeys, t.len - j0)), k_row, tid);
+        cv.load(rows_of(vbase, t.start + j0, v_row, min(kKeys, t.len - j0)), v_row, tid);
+    };
+    fetch(0);
+    for (int j0 = 0; j0 < last; j0 += kKeys) {
+        __syncthreads();  // every wave is done with the tile before
+        ck.store(sK, tid);
+        cv.store(sV, tid);
+        if (j0 + kKeys < last) fetch(j0 + kKeys);
+        __syncthreads();
+        if (j0 > q0 + 31) continue;  // nothing of this tile is attended by this wave's rows
+
+        f32x16 s[kSub];
+#pragma unroll
+        for (int u = 0; u < kSub; ++u) {
+            s[u] = f32x16{};
+            const char* row = sK + (32 * u + c) * Sz::kKStride + half * 16;
+#pragma unroll
+            for (int p = 0; p < kQPieces; ++p)
+                s[u] = mma<T>(*reinterpret_cast<const u32x4*>(row + p * 32), qf[p], s[u]);
+        }
+        if (j0 + kKeys - 1 > q0) {  // the diagonal: keys behind the row's own are not attended
+            const int most = q0 + c - j0 - 4 * half;
+#pragma unroll
+            for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (32 * u + 8 * (r / 4) + r % 4 > most) s[u][r] = -INFINITY;
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int u = 0; u < kSub; ++u)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) top = fmaxf(top, s[u][r]);
+        top = fmaxf(xor32_max(top), m);
+        const float alpha = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - top) * sc);
+        m = top;
+        const float ms = top == -INFINITY ? 0.f : top * sc;
+        float sum = 0.f;
+#pragma unroll
+        for (int u = 0; u < kSub; ++u)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                s[u][r] = __builtin_amdgcn_exp2f(fmaf(s[u][r], sc, -ms));
+                sum += s[u][r];
+            }
+        l = l * alpha + sum;
+#pragma unroll
+        for (int i = 0; i < kVTiles; ++i) acc[i] *= alpha;
+#pragma unroll
+        for (int u = 0; u < kSub; ++u)
+#pragma unroll
+            for (int p = 0; p < kP; ++p) {
+                const u32x4 b = as_operand<T>(s[u], p);
+#pragma unroll
+                for (int i = 0; i < kVTiles; ++i)
+                    acc[i] = mma<T>(transposed<T, Sz::kVStride>(sV + 32 * u * Sz::kVStride, 32 * i, p, lane), b, acc[i]);
+            }
+    }
+
+    // epilogue: lane c's query; registers 4 i .. 4 i + 3 of a tile are four
+    // neighbouring channels
+    const int row = q0 + c;
+    l = xor32_add(l);
+    if (row >= t.len) return;
+    const int64_t at = (t.start + row) * a.H + h;
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    if (a.lse != nullptr && half == 0) a.lse[at] = l > 0.f ? (m * sc + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+    T* out = static_cast<T*>(a.out) + at * DV;
+    const T* z = static_cast<const T*>(a.z) + at * DV;
+#pragma unroll
+    for (int i = 0; i < kVTiles; ++i)
+#pragma unroll
+        for (int r4 = 0; r4 < 4; ++r4) {
+            const int ch = 32 * i + 8 * r4 + 4 * half;
+            if (ch >= DV) continue;
+            float y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = acc[i][4 * r4 + e] * inv;
+            if (a.z != nullptr) {
+                float g[4];
+                ld4(z + ch, g);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] *= sigmoid_fast(g[e]);
+            }
+            st4(out + ch, y);
+        }
+}
+
+template <typename T, int DK, int DV>
+hipError_t launch_fwd(const AttnArgs& a, hipStream_t s) {
+    constexpr int lds = FwdSizes<T, DK, DV>::kLds;
+    static_assert(lds <= 160 * 1024, "one workgroup's LDS");
+    auto fn = attn_fwd_kernel<T, DK, DV>;
+    if (lds > 64 * 1024) {
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+        if (e != hipSuccess) return e;
+    }
+    const FwdK k{a.T, a.H, a.Hkv, a.N, a.cu, a.q, a.k, a.v, a.z, a.out, a.lse, a.scale};
+    LaunchTimer timer("attn_fwd", s);
+    fn<<<dim3(static_cast<unsigned>(attn_tiles(a.T, a.N, kQ) * a.H)), dim3(kThreads), lds, s>>>(k);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_attn_prefill(const AttnArgs& a, hipStream_t s) {
+    if (a.T == 0) return hipSuccess;
+    return attn_dispatch(a.x, a.dk, a.dv, [&](auto t, auto dk, auto dv) {
+        return launch_fwd<typename decltype(t)::type, decltype(dk)::value, decltype(dv)::value>(a, s);
+    });
+}
+
+}  // namespace kda

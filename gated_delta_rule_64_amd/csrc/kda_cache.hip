@@ -1,0 +1,588 @@
+// The pages of an attention cache: rows written into them, sequences forked
+// over them, pages freed, given out, moved together and copied.
+//
+// A page is free when refs[page], the number of table entries that name it,
+// is not positive.  There is no list of free pages: whoever needs some takes
+// the lowest-numbered ones, found by a scan over refs, so that the result
+// does not depend on the order in which workgroups run, and freeing is one
+// atomic subtraction per entry, in any order.
+#include "kda_common.h"
+#include "kda_internal.h"
+#include "kda_profile.h"
+
+namespace kda {
+namespace {
+
+constexpr int kPlan = 1024;  // threads of the planning workgroup
+constexpr int kCopy = 256;   // threads of a copying workgroup
+
+__device__ __forceinline__ bool names_page(int32_t e, int pages) { return e >= 0 && e < pages; }
+
+__device__ __forceinline__ int load_fresh(const int32_t* p) {  // past the vector L1
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void store_fresh(int32_t* p, int32_t v) {
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// Exclusive scan of one value per thread of the planning workgroup; `total`
+// gets the sum.  sums: kPlan / 64 words of LDS.  All threads call it.
+template <typename I>
+__device__ __forceinline__ I block_scan(I x, I* sums, I& total) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    I inc = x;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const I y = __shfl_up(inc, o);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 63) sums[wave] = inc;
+    __syncthreads();
+    I before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kPlan / 64; ++w) {
+        const I s = sums[w];
+        before += w < wave ? s : 0;
+        all += s;
+    }
+    __syncthreads();
+    total = all;
+    return before + inc - x;
+}
+
+// The lowest `want` free pages in order, list[0 .. want); returns how many
+// there are (at most want).  All threads of the planning workgroup call it.
+__device__ __forceinline__ int lowest_free(const int32_t* refs, int pages, int want, int32_t* list, int* sums) {
+    constexpr int kEach = 8;
+    int found = 0;
+    for (int p0 = 0; p0 < pages && found < want; p0 += kPlan * kEach) {
+        const int first = p0 + static_cast<int>(threadIdx.x) * kEach;
+        int r[kEach], mine = 0;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) r[i] = first + i < pages ? refs[first + i] : 1;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) mine += r[i] <= 0;
+        int total;
+        int at = found + block_scan(mine, sums, total);
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+            if (r[i] <= 0) {
+                if (at < want) store_fresh(list + at, first + i);
+                ++at;
+            }
+        found += total;
+    }
+    __threadfence();
+    __syncthreads();
+    return min(found, want);
+}
+
+// Of the entries of a call that name the same slot, the first that is good
+// keeps it.  claim: one word per slot.  Every thread passes its entries.
+template <typename Good>
+__device__ __forceinline__ void claim_slots(const int32_t* slot_of, int n, int32_t* claim, Good good) {
+    for (int i = threadIdx.x; i < n; i += kPlan)
+        if (good(i)) store_fresh(claim + slot_of[i], INT32_MAX);
+    __threadfence();
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kPlan)
+        if (good(i)) atomicMin(claim + slot_of[i], i);
+    __threadfence();
+    __syncthreads();
+}
+
+// ------------------------------------------------------------------- append
+
+struct AppendK {
+    CacheArgs c;
+    int64_t tokens, src_rows;
+    int N;
+    const int32_t *cu, *rows, *slot_indices;
+    const void *k_new, *v_new;
+};
+
+constexpr int kAppendTokens = 8;  // tokens of a workgroup
+
+__global__ __launch_bounds__(kCopy) void cache_append_kernel(AppendK a) {
+    __shared__ int64_t s_src[kAppendTokens], s_dst[kAppendTokens];
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kAppendTokens;
+    const CacheArgs& c = a.c;
+    if (threadIdx.x < kAppendTokens) {
+        const int64_t t = t0 + threadIdx.x;
+        int64_t src = -1, dst = -1;
+        if (t < a.tokens) {
+            int n = 0;
+            int64_t first = 0, end = a.tokens;
+            if (a.cu != nullptr) {
+                n = find_seq(a.cu, a.N, t);
+                first = a.cu[n];
+                end = a.cu[n + 1];
+            }
+            if (t >= first && t < end) {
+                const int slot = a.slot_indices != nullptr ? a.slot_indices[n] : n;
+                src = a.rows != nullptr ? a.rows[t] : t;
+                if (slot >= 0 && slot < c.slots && src >= 0 && src < a.src_rows) {
+                    const int64_t pos = static_cast<int64_t>(max(c.lens[slot], 0)) + (t - first);
+                    const int64_t col = pos >> c.page_shift;
+                    if (col < c.max_pages) {
+                        const int page = c.table[static_cast<int64_t>(slot) * c.max_pages + col];
+                        if (names_page(page, c.pages))
+                            dst = ((static_cast<int64_t>(page) * c.Hkv) << c.page_shift) + (pos & ((1 << c.page_shift) - 1));
+                    }
+                }
+            }
+        }
+        s_src[threadIdx.x] = src;
+        s_dst[threadIdx.x] = dst;  // row of head 0; head h is h << page_shift rows on
+    }
+    __syncthreads();
+    const int e = c.x == DT::BF16 ? 2 : 4;
+    const int k_pieces = c.dk * e / 16, v_pieces = c.dv * e / 16, head = k_pieces + v_pieces;
+    const int per_token = c.Hkv * head;
+    const uint4* kn = static_cast<const uint4*>(a.k_new);
+    const uint4* vn = static_cast<const uint4*>(a.v_new);
+    uint4* kc = static_cast<uint4*>(c.k_cache);
+    uint4* vc = static_cast<uint4*>(c.v_cache);
+    for (int i = threadIdx.x; i < kAppendTokens * per_token; i += kCopy) {
+        const int t = i / per_token, p = i - t * per_token;
+        const int64_t dst = s_dst[t], src = s_src[t];
+        if (dst < 0) continue;
+        const int k_all = c.Hkv * k_pieces;
+        if (p < k_all) {
+            const int h = p / k_pieces, x = p - h * k_pieces;
+            kc[(dst + (static_cast<int64_t>(h) << c.page_shift)) * k_pieces + x] = kn[src * k_all + p];
+        } else {
+            const int y = p - k_all, h = y / v_pieces, x = y - h * v_pieces;
+            vc[(dst + (static_cast<int64_t>(h) << c.page_shift)) * v_pieces + x] = vn[src * (c.Hkv * v_pieces) + y];
+        }
+    }
+}
+
+// --------------------------------------------------------------------- free
+
+__global__ __launch_bounds__(kCopy) void cache_free_kernel(CacheArgs c, const int32_t* slot_list) {
+    const int slot = slot_list[blockIdx.x];
+    if (slot < 0 || slot >= c.slots) return;
+    int32_t* row = c.table + static_cast<int64_t>(slot) * c.max_pages;
+    const int col = blockIdx.y * kCopy + threadIdx.x;
+    // the exchange gives an entry to one workgroup only, also where a slot is
+    // named twice
+    if (col < c.max_pages) {
+        const int page = atomicExch(row + col, -1);
+        if (names_page(page, c.pages)) atomicSub(c.refs + page, 1);
+    }
+    if (col == 0) c.lens[slot] = 0;
+}
+
+// --------------------------------------------------------------------- fork
+
+struct ForkK {
+    CacheArgs c;
+    int n;
+    const int32_t *src, *dst;
+    int32_t* status;
+    int32_t* claim;  // [slots]
+    int32_t* list;   // [n] free pages
+    int32_t* plan;   // [n][2]: source length (-1: refused), the new last page (-1: none needed)
+};
+
+__global__ __launch_bounds__(kPlan) void cache_fork_plan_kernel(ForkK a) {
+    __shared__ int sums[kPlan / 64];
+    const CacheArgs& c = a.c;
+    const int64_t most = static_cast<int64_t>(c.max_pages) << c.page_shift;
+    const int mask = (1 << c.page_shift) - 1;
+    auto good = [&](int i) {  // both slots exist and differ, the destination is empty
+        const int s = a.src[i], d = a.dst[i];
+        return s >= 0 && s < c.slots && d >= 0 && d < c.slots && s != d && c.lens[d] == 0 &&
+               !names_page(c.table[static_cast<int64_t>(d) * c.max_pages], c.pages);
+    };
+    auto length = [&](int i) {
+        const int64_t n = c.lens[a.src[i]];
+        return static_cast<int>(n < 0 ? 0 : n > most ? most : n);
+    };
+    claim_slots(a.dst, a.n, a.claim, good);
+    auto mine = [&](int i) { return i < a.n && good(i) && load_fresh(a.claim + a.dst[i]) == i; };
+    auto needs = [&](int i) {  // a last page that is partly filled
+        const int len = length(i);
+        return (len & mask) != 0 &&
+               names_page(c.table[static_cast<int64_t>(a.src[i]) * c.max_pages + (len >> c.page_shift)], c.pages);
+    };
+    int want = 0;
+    for (int i0 = 0; i0 < a.n; i0 += kPlan) {
+        int total;
+        const int i = i0 + threadIdx.x;
+        block_scan<int>(mine(i) && needs(i), sums, total);
+        want += total;
+    }
+    const int have = lowest_free(c.refs, c.pages, want, a.list, sums);
+    int before = 0;
+    for (int i0 = 0; i0 < a.n; i0 += kPlan) {
+        const int i = i0 + threadIdx.x;
+        const bool ok = mine(i), need = ok && needs(i);
+        int total;
+        const int at = before + block_scan<int>(need, sums, total);
+        before += total;
+        if (i < a.n) {
+            int status = ok ? 0 : 2, page = -1;
+            if (need) {
+                if (at < have) {
+                    page = load_fresh(a.list + at);
+                    c.refs[page] = 1;
+                } else {
+                    status = 1;
+                }
+            }
+            a.plan[2 * i] = status == 0 ? length(i) : -1;
+            a.plan[2 * i + 1] = page;
+            if (a.status != nullptr) a.status[i] = status;
+        }
+    }
+}
+
+// Workgroup (i, 0) writes entry i's table row, (i, 1 + y) copies its share of
+// the rows of the last page.
+__global__ __launch_bounds__(kCopy) void cache_fork_apply_kernel(ForkK a) {
+    const CacheArgs& c = a.c;
+    const int i = blockIdx.x;
+    const int len = a.plan[2 * i], page = a.plan[2 * i + 1];
+    if (len < 0) return;
+    const int full = len >> c.page_shift, part = len & ((1 << c.page_shift) - 1);
+    const int32_t* from = c.table + static_cast<int64_t>(a.src[i]) * c.max_pages;
+    if (blockIdx.y == 0) {
+        int32_t* to = c.table + static_cast<int64_t>(a.dst[i]) * c.max_pages;
+        for (int j = threadIdx.x; j < full; j += kCopy) {
+            const int p = from[j];
+            to[j] = p;
+            if (names_page(p, c.pages)) atomicAdd(c.refs + p, 1);
+        }
+        if (threadIdx.x == 0) {
+            if (part > 0) to[full] = page;
+            c.lens[a.dst[i]] = len;
+        }
+        return;
+    }
+    if (page < 0) return;
+    const int e = c.x == DT::BF16 ? 2 : 4;
+    const int64_t old = from[full];
+    const int k_pieces = c.dk * e / 16, v_pieces = c.dv * e / 16;
+    // a head's rows of a page are contiguous: part * k_pieces, then part * v_pieces
+    const int per_head = part * (k_pieces + v_pieces), step = (gridDim.y - 1) * kCopy;
+    uint4* kc = static_cast<uint4*>(c.k_cache);
+    uint4* vc = static_cast<uint4*>(c.v_cache);
+    for (int64_t w = static_cast<int64_t>(blockIdx.y - 1) * kCopy + threadIdx.x; w < static_cast<int64_t>(c.Hkv) * per_head; w += step) {
+        const int h = static_cast<int>(w / per_head), x = static_cast<int>(w - static_cast<int64_t>(h) * per_head);
+        const int64_t r0 = (old * c.Hkv + h) << c.page_shift, r1 = (static_cast<int64_t>(page) * c.Hkv + h) << c.page_shift;
+        if (x < part * k_pieces) kc[r1 * k_pieces + x] = kc[r0 * k_pieces + x];
+        else vc[r1 * v_pieces + x - part * k_pieces] = vc[r0 * v_pieces + x - part * k_pieces];
+    }
+}
+
+// ------------------------------------------------------------------ reserve
+
+struct ReserveK {
+    CacheArgs c;
+    int n;
+    const int32_t *slot_list, *new_lens;
+    int32_t* status;
+    int32_t* claim;  // [slots]
+    int32_t* counts; // [n] pages wanted, then the first one's place in `list`
+    int32_t* list;   // [pages]
+};
+
+// One workgroup: a wave per entry counts the columns that lack a page, a scan
+// gives every entry its place, the lowest free pages go out in that order.
+__global__ __launch_bounds__(kPlan) void cache_reserve_kernel(ReserveK a) {
+    __shared__ int sums[kPlan / 64];
+    __shared__ int64_t sums64[kPlan / 64];  // the counts of a bad call may add up to more than 2^31
+    const CacheArgs& c = a.c;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int mask = (1 << c.page_shift) - 1;
+    auto columns = [&](int i) {  // -1: more than a table row holds
+        const int64_t n = (static_cast<int64_t>(max(a.new_lens[i], 0)) + mask) >> c.page_shift;
+        return n > c.max_pages ? -1 : static_cast<int>(n);
+    };
+    auto good = [&](int i) {
+        const int s = a.slot_list[i];
+        return s >= 0 && s < c.slots && columns(i) >= 0;
+    };
+    claim_slots(a.slot_list, a.n, a.claim, good);
+    auto first_column = [&](int slot) {  // the pages below the slot's length are there
+        return static_cast<int>((static_cast<int64_t>(max(c.lens[slot], 0)) + mask) >> c.page_shift);
+    };
+    for (int i = wave; i < a.n; i += kPlan / 64) {
+        int count = -1;
+        if (good(i) && load_fresh(a.claim + a.slot_list[i]) == i) {
+            const int slot = a.slot_list[i], end = columns(i);
+            const int32_t* row = c.table + static_cast<int64_t>(slot) * c.max_pages;
+            count = 0;
+            for (int j0 = first_column(slot); j0 < end; j0 += 64) {
+                const int j = j0 + lane;
+                count += __popcll(__ballot(j < end && !names_page(row[j < end ? j : 0], c.pages)));
+            }
+        }
+        if (lane == 0) store_fresh(a.counts + i, count);
+    }
+    __threadfence();
+    __syncthreads();
+    int64_t want = 0;
+    for (int i0 = 0; i0 < a.n; i0 += kPlan) {
+        const int i = i0 + threadIdx.x;
+        int64_t total;
+        block_scan<int64_t>(i < a.n ? max(load_fresh(a.counts + i), 0) : 0, sums64, total);
+        want += total;
+    }
+    const int have = lowest_free(c.refs, c.pages, static_cast<int>(min(want, static_cast<int64_t>(c.pages))), a.list, sums);
+    int64_t before = 0;
+    for (int i0 = 0; i0 < a.n; i0 += kPlan) {
+        const int i = i0 + threadIdx.x;
+        const int count = i < a.n ? load_fresh(a.counts + i) : 0;
+        int64_t total;
+        const int64_t at = before + block_scan<int64_t>(max(count, 0), sums64, total);
+        before += total;
+        if (i < a.n) {
+            const bool fits = count == 0 || (count > 0 && at + count <= have);
+            if (a.status != nullptr) a.status[i] = count < 0 ? 2 : fits ? 0 : 1;
+            store_fresh(a.counts + i, count > 0 && fits ? static_cast<int>(at) : -1);
+        }
+    }
+    __threadfence();
+    __syncthreads();
+    for (int i = wave; i < a.n; i += kPlan / 64) {
+        int at = load_fresh(a.counts + i);
+        if (at < 0) continue;
+        const int slot = a.slot_list[i], end = columns(i);
+        int32_t* row = c.table + static_cast<int64_t>(slot) * c.max_pages;
+        for (int j0 = first_column(slot); j0 < end; j0 += 64) {
+            const int j = j0 + lane;
+            const bool lacks = j < end && !names_page(row[j < end ? j : 0], c.pages);
+            const unsigned long long all = __ballot(lacks);
+            if (lacks) {
+                const int page = load_fresh(a.list + at + __popcll(all & ((1ull << lane) - 1)));
+                row[j] = page;
+                c.refs[page] = 1;
+            }
+            at += __popcll(all);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ compact
+
+struct CompactK {
+    CacheArgs c;
+    int32_t* live;    // [1]
+    int32_t* moves;   // [1] pages to move
+    int32_t* to;      // [pages] where a page goes
+    int32_t *from_list, *to_list;  // [pages]
+};
+
+__global__ __launch_bounds__(kPlan) void cache_compact_plan_kernel(CompactK a) {
+    __shared__ int sums[kPlan / 64];
+    const CacheArgs& c = a.c;
+    constexpr int kEach = 8;
+    int live = 0;
+    for (int p0 = 0; p0 < c.pages; p0 += kPlan * kEach) {
+        const int first = p0 + static_cast<int>(threadIdx.x) * kEach;
+        int mine = 0, total;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) mine += first + i < c.pages && c.refs[min(first + i, c.pages - 1)] > 0;
+        block_scan(mine, sums, total);
+        live += total;
+    }
+    // the k-th free page below `live` takes the k-th page in use behind it
+    int holes = 0, movers = 0;
+    for (int p0 = 0; p0 < c.pages; p0 += kPlan * kEach) {
+        const int first = p0 + static_cast<int>(threadIdx.x) * kEach;
+        bool hole[kEach], mover[kEach];
+        int h = 0, m = 0, th, tm;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int p = first + i;
+            const bool used = p < c.pages && c.refs[min(p, c.pages - 1)] > 0;
+            hole[i] = p < live && !used;
+            mover[i] = p >= live && used;
+            h += hole[i];
+            m += mover[i];
+        }
+        int ah = holes + block_scan(h, sums, th), am = movers + block_scan(m, sums, tm);
+        holes += th;
+        movers += tm;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            if (first + i < c.pages) store_fresh(a.to + first + i, first + i);
+            if (hole[i]) store_fresh(a.to_list + ah++, first + i);
+            if (mover[i]) store_fresh(a.from_list + am++, first + i);
+        }
+    }
+    __threadfence();
+    __syncthreads();
+    for (int k = threadIdx.x; k < movers; k += kPlan) {
+        const int s = load_fresh(a.from_list + k), d = load_fresh(a.to_list + k);
+        store_fresh(a.to + s, d);
+        c.refs[d] = c.refs[s];
+        c.refs[s] = 0;
+    }
+    if (threadIdx.x == 0) {
+        *a.live = live;
+        *a.moves = movers;
+    }
+}
+
+// One 16-byte piece per thread and step, four in flight.
+__device__ __forceinline__ void copy_pieces(const uint4* src, uint4* dst, int64_t n) {
+    constexpr int kEach = 4;
+    for (int64_t i0 = threadIdx.x; i0 < n; i0 += kCopy * kEach) {
+        uint4 r[kEach];
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+            if (i0 + i * kCopy < n) r[i] = src[i0 + i * kCopy];
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+            if (i0 + i * kCopy < n) dst[i0 + i * kCopy] = r[i];
+    }
+}
+
+constexpr int64_t kSegment = 1024;  // 16-byte pieces that a workgroup copies at a time
+
+// The first table_blocks workgroups rewrite the table, the others move pages.
+__global__ __launch_bounds__(kCopy) void cache_compact_move_kernel(CompactK a, int table_blocks) {
+    const CacheArgs& c = a.c;
+    if (static_cast<int>(blockIdx.x) < table_blocks) {
+        const int64_t entries = static_cast<int64_t>(c.slots) * c.max_pages;
+        for (int64_t i = static_cast<int64_t>(blockIdx.x) * kCopy + threadIdx.x; i < entries; i += static_cast<int64_t>(table_blocks) * kCopy) {
+            const int p = c.table[i];
+            if (names_page(p, c.pages)) c.table[i] = a.to[p];
+        }
+        return;
+    }
+    const int e = c.x == DT::BF16 ? 2 : 4;
+    const int64_t kp = (static_cast<int64_t>(c.Hkv) << c.page_shift) * (c.dk * e / 16);
+    const int64_t vp = (static_cast<int64_t>(c.Hkv) << c.page_shift) * (c.dv * e / 16);
+    const int64_t ks = (kp + kSegment - 1) / kSegment, vs = (vp + kSegment - 1) / kSegment;
+    const int64_t work = static_cast<int64_t>(*a.moves) * (ks + vs);
+    for (int64_t w = blockIdx.x - table_blocks; w < work; w += gridDim.x - table_blocks) {
+        const int64_t k = w / (ks + vs);
+        int64_t x = w - k * (ks + vs);
+        const bool is_k = x < ks;
+        const int64_t size = is_k ? kp : vp;
+        if (!is_k) x -= ks;
+        uint4* pool = static_cast<uint4*>(is_k ? c.k_cache : c.v_cache);
+        const int64_t at = x * kSegment;
+        copy_pieces(pool + a.from_list[k] * size + at, pool + a.to_list[k] * size + at, min(kSegment, size - at));
+    }
+}
+
+// --------------------------------------------------------------------- copy
+
+__global__ __launch_bounds__(kCopy) void cache_copy_kernel(uint4* pool, int64_t row_pieces, int rows, const int32_t* src, const int32_t* dst,
+                                                           int n) {
+    const int64_t segments = (row_pieces + kSegment - 1) / kSegment;
+    for (int64_t w = blockIdx.x; w < segments * n; w += gridDim.x) {
+        const int64_t i = w / segments, at = (w - i * segments) * kSegment;
+        const int s = src[i], d = dst[i];
+        if (s < 0 || s >= rows || d < 0 || d >= rows || s == d) continue;
+        copy_pieces(pool + s * row_pieces + at, pool + d * row_pieces + at, min(kSegment, row_pieces - at));
+    }
+}
+
+size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+constexpr int kMoveBlocks = 2048;
+
+}  // namespace
+
+hipError_t launch_cache_append(const CacheArgs& c, int64_t tokens, int N, const int32_t* cu, int64_t src_rows, const int32_t* rows,
+                               const void* k_new, const void* v_new, const int32_t* slot_indices, hipStream_t s) {
+    if (tokens == 0) return hipSuccess;
+    const AppendK a{c, tokens, src_rows, N, cu, rows, slot_indices, k_new, v_new};
+    LaunchTimer timer("cache_append", s);
+    cache_append_kernel<<<dim3(static_cast<unsigned>((tokens + kAppendTokens - 1) / kAppendTokens)), dim3(kCopy), 0, s>>>(a);
+    return hipGetLastError();
+}
+
+hipError_t launch_cache_free(const CacheArgs& c, int n, const int32_t* slot_list, hipStream_t s) {
+    if (n == 0) return hipSuccess;
+    LaunchTimer timer("cache_free", s);
+    cache_free_kernel<<<dim3(n, (c.max_pages + kCopy - 1) / kCopy), dim3(kCopy), 0, s>>>(c, slot_list);
+    return hipGetLastError();
+}
+
+size_t cache_workspace_bytes(int pages, int slots, int n) {
+    const size_t fork = up256(static_cast<size_t>(slots) * 4) + up256(static_cast<size_t>(n) * 4) + up256(static_cast<size_t>(n) * 8);
+    const size_t reserve = up256(static_cast<size_t>(slots) * 4) + up256(static_cast<size_t>(n) * 4) + up256(static_cast<size_t>(pages) * 4);
+    const size_t compact = 256 + 3 * up256(static_cast<size_t>(pages) * 4);
+    const size_t a = fork > reserve ? fork : reserve;
+    return a > compact ? a : compact;
+}
+
+hipError_t launch_cache_fork(const CacheArgs& c, int n, const int32_t* src, const int32_t* dst, int32_t* status, void* ws, hipStream_t s) {
+    if (n == 0) return hipSuccess;
+    char* w = static_cast<char*>(ws);
+    ForkK a{c, n, src, dst, status, nullptr, nullptr, nullptr};
+    a.claim = reinterpret_cast<int32_t*>(w);
+    w += up256(static_cast<size_t>(c.slots) * 4);
+    a.list = reinterpret_cast<int32_t*>(w);
+    w += up256(static_cast<size_t>(n) * 4);
+    a.plan = reinterpret_cast<int32_t*>(w);
+    {
+        LaunchTimer timer("cache_fork_plan", s);
+        cache_fork_plan_kernel<<<dim3(1), dim3(kPlan), 0, s>>>(a);
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int64_t page_bytes = (static_cast<int64_t>(c.Hkv) << c.page_shift) * (c.dk + c.dv) * (c.x == DT::BF16 ? 2 : 4);
+    int64_t shares = page_bytes / (16 * kCopy * 8);  // eight pieces a thread of a full page
+    shares = shares < 1 ? 1 : shares > 64 ? 64 : shares;
+    LaunchTimer timer("cache_fork_apply", s);
+    cache_fork_apply_kernel<<<dim3(n, static_cast<unsigned>(1 + shares)), dim3(kCopy), 0, s>>>(a);
+    return hipGetLastError();
+}
+
+hipError_t launch_cache_reserve(const CacheArgs& c, int n, const int32_t* slot_list, const int32_t* new_lens, int32_t* status, void* ws,
+                                hipStream_t s) {
+    if (n == 0) return hipSuccess;
+    char* w = static_cast<char*>(ws);
+    ReserveK a{c, n, slot_list, new_lens, status, nullptr, nullptr, nullptr};
+    a.claim = reinterpret_cast<int32_t*>(w);
+    w += up256(static_cast<size_t>(c.slots) * 4);
+    a.counts = reinterpret_cast<int32_t*>(w);
+    w += up256(static_cast<size_t>(n) * 4);
+    a.list = reinterpret_cast<int32_t*>(w);
+    LaunchTimer timer("cache_reserve", s);
+    cache_reserve_kernel<<<dim3(1), dim3(kPlan), 0, s>>>(a);
+    return hipGetLastError();
+}
+
+hipError_t launch_cache_compact(const CacheArgs& c, int32_t* live, void* ws, hipStream_t s) {
+    char* w = static_cast<char*>(ws);
+    CompactK a{c, live, nullptr, nullptr, nullptr, nullptr};
+    a.moves = reinterpret_cast<int32_t*>(w);
+    w += 256;
+    const size_t list = up256(static_cast<size_t>(c.pages) * 4);
+    a.to = reinterpret_cast<int32_t*>(w);
+    a.from_list = reinterpret_cast<int32_t*>(w + list);
+    a.to_list = reinterpret_cast<int32_t*>(w + 2 * list);
+    {
+        LaunchTimer timer("cache_compact_plan", s);
+        cache_compact_plan_kernel<<<dim3(1), dim3(kPlan), 0, s>>>(a);
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int64_t entries = static_cast<int64_t>(c.slots) * c.max_pages;
+    const int64_t want = (entries + 4 * kCopy - 1) / (4 * kCopy);
+    const int table_blocks = static_cast<int>(want < 1 ? 1 : want > 256 ? 256 : want);
+    LaunchTimer timer("cache_compact_move", s);
+    cache_compact_move_kernel<<<dim3(table_blocks + kMoveBlocks), dim3(kCopy), 0, s>>>(a, table_blocks);
+    return hipGetLastError();
+}
+
+hipError_t launch_cache_copy(void* pool, int64_t row_bytes, int rows, const int32_t* src, const int32_t* dst, int n, hipStream_t s) {
+    if (n == 0 || row_bytes == 0) return hipSuccess;
+    const int64_t pieces = row_bytes / 16, work = (pieces + kSegment - 1) / kSegment * n;
+    LaunchTimer timer("cache_copy", s);
+    cache_copy_kernel<<<dim3(static_cast<unsigned>(work < 4096 ? work : 4096)), dim3(kCopy), 0, s>>>(static_cast<uint4*>(pool), pieces, rows,
+                                                                                                 src, dst, n);
+    return hipGetLastError();
+}
+
+}  // namespace kda

@@ -8,6 +8,8 @@
 
 namespace kda {
 
+struct bf16;
+
 enum class DT : int { F32 = 0, BF16 = 1 };
 
 // Optional state snapshots from the prefill: the state after every
@@ -132,6 +134,98 @@ hipError_t launch_gen_forward(const PrefillArgs& a, hipStream_t s, int32_t* base
 hipError_t launch_gen_state(const PrefillArgs& a, hipStream_t s, int32_t* base, float* rec);
 // the fp32 path's chunk records (phase 1) alone
 hipError_t launch_chunk_records(const PrefillArgs& a, hipStream_t s, const int32_t* base, float* rec);
+
+// Full attention (grouped heads).  Head sizes and element types as
+// attn_dispatch names them.
+struct AttnArgs {
+    int64_t T;
+    int H, Hkv, dk, dv, N;
+    const int32_t* cu;  // may be NULL: one sequence [0, T)
+    DT x;
+    float scale;
+    const void *q, *k, *v, *z;
+    void* out;
+    float* lse;
+};
+struct AttnBackwardArgs {
+    AttnArgs f;  // the forward call's arguments (out and lse are its results)
+    const void* dy;
+    void *dq, *dk, *dv, *dz;
+    void* ws;
+};
+
+constexpr int kTreeMaxTokens = 64;
+struct TreeArgs {
+    int B, T, H, Hkv, dk, dv;
+    DT x;
+    float scale;
+    const void *q, *k_new, *v_new, *z;
+    const int64_t* mask;  // [B, T] or NULL: a chain
+    const void *k_cache, *v_cache;
+    int pages, page_shift;
+    const int32_t* table;  // [slots, max_pages]
+    int slots, max_pages;
+    const int32_t* lens;   // [slots]
+    const int32_t* slot_indices;  // [B] or NULL
+    void* out;
+    float* lse;
+    void* ws;
+};
+
+// A paged cache: two pools, the slots' page table and lengths, the pages'
+// counts of table entries.
+struct CacheArgs {
+    int Hkv, dk, dv, pages, page_shift, slots, max_pages;
+    DT x;
+    void *k_cache, *v_cache;
+    int32_t *table, *lens, *refs;
+};
+
+// Row tiles of a packed batch, whatever its lengths: every sequence adds at
+// most one partly filled tile.
+constexpr int64_t attn_tiles(int64_t T, int N, int rows) { return T / rows + (T < N ? T : N); }
+
+constexpr bool attn_head_sizes(int dk, int dv) {
+    return (dk == dv && (dk == 16 || dk == 32 || dk == 64 || dk == 128)) || (dk == 192 && dv == 128);
+}
+template <typename T>
+struct TypeTag {
+    using type = T;
+};
+template <int V>
+struct IntTag {
+    static constexpr int value = V;
+};
+// f(element type, dk, dv) as compile-time tags
+template <typename T, typename F>
+hipError_t attn_dispatch_sizes(int dk, int dv, F&& f) {
+    if (dk == 192 && dv == 128) return f(TypeTag<T>{}, IntTag<192>{}, IntTag<128>{});
+    if (dk == 128 && dv == 128) return f(TypeTag<T>{}, IntTag<128>{}, IntTag<128>{});
+    if (dk == 64 && dv == 64) return f(TypeTag<T>{}, IntTag<64>{}, IntTag<64>{});
+    if (dk == 32 && dv == 32) return f(TypeTag<T>{}, IntTag<32>{}, IntTag<32>{});
+    if (dk == 16 && dv == 16) return f(TypeTag<T>{}, IntTag<16>{}, IntTag<16>{});
+    return hipErrorInvalidValue;
+}
+template <typename F>
+hipError_t attn_dispatch(DT x, int dk, int dv, F&& f) {
+    return x == DT::BF16 ? attn_dispatch_sizes<bf16>(dk, dv, f) : attn_dispatch_sizes<float>(dk, dv, f);
+}
+
+hipError_t launch_attn_prefill(const AttnArgs& a, hipStream_t s);
+size_t attn_backward_workspace_bytes(int64_t T, int N, int H, int Hkv, int dk, int dv, DT x, bool gate);
+hipError_t launch_attn_prefill_backward(const AttnBackwardArgs& a, hipStream_t s);
+size_t attn_tree_workspace_bytes(int B, int T, int H, int Hkv, int dk, int dv, DT x, int64_t max_ctx);
+hipError_t launch_attn_tree(const TreeArgs& a, hipStream_t s);
+
+hipError_t launch_cache_append(const CacheArgs& c, int64_t tokens, int N, const int32_t* cu, int64_t src_rows, const int32_t* rows,
+                               const void* k_new, const void* v_new, const int32_t* slot_indices, hipStream_t s);
+hipError_t launch_cache_free(const CacheArgs& c, int n, const int32_t* slot_list, hipStream_t s);
+size_t cache_workspace_bytes(int pages, int slots, int n);
+hipError_t launch_cache_fork(const CacheArgs& c, int n, const int32_t* src, const int32_t* dst, int32_t* status, void* ws, hipStream_t s);
+hipError_t launch_cache_reserve(const CacheArgs& c, int n, const int32_t* slot_list, const int32_t* new_lens, int32_t* status, void* ws,
+                                hipStream_t s);
+hipError_t launch_cache_compact(const CacheArgs& c, int32_t* live, void* ws, hipStream_t s);
+hipError_t launch_cache_copy(void* pool, int64_t row_bytes, int rows, const int32_t* src, const int32_t* dst, int n, hipStream_t s);
 
 // chunked prefill: workspace layout and the two implementations
 bool prefill_uses_mfma(int dk, int dv, DT x);

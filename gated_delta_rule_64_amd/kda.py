@@ -266,6 +266,269 @@ def kda_prefill_backward(q, k, v, log_alpha, beta, dy, out_gate=None, initial_st
     return g
 
 
+def _device(*tensors):
+    """The one device of a call's tensors (None entries are skipped)."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device} in one call")
+    return dev
+
+
+def _shape(name, t, shape, dtype):
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
+
+
+def _call(dev, name, *args):
+    """One call of the library on the device's current stream."""
+    fn = getattr(lib(), name)
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        check(fn(*args, _stream(dev)))
+    else:
+        with torch.cuda.device(dev):
+            check(fn(*args, _stream(dev)))
+
+
+def _workspace(workspace, need, dev):
+    if workspace is None:
+        return torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    if workspace.dtype != torch.uint8:
+        raise TypeError("workspace must be uint8")
+    return workspace
+
+
+def _attn_shapes(q, k, v, out_gate, cu_seqlens):
+    """Sizes of a packed attention batch, every tensor checked against them."""
+    T, H, dk = q.shape
+    Hkv, dv = k.shape[1], v.shape[2]
+    _shape("k", k, (T, Hkv, dk), q.dtype)
+    _shape("v", v, (T, Hkv, dv), q.dtype)
+    if out_gate is not None:
+        _shape("out_gate", out_gate, (T, H, dv), q.dtype)
+    return T, H, Hkv, dk, dv, _n_seqs(cu_seqlens)
+
+
+def kda_attn_prefill(q, k, v, out_gate=None, cu_seqlens=None, scale=None, out=None, lse=None):
+    """Causal attention over packed prompts: q [T,H,dk], k [T,Hkv,dk], v
+    [T,Hkv,dv]; ``scale`` defaults to dk^-0.5.  Returns (out [T,H,dv], lse
+    fp32 [T,H]).  Rows behind cu_seqlens[-1] are left as they were."""
+    T, H, Hkv, dk, dv, N = _attn_shapes(q, k, v, out_gate, cu_seqlens)
+    dev = _device(q, k, v, out_gate, cu_seqlens, out, lse)
+    if out is None:
+        out = torch.empty((T, H, dv), dtype=q.dtype, device=dev)
+    else:
+        _shape("out", out, (T, H, dv), q.dtype)
+    if lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+    else:
+        _shape("lse", lse, (T, H), torch.float32)
+    _call(dev, "kda_attn_prefill", T, H, Hkv, dk, dv, _ptr(cu_seqlens), N, _dtype_code(q),
+          dk ** -0.5 if scale is None else scale, _ptr(q), _ptr(k), _ptr(v), _ptr(out_gate), _ptr(out), _ptr(lse))
+    return out, lse
+
+
+def kda_attn_backward_workspace_bytes(T_tot, N, H, Hkv, dk, dv, x_dtype, with_gate):
+    if isinstance(x_dtype, torch.dtype):
+        x_dtype = KDA_BF16 if x_dtype == torch.bfloat16 else KDA_F32
+    return int(lib().kda_attn_backward_workspace_bytes(T_tot, N, H, Hkv, dk, dv, x_dtype, int(bool(with_gate))))
+
+
+def kda_attn_prefill_backward(q, k, v, out, lse, dy, out_gate=None, cu_seqlens=None, scale=None, workspace=None):
+    """Gradients of kda_attn_prefill for output gradients dy [T,H,dv]; ``out``
+    and ``lse`` are what it returned.  Returns a dict of dq [T,H,dk], dk
+    [T,Hkv,dk], dv [T,Hkv,dv] and dz [T,H,dv] (None without a gate) in q's
+    type.  Rows behind cu_seqlens[-1] are not written."""
+    T, H, Hkv, dk, dv, N = _attn_shapes(q, k, v, out_gate, cu_seqlens)
+    dev = _device(q, k, v, out, lse, dy, out_gate, cu_seqlens, workspace)
+    for name, t in (("out", out), ("dy", dy)):
+        _shape(name, t, (T, H, dv), q.dtype)
+    _shape("lse", lse, (T, H), torch.float32)
+    x = _dtype_code(q)
+    g = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v),
+         "dz": torch.empty_like(out_gate) if out_gate is not None else None}
+    need = kda_attn_backward_workspace_bytes(T, N, H, Hkv, dk, dv, x, out_gate is not None)
+    workspace = _workspace(workspace, need, dev)
+    _call(dev, "kda_attn_prefill_backward", T, H, Hkv, dk, dv, _ptr(cu_seqlens), N, x,
+          dk ** -0.5 if scale is None else scale, _ptr(q), _ptr(k), _ptr(v), _ptr(out_gate), _ptr(out), _ptr(lse),
+          _ptr(dy), _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dv"]), _ptr(g["dz"]), _ptr(workspace), workspace.numel())
+    return g
+
+
+def _cache_shapes(k_cache, v_cache, page_table):
+    """(num_pages, Hkv, page_size, dk, dv, slots, max_pages) of a cache."""
+    pages, Hkv, page, dk = k_cache.shape
+    dv = v_cache.shape[3]
+    _shape("v_cache", v_cache, (pages, Hkv, page, dv), k_cache.dtype)
+    slots, width = page_table.shape
+    _shape("page_table", page_table, (slots, width), torch.int32)
+    return pages, Hkv, page, dk, dv, slots, width
+
+
+def kda_attn_tree_workspace_bytes(B, T, H, Hkv, dk, dv, x_dtype, max_context):
+    """``max_context``: tokens that a page-table row can hold."""
+    if isinstance(x_dtype, torch.dtype):
+        x_dtype = KDA_BF16 if x_dtype == torch.bfloat16 else KDA_F32
+    return int(lib().kda_attn_tree_workspace_bytes(B, T, H, Hkv, dk, dv, x_dtype, max_context))
+
+
+def kda_attn_tree(q, k_new, v_new, k_cache, v_cache, page_table, lens, tree_mask=None, out_gate=None,
+                  slot_indices=None, scale=None, workspace=None, out=None, lse=None):
+    """Drafted tokens q [B,T,H,dk] (T <= 64; T = 1 is plain decode) over the
+    paged cache and over each other: ``tree_mask`` int64 [B,T], bit j of word
+    t set where token t attends draft j (None: a chain).  k_new [B,T,Hkv,dk]
+    and v_new [B,T,Hkv,dv] are the drafts' own keys and values, not yet in the
+    cache.  Sequence b uses slot ``slot_indices[b]`` (None: b) of page_table
+    int32 [S,max_pages] and lens int32 [S]; an index outside [0, S) marks a
+    padding row, whose output is zero.  Returns (out [B,T,H,dv], lse fp32
+    [B,T,H])."""
+    B, T, H, dk = q.shape
+    pages, Hkv, page, _, dv, slots, width = _cache_shapes(k_cache, v_cache, page_table)
+    _shape("k_cache", k_cache, (pages, Hkv, page, dk), q.dtype)
+    _shape("k_new", k_new, (B, T, Hkv, dk), q.dtype)
+    _shape("v_new", v_new, (B, T, Hkv, dv), q.dtype)
+    _shape("lens", lens, (slots,), torch.int32)
+    if tree_mask is not None:
+        _shape("tree_mask", tree_mask, (B, T), torch.int64)
+    if out_gate is not None:
+        _shape("out_gate", out_gate, (B, T, H, dv), q.dtype)
+    if slot_indices is not None:
+        _shape("slot_indices", slot_indices, (B,), torch.int32)
+    dev = _device(q, k_new, v_new, k_cache, v_cache, page_table, lens, tree_mask, out_gate, slot_indices, workspace,
+                  out, lse)
+    if out is None:
+        out = torch.empty((B, T, H, dv), dtype=q.dtype, device=dev)
+    else:
+        _shape("out", out, (B, T, H, dv), q.dtype)
+    if lse is None:
+        lse = torch.empty((B, T, H), dtype=torch.float32, device=dev)
+    else:
+        _shape("lse", lse, (B, T, H), torch.float32)
+    x = _dtype_code(q)
+    workspace = _workspace(workspace, kda_attn_tree_workspace_bytes(B, T, H, Hkv, dk, dv, x, width * page), dev)
+    _call(dev, "kda_attn_tree", B, T, H, Hkv, dk, dv, x, dk ** -0.5 if scale is None else scale,
+          _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(tree_mask), _ptr(out_gate), _ptr(k_cache), _ptr(v_cache), pages, page,
+          _ptr(page_table), slots, width, _ptr(lens), _ptr(slot_indices), _ptr(out), _ptr(lse),
+          _ptr(workspace), workspace.numel())
+    return out, lse
+
+
+def kda_cache_append(k_new, v_new, k_cache, v_cache, page_table, lens, cu_seqlens=None, rows=None, slot_indices=None):
+    """Writes new tokens' keys and values k_new [R,Hkv,dk], v_new [R,Hkv,dv]
+    into the cache: sequence n's tokens cu_seqlens[n] .. cu_seqlens[n+1] - 1
+    go behind the lens[slot] tokens that its slot (``slot_indices[n]``, or n)
+    holds; token t comes from row ``rows[t]`` (int32; None: row t).  lens is
+    not advanced."""
+    pages, Hkv, page, dk, dv, slots, width = _cache_shapes(k_cache, v_cache, page_table)
+    R, N = k_new.shape[0], _n_seqs(cu_seqlens)
+    _shape("k_new", k_new, (R, Hkv, dk), k_cache.dtype)
+    _shape("v_new", v_new, (R, Hkv, dv), k_cache.dtype)
+    _shape("lens", lens, (slots,), torch.int32)
+    T = R
+    if rows is not None:
+        T = rows.numel()
+        _shape("rows", rows, (T,), torch.int32)
+    if slot_indices is not None:
+        _shape("slot_indices", slot_indices, (N,), torch.int32)
+    dev = _device(k_new, v_new, k_cache, v_cache, page_table, lens, cu_seqlens, rows, slot_indices)
+    _call(dev, "kda_cache_append", T, N, _ptr(cu_seqlens), R, _ptr(rows), Hkv, dk, dv, _dtype_code(k_cache),
+          _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache), pages, page, _ptr(page_table), slots, width,
+          _ptr(lens), _ptr(slot_indices))
+
+
+def kda_cache_workspace_bytes(num_pages, slots, n):
+    return int(lib().kda_cache_workspace_bytes(num_pages, slots, n))
+
+
+def _slot_list(name, t):
+    _shape(name, t, (t.numel(),), torch.int32)
+    return t.numel()
+
+
+def _status(status, n, dev):
+    if status is None:
+        return torch.empty(n, dtype=torch.int32, device=dev)
+    _shape("status", status, (n,), torch.int32)
+    return status
+
+
+def kda_cache_free(slot_list, page_table, lens, refs):
+    """Empties the slots of ``slot_list`` (int32 [n]); pages that no other
+    slot names become free."""
+    n = _slot_list("slot_list", slot_list)
+    slots, width = page_table.shape
+    _shape("page_table", page_table, (slots, width), torch.int32)
+    _shape("lens", lens, (slots,), torch.int32)
+    _shape("refs", refs, (refs.numel(),), torch.int32)
+    dev = _device(slot_list, page_table, lens, refs)
+    _call(dev, "kda_cache_free", n, _ptr(slot_list), refs.numel(), _ptr(page_table), slots, width, _ptr(lens), _ptr(refs))
+
+
+def kda_cache_fork(src, dst, k_cache, v_cache, page_table, lens, refs, status=None, workspace=None):
+    """Slot dst[i] (empty) becomes a copy of slot src[i]: full pages shared,
+    the rows of a partly filled last page copied.  Returns status int32 [n]:
+    0 done, 1 too few free pages, 2 refused."""
+    pages, Hkv, page, dk, dv, slots, width = _cache_shapes(k_cache, v_cache, page_table)
+    n = _slot_list("src", src)
+    _shape("dst", dst, (n,), torch.int32)
+    _shape("lens", lens, (slots,), torch.int32)
+    _shape("refs", refs, (pages,), torch.int32)
+    dev = _device(src, dst, k_cache, v_cache, page_table, lens, refs, status, workspace)
+    status = _status(status, n, dev)
+    workspace = _workspace(workspace, kda_cache_workspace_bytes(pages, slots, n), dev)
+    _call(dev, "kda_cache_fork", n, _ptr(src), _ptr(dst), Hkv, dk, dv, _dtype_code(k_cache), _ptr(k_cache), _ptr(v_cache),
+          pages, page, _ptr(page_table), slots, width, _ptr(lens), _ptr(refs), _ptr(status), _ptr(workspace),
+          workspace.numel())
+    return status
+
+
+def kda_cache_reserve(slot_list, new_lens, page_size, page_table, lens, refs, status=None, workspace=None):
+    """Gives every listed slot the pages that it lacks for new_lens[i] tokens.
+    Returns status int32 [n]: 0 done, 1 too few free pages, 2 refused."""
+    n = _slot_list("slot_list", slot_list)
+    _shape("new_lens", new_lens, (n,), torch.int32)
+    slots, width = page_table.shape
+    _shape("page_table", page_table, (slots, width), torch.int32)
+    _shape("lens", lens, (slots,), torch.int32)
+    _shape("refs", refs, (refs.numel(),), torch.int32)
+    dev = _device(slot_list, new_lens, page_table, lens, refs, status, workspace)
+    status = _status(status, n, dev)
+    workspace = _workspace(workspace, kda_cache_workspace_bytes(refs.numel(), slots, n), dev)
+    _call(dev, "kda_cache_reserve", n, _ptr(slot_list), _ptr(new_lens), refs.numel(), page_size, _ptr(page_table), slots,
+          width, _ptr(lens), _ptr(refs), _ptr(status), _ptr(workspace), workspace.numel())
+    return status
+
+
+def kda_cache_compact(k_cache, v_cache, page_table, refs, live=None, workspace=None):
+    """Moves the pages in use to the front of the pool.  Returns ``live``
+    int32 [1], how many there are (pages from there on are free)."""
+    pages, Hkv, page, dk, dv, slots, width = _cache_shapes(k_cache, v_cache, page_table)
+    _shape("refs", refs, (pages,), torch.int32)
+    dev = _device(k_cache, v_cache, page_table, refs, live, workspace)
+    if live is None:
+        live = torch.empty(1, dtype=torch.int32, device=dev)
+    else:
+        _shape("live", live, (1,), torch.int32)
+    workspace = _workspace(workspace, kda_cache_workspace_bytes(pages, slots, 0), dev)
+    _call(dev, "kda_cache_compact", Hkv, dk, dv, _dtype_code(k_cache), _ptr(k_cache), _ptr(v_cache), pages, page,
+          _ptr(page_table), slots, width, _ptr(refs), _ptr(live), _ptr(workspace), workspace.numel())
+    return live
+
+
+def kda_cache_copy(pool, src, dst):
+    """Row dst[i] of ``pool`` (any type, [rows, ...]) becomes a copy of row
+    src[i] (int32 lists): pages of a cache, or rows of the KDA state and
+    conv-history pools of a sequence that is forked."""
+    n = _slot_list("src", src)
+    _shape("dst", dst, (n,), torch.int32)
+    rows = pool.shape[0]
+    row_bytes = pool.numel() // max(rows, 1) * pool.element_size()
+    dev = _device(pool, src, dst)
+    _call(dev, "kda_cache_copy", _ptr(pool), row_bytes, rows, _ptr(src), _ptr(dst), n)
+
+
 def kda_probe_peak(kind, blocks, iters=0, src=None, out=None):
     """Peak-rate probe (see kda.h): kind 0 bf16 matrix-core loop, 1 fp32
     matrix-core loop, 2 streaming read of ``src``.  Returns ``out``."""

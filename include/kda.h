@@ -432,6 +432,209 @@ int kda_spec_verify(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv,
                     void* stream);
 
 /*
+ * Full attention: the layers that stand between the KDA layers of the hybrid
+ * model (one in six there; the "Every architecture field" table of the page
+ * "Ling 3.0 Flash" gives heads of 192, 128 and 64 rotary, over values of 128).
+ *
+ * Shared by the calls below.
+ *  - Heads: H query heads over Hkv key and value heads (Hkv divides H); query
+ *    head h reads key head h / (H / Hkv).  dk = dv = 16, 32, 64 or 128, or
+ *    dk = 192 with dv = 128 (else KDA_ERR_UNSUPPORTED).
+ *  - Types: x_dtype (fp32 or bf16) for every tensor without another type.
+ *    Scores, softmax statistics and sums are fp32; with bf16 the weights are
+ *    rounded to bf16 for their product with the values.
+ *  - scale multiplies q . k; positive and finite.
+ *  - out_gate: NULL, or logits z of out's shape: out = o * sigmoid(z).
+ *  - A row that attends nothing gets 0, and -infinity as its lse.
+ *  - Non-finite values reach every row that attends them.  In a tile that
+ *    a row attends in part, a non-finite value behind the row's own position
+ *    (same sequence only) may reach it too; other sequences' rows, memory
+ *    behind a sequence's end and stale page contents never do.
+ *  - Rows of T_tot behind the last sequence are neither read nor written:
+ *    cu_seqlens[N] may be below T_tot.
+ *
+ * kda_attn_prefill -- causal attention over a packed batch of whole prompts:
+ * token i of a sequence attends its tokens 0 .. i,
+ *     s_ij = scale q_i . k_j,   o_i = sum_j softmax_j(s_ij) v_j,
+ *     lse_i = log sum_j e^(s_ij).
+ * Arguments:
+ *   q [T_tot, H, dk]; k [T_tot, Hkv, dk]; v [T_tot, Hkv, dv];
+ *   out [T_tot, H, dv];  lse NULL or fp32 [T_tot, H] (the gradients need it).
+ * The call needs no workspace.  H x (T_tot/128 + min(N, T_tot)) must stay
+ * below 2^31 (KDA_ERR_UNSUPPORTED otherwise).
+ */
+int kda_attn_prefill(int64_t T_tot, int32_t H, int32_t Hkv, int32_t dk, int32_t dv,
+                     const int32_t* cu_seqlens, int32_t N, int32_t x_dtype, float scale,
+                     const void* q, const void* k, const void* v,
+                     const void* out_gate,
+                     void* out, float* lse,
+                     void* stream);
+
+/*
+ * kda_attn_prefill_backward -- gradients of kda_attn_prefill for output
+ * gradients dy.  The scores are formed again from q, k and lse; key and value
+ * gradients are summed over the query heads that share a head.  Every sum has
+ * one owner and a fixed order: the same inputs give the same bits.
+ * Arguments: those of kda_attn_prefill, with out and lse as it wrote them, and
+ *   dy            [T_tot, H, dv];
+ *   grad_q [T_tot, H, dk], grad_k [T_tot, Hkv, dk], grad_v [T_tot, Hkv, dv]:
+ *                 in x_dtype (they feed x_dtype products; the sums are fp32);
+ *   grad_out_gate [T_tot, H, dv], required exactly when out_gate is given;
+ *   workspace     at least kda_attn_backward_workspace_bytes() bytes (of the
+ *                 same sizes; with_gate: whether out_gate is given), 256-byte
+ *                 aligned; contents on entry are ignored.
+ */
+size_t kda_attn_backward_workspace_bytes(int64_t T_tot, int32_t N, int32_t H, int32_t Hkv,
+                                         int32_t dk, int32_t dv, int32_t x_dtype, int32_t with_gate);
+int kda_attn_prefill_backward(int64_t T_tot, int32_t H, int32_t Hkv, int32_t dk, int32_t dv,
+                              const int32_t* cu_seqlens, int32_t N, int32_t x_dtype, float scale,
+                              const void* q, const void* k, const void* v,
+                              const void* out_gate, const void* out, const float* lse,
+                              const void* dy,
+                              void* grad_q, void* grad_k, void* grad_v, void* grad_out_gate,
+                              void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/*
+ * A paged cache of keys and values.
+ *   k_cache [num_pages, Hkv, page_size, dk], v_cache [num_pages, Hkv,
+ *   page_size, dv]: the pools (x_dtype; page_size a power of two, 16 .. 1024);
+ *   page_table  int32 [slots, max_pages]: token p of a slot is row
+ *               p % page_size of page page_table[slot][p / page_size]; an
+ *               entry outside [0, num_pages) names no page;
+ *   lens        int32 [slots]: committed tokens of each slot;
+ *   refs        int32 [num_pages]: table entries that name the page; a page
+ *               whose count is not positive is free.
+ * A slot's pages stand at the front of its table row; a slot without pages
+ * has length 0 and -1 in its entries (page_table filled with -1, lens and
+ * refs with 0 is an empty cache).  Calls on one cache are ordered by the
+ * stream; two that overlap in time race.
+ *
+ * kda_attn_tree -- attention of a tree of drafted tokens over the cache: the
+ * full-attention side of a kda_spec_verify call, and with T = 1 plain decode.
+ * Token t of sequence b attends all lens[slot] tokens of its slot and the
+ * drafted tokens j whose bit j is set in its mask word (its own bit
+ * included: a word of 0 attends the cache alone).  The drafts' keys and
+ * values are given dense and are not written to the cache; commit the
+ * accepted ones with kda_cache_append.
+ * Arguments:
+ *   B, T          sequences and drafted tokens per sequence (0 <= T <= 64);
+ *   q [B, T, H, dk], k_new [B, T, Hkv, dk], v_new [B, T, Hkv, dv];
+ *   tree_mask     NULL (a chain: token t attends drafts 0 .. t) or int64 [B, T];
+ *   slot_indices  NULL (sequence b uses slot b; then slots must be B) or
+ *                 device int32 [B]; several sequences may name one slot.  An
+ *                 index outside [0, slots) marks a padding row: its outputs
+ *                 are 0 (lse -infinity) and nothing of it is read;
+ *   out [B, T, H, dv]; lse NULL or fp32 [B, T, H];
+ *   workspace     at least kda_attn_tree_workspace_bytes() bytes for
+ *                 max_context = max_pages * page_size, 256-byte aligned.
+ * Tokens whose table entry names no page are not attended.  Lengths are
+ * clamped to what a table row holds.  B x T x H must be below 2^30.
+ */
+size_t kda_attn_tree_workspace_bytes(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t dk,
+                                     int32_t dv, int32_t x_dtype, int64_t max_context);
+int kda_attn_tree(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t dk, int32_t dv,
+                  int32_t x_dtype, float scale,
+                  const void* q, const void* k_new, const void* v_new,
+                  const int64_t* tree_mask, const void* out_gate,
+                  const void* k_cache, const void* v_cache, int32_t num_pages, int32_t page_size,
+                  const int32_t* page_table, int32_t slots, int32_t max_pages,
+                  const int32_t* lens, const int32_t* slot_indices,
+                  void* out, float* lse,
+                  void* workspace, size_t workspace_bytes,
+                  void* stream);
+
+/*
+ * kda_cache_append -- writes the keys and values of new tokens into pages.
+ * Sequence n's tokens are t = cu_seqlens[n] .. cu_seqlens[n+1] - 1; token t
+ * comes from row rows[t] of k_new and v_new (row t when rows is NULL) and goes
+ * to position lens[slot] + t - cu_seqlens[n] of its slot.  So one call takes a
+ * packed batch of prompts (rows NULL) or the accepted path of each draft tree
+ * (rows: b * T + the path's tokens, in order).  lens is read, not advanced:
+ * the caller adds the counts when the tokens are committed.
+ * Arguments:
+ *   cu_seqlens int32 [N+1] or NULL (one sequence of T_tot tokens);
+ *   k_new [src_rows, Hkv, dk], v_new [src_rows, Hkv, dv]; rows int32 [T_tot];
+ *   slot_indices NULL (sequence n uses slot n) or int32 [N], distinct where
+ *                the sequences are not empty.
+ * Dropped: tokens at or behind cu_seqlens[N], of slots outside [0, slots),
+ * from rows outside [0, src_rows), and at positions whose table entry names no
+ * page (kda_cache_reserve gives a slot its pages first).
+ */
+int kda_cache_append(int64_t T_tot, int32_t N, const int32_t* cu_seqlens,
+                     int64_t src_rows, const int32_t* rows,
+                     int32_t Hkv, int32_t dk, int32_t dv, int32_t x_dtype,
+                     const void* k_new, const void* v_new,
+                     void* k_cache, void* v_cache, int32_t num_pages, int32_t page_size,
+                     const int32_t* page_table, int32_t slots, int32_t max_pages,
+                     const int32_t* lens, const int32_t* slot_indices,
+                     void* stream);
+
+/*
+ * The pages of a cache.  status (NULL or int32 [n], written): 0 done, 1 the
+ * pool has too few free pages, 2 refused (a slot outside [0, slots), or as
+ * said below); an entry that is not done changes nothing.  Free pages go out
+ * lowest number first, in the order of the entries, so the results do not
+ * depend on timing; the first entry that does not fit and every later one
+ * that needs pages get status 1.  Workspace: at least
+ * kda_cache_workspace_bytes(num_pages, slots, n) bytes (n = 0 for
+ * kda_cache_compact), 256-byte aligned; contents on entry are ignored.
+ *
+ * kda_cache_free -- empties the listed slots: their entries become -1, their
+ * lengths 0, and the counts of their pages drop by one each.  Slots outside
+ * [0, slots) are skipped; naming a slot twice is naming it once.
+ *
+ * kda_cache_fork -- slot dst[i] becomes a copy of slot src[i]: the full pages
+ * are shared (their counts rise), the rows in use of a partly filled last
+ * page are copied to a new page, so both slots can be appended to.  Refused:
+ * src[i] = dst[i], a dst that holds tokens or pages, and a dst that an earlier
+ * entry of the call names.  A slot may be forked many times in one call.
+ *
+ * kda_cache_reserve -- gives slot slot_list[i] the pages that it lacks for
+ * new_lens[i] tokens: every table entry from its length's last page on, up to
+ * the new length, that names no page gets one.  lens is not changed.
+ * Refused: lengths that a table row does not hold, and a slot that an earlier
+ * entry of the call names.
+ *
+ * kda_cache_compact -- moves the pages in use to the front of the pool (live
+ * of them, written to live[0]): the k-th page in use at or behind `live` moves
+ * to the k-th free page before it, counts and table entries follow.  The rest
+ * stay where they are; pages from live[0] on are free after the call.
+ *
+ * kda_cache_copy -- row src[i] of a pool [rows, row_bytes] is copied to row
+ * dst[i]: pages of a cache, or rows of the KDA state and conv-history pools
+ * when a sequence is forked.  row_bytes is a multiple of 16.  Entries with a
+ * row outside [0, rows), or with src[i] = dst[i], are skipped.  No row may be
+ * written twice, or read and written, by one call (its contents would depend
+ * on timing); with KDA_DEBUG_CHECK=1 the call checks that, synchronising the
+ * stream.
+ */
+size_t kda_cache_workspace_bytes(int32_t num_pages, int32_t slots, int32_t n);
+int kda_cache_free(int32_t n, const int32_t* slot_list, int32_t num_pages,
+                   int32_t* page_table, int32_t slots, int32_t max_pages,
+                   int32_t* lens, int32_t* refs, void* stream);
+int kda_cache_fork(int32_t n, const int32_t* src, const int32_t* dst,
+                   int32_t Hkv, int32_t dk, int32_t dv, int32_t x_dtype,
+                   void* k_cache, void* v_cache, int32_t num_pages, int32_t page_size,
+                   int32_t* page_table, int32_t slots, int32_t max_pages,
+                   int32_t* lens, int32_t* refs,
+                   int32_t* status,
+                   void* workspace, size_t workspace_bytes, void* stream);
+int kda_cache_reserve(int32_t n, const int32_t* slot_list, const int32_t* new_lens,
+                      int32_t num_pages, int32_t page_size,
+                      int32_t* page_table, int32_t slots, int32_t max_pages,
+                      const int32_t* lens, int32_t* refs,
+                      int32_t* status,
+                      void* workspace, size_t workspace_bytes, void* stream);
+int kda_cache_compact(int32_t Hkv, int32_t dk, int32_t dv, int32_t x_dtype,
+                      void* k_cache, void* v_cache, int32_t num_pages, int32_t page_size,
+                      int32_t* page_table, int32_t slots, int32_t max_pages,
+                      int32_t* refs, int32_t* live,
+                      void* workspace, size_t workspace_bytes, void* stream);
+int kda_cache_copy(void* pool, int64_t row_bytes, int32_t rows,
+                   const int32_t* src, const int32_t* dst, int32_t n, void* stream);
+
+/*
  * Kernel timing for profiling tools (not needed for normal use).
  * kda_profile_enable(1) makes every later call on the calling host thread
  * bracket each kernel it launches with a pair of HIP events recorded on the
