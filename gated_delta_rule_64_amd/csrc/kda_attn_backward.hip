@@ -33,6 +33,8 @@ struct BwdK {
     float* delta;     // [T, H]
     void* dog;        // [T, H, dv]: dy * sigmoid(z), or dy itself without a gate
     float scale;
+    int parts;
+    float* part;      // [parts][T, Hkv][dk + dv]
 };
 
 // One row (token, head) per 16 lanes.
@@ -93,22 +95,20 @@ __device__ __forceinline__ void store_rows(T* row, const f32x16 (&acc)[kTiles], 
 
 template <typename T, int DK, int DV>
 struct DqSizes {
-    static constexpr int kKeys = sizeof(T) == 4 && DK > 128 ? 32 : 64;
-    static constexpr int kKStride = DK * static_cast<int>(sizeof(T)) + kBothPad;
-    static constexpr int kVStride = DV * static_cast<int>(sizeof(T)) + kRowPad;
-    static constexpr int kLds = kKeys * (kKStride + kVStride) + kTrSlack;
+    static constexpr int kKeys = sizeof(T) == 4 && DK > 64 ? 32 : 64;
+    static constexpr int kBuf = kKeys * (DK + DV) * static_cast<int>(sizeof(T));
+    static constexpr int kLds = 2 * kBuf + kTrSlack;
 };
 
 template <typename T, int DK, int DV>
-__global__ __launch_bounds__(kThreads) void attn_bwd_dq_kernel(BwdK a) {
+__global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && DK <= 128 ? 2 : 1)) void attn_bwd_dq_kernel(BwdK a) {
     using Sz = DqSizes<T, DK, DV>;
     constexpr int kKeys = Sz::kKeys, kSub = kKeys / 32;
     constexpr int kQPieces = DK / (2 * Elem<T>::kPer16), kVPieces = DV / (2 * Elem<T>::kPer16);
     constexpr int kKTiles = (DK + 31) / 32;
     constexpr int kP = Elem<T>::kPieces;
     extern __shared__ __align__(16) char smem[];
-    char* sK = smem;
-    char* sV = smem + kKeys * Sz::kKStride;
+    constexpr int kV = kKeys * DK * static_cast<int>(sizeof(T));  // the values, behind the keys
 
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int c = lane & 31, half = lane >> 5;
@@ -140,8 +140,13 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_dq_kernel(BwdK a) {
     f32x16 acc[kKTiles];
 #pragma unroll
     for (int i = 0; i < kKTiles; ++i) acc[i] = f32x16{};
-    TileCopy<T, kKeys, DK, kBothPad, kThreads> ck;
-    TileCopy<T, kKeys, DV, kRowPad, kThreads> cv;
+    TileCopy<T, kKeys, DK, kThreads> ck;
+    TileCopy<T, kKeys, DV, kThreads> cv;
+    TileRead<T, DK> rk;
+    TileRead<T, DV> rv;
+    rk.init_rows(c, half);
+    rk.init_columns(lane);
+    rv.init_rows(c, half);
     const int last = min(t.level * kRows + kRows, t.len);
     const T* kbase = static_cast<const T*>(a.k) + kvh * DK;
     const T* vbase = static_cast<const T*>(a.v) + kvh * DV;
@@ -149,24 +154,21 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_dq_kernel(BwdK a) {
         ck.load(rows_of(kbase, t.start + j0, k_row, min(kKeys, t.len - j0)), k_row, tid);
         cv.load(rows_of(vbase, t.start + j0, v_row, min(kKeys, t.len - j0)), v_row, tid);
     };
-    fetch(0);
-    for (int j0 = 0; j0 < last; j0 += kKeys) {
-        __syncthreads();
-        ck.store(sK, tid);
-        cv.store(sV, tid);
-        if (j0 + kKeys < last) fetch(j0 + kKeys);
-        __syncthreads();
+    auto put = [&](char* buf) {
+        ck.store(buf, tid);
+        cv.store(buf + kV, tid);
+    };
+    auto work = [&](const char* sK, int j0) {
+        const char* sV = sK + kV;
 #pragma unroll
         for (int u = 0; u < kSub; ++u) {
             const int k0 = j0 + 32 * u;
             if (k0 > q0 + 31) break;
             f32x16 s{}, dp{};
-            const char* krow = sK + (32 * u + c) * Sz::kKStride + half * 16;
-            const char* vrow = sV + (32 * u + c) * Sz::kVStride + half * 16;
 #pragma unroll
-            for (int p = 0; p < kQPieces; ++p) s = mma<T>(*reinterpret_cast<const u32x4*>(krow + p * 32), qf[p], s);
+            for (int p = 0; p < kQPieces; ++p) s = mma<T>(rk.rows(sK + 32 * u * rk.kRow, p), qf[p], s);
 #pragma unroll
-            for (int p = 0; p < kVPieces; ++p) dp = mma<T>(*reinterpret_cast<const u32x4*>(vrow + p * 32), of[p], dp);
+            for (int p = 0; p < kVPieces; ++p) dp = mma<T>(rv.rows(sV + 32 * u * rv.kRow, p), of[p], dp);
             const int most = q0 + c - k0 - 4 * half;
             const bool diagonal = k0 + 31 > q0;
 #pragma unroll
@@ -179,9 +181,22 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_dq_kernel(BwdK a) {
                 const u32x4 b = as_operand<T>(s, p);
 #pragma unroll
                 for (int i = 0; i < kKTiles; ++i)
-                    acc[i] = mma<T>(transposed<T, Sz::kKStride>(sK + 32 * u * Sz::kKStride, 32 * i, p, lane), b, acc[i]);
+                    acc[i] = mma<T>(rk.columns(sK + 32 * u * rk.kRow, i, p), b, acc[i]);
             }
         }
+    };
+    fetch(0);
+    put(smem);
+    for (int j0 = 0; j0 < last; j0 += 2 * kKeys) {
+        tile_barrier();
+        if (j0 + kKeys < last) fetch(j0 + kKeys);
+        work(smem, j0);
+        if (j0 + kKeys >= last) break;
+        put(smem + Sz::kBuf);
+        tile_barrier();
+        if (j0 + 2 * kKeys < last) fetch(j0 + 2 * kKeys);
+        work(smem + Sz::kBuf, j0 + kKeys);
+        if (j0 + 2 * kKeys < last) put(smem);
     }
     if (c < rows) store_rows<T, DK>(static_cast<T*>(a.dq) + at * DK, acc, a.scale, half);
 }
@@ -189,12 +204,15 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_dq_kernel(BwdK a) {
 template <typename T, int DK, int DV>
 struct DkvSizes {
     static constexpr int kQ = 32;  // queries of a step
-    static constexpr int kQStride = DK * static_cast<int>(sizeof(T)) + kBothPad;
-    static constexpr int kOStride = DV * static_cast<int>(sizeof(T)) + kBothPad;
     static constexpr int kStats = kQ * 2 * 4;  // lse and delta of the step's queries
-    static constexpr int kLds = kQ * (kQStride + kOStride) + kTrSlack + kStats;
+    static constexpr int kBuf = kQ * (DK + DV) * static_cast<int>(sizeof(T)) + kStats;
+    static constexpr int kLds = 2 * kBuf + kTrSlack;
 };
 
+// One workgroup per (tile of 128 keys, key head, part).  The tile's work is
+// the sequence of its steps of 32 queries, head by head of the group; the
+// parts cut it into equal pieces where there are few tiles, and their sums
+// (fp32) are added by attn_bwd_sum_kernel.
 template <typename T, int DK, int DV>
 __global__ __launch_bounds__(kThreads) void attn_bwd_dkv_kernel(BwdK a) {
     using Sz = DkvSizes<T, DK, DV>;
@@ -202,17 +220,16 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_dkv_kernel(BwdK a) {
     constexpr int kKPieces = DK / (2 * Elem<T>::kPer16), kVPieces = DV / (2 * Elem<T>::kPer16);
     constexpr int kKTiles = (DK + 31) / 32, kVTiles = (DV + 31) / 32;
     constexpr int kP = Elem<T>::kPieces;
+    constexpr int kO = kQ * DK * static_cast<int>(sizeof(T));       // the output gradients, behind the queries
+    constexpr int kS = kO + kQ * DV * static_cast<int>(sizeof(T));  // the statistics, behind both
     extern __shared__ __align__(16) char smem[];
-    float* sLse = reinterpret_cast<float*>(smem);
-    float* sDelta = sLse + kQ;
-    char* sQ = smem + Sz::kStats;
-    char* sO = sQ + kQ * Sz::kQStride;
 
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int c = lane & 31, half = lane >> 5;
     const int G = a.H / a.Hkv;
-    const int64_t rank = blockIdx.x / a.Hkv;
-    const int kvh = blockIdx.x % a.Hkv;
+    const int64_t rank = blockIdx.x / (a.Hkv * a.parts);
+    const int slot = blockIdx.x % (a.Hkv * a.parts);
+    const int kvh = slot % a.Hkv, part = slot / a.Hkv;
     const Tile t = find_tile<kRows>(a.cu, a.N, a.T, rank);
     if (!t.there) return;
     // the first keys of a sequence have the most queries: levels from the end
@@ -243,10 +260,18 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_dkv_kernel(BwdK a) {
 #pragma unroll
     for (int i = 0; i < kVTiles; ++i) gv[i] = f32x16{};
 
-    TileCopy<T, kQ, DK, kBothPad, kThreads> cq;
-    TileCopy<T, kQ, DV, kBothPad, kThreads> co;
+    TileCopy<T, kQ, DK, kThreads> cq;
+    TileCopy<T, kQ, DV, kThreads> co;
+    TileRead<T, DK> rq;
+    TileRead<T, DV> ro;
+    rq.init_rows(c, half);
+    rq.init_columns(lane);
+    ro.init_rows(c, half);
+    ro.init_columns(lane);
     float stat = 0.f;
     const int steps = (t.len - k_first + kQ - 1) / kQ;  // per head
+    const int64_t all = static_cast<int64_t>(steps) * G;
+    const int n_end = static_cast<int>(all * (part + 1) / a.parts);
     auto fetch = [&](int n) {
         const int h = kvh * G + n / steps, i0 = k_first + (n % steps) * kQ;
         const int here = min(kQ, t.len - i0);
@@ -259,32 +284,28 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_dkv_kernel(BwdK a) {
             stat = tid < kQ ? (i < here ? a.lse[at] * kLog2e : INFINITY) : (i < here ? a.delta[at] : 0.f);
         }
     };
-    fetch(0);
-    for (int n = 0; n < steps * G; ++n) {
-        __syncthreads();
-        cq.store(sQ, tid);
-        co.store(sO, tid);
-        if (tid < 2 * kQ) sLse[tid] = stat;
-        if (n + 1 < steps * G) fetch(n + 1);
-        __syncthreads();
+    auto put = [&](char* buf) {
+        cq.store(buf, tid);
+        co.store(buf + kO, tid);
+        if (tid < 2 * kQ) reinterpret_cast<float*>(buf + kS)[tid] = stat;
+    };
+    auto work = [&](const char* sQ, int n) {
         const int i0 = k_first + (n % steps) * kQ;
-        if (i0 + kQ - 1 < k0) continue;  // queries before this wave's keys
+        if (i0 + kQ - 1 < k0) return;  // queries before this wave's keys
+        const char* sO = sQ + kO;
+        const float* sLse = reinterpret_cast<const float*>(sQ + kS);
         f32x16 s{}, dp{};
-        const char* qrow = sQ + c * Sz::kQStride + half * 16;
-        const char* orow = sO + c * Sz::kOStride + half * 16;
 #pragma unroll
-        for (int p = 0; p < kKPieces; ++p)
-            s = mma<T>(*reinterpret_cast<const u32x4*>(qrow + p * 32), kKeep ? kf[kKeep ? p : 0] : buffer_load16(ks, k_at + p * 32), s);
+        for (int p = 0; p < kKPieces; ++p) s = mma<T>(rq.rows(sQ, p), kKeep ? kf[kKeep ? p : 0] : buffer_load16(ks, k_at + p * 32), s);
 #pragma unroll
-        for (int p = 0; p < kVPieces; ++p)
-            dp = mma<T>(*reinterpret_cast<const u32x4*>(orow + p * 32), kKeep ? vf[kKeep ? p : 0] : buffer_load16(vs, v_at + p * 32), dp);
+        for (int p = 0; p < kVPieces; ++p) dp = mma<T>(ro.rows(sO, p), kKeep ? vf[kKeep ? p : 0] : buffer_load16(vs, v_at + p * 32), dp);
         // register r: query i0 + 8 (r / 4) + 4 half + r % 4; key k0 + c
         const int least = k0 + c - i0 - 4 * half;
         const bool diagonal = i0 < k0 + 31;
 #pragma unroll
         for (int r4 = 0; r4 < 4; ++r4) {
             const f32x4 ls = *reinterpret_cast<const f32x4*>(sLse + 8 * r4 + 4 * half);
-            const f32x4 de = *reinterpret_cast<const f32x4*>(sDelta + 8 * r4 + 4 * half);
+            const f32x4 de = *reinterpret_cast<const f32x4*>(sLse + kQ + 8 * r4 + 4 * half);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int r = 4 * r4 + e;
@@ -298,16 +319,67 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_dkv_kernel(BwdK a) {
         for (int p = 0; p < kP; ++p) {
             const u32x4 b = as_operand<T>(s, p), d = as_operand<T>(dp, p);
 #pragma unroll
-            for (int i = 0; i < kVTiles; ++i) gv[i] = mma<T>(transposed<T, Sz::kOStride>(sO, 32 * i, p, lane), b, gv[i]);
+            for (int i = 0; i < kVTiles; ++i) gv[i] = mma<T>(ro.columns(sO, i, p), b, gv[i]);
 #pragma unroll
-            for (int i = 0; i < kKTiles; ++i) gk[i] = mma<T>(transposed<T, Sz::kQStride>(sQ, 32 * i, p, lane), d, gk[i]);
+            for (int i = 0; i < kKTiles; ++i) gk[i] = mma<T>(rq.columns(sQ, i, p), d, gk[i]);
         }
+    };
+    int n = static_cast<int>(all * part / a.parts);
+    if (n < n_end) {
+        fetch(n);
+        put(smem);
+    }
+    for (; n < n_end; n += 2) {
+        tile_barrier();
+        if (n + 1 < n_end) fetch(n + 1);
+        work(smem, n);
+        if (n + 1 >= n_end) break;
+        put(smem + Sz::kBuf);
+        tile_barrier();
+        if (n + 2 < n_end) fetch(n + 2);
+        work(smem + Sz::kBuf, n + 1);
+        if (n + 2 < n_end) put(smem);
     }
     if (c < rows) {
         const int64_t at = (t.start + k0 + c) * a.Hkv + kvh;
-        store_rows<T, DK>(static_cast<T*>(a.dk) + at * DK, gk, a.scale, half);
-        store_rows<T, DV>(static_cast<T*>(a.dv) + at * DV, gv, 1.f, half);
+        if (a.parts > 1) {
+            float* to = a.part + (static_cast<int64_t>(part) * a.T * a.Hkv + at) * (DK + DV);
+            store_rows<float, DK>(to, gk, a.scale, half);
+            store_rows<float, DV>(to + DK, gv, 1.f, half);
+        } else {
+            store_rows<T, DK>(static_cast<T*>(a.dk) + at * DK, gk, a.scale, half);
+            store_rows<T, DV>(static_cast<T*>(a.dv) + at * DV, gv, 1.f, half);
+        }
     }
+}
+
+// Adds the parts in their order, four channels per thread.
+template <typename T, int DK, int DV>
+__global__ __launch_bounds__(kThreads) void attn_bwd_sum_kernel(BwdK a) {
+    constexpr int kRow = (DK + DV) / 4;
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    const int64_t tokens = a.cu == nullptr ? a.T : min(static_cast<int64_t>(max(a.cu[a.N], 0)), a.T);
+    const int64_t row = i / kRow;
+    if (row >= tokens * a.Hkv) return;
+    const int ch = static_cast<int>(i % kRow) * 4;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int p = 0; p < a.parts; ++p) {
+        float x[4];
+        ld4(a.part + (static_cast<int64_t>(p) * a.T * a.Hkv + row) * (DK + DV) + ch, x);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[e] += x[e];
+    }
+    if (ch < DK) st4(static_cast<T*>(a.dk) + row * DK + ch, sum);
+    else st4(static_cast<T*>(a.dv) + row * DV + ch - DK, sum);
+}
+
+// Into how many parts the work of a key tile is cut: enough workgroups to
+// fill the chip several times, since their lengths differ.
+int dkv_parts(int64_t T, int N, int Hkv) {
+    const int64_t units = attn_tiles(T, N, kRows) * Hkv;
+    if (units == 0) return 1;
+    const int64_t parts = (1024 + units - 1) / units;
+    return static_cast<int>(parts < 1 ? 1 : parts > 8 ? 8 : parts);
 }
 
 size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -329,6 +401,9 @@ hipError_t launch_bwd(const AttnBackwardArgs& a, hipStream_t s) {
     k.delta = reinterpret_cast<float*>(ws);
     ws += up256(static_cast<size_t>(f.T) * f.H * 4);
     k.dog = f.z != nullptr ? static_cast<void*>(ws) : const_cast<void*>(a.dy);
+    if (f.z != nullptr) ws += up256(static_cast<size_t>(f.T) * f.H * DV * sizeof(T));
+    k.parts = dkv_parts(f.T, f.N, f.Hkv);
+    k.part = reinterpret_cast<float*>(ws);
     hipError_t e = allow_lds(attn_bwd_dq_kernel<T, DK, DV>, DqSizes<T, DK, DV>::kLds);
     if (e == hipSuccess) e = allow_lds(attn_bwd_dkv_kernel<T, DK, DV>, DkvSizes<T, DK, DV>::kLds);
     if (e != hipSuccess) return e;
@@ -342,10 +417,17 @@ hipError_t launch_bwd(const AttnBackwardArgs& a, hipStream_t s) {
     const int64_t tiles = attn_tiles(f.T, f.N, kRows);
     {
         LaunchTimer timer("attn_bwd_dkv", s);
-        attn_bwd_dkv_kernel<T, DK, DV><<<dim3(static_cast<unsigned>(tiles * f.Hkv)), dim3(kThreads), DkvSizes<T, DK, DV>::kLds, s>>>(k);
+        attn_bwd_dkv_kernel<T, DK, DV><<<dim3(static_cast<unsigned>(tiles * f.Hkv * k.parts)), dim3(kThreads), DkvSizes<T, DK, DV>::kLds, s>>>(k);
     }
     e = hipGetLastError();
     if (e != hipSuccess) return e;
+    if (k.parts > 1) {
+        LaunchTimer timer("attn_bwd_sum", s);
+        const int64_t threads = f.T * f.Hkv * ((DK + DV) / 4);
+        attn_bwd_sum_kernel<T, DK, DV><<<dim3(static_cast<unsigned>((threads + kThreads - 1) / kThreads)), dim3(kThreads), 0, s>>>(k);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
     {
         LaunchTimer timer("attn_bwd_dq", s);
         attn_bwd_dq_kernel<T, DK, DV><<<dim3(static_cast<unsigned>(tiles * f.H)), dim3(kThreads), DqSizes<T, DK, DV>::kLds, s>>>(k);
@@ -357,7 +439,9 @@ hipError_t launch_bwd(const AttnBackwardArgs& a, hipStream_t s) {
 
 size_t attn_backward_workspace_bytes(int64_t T, int N, int H, int Hkv, int dk, int dv, DT x, bool gate) {
     const size_t rows = static_cast<size_t>(T) * H;
-    return up256(rows * 4) + (gate ? up256(rows * dv * (x == DT::BF16 ? 2 : 4)) : 0);
+    const int parts = dkv_parts(T, N, Hkv);
+    return up256(rows * 4) + (gate ? up256(rows * dv * (x == DT::BF16 ? 2 : 4)) : 0) +
+           (parts > 1 ? up256(static_cast<size_t>(parts) * T * Hkv * (dk + dv) * 4) : 0);
 }
 
 hipError_t launch_attn_prefill_backward(const AttnBackwardArgs& a, hipStream_t s) {

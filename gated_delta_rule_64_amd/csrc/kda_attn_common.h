@@ -69,40 +69,17 @@ __device__ __forceinline__ u32x4 as_operand<float>(const f32x16& x, int p) {
     return r;
 }
 
-// The A operand that goes with as_operand(x, p): the transpose of a row-major
-// LDS tile [32 rows][stride elements], its 32 columns from `col` as operand
-// rows, contraction over the tile's rows in the order in which the lane's half
-// holds them (see above).  For bf16 two transposing LDS reads of four rows
-// each: in a group of 16 lanes, lane i names row r0 + (i >> 2) at column
-// col + 4 (i & 3) and receives column col + i of rows r0 .. r0 + 3.
+// The A operand that goes with as_operand(x, p) is the transpose of a row-major
+// LDS tile: 32 columns as operand rows, contraction over the tile's rows in the
+// order in which the lane's half holds them.  For bf16 two transposing LDS
+// reads of four rows each: in a group of 16 lanes, lane i names row
+// r0 + (i >> 2) at column col + 4 (i & 3) and receives column col + i of rows
+// r0 .. r0 + 3 (TileRead::columns).
 typedef short tr16_v4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ uint2 lds_read_tr(const char* p) {
     const tr16_v4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) tr16_v4*)(p));
     return __builtin_bit_cast(uint2, v);
 }
-template <typename T, int kStride>  // stride in bytes
-__device__ __forceinline__ u32x4 transposed(const char* tile, int col, int p, int lane);
-template <int kStride>
-struct TransposedOf {
-    static __device__ __forceinline__ u32x4 get(const bf16*, const char* tile, int col, int p, int lane) {
-        const int i = lane & 15, h = lane >> 5, g = (lane >> 4) & 1;
-        const char* at = tile + (16 * p + 4 * h + (i >> 2)) * kStride + (col + 16 * g + 4 * (i & 3)) * 2;
-        const uint2 a = lds_read_tr(at), b = lds_read_tr(at + 8 * kStride);
-        return u32x4{a.x, a.y, b.x, b.y};
-    }
-    static __device__ __forceinline__ u32x4 get(const float*, const char* tile, int col, int p, int lane) {
-        const char* at = tile + (8 * p + 4 * (lane >> 5)) * kStride + (col + (lane & 31)) * 4;
-        u32x4 r;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) r[i] = *reinterpret_cast<const uint32_t*>(at + i * kStride);
-        return r;
-    }
-};
-template <typename T, int kStride>
-__device__ __forceinline__ u32x4 transposed(const char* tile, int col, int p, int lane) {
-    return TransposedOf<kStride>::get(static_cast<const T*>(nullptr), tile, col, p, lane);
-}
-
 // Larger of the two halves' values (lanes l and l + 32)
 __device__ __forceinline__ float xor32_max(float x) {
     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -226,15 +203,92 @@ __device__ __forceinline__ Tile find_tile(const int32_t* cu, int N, int64_t T, i
     return t;
 }
 
-// Copy of a tile [kRows][kCols] (rows of `row_bytes` in memory, kPad bytes of
-// padding behind each row in LDS) in two steps: load() puts this thread's
-// 16-byte pieces in flight, store() writes them to LDS.
-template <typename T, int kRows, int kCols, int kPad, int kThreads>
+// A tile in LDS without padding: rows of kPieces 16-byte pieces, piece p of row
+// r stored in place p ^ turn(r).  LDS has 64 banks of 4 bytes, 16 pieces side
+// by side, and the turn is such that neither way of reading meets itself in a
+// bank: the same piece of 16 rows (operand rows), or 64 bytes of each of four
+// neighbouring rows (transposed).  It depends on r % 16 alone.
+template <int kPieces>
+__device__ __forceinline__ int turn(int r) {
+    if constexpr (kPieces % 16 == 0) return (r & 3) << 2 | (r >> 2 & 3);      // a row fills the banks
+    else if constexpr (kPieces % 8 == 0) return (r >> 1 & 1) << 2 | (r >> 2 & 3);  // rows start 8 pieces apart
+    else if constexpr (kPieces == 4) return r >> 2 & 3;
+    else return r >> 3 & 1;
+}
+
+// Reads of such a tile (columns of T, kCols a row) by one lane.  The lane's
+// offsets are computed once; tiles, rows 32 apart and neighbouring tiles in
+// LDS are constant offsets from them.
+template <typename T, int kCols>
+struct TileRead {
+    static constexpr int kRow = kCols * static_cast<int>(sizeof(T));
+    static constexpr int kPieces = kRow / 16;
+    static constexpr int kOps = kPieces / 2;          // operand pieces of a row, per half
+    static constexpr int kTiles = (kCols + 31) / 32;  // 32-column tiles, transposed
+    // bf16: the offsets themselves; fp32, whose products leave the vector
+    // units idle and whose rows would take twice the registers: what they are
+    // made of
+    static constexpr bool kStored = sizeof(T) == 2;
+    int row[kStored ? kOps : 2];
+    int col[kStored ? kTiles : 1][2];
+    // operand rows: this lane's row is c
+    __device__ __forceinline__ void init_rows(int c, int half) {
+        if constexpr (kStored) {
+#pragma unroll
+            for (int p = 0; p < kOps; ++p) row[p] = c * kRow + ((2 * p + half) ^ turn<kPieces>(c)) * 16;
+        } else {
+            row[0] = c * kRow;
+            row[1] = (half ^ turn<kPieces>(c)) * 16;
+        }
+    }
+    __device__ __forceinline__ u32x4 rows(const char* tile, int p) const {
+        return *reinterpret_cast<const u32x4*>(tile + (kStored ? row[kStored ? p : 0] : row[0] + (row[1] ^ 32 * p)));
+    }
+    // transposed: see lds_read_tr for which lane names which element.  A
+    // 32-column tile of a narrower matrix reads into the row behind it, and
+    // up to 64 bytes behind the last; those results are not used.
+    __device__ __forceinline__ void init_columns(int lane) {
+        const int half = lane >> 5;
+        if constexpr (sizeof(T) == 2) {
+            const int i = lane & 15, g = lane >> 4 & 1;
+            const int r = 4 * half + (i >> 2);
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) {
+                const int piece = 4 * t + 2 * g + ((i & 3) >> 1);
+                col[t][0] = r * kRow + (piece ^ turn<kPieces>(r)) * 16 + (i & 1) * 8;
+                col[t][1] = (r + 8) * kRow + (piece ^ turn<kPieces>(r + 8)) * 16 + (i & 1) * 8;
+            }
+        } else {
+            col[0][0] = (lane & 31) * 4;
+            col[0][1] = 4 * half;
+        }
+    }
+    __device__ __forceinline__ u32x4 columns(const char* tile, int t, int p) const {
+        if constexpr (sizeof(T) == 2) {
+            const uint2 a = lds_read_tr(tile + 16 * p * kRow + col[t][0]), b = lds_read_tr(tile + 16 * p * kRow + col[t][1]);
+            return u32x4{a.x, a.y, b.x, b.y};
+        } else {
+            u32x4 r;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int at = 8 * p + col[0][1] + i;
+                r[i] = *reinterpret_cast<const uint32_t*>(tile + at * kRow + ((128 * t + col[0][0]) ^ turn<kPieces>(at) * 16));
+            }
+            return r;
+        }
+    }
+};
+constexpr int kTrSlack = 64;
+
+// Copy of kRows rows into such a tile in two steps: load() puts this thread's
+// pieces in flight, store() writes them to LDS.
+template <typename T, int kRows, int kCols, int kThreads>
 struct TileCopy {
-    static constexpr int kRowPieces = kCols * static_cast<int>(sizeof(T)) / 16;
+    static constexpr int kRow = kCols * static_cast<int>(sizeof(T));
+    static constexpr int kRowPieces = kRow / 16;
     static constexpr int kPieces = kRows * kRowPieces;
     static constexpr int kEach = (kPieces + kThreads - 1) / kThreads;
-    static constexpr int kStride = kCols * static_cast<int>(sizeof(T)) + kPad;
+    static constexpr int kBytes = kRows * kRow;
     u32x4 r[kEach];
     __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t src, int row_bytes, int tid) {
 #pragma unroll
@@ -247,24 +301,16 @@ struct TileCopy {
     __device__ __forceinline__ void store(char* dst, int tid) const {
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
-            const int p = tid + i * kThreads;
+            const int p = tid + i * kThreads, row = p / kRowPieces;
             if (kPieces % kThreads == 0 || p < kPieces)
-                *reinterpret_cast<u32x4*>(dst + (p / kRowPieces) * kStride + (p % kRowPieces) * 16) = r[i];
+                *reinterpret_cast<u32x4*>(dst + row * kRow + (p % kRowPieces ^ turn<kRowPieces>(row)) * 16) = r[i];
         }
     }
 };
 
-// LDS row padding in bytes.  Rows read as operand pieces (16 bytes a lane, 32
-// rows): 16 bytes, so that neighbouring rows start four banks apart.  Rows
-// read transposed (four rows of 64 bytes at once): such that four rows start
-// 16 banks apart.
-constexpr int kRowPad = 16;
-constexpr int tr_pad(int row_bytes) { return (256 + 64 - row_bytes % 128) % 128; }
-// both ways: a compromise, two rows share a bank in either read
-constexpr int kBothPad = 32;
-// bytes of LDS that a transposed read may touch behind a tile whose rows are
-// shorter than the 32 columns of an operand (the results are not used)
-constexpr int kTrSlack = 64;
+// Workgroup barrier that orders LDS accesses only: loads from memory stay in
+// flight across it.
+__device__ __forceinline__ void tile_barrier() { lds_barrier(); }
 
 }  // namespace attn
 }  // namespace kda

@@ -33,22 +33,20 @@ struct FwdK {
 
 template <typename T, int DK, int DV>
 struct FwdSizes {
-    static constexpr int kKeys = 64;  // keys of a tile
-    static constexpr int kKStride = DK * static_cast<int>(sizeof(T)) + kRowPad;
-    static constexpr int kVStride = DV * static_cast<int>(sizeof(T)) + tr_pad(DV * sizeof(T));
-    static constexpr int kLds = kKeys * (kKStride + kVStride) + kTrSlack;
+    static constexpr int kKeys = sizeof(T) == 4 && DK > 64 ? 32 : 64;  // keys of a tile
+    static constexpr int kBuf = kKeys * (DK + DV) * static_cast<int>(sizeof(T));
+    static constexpr int kLds = 2 * kBuf + kTrSlack;
 };
 
 template <typename T, int DK, int DV>
-__global__ __launch_bounds__(kThreads) void attn_fwd_kernel(FwdK a) {
+__global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && DK <= 128 ? 2 : 1)) void attn_fwd_kernel(FwdK a) {
     using Sz = FwdSizes<T, DK, DV>;
     constexpr int kKeys = Sz::kKeys, kSub = kKeys / 32;
     constexpr int kQPieces = DK / (2 * Elem<T>::kPer16);  // operand pieces per lane of a query or key row
     constexpr int kVTiles = (DV + 31) / 32;
     constexpr int kP = Elem<T>::kPieces;
     extern __shared__ __align__(16) char smem[];
-    char* sK = smem;
-    char* sV = smem + kKeys * Sz::kKStride;
+    constexpr int kV = kKeys * DK * static_cast<int>(sizeof(T));  // the values, behind the keys
 
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int c = lane & 31, half = lane >> 5;
@@ -75,8 +73,12 @@ __global__ __launch_bounds__(kThreads) void attn_fwd_kernel(FwdK a) {
 #pragma unroll
     for (int i = 0; i < kVTiles; ++i) acc[i] = f32x16{};
 
-    TileCopy<T, kKeys, DK, kRowPad, kThreads> ck;
-    TileCopy<T, kKeys, DV, tr_pad(DV * sizeof(T)), kThreads> cv;
+    TileCopy<T, kKeys, DK, kThreads> ck;
+    TileCopy<T, kKeys, DV, kThreads> cv;
+    TileRead<T, DK> rk;
+    TileRead<T, DV> rv;
+    rk.init_rows(c, half);
+    rv.init_columns(lane);
     const int last = min(t.level * kQ + kQ, t.len);  // keys [0, last) are attended by some row
     const T* kbase = static_cast<const T*>(a.k) + kvh * DK;
     const T* vbase = static_cast<const T*>(a.v) + kvh * DV;
@@ -84,23 +86,20 @@ __global__ __launch_bounds__(kThreads) void attn_fwd_kernel(FwdK a) {
         ck.load(rows_of(kbase, t.start + j0, k_row, min(kKeys, t.len - j0)), k_row, tid);
         cv.load(rows_of(vbase, t.start + j0, v_row, min(kKeys, t.len - j0)), v_row, tid);
     };
-    fetch(0);
-    for (int j0 = 0; j0 < last; j0 += kKeys) {
-        __syncthreads();  // every wave is done with the tile before
-        ck.store(sK, tid);
-        cv.store(sV, tid);
-        if (j0 + kKeys < last) fetch(j0 + kKeys);
-        __syncthreads();
-        if (j0 > q0 + 31) continue;  // nothing of this tile is attended by this wave's rows
-
+    // Two tiles in LDS: while one is worked on, the next one's rows arrive in
+    // registers and are stored behind it; one barrier a tile.
+    auto put = [&](char* buf) {
+        ck.store(buf, tid);
+        cv.store(buf + kV, tid);
+    };
+    auto work = [&](const char* sK, int j0) {
+        const char* sV = sK + kV;
         f32x16 s[kSub];
 #pragma unroll
         for (int u = 0; u < kSub; ++u) {
             s[u] = f32x16{};
-            const char* row = sK + (32 * u + c) * Sz::kKStride + half * 16;
 #pragma unroll
-            for (int p = 0; p < kQPieces; ++p)
-                s[u] = mma<T>(*reinterpret_cast<const u32x4*>(row + p * 32), qf[p], s[u]);
+            for (int p = 0; p < kQPieces; ++p) s[u] = mma<T>(rk.rows(sK + 32 * u * rk.kRow, p), qf[p], s[u]);
         }
         if (j0 + kKeys - 1 > q0) {  // the diagonal: keys behind the row's own are not attended
             const int most = q0 + c - j0 - 4 * half;
@@ -137,8 +136,21 @@ __global__ __launch_bounds__(kThreads) void attn_fwd_kernel(FwdK a) {
                 const u32x4 b = as_operand<T>(s[u], p);
 #pragma unroll
                 for (int i = 0; i < kVTiles; ++i)
-                    acc[i] = mma<T>(transposed<T, Sz::kVStride>(sV + 32 * u * Sz::kVStride, 32 * i, p, lane), b, acc[i]);
+                    acc[i] = mma<T>(rv.columns(sV + 32 * u * rv.kRow, i, p), b, acc[i]);
             }
+    };
+    fetch(0);
+    put(smem);
+    for (int j0 = 0; j0 < last; j0 += 2 * kKeys) {
+        tile_barrier();
+        if (j0 + kKeys < last) fetch(j0 + kKeys);
+        if (j0 <= q0 + 31) work(smem, j0);  // else nothing of the tile is attended by this wave's rows
+        if (j0 + kKeys >= last) break;
+        put(smem + Sz::kBuf);
+        tile_barrier();
+        if (j0 + 2 * kKeys < last) fetch(j0 + 2 * kKeys);
+        if (j0 + kKeys <= q0 + 31) work(smem + Sz::kBuf, j0 + kKeys);
+        if (j0 + 2 * kKeys < last) put(smem);
     }
 
     // epilogue: lane c's query; registers 4 i .. 4 i + 3 of a tile are four

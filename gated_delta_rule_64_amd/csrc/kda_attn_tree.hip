@@ -43,9 +43,7 @@ struct TreeK {
 
 template <typename T, int DK, int DV, int NQ>
 struct TreeSizes {
-    static constexpr int kKStride = DK * static_cast<int>(sizeof(T)) + kRowPad;
-    static constexpr int kVStride = DV * static_cast<int>(sizeof(T)) + tr_pad(DV * sizeof(T));
-    static constexpr int kTile = (kKeys * (kKStride + kVStride) + kTrSlack + 15) / 16 * 16;
+    static constexpr int kTile = kKeys * (DK + DV) * static_cast<int>(sizeof(T)) + kTrSlack;
     static constexpr int kWaves = 4 * kTile <= 160 * 1024 ? 4 : 2;
     static constexpr int kVTiles = (DV + 31) / 32;
     static constexpr int kPart = NQ * kVTiles * 16 * 64 * 4;        // one wave's sums
@@ -94,7 +92,11 @@ __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV, NQ>::kWaves)) void attn_
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int c = lane & 31, half = lane >> 5;
     char* sK = smem + wave * Sz::kTile;
-    char* sV = sK + kKeys * Sz::kKStride;
+    char* sV = sK + kKeys * kKRow;
+    TileRead<T, DK> rk;
+    TileRead<T, DV> rv;
+    rk.init_rows(c, half);
+    rv.init_columns(lane);
 
     const int G = a.H / a.Hkv, rows = a.T * G;
     int id = blockIdx.x;
@@ -208,13 +210,15 @@ __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV, NQ>::kWaves)) void attn_
                 for (int i = 0; i < kKEach; ++i) {
                     const int p = lane + 64 * i;
                     if (p < 16 * kKRow / 16)
-                        *reinterpret_cast<u32x4*>(sK + (16 * x + p / (kKRow / 16)) * Sz::kKStride + p % (kKRow / 16) * 16) = kr[x][i];
+                        *reinterpret_cast<u32x4*>(sK + (16 * x + p / (kKRow / 16)) * kKRow +
+                                                  (p % (kKRow / 16) ^ turn<kKRow / 16>(p / (kKRow / 16))) * 16) = kr[x][i];
                 }
 #pragma unroll
                 for (int i = 0; i < kVEach; ++i) {
                     const int p = lane + 64 * i;
                     if (p < 16 * kVRow / 16)
-                        *reinterpret_cast<u32x4*>(sV + (16 * x + p / (kVRow / 16)) * Sz::kVStride + p % (kVRow / 16) * 16) = vr[x][i];
+                        *reinterpret_cast<u32x4*>(sV + (16 * x + p / (kVRow / 16)) * kVRow +
+                                                  (p % (kVRow / 16) ^ turn<kVRow / 16>(p / (kVRow / 16))) * 16) = vr[x][i];
                 }
             }
             const int n0 = there[0], n1 = there[1];
@@ -226,9 +230,8 @@ __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV, NQ>::kWaves)) void attn_
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
                 f32x16 s{};
-                const char* kp = sK + c * Sz::kKStride + half * 16;
 #pragma unroll
-                for (int p = 0; p < kQPieces; ++p) s = mma<T>(*reinterpret_cast<const u32x4*>(kp + p * 32), qf[n][p], s);
+                for (int p = 0; p < kQPieces; ++p) s = mma<T>(rk.rows(sK, p), qf[n][p], s);
                 if (draft) {
                     const uint64_t bits = seen[n] >> draft0;
 #pragma unroll
@@ -264,7 +267,7 @@ __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV, NQ>::kWaves)) void attn_
                     const u32x4 x = as_operand<T>(s, p);
 #pragma unroll
                     for (int i = 0; i < kVTiles; ++i)
-                        acc[n][i] = mma<T>(transposed<T, Sz::kVStride>(sV, 32 * i, p, lane), x, acc[n][i]);
+                        acc[n][i] = mma<T>(rv.columns(sV, i, p), x, acc[n][i]);
                 }
             }
         }

@@ -78,6 +78,7 @@ def test_backward_refuses(lib, kw, status, word):
 
 def test_backward_workspace(lib):
     w = lib.kda_attn_backward_workspace_bytes
+    assert w(0, 1, 4, 2, 64, 64, 1, 1) == 0  # no tokens: nothing is needed
     assert w(64, 1, 4, 2, 64, 64, 1, 1) > w(64, 1, 4, 2, 64, 64, 1, 0) >= 64 * 4 * 4
     assert w(64, 1, 4, 3, 64, 64, 1, 0) == 0 and w(64, 1, 4, 2, 64, 32, 1, 0) == 0 and w(-1, 1, 4, 2, 64, 64, 1, 0) == 0
 
