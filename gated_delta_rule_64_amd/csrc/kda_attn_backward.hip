@@ -158,7 +158,7 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && DK <= 128 ? 2 : 1)) vo
         ck.store(buf, tid);
         cv.store(buf + kV, tid);
     };
-    auto work = [&](const char* sK, int j0) {
+    auto work = [&](const char* sK, int j0) __attribute__((always_inline)) {
         const char* sV = sK + kV;
 #pragma unroll
         for (int u = 0; u < kSub; ++u) {
@@ -169,12 +169,13 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && DK <= 128 ? 2 : 1)) vo
             for (int p = 0; p < kQPieces; ++p) s = mma<T>(rk.rows(sK + 32 * u * rk.kRow, p), qf[p], s);
 #pragma unroll
             for (int p = 0; p < kVPieces; ++p) dp = mma<T>(rv.rows(sV + 32 * u * rv.kRow, p), of[p], dp);
-            const int most = q0 + c - k0 - 4 * half;
-            const bool diagonal = k0 + 31 > q0;
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const float p = __builtin_amdgcn_exp2f(fmaf(s[r], sc, -lse2));
-                s[r] = diagonal && 8 * (r / 4) + r % 4 > most ? 0.f : p * (dp[r] - delta);
+            for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], sc, -lse2)) * (dp[r] - delta);
+            if (k0 + 31 > q0) {  // the diagonal: keys behind the row's own are not attended
+                const int most = opaque(q0 + c - k0 - 4 * half);
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (8 * (r / 4) + r % 4 > most) s[r] = 0.f;
             }
 #pragma unroll
             for (int p = 0; p < kP; ++p) {
@@ -186,6 +187,8 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && DK <= 128 ? 2 : 1)) vo
         }
     };
     fetch(0);
+    arrive(qf);
+    arrive(of);
     put(smem);
     for (int j0 = 0; j0 < last; j0 += 2 * kKeys) {
         tile_barrier();
@@ -289,7 +292,7 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_dkv_kernel(BwdK a) {
         co.store(buf + kO, tid);
         if (tid < 2 * kQ) reinterpret_cast<float*>(buf + kS)[tid] = stat;
     };
-    auto work = [&](const char* sQ, int n) {
+    auto work = [&](const char* sQ, int n) __attribute__((always_inline)) {
         const int i0 = k_first + (n % steps) * kQ;
         if (i0 + kQ - 1 < k0) return;  // queries before this wave's keys
         const char* sO = sQ + kO;
@@ -300,8 +303,6 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_dkv_kernel(BwdK a) {
 #pragma unroll
         for (int p = 0; p < kVPieces; ++p) dp = mma<T>(ro.rows(sO, p), kKeep ? vf[kKeep ? p : 0] : buffer_load16(vs, v_at + p * 32), dp);
         // register r: query i0 + 8 (r / 4) + 4 half + r % 4; key k0 + c
-        const int least = k0 + c - i0 - 4 * half;
-        const bool diagonal = i0 < k0 + 31;
 #pragma unroll
         for (int r4 = 0; r4 < 4; ++r4) {
             const f32x4 ls = *reinterpret_cast<const f32x4*>(sLse + 8 * r4 + 4 * half);
@@ -309,11 +310,15 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_dkv_kernel(BwdK a) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int r = 4 * r4 + e;
-                float p = __builtin_amdgcn_exp2f(fmaf(s[r], sc, -ls[e]));
-                if (diagonal && 8 * r4 + e < least) p = 0.f;
-                s[r] = p;
-                dp[r] = p * (dp[r] - de[e]);
+                s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], sc, -ls[e]));
+                dp[r] = s[r] * (dp[r] - de[e]);
             }
+        }
+        if (i0 < k0 + 31) {  // the diagonal: queries before the key do not attend it
+            const int least = opaque(k0 + c - i0 - 4 * half);
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                if (8 * (r / 4) + r % 4 < least) s[r] = dp[r] = 0.f;
         }
 #pragma unroll
         for (int p = 0; p < kP; ++p) {
@@ -325,6 +330,10 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_dkv_kernel(BwdK a) {
         }
     };
     int n = static_cast<int>(all * part / a.parts);
+    if constexpr (kKeep) {
+        arrive(kf);
+        arrive(vf);
+    }
     if (n < n_end) {
         fetch(n);
         put(smem);

@@ -25,6 +25,12 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
+// The maximum that softmax weights are taken against moves only when a row
+// outgrows it by 2^kRise: until then they stay below 2^kRise, which fp32 sums
+// and bf16 weights hold as well as 1.  Most tiles then leave the sums as they
+// are (16 multiplications per 32 channels and lane).
+constexpr float kRise = 6.f;
+
 constexpr int kBufferDword3 = 0x00020000;  // raw buffer: byte offsets, reads past the end give 0
 
 // One 16-byte operand piece of A times one of B, added to a 32 x 32 result.
@@ -90,6 +96,23 @@ __device__ __forceinline__ u32x4 buffer_load16(__amdgpu_buffer_rsrc_t r, int off
     return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, offset, 0, 0));
 }
 
+// A value that the compiler knows nothing about.  A mask inside a wave-uniform
+// branch compares with such a value and so stays in its branch: turned into
+// selects, what one tile in many needs would cost every tile its compares.
+__device__ __forceinline__ int opaque(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
+// Waits for loads that a loop uses in every pass.  Left to their first use
+// inside the loop, the wait there (a count of loads in flight) would also wait
+// for the tile that the pass has just put in flight, in every pass.
+template <int N>
+__device__ __forceinline__ void arrive(u32x4 (&x)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+v"(x[i]));
+}
+
 // A wave-uniform value in scalar registers.
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 __device__ __forceinline__ int64_t uniform64(int64_t x) {
@@ -104,7 +127,10 @@ __device__ __forceinline__ int64_t uniform64(int64_t x) {
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const void* base, int64_t first, int64_t row_bytes, int rows) {
     const char* p = static_cast<const char*>(base) + first * row_bytes;
     const int64_t bytes = rows > 0 ? rows * row_bytes : 0;
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), 0, static_cast<int>(bytes), kBufferDword3);
+    // (the same in every lane, and said so: a descriptor that the compiler
+    // takes for different ones makes a loop over the lanes of every load)
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<char*>(uniform64(reinterpret_cast<int64_t>(p))), 0,
+                                             uniform(static_cast<int>(bytes)), kBufferDword3);
 }
 
 // One tile of a packed batch: rows [start + first, start + len) of the tensor

@@ -33,13 +33,13 @@ struct FwdK {
 
 template <typename T, int DK, int DV>
 struct FwdSizes {
-    static constexpr int kKeys = sizeof(T) == 4 && DK > 64 ? 32 : 64;  // keys of a tile
+    static constexpr int kKeys = DK > 128 || (sizeof(T) == 4 && DK > 64) ? 32 : 64;  // keys of a tile
     static constexpr int kBuf = kKeys * (DK + DV) * static_cast<int>(sizeof(T));
     static constexpr int kLds = 2 * kBuf + kTrSlack;
 };
 
 template <typename T, int DK, int DV>
-__global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && DK <= 128 ? 2 : 1)) void attn_fwd_kernel(FwdK a) {
+__global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void attn_fwd_kernel(FwdK a) {
     using Sz = FwdSizes<T, DK, DV>;
     constexpr int kKeys = Sz::kKeys, kSub = kKeys / 32;
     constexpr int kQPieces = DK / (2 * Elem<T>::kPer16);  // operand pieces per lane of a query or key row
@@ -92,7 +92,8 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && DK <= 128 ? 2 : 1)) vo
         ck.store(buf, tid);
         cv.store(buf + kV, tid);
     };
-    auto work = [&](const char* sK, int j0) {
+    auto work = [&](const char* sK, int j0) __attribute__((always_inline)) {
+        if (j0 > q0 + 31) return;  // nothing of the tile is attended by this wave's rows
         const char* sV = sK + kV;
         f32x16 s[kSub];
 #pragma unroll
@@ -102,7 +103,7 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && DK <= 128 ? 2 : 1)) vo
             for (int p = 0; p < kQPieces; ++p) s[u] = mma<T>(rk.rows(sK + 32 * u * rk.kRow, p), qf[p], s[u]);
         }
         if (j0 + kKeys - 1 > q0) {  // the diagonal: keys behind the row's own are not attended
-            const int most = q0 + c - j0 - 4 * half;
+            const int most = opaque(q0 + c - j0 - 4 * half);
 #pragma unroll
             for (int u = 0; u < kSub; ++u)
 #pragma unroll
@@ -114,10 +115,16 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && DK <= 128 ? 2 : 1)) vo
         for (int u = 0; u < kSub; ++u)
 #pragma unroll
             for (int r = 0; r < 16; ++r) top = fmaxf(top, s[u][r]);
-        top = fmaxf(xor32_max(top), m);
-        const float alpha = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - top) * sc);
-        m = top;
-        const float ms = top == -INFINITY ? 0.f : top * sc;
+        top = xor32_max(top);
+        if (__any((top - m) * sc > kRise)) {  // m is -infinity at first
+            const float next = fmaxf(m, top);
+            const float alpha = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - next) * sc);
+            m = next;
+            l *= alpha;
+#pragma unroll
+            for (int i = 0; i < kVTiles; ++i) acc[i] *= alpha;
+        }
+        const float ms = m == -INFINITY ? 0.f : m * sc;
         float sum = 0.f;
 #pragma unroll
         for (int u = 0; u < kSub; ++u)
@@ -126,9 +133,7 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && DK <= 128 ? 2 : 1)) vo
                 s[u][r] = __builtin_amdgcn_exp2f(fmaf(s[u][r], sc, -ms));
                 sum += s[u][r];
             }
-        l = l * alpha + sum;
-#pragma unroll
-        for (int i = 0; i < kVTiles; ++i) acc[i] *= alpha;
+        l += sum;
 #pragma unroll
         for (int u = 0; u < kSub; ++u)
 #pragma unroll
@@ -140,16 +145,17 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && DK <= 128 ? 2 : 1)) vo
             }
     };
     fetch(0);
+    arrive(qf);
     put(smem);
     for (int j0 = 0; j0 < last; j0 += 2 * kKeys) {
         tile_barrier();
         if (j0 + kKeys < last) fetch(j0 + kKeys);
-        if (j0 <= q0 + 31) work(smem, j0);  // else nothing of the tile is attended by this wave's rows
+        work(smem, j0);
         if (j0 + kKeys >= last) break;
         put(smem + Sz::kBuf);
         tile_barrier();
         if (j0 + 2 * kKeys < last) fetch(j0 + 2 * kKeys);
-        if (j0 + kKeys <= q0 + 31) work(smem + Sz::kBuf, j0 + kKeys);
+        work(smem + Sz::kBuf, j0 + kKeys);
         if (j0 + 2 * kKeys < last) put(smem);
     }
 

@@ -81,7 +81,7 @@ __device__ __forceinline__ void wave_lds_fence() {
 }
 
 template <typename T, int DK, int DV, int NQ>
-__global__ __launch_bounds__((64 * TreeSizes<T, DK, DV, NQ>::kWaves)) void attn_tree_kernel(TreeK a) {
+__global__ __launch_bounds__((64 * TreeSizes<T, DK, DV, NQ>::kWaves), (sizeof(T) == 2 && NQ == 1 && DK <= 128 ? 2 : 1)) void attn_tree_kernel(TreeK a) {
     using Sz = TreeSizes<T, DK, DV, NQ>;
     constexpr int kE = sizeof(T);
     constexpr int kQPieces = DK / (2 * Elem<T>::kPer16);
@@ -137,139 +137,190 @@ __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV, NQ>::kWaves)) void attn_
     int tile = split * each + wave;
 
     if (tile < t_end) {
-        u32x4 qf[NQ][kQPieces];
+        // the rows' queries stay in registers, but for the longest fp32 ones,
+        // which are read again from the caches for every tile
+        constexpr bool kKeep = kE == 2 || DK <= 128;
+        u32x4 qf[NQ][kKeep ? kQPieces : 1];
+        const char* q_row[NQ];
         uint64_t seen[NQ];
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
-            const char* src = static_cast<const char*>(a.q) + q_at[n] * kKRow + half * 16;
+            q_row[n] = static_cast<const char*>(a.q) + q_at[n] * kKRow + half * 16;
+            if constexpr (kKeep) {
 #pragma unroll
-            for (int p = 0; p < kQPieces; ++p) qf[n][p] = *reinterpret_cast<const u32x4*>(src + p * 32);
+                for (int p = 0; p < kQPieces; ++p) qf[n][p] = *reinterpret_cast<const u32x4*>(q_row[n] + p * 32);
+            }
             const int t = (mine[n] ? row[n] : 0) / G;
             seen[n] = a.mask != nullptr ? static_cast<uint64_t>(a.mask[static_cast<int64_t>(b) * a.T + t])
                                         : ~0ull >> (63 - t);
         }
         const float sc = a.scale * kLog2e;
 
-        // 16 rows of keys and of values in flight, as 16-byte pieces; twice a tile
-        constexpr int kKEach = (16 * kKRow / 16 + 63) / 64, kVEach = (16 * kVRow / 16 + 63) / 64;
-        u32x4 kr[2][kKEach], vr[2][kVEach];
-        int there[2];  // rows of each half tile that hold a token (whole wave)
-        auto fetch = [&](int n) {
+        // Half a tile: 16 rows of keys and of values, 16-byte pieces
+        constexpr int kKPieces = kKRow, kVPieces = kVRow;  // 16 rows of kRow / 16 pieces
+        constexpr int kKEach = (kKPieces + 63) / 64, kVEach = (kVPieces + 63) / 64;
+        // fp32 tiles, twice as large, do not fit beside the sums: their halves
+        // pass through the same registers when they are stored
+        constexpr bool kAhead = kE == 2 && (NQ == 1 || DK < 128);
+        u32x4 kr[kAhead ? 2 : 1][kKEach], vr[kAhead ? 2 : 1][kVEach];
+        // The table entries of a tile's halves, read as scalars: a vector load
+        // would have to be waited for behind the rows in flight.
+        typedef const __attribute__((address_space(4))) int32_t* scalar_ints;
+        const scalar_ints entries = (scalar_ints)(a.table + static_cast<int64_t>(slot) * a.max_pages);
+        struct Halves {
+            int page[2], rows[2];  // rows that hold a token
+        };
+        const int in_page = (1 << a.page_shift) - 1;
+        auto look_up = [&](int n) __attribute__((always_inline)) {
+            Halves e;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                __amdgpu_buffer_rsrc_t ks, vs;
-                int k_step = kKRow, v_step = kVRow;
-                if (n < ctx_tiles) {
-                    const int t0 = n * kKeys + 16 * x;
-                    int got = min(16, max(0, ctx - t0));
-                    int page = 0;
-                    if (got > 0) {
-                        page = a.table[static_cast<int64_t>(slot) * a.max_pages + (t0 >> a.page_shift)];
-                        if (page < 0 || page >= a.pages) got = 0;  // no such page: its tokens are not there
-                    }
-                    got = uniform(got);
-                    page = uniform(got > 0 ? page : 0);
-                    const int64_t first = ((static_cast<int64_t>(page) * a.Hkv + kvh) << a.page_shift) + (t0 & ((1 << a.page_shift) - 1));
-                    there[x] = got;
-                    ks = rows_of(a.k_cache, first, kKRow, got);
-                    vs = rows_of(a.v_cache, first, kVRow, got);
-                } else {
-                    const int t0 = (n - ctx_tiles) * kKeys + 16 * x;
-                    there[x] = min(16, max(0, a.T - t0));
-                    const int64_t first = static_cast<int64_t>(b) * a.T + t0;
-                    k_step = kKRow * a.Hkv;
-                    v_step = kVRow * a.Hkv;
-                    // bounded to the rows of this head: the last one ends inside its token's row
-                    const char* kb = static_cast<const char*>(a.k_new) + first * k_step + kvh * kKRow;
-                    const char* vb = static_cast<const char*>(a.v_new) + first * v_step + kvh * kVRow;
-                    ks = rows_of(kb, 0, k_step, there[x]);
-                    vs = rows_of(vb, 0, v_step, there[x]);
-                }
+                const int t0 = n * kKeys + 16 * x;
+                e.rows[x] = min(16, max(0, ctx - t0));
+                // (clamped: a column behind the context is not looked at)
+                e.page[x] = entries[min(t0, ctx - 1) >> a.page_shift];
+            }
+            return e;
+        };
+        auto fetch_half = [&](int n, Halves& e, int x) __attribute__((always_inline)) {
+            const bool there = e.page[x] >= 0 && e.page[x] < a.pages;  // else its tokens are not attended
+            e.rows[x] = there ? e.rows[x] : 0;
+            const int64_t head = static_cast<int64_t>(there ? e.page[x] : 0) * a.Hkv + kvh;
+            const int64_t first = (head << a.page_shift) + ((n * kKeys + 16 * x) & in_page);
+            const auto ks = rows_of(a.k_cache, first, kKRow, e.rows[x]);
+            const auto vs = rows_of(a.v_cache, first, kVRow, e.rows[x]);
+            const int to = kAhead ? x : 0;
 #pragma unroll
-                for (int i = 0; i < kKEach; ++i) {
-                    const int p = lane + 64 * i, r = p / (kKRow / 16);
-                    kr[x][i] = r < there[x] ? buffer_load16(ks, r * k_step + p % (kKRow / 16) * 16) : u32x4{};
-                }
+            for (int i = 0; i < kKEach; ++i)
+                if (kKPieces >= 64 || lane < kKPieces) kr[to][i] = buffer_load16(ks, (lane + 64 * i) * 16);
 #pragma unroll
-                for (int i = 0; i < kVEach; ++i) {
-                    const int p = lane + 64 * i, r = p / (kVRow / 16);
-                    vr[x][i] = r < there[x] ? buffer_load16(vs, r * v_step + p % (kVRow / 16) * 16) : u32x4{};
-                }
+            for (int i = 0; i < kVEach; ++i)
+                if (kVPieces >= 64 || lane < kVPieces) vr[to][i] = buffer_load16(vs, (lane + 64 * i) * 16);
+        };
+        auto put_half = [&](int x) __attribute__((always_inline)) {
+            const int from = kAhead ? x : 0;
+#pragma unroll
+            for (int i = 0; i < kKEach; ++i) {
+                const int p = lane + 64 * i, r = 16 * x + p / (kKRow / 16);
+                if (kKPieces >= 64 || lane < kKPieces)
+                    *reinterpret_cast<u32x4*>(sK + r * kKRow + (p % (kKRow / 16) ^ turn<kKRow / 16>(r)) * 16) = kr[from][i];
+            }
+#pragma unroll
+            for (int i = 0; i < kVEach; ++i) {
+                const int p = lane + 64 * i, r = 16 * x + p / (kVRow / 16);
+                if (kVPieces >= 64 || lane < kVPieces)
+                    *reinterpret_cast<u32x4*>(sV + r * kVRow + (p % (kVRow / 16) ^ turn<kVRow / 16>(r)) * 16) = vr[from][i];
             }
         };
-        // fp32 tiles are twice as large and do not fit beside the sums: they
-        // are fetched when they are stored
-        constexpr bool kAhead = kE == 2 && (NQ == 1 || DK < 128);
-        if (kAhead) fetch(tile);
-        for (; tile < t_end; tile += kWaves) {
-            if (!kAhead) fetch(tile);
+        // the tile in LDS; hide(scores, n) masks those of row block n
+        auto work = [&](auto hide) __attribute__((always_inline)) {
             wave_lds_fence();
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-#pragma unroll
-                for (int i = 0; i < kKEach; ++i) {
-                    const int p = lane + 64 * i;
-                    if (p < 16 * kKRow / 16)
-                        *reinterpret_cast<u32x4*>(sK + (16 * x + p / (kKRow / 16)) * kKRow +
-                                                  (p % (kKRow / 16) ^ turn<kKRow / 16>(p / (kKRow / 16))) * 16) = kr[x][i];
-                }
-#pragma unroll
-                for (int i = 0; i < kVEach; ++i) {
-                    const int p = lane + 64 * i;
-                    if (p < 16 * kVRow / 16)
-                        *reinterpret_cast<u32x4*>(sV + (16 * x + p / (kVRow / 16)) * kVRow +
-                                                  (p % (kVRow / 16) ^ turn<kVRow / 16>(p / (kVRow / 16))) * 16) = vr[x][i];
-                }
-            }
-            const int n0 = there[0], n1 = there[1];
-            const bool draft = tile >= ctx_tiles;
-            const int draft0 = (tile - ctx_tiles) * kKeys;
-            if (kAhead && tile + kWaves < t_end) fetch(tile + kWaves);
-            wave_lds_fence();
-
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
                 f32x16 s{};
 #pragma unroll
-                for (int p = 0; p < kQPieces; ++p) s = mma<T>(rk.rows(sK, p), qf[n][p], s);
-                if (draft) {
-                    const uint64_t bits = seen[n] >> draft0;
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const int key = 8 * (r / 4) + 4 * half + r % 4;
-                        if (draft0 + key >= a.T || (bits >> key & 1) == 0) s[r] = -INFINITY;
-                    }
-                } else if (n0 + n1 < kKeys) {
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const int key = 8 * (r / 4) + 4 * half + r % 4;
-                        if (key - (r >= 8 ? 16 : 0) >= (r >= 8 ? n1 : n0)) s[r] = -INFINITY;
-                    }
-                }
+                for (int p = 0; p < kQPieces; ++p) 
+                    s = mma<T>(rk.rows(sK, p), kKeep ? qf[n][kKeep ? p : 0] : *reinterpret_cast<const u32x4*>(q_row[n] + p * 32), s);
+                hide(s, n);
                 float top = s[0];
 #pragma unroll
                 for (int r = 1; r < 16; ++r) top = fmaxf(top, s[r]);
-                top = fmaxf(xor32_max(top), m[n]);
-                const float alpha = m[n] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m[n] - top) * sc);
-                m[n] = top;
-                const float ms = top == -INFINITY ? 0.f : top * sc;
+                top = xor32_max(top);
+                if (__any((top - m[n]) * sc > kRise)) {
+                    const float next = fmaxf(m[n], top);
+                    const float alpha = m[n] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m[n] - next) * sc);
+                    m[n] = next;
+                    l[n] *= alpha;
+#pragma unroll
+                    for (int i = 0; i < kVTiles; ++i) acc[n][i] *= alpha;
+                }
+                const float ms = m[n] == -INFINITY ? 0.f : m[n] * sc;
                 float sum = 0.f;
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
                     s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], sc, -ms));
                     sum += s[r];
                 }
-                l[n] = l[n] * alpha + sum;
-#pragma unroll
-                for (int i = 0; i < kVTiles; ++i) acc[n][i] *= alpha;
+                l[n] += sum;
 #pragma unroll
                 for (int p = 0; p < kP; ++p) {
                     const u32x4 x = as_operand<T>(s, p);
 #pragma unroll
-                    for (int i = 0; i < kVTiles; ++i)
-                        acc[n][i] = mma<T>(rv.columns(sV, i, p), x, acc[n][i]);
+                    for (int i = 0; i < kVTiles; ++i) acc[n][i] = mma<T>(rv.columns(sV, i, p), x, acc[n][i]);
                 }
             }
+        };
+        // register r of a score: key 8 (r / 4) + 4 half + r % 4 of the tile
+
+        // the committed tokens: a tile's rows are in flight while the one
+        // before is worked on, its table entries one tile earlier still
+        const int c_end = min(t_end, ctx_tiles);
+        if (tile < c_end) {
+            Halves now = look_up(tile), next = now;
+            if constexpr (kAhead) {
+                fetch_half(tile, now, 0);
+                fetch_half(tile, now, 1);
+            }
+            if (tile + kWaves < c_end) next = look_up(tile + kWaves);
+            if constexpr (kKeep) {
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) arrive(qf[n]);
+            }
+            for (; tile < c_end; tile += kWaves) {
+                wave_lds_fence();
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if constexpr (!kAhead) fetch_half(tile, now, x);
+                    put_half(x);
+                }
+                const int n0 = now.rows[0], n1 = now.rows[1];
+                if (tile + kWaves < c_end) {
+                    now = next;
+                    if constexpr (kAhead) {
+                        fetch_half(tile + kWaves, now, 0);
+                        fetch_half(tile + kWaves, now, 1);
+                    }
+                    if (tile + 2 * kWaves < c_end) next = look_up(tile + 2 * kWaves);
+                }
+                work([&](f32x16& s, int) __attribute__((always_inline)) {
+                    if (n0 + n1 == kKeys) return;
+                    const int lo = opaque(n0 - 4 * half), hi = opaque(n1 - 4 * half);
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (8 * (r / 4) + r % 4 - (r >= 8 ? 16 : 0) >= (r >= 8 ? hi : lo)) s[r] = -INFINITY;
+                });
+            }
+        }
+        // the drafts: dense rows, a tile or two
+        for (; tile < t_end; tile += kWaves) {
+            const int t0 = (tile - ctx_tiles) * kKeys;
+            const int k_step = kKRow * a.Hkv, v_step = kVRow * a.Hkv;
+            const char* kb = static_cast<const char*>(a.k_new) + (static_cast<int64_t>(b) * a.T + t0) * k_step + kvh * kKRow;
+            const char* vb = static_cast<const char*>(a.v_new) + (static_cast<int64_t>(b) * a.T + t0) * v_step + kvh * kVRow;
+            wave_lds_fence();
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int to = kAhead ? x : 0;
+#pragma unroll
+                for (int i = 0; i < kKEach; ++i) {
+                    const int p = lane + 64 * i, r = 16 * x + p / (kKRow / 16);
+                    kr[to][i] = t0 + r < a.T ? *reinterpret_cast<const u32x4*>(kb + static_cast<int64_t>(r) * k_step + p % (kKRow / 16) * 16) : u32x4{};
+                }
+#pragma unroll
+                for (int i = 0; i < kVEach; ++i) {
+                    const int p = lane + 64 * i, r = 16 * x + p / (kVRow / 16);
+                    vr[to][i] = t0 + r < a.T ? *reinterpret_cast<const u32x4*>(vb + static_cast<int64_t>(r) * v_step + p % (kVRow / 16) * 16) : u32x4{};
+                }
+                put_half(x);
+            }
+            work([&](f32x16& s, int n) __attribute__((always_inline)) {
+                const uint32_t bits = static_cast<uint32_t>(seen[n] >> t0) >> (4 * half);
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int key = 8 * (r / 4) + r % 4;
+                    if (t0 + 4 * half + key >= a.T || (bits >> key & 1) == 0) s[r] = -INFINITY;
+                }
+            });
         }
     }
 #pragma unroll
