@@ -166,9 +166,11 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && DK <= 128 ? 2 : 1)) vo
             if (k0 > q0 + 31) break;
             f32x16 s{}, dp{};
 #pragma unroll
-            for (int p = 0; p < kQPieces; ++p) s = mma<T>(rk.rows(sK + 32 * u * rk.kRow, p), qf[p], s);
-#pragma unroll
-            for (int p = 0; p < kVPieces; ++p) dp = mma<T>(rv.rows(sV + 32 * u * rv.kRow, p), of[p], dp);
+            for (int p = 0; p < kQPieces; ++p) {
+                s = mma<T>(rk.rows(sK + 32 * u * rk.kRow, p), qf[p], s);
+                if (p < kVPieces) dp = mma<T>(rv.rows(sV + 32 * u * rv.kRow, p), of[p < kVPieces ? p : 0], dp);
+            }
+            lookahead<kQPieces + kVPieces, 3, Elem<T>::kMfmas>();
 #pragma unroll
             for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], sc, -lse2)) * (dp[r] - delta);
             if (k0 + 31 > q0) {  // the diagonal: keys behind the row's own are not attended
@@ -209,7 +211,12 @@ struct DkvSizes {
     static constexpr int kQ = 32;  // queries of a step
     static constexpr int kStats = kQ * 2 * 4;  // lse and delta of the step's queries
     static constexpr int kBuf = kQ * (DK + DV) * static_cast<int>(sizeof(T)) + kStats;
-    static constexpr int kLds = 2 * kBuf + kTrSlack;
+    // Where a lane's sums, keys and values together exceed half its registers,
+    // the values are read from LDS for every step: two workgroups then share a
+    // CU, and one's products cover the other's exponentials and LDS reads.
+    static constexpr bool kValuesInLds = sizeof(T) == 2 && DK == 128;
+    static constexpr int kValues = kValuesInLds ? kRows * DV * static_cast<int>(sizeof(T)) : 0;
+    static constexpr int kLds = 2 * kBuf + kTrSlack + kValues;
 };
 
 // One workgroup per (tile of 128 keys, key head, part).  The tile's work is
@@ -217,7 +224,7 @@ struct DkvSizes {
 // parts cut it into equal pieces where there are few tiles, and their sums
 // (fp32) are added by attn_bwd_sum_kernel.
 template <typename T, int DK, int DV>
-__global__ __launch_bounds__(kThreads) void attn_bwd_dkv_kernel(BwdK a) {
+__global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && DK <= 128 ? 2 : 1)) void attn_bwd_dkv_kernel(BwdK a) {
     using Sz = DkvSizes<T, DK, DV>;
     constexpr int kQ = Sz::kQ;
     constexpr int kKPieces = DK / (2 * Elem<T>::kPer16), kVPieces = DV / (2 * Elem<T>::kPer16);
@@ -249,12 +256,21 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_dkv_kernel(BwdK a) {
     const auto ks = rows_of(static_cast<const T*>(a.k) + kvh * DK, t.start + k0, k_row, rows);
     const auto vs = rows_of(static_cast<const T*>(a.v) + kvh * DV, t.start + k0, v_row, rows);
     const int k_at = c * k_row + half * 16, v_at = c * v_row + half * 16;
-    u32x4 kf[kKeep ? kKPieces : 1], vf[kKeep ? kVPieces : 1];
+    constexpr bool kVLds = Sz::kValuesInLds, kVKeep = kKeep && !kVLds;
+    char* sV = smem + 2 * Sz::kBuf + kTrSlack;
+    u32x4 kf[kKeep ? kKPieces : 1], vf[kVKeep ? kVPieces : 1];
     if constexpr (kKeep) {
 #pragma unroll
         for (int s = 0; s < kKPieces; ++s) kf[s] = buffer_load16(ks, k_at + s * 32);
+    }
+    if constexpr (kVKeep) {
 #pragma unroll
         for (int s = 0; s < kVPieces; ++s) vf[s] = buffer_load16(vs, v_at + s * 32);
+    }
+    if constexpr (kVLds) {
+        TileCopy<T, kRows, DV, kThreads> cv;
+        cv.load(rows_of(static_cast<const T*>(a.v) + kvh * DV, t.start + k_first, v_row, min(kRows, t.len - k_first)), v_row, tid);
+        cv.store(sV, tid);
     }
     const float sc = a.scale * kLog2e;
     f32x16 gk[kKTiles], gv[kVTiles];
@@ -299,9 +315,17 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_dkv_kernel(BwdK a) {
         const float* sLse = reinterpret_cast<const float*>(sQ + kS);
         f32x16 s{}, dp{};
 #pragma unroll
-        for (int p = 0; p < kKPieces; ++p) s = mma<T>(rq.rows(sQ, p), kKeep ? kf[kKeep ? p : 0] : buffer_load16(ks, k_at + p * 32), s);
-#pragma unroll
-        for (int p = 0; p < kVPieces; ++p) dp = mma<T>(ro.rows(sO, p), kKeep ? vf[kKeep ? p : 0] : buffer_load16(vs, v_at + p * 32), dp);
+        for (int p = 0; p < kKPieces; ++p) {
+            s = mma<T>(rq.rows(sQ, p), kKeep ? kf[kKeep ? p : 0] : buffer_load16(ks, k_at + p * 32), s);
+            if (p < kVPieces) {
+                u32x4 v;
+                if constexpr (kVLds) v = ro.rows(sV + wave * 32 * ro.kRow, p);
+                else if constexpr (kVKeep) v = vf[p < kVPieces ? p : 0];
+                else v = buffer_load16(vs, v_at + p * 32);
+                dp = mma<T>(ro.rows(sO, p), v, dp);
+            }
+        }
+        if constexpr (kVKeep) lookahead<kKPieces + kVPieces, 4, Elem<T>::kMfmas>();
         // register r: query i0 + 8 (r / 4) + 4 half + r % 4; key k0 + c
 #pragma unroll
         for (int r4 = 0; r4 < 4; ++r4) {
@@ -330,10 +354,8 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_dkv_kernel(BwdK a) {
         }
     };
     int n = static_cast<int>(all * part / a.parts);
-    if constexpr (kKeep) {
-        arrive(kf);
-        arrive(vf);
-    }
+    if constexpr (kKeep) arrive(kf);
+    if constexpr (kVKeep) arrive(vf);
     if (n < n_end) {
         fetch(n);
         put(smem);

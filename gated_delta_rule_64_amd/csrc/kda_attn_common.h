@@ -55,6 +55,8 @@ struct Elem {
     static constexpr int kSize = sizeof(T);
     static constexpr int kPer16 = 16 / sizeof(T);
     static constexpr int kPieces = 16 / kPer16;  // bf16: 2 (16 rows each), fp32: 4 (8 rows each)
+    static constexpr int kMfmas = sizeof(T) == 2 ? 1 : 4;  // products of one operand piece
+    static constexpr int kTrReads = sizeof(T) == 2 ? 2 : 4;  // LDS reads of a transposed operand
 };
 
 // Piece p of a 32 x 32 result as a B operand: registers p * kPer16 ..
@@ -86,6 +88,22 @@ __device__ __forceinline__ uint2 lds_read_tr(const char* p) {
     const tr16_v4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) tr16_v4*)(p));
     return __builtin_bit_cast(uint2, v);
 }
+// Asks the scheduler to keep kAhead LDS operands in front of the products that
+// use them, in a block of kOperands operands of kReads reads and kMfmas
+// products each (left to itself it issues a read, waits for it and multiplies).
+template <int kOperands, int kAhead, int kMfmas, int kReads = 1>
+__device__ __forceinline__ void lookahead() {
+    constexpr int kMfma = 0x8, kDsRead = 0x100;
+    constexpr int kFirst = kAhead < kOperands ? kAhead : kOperands;
+    __builtin_amdgcn_sched_group_barrier(kDsRead, kFirst * kReads, 0);
+#pragma unroll
+    for (int i = 0; i < kOperands - kFirst; ++i) {
+        __builtin_amdgcn_sched_group_barrier(kMfma, kMfmas, 0);
+        __builtin_amdgcn_sched_group_barrier(kDsRead, kReads, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(kMfma, kFirst * kMfmas, 0);
+}
+
 // Larger of the two halves' values (lanes l and l + 32)
 __device__ __forceinline__ float xor32_max(float x) {
     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);

@@ -97,11 +97,12 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void attn_fwd_k
         const char* sV = sK + kV;
         f32x16 s[kSub];
 #pragma unroll
-        for (int u = 0; u < kSub; ++u) {
-            s[u] = f32x16{};
+        for (int u = 0; u < kSub; ++u) s[u] = f32x16{};
 #pragma unroll
-            for (int p = 0; p < kQPieces; ++p) s[u] = mma<T>(rk.rows(sK + 32 * u * rk.kRow, p), qf[p], s[u]);
-        }
+        for (int p = 0; p < kQPieces; ++p)
+#pragma unroll
+            for (int u = 0; u < kSub; ++u) s[u] = mma<T>(rk.rows(sK + 32 * u * rk.kRow, p), qf[p], s[u]);
+        lookahead<kQPieces * kSub, 4, Elem<T>::kMfmas>();
         if (j0 + kKeys - 1 > q0) {  // the diagonal: keys behind the row's own are not attended
             const int most = opaque(q0 + c - j0 - 4 * half);
 #pragma unroll

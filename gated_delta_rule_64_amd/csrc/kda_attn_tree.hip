@@ -161,7 +161,7 @@ __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV, NQ>::kWaves), (sizeof(T)
         constexpr int kKEach = (kKPieces + 63) / 64, kVEach = (kVPieces + 63) / 64;
         // fp32 tiles, twice as large, do not fit beside the sums: their halves
         // pass through the same registers when they are stored
-        constexpr bool kAhead = kE == 2 && (NQ == 1 || DK < 128);
+        constexpr bool kAhead = kE == 2;
         u32x4 kr[kAhead ? 2 : 1][kKEach], vr[kAhead ? 2 : 1][kVEach];
         // The table entries of a tile's halves, read as scalars: a vector load
         // would have to be waited for behind the rows in flight.
@@ -411,14 +411,24 @@ __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV, NQ>::kWaves), (sizeof(T)
     }
 }
 
-// Joins the parts of one row per wave: lanes of half h take the splits of
-// that parity, four channels each.
-template <typename T, int DV>
-__global__ __launch_bounds__(256) void attn_tree_join_kernel(TreeK a) {
-    const int64_t r = static_cast<int64_t>(blockIdx.x) * 4 + uniform(threadIdx.x >> 6);
-    const int64_t total = static_cast<int64_t>(a.B) * a.T * a.H;
-    if (r >= total) return;
-    const int lane = threadIdx.x & 63, half = lane >> 5, ch = (lane & 31) * 4;
+// Joins the parts, kWaves waves to a row: thread s of the row weighs part s,
+// then the row's half waves take the parts in turn, four channels a lane, and
+// their sums are added in LDS.  Many rows of few parts take a wave each (16,384
+// rows of 4 parts: 16 us, with four waves each 33 us); few rows of many parts
+// four (128 rows of 128 parts: 9 us, with one wave each 59 us).
+constexpr int kJoinThreads = 256;
+constexpr int kFewParts = 16;
+static_assert(kMaxSplits <= kJoinThreads && kFewParts <= 64, "a thread per part");
+
+template <typename T, int DV, int kWaves>
+__global__ __launch_bounds__(kJoinThreads) void attn_tree_join_kernel(TreeK a) {
+    constexpr int kRows = 4 / kWaves, kThreads = 64 * kWaves, kTurns = 2 * kWaves;
+    __shared__ float weight[kJoinThreads], tops[4], sums[4];
+    __shared__ f32x4 added[8][32];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, ch = (lane & 31) * 4;
+    const int mine = wave / kWaves, tid = threadIdx.x % kThreads, turn = tid >> 5, first = mine * kWaves;
+    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kRows + mine, total = static_cast<int64_t>(a.B) * a.T * a.H;
+    const int64_t r = r0 < total ? r0 : total - 1;
     const int G = a.H / a.Hkv, rows = a.T * G;
     const int h = static_cast<int>(r % a.H), t = static_cast<int>(r / a.H % a.T), b = static_cast<int>(r / a.H / a.T);
     const int64_t at = (static_cast<int64_t>(b) * a.Hkv + h / G) * rows + t * G + h % G;
@@ -426,37 +436,61 @@ __global__ __launch_bounds__(256) void attn_tree_join_kernel(TreeK a) {
     int slot, ctx;
     const bool real = slot_of(a, b, slot, ctx);
     const float sc = a.scale * kLog2e;
-    float top = -INFINITY;
-    if (real)
-        for (int s = lane; s < a.splits; s += 64) top = fmaxf(top, a.stats[2 * (at + s * step)]);
+    float m = -INFINITY, l = 0.f;
+    if (real && tid < a.splits) {
+        m = a.stats[2 * (at + tid * step)];
+        l = a.stats[2 * (at + tid * step) + 1];
+    }
+    float top = m;
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
-    float l = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
-    if (top != -INFINITY) {
-        for (int s = half; s < a.splits; s += 2) {
-            const int64_t p = at + s * step;
-            const float lp = a.stats[2 * p + 1];
-            if (!(lp > 0.f)) continue;
-            const float f = __builtin_amdgcn_exp2f((a.stats[2 * p] - top) * sc);
-            l += lp * f;
-            if (ch < DV) {
-                const f32x4 o = *reinterpret_cast<const f32x4*>(a.part + p * DV + ch);
+    if (lane == 0) tops[wave] = top;
+    __syncthreads();
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] += o[e] * f;
+    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, tops[first + w]);
+    const float f = l > 0.f ? __builtin_amdgcn_exp2f((m - top) * sc) : 0.f;  // no part was written where l is 0
+    weight[threadIdx.x] = f;
+    l = wave_sum(l * f);
+    if (lane == 0) sums[wave] = l;
+    __syncthreads();
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) l += sums[first + w];
+    f32x4 y{};
+    if (ch < DV) {
+        constexpr int kEach = 4;  // parts in flight
+        for (int s0 = turn; s0 < a.splits; s0 += kTurns * kEach) {
+            f32x4 o[kEach];
+            float w[kEach];
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                const int s = s0 + kTurns * i;
+                w[i] = s < a.splits ? weight[mine * kThreads + s] : 0.f;
+                o[i] = w[i] > 0.f ? *reinterpret_cast<const f32x4*>(a.part + (at + s * step) * DV + ch) : f32x4{};
             }
+#pragma unroll
+            for (int i = 0; i < kEach; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] += o[i][e] * w[i];
         }
     }
-    l = xor32_add(l);
+    added[mine * kTurns + turn][lane & 31] = y;
+    __syncthreads();
+    if (turn != 0 || r0 >= total) return;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) y[e] = xor32_add(y[e]);
-    if (half != 0) return;
+    for (int p = 1; p < kTurns; ++p) {
+        const f32x4 o = added[mine * kTurns + p][lane];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] += o[e];
+    }
     const float inv = l > 0.f ? 1.f / l : 0.f;
+    float out[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) y[e] *= inv;
+    for (int e = 0; e < 4; ++e) out[e] = y[e] * inv;
     if (a.lse != nullptr && lane == 0) a.lse[r] = l > 0.f ? (top * sc + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
     if (ch < DV)
         store4<T>(static_cast<T*>(a.out) + r * DV + ch,
-                  a.z != nullptr && real ? static_cast<const T*>(a.z) + r * DV + ch : nullptr, y);
+                  a.z != nullptr && real ? static_cast<const T*>(a.z) + r * DV + ch : nullptr, out);
 }
 
 // Whether a wave can take two blocks of 32 rows: their sums and queries fit
@@ -514,7 +548,10 @@ hipError_t launch_tree(const TreeArgs& a, hipStream_t s) {
     if (e != hipSuccess || p.splits == 1) return e;
     LaunchTimer timer("attn_tree_join", s);
     const int64_t rows = static_cast<int64_t>(a.B) * a.T * a.H;
-    attn_tree_join_kernel<T, DV><<<dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(256), 0, s>>>(k);
+    if (p.splits <= kFewParts)
+        attn_tree_join_kernel<T, DV, 1><<<dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(kJoinThreads), 0, s>>>(k);
+    else
+        attn_tree_join_kernel<T, DV, 4><<<dim3(static_cast<unsigned>(rows)), dim3(kJoinThreads), 0, s>>>(k);
     return hipGetLastError();
 }
 
