@@ -186,6 +186,7 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && DK <= 128 ? 2 : 1)) vo
                 for (int i = 0; i < kKTiles; ++i)
                     acc[i] = mma<T>(rk.columns(sK + 32 * u * rk.kRow, i, p), b, acc[i]);
             }
+            if constexpr (sizeof(T) == 2) lookahead<kKTiles * kP, 3, 1, 2>();
         }
     };
     fetch(0);
@@ -326,6 +327,7 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && DK <= 128 ? 2 : 1)) vo
             }
         }
         if constexpr (kVKeep) lookahead<kKPieces + kVPieces, 4, Elem<T>::kMfmas>();
+        else if constexpr (kVLds) lookahead<kKPieces, 1, 2, 3>();
         // register r: query i0 + 8 (r / 4) + 4 half + r % 4; key k0 + c
 #pragma unroll
         for (int r4 = 0; r4 < 4; ++r4) {
@@ -352,6 +354,7 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && DK <= 128 ? 2 : 1)) vo
 #pragma unroll
             for (int i = 0; i < kKTiles; ++i) gk[i] = mma<T>(rq.columns(sQ, i, p), d, gk[i]);
         }
+        if constexpr (sizeof(T) == 2) lookahead<(kVTiles + kKTiles) * kP, 3, 1, 2>();
     };
     int n = static_cast<int>(all * part / a.parts);
     if constexpr (kKeep) arrive(kf);
