@@ -30,7 +30,7 @@ struct BwdK {
     const void *q, *k, *v, *z, *out, *dy;
     const float* lse;
     void *dq, *dk, *dv, *dz;
-    float* delta;     // [T, H]
+    float2* stats;    // [T, H]: lse log2(e), delta
     void* dog;        // [T, H, dv]: dy * sigmoid(z), or dy itself without a gate
     float scale;
     int parts;
@@ -73,7 +73,7 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_rows_kernel(BwdK a) {
     sum = row_ror_add<2>(sum);
     sum = row_ror_add<4>(sum);
     sum = row_ror_add<8>(sum);
-    if (there && c == 0) a.delta[row] = sum;
+    if (there && c == 0) a.stats[row] = make_float2(a.lse[row] * kLog2e, sum);
 }
 
 // Writes a transposed 32-column result (register 4 i + e: channel 8 i + 4 half
@@ -133,8 +133,8 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && DK <= 128 ? 2 : 1)) vo
         for (int s = 0; s < kVPieces; ++s) of[s] = buffer_load16(os, c * o_row + (2 * s + half) * 16);
     }
     const int64_t at = (t.start + q0 + c) * a.H + h;
-    const float lse2 = c < rows ? a.lse[at] * kLog2e : 0.f;
-    const float delta = c < rows ? a.delta[at] : 0.f;
+    const float2 stat = c < rows ? a.stats[at] : make_float2(0.f, 0.f);
+    const float lse2 = stat.x, delta = stat.y;
     const float sc = a.scale * kLog2e;
 
     f32x16 acc[kKTiles];
@@ -210,7 +210,7 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && DK <= 128 ? 2 : 1)) vo
 template <typename T, int DK, int DV>
 struct DkvSizes {
     static constexpr int kQ = 32;  // queries of a step
-    static constexpr int kStats = kQ * 2 * 4;  // lse and delta of the step's queries
+    static constexpr int kStats = kQ * 2 * 4;  // lse and delta of the step's queries, in pairs
     static constexpr int kBuf = kQ * (DK + DV) * static_cast<int>(sizeof(T)) + kStats;
     // Where a lane's sums, keys and values together exceed half its registers,
     // the values are read from LDS for every step: two workgroups then share a
@@ -288,32 +288,36 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && DK <= 128 ? 2 : 1)) vo
     rq.init_columns(lane);
     ro.init_rows(c, half);
     ro.init_columns(lane);
-    float stat = 0.f;
+    uint2 stat{};
     const int steps = (t.len - k_first + kQ - 1) / kQ;  // per head
     const int64_t all = static_cast<int64_t>(steps) * G;
+    int n = static_cast<int>(all * part / a.parts);
     const int n_end = static_cast<int>(all * (part + 1) / a.parts);
-    auto fetch = [&](int n) {
-        const int h = kvh * G + n / steps, i0 = k_first + (n % steps) * kQ;
-        const int here = min(kQ, t.len - i0);
-        cq.load(rows_of(static_cast<const T*>(a.q) + h * DK, t.start + i0, q_row, here), q_row, tid);
-        co.load(rows_of(static_cast<const T*>(a.dog) + h * DV, t.start + i0, o_row, here), o_row, tid);
-        if (tid < 2 * kQ) {
-            // a row behind the sequence's end weighs nothing: e^(s - inf)
-            const int i = tid % kQ;
-            const int64_t at = (t.start + i0 + i) * a.H + h;
-            stat = tid < kQ ? (i < here ? a.lse[at] * kLog2e : INFINITY) : (i < here ? a.delta[at] : 0.f);
+    int f_head = uniform(kvh * G + n / steps), f_i0 = uniform(k_first + n % steps * kQ);  // the next step to fetch
+    auto fetch = [&]() __attribute__((always_inline)) {
+        const int here = min(kQ, t.len - f_i0);
+        cq.load(rows_of(static_cast<const T*>(a.q) + f_head * DK, t.start + f_i0, q_row, here), q_row, tid);
+        co.load(rows_of(static_cast<const T*>(a.dog) + f_head * DV, t.start + f_i0, o_row, here), o_row, tid);
+        // rows behind the sequence's end are 0 in all three and add nothing
+        if (wave == 0)
+            stat = buffer_load8(rows_of(a.stats + f_head, t.start + f_i0, a.H * 8, here), c * a.H * 8);
+        f_i0 += kQ;
+        if (f_i0 >= t.len) {
+            f_i0 = k_first;
+            ++f_head;
         }
     };
-    auto put = [&](char* buf) {
+    auto put = [&](char* buf) __attribute__((always_inline)) {
         cq.store(buf, tid);
         co.store(buf + kO, tid);
-        if (tid < 2 * kQ) reinterpret_cast<float*>(buf + kS)[tid] = stat;
+        if (wave == 0) reinterpret_cast<uint2*>(buf + kS)[c] = stat;
     };
-    auto work = [&](const char* sQ, int n) __attribute__((always_inline)) {
-        const int i0 = k_first + (n % steps) * kQ;
+    int i0 = f_i0 - kQ;  // the step worked on
+    auto work = [&](const char* sQ) __attribute__((always_inline)) {
+        i0 = i0 + kQ < t.len ? i0 + kQ : k_first;
         if (i0 + kQ - 1 < k0) return;  // queries before this wave's keys
         const char* sO = sQ + kO;
-        const float* sLse = reinterpret_cast<const float*>(sQ + kS);
+        const f32x4* sStats = reinterpret_cast<const f32x4*>(sQ + kS);
         f32x16 s{}, dp{};
 #pragma unroll
         for (int p = 0; p < kKPieces; ++p) {
@@ -331,13 +335,12 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && DK <= 128 ? 2 : 1)) vo
         // register r: query i0 + 8 (r / 4) + 4 half + r % 4; key k0 + c
 #pragma unroll
         for (int r4 = 0; r4 < 4; ++r4) {
-            const f32x4 ls = *reinterpret_cast<const f32x4*>(sLse + 8 * r4 + 4 * half);
-            const f32x4 de = *reinterpret_cast<const f32x4*>(sLse + kQ + 8 * r4 + 4 * half);
+            const f32x4 lo = sStats[4 * r4 + 2 * half], hi = sStats[4 * r4 + 2 * half + 1];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int r = 4 * r4 + e;
-                s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], sc, -ls[e]));
-                dp[r] = s[r] * (dp[r] - de[e]);
+                s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], sc, -(e < 2 ? lo : hi)[e % 2 * 2]));
+                dp[r] = s[r] * (dp[r] - (e < 2 ? lo : hi)[e % 2 * 2 + 1]);
             }
         }
         if (i0 < k0 + 31) {  // the diagonal: queries before the key do not attend it
@@ -356,22 +359,21 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && DK <= 128 ? 2 : 1)) vo
         }
         if constexpr (sizeof(T) == 2) lookahead<(kVTiles + kKTiles) * kP, 3, 1, 2>();
     };
-    int n = static_cast<int>(all * part / a.parts);
     if constexpr (kKeep) arrive(kf);
     if constexpr (kVKeep) arrive(vf);
     if (n < n_end) {
-        fetch(n);
+        fetch();
         put(smem);
     }
     for (; n < n_end; n += 2) {
         tile_barrier();
-        if (n + 1 < n_end) fetch(n + 1);
-        work(smem, n);
+        if (n + 1 < n_end) fetch();
+        work(smem);
         if (n + 1 >= n_end) break;
         put(smem + Sz::kBuf);
         tile_barrier();
-        if (n + 2 < n_end) fetch(n + 2);
-        work(smem + Sz::kBuf, n + 1);
+        if (n + 2 < n_end) fetch();
+        work(smem + Sz::kBuf);
         if (n + 2 < n_end) put(smem);
     }
     if (c < rows) {
@@ -432,8 +434,8 @@ hipError_t launch_bwd(const AttnBackwardArgs& a, hipStream_t s) {
     k.q = f.q; k.k = f.k; k.v = f.v; k.z = f.z; k.out = f.out; k.dy = a.dy; k.lse = f.lse;
     k.dq = a.dq; k.dk = a.dk; k.dv = a.dv; k.dz = a.dz; k.scale = f.scale;
     char* ws = static_cast<char*>(a.ws);
-    k.delta = reinterpret_cast<float*>(ws);
-    ws += up256(static_cast<size_t>(f.T) * f.H * 4);
+    k.stats = reinterpret_cast<float2*>(ws);
+    ws += up256(static_cast<size_t>(f.T) * f.H * 8);
     k.dog = f.z != nullptr ? static_cast<void*>(ws) : const_cast<void*>(a.dy);
     if (f.z != nullptr) ws += up256(static_cast<size_t>(f.T) * f.H * DV * sizeof(T));
     k.parts = dkv_parts(f.T, f.N, f.Hkv);
@@ -474,7 +476,7 @@ hipError_t launch_bwd(const AttnBackwardArgs& a, hipStream_t s) {
 size_t attn_backward_workspace_bytes(int64_t T, int N, int H, int Hkv, int dk, int dv, DT x, bool gate) {
     const size_t rows = static_cast<size_t>(T) * H;
     const int parts = dkv_parts(T, N, Hkv);
-    return up256(rows * 4) + (gate ? up256(rows * dv * (x == DT::BF16 ? 2 : 4)) : 0) +
+    return up256(rows * 8) + (gate ? up256(rows * dv * (x == DT::BF16 ? 2 : 4)) : 0) +
            (parts > 1 ? up256(static_cast<size_t>(parts) * T * Hkv * (dk + dv) * 4) : 0);
 }
 

@@ -88,6 +88,10 @@ __device__ __forceinline__ uint2 lds_read_tr(const char* p) {
     const tr16_v4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) tr16_v4*)(p));
     return __builtin_bit_cast(uint2, v);
 }
+__device__ __forceinline__ uint2 buffer_load8(__amdgpu_buffer_rsrc_t r, int offset) {
+    return __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(r, offset, 0, 0));
+}
+
 // Asks the scheduler to keep kAhead LDS operands in front of the products that
 // use them, in a block of kOperands operands of kReads reads and kMfmas
 // products each (left to itself it issues a read, waits for it and multiplies).
