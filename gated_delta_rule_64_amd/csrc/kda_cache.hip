@@ -50,23 +50,41 @@ __device__ __forceinline__ I block_scan(I x, I* sums, I& total) {
     return before + inc - x;
 }
 
+// Counts of kEach neighbouring pages per thread and step.  The first step's
+// can be put in flight long before they are looked at, and are kept: a pool of
+// up to 8,192 pages is read once.
+constexpr int kEach = 8;
+struct PageCounts {
+    int r[kEach];
+    __device__ __forceinline__ void load(const int32_t* refs, int pages, int p0) {
+        const int first = p0 + static_cast<int>(threadIdx.x) * kEach;
+        if (first + kEach <= pages && (reinterpret_cast<uintptr_t>(refs) & 15) == 0) {
+            const int4 a = reinterpret_cast<const int4*>(refs + first)[0], b = reinterpret_cast<const int4*>(refs + first)[1];
+            r[0] = a.x; r[1] = a.y; r[2] = a.z; r[3] = a.w;
+            r[4] = b.x; r[5] = b.y; r[6] = b.z; r[7] = b.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) r[i] = first + i < pages ? refs[first + i] : 1;
+        }
+    }
+};
+
 // The lowest `want` free pages in order, list[0 .. want); returns how many
-// there are (at most want).  All threads of the planning workgroup call it.
-__device__ __forceinline__ int lowest_free(const int32_t* refs, int pages, int want, int32_t* list, int* sums) {
-    constexpr int kEach = 8;
+// there are (at most want).  counts: the first step's.  All threads of the
+// planning workgroup call it.
+__device__ __forceinline__ int lowest_free(const int32_t* refs, int pages, PageCounts counts, int want, int32_t* list, int* sums) {
     int found = 0;
     for (int p0 = 0; p0 < pages && found < want; p0 += kPlan * kEach) {
+        if (p0 > 0) counts.load(refs, pages, p0);
         const int first = p0 + static_cast<int>(threadIdx.x) * kEach;
-        int r[kEach], mine = 0;
+        int mine = 0;
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) r[i] = first + i < pages ? refs[first + i] : 1;
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) mine += r[i] <= 0;
+        for (int i = 0; i < kEach; ++i) mine += counts.r[i] <= 0;
         int total;
         int at = found + block_scan(mine, sums, total);
 #pragma unroll
         for (int i = 0; i < kEach; ++i)
-            if (r[i] <= 0) {
+            if (counts.r[i] <= 0) {
                 if (at < want) store_fresh(list + at, first + i);
                 ++at;
             }
@@ -77,19 +95,34 @@ __device__ __forceinline__ int lowest_free(const int32_t* refs, int pages, int w
     return min(found, want);
 }
 
-// Of the entries of a call that name the same slot, the first that is good
-// keeps it.  claim: one word per slot.  Every thread passes its entries.
-template <typename Good>
-__device__ __forceinline__ void claim_slots(const int32_t* slot_of, int n, int32_t* claim, Good good) {
-    for (int i = threadIdx.x; i < n; i += kPlan)
-        if (good(i)) store_fresh(claim + slot_of[i], INT32_MAX);
-    __threadfence();
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kPlan)
-        if (good(i)) atomicMin(claim + slot_of[i], i);
-    __threadfence();
-    __syncthreads();
-}
+// Of the good entries of a call that name the same slot, the first keeps it.
+// The claims stand in LDS where the cache has few slots, else in the
+// workspace, a word per slot.
+constexpr int kLdsSlots = 8192;
+struct Claims {
+    int* lds;
+    int32_t* memory;
+    bool in_lds;
+    __device__ __forceinline__ void clear(int slots, const int32_t* slot_of, int n) const {
+        if (in_lds) {
+            for (int s = threadIdx.x; s < slots; s += kPlan) lds[s] = INT32_MAX;
+        } else {
+            for (int i = threadIdx.x; i < n; i += kPlan)
+                if (slot_of[i] >= 0 && slot_of[i] < slots) store_fresh(memory + slot_of[i], INT32_MAX);
+            __threadfence();
+        }
+        __syncthreads();
+    }
+    __device__ __forceinline__ void claim(int slot, int i) const {
+        if (in_lds) atomicMin(lds + slot, i);
+        else atomicMin(memory + slot, i);
+    }
+    __device__ __forceinline__ void settle() const {
+        if (!in_lds) __threadfence();
+        __syncthreads();
+    }
+    __device__ __forceinline__ int owner(int slot) const { return in_lds ? lds[slot] : load_fresh(memory + slot); }
+};
 
 // ------------------------------------------------------------------- append
 
@@ -188,51 +221,66 @@ struct ForkK {
 
 __global__ __launch_bounds__(kPlan) void cache_fork_plan_kernel(ForkK a) {
     __shared__ int sums[kPlan / 64];
+    __shared__ int claims[kLdsSlots];
     const CacheArgs& c = a.c;
     const int64_t most = static_cast<int64_t>(c.max_pages) << c.page_shift;
     const int mask = (1 << c.page_shift) - 1;
-    auto good = [&](int i) {  // both slots exist and differ, the destination is empty
+    PageCounts counts;
+    counts.load(c.refs, c.pages, 0);
+    const Claims slots{claims, a.claim, c.slots <= kLdsSlots};
+    slots.clear(c.slots, a.dst, a.n);
+    // what an entry is, kept in the plan by the thread that reads it again:
+    // the source's length (-1: refused), whether its last page is to be copied
+    for (int i = threadIdx.x; i < a.n; i += kPlan) {
         const int s = a.src[i], d = a.dst[i];
-        return s >= 0 && s < c.slots && d >= 0 && d < c.slots && s != d && c.lens[d] == 0 &&
-               !names_page(c.table[static_cast<int64_t>(d) * c.max_pages], c.pages);
-    };
-    auto length = [&](int i) {
-        const int64_t n = c.lens[a.src[i]];
-        return static_cast<int>(n < 0 ? 0 : n > most ? most : n);
-    };
-    claim_slots(a.dst, a.n, a.claim, good);
-    auto mine = [&](int i) { return i < a.n && good(i) && load_fresh(a.claim + a.dst[i]) == i; };
-    auto needs = [&](int i) {  // a last page that is partly filled
-        const int len = length(i);
-        return (len & mask) != 0 &&
-               names_page(c.table[static_cast<int64_t>(a.src[i]) * c.max_pages + (len >> c.page_shift)], c.pages);
-    };
+        int len = -1, need = 0;
+        if (s >= 0 && s < c.slots && d >= 0 && d < c.slots && s != d) {
+            const int dst_len = c.lens[d], dst_first = c.table[static_cast<int64_t>(d) * c.max_pages];
+            const int64_t n = c.lens[s];
+            if (dst_len == 0 && !names_page(dst_first, c.pages)) {  // the destination is empty
+                len = static_cast<int>(n < 0 ? 0 : n > most ? most : n);
+                if ((len & mask) != 0)
+                    need = names_page(c.table[static_cast<int64_t>(s) * c.max_pages + (len >> c.page_shift)], c.pages);
+                slots.claim(d, i);
+            }
+        }
+        a.plan[2 * i] = len;
+        a.plan[2 * i + 1] = need;
+    }
+    slots.settle();
     int want = 0;
     for (int i0 = 0; i0 < a.n; i0 += kPlan) {
-        int total;
         const int i = i0 + threadIdx.x;
-        block_scan<int>(mine(i) && needs(i), sums, total);
+        int total, need = 0;
+        if (i < a.n) {
+            need = a.plan[2 * i + 1];
+            if (a.plan[2 * i] >= 0 && slots.owner(a.dst[i]) != i) {
+                a.plan[2 * i] = -1;
+                a.plan[2 * i + 1] = need = 0;
+            }
+        }
+        block_scan<int>(need, sums, total);
         want += total;
     }
-    const int have = lowest_free(c.refs, c.pages, want, a.list, sums);
+    const int have = lowest_free(c.refs, c.pages, counts, want, a.list, sums);
     int before = 0;
     for (int i0 = 0; i0 < a.n; i0 += kPlan) {
         const int i = i0 + threadIdx.x;
-        const bool ok = mine(i), need = ok && needs(i);
+        const int len = i < a.n ? a.plan[2 * i] : -1, need = i < a.n ? a.plan[2 * i + 1] : 0;
         int total;
         const int at = before + block_scan<int>(need, sums, total);
         before += total;
         if (i < a.n) {
-            int status = ok ? 0 : 2, page = -1;
+            int status = len >= 0 ? 0 : 2, page = -1;
             if (need) {
                 if (at < have) {
                     page = load_fresh(a.list + at);
                     c.refs[page] = 1;
                 } else {
                     status = 1;
+                    a.plan[2 * i] = -1;
                 }
             }
-            a.plan[2 * i] = status == 0 ? length(i) : -1;
             a.plan[2 * i + 1] = page;
             if (a.status != nullptr) a.status[i] = status;
         }
@@ -289,36 +337,69 @@ struct ReserveK {
     int32_t* list;   // [pages]
 };
 
-// One workgroup: a wave per entry counts the columns that lack a page, a scan
-// gives every entry its place, the lowest free pages go out in that order.
+// One workgroup.  Every entry's columns that lack a page are counted, a scan
+// gives every entry its place, and the lowest free pages go out in that order.
+// An entry of few columns (a decode step's) is one thread's, so that the
+// entries' dependent loads overlap (256 entries: 49 us with a wave each); one
+// of many columns (a prompt's) a wave's.
+constexpr int kFewColumns = 16;
+
 __global__ __launch_bounds__(kPlan) void cache_reserve_kernel(ReserveK a) {
     __shared__ int sums[kPlan / 64];
     __shared__ int64_t sums64[kPlan / 64];  // the counts of a bad call may add up to more than 2^31
+    __shared__ int claims[kLdsSlots];
+    __shared__ int many;  // whether any entry has many columns
+    if (threadIdx.x == 0) many = 0;
     const CacheArgs& c = a.c;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int mask = (1 << c.page_shift) - 1;
-    auto columns = [&](int i) {  // -1: more than a table row holds
+    PageCounts pages;
+    pages.load(c.refs, c.pages, 0);
+    const Claims slots{claims, a.claim, c.slots <= kLdsSlots};
+    slots.clear(c.slots, a.slot_list, a.n);
+    struct Entry {
+        int slot, first, end;  // the columns [first, end) are looked at; slot -1: refused
+    };
+    auto entry = [&](int i) {
+        Entry e;
+        e.slot = a.slot_list[i];
         const int64_t n = (static_cast<int64_t>(max(a.new_lens[i], 0)) + mask) >> c.page_shift;
-        return n > c.max_pages ? -1 : static_cast<int>(n);
+        if (e.slot < 0 || e.slot >= c.slots || n > c.max_pages) return Entry{-1, 0, 0};
+        e.end = static_cast<int>(n);
+        // (the pages below the slot's length are there)
+        e.first = min(static_cast<int>((static_cast<int64_t>(max(c.lens[e.slot], 0)) + mask) >> c.page_shift), e.end);
+        return e;
     };
-    auto good = [&](int i) {
+    for (int i = threadIdx.x; i < a.n; i += kPlan) {
         const int s = a.slot_list[i];
-        return s >= 0 && s < c.slots && columns(i) >= 0;
-    };
-    claim_slots(a.slot_list, a.n, a.claim, good);
-    auto first_column = [&](int slot) {  // the pages below the slot's length are there
-        return static_cast<int>((static_cast<int64_t>(max(c.lens[slot], 0)) + mask) >> c.page_shift);
-    };
-    for (int i = wave; i < a.n; i += kPlan / 64) {
+        if (s >= 0 && s < c.slots && ((static_cast<int64_t>(max(a.new_lens[i], 0)) + mask) >> c.page_shift) <= c.max_pages) slots.claim(s, i);
+    }
+    slots.settle();
+    auto owned = [&](int i, const Entry& e) { return e.slot >= 0 && slots.owner(e.slot) == i; };
+    for (int i = threadIdx.x; i < a.n; i += kPlan) {
+        const Entry e = entry(i);
         int count = -1;
-        if (good(i) && load_fresh(a.claim + a.slot_list[i]) == i) {
-            const int slot = a.slot_list[i], end = columns(i);
-            const int32_t* row = c.table + static_cast<int64_t>(slot) * c.max_pages;
+        if (owned(i, e)) {
             count = 0;
-            for (int j0 = first_column(slot); j0 < end; j0 += 64) {
-                const int j = j0 + lane;
-                count += __popcll(__ballot(j < end && !names_page(row[j < end ? j : 0], c.pages)));
+            if (e.end - e.first <= kFewColumns) {
+                const int32_t* row = c.table + static_cast<int64_t>(e.slot) * c.max_pages;
+                for (int j = e.first; j < e.end; ++j) count += !names_page(row[j], c.pages);
+            } else {
+                many = 1;
             }
+        }
+        store_fresh(a.counts + i, count);
+    }
+    __threadfence();
+    __syncthreads();
+    for (int i = wave; many != 0 && i < a.n; i += kPlan / 64) {
+        const Entry e = entry(i);
+        if (e.end - e.first <= kFewColumns || !owned(i, e)) continue;
+        const int32_t* row = c.table + static_cast<int64_t>(e.slot) * c.max_pages;
+        int count = 0;
+        for (int j0 = e.first; j0 < e.end; j0 += 64) {
+            const int j = j0 + lane;
+            count += __popcll(__ballot(j < e.end && !names_page(row[j < e.end ? j : 0], c.pages)));
         }
         if (lane == 0) store_fresh(a.counts + i, count);
     }
@@ -331,7 +412,7 @@ __global__ __launch_bounds__(kPlan) void cache_reserve_kernel(ReserveK a) {
         block_scan<int64_t>(i < a.n ? max(load_fresh(a.counts + i), 0) : 0, sums64, total);
         want += total;
     }
-    const int have = lowest_free(c.refs, c.pages, static_cast<int>(min(want, static_cast<int64_t>(c.pages))), a.list, sums);
+    const int have = lowest_free(c.refs, c.pages, pages, static_cast<int>(min(want, static_cast<int64_t>(c.pages))), a.list, sums);
     int64_t before = 0;
     for (int i0 = 0; i0 < a.n; i0 += kPlan) {
         const int i = i0 + threadIdx.x;
@@ -342,19 +423,34 @@ __global__ __launch_bounds__(kPlan) void cache_reserve_kernel(ReserveK a) {
         if (i < a.n) {
             const bool fits = count == 0 || (count > 0 && at + count <= have);
             if (a.status != nullptr) a.status[i] = count < 0 ? 2 : fits ? 0 : 1;
-            store_fresh(a.counts + i, count > 0 && fits ? static_cast<int>(at) : -1);
+            int place = count > 0 && fits ? static_cast<int>(at) : -1;
+            if (place >= 0) {
+                const Entry e = entry(i);
+                if (e.end - e.first <= kFewColumns) {
+                    int32_t* row = c.table + static_cast<int64_t>(e.slot) * c.max_pages;
+                    for (int j = e.first; j < e.end; ++j)
+                        if (!names_page(row[j], c.pages)) {
+                            const int page = load_fresh(a.list + place++);
+                            row[j] = page;
+                            c.refs[page] = 1;
+                        }
+                    place = -1;
+                }
+            }
+            store_fresh(a.counts + i, place);
         }
     }
+    if (many == 0) return;
     __threadfence();
     __syncthreads();
     for (int i = wave; i < a.n; i += kPlan / 64) {
         int at = load_fresh(a.counts + i);
         if (at < 0) continue;
-        const int slot = a.slot_list[i], end = columns(i);
-        int32_t* row = c.table + static_cast<int64_t>(slot) * c.max_pages;
-        for (int j0 = first_column(slot); j0 < end; j0 += 64) {
+        const Entry e = entry(i);
+        int32_t* row = c.table + static_cast<int64_t>(e.slot) * c.max_pages;
+        for (int j0 = e.first; j0 < e.end; j0 += 64) {
             const int j = j0 + lane;
-            const bool lacks = j < end && !names_page(row[j < end ? j : 0], c.pages);
+            const bool lacks = j < e.end && !names_page(row[j < e.end ? j : 0], c.pages);
             const unsigned long long all = __ballot(lacks);
             if (lacks) {
                 const int page = load_fresh(a.list + at + __popcll(all & ((1ull << lane) - 1)));
@@ -378,35 +474,38 @@ struct CompactK {
 
 __global__ __launch_bounds__(kPlan) void cache_compact_plan_kernel(CompactK a) {
     __shared__ int sums[kPlan / 64];
+    __shared__ int64_t sums64[kPlan / 64];
     const CacheArgs& c = a.c;
-    constexpr int kEach = 8;
+    PageCounts counts;
     int live = 0;
     for (int p0 = 0; p0 < c.pages; p0 += kPlan * kEach) {
+        counts.load(c.refs, c.pages, p0);
         const int first = p0 + static_cast<int>(threadIdx.x) * kEach;
         int mine = 0, total;
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) mine += first + i < c.pages && c.refs[min(first + i, c.pages - 1)] > 0;
+        for (int i = 0; i < kEach; ++i) mine += first + i < c.pages && counts.r[i] > 0;
         block_scan(mine, sums, total);
         live += total;
     }
     // the k-th free page below `live` takes the k-th page in use behind it
     int holes = 0, movers = 0;
     for (int p0 = 0; p0 < c.pages; p0 += kPlan * kEach) {
+        if (c.pages > kPlan * kEach) counts.load(c.refs, c.pages, p0);  // else they are still there
         const int first = p0 + static_cast<int>(threadIdx.x) * kEach;
         bool hole[kEach], mover[kEach];
-        int h = 0, m = 0, th, tm;
+        int64_t both = 0, all;  // holes in the low word, movers in the high one
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
             const int p = first + i;
-            const bool used = p < c.pages && c.refs[min(p, c.pages - 1)] > 0;
+            const bool used = p < c.pages && counts.r[i] > 0;
             hole[i] = p < live && !used;
             mover[i] = p >= live && used;
-            h += hole[i];
-            m += mover[i];
+            both += static_cast<int64_t>(hole[i]) + (static_cast<int64_t>(mover[i]) << 32);
         }
-        int ah = holes + block_scan(h, sums, th), am = movers + block_scan(m, sums, tm);
-        holes += th;
-        movers += tm;
+        const int64_t at = block_scan(both, sums64, all);
+        int ah = holes + static_cast<int>(at), am = movers + static_cast<int>(at >> 32);
+        holes += static_cast<int>(all);
+        movers += static_cast<int>(all >> 32);
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
             if (first + i < c.pages) store_fresh(a.to + first + i, first + i);
@@ -430,14 +529,14 @@ __global__ __launch_bounds__(kPlan) void cache_compact_plan_kernel(CompactK a) {
 
 // One 16-byte piece per thread and step, four in flight.
 __device__ __forceinline__ void copy_pieces(const uint4* src, uint4* dst, int64_t n) {
-    constexpr int kEach = 4;
-    for (int64_t i0 = threadIdx.x; i0 < n; i0 += kCopy * kEach) {
-        uint4 r[kEach];
+    constexpr int kFlight = 4;
+    for (int64_t i0 = threadIdx.x; i0 < n; i0 += kCopy * kFlight) {
+        uint4 r[kFlight];
 #pragma unroll
-        for (int i = 0; i < kEach; ++i)
+        for (int i = 0; i < kFlight; ++i)
             if (i0 + i * kCopy < n) r[i] = src[i0 + i * kCopy];
 #pragma unroll
-        for (int i = 0; i < kEach; ++i)
+        for (int i = 0; i < kFlight; ++i)
             if (i0 + i * kCopy < n) dst[i0 + i * kCopy] = r[i];
     }
 }

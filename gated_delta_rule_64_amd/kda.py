@@ -272,6 +272,8 @@ def _device(*tensors):
     for t in tensors:
         if t is not None and t.device != dev:
             raise ValueError(f"tensors on {dev} and {t.device} in one call")
+    if dev.type != "cuda":
+        raise ValueError("libkda takes device tensors")
     return dev
 
 
@@ -282,14 +284,34 @@ def _shape(name, t, shape, dtype):
         raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
 
 
+# the current stream's handle without the wrapper object that
+# torch.cuda.current_stream makes (3 of the 12 us of a small call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _addr(t):
+    """A tensor's device address as a plain number (None stays None), for
+    arguments that ctypes already takes as pointers."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError("libkda takes device tensors")
+    if not t.is_contiguous():
+        raise ValueError("libkda takes contiguous tensors")
+    return t.data_ptr()
+
+
 def _call(dev, name, *args):
     """One call of the library on the device's current stream."""
-    fn = getattr(lib(), name)
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        check(fn(*args, _stream(dev)))
+    fn, index = getattr(lib(), name), dev.index
+    if index == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
-            check(fn(*args, _stream(dev)))
+            status = fn(*args, _raw_stream(index))
+    if status != 0:
+        check(status)
 
 
 def _workspace(workspace, need, dev):
@@ -325,8 +347,8 @@ def kda_attn_prefill(q, k, v, out_gate=None, cu_seqlens=None, scale=None, out=No
         lse = torch.empty((T, H), dtype=torch.float32, device=dev)
     else:
         _shape("lse", lse, (T, H), torch.float32)
-    _call(dev, "kda_attn_prefill", T, H, Hkv, dk, dv, _ptr(cu_seqlens), N, _dtype_code(q),
-          dk ** -0.5 if scale is None else scale, _ptr(q), _ptr(k), _ptr(v), _ptr(out_gate), _ptr(out), _ptr(lse))
+    _call(dev, "kda_attn_prefill", T, H, Hkv, dk, dv, _addr(cu_seqlens), N, _dtype_code(q),
+          dk ** -0.5 if scale is None else scale, _addr(q), _addr(k), _addr(v), _addr(out_gate), _addr(out), _addr(lse))
     return out, lse
 
 
@@ -351,9 +373,9 @@ def kda_attn_prefill_backward(q, k, v, out, lse, dy, out_gate=None, cu_seqlens=N
          "dz": torch.empty_like(out_gate) if out_gate is not None else None}
     need = kda_attn_backward_workspace_bytes(T, N, H, Hkv, dk, dv, x, out_gate is not None)
     workspace = _workspace(workspace, need, dev)
-    _call(dev, "kda_attn_prefill_backward", T, H, Hkv, dk, dv, _ptr(cu_seqlens), N, x,
-          dk ** -0.5 if scale is None else scale, _ptr(q), _ptr(k), _ptr(v), _ptr(out_gate), _ptr(out), _ptr(lse),
-          _ptr(dy), _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dv"]), _ptr(g["dz"]), _ptr(workspace), workspace.numel())
+    _call(dev, "kda_attn_prefill_backward", T, H, Hkv, dk, dv, _addr(cu_seqlens), N, x,
+          dk ** -0.5 if scale is None else scale, _addr(q), _addr(k), _addr(v), _addr(out_gate), _addr(out), _addr(lse),
+          _addr(dy), _addr(g["dq"]), _addr(g["dk"]), _addr(g["dv"]), _addr(g["dz"]), _addr(workspace), workspace.numel())
     return g
 
 
@@ -409,9 +431,9 @@ def kda_attn_tree(q, k_new, v_new, k_cache, v_cache, page_table, lens, tree_mask
     x = _dtype_code(q)
     workspace = _workspace(workspace, kda_attn_tree_workspace_bytes(B, T, H, Hkv, dk, dv, x, width * page), dev)
     _call(dev, "kda_attn_tree", B, T, H, Hkv, dk, dv, x, dk ** -0.5 if scale is None else scale,
-          _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(tree_mask), _ptr(out_gate), _ptr(k_cache), _ptr(v_cache), pages, page,
-          _ptr(page_table), slots, width, _ptr(lens), _ptr(slot_indices), _ptr(out), _ptr(lse),
-          _ptr(workspace), workspace.numel())
+          _addr(q), _addr(k_new), _addr(v_new), _addr(tree_mask), _addr(out_gate), _addr(k_cache), _addr(v_cache), pages, page,
+          _addr(page_table), slots, width, _addr(lens), _addr(slot_indices), _addr(out), _addr(lse),
+          _addr(workspace), workspace.numel())
     return out, lse
 
 
@@ -433,9 +455,9 @@ def kda_cache_append(k_new, v_new, k_cache, v_cache, page_table, lens, cu_seqlen
     if slot_indices is not None:
         _shape("slot_indices", slot_indices, (N,), torch.int32)
     dev = _device(k_new, v_new, k_cache, v_cache, page_table, lens, cu_seqlens, rows, slot_indices)
-    _call(dev, "kda_cache_append", T, N, _ptr(cu_seqlens), R, _ptr(rows), Hkv, dk, dv, _dtype_code(k_cache),
-          _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache), pages, page, _ptr(page_table), slots, width,
-          _ptr(lens), _ptr(slot_indices))
+    _call(dev, "kda_cache_append", T, N, _addr(cu_seqlens), R, _addr(rows), Hkv, dk, dv, _dtype_code(k_cache),
+          _addr(k_new), _addr(v_new), _addr(k_cache), _addr(v_cache), pages, page, _addr(page_table), slots, width,
+          _addr(lens), _addr(slot_indices))
 
 
 def kda_cache_workspace_bytes(num_pages, slots, n):
@@ -463,7 +485,7 @@ def kda_cache_free(slot_list, page_table, lens, refs):
     _shape("lens", lens, (slots,), torch.int32)
     _shape("refs", refs, (refs.numel(),), torch.int32)
     dev = _device(slot_list, page_table, lens, refs)
-    _call(dev, "kda_cache_free", n, _ptr(slot_list), refs.numel(), _ptr(page_table), slots, width, _ptr(lens), _ptr(refs))
+    _call(dev, "kda_cache_free", n, _addr(slot_list), refs.numel(), _addr(page_table), slots, width, _addr(lens), _addr(refs))
 
 
 def kda_cache_fork(src, dst, k_cache, v_cache, page_table, lens, refs, status=None, workspace=None):
@@ -478,8 +500,8 @@ def kda_cache_fork(src, dst, k_cache, v_cache, page_table, lens, refs, status=No
     dev = _device(src, dst, k_cache, v_cache, page_table, lens, refs, status, workspace)
     status = _status(status, n, dev)
     workspace = _workspace(workspace, kda_cache_workspace_bytes(pages, slots, n), dev)
-    _call(dev, "kda_cache_fork", n, _ptr(src), _ptr(dst), Hkv, dk, dv, _dtype_code(k_cache), _ptr(k_cache), _ptr(v_cache),
-          pages, page, _ptr(page_table), slots, width, _ptr(lens), _ptr(refs), _ptr(status), _ptr(workspace),
+    _call(dev, "kda_cache_fork", n, _addr(src), _addr(dst), Hkv, dk, dv, _dtype_code(k_cache), _addr(k_cache), _addr(v_cache),
+          pages, page, _addr(page_table), slots, width, _addr(lens), _addr(refs), _addr(status), _addr(workspace),
           workspace.numel())
     return status
 
@@ -496,8 +518,8 @@ def kda_cache_reserve(slot_list, new_lens, page_size, page_table, lens, refs, st
     dev = _device(slot_list, new_lens, page_table, lens, refs, status, workspace)
     status = _status(status, n, dev)
     workspace = _workspace(workspace, kda_cache_workspace_bytes(refs.numel(), slots, n), dev)
-    _call(dev, "kda_cache_reserve", n, _ptr(slot_list), _ptr(new_lens), refs.numel(), page_size, _ptr(page_table), slots,
-          width, _ptr(lens), _ptr(refs), _ptr(status), _ptr(workspace), workspace.numel())
+    _call(dev, "kda_cache_reserve", n, _addr(slot_list), _addr(new_lens), refs.numel(), page_size, _addr(page_table), slots,
+          width, _addr(lens), _addr(refs), _addr(status), _addr(workspace), workspace.numel())
     return status
 
 
@@ -512,8 +534,8 @@ def kda_cache_compact(k_cache, v_cache, page_table, refs, live=None, workspace=N
     else:
         _shape("live", live, (1,), torch.int32)
     workspace = _workspace(workspace, kda_cache_workspace_bytes(pages, slots, 0), dev)
-    _call(dev, "kda_cache_compact", Hkv, dk, dv, _dtype_code(k_cache), _ptr(k_cache), _ptr(v_cache), pages, page,
-          _ptr(page_table), slots, width, _ptr(refs), _ptr(live), _ptr(workspace), workspace.numel())
+    _call(dev, "kda_cache_compact", Hkv, dk, dv, _dtype_code(k_cache), _addr(k_cache), _addr(v_cache), pages, page,
+          _addr(page_table), slots, width, _addr(refs), _addr(live), _addr(workspace), workspace.numel())
     return live
 
 
@@ -526,7 +548,7 @@ def kda_cache_copy(pool, src, dst):
     rows = pool.shape[0]
     row_bytes = pool.numel() // max(rows, 1) * pool.element_size()
     dev = _device(pool, src, dst)
-    _call(dev, "kda_cache_copy", _ptr(pool), row_bytes, rows, _ptr(src), _ptr(dst), n)
+    _call(dev, "kda_cache_copy", _addr(pool), row_bytes, rows, _addr(src), _addr(dst), n)
 
 
 def kda_probe_peak(kind, blocks, iters=0, src=None, out=None):
