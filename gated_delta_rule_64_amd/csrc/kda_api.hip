@@ -819,7 +819,7 @@ int kda_attn_prefill_backward(int64_t T_tot, int32_t H, int32_t Hkv, int32_t dk,
                               const void* dy, void* grad_q, void* grad_k, void* grad_v, void* grad_out_gate,
                               void* workspace, size_t workspace_bytes, void* stream) {
     int st = check_heads(H, Hkv, dk, dv, x_dtype, scale);
-    if (st == KDA_OK) st = check_packed(T_tot, N, cu_seqlens, H);
+    if (st == KDA_OK) st = check_packed(T_tot, N, cu_seqlens, 2 * static_cast<int64_t>(H));
     if (st != KDA_OK) return st;
     if ((out_gate != nullptr) != (grad_out_gate != nullptr) && T_tot > 0)
         return fail(KDA_ERR_INVALID_ARGUMENT, "grad_out_gate is required exactly when out_gate is given");

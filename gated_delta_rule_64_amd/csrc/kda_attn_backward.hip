@@ -7,9 +7,9 @@
 //   dz   = dy * y * (1 - sigmoid(z))    (y sigmoid'(z) / sigmoid(z); no division)
 // i over the queries of every head that shares the key head.
 //
-// Three kernels: delta, dz and the gated do per row; dk and dv per tile of
-// keys, looping over the queries; dq per tile of queries, looping over the
-// keys.  The scores are formed in both, seven products for five, and in
+// Three kernels: delta, dz and the gated do per row; then dk and dv per tile of
+// keys, looping over the queries, and dq per tile of queries, looping over the
+// keys; then the sum of dk's and dv's parts, where there are several.  The scores are formed in both, seven products for five, and in
 // exchange every sum is one workgroup's, in a fixed order: no atomics.
 #include "kda_attn_common.h"
 #include "kda_internal.h"
@@ -100,21 +100,21 @@ struct DqSizes {
     static constexpr int kLds = 2 * kBuf + kTrSlack;
 };
 
+// Query gradients: one workgroup per (tile of 128 queries, head).
 template <typename T, int DK, int DV>
-__global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && DK <= 128 ? 2 : 1)) void attn_bwd_dq_kernel(BwdK a) {
+__device__ __forceinline__ void query_gradients(const BwdK& a, unsigned block, char* smem) {
     using Sz = DqSizes<T, DK, DV>;
     constexpr int kKeys = Sz::kKeys, kSub = kKeys / 32;
     constexpr int kQPieces = DK / (2 * Elem<T>::kPer16), kVPieces = DV / (2 * Elem<T>::kPer16);
     constexpr int kKTiles = (DK + 31) / 32;
     constexpr int kP = Elem<T>::kPieces;
-    extern __shared__ __align__(16) char smem[];
     constexpr int kV = kKeys * DK * static_cast<int>(sizeof(T));  // the values, behind the keys
 
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int c = lane & 31, half = lane >> 5;
     const int G = a.H / a.Hkv;
-    const int64_t rank = blockIdx.x / a.H;
-    const int slot = blockIdx.x % a.H;
+    const int64_t rank = block / a.H;
+    const int slot = block % a.H;
     const int kvh = slot % a.Hkv, h = kvh * G + slot / a.Hkv;
     const Tile t = find_tile<kRows>(a.cu, a.N, a.T, rank);
     if (!t.there) return;
@@ -220,12 +220,12 @@ struct DkvSizes {
     static constexpr int kLds = 2 * kBuf + kTrSlack + kValues;
 };
 
-// One workgroup per (tile of 128 keys, key head, part).  The tile's work is
+// Key and value gradients: one workgroup per (tile of 128 keys, key head, part).  The tile's work is
 // the sequence of its steps of 32 queries, head by head of the group; the
 // parts cut it into equal pieces where there are few tiles, and their sums
 // (fp32) are added by attn_bwd_sum_kernel.
 template <typename T, int DK, int DV>
-__global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && DK <= 128 ? 2 : 1)) void attn_bwd_dkv_kernel(BwdK a) {
+__device__ __forceinline__ void key_gradients(const BwdK& a, unsigned block, char* smem) {
     using Sz = DkvSizes<T, DK, DV>;
     constexpr int kQ = Sz::kQ;
     constexpr int kKPieces = DK / (2 * Elem<T>::kPer16), kVPieces = DV / (2 * Elem<T>::kPer16);
@@ -233,13 +233,12 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && DK <= 128 ? 2 : 1)) vo
     constexpr int kP = Elem<T>::kPieces;
     constexpr int kO = kQ * DK * static_cast<int>(sizeof(T));       // the output gradients, behind the queries
     constexpr int kS = kO + kQ * DV * static_cast<int>(sizeof(T));  // the statistics, behind both
-    extern __shared__ __align__(16) char smem[];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int c = lane & 31, half = lane >> 5;
     const int G = a.H / a.Hkv;
-    const int64_t rank = blockIdx.x / (a.Hkv * a.parts);
-    const int slot = blockIdx.x % (a.Hkv * a.parts);
+    const int64_t rank = block / (a.Hkv * a.parts);
+    const int slot = block % (a.Hkv * a.parts);
     const int kvh = slot % a.Hkv, part = slot / a.Hkv;
     const Tile t = find_tile<kRows>(a.cu, a.N, a.T, rank);
     if (!t.there) return;
@@ -389,6 +388,17 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && DK <= 128 ? 2 : 1)) vo
     }
 }
 
+// Both in one launch, the key gradients' workgroups first: they are the longer
+// ones, and the query gradients' fill the chip behind them (one after the
+// other, each launch ends with most of the chip idle: the small fp32 batch
+// takes 55 + 59 us so).
+template <typename T, int DK, int DV>
+__global__ __launch_bounds__(kThreads, (DK * sizeof(T) <= 256 ? 2 : 1)) void attn_bwd_kernel(BwdK a, unsigned key_groups) {
+    extern __shared__ __align__(16) char smem[];
+    if (blockIdx.x < key_groups) key_gradients<T, DK, DV>(a, blockIdx.x, smem);
+    else query_gradients<T, DK, DV>(a, blockIdx.x - key_groups, smem);
+}
+
 // Adds the parts in their order, four channels per thread.
 template <typename T, int DK, int DV>
 __global__ __launch_bounds__(kThreads) void attn_bwd_sum_kernel(BwdK a) {
@@ -440,8 +450,8 @@ hipError_t launch_bwd(const AttnBackwardArgs& a, hipStream_t s) {
     if (f.z != nullptr) ws += up256(static_cast<size_t>(f.T) * f.H * DV * sizeof(T));
     k.parts = dkv_parts(f.T, f.N, f.Hkv);
     k.part = reinterpret_cast<float*>(ws);
-    hipError_t e = allow_lds(attn_bwd_dq_kernel<T, DK, DV>, DqSizes<T, DK, DV>::kLds);
-    if (e == hipSuccess) e = allow_lds(attn_bwd_dkv_kernel<T, DK, DV>, DkvSizes<T, DK, DV>::kLds);
+    constexpr int lds = DqSizes<T, DK, DV>::kLds > DkvSizes<T, DK, DV>::kLds ? DqSizes<T, DK, DV>::kLds : DkvSizes<T, DK, DV>::kLds;
+    hipError_t e = allow_lds(attn_bwd_kernel<T, DK, DV>, lds);
     if (e != hipSuccess) return e;
     {
         LaunchTimer timer("attn_bwd_rows", s);
@@ -452,8 +462,10 @@ hipError_t launch_bwd(const AttnBackwardArgs& a, hipStream_t s) {
     if (e != hipSuccess) return e;
     const int64_t tiles = attn_tiles(f.T, f.N, kRows);
     {
-        LaunchTimer timer("attn_bwd_dkv", s);
-        attn_bwd_dkv_kernel<T, DK, DV><<<dim3(static_cast<unsigned>(tiles * f.Hkv * k.parts)), dim3(kThreads), DkvSizes<T, DK, DV>::kLds, s>>>(k);
+        LaunchTimer timer("attn_bwd", s);
+        const int64_t key_groups = tiles * f.Hkv * k.parts;
+        attn_bwd_kernel<T, DK, DV><<<dim3(static_cast<unsigned>(key_groups + tiles * f.H)), dim3(kThreads), lds, s>>>(
+            k, static_cast<unsigned>(key_groups));
     }
     e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -463,10 +475,6 @@ hipError_t launch_bwd(const AttnBackwardArgs& a, hipStream_t s) {
         attn_bwd_sum_kernel<T, DK, DV><<<dim3(static_cast<unsigned>((threads + kThreads - 1) / kThreads)), dim3(kThreads), 0, s>>>(k);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
-    }
-    {
-        LaunchTimer timer("attn_bwd_dq", s);
-        attn_bwd_dq_kernel<T, DK, DV><<<dim3(static_cast<unsigned>(tiles * f.H)), dim3(kThreads), DqSizes<T, DK, DV>::kLds, s>>>(k);
     }
     return hipGetLastError();
 }
