@@ -97,7 +97,7 @@ template <typename T, int DK, int DV>
 struct DqSizes {
     static constexpr int kKeys = sizeof(T) == 4 && DK > 64 ? 32 : 64;
     static constexpr int kBuf = kKeys * (DK + DV) * static_cast<int>(sizeof(T));
-    static constexpr int kLds = 2 * kBuf + kTrSlack;
+    static constexpr int kLds = 2 * kBuf + tr_slack(DV);
 };
 
 // Query gradients: one workgroup per (tile of 128 queries, head).
@@ -217,7 +217,7 @@ struct DkvSizes {
     // CU, and one's products cover the other's exponentials and LDS reads.
     static constexpr bool kValuesInLds = sizeof(T) == 2 && DK == 128;
     static constexpr int kValues = kValuesInLds ? kRows * DV * static_cast<int>(sizeof(T)) : 0;
-    static constexpr int kLds = 2 * kBuf + kTrSlack + kValues;
+    static constexpr int kLds = 2 * kBuf + tr_slack(DV) + kValues;
 };
 
 // Key and value gradients: one workgroup per (tile of 128 keys, key head, part).  The tile's work is
@@ -257,7 +257,7 @@ __device__ __forceinline__ void key_gradients(const BwdK& a, unsigned block, cha
     const auto vs = rows_of(static_cast<const T*>(a.v) + kvh * DV, t.start + k0, v_row, rows);
     const int k_at = c * k_row + half * 16, v_at = c * v_row + half * 16;
     constexpr bool kVLds = Sz::kValuesInLds, kVKeep = kKeep && !kVLds;
-    char* sV = smem + 2 * Sz::kBuf + kTrSlack;
+    char* sV = smem + 2 * Sz::kBuf + tr_slack(DV);
     u32x4 kf[kKeep ? kKPieces : 1], vf[kVKeep ? kVPieces : 1];
     if constexpr (kKeep) {
 #pragma unroll

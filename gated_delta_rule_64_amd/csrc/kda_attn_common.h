@@ -179,10 +179,16 @@ __device__ __forceinline__ void seq_bounds(const int32_t* cu, int n, int64_t T, 
     len = static_cast<int>(b - a);
 }
 
+// Sum over the wave without the LDS path (as wave_sum, for whole numbers)
 __device__ __forceinline__ int wave_sum_int(int x) {
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) x += __shfl_xor(x, o);
-    return uniform(x);
+    x += __builtin_amdgcn_mov_dpp(x, 0x121, 0xF, 0xF, false);
+    x += __builtin_amdgcn_mov_dpp(x, 0x122, 0xF, 0xF, false);
+    x += __builtin_amdgcn_mov_dpp(x, 0x124, 0xF, 0xF, false);
+    x += __builtin_amdgcn_mov_dpp(x, 0x128, 0xF, 0xF, false);
+    const auto a = __builtin_amdgcn_permlane16_swap(static_cast<unsigned>(x), static_cast<unsigned>(x), false, false);
+    x = static_cast<int>(a[0] + a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(static_cast<unsigned>(x), static_cast<unsigned>(x), false, false);
+    return uniform(static_cast<int>(b[0] + b[1]));
 }
 
 // The rank-th tile of the batch, tiles ordered by falling level (in causal
@@ -204,6 +210,9 @@ __device__ __forceinline__ Tile find_tile(const int32_t* cu, int N, int64_t T, i
         t.level = t.there ? t.tiles - 1 - static_cast<int>(rank) : 0;
         return t;
     }
+    int64_t my_start = 0;  // the first 64 sequences stay in registers
+    int my_len = 0;
+    if (lane < N) seq_bounds(cu, lane, T, my_start, my_len);
     auto tiles_of = [&](int n) {
         if (n >= N) return 0;
         int64_t start;
@@ -211,7 +220,7 @@ __device__ __forceinline__ Tile find_tile(const int32_t* cu, int N, int64_t T, i
         seq_bounds(cu, n, T, start, len);
         return (len + kRows - 1) / kRows;
     };
-    const int mine = tiles_of(lane);  // the first 64 sequences stay in a register
+    const int mine = (my_len + kRows - 1) / kRows;
     auto at_least = [&](int j) {      // tiles at level j or above (at most 2^31 / kRows + N)
         int s = max(0, mine - j);
         for (int n = 64 + lane; n < N; n += 64) s += max(0, tiles_of(n) - j);
@@ -241,7 +250,12 @@ __device__ __forceinline__ Tile find_tile(const int32_t* cu, int N, int64_t T, i
         }
         for (; left > 0; --left) has &= has - 1;
         const int n = uniform(n0 + __ffsll(static_cast<long long>(has)) - 1);
-        seq_bounds(cu, n, T, t.start, t.len);
+        if (n < 64) {
+            t.start = __builtin_amdgcn_readlane(static_cast<int>(my_start), n);  // below 2^31
+            t.len = __builtin_amdgcn_readlane(my_len, n);
+        } else {
+            seq_bounds(cu, n, T, t.start, t.len);
+        }
         t.len = uniform(t.len);
         t.start = uniform64(t.start);
         t.level = lo;
@@ -290,7 +304,8 @@ struct TileRead {
         }
     }
     __device__ __forceinline__ u32x4 rows(const char* tile, int p) const {
-        return *reinterpret_cast<const u32x4*>(tile + (kStored ? row[kStored ? p : 0] : row[0] + (row[1] ^ 32 * p)));
+        if constexpr (kStored) return *reinterpret_cast<const u32x4*>(tile + row[p]);
+        else return *reinterpret_cast<const u32x4*>(tile + row[0] + (row[1] ^ 32 * p));
     }
     // transposed: see lds_read_tr for which lane names which element.  A
     // 32-column tile of a narrower matrix reads into the row behind it, and
@@ -326,7 +341,7 @@ struct TileRead {
         }
     }
 };
-constexpr int kTrSlack = 64;
+constexpr int tr_slack(int cols) { return cols < 32 ? 64 : 0; }
 
 // Copy of kRows rows into such a tile in two steps: load() puts this thread's
 // pieces in flight, store() writes them to LDS.
@@ -355,6 +370,61 @@ struct TileCopy {
         }
     }
 };
+
+__device__ __forceinline__ void wave_lds_fence() {
+    // LDS operations of one wave complete in order; this keeps the compiler
+    // from moving them past each other (lanes read what other lanes wrote)
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// Hands out a transposed result (lane column c: row c; register 4 i + e of tile
+// t: channel 32 t + 8 i + 4 half + e) as 16-byte pieces of whole rows:
+// put(row, channel, values), neighbouring lanes with neighbouring pieces, so
+// that stores (and the loads that go with them) take whole rows; straight from
+// the registers a store instruction touches 32 rows, 16 bytes of each.
+// lds: 32 * D floats of this wave's own.
+template <typename T, int D, int kTiles, typename Put>
+__device__ __forceinline__ void by_rows(char* lds, const f32x16 (&acc)[kTiles], int lane, Put put) {
+    constexpr int kPieces = D / 4, kPer = 16 / static_cast<int>(sizeof(T));
+    const int c = lane & 31, half = lane >> 5;
+    wave_lds_fence();
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int p = 8 * t + 2 * i + half;
+            if (4 * p < D)
+                *reinterpret_cast<f32x4*>(lds + c * D * 4 + (p ^ turn<kPieces>(c)) * 16) =
+                    f32x4{acc[t][4 * i], acc[t][4 * i + 1], acc[t][4 * i + 2], acc[t][4 * i + 3]};
+        }
+    wave_lds_fence();
+#pragma unroll
+    for (int n = 0; n < 32 * D / (64 * kPer); ++n) {
+        const int at = lane + 64 * n, row = at / (D / kPer), ch = at % (D / kPer) * kPer;
+        float y[kPer];
+#pragma unroll
+        for (int q = 0; q < kPer / 4; ++q) {
+            const f32x4 x = *reinterpret_cast<const f32x4*>(lds + row * D * 4 + ((ch / 4 + q) ^ turn<kPieces>(row)) * 16);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[4 * q + e] = x[e];
+        }
+        put(row, ch, y);
+    }
+}
+__device__ __forceinline__ void store_piece(bf16* p, const float (&x)[8]) { st8(p, x); }
+__device__ __forceinline__ void store_piece(float* p, const float (&x)[4]) { st4(p, x); }
+__device__ __forceinline__ void unpack_piece(u32x4 v, float (&x)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(v[i] << 16);
+        x[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void unpack_piece(u32x4 v, float (&x)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(v[i]);
+}
 
 // Workgroup barrier that orders LDS accesses only: loads from memory stay in
 // flight across it.

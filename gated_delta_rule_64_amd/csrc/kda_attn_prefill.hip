@@ -35,7 +35,8 @@ template <typename T, int DK, int DV>
 struct FwdSizes {
     static constexpr int kKeys = DK > 128 || (sizeof(T) == 4 && DK > 64) ? 32 : 64;  // keys of a tile
     static constexpr int kBuf = kKeys * (DK + DV) * static_cast<int>(sizeof(T));
-    static constexpr int kLds = 2 * kBuf + kTrSlack;
+    static constexpr int kTiles = 2 * kBuf + tr_slack(DV), kRows = kWaves * 32 * DV * 4;
+    static constexpr int kLds = kTiles > kRows ? kTiles : kRows;  // the results pass through the tiles' space
 };
 
 template <typename T, int DK, int DV>
@@ -160,33 +161,35 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void attn_fwd_k
         if (j0 + 2 * kKeys < last) put(smem);
     }
 
-    // epilogue: lane c's query; registers 4 i .. 4 i + 3 of a tile are four
-    // neighbouring channels
     const int row = q0 + c;
+    const int64_t first = (t.start + q0) * a.H + h;  // this wave's first row in [T, H]
+    constexpr int kPer = Elem<T>::kPer16, kOut = 32 * DV / (64 * kPer), kRowPieces = DV / kPer;
+    // the gate's logits, in flight while the results are laid out by rows
+    u32x4 z[kOut];
+    if (a.z != nullptr) {
+        const auto src = rows_of(static_cast<const T*>(a.z) + h * DV, t.start + q0, a.H * DV * static_cast<int>(sizeof(T)), min(32, t.len - q0));
+#pragma unroll
+        for (int n = 0; n < kOut; ++n)
+            z[n] = buffer_load16(src, (lane + 64 * n) / kRowPieces * (a.H * DV * static_cast<int>(sizeof(T))) + (lane + 64 * n) % kRowPieces * 16);
+    }
     l = xor32_add(l);
-    if (row >= t.len) return;
-    const int64_t at = (t.start + row) * a.H + h;
     const float inv = l > 0.f ? 1.f / l : 0.f;
-    if (a.lse != nullptr && half == 0) a.lse[at] = l > 0.f ? (m * sc + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
-    T* out = static_cast<T*>(a.out) + at * DV;
-    const T* z = static_cast<const T*>(a.z) + at * DV;
+    if (a.lse != nullptr && half == 0 && row < t.len)
+        a.lse[first + static_cast<int64_t>(c) * a.H] = l > 0.f ? (m * sc + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
 #pragma unroll
-    for (int i = 0; i < kVTiles; ++i)
+    for (int i = 0; i < kVTiles; ++i) acc[i] *= inv;
+    tile_barrier();  // every wave is done with the tiles
+    int n = 0;
+    by_rows<T, DV>(smem + wave * 32 * DV * 4, acc, lane, [&](int r, int ch, auto& y) __attribute__((always_inline)) {
+        if (a.z != nullptr) {
+            float g[kPer];
+            unpack_piece(z[n], g);
 #pragma unroll
-        for (int r4 = 0; r4 < 4; ++r4) {
-            const int ch = 32 * i + 8 * r4 + 4 * half;
-            if (ch >= DV) continue;
-            float y[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = acc[i][4 * r4 + e] * inv;
-            if (a.z != nullptr) {
-                float g[4];
-                ld4(z + ch, g);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] *= sigmoid_fast(g[e]);
-            }
-            st4(out + ch, y);
+            for (int e = 0; e < kPer; ++e) y[e] *= sigmoid_fast(g[e]);
         }
+        ++n;
+        if (q0 + r < t.len) store_piece(static_cast<T*>(a.out) + (first + static_cast<int64_t>(r) * a.H) * DV + ch, y);
+    });
 }
 
 template <typename T, int DK, int DV>

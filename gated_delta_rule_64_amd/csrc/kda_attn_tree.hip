@@ -43,7 +43,7 @@ struct TreeK {
 
 template <typename T, int DK, int DV, int NQ>
 struct TreeSizes {
-    static constexpr int kTile = kKeys * (DK + DV) * static_cast<int>(sizeof(T)) + kTrSlack;
+    static constexpr int kTile = kKeys * (DK + DV) * static_cast<int>(sizeof(T)) + tr_slack(DV);
     static constexpr int kWaves = 4 * kTile <= 160 * 1024 ? 4 : 2;
     static constexpr int kVTiles = (DV + 31) / 32;
     static constexpr int kPart = NQ * kVTiles * 16 * 64 * 4;        // one wave's sums
@@ -71,13 +71,6 @@ __device__ __forceinline__ void store4(T* out, const T* z, float (&y)[4]) {
         for (int e = 0; e < 4; ++e) y[e] *= sigmoid_fast(g[e]);
     }
     st4(out, y);
-}
-
-__device__ __forceinline__ void wave_lds_fence() {
-    // LDS operations of one wave complete in order; this keeps the compiler
-    // from moving them past each other (lanes read what other lanes wrote)
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
 }
 
 template <typename T, int DK, int DV, int NQ>
