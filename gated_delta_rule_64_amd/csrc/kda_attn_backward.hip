@@ -53,20 +53,26 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_rows_kernel(BwdK a) {
             float dy[kV], y[kV];
             ld4(static_cast<const T*>(a.dy) + at + ch, dy);
             ld4(static_cast<const T*>(a.out) + at + ch, y);
+            if (a.z == nullptr) {
 #pragma unroll
-            for (int e = 0; e < kV; ++e) sum += dy[e] * y[e];
-            if (a.z != nullptr) {
-                float z[kV], g[kV];
-                ld4(static_cast<const T*>(a.z) + at + ch, z);
-#pragma unroll
-                for (int e = 0; e < kV; ++e) {
-                    const float sg = sigmoid_fast(z[e]);
-                    g[e] = dy[e] * sg;
-                    z[e] = dy[e] * y[e] * sigmoid_fast(-z[e]);  // 1 - sigmoid(z) without cancellation
-                }
-                st4(static_cast<T*>(a.dog) + at + ch, g);
-                st4(static_cast<T*>(a.dz) + at + ch, z);
+                for (int e = 0; e < kV; ++e) sum += dy[e] * y[e];
+                continue;
             }
+            // delta from the gated gradient as it is stored, do . o with
+            // o = y / sigmoid(z): do . v - delta then cancels as it must in
+            // rows of few keys (dy . y, of the unrounded gradient, leaves the
+            // rounding of do there).  A gate that is all but closed has y = 0.
+            float z[kV], g[kV];
+            ld4(static_cast<const T*>(a.z) + at + ch, z);
+#pragma unroll
+            for (int e = 0; e < kV; ++e) {
+                const float sg = sigmoid_fast(z[e]);
+                g[e] = round_to<T>(dy[e] * sg);
+                sum += sg > 1e-30f ? g[e] * (y[e] / sg) : 0.f;
+                z[e] = dy[e] * y[e] * sigmoid_fast(-z[e]);  // 1 - sigmoid(z) without cancellation
+            }
+            st4(static_cast<T*>(a.dog) + at + ch, g);
+            st4(static_cast<T*>(a.dz) + at + ch, z);
         }
     }
     sum = row_ror_add<1>(sum);
