@@ -21,7 +21,8 @@ namespace {
 using namespace attn;
 
 constexpr int kThreads = 256;
-constexpr int kRows = 128;  // rows of a workgroup in either kernel, 32 a wave
+constexpr int kRows = 128;  // rows of a workgroup, 32 a wave
+constexpr int kMostParts = 8;
 
 struct BwdK {
     int64_t T;
@@ -33,8 +34,9 @@ struct BwdK {
     float2* stats;    // [T, H]: lse log2(e), delta
     void* dog;        // [T, H, dv]: dy * sigmoid(z), or dy itself without a gate
     float scale;
-    int parts;
+    int parts, q_parts;
     float* part;      // [parts][T, Hkv][dk + dv]
+    float* q_part;    // [q_parts][T, H][dk]
 };
 
 // One row (token, head) per 16 lanes.
@@ -106,7 +108,8 @@ struct DqSizes {
     static constexpr int kLds = 2 * kBuf + tr_slack(DV);
 };
 
-// Query gradients: one workgroup per (tile of 128 queries, head).
+// Query gradients: one workgroup per (tile of 128 queries, head, part of the
+// keys).
 template <typename T, int DK, int DV>
 __device__ __forceinline__ void query_gradients(const BwdK& a, unsigned block, char* smem) {
     using Sz = DqSizes<T, DK, DV>;
@@ -119,8 +122,8 @@ __device__ __forceinline__ void query_gradients(const BwdK& a, unsigned block, c
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int c = lane & 31, half = lane >> 5;
     const int G = a.H / a.Hkv;
-    const int64_t rank = block / a.H;
-    const int slot = block % a.H;
+    const int64_t rank = block / (a.H * a.q_parts);
+    const int slot = block % (a.H * a.q_parts) / a.q_parts, part = block % a.q_parts;
     const int kvh = slot % a.Hkv, h = kvh * G + slot / a.Hkv;
     const Tile t = find_tile<kRows>(a.cu, a.N, a.T, rank);
     if (!t.there) return;
@@ -153,7 +156,9 @@ __device__ __forceinline__ void query_gradients(const BwdK& a, unsigned block, c
     rk.init_rows(c, half);
     rk.init_columns(lane);
     rv.init_rows(c, half);
-    const int last = min(t.level * kRows + kRows, t.len);
+    const int64_t steps = (min(t.level * kRows + kRows, t.len) + kKeys - 1) / kKeys;  // keys [0, steps kKeys) are attended by some row
+    const int start = static_cast<int>(steps * part / a.q_parts) * kKeys;
+    const int last = static_cast<int>(steps * (part + 1) / a.q_parts) * kKeys;
     const T* kbase = static_cast<const T*>(a.k) + kvh * DK;
     const T* vbase = static_cast<const T*>(a.v) + kvh * DV;
     auto fetch = [&](int j0) {
@@ -176,7 +181,7 @@ __device__ __forceinline__ void query_gradients(const BwdK& a, unsigned block, c
                 s = mma<T>(rk.rows(sK + 32 * u * rk.kRow, p), qf[p], s);
                 if (p < kVPieces) dp = mma<T>(rv.rows(sV + 32 * u * rv.kRow, p), of[p < kVPieces ? p : 0], dp);
             }
-            lookahead<kQPieces + kVPieces, 3, Elem<T>::kMfmas>();
+            lookahead<kQPieces + kVPieces, sizeof(T) == 2 ? 3 : 1, Elem<T>::kMfmas>();
 #pragma unroll
             for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], sc, -lse2)) * (dp[r] - delta);
             if (k0 + 31 > q0) {  // the diagonal: keys behind the row's own are not attended
@@ -195,11 +200,13 @@ __device__ __forceinline__ void query_gradients(const BwdK& a, unsigned block, c
             if constexpr (sizeof(T) == 2) lookahead<kKTiles * kP, 3, 1, 2>();
         }
     };
-    fetch(0);
-    arrive(qf);
-    arrive(of);
-    put(smem);
-    for (int j0 = 0; j0 < last; j0 += 2 * kKeys) {
+    if (start < last) {
+        fetch(start);
+        arrive(qf);
+        arrive(of);
+        put(smem);
+    }
+    for (int j0 = start; j0 < last; j0 += 2 * kKeys) {
         tile_barrier();
         if (j0 + kKeys < last) fetch(j0 + kKeys);
         work(smem, j0);
@@ -210,7 +217,11 @@ __device__ __forceinline__ void query_gradients(const BwdK& a, unsigned block, c
         work(smem + Sz::kBuf, j0 + kKeys);
         if (j0 + 2 * kKeys < last) put(smem);
     }
-    if (c < rows) store_rows<T, DK>(static_cast<T*>(a.dq) + at * DK, acc, a.scale, half);
+    if (c >= rows) return;
+    if (a.q_parts > 1)
+        store_rows<float, DK>(a.q_part + (static_cast<int64_t>(part) * a.T * a.H + at) * DK, acc, a.scale, half);
+    else
+        store_rows<T, DK>(static_cast<T*>(a.dq) + at * DK, acc, a.scale, half);
 }
 
 template <typename T, int DK, int DV>
@@ -399,39 +410,57 @@ __device__ __forceinline__ void key_gradients(const BwdK& a, unsigned block, cha
 // other, each launch ends with most of the chip idle: the small fp32 batch
 // takes 55 + 59 us so).
 template <typename T, int DK, int DV>
-__global__ __launch_bounds__(kThreads, (DK * sizeof(T) <= 256 ? 2 : 1)) void attn_bwd_kernel(BwdK a, unsigned key_groups) {
+__global__ __launch_bounds__(kThreads, (DK * sizeof(T) < 256 || (sizeof(T) == 2 && DK == 128) ? 2 : 1)) void attn_bwd_kernel(BwdK a, unsigned key_groups) {
     extern __shared__ __align__(16) char smem[];
     if (blockIdx.x < key_groups) key_gradients<T, DK, DV>(a, blockIdx.x, smem);
     else query_gradients<T, DK, DV>(a, blockIdx.x - key_groups, smem);
 }
 
-// Adds the parts in their order, four channels per thread.
+// Adds the parts in their order, four channels per thread: first the rows of
+// the key heads (dk and dv together), then those of the query heads.
 template <typename T, int DK, int DV>
 __global__ __launch_bounds__(kThreads) void attn_bwd_sum_kernel(BwdK a) {
-    constexpr int kRow = (DK + DV) / 4;
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    constexpr int kKv = (DK + DV) / 4, kQ = DK / 4;
     const int64_t tokens = a.cu == nullptr ? a.T : min(static_cast<int64_t>(max(a.cu[a.N], 0)), a.T);
-    const int64_t row = i / kRow;
-    if (row >= tokens * a.Hkv) return;
-    const int ch = static_cast<int>(i % kRow) * 4;
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int p = 0; p < a.parts; ++p) {
-        float x[4];
-        ld4(a.part + (static_cast<int64_t>(p) * a.T * a.Hkv + row) * (DK + DV) + ch, x);
+    const int64_t kv_all = a.parts > 1 ? tokens * a.Hkv * kKv : 0, q_all = a.q_parts > 1 ? tokens * a.H * kQ : 0;
+    int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    auto add = [&](const float* from, int64_t step, int parts, float (&sum)[4]) {
+        for (int p = 0; p < parts; ++p) {
+            float x[4];
+            ld4(from + p * step, x);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sum[e] += x[e];
+            for (int e = 0; e < 4; ++e) sum[e] += x[e];
+        }
+    };
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    if (i < kv_all) {
+        const int64_t row = i / kKv;
+        const int ch = static_cast<int>(i % kKv) * 4;
+        add(a.part + row * (DK + DV) + ch, a.T * a.Hkv * (DK + DV), a.parts, sum);
+        if (ch < DK) st4(static_cast<T*>(a.dk) + row * DK + ch, sum);
+        else st4(static_cast<T*>(a.dv) + row * DV + ch - DK, sum);
+        return;
     }
-    if (ch < DK) st4(static_cast<T*>(a.dk) + row * DK + ch, sum);
-    else st4(static_cast<T*>(a.dv) + row * DV + ch - DK, sum);
+    i -= kv_all;
+    if (i >= q_all) return;
+    add(a.q_part + i * 4, a.T * a.H * DK, a.q_parts, sum);
+    st4(static_cast<T*>(a.dq) + i * 4, sum);
 }
 
-// Into how many parts the work of a key tile is cut: enough workgroups to
-// fill the chip several times, since their lengths differ.
-int dkv_parts(int64_t T, int N, int Hkv) {
-    const int64_t units = attn_tiles(T, N, kRows) * Hkv;
-    if (units == 0) return 1;
-    const int64_t parts = (1024 + units - 1) / units;
-    return static_cast<int>(parts < 1 ? 1 : parts > 8 ? 8 : parts);
+// Into how many parts the work of a tile is cut: key tiles so that their
+// workgroups, which differ in length, fill the chip several times; query tiles
+// where they and the key tiles' together leave it half empty.
+struct BwdParts {
+    int key, query;
+};
+BwdParts bwd_parts(int64_t T, int N, int H, int Hkv) {
+    const int64_t tiles = attn_tiles(T, N, kRows), keys = tiles * Hkv, queries = tiles * H;
+    if (tiles == 0) return {1, 1};
+    auto parts = [](int64_t want, int64_t units, int64_t most) {
+        const int64_t p = (want + units - 1) / units;
+        return static_cast<int>(p < 1 ? 1 : p > most ? most : p);
+    };
+    return {parts(1024, keys, kMostParts), parts(384, queries, kMostParts / 2)};
 }
 
 size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -454,8 +483,12 @@ hipError_t launch_bwd(const AttnBackwardArgs& a, hipStream_t s) {
     ws += up256(static_cast<size_t>(f.T) * f.H * 8);
     k.dog = f.z != nullptr ? static_cast<void*>(ws) : const_cast<void*>(a.dy);
     if (f.z != nullptr) ws += up256(static_cast<size_t>(f.T) * f.H * DV * sizeof(T));
-    k.parts = dkv_parts(f.T, f.N, f.Hkv);
+    const BwdParts parts = bwd_parts(f.T, f.N, f.H, f.Hkv);
+    k.parts = parts.key;
+    k.q_parts = parts.query;
     k.part = reinterpret_cast<float*>(ws);
+    if (k.parts > 1) ws += up256(static_cast<size_t>(k.parts) * f.T * f.Hkv * (DK + DV) * 4);
+    k.q_part = reinterpret_cast<float*>(ws);
     constexpr int lds = DqSizes<T, DK, DV>::kLds > DkvSizes<T, DK, DV>::kLds ? DqSizes<T, DK, DV>::kLds : DkvSizes<T, DK, DV>::kLds;
     hipError_t e = allow_lds(attn_bwd_kernel<T, DK, DV>, lds);
     if (e != hipSuccess) return e;
@@ -470,14 +503,14 @@ hipError_t launch_bwd(const AttnBackwardArgs& a, hipStream_t s) {
     {
         LaunchTimer timer("attn_bwd", s);
         const int64_t key_groups = tiles * f.Hkv * k.parts;
-        attn_bwd_kernel<T, DK, DV><<<dim3(static_cast<unsigned>(key_groups + tiles * f.H)), dim3(kThreads), lds, s>>>(
+        attn_bwd_kernel<T, DK, DV><<<dim3(static_cast<unsigned>(key_groups + tiles * f.H * k.q_parts)), dim3(kThreads), lds, s>>>(
             k, static_cast<unsigned>(key_groups));
     }
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    if (k.parts > 1) {
+    if (k.parts > 1 || k.q_parts > 1) {
         LaunchTimer timer("attn_bwd_sum", s);
-        const int64_t threads = f.T * f.Hkv * ((DK + DV) / 4);
+        const int64_t threads = (k.parts > 1 ? f.T * f.Hkv * ((DK + DV) / 4) : 0) + (k.q_parts > 1 ? f.T * f.H * (DK / 4) : 0);
         attn_bwd_sum_kernel<T, DK, DV><<<dim3(static_cast<unsigned>((threads + kThreads - 1) / kThreads)), dim3(kThreads), 0, s>>>(k);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
@@ -489,9 +522,10 @@ hipError_t launch_bwd(const AttnBackwardArgs& a, hipStream_t s) {
 
 size_t attn_backward_workspace_bytes(int64_t T, int N, int H, int Hkv, int dk, int dv, DT x, bool gate) {
     const size_t rows = static_cast<size_t>(T) * H;
-    const int parts = dkv_parts(T, N, Hkv);
+    const BwdParts parts = bwd_parts(T, N, H, Hkv);
     return up256(rows * 8) + (gate ? up256(rows * dv * (x == DT::BF16 ? 2 : 4)) : 0) +
-           (parts > 1 ? up256(static_cast<size_t>(parts) * T * Hkv * (dk + dv) * 4) : 0);
+           (parts.key > 1 ? up256(static_cast<size_t>(parts.key) * T * Hkv * (dk + dv) * 4) : 0) +
+           (parts.query > 1 ? up256(static_cast<size_t>(parts.query) * rows * dk * 4) : 0);
 }
 
 hipError_t launch_attn_prefill_backward(const AttnBackwardArgs& a, hipStream_t s) {
