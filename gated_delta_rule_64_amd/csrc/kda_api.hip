@@ -853,7 +853,7 @@ size_t kda_attn_tree_workspace_bytes(int32_t B, int32_t T, int32_t H, int32_t Hk
     if (B < 0 || T < 0 || T > kda::kTreeMaxTokens || H < 1 || H > 65535 || Hkv < 1 || H % Hkv != 0 || max_context < 0 ||
         max_context >= (int64_t(1) << 31) || !kda::attn_head_sizes(dk, dv) || !valid_dtype(x_dtype))
         return 0;
-    return kda::attn_tree_workspace_bytes(B, T, H, Hkv, dk, dv, static_cast<kda::DT>(x_dtype), max_context);
+    return kda::attn_tree_workspace_bytes(B, T, H, Hkv, dv, max_context);
 }
 
 int kda_attn_tree(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t dk, int32_t dv, int32_t x_dtype, float scale,

@@ -39,15 +39,16 @@ struct TreeK {
     float* part;   // [splits][B, Hkv, T G][dv]
     float* stats;  // [splits][B, Hkv, T G][2]: maximum (raw scores), sum of weights
     int splits, blocks;  // workgroups per (sequence, key head): parts of the keys, blocks of rows
+    int units;           // all but the blocks: sequences, key heads and parts
 };
 
-template <typename T, int DK, int DV, int NQ>
+template <typename T, int DK, int DV>
 struct TreeSizes {
     static constexpr int kTile = kKeys * (DK + DV) * static_cast<int>(sizeof(T)) + tr_slack(DV);
     static constexpr int kWaves = 4 * kTile <= 160 * 1024 ? 4 : 2;
     static constexpr int kVTiles = (DV + 31) / 32;
-    static constexpr int kPart = NQ * kVTiles * 16 * 64 * 4;        // one wave's sums
-    static constexpr int kJoin = kWaves / 2 * (kPart + NQ * 2 * 64 * 4);
+    static constexpr int kPart = kVTiles * 16 * 64 * 4;        // one wave's sums
+    static constexpr int kJoin = kWaves / 2 * (kPart + 2 * 64 * 4);
     static constexpr int kLds = kWaves * kTile > kJoin ? kWaves * kTile : kJoin;
 };
 
@@ -73,9 +74,9 @@ __device__ __forceinline__ void store4(T* out, const T* z, float (&y)[4]) {
     st4(out, y);
 }
 
-template <typename T, int DK, int DV, int NQ>
-__global__ __launch_bounds__((64 * TreeSizes<T, DK, DV, NQ>::kWaves), (sizeof(T) == 2 && NQ == 1 && DK <= 128 ? 2 : 1)) void attn_tree_kernel(TreeK a) {
-    using Sz = TreeSizes<T, DK, DV, NQ>;
+template <typename T, int DK, int DV>
+__global__ __launch_bounds__((64 * TreeSizes<T, DK, DV>::kWaves), (sizeof(T) == 2 && DK <= 128 ? 2 : 1)) void attn_tree_kernel(TreeK a) {
+    using Sz = TreeSizes<T, DK, DV>;
     constexpr int kE = sizeof(T);
     constexpr int kQPieces = DK / (2 * Elem<T>::kPer16);
     constexpr int kVTiles = Sz::kVTiles, kWaves = Sz::kWaves;
@@ -92,9 +93,13 @@ __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV, NQ>::kWaves), (sizeof(T)
     rv.init_columns(lane);
 
     const int G = a.H / a.Hkv, rows = a.T * G;
-    int id = blockIdx.x;
-    const int block = id % a.blocks;
-    id /= a.blocks;
+    // The row blocks of the same keys eight workgroups apart: on the same XCD
+    // (workgroups go to the eight in turn) and at about the same time, so that
+    // the keys come from its L2 for all but one of them.
+    const int group = blockIdx.x / (8 * a.blocks), within = blockIdx.x % (8 * a.blocks);
+    const int block = within / 8;
+    int id = group * 8 + within % 8;
+    if (id >= a.units) return;
     const int split = id % a.splits;
     id /= a.splits;
     const int kvh = id % a.Hkv, b = id / a.Hkv;
@@ -103,26 +108,15 @@ __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV, NQ>::kWaves), (sizeof(T)
     slot = uniform(slot);
     ctx = uniform(ctx);
 
-    // this lane's rows (columns of the transposed scores)
-    int row[NQ];
-    int64_t q_at[NQ];  // index of the row in [B, T, H]
-    bool mine[NQ];
+    // this lane's row (column of the transposed scores)
+    const int row = block * 32 + c;
+    const bool mine = row < rows;
+    const int token = (mine ? row : 0) / G;
+    const int64_t q_at = (static_cast<int64_t>(b) * a.T + token) * a.H + kvh * G + (mine ? row : 0) % G;  // the row in [B, T, H]
+    f32x16 acc[kVTiles];
+    float m = -INFINITY, l = 0.f;
 #pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-        row[n] = (block * NQ + n) * 32 + c;
-        mine[n] = row[n] < rows;
-        const int r = mine[n] ? row[n] : 0;
-        q_at[n] = (static_cast<int64_t>(b) * a.T + r / G) * a.H + kvh * G + r % G;
-    }
-    f32x16 acc[NQ][kVTiles];
-    float m[NQ], l[NQ];
-#pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-        m[n] = -INFINITY;
-        l[n] = 0.f;
-#pragma unroll
-        for (int i = 0; i < kVTiles; ++i) acc[n][i] = f32x16{};
-    }
+    for (int i = 0; i < kVTiles; ++i) acc[i] = f32x16{};
 
     const int ctx_tiles = (ctx + kKeys - 1) / kKeys, tiles = ctx_tiles + (a.T + kKeys - 1) / kKeys;
     const int each = (tiles + a.splits - 1) / a.splits;
@@ -130,23 +124,17 @@ __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV, NQ>::kWaves), (sizeof(T)
     int tile = split * each + wave;
 
     if (tile < t_end) {
-        // the rows' queries stay in registers, but for the longest fp32 ones,
-        // which are read again from the caches for every tile
+        // the row's query stays in registers, but for the longest fp32 one,
+        // which is read again from the caches for every tile
         constexpr bool kKeep = kE == 2 || DK <= 128;
-        u32x4 qf[NQ][kKeep ? kQPieces : 1];
-        const char* q_row[NQ];
-        uint64_t seen[NQ];
+        u32x4 qf[kKeep ? kQPieces : 1];
+        const char* q_row = static_cast<const char*>(a.q) + q_at * kKRow + half * 16;
+        if constexpr (kKeep) {
 #pragma unroll
-        for (int n = 0; n < NQ; ++n) {
-            q_row[n] = static_cast<const char*>(a.q) + q_at[n] * kKRow + half * 16;
-            if constexpr (kKeep) {
-#pragma unroll
-                for (int p = 0; p < kQPieces; ++p) qf[n][p] = *reinterpret_cast<const u32x4*>(q_row[n] + p * 32);
-            }
-            const int t = (mine[n] ? row[n] : 0) / G;
-            seen[n] = a.mask != nullptr ? static_cast<uint64_t>(a.mask[static_cast<int64_t>(b) * a.T + t])
-                                        : ~0ull >> (63 - t);
+            for (int p = 0; p < kQPieces; ++p) qf[p] = *reinterpret_cast<const u32x4*>(q_row + p * 32);
         }
+        const uint64_t seen = a.mask != nullptr ? static_cast<uint64_t>(a.mask[static_cast<int64_t>(b) * a.T + token])
+                                                : ~0ull >> (63 - token);
         const float sc = a.scale * kLog2e;
 
         // Half a tile: 16 rows of keys and of values, 16-byte pieces
@@ -205,42 +193,43 @@ __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV, NQ>::kWaves), (sizeof(T)
                     *reinterpret_cast<u32x4*>(sV + r * kVRow + (p % (kVRow / 16) ^ turn<kVRow / 16>(r)) * 16) = vr[from][i];
             }
         };
-        // the tile in LDS; hide(scores, n) masks those of row block n
+        // the tile in LDS; hide(scores) masks its scores
         auto work = [&](auto hide) __attribute__((always_inline)) {
             wave_lds_fence();
+            f32x16 s{};
 #pragma unroll
-            for (int n = 0; n < NQ; ++n) {
-                f32x16 s{};
+            for (int p = 0; p < kQPieces; ++p) {
+                u32x4 x;
+                if constexpr (kKeep) x = qf[p];
+                else x = *reinterpret_cast<const u32x4*>(q_row + p * 32);
+                s = mma<T>(rk.rows(sK, p), x, s);
+            }
+            hide(s);
+            float top = s[0];
 #pragma unroll
-                for (int p = 0; p < kQPieces; ++p) 
-                    s = mma<T>(rk.rows(sK, p), kKeep ? qf[n][kKeep ? p : 0] : *reinterpret_cast<const u32x4*>(q_row[n] + p * 32), s);
-                hide(s, n);
-                float top = s[0];
+            for (int r = 1; r < 16; ++r) top = fmaxf(top, s[r]);
+            top = xor32_max(top);
+            if (__any((top - m) * sc > kRise)) {
+                const float next = fmaxf(m, top);
+                const float alpha = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - next) * sc);
+                m = next;
+                l *= alpha;
 #pragma unroll
-                for (int r = 1; r < 16; ++r) top = fmaxf(top, s[r]);
-                top = xor32_max(top);
-                if (__any((top - m[n]) * sc > kRise)) {
-                    const float next = fmaxf(m[n], top);
-                    const float alpha = m[n] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m[n] - next) * sc);
-                    m[n] = next;
-                    l[n] *= alpha;
+                for (int i = 0; i < kVTiles; ++i) acc[i] *= alpha;
+            }
+            const float ms = m == -INFINITY ? 0.f : m * sc;
+            float sum = 0.f;
 #pragma unroll
-                    for (int i = 0; i < kVTiles; ++i) acc[n][i] *= alpha;
-                }
-                const float ms = m[n] == -INFINITY ? 0.f : m[n] * sc;
-                float sum = 0.f;
+            for (int r = 0; r < 16; ++r) {
+                s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], sc, -ms));
+                sum += s[r];
+            }
+            l += sum;
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], sc, -ms));
-                    sum += s[r];
-                }
-                l[n] += sum;
+            for (int p = 0; p < kP; ++p) {
+                const u32x4 x = as_operand<T>(s, p);
 #pragma unroll
-                for (int p = 0; p < kP; ++p) {
-                    const u32x4 x = as_operand<T>(s, p);
-#pragma unroll
-                    for (int i = 0; i < kVTiles; ++i) acc[n][i] = mma<T>(rv.columns(sV, i, p), x, acc[n][i]);
-                }
+                for (int i = 0; i < kVTiles; ++i) acc[i] = mma<T>(rv.columns(sV, i, p), x, acc[i]);
             }
         };
         // register r of a score: key 8 (r / 4) + 4 half + r % 4 of the tile
@@ -255,10 +244,7 @@ __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV, NQ>::kWaves), (sizeof(T)
                 fetch_half(tile, now, 1);
             }
             if (tile + kWaves < c_end) next = look_up(tile + kWaves);
-            if constexpr (kKeep) {
-#pragma unroll
-                for (int n = 0; n < NQ; ++n) arrive(qf[n]);
-            }
+            if constexpr (kKeep) arrive(qf);
             for (; tile < c_end; tile += kWaves) {
                 wave_lds_fence();
 #pragma unroll
@@ -275,7 +261,7 @@ __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV, NQ>::kWaves), (sizeof(T)
                     }
                     if (tile + 2 * kWaves < c_end) next = look_up(tile + 2 * kWaves);
                 }
-                work([&](f32x16& s, int) __attribute__((always_inline)) {
+                work([&](f32x16& s) __attribute__((always_inline)) {
                     if (n0 + n1 == kKeys) return;
                     const int lo = opaque(n0 - 4 * half), hi = opaque(n1 - 4 * half);
 #pragma unroll
@@ -306,8 +292,8 @@ __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV, NQ>::kWaves), (sizeof(T)
                 }
                 put_half(x);
             }
-            work([&](f32x16& s, int n) __attribute__((always_inline)) {
-                const uint32_t bits = static_cast<uint32_t>(seen[n] >> t0) >> (4 * half);
+            work([&](f32x16& s) __attribute__((always_inline)) {
+                const uint32_t bits = static_cast<uint32_t>(seen >> t0) >> (4 * half);
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
                     const int key = 8 * (r / 4) + r % 4;
@@ -316,92 +302,80 @@ __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV, NQ>::kWaves), (sizeof(T)
             });
         }
     }
-#pragma unroll
-    for (int n = 0; n < NQ; ++n) l[n] = xor32_add(l[n]);
+    l = xor32_add(l);
 
     // join the waves, the upper half of them into the lower, until one is left
     __syncthreads();
     const float sc = a.scale * kLog2e;
     for (int left = kWaves / 2; left >= 1; left /= 2) {
-        char* at = smem + (wave % left) * (Sz::kPart + NQ * 2 * 64 * 4);
+        char* at = smem + (wave % left) * (Sz::kPart + 2 * 64 * 4);
         float* stats = reinterpret_cast<float*>(at + Sz::kPart);
         if (wave >= left && wave < 2 * left) {
 #pragma unroll
-            for (int n = 0; n < NQ; ++n) {
+            for (int i = 0; i < kVTiles; ++i)
 #pragma unroll
-                for (int i = 0; i < kVTiles; ++i)
-#pragma unroll
-                    for (int r4 = 0; r4 < 4; ++r4)
-                        *reinterpret_cast<f32x4*>(at + (((n * kVTiles + i) * 4 + r4) * 64 + lane) * 16) =
-                            f32x4{acc[n][i][4 * r4], acc[n][i][4 * r4 + 1], acc[n][i][4 * r4 + 2], acc[n][i][4 * r4 + 3]};
-                stats[(2 * n) * 64 + lane] = m[n];
-                stats[(2 * n + 1) * 64 + lane] = l[n];
-            }
+                for (int r4 = 0; r4 < 4; ++r4)
+                    *reinterpret_cast<f32x4*>(at + ((i * 4 + r4) * 64 + lane) * 16) =
+                        f32x4{acc[i][4 * r4], acc[i][4 * r4 + 1], acc[i][4 * r4 + 2], acc[i][4 * r4 + 3]};
+            stats[lane] = m;
+            stats[64 + lane] = l;
         }
         __syncthreads();
         if (wave < left) {
+            const float mo = stats[lane], lo = stats[64 + lane];
+            const float top = fmaxf(m, mo);
+            const float fa = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - top) * sc);
+            const float fb = mo == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((mo - top) * sc);
+            m = top;
+            l = l * fa + lo * fb;
 #pragma unroll
-            for (int n = 0; n < NQ; ++n) {
-                const float mo = stats[(2 * n) * 64 + lane], lo = stats[(2 * n + 1) * 64 + lane];
-                const float top = fmaxf(m[n], mo);
-                const float fa = m[n] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m[n] - top) * sc);
-                const float fb = mo == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((mo - top) * sc);
-                m[n] = top;
-                l[n] = l[n] * fa + lo * fb;
+            for (int i = 0; i < kVTiles; ++i)
 #pragma unroll
-                for (int i = 0; i < kVTiles; ++i)
+                for (int r4 = 0; r4 < 4; ++r4) {
+                    const f32x4 o = *reinterpret_cast<const f32x4*>(at + ((i * 4 + r4) * 64 + lane) * 16);
 #pragma unroll
-                    for (int r4 = 0; r4 < 4; ++r4) {
-                        const f32x4 o = *reinterpret_cast<const f32x4*>(at + (((n * kVTiles + i) * 4 + r4) * 64 + lane) * 16);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[n][i][4 * r4 + e] = acc[n][i][4 * r4 + e] * fa + o[e] * fb;
-                    }
-            }
+                    for (int e = 0; e < 4; ++e) acc[i][4 * r4 + e] = acc[i][4 * r4 + e] * fa + o[e] * fb;
+                }
         }
         __syncthreads();
     }
-    if (wave != 0) return;
+    if (wave != 0 || !mine) return;
 
-#pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-        if (!mine[n]) continue;
-        if (a.splits > 1) {
-            if (!real) continue;  // the joining kernel writes padding rows
-            const int64_t at = ((static_cast<int64_t>(split) * a.B + b) * a.Hkv + kvh) * rows + row[n];
-            if (half == 0) {
-                a.stats[2 * at] = m[n];
-                a.stats[2 * at + 1] = l[n];
-            }
-            if (l[n] > 0.f) {
-#pragma unroll
-                for (int i = 0; i < kVTiles; ++i)
-#pragma unroll
-                    for (int r4 = 0; r4 < 4; ++r4) {
-                        const int ch = 32 * i + 8 * r4 + 4 * half;
-                        if (ch < DV)
-                            *reinterpret_cast<f32x4*>(a.part + at * DV + ch) =
-                                f32x4{acc[n][i][4 * r4], acc[n][i][4 * r4 + 1], acc[n][i][4 * r4 + 2], acc[n][i][4 * r4 + 3]};
-                    }
-            }
-            continue;
+    if (a.splits > 1) {
+        if (!real) return;  // the joining kernel writes padding rows
+        const int64_t at = ((static_cast<int64_t>(split) * a.B + b) * a.Hkv + kvh) * rows + row;
+        if (half == 0) {
+            a.stats[2 * at] = m;
+            a.stats[2 * at + 1] = l;
         }
-        const float inv = l[n] > 0.f ? 1.f / l[n] : 0.f;
-        if (a.lse != nullptr && half == 0)
-            a.lse[q_at[n]] = l[n] > 0.f ? (m[n] * sc + __builtin_amdgcn_logf(l[n])) * kLn2 : -INFINITY;
-        T* out = static_cast<T*>(a.out) + q_at[n] * DV;
-        const T* z = a.z != nullptr && real ? static_cast<const T*>(a.z) + q_at[n] * DV : nullptr;
+        if (l > 0.f) {
 #pragma unroll
-        for (int i = 0; i < kVTiles; ++i)
+            for (int i = 0; i < kVTiles; ++i)
 #pragma unroll
-            for (int r4 = 0; r4 < 4; ++r4) {
-                const int ch = 32 * i + 8 * r4 + 4 * half;
-                if (ch >= DV) continue;
-                float y[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = acc[n][i][4 * r4 + e] * inv;
-                store4<T>(out + ch, z != nullptr ? z + ch : nullptr, y);
-            }
+                for (int r4 = 0; r4 < 4; ++r4) {
+                    const int ch = 32 * i + 8 * r4 + 4 * half;
+                    if (ch < DV)
+                        *reinterpret_cast<f32x4*>(a.part + at * DV + ch) =
+                            f32x4{acc[i][4 * r4], acc[i][4 * r4 + 1], acc[i][4 * r4 + 2], acc[i][4 * r4 + 3]};
+                }
+        }
+        return;
     }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    if (a.lse != nullptr && half == 0) a.lse[q_at] = l > 0.f ? (m * sc + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+    T* out = static_cast<T*>(a.out) + q_at * DV;
+    const T* z = a.z != nullptr && real ? static_cast<const T*>(a.z) + q_at * DV : nullptr;
+#pragma unroll
+    for (int i = 0; i < kVTiles; ++i)
+#pragma unroll
+        for (int r4 = 0; r4 < 4; ++r4) {
+            const int ch = 32 * i + 8 * r4 + 4 * half;
+            if (ch >= DV) continue;
+            float y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = acc[i][4 * r4 + e] * inv;
+            store4<T>(out + ch, z != nullptr ? z + ch : nullptr, y);
+        }
 }
 
 // Joins the parts, kWaves waves to a row: thread s of the row weighs part s,
@@ -486,22 +460,23 @@ __global__ __launch_bounds__(kJoinThreads) void attn_tree_join_kernel(TreeK a) {
                   a.z != nullptr && real ? static_cast<const T*>(a.z) + r * DV + ch : nullptr, out);
 }
 
-// Whether a wave can take two blocks of 32 rows: their sums and queries fit
-// the registers beside a tile in flight.
-constexpr bool two_blocks(int dk, DT x) { return x == DT::BF16 && dk <= 128; }
-
-// Row blocks and splits of a call.
+// Row blocks and parts of a call.
 struct TreePlan {
-    int nq, blocks, splits;
+    int blocks, splits;
 };
-TreePlan tree_plan(int B, int T, int H, int Hkv, int dk, DT x, int64_t max_ctx) {
+TreePlan tree_plan(int B, int T, int H, int Hkv, int64_t max_ctx) {
     const int64_t rows = static_cast<int64_t>(T) * (H / Hkv);
     TreePlan p;
-    p.nq = rows > 32 && two_blocks(dk, x) ? 2 : 1;
-    p.blocks = static_cast<int>((rows + 32 * p.nq - 1) / (32 * p.nq));
+    p.blocks = static_cast<int>((rows + 31) / 32);
     const int64_t units = static_cast<int64_t>(B) * Hkv * p.blocks;
     const int64_t tiles = (max_ctx + kKeys - 1) / kKeys + (T + kKeys - 1) / kKeys;
-    int64_t s = (1024 + units - 1) / units;
+    // Two workgroups fit a CU.  The parts of one sequence are equally long:
+    // one round of them (262,144 tokens: 193 us and 8 us to join them, against
+    // 198 and 9 us in two rounds).  Sequences differ, and two rounds let the
+    // short ones fill up behind the long (64 of up to 8,000 tokens: 219 us
+    // against 239 us in one).
+    const int64_t want = B == 1 ? 512 : 1024;
+    int64_t s = (want + units - 1) / units;
     if (s > tiles / 8) s = tiles / 8;  // two tiles a wave at least
     p.splits = static_cast<int>(s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s);
     return p;
@@ -509,35 +484,28 @@ TreePlan tree_plan(int B, int T, int H, int Hkv, int dk, DT x, int64_t max_ctx) 
 
 size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
-template <typename T, int DK, int DV, int NQ>
-hipError_t launch_nq(const TreeK& k, hipStream_t s) {
-    using Sz = TreeSizes<T, DK, DV, NQ>;
-    static_assert(Sz::kLds <= 160 * 1024, "one workgroup's LDS");
-    auto fn = attn_tree_kernel<T, DK, DV, NQ>;
-    if (Sz::kLds > 64 * 1024) {
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, Sz::kLds);
-        if (e != hipSuccess) return e;
-    }
-    LaunchTimer timer("attn_tree", s);
-    const int64_t groups = static_cast<int64_t>(k.B) * k.Hkv * k.blocks * k.splits;
-    fn<<<dim3(static_cast<unsigned>(groups)), dim3(64 * Sz::kWaves), Sz::kLds, s>>>(k);
-    return hipGetLastError();
-}
-
 template <typename T, int DK, int DV>
 hipError_t launch_tree(const TreeArgs& a, hipStream_t s) {
-    const TreePlan p = tree_plan(a.B, a.T, a.H, a.Hkv, DK, a.x, static_cast<int64_t>(a.max_pages) << a.page_shift);
+    const TreePlan p = tree_plan(a.B, a.T, a.H, a.Hkv, static_cast<int64_t>(a.max_pages) << a.page_shift);
     const size_t parts = static_cast<size_t>(p.splits) * a.B * a.T * a.H;
     float* part = static_cast<float*>(a.ws);
     float* stats = reinterpret_cast<float*>(static_cast<char*>(a.ws) + up256(parts * DV * 4));
     const TreeK k{a.B, a.T, a.H, a.Hkv, a.scale, a.q, a.k_new, a.v_new, a.z, a.mask, a.k_cache, a.v_cache,
                   a.pages, a.page_shift, a.table, a.slots, a.max_pages, a.lens, a.slot_indices, a.out, a.lse,
-                  part, stats, p.splits, p.blocks};
-    hipError_t e = hipErrorInvalidValue;
-    if constexpr (two_blocks(DK, sizeof(T) == 2 ? DT::BF16 : DT::F32)) {
-        if (p.nq == 2) e = launch_nq<T, DK, DV, 2>(k, s);
+                  part, stats, p.splits, p.blocks, a.B * a.Hkv * p.splits};
+    using Sz = TreeSizes<T, DK, DV>;
+    static_assert(Sz::kLds <= 160 * 1024, "one workgroup's LDS");
+    auto fn = attn_tree_kernel<T, DK, DV>;
+    if (Sz::kLds > 64 * 1024) {
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, Sz::kLds);
+        if (e != hipSuccess) return e;
     }
-    if (p.nq == 1) e = launch_nq<T, DK, DV, 1>(k, s);
+    {
+        LaunchTimer timer("attn_tree", s);
+        const int64_t groups = static_cast<int64_t>((k.units + 7) / 8) * 8 * k.blocks;
+        fn<<<dim3(static_cast<unsigned>(groups)), dim3(64 * Sz::kWaves), Sz::kLds, s>>>(k);
+    }
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
     LaunchTimer timer("attn_tree_join", s);
     const int64_t rows = static_cast<int64_t>(a.B) * a.T * a.H;
@@ -550,9 +518,9 @@ hipError_t launch_tree(const TreeArgs& a, hipStream_t s) {
 
 }  // namespace
 
-size_t attn_tree_workspace_bytes(int B, int T, int H, int Hkv, int dk, int dv, DT x, int64_t max_ctx) {
+size_t attn_tree_workspace_bytes(int B, int T, int H, int Hkv, int dv, int64_t max_ctx) {
     if (B == 0 || T == 0) return 0;
-    const TreePlan p = tree_plan(B, T, H, Hkv, dk, x, max_ctx);
+    const TreePlan p = tree_plan(B, T, H, Hkv, max_ctx);
     if (p.splits == 1) return 0;
     const size_t parts = static_cast<size_t>(p.splits) * B * T * H;
     return up256(parts * dv * 4) + up256(parts * 8);
