@@ -74,6 +74,22 @@ __device__ __forceinline__ void store4(T* out, const T* z, float (&y)[4]) {
     st4(out, y);
 }
 
+// Replaces the values of a 16-byte piece that are not finite by 0; other than 0
+// if there are any.  An exponent of all ones is found by its carry.
+template <typename T>
+__device__ __forceinline__ uint32_t take_odd(u32x4& x) {
+    constexpr uint32_t kExponent = sizeof(T) == 2 ? 0x7f807f80u : 0x7f800000u, kOne = sizeof(T) == 2 ? 0x00800080u : 0x00800000u;
+    constexpr uint32_t kCarry = sizeof(T) == 2 ? 0x80008000u : 0x80000000u;
+    uint32_t any = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t odd = ((x[i] & kExponent) + kOne) & kCarry;
+        x[i] &= ~(sizeof(T) == 2 ? (odd >> 15) * 0xffffu : static_cast<uint32_t>(static_cast<int32_t>(odd) >> 31));
+        any |= odd;
+    }
+    return any;
+}
+
 template <typename T, int DK, int DV>
 __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV>::kWaves), (sizeof(T) == 2 && DK <= 128 ? 2 : 1)) void attn_tree_kernel(TreeK a) {
     using Sz = TreeSizes<T, DK, DV>;
@@ -277,7 +293,9 @@ __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV>::kWaves), (sizeof(T) == 
             const char* kb = static_cast<const char*>(a.k_new) + (static_cast<int64_t>(b) * a.T + t0) * k_step + kvh * kKRow;
             const char* vb = static_cast<const char*>(a.v_new) + (static_cast<int64_t>(b) * a.T + t0) * v_step + kvh * kVRow;
             wave_lds_fence();
-#pragma unroll
+            uint32_t odd = 0;
+            constexpr int kAtOnce = kAhead ? 2 : 1;
+#pragma unroll kAtOnce
             for (int x = 0; x < 2; ++x) {
                 const int to = kAhead ? x : 0;
 #pragma unroll
@@ -290,16 +308,34 @@ __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV>::kWaves), (sizeof(T) == 
                     const int p = lane + 64 * i, r = 16 * x + p / (kVRow / 16);
                     vr[to][i] = t0 + r < a.T ? *reinterpret_cast<const u32x4*>(vb + static_cast<int64_t>(r) * v_step + p % (kVRow / 16) * 16) : u32x4{};
                 }
+                // A value that is not finite must not meet a weight of 0 in a
+                // product: rows that do not attend its draft would get NaN.
+#pragma unroll
+                for (int i = 0; i < kVEach; ++i) odd |= take_odd<T>(vr[to][i]);
                 put_half(x);
             }
+            const uint32_t bits = static_cast<uint32_t>(seen >> t0);
             work([&](f32x16& s) __attribute__((always_inline)) {
-                const uint32_t bits = static_cast<uint32_t>(seen >> t0) >> (4 * half);
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    const int key = 8 * (r / 4) + r % 4;
-                    if (t0 + 4 * half + key >= a.T || (bits >> key & 1) == 0) s[r] = -INFINITY;
+                    const int key = 8 * (r / 4) + 4 * half + r % 4;
+                    if (t0 + key >= a.T || (bits >> key & 1) == 0) s[r] = -INFINITY;
                 }
             });
+            // (rare) such values reach the rows that attend them, as they are
+            if (__any(odd != 0)) {
+                const T* from = reinterpret_cast<const T*>(vb);
+                for (int key = 0; key < kKeys && t0 + key < a.T; ++key, from += a.Hkv * DV) {
+#pragma unroll
+                    for (int i = 0; i < kVTiles; ++i)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) {
+                            const int ch = 32 * i + 8 * (r / 4) + 4 * half + r % 4;
+                            const float v = ch < DV ? ld(from + ch) : 0.f;
+                            if ((bits >> key & 1) != 0 && !(fabsf(v) < INFINITY)) acc[i][r] += v;
+                        }
+                }
+            }
         }
     }
     l = xor32_add(l);

@@ -446,10 +446,11 @@ int kda_spec_verify(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv,
  *  - scale multiplies q . k; positive and finite.
  *  - out_gate: NULL, or logits z of out's shape: out = o * sigmoid(z).
  *  - A row that attends nothing gets 0, and -infinity as its lse.
- *  - Non-finite values reach every row that attends them.  In a tile that
- *    a row attends in part, a non-finite value behind the row's own position
- *    (same sequence only) may reach it too; other sequences' rows, memory
- *    behind a sequence's end and stale page contents never do.
+ *  - Non-finite values reach the rows that attend them.  Other sequences'
+ *    rows, memory behind a sequence's end, stale page contents and drafts that
+ *    a row does not attend never reach it.  Within one sequence of
+ *    kda_attn_prefill and its gradients, a non-finite row may also reach
+ *    rows up to 127 tokens before it (0 x infinity in a shared tile).
  *  - Rows of T_tot behind the last sequence are neither read nor written:
  *    cu_seqlens[N] may be below T_tot.
  *

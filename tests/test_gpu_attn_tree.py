@@ -231,6 +231,37 @@ def test_offsets_past_32_bits(K):
     _check(K, x, torch.bfloat16)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_drafts_that_are_not_finite(K, dtype):
+    """Unused drafts may hold anything (a padded tree); a value that is not
+    finite reaches the rows that attend its draft and no others."""
+    x = _make(14, [70, 0, 33], 40, 4, 2, 64, 64, 16, TYPES[dtype])
+    want, wl = _call(K, x)
+    words = x["mask"].cpu()
+    y = dict(x, k_new=x["k_new"].clone(), v_new=x["v_new"].clone(), mask=x["mask"].clone())
+    for b, j in ((0, 7), (1, 39), (2, 33)):  # drafts that nobody attends any more
+        y["mask"][b] &= ~(1 << j)
+        y["k_new"][b, j], y["v_new"][b, j] = math.nan, math.inf
+    out, lse = _call(K, y)
+    clean = dict(y, k_new=x["k_new"], v_new=x["v_new"])
+    a, al = _call(K, clean)
+    assert torch.equal(out, a) and torch.equal(lse, al)
+    y = dict(x, v_new=x["v_new"].clone())
+    y["v_new"][0, 5, 1, 3], y["v_new"][0, 38, 0, 63] = math.nan, -math.inf
+    out, lse = _call(K, y)
+    assert torch.equal(lse, wl)
+    for t in range(40):
+        w = want[0, t].clone()
+        if int(words[0, t]) >> 5 & 1:
+            w[2:, 3] = math.nan
+        if int(words[0, t]) >> 38 & 1:
+            w[:2, 63] = -math.inf
+        assert torch.equal(torch.isnan(out[0, t]), torch.isnan(w)), t
+        fine = ~torch.isnan(w)
+        assert torch.equal(out[0, t][fine], w[fine]), t
+    assert torch.equal(out[1:], want[1:])
+
+
 def test_captured_and_replayed(K):
     """One graph over a decode step whose lengths and tables change."""
     x = _make(11, [900, 300, 20], 4, 8, 2, 128, 128, 64, torch.bfloat16, width=40)
