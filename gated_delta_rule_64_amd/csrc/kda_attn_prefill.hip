@@ -97,6 +97,9 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void attn_fwd_k
         if (j0 > q0 + 31) return;  // nothing of the tile is attended by this wave's rows
         const char* sV = sK + kV;
         f32x16 s[kSub];
+        // the wave that multiplies goes before the one that exponentiates
+        // (2,158 to 2,136 us at 16,384 tokens)
+        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int u = 0; u < kSub; ++u) s[u] = f32x16{};
 #pragma unroll
@@ -104,6 +107,7 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void attn_fwd_k
 #pragma unroll
             for (int u = 0; u < kSub; ++u) s[u] = mma<T>(rk.rows(sK + 32 * u * rk.kRow, p), qf[p], s[u]);
         lookahead<kQPieces * kSub, 4, Elem<T>::kMfmas>();
+        __builtin_amdgcn_s_setprio(0);
         if (j0 + kKeys - 1 > q0) {  // the diagonal: keys behind the row's own are not attended
             const int most = opaque(q0 + c - j0 - 4 * half);
 #pragma unroll

@@ -370,14 +370,17 @@ __global__ __launch_bounds__(kPlan) void cache_reserve_kernel(ReserveK a) {
         e.first = min(static_cast<int>((static_cast<int64_t>(max(c.lens[e.slot], 0)) + mask) >> c.page_shift), e.end);
         return e;
     };
+    // a thread's first entry stays in its registers
+    const Entry mine = static_cast<int>(threadIdx.x) < a.n ? entry(threadIdx.x) : Entry{-1, 0, 0};
+    auto my_entry = [&](int i) { return i < kPlan ? mine : entry(i); };  // of a loop from threadIdx.x on
     for (int i = threadIdx.x; i < a.n; i += kPlan) {
-        const int s = a.slot_list[i];
-        if (s >= 0 && s < c.slots && ((static_cast<int64_t>(max(a.new_lens[i], 0)) + mask) >> c.page_shift) <= c.max_pages) slots.claim(s, i);
+        const Entry e = my_entry(i);
+        if (e.slot >= 0) slots.claim(e.slot, i);
     }
     slots.settle();
     auto owned = [&](int i, const Entry& e) { return e.slot >= 0 && slots.owner(e.slot) == i; };
     for (int i = threadIdx.x; i < a.n; i += kPlan) {
-        const Entry e = entry(i);
+        const Entry e = my_entry(i);
         int count = -1;
         if (owned(i, e)) {
             count = 0;
@@ -425,7 +428,7 @@ __global__ __launch_bounds__(kPlan) void cache_reserve_kernel(ReserveK a) {
             if (a.status != nullptr) a.status[i] = count < 0 ? 2 : fits ? 0 : 1;
             int place = count > 0 && fits ? static_cast<int>(at) : -1;
             if (place >= 0) {
-                const Entry e = entry(i);
+                const Entry e = my_entry(i);
                 if (e.end - e.first <= kFewColumns) {
                     int32_t* row = c.table + static_cast<int64_t>(e.slot) * c.max_pages;
                     for (int j = e.first; j < e.end; ++j)

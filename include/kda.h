@@ -450,7 +450,7 @@ int kda_spec_verify(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv,
  *    rows, memory behind a sequence's end, stale page contents and drafts that
  *    a row does not attend never reach it.  Within one sequence of
  *    kda_attn_prefill and its gradients, a non-finite row may also reach
- *    rows up to 127 tokens before it (0 x infinity in a shared tile).
+ *    rows up to 127 tokens from it (0 x infinity in a shared tile).
  *  - Rows of T_tot behind the last sequence are neither read nor written:
  *    cu_seqlens[N] may be below T_tot.
  *
