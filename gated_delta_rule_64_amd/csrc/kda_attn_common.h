@@ -191,15 +191,19 @@ __device__ __forceinline__ int wave_sum_int(int x) {
     return uniform(static_cast<int>(b[0] + b[1]));
 }
 
-// The rank-th tile of the batch, tiles ordered by falling level (in causal
-// attention a tile's work grows with its level, so the longest start first
-// and the short ones fill the end), sequences in order within a level.  With
-// ge(j) = sum over sequences of max(0, tiles_n - j), the tiles at level j or
-// above, the level is the largest j with ge(j) > rank: a binary search, each
-// step a sum over the sequences by the wave's lanes.  All 64 lanes call it.
+// The rank-th tile of the batch.  The tiles of a sequence follow each other, so
+// that the workgroups that read the same keys (or queries) run at about the
+// same time and find them in the L2; the longest sequences come first, and
+// within one the levels fall (in causal attention a tile's work grows with its
+// level), so that the short tiles fill the end.  Sequences are ordered so in
+// groups of 64, a lane each: a lane counts the tiles of those before its own
+// and the one whose range holds the rank answers.  All 64 lanes call it.
 template <int kRows>
 __device__ __forceinline__ Tile find_tile(const int32_t* cu, int N, int64_t T, int64_t rank) {
     Tile t;
+    t.there = false;
+    t.start = 0;
+    t.len = t.level = t.tiles = 0;
     const int lane = threadIdx.x & 63;
     if (N == 1) {
         seq_bounds(cu, 0, T, t.start, t.len);
@@ -210,57 +214,28 @@ __device__ __forceinline__ Tile find_tile(const int32_t* cu, int N, int64_t T, i
         t.level = t.there ? t.tiles - 1 - static_cast<int>(rank) : 0;
         return t;
     }
-    int64_t my_start = 0;  // the first 64 sequences stay in registers
-    int my_len = 0;
-    if (lane < N) seq_bounds(cu, lane, T, my_start, my_len);
-    auto tiles_of = [&](int n) {
-        if (n >= N) return 0;
-        int64_t start;
-        int len;
-        seq_bounds(cu, n, T, start, len);
-        return (len + kRows - 1) / kRows;
-    };
-    const int mine = (my_len + kRows - 1) / kRows;
-    auto at_least = [&](int j) {      // tiles at level j or above (at most 2^31 / kRows + N)
-        int s = max(0, mine - j);
-        for (int n = 64 + lane; n < N; n += 64) s += max(0, tiles_of(n) - j);
-        return wave_sum_int(s);
-    };
-    t.there = rank < at_least(0);
-    t.start = 0;
-    t.len = t.level = t.tiles = 0;
-    if (!t.there) return t;
-    int lo = 0, hi = 1;  // at_least(lo) > rank
-    while (at_least(hi) > rank) {
-        lo = hi;
-        hi *= 2;
-    }
-    while (hi - lo > 1) {
-        const int mid = lo + (hi - lo) / 2;
-        if (at_least(mid) > rank) lo = mid; else hi = mid;
-    }
-    int left = static_cast<int>(rank) - at_least(lo + 1);  // which of the level's sequences
+    int left = static_cast<int>(rank);  // below 2^31 / kRows + N
     for (int n0 = 0; n0 < N; n0 += 64) {
-        const int tn = n0 == 0 ? mine : tiles_of(n0 + lane);
-        unsigned long long has = __ballot(tn > lo);
-        const int count = __popcll(has);
-        if (left >= count) {
-            left -= count;
+        int64_t start = 0;
+        int len = 0;
+        if (n0 + lane < N) seq_bounds(cu, n0 + lane, T, start, len);
+        const int mine = (len + kRows - 1) / kRows, all = wave_sum_int(mine);
+        if (left >= all) {
+            left -= all;
             continue;
         }
-        for (; left > 0; --left) has &= has - 1;
-        const int n = uniform(n0 + __ffsll(static_cast<long long>(has)) - 1);
-        if (n < 64) {
-            t.start = __builtin_amdgcn_readlane(static_cast<int>(my_start), n);  // below 2^31
-            t.len = __builtin_amdgcn_readlane(my_len, n);
-        } else {
-            seq_bounds(cu, n, T, t.start, t.len);
+        int before = 0;
+        for (int m = 0; m < min(64, N - n0); ++m) {
+            const int other = __builtin_amdgcn_readlane(mine, m);
+            before += other > mine || (other == mine && m < lane) ? other : 0;
         }
-        t.len = uniform(t.len);
-        t.start = uniform64(t.start);
-        t.level = lo;
-        t.tiles = (t.len + kRows - 1) / kRows;
-        break;
+        const int owner = uniform(__ffsll(static_cast<long long>(__ballot(left >= before && left < before + mine))) - 1);
+        t.start = __builtin_amdgcn_readlane(static_cast<int>(start), owner);  // below 2^31
+        t.len = __builtin_amdgcn_readlane(len, owner);
+        t.tiles = __builtin_amdgcn_readlane(mine, owner);
+        t.level = t.tiles - 1 - (left - __builtin_amdgcn_readlane(before, owner));
+        t.there = true;
+        return t;
     }
     return t;
 }
