@@ -737,7 +737,7 @@ int check_cache(int32_t num_pages, int32_t page_size, int32_t slots, int32_t max
     if (page_size < 16 || page_size > 1024 || (1 << shift) != page_size)
         return fail(KDA_ERR_UNSUPPORTED, "page_size=%d is not a power of two in [16, 1024]", page_size);
     if (slots < 0) return fail(KDA_ERR_INVALID_ARGUMENT, "slots=%d is negative", slots);
-    if (max_pages < 1 || max_pages >= (1 << 24)) return fail(KDA_ERR_INVALID_ARGUMENT, "max_pages=%d out of range [1, 2^24)", max_pages);
+    if (max_pages < 1 || max_pages >= (1 << 23)) return fail(KDA_ERR_INVALID_ARGUMENT, "max_pages=%d out of range [1, 2^23)", max_pages);
     if ((static_cast<int64_t>(max_pages) << shift) >= (int64_t(1) << 31))
         return fail(KDA_ERR_UNSUPPORTED, "max_pages=%d pages of %d tokens reach 2^31 tokens", max_pages, page_size);
     return KDA_OK;

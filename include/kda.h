@@ -502,7 +502,8 @@ int kda_attn_prefill_backward(int64_t T_tot, int32_t H, int32_t Hkv, int32_t dk,
  *   page_size, dv]: the pools (x_dtype; page_size a power of two, 16 .. 1024);
  *   page_table  int32 [slots, max_pages]: token p of a slot is row
  *               p % page_size of page page_table[slot][p / page_size]; an
- *               entry outside [0, num_pages) names no page;
+ *               entry outside [0, num_pages) names no page (1 <= max_pages <
+ *               2^23, max_pages * page_size < 2^31);
  *   lens        int32 [slots]: committed tokens of each slot;
  *   refs        int32 [num_pages]: table entries that name the page; a page
  *               whose count is not positive is free.

@@ -95,10 +95,10 @@ def tree(lib, **kw):
 
 
 CACHE_REFUSALS = [(dict(pages=0), BAD, "num_pages"), (dict(pages=1 << 24), BAD, "num_pages"), (dict(slots=-1), BAD, "slots"),
-                  (dict(width=0), BAD, "max_pages")]
+                  (dict(width=0), BAD, "max_pages"), (dict(width=1 << 23), BAD, "max_pages")]
 PAGE_REFUSALS = [(dict(page=24), UNSUP, "page_size"), (dict(page=8), UNSUP, "page_size"), (dict(page=2048), UNSUP, "page_size"),
                  (dict(page=0), UNSUP, "page_size"), (dict(page=-16), UNSUP, "page_size"),
-                 (dict(width=(1 << 24) - 1, page=1024), UNSUP, "2^31")]
+                 (dict(width=(1 << 23) - 1, page=1024), UNSUP, "2^31")]
 
 
 @pytest.mark.parametrize("kw,status,word", HEAD_REFUSALS + CACHE_REFUSALS + PAGE_REFUSALS + [
