@@ -292,11 +292,10 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
 
 def _addr(t):
     """A tensor's device address as a plain number (None stays None), for
-    arguments that ctypes already takes as pointers."""
+    arguments that ctypes already takes as pointers.  _device has seen that it
+    is a device tensor."""
     if t is None:
         return None
-    if not t.is_cuda:
-        raise ValueError("libkda takes device tensors")
     if not t.is_contiguous():
         raise ValueError("libkda takes contiguous tensors")
     return t.data_ptr()
