@@ -705,12 +705,17 @@ int check_heads(int32_t H, int32_t Hkv, int32_t dk, int32_t dv, int32_t x_dtype,
     return KDA_OK;
 }
 
+// A launch holds fewer than 2^32 threads: workgroups of 256 stay below this.
+constexpr int64_t kMostGroups = int64_t(1) << 24;
+
+// per_tile: workgroups of a tile of 128 rows.
 int check_packed(int64_t T, int32_t N, const int32_t* cu, int64_t per_tile) {
     if (T < 0 || T >= (int64_t(1) << 31)) return fail(KDA_ERR_INVALID_ARGUMENT, "T_tot=%lld out of range [0, 2^31)", (long long)T);
     if (N < 1) return fail(KDA_ERR_INVALID_ARGUMENT, "N=%d must be >= 1", N);
     if (cu == nullptr && N != 1) return fail(KDA_ERR_INVALID_ARGUMENT, "cu_seqlens is NULL but N=%d", N);
-    if (kda::attn_tiles(T, N, 128) * per_tile >= (int64_t(1) << 31) || T * per_tile / 16 >= (int64_t(1) << 31))
-        return fail(KDA_ERR_UNSUPPORTED, "T_tot=%lld, N=%d, H=%lld: more than 2^31 workgroups", (long long)T, N, (long long)per_tile);
+    const int64_t groups = kda::attn_tiles(T, N, 128) * per_tile;
+    if (groups >= kMostGroups)
+        return fail(KDA_ERR_UNSUPPORTED, "T_tot=%lld, N=%d: %lld workgroups are not below 2^24", (long long)T, N, (long long)groups);
     return KDA_OK;
 }
 
@@ -740,6 +745,13 @@ int check_cache(int32_t num_pages, int32_t page_size, int32_t slots, int32_t max
     if (max_pages < 1 || max_pages >= (1 << 23)) return fail(KDA_ERR_INVALID_ARGUMENT, "max_pages=%d out of range [1, 2^23)", max_pages);
     if ((static_cast<int64_t>(max_pages) << shift) >= (int64_t(1) << 31))
         return fail(KDA_ERR_UNSUPPORTED, "max_pages=%d pages of %d tokens reach 2^31 tokens", max_pages, page_size);
+    return KDA_OK;
+}
+
+// A list of slots: a workgroup each.
+int check_entries(int32_t n) {
+    if (n < 0) return fail(KDA_ERR_INVALID_ARGUMENT, "n=%d is negative", n);
+    if (n >= kMostGroups) return fail(KDA_ERR_UNSUPPORTED, "n=%d entries: the workgroups are not below 2^24", n);
     return KDA_OK;
 }
 
@@ -821,6 +833,8 @@ int kda_attn_prefill_backward(int64_t T_tot, int32_t H, int32_t Hkv, int32_t dk,
     int st = check_heads(H, Hkv, dk, dv, x_dtype, scale);
     if (st == KDA_OK) st = check_packed(T_tot, N, cu_seqlens, 2 * static_cast<int64_t>(H));
     if (st != KDA_OK) return st;
+    if (T_tot * H >= 16 * kMostGroups)  // the kernel of the rows takes 16 a workgroup
+        return fail(KDA_ERR_UNSUPPORTED, "T_tot=%lld, H=%d: rows for more than 2^24 workgroups", (long long)T_tot, H);
     if ((out_gate != nullptr) != (grad_out_gate != nullptr) && T_tot > 0)
         return fail(KDA_ERR_INVALID_ARGUMENT, "grad_out_gate is required exactly when out_gate is given");
     const size_t xs = dsize(x_dtype), T = static_cast<size_t>(T_tot);
@@ -872,6 +886,9 @@ int kda_attn_tree(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t dk, int3
         return fail(KDA_ERR_INVALID_ARGUMENT, "slot_indices is NULL but slots=%d is not B=%d", slots, B);
     if (static_cast<int64_t>(B) * T * H >= (int64_t(1) << 30))
         return fail(KDA_ERR_UNSUPPORTED, "B x T x H = %lld rows are not below 2^30", static_cast<long long>(B) * T * H);
+    if (kda::attn_tree_groups(B, T, H, Hkv) >= kMostGroups)
+        return fail(KDA_ERR_UNSUPPORTED, "B=%d, T=%d, H=%d, Hkv=%d: %lld workgroups are not below 2^24", B, T, H, Hkv,
+                    static_cast<long long>(kda::attn_tree_groups(B, T, H, Hkv)));
     const size_t xs = dsize(x_dtype), BT = static_cast<size_t>(B) * T;
     const size_t page = static_cast<size_t>(num_pages) * Hkv * page_size;
     const bool any = BT > 0;
@@ -930,6 +947,8 @@ int kda_cache_append(int64_t T_tot, int32_t N, const int32_t* cu_seqlens, int64_
                      void* k_cache, void* v_cache, int32_t num_pages, int32_t page_size, const int32_t* page_table,
                      int32_t slots, int32_t max_pages, const int32_t* lens, const int32_t* slot_indices, void* stream) {
     if (T_tot < 0 || T_tot >= (int64_t(1) << 31)) return fail(KDA_ERR_INVALID_ARGUMENT, "T_tot=%lld out of range [0, 2^31)", (long long)T_tot);
+    if (T_tot >= 8 * kMostGroups)
+        return fail(KDA_ERR_UNSUPPORTED, "T_tot=%lld: 8 tokens each, the workgroups are not below 2^24", (long long)T_tot);
     if (N < 1) return fail(KDA_ERR_INVALID_ARGUMENT, "N=%d must be >= 1", N);
     if (cu_seqlens == nullptr && N != 1) return fail(KDA_ERR_INVALID_ARGUMENT, "cu_seqlens is NULL but N=%d", N);
     if (slot_indices == nullptr && slots < N)
@@ -971,7 +990,8 @@ int kda_cache_free(int32_t n, const int32_t* slot_list, int32_t num_pages, int32
     int shift = 0;
     int st = check_cache(num_pages, 16, slots, max_pages, shift);
     if (st != KDA_OK) return st;
-    if (n < 0) return fail(KDA_ERR_INVALID_ARGUMENT, "n=%d is negative", n);
+    st = check_entries(n);
+    if (st != KDA_OK) return st;
     if (n == 0) return ok();
     const SpanList sp = {
         {"slot_list", slot_list, static_cast<size_t>(n) * 4, false, 4}, {"page_table", page_table, table_bytes(slots, max_pages), true, 4},
@@ -994,7 +1014,8 @@ int kda_cache_fork(int32_t n, const int32_t* src, const int32_t* dst, int32_t Hk
     kda::CacheArgs c;
     int st = cache_args(Hkv, dk, dv, x_dtype, k_cache, v_cache, num_pages, page_size, page_table, slots, max_pages, lens, refs, sp, c);
     if (st != KDA_OK) return st;
-    if (n < 0) return fail(KDA_ERR_INVALID_ARGUMENT, "n=%d is negative", n);
+    st = check_entries(n);
+    if (st != KDA_OK) return st;
     if (n == 0) return ok();
     sp.push_back({"lens", lens, static_cast<size_t>(slots) * 4, true, 4});
     sp.push_back({"refs", refs, static_cast<size_t>(num_pages) * 4, true, 4});
@@ -1015,7 +1036,8 @@ int kda_cache_reserve(int32_t n, const int32_t* slot_list, const int32_t* new_le
     int shift = 0;
     int st = check_cache(num_pages, page_size, slots, max_pages, shift);
     if (st != KDA_OK) return st;
-    if (n < 0) return fail(KDA_ERR_INVALID_ARGUMENT, "n=%d is negative", n);
+    st = check_entries(n);
+    if (st != KDA_OK) return st;
     if (n == 0) return ok();
     SpanList sp = {
         {"slot_list", slot_list, static_cast<size_t>(n) * 4, false, 4}, {"new_lens", new_lens, static_cast<size_t>(n) * 4, false, 4},

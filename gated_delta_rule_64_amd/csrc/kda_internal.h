@@ -185,6 +185,12 @@ struct CacheArgs {
 // most one partly filled tile.
 constexpr int64_t attn_tiles(int64_t T, int N, int rows) { return T / rows + (T < N ? T : N); }
 
+// Workgroups of kda_attn_tree without a split (a split comes with few of them):
+// a sequence, key head and 32 rows each, the first two rounded up to 8.
+constexpr int64_t attn_tree_groups(int64_t B, int64_t T, int64_t H, int64_t Hkv) {
+    return (B * Hkv + 7) / 8 * 8 * ((T * (H / Hkv) + 31) / 32);
+}
+
 constexpr bool attn_head_sizes(int dk, int dv) {
     return (dk == dv && (dk == 16 || dk == 32 || dk == 64 || dk == 128)) || (dk == 192 && dv == 128);
 }

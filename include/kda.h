@@ -453,6 +453,8 @@ int kda_spec_verify(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv,
  *    rows up to 127 tokens from it (0 x infinity in a shared tile).
  *  - Rows of T_tot behind the last sequence are neither read nor written:
  *    cu_seqlens[N] may be below T_tot.
+ *  - Calls, or replays of captured graphs, that overlap in time need a
+ *    workspace each; in turn on one stream they can share one.
  *
  * kda_attn_prefill -- causal attention over a packed batch of whole prompts:
  * token i of a sequence attends its tokens 0 .. i,
@@ -462,7 +464,7 @@ int kda_spec_verify(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv,
  *   q [T_tot, H, dk]; k [T_tot, Hkv, dk]; v [T_tot, Hkv, dv];
  *   out [T_tot, H, dv];  lse NULL or fp32 [T_tot, H] (the gradients need it).
  * The call needs no workspace.  H x (T_tot/128 + min(N, T_tot)) must stay
- * below 2^31 (KDA_ERR_UNSUPPORTED otherwise).
+ * below 2^24 (KDA_ERR_UNSUPPORTED otherwise).
  */
 int kda_attn_prefill(int64_t T_tot, int32_t H, int32_t Hkv, int32_t dk, int32_t dv,
                      const int32_t* cu_seqlens, int32_t N, int32_t x_dtype, float scale,
@@ -484,6 +486,8 @@ int kda_attn_prefill(int64_t T_tot, int32_t H, int32_t Hkv, int32_t dk, int32_t 
  *   workspace     at least kda_attn_backward_workspace_bytes() bytes (of the
  *                 same sizes; with_gate: whether out_gate is given), 256-byte
  *                 aligned; contents on entry are ignored.
+ * H x (T_tot/128 + min(N, T_tot)) must stay below 2^23 and T_tot x H below
+ * 2^28 (KDA_ERR_UNSUPPORTED otherwise).
  */
 size_t kda_attn_backward_workspace_bytes(int64_t T_tot, int32_t N, int32_t H, int32_t Hkv,
                                          int32_t dk, int32_t dv, int32_t x_dtype, int32_t with_gate);
@@ -531,7 +535,9 @@ int kda_attn_prefill_backward(int64_t T_tot, int32_t H, int32_t Hkv, int32_t dk,
  *   workspace     at least kda_attn_tree_workspace_bytes() bytes for
  *                 max_context = max_pages * page_size, 256-byte aligned.
  * Tokens whose table entry names no page are not attended.  Lengths are
- * clamped to what a table row holds.  B x T x H must be below 2^30.
+ * clamped to what a table row holds.  B x T x H must be below 2^30, and
+ * B x Hkv x ceil(T x H/Hkv / 32) below 2^24 (B x Hkv rounded up to 8;
+ * KDA_ERR_UNSUPPORTED otherwise).
  */
 size_t kda_attn_tree_workspace_bytes(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t dk,
                                      int32_t dv, int32_t x_dtype, int64_t max_context);
@@ -561,7 +567,8 @@ int kda_attn_tree(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t dk, int3
  *                the sequences are not empty.
  * Dropped: tokens at or behind cu_seqlens[N], of slots outside [0, slots),
  * from rows outside [0, src_rows), and at positions whose table entry names no
- * page (kda_cache_reserve gives a slot its pages first).
+ * page (kda_cache_reserve gives a slot its pages first).  T_tot must be below
+ * 2^27 (KDA_ERR_UNSUPPORTED otherwise).
  */
 int kda_cache_append(int64_t T_tot, int32_t N, const int32_t* cu_seqlens,
                      int64_t src_rows, const int32_t* rows,
@@ -580,7 +587,8 @@ int kda_cache_append(int64_t T_tot, int32_t N, const int32_t* cu_seqlens,
  * depend on timing; the first entry that does not fit and every later one
  * that needs pages get status 1.  Workspace: at least
  * kda_cache_workspace_bytes(num_pages, slots, n) bytes (n = 0 for
- * kda_cache_compact), 256-byte aligned; contents on entry are ignored.
+ * kda_cache_compact), 256-byte aligned; contents on entry are ignored.  Lists
+ * of slots must be shorter than 2^24 (KDA_ERR_UNSUPPORTED otherwise).
  *
  * kda_cache_free -- empties the listed slots: their entries become -1, their
  * lengths 0, and the counts of their pages drop by one each.  Slots outside

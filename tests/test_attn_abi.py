@@ -204,3 +204,27 @@ def test_workspaces_hold_every_call(lib):
     w = lib.kda_cache_workspace_bytes
     assert w(10, 2, 3) >= 256 and w(0, 2, 3) == 0 and w(10, -1, 3) == 0 and w(10, 2, -1) == 0
     assert w(1000, 2, 0) >= 3 * 4000
+
+
+# A launch holds fewer than 2^32 threads, so 2^24 workgroups of 256 are too
+# many: each call just past its limit.  (Below the limit a call would launch.)
+TOO_MANY = 1 << 24
+
+
+@pytest.mark.parametrize("call,kw", [
+    (prefill, dict(T=1 << 28, H=8, Hkv=1, dk=16, dv=16)),  # 2^21 tiles and one more of 8 heads
+    (prefill, dict(T=TOO_MANY, N=TOO_MANY, H=1, Hkv=1, dk=16, dv=16, cu=FAKE + (1 << 37))),
+    (backward, dict(T=1 << 26, H=16, Hkv=1, dk=16, dv=16)),  # tiles of both kinds of gradients
+    (backward, dict(T=1 << 25, H=8, Hkv=1, dk=16, dv=16)),  # 2^28 rows, 16 a workgroup
+    (tree, dict(B=TOO_MANY - 8, slots=TOO_MANY - 8, T=33, H=1, Hkv=1, dk=16, dv=16)),
+    (tree, dict(B=TOO_MANY, slots=TOO_MANY, T=1, H=1, Hkv=1, dk=16, dv=16)),
+    (append, dict(T=1 << 27, R=1 << 27))])
+def test_launches_past_the_grid_are_refused(lib, call, kw):
+    assert call(lib, **kw) == UNSUP
+    assert "workgroups" in detail(lib)
+
+
+@pytest.mark.parametrize("which", ["free", "fork", "reserve"])
+def test_entry_lists_past_the_grid_are_refused(lib, which):
+    assert pages_call(lib, which, n=TOO_MANY) == UNSUP
+    assert "workgroups" in detail(lib)
