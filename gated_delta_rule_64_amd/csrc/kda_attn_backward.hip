@@ -9,8 +9,14 @@
 //
 // Three kernels: delta, dz and the gated do per row; then dk and dv per tile of
 // keys, looping over the queries, and dq per tile of queries, looping over the
-// keys; then the sum of dk's and dv's parts, where there are several.  The scores are formed in both, seven products for five, and in
-// exchange every sum is one workgroup's, in a fixed order: no atomics.
+// keys; then the sum of dk's and dv's parts, where there are several.  The
+// scores are formed in both, seven products for five, and in exchange every sum
+// is one workgroup's, in a fixed order: no atomics.
+//
+// 4,096 tokens of 32 heads of 128 over 8, bf16: 512 us in all, 671 TFLOP/s on
+// five products (940 on the seven), matrix cores 51 % of the cycles, waits 30 %.
+// Six ragged fp32 sequences of up to 500 tokens, 8 heads of 64 over 2: 73 us,
+// bound by the length of a workgroup's chain of fp32 products (matrix cores 30 %).
 #include "kda_attn_common.h"
 #include "kda_internal.h"
 #include "kda_profile.h"
@@ -39,7 +45,9 @@ struct BwdK {
     float* q_part;    // [q_parts][T, H][dk]
 };
 
-// One row (token, head) per 16 lanes.
+// One row (token, head) per 16 lanes, so that a load takes whole lines of
+// neighbouring rows.  Bound by memory: 131,072 rows of 128, 68 MB, in 15 us
+// (4.5 TB/s).
 template <typename T, int DV>
 __global__ __launch_bounds__(kThreads) void attn_bwd_rows_kernel(BwdK a) {
     const int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreads / 16) + (threadIdx.x >> 4);
@@ -109,7 +117,8 @@ struct DqSizes {
 };
 
 // Query gradients: one workgroup per (tile of 128 queries, head, part of the
-// keys).
+// keys); a wave's queries, output gradients and sums stay in its registers, the
+// keys and values pass through LDS once for four waves.
 template <typename T, int DK, int DV>
 __device__ __forceinline__ void query_gradients(const BwdK& a, unsigned block, char* smem) {
     using Sz = DqSizes<T, DK, DV>;
@@ -417,7 +426,9 @@ __global__ __launch_bounds__(kThreads, (DK * sizeof(T) < 256 || (sizeof(T) == 2 
 }
 
 // Adds the parts in their order, four channels per thread: first the rows of
-// the key heads (dk and dv together), then those of the query heads.
+// the key heads (dk and dv together), then those of the query heads.  Bound by
+// memory: four parts of 4,096 tokens of 8 heads, 151 MB, in 23 us (6.6 TB/s,
+// a part of it from the caches).
 template <typename T, int DK, int DV>
 __global__ __launch_bounds__(kThreads) void attn_bwd_sum_kernel(BwdK a) {
     constexpr int kKv = (DK + DV) / 4, kQ = DK / 4;

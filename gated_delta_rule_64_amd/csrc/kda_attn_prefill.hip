@@ -8,6 +8,15 @@
 // formed transposed, S^T = K Q^T, so that a lane holds one query's scores (its
 // softmax statistics need one exchange between the wave's halves, no shuffle
 // tree) and P^T is the B operand of O^T += V^T P^T as it stands in registers.
+//
+// 128 rows of one head a workgroup, 32 a wave: the queries and sums of a wave
+// fill its registers so that two workgroups share a CU, and a key tile read
+// into LDS once serves four waves.  16,384 tokens of 32 heads of 128 over 8, in
+// bf16: 2,173 us, 1,010 TFLOP/s (a large bf16 product of the library reaches
+// 1,390); the matrix cores work in 53 % of the cycles, the vector units' softmax
+// in 47 %.  Twelve ragged sequences of up to 2,048 tokens at 192/128 channels,
+// gated: 341 us, 650 TFLOP/s, matrix cores 36 %, waits 28 %: their workgroups
+// live for about ten tiles, and the first tile and the gate are not hidden.
 #include "kda_attn_common.h"
 #include "kda_internal.h"
 #include "kda_profile.h"

@@ -6,6 +6,10 @@
 // the lowest-numbered ones, found by a scan over refs, so that the result
 // does not depend on the order in which workgroups run, and freeing is one
 // atomic subtraction per entry, in any order.
+//
+// What bounds them: the copies memory, the planning workgroups the length of
+// their chains of dependent loads and scans.  Measured with pages of 8 heads of
+// 128 in bf16; the sizes stand at each kernel.
 #include "kda_common.h"
 #include "kda_internal.h"
 #include "kda_profile.h"
@@ -134,6 +138,9 @@ struct AppendK {
     const void *k_new, *v_new;
 };
 
+// Eight tokens find their rows, then the workgroup copies them in pieces of 16
+// bytes, a token's heads side by side.  33,256 prompt tokens, 273 MB moved: 50 us (5.4
+// TB/s); four pieces in flight per thread were slower (62 to 69 us a call).
 constexpr int kAppendTokens = 8;  // tokens of a workgroup
 
 __global__ __launch_bounds__(kCopy) void cache_append_kernel(AppendK a) {
@@ -193,6 +200,7 @@ __global__ __launch_bounds__(kCopy) void cache_append_kernel(AppendK a) {
 
 // --------------------------------------------------------------------- free
 
+// A thread per table entry: 256 slots in 3 us, a launch's latency.
 __global__ __launch_bounds__(kCopy) void cache_free_kernel(CacheArgs c, const int32_t* slot_list) {
     const int slot = slot_list[blockIdx.x];
     if (slot < 0 || slot >= c.slots) return;
@@ -219,6 +227,8 @@ struct ForkK {
     int32_t* plan;   // [n][2]: source length (-1: refused), the new last page (-1: none needed)
 };
 
+// One workgroup: every entry is checked, the destinations claimed, then one scan
+// over refs finds the pages.  256 forks: 10 us.
 __global__ __launch_bounds__(kPlan) void cache_fork_plan_kernel(ForkK a) {
     __shared__ int sums[kPlan / 64];
     __shared__ int claims[kLdsSlots];
@@ -288,7 +298,7 @@ __global__ __launch_bounds__(kPlan) void cache_fork_plan_kernel(ForkK a) {
 }
 
 // Workgroup (i, 0) writes entry i's table row, (i, 1 + y) copies its share of
-// the rows of the last page.
+// the rows of the last page: 256 forks, 58 MB moved, in 14.5 us (4.0 TB/s).
 __global__ __launch_bounds__(kCopy) void cache_fork_apply_kernel(ForkK a) {
     const CacheArgs& c = a.c;
     const int i = blockIdx.x;
@@ -340,7 +350,7 @@ struct ReserveK {
 // One workgroup.  Every entry's columns that lack a page are counted, a scan
 // gives every entry its place, and the lowest free pages go out in that order.
 // An entry of few columns (a decode step's) is one thread's, so that the
-// entries' dependent loads overlap (256 entries: 49 us with a wave each); one
+// entries' dependent loads overlap (256 entries: 17 us, 49 with a wave each); one
 // of many columns (a prompt's) a wave's.
 constexpr int kFewColumns = 16;
 
@@ -475,6 +485,7 @@ struct CompactK {
     int32_t *from_list, *to_list;  // [pages]
 };
 
+// One workgroup, two scans over refs.  8,192 pages: 16 us.
 __global__ __launch_bounds__(kPlan) void cache_compact_plan_kernel(CompactK a) {
     __shared__ int sums[kPlan / 64];
     __shared__ int64_t sums64[kPlan / 64];
@@ -546,7 +557,9 @@ __device__ __forceinline__ void copy_pieces(const uint4* src, uint4* dst, int64_
 
 constexpr int64_t kSegment = 1024;  // 16-byte pieces that a workgroup copies at a time
 
-// The first table_blocks workgroups rewrite the table, the others move pages.
+// The first table_blocks workgroups rewrite the table, the others move pages, a
+// segment of 16 KiB at a time so that few pages still fill the chip: 969 MB in
+// 203 us (4.8 TB/s of the 5.1 that a large copy reaches).
 __global__ __launch_bounds__(kCopy) void cache_compact_move_kernel(CompactK a, int table_blocks) {
     const CacheArgs& c = a.c;
     if (static_cast<int>(blockIdx.x) < table_blocks) {
