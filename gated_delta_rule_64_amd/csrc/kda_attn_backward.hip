@@ -13,10 +13,10 @@
 // scores are formed in both, seven products for five, and in exchange every sum
 // is one workgroup's, in a fixed order: no atomics.
 //
-// 4,096 tokens of 32 heads of 128 over 8, bf16: 512 us in all, 671 TFLOP/s on
-// five products (940 on the seven), matrix cores 51 % of the cycles, waits 30 %.
-// Six ragged fp32 sequences of up to 500 tokens, 8 heads of 64 over 2: 73 us,
-// bound by the length of a workgroup's chain of fp32 products (matrix cores 30 %).
+// 4,096 tokens of 32 heads of 128 over 8, bf16: 490 to 512 us in all, 670 to 700
+// TFLOP/s on five products (940 to 980 on the seven), matrix cores 51 % of the
+// cycles, waits 30 %.  Six ragged fp32 sequences of up to 500 tokens, 8 heads of
+// 64 over 2: 70 us, bound by the length of a workgroup's chain of fp32 products.
 #include "kda_attn_common.h"
 #include "kda_internal.h"
 #include "kda_profile.h"
@@ -111,7 +111,9 @@ __device__ __forceinline__ void store_rows(T* row, const f32x16 (&acc)[kTiles], 
 
 template <typename T, int DK, int DV>
 struct DqSizes {
-    static constexpr int kKeys = sizeof(T) == 4 && DK > 64 ? 32 : 64;
+    // 64 keys a tile where two workgroups' registers allow it (fp32 at 64
+    // channels: 256 and 2 spilled, with 32 keys 218)
+    static constexpr int kKeys = sizeof(T) == 4 && DK >= 64 ? 32 : 64;
     static constexpr int kBuf = kKeys * (DK + DV) * static_cast<int>(sizeof(T));
     static constexpr int kLds = 2 * kBuf + tr_slack(DV);
 };
@@ -240,8 +242,11 @@ struct DkvSizes {
     static constexpr int kBuf = kQ * (DK + DV) * static_cast<int>(sizeof(T)) + kStats;
     // Where a lane's sums, keys and values together exceed half its registers,
     // the values are read from LDS for every step: two workgroups then share a
-    // CU, and one's products cover the other's exponentials and LDS reads.
-    static constexpr bool kValuesInLds = sizeof(T) == 2 && DK == 128;
+    // CU, and one's products cover the other's exponentials and LDS reads.  In
+    // fp32 they would else come from the caches: ragged sequences of up to 1,000
+    // tokens take 301 us so at 64 channels (304 from the caches) and 676 at 128
+    // (697); at 16 channels the caches are faster (47 against 51 us).
+    static constexpr bool kValuesInLds = DK == 128 || (sizeof(T) == 4 && DK == 64);
     static constexpr int kValues = kValuesInLds ? kRows * DV * static_cast<int>(sizeof(T)) : 0;
     static constexpr int kLds = 2 * kBuf + tr_slack(DV) + kValues;
 };
@@ -275,9 +280,10 @@ __device__ __forceinline__ void key_gradients(const BwdK& a, unsigned block, cha
 
     const int q_row = a.H * DK * static_cast<int>(sizeof(T)), o_row = a.H * DV * static_cast<int>(sizeof(T));
     const int k_row = a.Hkv * DK * static_cast<int>(sizeof(T)), v_row = a.Hkv * DV * static_cast<int>(sizeof(T));
-    // bf16: this wave's keys and values stay in registers.  fp32: they would
-    // not fit beside the sums, and each step, whose products take four times
-    // as many cycles per byte, reads them again from the caches.
+    // bf16: this wave's keys, and its values where they fit, stay in registers.
+    // fp32: they would not fit beside the sums, and each step, whose products
+    // take four times as many cycles per byte, reads them again, the keys from
+    // the caches.
     constexpr bool kKeep = sizeof(T) == 2;
     const auto ks = rows_of(static_cast<const T*>(a.k) + kvh * DK, t.start + k0, k_row, rows);
     const auto vs = rows_of(static_cast<const T*>(a.v) + kvh * DV, t.start + k0, v_row, rows);
@@ -417,9 +423,11 @@ __device__ __forceinline__ void key_gradients(const BwdK& a, unsigned block, cha
 // Both in one launch, the key gradients' workgroups first: they are the longer
 // ones, and the query gradients' fill the chip behind them (one after the
 // other, each launch ends with most of the chip idle: the small fp32 batch
-// takes 55 + 59 us so).
+// takes 55 + 59 us so).  Rows of up to 256 bytes leave registers for two
+// workgroups a CU (fp32 at 64 channels: 4,000 tokens 1,900 us, 2,180 with one;
+// the ragged batch of up to 1,000 tokens 301 us, 355 with one).
 template <typename T, int DK, int DV>
-__global__ __launch_bounds__(kThreads, (DK * sizeof(T) < 256 || (sizeof(T) == 2 && DK == 128) ? 2 : 1)) void attn_bwd_kernel(BwdK a, unsigned key_groups) {
+__global__ __launch_bounds__(kThreads, (DK * sizeof(T) <= 256 ? 2 : 1)) void attn_bwd_kernel(BwdK a, unsigned key_groups) {
     extern __shared__ __align__(16) char smem[];
     if (blockIdx.x < key_groups) key_gradients<T, DK, DV>(a, blockIdx.x, smem);
     else query_gradients<T, DK, DV>(a, blockIdx.x - key_groups, smem);

@@ -12,11 +12,12 @@
 // 128 rows of one head a workgroup, 32 a wave: the queries and sums of a wave
 // fill its registers so that two workgroups share a CU, and a key tile read
 // into LDS once serves four waves.  16,384 tokens of 32 heads of 128 over 8, in
-// bf16: 2,173 us, 1,010 TFLOP/s (a large bf16 product of the library reaches
-// 1,390); the matrix cores work in 53 % of the cycles, the vector units' softmax
-// in 47 %.  Twelve ragged sequences of up to 2,048 tokens at 192/128 channels,
-// gated: 341 us, 650 TFLOP/s, matrix cores 36 %, waits 28 %: their workgroups
-// live for about ten tiles, and the first tile and the gate are not hidden.
+// bf16: 2,090 to 2,170 us, 1,010 to 1,050 TFLOP/s (a large bf16 product of the
+// library reaches 1,390); the matrix cores work in 53 % of the cycles, the vector
+// units' softmax in 47 %.  Twelve ragged sequences of up to 2,048 tokens at
+// 192/128 channels, gated: 326 to 341 us, 650 to 680 TFLOP/s, matrix cores 36 %,
+// waits 28 %: such a batch also moves 0.69 GB (125 us), of which the queries, the
+// gate and the results are not under the products (without a gate: 22 us less).
 #include "kda_attn_common.h"
 #include "kda_internal.h"
 #include "kda_profile.h"
