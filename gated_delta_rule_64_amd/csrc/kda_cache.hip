@@ -29,6 +29,15 @@ __device__ __forceinline__ void store_fresh(int32_t* p, int32_t v) {
     __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
+// A barrier of the planning workgroup behind stores that its other threads
+// read: every wave waits until the L2 has its stores, where load_fresh finds
+// them.  (A device-wide fence would write the L2 back as well, for other dies
+// that do not read here: kda_cache_reserve's kernel for 256 slots 17 us, so 8.)
+__device__ __forceinline__ void stored_barrier() {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+}
+
 // Exclusive scan of one value per thread of the planning workgroup; `total`
 // gets the sum.  sums: kPlan / 64 words of LDS.  All threads call it.
 template <typename I>
@@ -94,8 +103,7 @@ __device__ __forceinline__ int lowest_free(const int32_t* refs, int pages, PageC
             }
         found += total;
     }
-    __threadfence();
-    __syncthreads();
+    stored_barrier();
     return min(found, want);
 }
 
@@ -113,17 +121,15 @@ struct Claims {
         } else {
             for (int i = threadIdx.x; i < n; i += kPlan)
                 if (slot_of[i] >= 0 && slot_of[i] < slots) store_fresh(memory + slot_of[i], INT32_MAX);
-            __threadfence();
         }
-        __syncthreads();
+        stored_barrier();
     }
     __device__ __forceinline__ void claim(int slot, int i) const {
         if (in_lds) atomicMin(lds + slot, i);
         else atomicMin(memory + slot, i);
     }
     __device__ __forceinline__ void settle() const {
-        if (!in_lds) __threadfence();
-        __syncthreads();
+        stored_barrier();
     }
     __device__ __forceinline__ int owner(int slot) const { return in_lds ? lds[slot] : load_fresh(memory + slot); }
 };
@@ -228,7 +234,7 @@ struct ForkK {
 };
 
 // One workgroup: every entry is checked, the destinations claimed, then one scan
-// over refs finds the pages.  256 forks: 10 us.
+// over refs finds the pages.  256 forks: 8 us.
 __global__ __launch_bounds__(kPlan) void cache_fork_plan_kernel(ForkK a) {
     __shared__ int sums[kPlan / 64];
     __shared__ int claims[kLdsSlots];
@@ -350,7 +356,7 @@ struct ReserveK {
 // One workgroup.  Every entry's columns that lack a page are counted, a scan
 // gives every entry its place, and the lowest free pages go out in that order.
 // An entry of few columns (a decode step's) is one thread's, so that the
-// entries' dependent loads overlap (256 entries: 17 us, 49 with a wave each); one
+// entries' dependent loads overlap (256 entries: 8 us, several times that with a wave each); one
 // of many columns (a prompt's) a wave's.
 constexpr int kFewColumns = 16;
 
@@ -403,8 +409,7 @@ __global__ __launch_bounds__(kPlan) void cache_reserve_kernel(ReserveK a) {
         }
         store_fresh(a.counts + i, count);
     }
-    __threadfence();
-    __syncthreads();
+    stored_barrier();
     for (int i = wave; many != 0 && i < a.n; i += kPlan / 64) {
         const Entry e = entry(i);
         if (e.end - e.first <= kFewColumns || !owned(i, e)) continue;
@@ -416,8 +421,7 @@ __global__ __launch_bounds__(kPlan) void cache_reserve_kernel(ReserveK a) {
         }
         if (lane == 0) store_fresh(a.counts + i, count);
     }
-    __threadfence();
-    __syncthreads();
+    stored_barrier();
     int64_t want = 0;
     for (int i0 = 0; i0 < a.n; i0 += kPlan) {
         const int i = i0 + threadIdx.x;
@@ -454,8 +458,7 @@ __global__ __launch_bounds__(kPlan) void cache_reserve_kernel(ReserveK a) {
         }
     }
     if (many == 0) return;
-    __threadfence();
-    __syncthreads();
+    stored_barrier();
     for (int i = wave; i < a.n; i += kPlan / 64) {
         int at = load_fresh(a.counts + i);
         if (at < 0) continue;
@@ -485,7 +488,7 @@ struct CompactK {
     int32_t *from_list, *to_list;  // [pages]
 };
 
-// One workgroup, two scans over refs.  8,192 pages: 16 us.
+// One workgroup, two scans over refs.  8,192 pages: 12 us.
 __global__ __launch_bounds__(kPlan) void cache_compact_plan_kernel(CompactK a) {
     __shared__ int sums[kPlan / 64];
     __shared__ int64_t sums64[kPlan / 64];
@@ -527,8 +530,7 @@ __global__ __launch_bounds__(kPlan) void cache_compact_plan_kernel(CompactK a) {
             if (mover[i]) store_fresh(a.from_list + am++, first + i);
         }
     }
-    __threadfence();
-    __syncthreads();
+    stored_barrier();
     for (int k = threadIdx.x; k < movers; k += kPlan) {
         const int s = load_fresh(a.from_list + k), d = load_fresh(a.to_list + k);
         store_fresh(a.to + s, d);
@@ -559,7 +561,7 @@ constexpr int64_t kSegment = 1024;  // 16-byte pieces that a workgroup copies at
 
 // The first table_blocks workgroups rewrite the table, the others move pages, a
 // segment of 16 KiB at a time so that few pages still fill the chip: 969 MB in
-// 203 us (4.8 TB/s of the 5.1 that a large copy reaches).
+// 175 to 203 us (4.8 to 5.5 TB/s; a large copy reaches 5.1 on the slower card).
 __global__ __launch_bounds__(kCopy) void cache_compact_move_kernel(CompactK a, int table_blocks) {
     const CacheArgs& c = a.c;
     if (static_cast<int>(blockIdx.x) < table_blocks) {
