@@ -356,7 +356,7 @@ struct ReserveK {
 // One workgroup.  Every entry's columns that lack a page are counted, a scan
 // gives every entry its place, and the lowest free pages go out in that order.
 // An entry of few columns (a decode step's) is one thread's, so that the
-// entries' dependent loads overlap (256 entries: 8 us, several times that with a wave each); one
+// entries' dependent loads overlap (256 entries with a wave each: 49 us where threads took 20); one
 // of many columns (a prompt's) a wave's.
 constexpr int kFewColumns = 16;
 
@@ -561,7 +561,7 @@ constexpr int64_t kSegment = 1024;  // 16-byte pieces that a workgroup copies at
 
 // The first table_blocks workgroups rewrite the table, the others move pages, a
 // segment of 16 KiB at a time so that few pages still fill the chip: 969 MB in
-// 175 to 203 us (4.8 to 5.5 TB/s; a large copy reaches 5.1 on the slower card).
+// 175 to 203 us (4.8 to 5.5 TB/s; a large copy measured 5.1).
 __global__ __launch_bounds__(kCopy) void cache_compact_move_kernel(CompactK a, int table_blocks) {
     const CacheArgs& c = a.c;
     if (static_cast<int>(blockIdx.x) < table_blocks) {

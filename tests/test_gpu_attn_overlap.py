@@ -6,8 +6,8 @@ import random
 import pytest
 import torch
 
-from test_gpu_attn_prefill import _cu, _inputs
-from test_gpu_attn_tree import _make
+from test_gpu_attn_prefill import _check_backward, _check_forward, _cu, _inputs
+from test_gpu_attn_tree import _check, _make
 from test_gpu_cache import Device, Model, _ints
 
 pytestmark = pytest.mark.gpu
@@ -117,3 +117,31 @@ def test_slots_of_a_large_cache(K, slots):
     m.free(gone)
     d.same(m)
     assert not m.refs.any()
+
+
+@pytest.mark.parametrize("T", [32, 33, 63, 64])
+def test_chains_of_many_tokens(K, T):
+    """The last bits of a mask word, as a chain and as words of all ones up to
+    the token (bit 63 makes a word negative)."""
+    x = _make(21, [50, 0], T, 4, 2, 64, 64, 32, torch.float32, mask="chain")
+    a = _check(K, x, torch.float32)
+    words = [(1 << (t + 1)) - 1 for t in range(T)]
+    x["mask"] = torch.tensor([w - (1 << 64) if w >> 63 else w for w in words], dtype=torch.int64, device="cuda").repeat(2, 1)
+    b = _check(K, x, torch.float32)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128)])
+@pytest.mark.parametrize("lens", [[0, 129, 0, 1], [0, 0, 0], [500, 3, 0]])
+def test_empty_sequences_and_a_gate(K, lens, dk, dv, dtype):
+    """Sequences of no tokens between others, and a batch of nothing but rows
+    behind the last sequence."""
+    t = {"f32": torch.float32, "bf16": torch.bfloat16}[dtype]
+    x = _inputs(31, lens, 4, 1, dk, dv, t, True, spare=130)
+    out, lse = _check_forward(K, x, lens, t)
+    if sum(lens):
+        _check_backward(K, x, lens, t, out, lse)
+    else:
+        K.kda_attn_prefill_backward(x["q"], x["k"], x["v"], out, lse, x["dy"], out_gate=x["z"], cu_seqlens=_cu(lens))
+        torch.cuda.synchronize()
