@@ -423,7 +423,7 @@ __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV>::kWaves), (sizeof(T) == 
 // Joins the parts, kWaves waves to a row: thread s of the row weighs part s,
 // then the row's half waves take the parts in turn, four channels a lane, and
 // their sums are added in LDS.  Many rows of few parts take a wave each (16,384
-// rows of 4 parts: 16 us, with four waves each 33 us); few rows of many parts
+// rows of 4 parts: 15.5 us, with four waves each 33 us); few rows of many parts
 // four (128 rows of 128 parts: 9 us, with one wave each 59 us).
 constexpr int kJoinThreads = 256;
 constexpr int kFewParts = 16;
@@ -436,10 +436,11 @@ __global__ __launch_bounds__(kJoinThreads) void attn_tree_join_kernel(TreeK a) {
     __shared__ f32x4 added[8][32];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, ch = (lane & 31) * 4;
     const int mine = wave / kWaves, tid = threadIdx.x % kThreads, turn = tid >> 5, first = mine * kWaves;
-    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kRows + mine, total = static_cast<int64_t>(a.B) * a.T * a.H;
+    // a wave's row: below 2^30, so that its divisions are scalar and short
+    const int r0 = uniform(static_cast<int>(blockIdx.x) * kRows + mine), total = a.B * a.T * a.H;
     const int64_t r = r0 < total ? r0 : total - 1;
     const int G = a.H / a.Hkv, rows = a.T * G;
-    const int h = static_cast<int>(r % a.H), t = static_cast<int>(r / a.H % a.T), b = static_cast<int>(r / a.H / a.T);
+    const int token = static_cast<int>(r) / a.H, h = static_cast<int>(r) - token * a.H, b = token / a.T, t = token - b * a.T;
     const int64_t at = (static_cast<int64_t>(b) * a.Hkv + h / G) * rows + t * G + h % G;
     const int64_t step = static_cast<int64_t>(a.B) * a.Hkv * rows;
     int slot, ctx;
