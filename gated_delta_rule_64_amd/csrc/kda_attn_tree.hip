@@ -390,7 +390,7 @@ __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV>::kWaves), (sizeof(T) == 
             a.stats[2 * at] = m;
             a.stats[2 * at + 1] = l;
         }
-        if (l > 0.f) {
+        if (l != 0.f) {  // (NaN too)
 #pragma unroll
             for (int i = 0; i < kVTiles; ++i)
 #pragma unroll
@@ -458,8 +458,12 @@ __global__ __launch_bounds__(kJoinThreads) void attn_tree_join_kernel(TreeK a) {
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) top = fmaxf(top, tops[first + w]);
-    const float f = l > 0.f ? __builtin_amdgcn_exp2f((m - top) * sc) : 0.f;  // no part was written where l is 0
-    weight[threadIdx.x] = f;
+    // No part was written where l is 0: its weight is below 0.  Every other part
+    // is added, also with a weight of 0, so that a value that is not finite
+    // reaches the row as it does in one piece, and an l of NaN makes it NaN.
+    const bool there = l != 0.f;
+    const float f = there ? __builtin_amdgcn_exp2f((m - top) * sc) : 0.f;
+    weight[threadIdx.x] = there ? f : -1.f;
     l = wave_sum(l * f);
     if (lane == 0) sums[wave] = l;
     __syncthreads();
@@ -475,8 +479,8 @@ __global__ __launch_bounds__(kJoinThreads) void attn_tree_join_kernel(TreeK a) {
 #pragma unroll
             for (int i = 0; i < kEach; ++i) {
                 const int s = s0 + kTurns * i;
-                w[i] = s < a.splits ? weight[mine * kThreads + s] : 0.f;
-                o[i] = w[i] > 0.f ? *reinterpret_cast<const f32x4*>(a.part + (at + s * step) * DV + ch) : f32x4{};
+                w[i] = s < a.splits ? weight[mine * kThreads + s] : -1.f;
+                o[i] = !(w[i] < 0.f) ? *reinterpret_cast<const f32x4*>(a.part + (at + s * step) * DV + ch) : f32x4{};
             }
 #pragma unroll
             for (int i = 0; i < kEach; ++i)
@@ -493,11 +497,11 @@ __global__ __launch_bounds__(kJoinThreads) void attn_tree_join_kernel(TreeK a) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[e] += o[e];
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l != 0.f ? 1.f / l : 0.f;
     float out[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) out[e] = y[e] * inv;
-    if (a.lse != nullptr && lane == 0) a.lse[r] = l > 0.f ? (top * sc + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+    if (a.lse != nullptr && lane == 0) a.lse[r] = l != 0.f ? (top * sc + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
     if (ch < DV)
         store4<T>(static_cast<T*>(a.out) + r * DV + ch,
                   a.z != nullptr && real ? static_cast<const T*>(a.z) + r * DV + ch : nullptr, out);
