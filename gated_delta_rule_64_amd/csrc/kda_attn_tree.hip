@@ -403,8 +403,8 @@ __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV>::kWaves), (sizeof(T) == 
         }
         return;
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    if (a.lse != nullptr && half == 0) a.lse[q_at] = l > 0.f ? (m * sc + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    if (a.lse != nullptr && half == 0) a.lse[q_at] = l != 0.f ? (m * sc + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
     T* out = static_cast<T*>(a.out) + q_at * DV;
     const T* z = a.z != nullptr && real ? static_cast<const T*>(a.z) + q_at * DV : nullptr;
 #pragma unroll

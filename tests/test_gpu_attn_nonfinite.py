@@ -13,8 +13,8 @@ from test_gpu_attn_tree import TYPES, _call, _make
 pytestmark = pytest.mark.gpu
 
 # the parts that the keys are cut into for the sequences below, and the pages
-# of a table row: few parts (joined by a wave a row), many (by four)
-WIDTHS = {8: 128, 40: 640}
+# of a table row: one, few parts (joined by a wave a row), many (by four)
+WIDTHS = {1: 27, 8: 128, 40: 640}
 
 
 @pytest.fixture(scope="module")
@@ -75,7 +75,7 @@ def _tree(K, parts, dtype, dk=64, dv=64, lens=(300, 40), T=5):
     x = _make(31, list(lens), T, 4, 2, dk, dv, 16, TYPES[dtype], gate=True, width=WIDTHS[parts])
     need = K.kda_attn_tree_workspace_bytes(len(lens), T, 4, 2, dk, dv, TYPES[dtype], WIDTHS[parts] * 16)
     each = len(lens) * T * 4 * (dv * 4 + 8)
-    assert parts * each <= need < (parts + 1) * each, "not cut as the test means it"
+    assert (need == 0) if parts == 1 else parts * each <= need < (parts + 1) * each, "not cut as the test means it"
     return x
 
 
@@ -137,3 +137,43 @@ def test_other_head_sizes(K, parts):
             _committed(x, 1, 17, 1, k={dk - 1: math.nan})
             x["k_new"][0, 1, 1, 4] = math.inf
             _check_tree(K, x, TYPES[dtype])
+
+
+def _prefill(K, q, k, v, z, dtype):
+    """One sequence, every head's rows checked."""
+    out, lse = K.kda_attn_prefill(q, k, v, out_gate=z)
+    torch.cuda.synchronize()
+    n, H, dk = q.shape
+    seen, G = R.causal(n, "cuda"), H // k.shape[1]
+    for h in range(H):
+        _rows(q[:, h].double(), k[:, h // G].double(), v[:, h // G].double(), dk ** -0.5, seen, dtype)(
+            f"head {h}", out[:, h], lse[:, h], None if z is None else z[:, h])
+    return out, lse
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dk,dv", [(16, 16), (64, 64), (128, 128), (192, 128)])
+@pytest.mark.parametrize("which", ["query", "key"])
+def test_prefill(K, which, dk, dv, dtype):
+    t = TYPES[dtype]
+    g = torch.Generator(device="cuda")
+    g.manual_seed(dk)
+    new = lambda *s: torch.randn(s, generator=g, device="cuda").to(t)  # noqa: E731
+    q, k, v, z = new(150, 4, dk), new(150, 2, dk), new(150, 2, dv), new(150, 4, dv)
+    print(f"prefill {which} {dk}/{dv} {dtype}", flush=True)
+    if which == "query":
+        q[5, 0, 3], q[70, 1, 0], q[149, 3, dk - 1] = math.nan, math.inf, -math.inf
+    else:
+        k[40, 0, 2], k[100, 1, 1] = math.nan, math.inf
+    out, lse = _prefill(K, q, k, v, z, t)
+    # the gradients of a broken row are NaN, and reach what the row attends
+    dy = new(150, 4, dv)
+    grads = K.kda_attn_prefill_backward(q, k, v, out, lse, dy, out_gate=z)
+    torch.cuda.synchronize()
+    broken = torch.isnan(lse)
+    assert bool(broken.any()) and bool(torch.isnan(grads["dq"][broken]).all())
+    for h in range(4):
+        if bool(broken[:, h].any()):
+            last = int(torch.nonzero(broken[:, h])[-1, 0])
+            for name in ("dk", "dv"):
+                assert bool(torch.isnan(grads[name][:last + 1, h // 2]).all()), name
