@@ -187,9 +187,11 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void attn_fwd_k
             z[n] = buffer_load16(src, (lane + 64 * n) / kRowPieces * (a.H * DV * static_cast<int>(sizeof(T))) + (lane + 64 * n) % kRowPieces * 16);
     }
     l = xor32_add(l);
-    const float inv = l != 0.f ? 1.f / l : 0.f;  // a sum of NaN makes the row and its lse NaN
+    // A row attends itself at least.  A sum of NaN, or of 0 (every score is
+    // -infinity), makes it and its lse NaN.
+    const float inv = l > 0.f ? 1.f / l : NAN;
     if (a.lse != nullptr && half == 0 && row < t.len)
-        a.lse[first + static_cast<int64_t>(c) * a.H] = l != 0.f ? (m * sc + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+        a.lse[first + static_cast<int64_t>(c) * a.H] = l > 0.f ? (m * sc + __builtin_amdgcn_logf(l)) * kLn2 : NAN;
 #pragma unroll
     for (int i = 0; i < kVTiles; ++i) acc[i] *= inv;
     tile_barrier();  // every wave is done with the tiles

@@ -18,6 +18,8 @@
 // 6.3 that a streaming read reaches); trees of 16 over 32 ragged sequences take
 // 136 us with their join, 1.07 times the traffic; a chain of 4 over 262,144
 // tokens 191 us (5.6 TB/s).
+#include <cfloat>
+
 #include "kda_attn_common.h"
 #include "kda_internal.h"
 #include "kda_profile.h"
@@ -66,6 +68,19 @@ __device__ __forceinline__ bool slot_of(const TreeK& a, int b, int& slot, int& c
     const int n = a.lens[slot];
     ctx = n < 0 ? 0 : static_cast<int>(n > most ? most : n);
     return true;
+}
+
+// What a row's sums are multiplied by, and its lse.  l is 0 where nothing is
+// attended (m is -infinity), and where every attended score is -infinity (m is
+// kLowest): that row is NaN, as is one whose l is NaN.
+constexpr float kLowest = -FLT_MAX;
+struct Norm {
+    float inv, lse;
+};
+__device__ __forceinline__ bool attends(float m, float l) { return l != 0.f || m != -INFINITY; }
+__device__ __forceinline__ Norm normalise(float m, float l, float sc) {
+    if (l > 0.f) return Norm{1.f / l, (m * sc + __builtin_amdgcn_logf(l)) * kLn2};
+    return attends(m, l) ? Norm{NAN, NAN} : Norm{0.f, -INFINITY};
 }
 
 // Final rows: y = o / l, gated, and the log of the sum.
@@ -137,6 +152,7 @@ __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV>::kWaves), (sizeof(T) == 
     const int64_t q_at = (static_cast<int64_t>(b) * a.T + token) * a.H + kvh * G + (mine ? row : 0) % G;  // the row in [B, T, H]
     f32x16 acc[kVTiles];
     float m = -INFINITY, l = 0.f;
+    uint32_t any = 0;  // other than 0: the row attends some token of this wave's
 #pragma unroll
     for (int i = 0; i < kVTiles; ++i) acc[i] = f32x16{};
 
@@ -275,6 +291,7 @@ __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV>::kWaves), (sizeof(T) == 
                     put_half(x);
                 }
                 const int n0 = now.rows[0], n1 = now.rows[1];
+                any |= n0 | n1;
                 if (tile + kWaves < c_end) {
                     now = next;
                     if constexpr (kAhead) {
@@ -321,6 +338,7 @@ __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV>::kWaves), (sizeof(T) == 
                 put_half(x);
             }
             const uint32_t bits = static_cast<uint32_t>(seen >> t0);
+            any |= bits & ~0u >> max(0, kKeys - (a.T - t0));
             work([&](f32x16& s) __attribute__((always_inline)) {
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
@@ -345,6 +363,7 @@ __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV>::kWaves), (sizeof(T) == 
         }
     }
     l = xor32_add(l);
+    if (any != 0 && m == -INFINITY) m = kLowest;
 
     // join the waves, the upper half of them into the lower, until one is left
     __syncthreads();
@@ -390,7 +409,7 @@ __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV>::kWaves), (sizeof(T) == 
             a.stats[2 * at] = m;
             a.stats[2 * at + 1] = l;
         }
-        if (l != 0.f) {  // (NaN too)
+        if (attends(m, l)) {
 #pragma unroll
             for (int i = 0; i < kVTiles; ++i)
 #pragma unroll
@@ -403,8 +422,8 @@ __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV>::kWaves), (sizeof(T) == 
         }
         return;
     }
-    const float inv = l != 0.f ? 1.f / l : 0.f;
-    if (a.lse != nullptr && half == 0) a.lse[q_at] = l != 0.f ? (m * sc + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+    const Norm norm = normalise(m, l, sc);
+    if (a.lse != nullptr && half == 0) a.lse[q_at] = norm.lse;
     T* out = static_cast<T*>(a.out) + q_at * DV;
     const T* z = a.z != nullptr && real ? static_cast<const T*>(a.z) + q_at * DV : nullptr;
 #pragma unroll
@@ -415,7 +434,7 @@ __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV>::kWaves), (sizeof(T) == 
             if (ch >= DV) continue;
             float y[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = acc[i][4 * r4 + e] * inv;
+            for (int e = 0; e < 4; ++e) y[e] = acc[i][4 * r4 + e] * norm.inv;
             store4<T>(out + ch, z != nullptr ? z + ch : nullptr, y);
         }
 }
@@ -458,10 +477,10 @@ __global__ __launch_bounds__(kJoinThreads) void attn_tree_join_kernel(TreeK a) {
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) top = fmaxf(top, tops[first + w]);
-    // No part was written where l is 0: its weight is below 0.  Every other part
-    // is added, also with a weight of 0, so that a value that is not finite
-    // reaches the row as it does in one piece, and an l of NaN makes it NaN.
-    const bool there = l != 0.f;
+    // No part was written where nothing is attended: its weight is below 0.
+    // Every other part is added, also with a weight of 0, so that a value that
+    // is not finite reaches the row as it does in one piece.
+    const bool there = attends(m, l);
     const float f = there ? __builtin_amdgcn_exp2f((m - top) * sc) : 0.f;
     weight[threadIdx.x] = there ? f : -1.f;
     l = wave_sum(l * f);
@@ -497,11 +516,11 @@ __global__ __launch_bounds__(kJoinThreads) void attn_tree_join_kernel(TreeK a) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[e] += o[e];
     }
-    const float inv = l != 0.f ? 1.f / l : 0.f;
+    const Norm norm = normalise(top, l, sc);
     float out[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) out[e] = y[e] * inv;
-    if (a.lse != nullptr && lane == 0) a.lse[r] = l != 0.f ? (top * sc + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+    for (int e = 0; e < 4; ++e) out[e] = y[e] * norm.inv;
+    if (a.lse != nullptr && lane == 0) a.lse[r] = norm.lse;
     if (ch < DV)
         store4<T>(static_cast<T*>(a.out) + r * DV + ch,
                   a.z != nullptr && real ? static_cast<const T*>(a.z) + r * DV + ch : nullptr, out);

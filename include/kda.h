@@ -446,7 +446,8 @@ int kda_spec_verify(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv,
  *  - scale multiplies q . k; positive and finite.
  *  - out_gate: NULL, or logits z of out's shape: out = o * sigmoid(z).
  *  - A row that attends nothing gets 0, and -infinity as its lse.  A row that
- *    attends a score that is NaN or +infinity is NaN, and so is its lse.
+ *    attends a score that is NaN or +infinity, or scores of -infinity alone, is
+ *    NaN, and so is its lse.
  *  - Non-finite values reach the rows that attend them.  Other sequences'
  *    rows, memory behind a sequence's end, stale page contents and drafts that
  *    a row does not attend never reach it.  Within one sequence of

@@ -127,6 +127,21 @@ class TestTree:
         _check_tree(K, x, TYPES[dtype])
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("parts", WIDTHS)
+def test_rows_whose_scores_are_all_minus_infinity(K, parts, dtype):
+    """NaN: only a row that attends nothing is 0 with an lse of -infinity."""
+    x = _tree(K, parts, dtype, lens=(300, 40, 0))
+    x["q"][:, :, :, 0] = 1.5
+    for token in range(40):
+        _committed(x, 1, token, 1, k={0: -math.inf})
+    x["k_new"][2, 1, 0, 0] = -math.inf
+    x["mask"][1, 2], x["mask"][2, 3], x["mask"][2, 4] = 0, 1 << 1 | 1 << 40, 1 << 5
+    out, lse = _check_tree(K, x, TYPES[dtype])
+    assert bool(torch.isnan(out[1, 2, 2:]).all()) and bool(torch.isnan(out[2, 3, :2]).all())
+    assert bool((out[2, 4] == 0).all())
+
+
 @pytest.mark.parametrize("parts", WIDTHS)
 def test_other_head_sizes(K, parts):
     for dk, dv in ((16, 16), (32, 32), (128, 128), (192, 128)):
@@ -153,7 +168,7 @@ def _prefill(K, q, k, v, z, dtype):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("dk,dv", [(16, 16), (64, 64), (128, 128), (192, 128)])
-@pytest.mark.parametrize("which", ["query", "key"])
+@pytest.mark.parametrize("which", ["query", "key", "far"])
 def test_prefill(K, which, dk, dv, dtype):
     t = TYPES[dtype]
     g = torch.Generator(device="cuda")
@@ -163,8 +178,11 @@ def test_prefill(K, which, dk, dv, dtype):
     print(f"prefill {which} {dk}/{dv} {dtype}", flush=True)
     if which == "query":
         q[5, 0, 3], q[70, 1, 0], q[149, 3, dk - 1] = math.nan, math.inf, -math.inf
-    else:
+    elif which == "key":
         k[40, 0, 2], k[100, 1, 1] = math.nan, math.inf
+    else:  # the first rows attend scores of -infinity alone
+        q[:, :, 1] = 0.5
+        k[:3, 0, 1], k[60, 1, 1] = -math.inf, -math.inf
     out, lse = _prefill(K, q, k, v, z, t)
     # the gradients of a broken row are NaN, and reach what the row attends
     dy = new(150, 4, dv)
