@@ -31,6 +31,13 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 // are (16 multiplications per 32 channels and lane).
 constexpr float kRise = 6.f;
 
+// A weight is e^((s - m) scale), formed as 2^(s c - m c) with one fused
+// multiply-add (c = scale log2(e)) while |m c| stays below 2^kFar: m c is off by
+// half a step, at most 2^-12 there, less than the fp32 scores themselves.  Past
+// it the maximum is taken off first (at |m c| of 2^33 the half step alone would
+// make every weight of a row 0 or infinite).
+constexpr float kFar = 4096.f;
+
 constexpr int kBufferDword3 = 0x00020000;  // raw buffer: byte offsets, reads past the end give 0
 
 // One 16-byte operand piece of A times one of B, added to a 32 x 32 result.
@@ -121,7 +128,8 @@ __device__ __forceinline__ u32x4 buffer_load16(__amdgpu_buffer_rsrc_t r, int off
 // A value that the compiler knows nothing about.  A mask inside a wave-uniform
 // branch compares with such a value and so stays in its branch: turned into
 // selects, what one tile in many needs would cost every tile its compares.
-__device__ __forceinline__ int opaque(int x) {
+template <typename X>
+__device__ __forceinline__ X opaque(X x) {
     asm volatile("" : "+v"(x));
     return x;
 }

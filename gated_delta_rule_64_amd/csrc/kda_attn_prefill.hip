@@ -140,7 +140,15 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void attn_fwd_k
 #pragma unroll
             for (int i = 0; i < kVTiles; ++i) acc[i] *= alpha;
         }
-        const float ms = m == -INFINITY ? 0.f : m * sc;
+        float ms = m == -INFINITY ? 0.f : m * sc;
+        if (__any(fabsf(ms) > kFar)) {
+            const float off = opaque(m == -INFINITY ? 0.f : m);
+#pragma unroll
+            for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[u][r] -= off;
+            ms = 0.f;
+        }
         float sum = 0.f;
 #pragma unroll
         for (int u = 0; u < kSub; ++u)

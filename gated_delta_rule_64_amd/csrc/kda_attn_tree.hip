@@ -255,7 +255,13 @@ __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV>::kWaves), (sizeof(T) == 
 #pragma unroll
                 for (int i = 0; i < kVTiles; ++i) acc[i] *= alpha;
             }
-            const float ms = m == -INFINITY ? 0.f : m * sc;
+            float ms = m == -INFINITY ? 0.f : m * sc;
+            if (__any(fabsf(ms) > kFar)) {
+                const float off = opaque(m == -INFINITY ? 0.f : m);
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[r] -= off;
+                ms = 0.f;
+            }
             float sum = 0.f;
 #pragma unroll
             for (int r = 0; r < 16; ++r) {

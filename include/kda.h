@@ -479,7 +479,9 @@ int kda_attn_prefill(int64_t T_tot, int32_t H, int32_t Hkv, int32_t dk, int32_t 
  * kda_attn_prefill_backward -- gradients of kda_attn_prefill for output
  * gradients dy.  The scores are formed again from q, k and lse; key and value
  * gradients are summed over the query heads that share a head.  Every sum has
- * one owner and a fixed order: the same inputs give the same bits.
+ * one owner and a fixed order: the same inputs give the same bits.  A row's
+ * weights e^(s - lse) are as right as its fp32 lse, to about |lse| 2^-23 of
+ * themselves (10^-3 at scores of 10^4; past 10^8 the gradients mean nothing).
  * Arguments: those of kda_attn_prefill, with out and lse as it wrote them, and
  *   dy            [T_tot, H, dv];
  *   grad_q [T_tot, H, dk], grad_k [T_tot, Hkv, dk], grad_v [T_tot, Hkv, dv]:

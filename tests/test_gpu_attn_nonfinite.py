@@ -1,6 +1,6 @@
-"""Attention of rows that meet NaN or infinity: such a row is NaN and so is its
-lse, however the call is cut into parts, and the rows beside it are as if
-nothing had been there."""
+"""Attention of rows that meet NaN, infinity or scores past fp32's range: such a
+row is NaN and so is its lse, however the call is cut into parts, and the rows
+beside it are as if nothing had been there."""
 
 import math
 
@@ -115,6 +115,15 @@ class TestTree:
         x["k_new"][1, 4, 1, 0] = value
         _check_tree(K, x, TYPES[dtype])
 
+    def test_scores_that_overflow(self, K, parts, dtype):
+        """A row whose own scores are past fp32's range is NaN.  The rows beside
+        it have scores of 10^29: the largest takes all the weight."""
+        x = _tree(K, parts, dtype)
+        x["q"][0, 3, 1, 8] = 1e30
+        _committed(x, 0, 33, 0, k={8: 1e30})
+        _committed(x, 0, 200, 0, k={8: -1e30})
+        _check_tree(K, x, TYPES[dtype])
+
     @pytest.mark.parametrize("value", [math.nan, math.inf])
     def test_a_committed_value(self, K, parts, dtype, value):
         """The channel, also where the weights of the key and of all around it
@@ -168,7 +177,7 @@ def _prefill(K, q, k, v, z, dtype):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("dk,dv", [(16, 16), (64, 64), (128, 128), (192, 128)])
-@pytest.mark.parametrize("which", ["query", "key", "far"])
+@pytest.mark.parametrize("which", ["query", "key", "far", "overflow"])
 def test_prefill(K, which, dk, dv, dtype):
     t = TYPES[dtype]
     g = torch.Generator(device="cuda")
@@ -180,6 +189,8 @@ def test_prefill(K, which, dk, dv, dtype):
         q[5, 0, 3], q[70, 1, 0], q[149, 3, dk - 1] = math.nan, math.inf, -math.inf
     elif which == "key":
         k[40, 0, 2], k[100, 1, 1] = math.nan, math.inf
+    elif which == "overflow":
+        q[120, 2, 4], k[20, 1, 4] = 1e30, 1e30
     else:  # the first rows attend scores of -infinity alone
         q[:, :, 1] = 0.5
         k[:3, 0, 1], k[60, 1, 1] = -math.inf, -math.inf
@@ -195,3 +206,52 @@ def test_prefill(K, which, dk, dv, dtype):
             last = int(torch.nonzero(broken[:, h])[-1, 0])
             for name in ("dk", "dv"):
                 assert bool(torch.isnan(grads[name][:last + 1, h // 2]).all()), name
+
+
+FAR = 1024.0  # its square is every score's size below; the scores are whole numbers, exact in fp32
+
+
+def _check_far(name, out, lse, q, k, v, seen, dtype):
+    """Scores of FAR^2 and a small number: the weights are those of the small
+    numbers alone, and lse is FAR^2 more (three roundings of a 24-bit number)."""
+    q, k = q.double().clone(), k.double().clone()
+    assert bool((q[:, 0] * k[:, 0].unique() == FAR * FAR).all())
+    q[:, 0] = 0
+    o, bo, l, bl, _, _ = R.softmax_rows(q, k, v.double(), 1.0, seen, R.UNIT[dtype])
+    R.check(name + " out", out, o, bo + R.UNIT[dtype] * (o.abs() + bo) + 1e-30)
+    R.check(name + " lse", lse, l + FAR * FAR, bl + 3 * FAR * FAR * 2.0 ** -24)
+
+
+def _far_row(q):
+    q.zero_()
+    q[..., 0], q[..., 1] = FAR, 1.0
+
+
+def _far_key(k):
+    k[..., 0], k[..., 1] = FAR, k[..., 1].round()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("parts", WIDTHS)
+def test_large_scores_keep_their_differences(K, parts, dtype):
+    t = TYPES[dtype]
+    x = _tree(K, parts, dtype)
+    x["z"] = None
+    _far_row(x["q"])
+    for y in (x["kc"], x["k_new"], *x["ctx_k"]):
+        _far_key(y)
+    out, lse = _call(K, x, scale=1.0)
+    for b in range(2):
+        new = torch.tensor([[bool(int(x["mask"][b, i]) >> j & 1) for j in range(5)] for i in range(5)], device="cuda")
+        seen = torch.cat([torch.ones(5, x["ctx_k"][b].shape[0], dtype=torch.bool, device="cuda"), new], 1)
+        for h in range(4):
+            _check_far(f"{b},{h}", out[b, :, h], lse[b, :, h], x["q"][b, :, h], torch.cat([x["ctx_k"][b][:, h // 2], x["k_new"][b, :, h // 2]]),
+                       torch.cat([x["ctx_v"][b][:, h // 2], x["v_new"][b, :, h // 2]]), seen, t)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(parts)
+    q, k, v = (torch.randn(n, generator=g, device="cuda").to(t) for n in ((200, 2, 128), (200, 1, 128), (200, 1, 128)))
+    _far_row(q)
+    _far_key(k)
+    out, lse = K.kda_attn_prefill(q, k, v, scale=1.0)
+    for h in range(2):
+        _check_far(f"prefill {h}", out[:, h], lse[:, h], q[:, h], k[:, 0], v[:, 0], R.causal(200, "cuda"), t)
