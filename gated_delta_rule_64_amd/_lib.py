@@ -62,8 +62,10 @@ _WORK = [_vp, _sz, _vp]          # workspace, its bytes, stream
 PROTOTYPES.update({
     "kda_attn_prefill": (ctypes.c_int, [_i64, _i32, _i32, _i32, _i32, _vp, _i32, _i32, _f32] + [_vp] * 6 + [_vp]),
     "kda_attn_backward_workspace_bytes": (_sz, [_i64] + [_i32] * 7),
+    "kda_attn_backward_max_workspace_bytes": (_sz, [_i64] + [_i32] * 6),
     "kda_attn_prefill_backward": (ctypes.c_int, [_i64, _i32, _i32, _i32, _i32, _vp, _i32, _i32, _f32] + [_vp] * 11 + _WORK),
     "kda_attn_tree_workspace_bytes": (_sz, [_i32] * 7 + [_i64]),
+    "kda_attn_tree_max_workspace_bytes": (_sz, [_i32] * 7 + [_i64]),
     "kda_attn_tree": (ctypes.c_int, [_i32] * 7 + [_f32] + [_vp] * 5 + _POOLS + _TABLE + [_vp] * 4 + _WORK),
     "kda_cache_append": (ctypes.c_int, [_i64, _i32, _vp, _i64, _vp] + [_i32] * 4 + [_vp, _vp] + _POOLS + _TABLE +
                          [_vp, _vp, _vp]),

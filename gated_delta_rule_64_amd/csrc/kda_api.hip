@@ -825,6 +825,12 @@ size_t kda_attn_backward_workspace_bytes(int64_t T_tot, int32_t N, int32_t H, in
     return kda::attn_backward_workspace_bytes(T_tot, N, H, Hkv, dk, dv, static_cast<kda::DT>(x_dtype), with_gate != 0);
 }
 
+size_t kda_attn_backward_max_workspace_bytes(int64_t max_T_tot, int32_t H, int32_t Hkv, int32_t dk, int32_t dv,
+                                             int32_t x_dtype, int32_t with_gate) {
+    if (kda_attn_backward_workspace_bytes(max_T_tot, 1, H, Hkv, dk, dv, x_dtype, with_gate) == 0) return 0;
+    return kda::attn_backward_max_workspace_bytes(max_T_tot, H, Hkv, dk, dv, static_cast<kda::DT>(x_dtype), with_gate != 0);
+}
+
 int kda_attn_prefill_backward(int64_t T_tot, int32_t H, int32_t Hkv, int32_t dk, int32_t dv,
                               const int32_t* cu_seqlens, int32_t N, int32_t x_dtype, float scale, const void* q,
                               const void* k, const void* v, const void* out_gate, const void* out, const float* lse,
@@ -862,12 +868,23 @@ int kda_attn_prefill_backward(int64_t T_tot, int32_t H, int32_t Hkv, int32_t dk,
     return ok();
 }
 
+namespace {
+bool tree_sizes(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t dk, int32_t dv, int32_t x_dtype, int64_t max_context) {
+    return B >= 0 && T >= 0 && T <= kda::kTreeMaxTokens && H >= 1 && H <= 65535 && Hkv >= 1 && H % Hkv == 0 && max_context >= 0 &&
+           max_context < (int64_t(1) << 31) && kda::attn_head_sizes(dk, dv) && valid_dtype(x_dtype);
+}
+}  // namespace
+
 size_t kda_attn_tree_workspace_bytes(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t dk, int32_t dv,
                                      int32_t x_dtype, int64_t max_context) {
-    if (B < 0 || T < 0 || T > kda::kTreeMaxTokens || H < 1 || H > 65535 || Hkv < 1 || H % Hkv != 0 || max_context < 0 ||
-        max_context >= (int64_t(1) << 31) || !kda::attn_head_sizes(dk, dv) || !valid_dtype(x_dtype))
-        return 0;
+    if (!tree_sizes(B, T, H, Hkv, dk, dv, x_dtype, max_context)) return 0;
     return kda::attn_tree_workspace_bytes(B, T, H, Hkv, dv, max_context);
+}
+
+size_t kda_attn_tree_max_workspace_bytes(int32_t max_B, int32_t max_T, int32_t H, int32_t Hkv, int32_t dk, int32_t dv,
+                                         int32_t x_dtype, int64_t max_context) {
+    if (!tree_sizes(max_B, max_T, H, Hkv, dk, dv, x_dtype, max_context)) return 0;
+    return kda::attn_tree_max_workspace_bytes(max_B, max_T, H, Hkv, dv, max_context);
 }
 
 int kda_attn_tree(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t dk, int32_t dv, int32_t x_dtype, float scale,

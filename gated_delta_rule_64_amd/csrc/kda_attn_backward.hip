@@ -469,6 +469,7 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_sum_kernel(BwdK a) {
 // Into how many parts the work of a tile is cut: key tiles so that their
 // workgroups, which differ in length, fill the chip several times; query tiles
 // where they and the key tiles' together leave it half empty.
+constexpr int kKeyWant = 1024, kQueryWant = 384;  // workgroups below which tiles are cut
 struct BwdParts {
     int key, query;
 };
@@ -479,7 +480,7 @@ BwdParts bwd_parts(int64_t T, int N, int H, int Hkv) {
         const int64_t p = (want + units - 1) / units;
         return static_cast<int>(p < 1 ? 1 : p > most ? most : p);
     };
-    return {parts(1024, keys, kMostParts), parts(384, queries, kMostParts / 2)};
+    return {parts(kKeyWant, keys, kMostParts), parts(kQueryWant, queries, kMostParts / 2)};
 }
 
 size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -545,6 +546,19 @@ size_t attn_backward_workspace_bytes(int64_t T, int N, int H, int Hkv, int dk, i
     return up256(rows * 8) + (gate ? up256(rows * dv * (x == DT::BF16 ? 2 : 4)) : 0) +
            (parts.key > 1 ? up256(static_cast<size_t>(parts.key) * T * Hkv * (dk + dv) * 4) : 0) +
            (parts.query > 1 ? up256(static_cast<size_t>(parts.query) * rows * dk * 4) : 0);
+}
+
+// More tokens have fewer parts, so what a call needs does not rise with its
+// sizes.  One sequence has the fewest tiles and so the most parts; of the
+// lengths of as many tiles the longest needs the most; from kKeyWant tiles on
+// there is one part.
+size_t attn_backward_max_workspace_bytes(int64_t T, int H, int Hkv, int dk, int dv, DT x, bool gate) {
+    size_t most = attn_backward_workspace_bytes(T, 1, H, Hkv, dk, dv, x, gate);
+    for (int64_t t = kRows - 1; t < T && t < static_cast<int64_t>(kKeyWant) * kRows; t += kRows) {
+        const size_t need = attn_backward_workspace_bytes(t, 1, H, Hkv, dk, dv, x, gate);
+        most = need > most ? need : most;
+    }
+    return most;
 }
 
 hipError_t launch_attn_prefill_backward(const AttnBackwardArgs& a, hipStream_t s) {

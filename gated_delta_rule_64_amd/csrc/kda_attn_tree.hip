@@ -536,6 +536,7 @@ __global__ __launch_bounds__(kJoinThreads) void attn_tree_join_kernel(TreeK a) {
 struct TreePlan {
     int blocks, splits;
 };
+constexpr int kWantUnits = 1024, kWantUnitsOfOne = 512;  // workgroups below which a call is split
 TreePlan tree_plan(int B, int T, int H, int Hkv, int64_t max_ctx) {
     const int64_t rows = static_cast<int64_t>(T) * (H / Hkv);
     TreePlan p;
@@ -547,7 +548,7 @@ TreePlan tree_plan(int B, int T, int H, int Hkv, int64_t max_ctx) {
     // 198 and 9 us in two rounds).  Sequences differ, and two rounds let the
     // short ones fill up behind the long (64 of up to 8,000 tokens: 219 us
     // against 239 us in one).
-    const int64_t want = B == 1 ? 512 : 1024;
+    const int64_t want = B == 1 ? kWantUnitsOfOne : kWantUnits;
     int64_t s = (want + units - 1) / units;
     if (s > tiles / 8) s = tiles / 8;  // two tiles a wave at least
     p.splits = static_cast<int>(s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s);
@@ -596,6 +597,20 @@ size_t attn_tree_workspace_bytes(int B, int T, int H, int Hkv, int dv, int64_t m
     if (p.splits == 1) return 0;
     const size_t parts = static_cast<size_t>(p.splits) * B * T * H;
     return up256(parts * dv * 4) + up256(parts * 8);
+}
+
+// More sequences or tokens have fewer parts of more rows, so what a call needs
+// does not rise with its sizes: all that are split are tried.
+size_t attn_tree_max_workspace_bytes(int B, int T, int H, int Hkv, int dv, int64_t max_ctx) {
+    size_t most = 0;
+    for (int t = 1; t <= T; ++t) {
+        const int64_t units = static_cast<int64_t>(Hkv) * ((static_cast<int64_t>(t) * (H / Hkv) + 31) / 32);  // of a sequence
+        for (int b = 1; b <= B && b * units < kWantUnits; ++b) {
+            const size_t need = attn_tree_workspace_bytes(b, t, H, Hkv, dv, max_ctx);
+            most = need > most ? need : most;
+        }
+    }
+    return most;
 }
 
 hipError_t launch_attn_tree(const TreeArgs& a, hipStream_t s) {

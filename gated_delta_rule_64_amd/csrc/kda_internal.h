@@ -219,8 +219,10 @@ hipError_t attn_dispatch(DT x, int dk, int dv, F&& f) {
 
 hipError_t launch_attn_prefill(const AttnArgs& a, hipStream_t s);
 size_t attn_backward_workspace_bytes(int64_t T, int N, int H, int Hkv, int dk, int dv, DT x, bool gate);
+size_t attn_backward_max_workspace_bytes(int64_t T, int H, int Hkv, int dk, int dv, DT x, bool gate);
 hipError_t launch_attn_prefill_backward(const AttnBackwardArgs& a, hipStream_t s);
 size_t attn_tree_workspace_bytes(int B, int T, int H, int Hkv, int dv, int64_t max_ctx);
+size_t attn_tree_max_workspace_bytes(int B, int T, int H, int Hkv, int dv, int64_t max_ctx);
 hipError_t launch_attn_tree(const TreeArgs& a, hipStream_t s);
 
 hipError_t launch_cache_append(const CacheArgs& c, int64_t tokens, int N, const int32_t* cu, int64_t src_rows, const int32_t* rows,

@@ -357,6 +357,14 @@ def kda_attn_backward_workspace_bytes(T_tot, N, H, Hkv, dk, dv, x_dtype, with_ga
     return int(lib().kda_attn_backward_workspace_bytes(T_tot, N, H, Hkv, dk, dv, x_dtype, int(bool(with_gate))))
 
 
+def kda_attn_backward_max_workspace_bytes(max_T_tot, H, Hkv, dk, dv, x_dtype, with_gate):
+    """What every call of up to ``max_T_tot`` tokens needs at most (a call of
+    fewer tokens can need more than a larger one)."""
+    if isinstance(x_dtype, torch.dtype):
+        x_dtype = KDA_BF16 if x_dtype == torch.bfloat16 else KDA_F32
+    return int(lib().kda_attn_backward_max_workspace_bytes(max_T_tot, H, Hkv, dk, dv, x_dtype, int(bool(with_gate))))
+
+
 def kda_attn_prefill_backward(q, k, v, out, lse, dy, out_gate=None, cu_seqlens=None, scale=None, workspace=None):
     """Gradients of kda_attn_prefill for output gradients dy [T,H,dv]; ``out``
     and ``lse`` are what it returned.  Returns a dict of dq [T,H,dk], dk
@@ -393,6 +401,14 @@ def kda_attn_tree_workspace_bytes(B, T, H, Hkv, dk, dv, x_dtype, max_context):
     if isinstance(x_dtype, torch.dtype):
         x_dtype = KDA_BF16 if x_dtype == torch.bfloat16 else KDA_F32
     return int(lib().kda_attn_tree_workspace_bytes(B, T, H, Hkv, dk, dv, x_dtype, max_context))
+
+
+def kda_attn_tree_max_workspace_bytes(max_B, max_T, H, Hkv, dk, dv, x_dtype, max_context):
+    """What every call of up to ``max_B`` sequences of up to ``max_T`` tokens
+    needs at most (a call of fewer sequences can need more than a larger one)."""
+    if isinstance(x_dtype, torch.dtype):
+        x_dtype = KDA_BF16 if x_dtype == torch.bfloat16 else KDA_F32
+    return int(lib().kda_attn_tree_max_workspace_bytes(max_B, max_T, H, Hkv, dk, dv, x_dtype, max_context))
 
 
 def kda_attn_tree(q, k_new, v_new, k_cache, v_cache, page_table, lens, tree_mask=None, out_gate=None,

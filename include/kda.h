@@ -489,12 +489,17 @@ int kda_attn_prefill(int64_t T_tot, int32_t H, int32_t Hkv, int32_t dk, int32_t 
  *   grad_out_gate [T_tot, H, dv], required exactly when out_gate is given;
  *   workspace     at least kda_attn_backward_workspace_bytes() bytes (of the
  *                 same sizes; with_gate: whether out_gate is given), 256-byte
- *                 aligned; contents on entry are ignored.
+ *                 aligned; contents on entry are ignored.  Fewer tokens can
+ *                 need more (their work is cut into more parts): a workspace
+ *                 of kda_attn_backward_max_workspace_bytes() bytes holds every
+ *                 call of up to max_T_tot tokens in any number of sequences.
  * H x (T_tot/128 + min(N, T_tot)) must stay below 2^23 and T_tot x H below
  * 2^28 (KDA_ERR_UNSUPPORTED otherwise).
  */
 size_t kda_attn_backward_workspace_bytes(int64_t T_tot, int32_t N, int32_t H, int32_t Hkv,
                                          int32_t dk, int32_t dv, int32_t x_dtype, int32_t with_gate);
+size_t kda_attn_backward_max_workspace_bytes(int64_t max_T_tot, int32_t H, int32_t Hkv,
+                                             int32_t dk, int32_t dv, int32_t x_dtype, int32_t with_gate);
 int kda_attn_prefill_backward(int64_t T_tot, int32_t H, int32_t Hkv, int32_t dk, int32_t dv,
                               const int32_t* cu_seqlens, int32_t N, int32_t x_dtype, float scale,
                               const void* q, const void* k, const void* v,
@@ -538,6 +543,11 @@ int kda_attn_prefill_backward(int64_t T_tot, int32_t H, int32_t Hkv, int32_t dk,
  *   out [B, T, H, dv]; lse NULL or fp32 [B, T, H];
  *   workspace     at least kda_attn_tree_workspace_bytes() bytes for
  *                 max_context = max_pages * page_size, 256-byte aligned.
+ *                 Fewer sequences can need more (their keys are cut into more
+ *                 parts): kda_attn_tree_max_workspace_bytes() bytes hold every
+ *                 call of up to max_B sequences of up to max_T tokens over
+ *                 tables of up to max_context (a query for setting up: it
+ *                 takes up to milliseconds).
  * Tokens whose table entry names no page are not attended.  Lengths are
  * clamped to what a table row holds.  B x T x H must be below 2^30, and
  * B x Hkv x ceil(T x H/Hkv / 32) below 2^24 (B x Hkv rounded up to 8;
@@ -545,6 +555,8 @@ int kda_attn_prefill_backward(int64_t T_tot, int32_t H, int32_t Hkv, int32_t dk,
  */
 size_t kda_attn_tree_workspace_bytes(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t dk,
                                      int32_t dv, int32_t x_dtype, int64_t max_context);
+size_t kda_attn_tree_max_workspace_bytes(int32_t max_B, int32_t max_T, int32_t H, int32_t Hkv, int32_t dk,
+                                         int32_t dv, int32_t x_dtype, int64_t max_context);
 int kda_attn_tree(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t dk, int32_t dv,
                   int32_t x_dtype, float scale,
                   const void* q, const void* k_new, const void* v_new,
