@@ -382,7 +382,8 @@ __global__ __launch_bounds__(kPlan) void cache_reserve_kernel(ReserveK a) {
         const int64_t n = (static_cast<int64_t>(max(a.new_lens[i], 0)) + mask) >> c.page_shift;
         if (e.slot < 0 || e.slot >= c.slots || n > c.max_pages) return Entry{-1, 0, 0};
         e.end = static_cast<int>(n);
-        // (the pages below the slot's length are there)
+        // (only the columns behind the length: a missing page in front of it had
+        // tokens, and a new page's stale contents would be attended as them)
         e.first = min(static_cast<int>((static_cast<int64_t>(max(c.lens[e.slot], 0)) + mask) >> c.page_shift), e.end);
         return e;
     };

@@ -522,8 +522,9 @@ def kda_cache_fork(src, dst, k_cache, v_cache, page_table, lens, refs, status=No
 
 
 def kda_cache_reserve(slot_list, new_lens, page_size, page_table, lens, refs, status=None, workspace=None):
-    """Gives every listed slot the pages that it lacks for new_lens[i] tokens.
-    Returns status int32 [n]: 0 done, 1 too few free pages, 2 refused."""
+    """Gives every listed slot the pages that it lacks behind its length for
+    new_lens[i] tokens.  Returns status int32 [n]: 0 done, 1 too few free
+    pages, 2 refused."""
     n = _slot_list("slot_list", slot_list)
     _shape("new_lens", new_lens, (n,), torch.int32)
     slots, width = page_table.shape

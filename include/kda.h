@@ -617,8 +617,12 @@ int kda_cache_append(int64_t T_tot, int32_t N, const int32_t* cu_seqlens,
  * entry of the call names.  A slot may be forked many times in one call.
  *
  * kda_cache_reserve -- gives slot slot_list[i] the pages that it lacks for
- * new_lens[i] tokens: every table entry from its length's last page on, up to
- * the new length, that names no page gets one.  lens is not changed.
+ * new_lens[i] tokens: every table entry behind those that hold its length, up
+ * to the new length, that names no page gets one.  lens is not changed.  An
+ * entry that holds a part of the length and names no page stays so, the last,
+ * partly filled one too: its tokens are gone, a page there would put stale
+ * contents in their place, and kda_cache_append drops what falls into it
+ * (free such a slot and write its tokens again).
  * Refused: lengths that a table row does not hold, and a slot that an earlier
  * entry of the call names.
  *
