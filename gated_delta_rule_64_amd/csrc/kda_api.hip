@@ -5,7 +5,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
-#include <initializer_list>
+#include <iterator>
 #include <mutex>
 #include <new>
 #include <vector>
@@ -56,8 +56,8 @@ int check_spans(const Spans& v) {
         if (reinterpret_cast<uintptr_t>(s.p) % s.align != 0)
             return fail(KDA_ERR_INVALID_ARGUMENT, "%s is not %zu-byte aligned", s.name, s.align);
     }
-    for (size_t i = 0; i < v.size(); ++i) {
-        for (size_t j = i + 1; j < v.size(); ++j) {
+    for (size_t i = 0; i < std::size(v); ++i) {
+        for (size_t j = i + 1; j < std::size(v); ++j) {
             const Span &a = v[i], &b = v[j];
             if (a.bytes == 0 || b.bytes == 0 || !(a.writes || b.writes)) continue;
             const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
@@ -670,27 +670,8 @@ int kda_prefill_layer_noalloc(int64_t T_tot, int32_t H, int32_t dk, int32_t dv, 
 
 namespace {
 
-// A call's buffers, in place: checking them allocates nothing and cannot throw.
-class SpanList {
-public:
-    SpanList() = default;
-    SpanList(std::initializer_list<Span> l) {
-        for (const Span& s : l) push_back(s);
-    }
-    void push_back(const Span& s) {
-        if (n_ < kMost) v_[n_++] = s;
-    }
-    Span& back() { return v_[n_ - 1]; }
-    const Span& operator[](size_t i) const { return v_[i]; }
-    size_t size() const { return n_; }
-    const Span* begin() const { return v_; }
-    const Span* end() const { return v_ + n_; }
-
-private:
-    static constexpr size_t kMost = 16;  // the longest list below has 13
-    Span v_[kMost];
-    size_t n_ = 0;
-};
+// (A call's buffers are an array of its own size in the calls below: checking
+// them allocates nothing, cannot throw and leaves none out.)
 
 // Sizes and types that the attention calls share.
 int check_heads(int32_t H, int32_t Hkv, int32_t dk, int32_t dv, int32_t x_dtype, float scale) {
@@ -781,11 +762,10 @@ int debug_check_copy(const int32_t* src, const int32_t* dst, int32_t n, int32_t 
 
 size_t table_bytes(int32_t slots, int32_t max_pages) { return static_cast<size_t>(slots) * max_pages * 4; }
 
-int check_workspace(const char* call, size_t have, size_t need, const void* p, SpanList& sp) {
+int check_workspace(const char* call, size_t have, size_t need, const void* p) {
     if (have < need) return fail(KDA_ERR_WORKSPACE_TOO_SMALL, "%s: workspace_bytes=%zu < %zu needed", call, have, need);
     if (need > 0 && (p == nullptr || (reinterpret_cast<uintptr_t>(p) & 255u) != 0))
         return fail(KDA_ERR_INVALID_ARGUMENT, "workspace is NULL or not 256-byte aligned");
-    sp.push_back({"workspace", p, need, true});
     return KDA_OK;
 }
 
@@ -800,7 +780,7 @@ int kda_attn_prefill(int64_t T_tot, int32_t H, int32_t Hkv, int32_t dk, int32_t 
     if (st == KDA_OK) st = check_packed(T_tot, N, cu_seqlens, H);
     if (st != KDA_OK) return st;
     const size_t xs = dsize(x_dtype), T = static_cast<size_t>(T_tot);
-    const SpanList sp = {
+    const Span sp[] = {
         {"q", q, T * H * dk * xs, false}, {"k", k, T * Hkv * dk * xs, false}, {"v", v, T * Hkv * dv * xs, false},
         {"out_gate", out_gate, out_gate ? T * H * dv * xs : 0, false},
         {"cu_seqlens", cu_seqlens, cu_seqlens ? (static_cast<size_t>(N) + 1) * 4 : 0, false, 4},
@@ -844,16 +824,17 @@ int kda_attn_prefill_backward(int64_t T_tot, int32_t H, int32_t Hkv, int32_t dk,
     if ((out_gate != nullptr) != (grad_out_gate != nullptr) && T_tot > 0)
         return fail(KDA_ERR_INVALID_ARGUMENT, "grad_out_gate is required exactly when out_gate is given");
     const size_t xs = dsize(x_dtype), T = static_cast<size_t>(T_tot);
-    SpanList sp = {
+    const size_t need = kda_attn_backward_workspace_bytes(T_tot, N, H, Hkv, dk, dv, x_dtype, out_gate != nullptr);
+    const Span sp[] = {
         {"q", q, T * H * dk * xs, false}, {"k", k, T * Hkv * dk * xs, false}, {"v", v, T * Hkv * dv * xs, false},
         {"out_gate", out_gate, out_gate ? T * H * dv * xs : 0, false}, {"out", out, T * H * dv * xs, false},
         {"lse", lse, T * H * 4, false, 4}, {"dy", dy, T * H * dv * xs, false},
         {"cu_seqlens", cu_seqlens, cu_seqlens ? (static_cast<size_t>(N) + 1) * 4 : 0, false, 4},
         {"grad_q", grad_q, T * H * dk * xs, true}, {"grad_k", grad_k, T * Hkv * dk * xs, true},
         {"grad_v", grad_v, T * Hkv * dv * xs, true}, {"grad_out_gate", grad_out_gate, grad_out_gate ? T * H * dv * xs : 0, true},
+        {"workspace", workspace, need, true},
     };
-    st = check_workspace("kda_attn_prefill_backward", workspace_bytes,
-                         kda_attn_backward_workspace_bytes(T_tot, N, H, Hkv, dk, dv, x_dtype, out_gate != nullptr), workspace, sp);
+    st = check_workspace("kda_attn_prefill_backward", workspace_bytes, need, workspace);
     if (st == KDA_OK) st = check_spans(sp);
     if (st != KDA_OK) return st;
     hipStream_t s = static_cast<hipStream_t>(stream);
@@ -909,7 +890,8 @@ int kda_attn_tree(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t dk, int3
     const size_t xs = dsize(x_dtype), BT = static_cast<size_t>(B) * T;
     const size_t page = static_cast<size_t>(num_pages) * Hkv * page_size;
     const bool any = BT > 0;
-    SpanList sp = {
+    const size_t need = kda_attn_tree_workspace_bytes(B, T, H, Hkv, dk, dv, x_dtype, static_cast<int64_t>(max_pages) << shift);
+    const Span sp[] = {
         {"q", q, BT * H * dk * xs, false}, {"k_new", k_new, BT * Hkv * dk * xs, false}, {"v_new", v_new, BT * Hkv * dv * xs, false},
         {"tree_mask", tree_mask, tree_mask ? BT * 8 : 0, false, 8}, {"out_gate", out_gate, out_gate ? BT * H * dv * xs : 0, false},
         {"k_cache", k_cache, any ? page * dk * xs : 0, false}, {"v_cache", v_cache, any ? page * dv * xs : 0, false},
@@ -917,9 +899,9 @@ int kda_attn_tree(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t dk, int3
         {"lens", lens, any ? static_cast<size_t>(slots) * 4 : 0, false, 4},
         {"slot_indices", slot_indices, slot_indices ? static_cast<size_t>(B) * 4 : 0, false, 4},
         {"out", out, BT * H * dv * xs, true}, {"lse", lse, lse ? BT * H * 4 : 0, true, 4},
+        {"workspace", workspace, need, true},
     };
-    st = check_workspace("kda_attn_tree", workspace_bytes,
-                         kda_attn_tree_workspace_bytes(B, T, H, Hkv, dk, dv, x_dtype, static_cast<int64_t>(max_pages) << shift), workspace, sp);
+    st = check_workspace("kda_attn_tree", workspace_bytes, need, workspace);
     if (st == KDA_OK) st = check_spans(sp);
     if (st != KDA_OK) return st;
     kda::TreeArgs a{B, T, H, Hkv, dk, dv, static_cast<kda::DT>(x_dtype), scale, q, k_new, v_new, out_gate, tree_mask,
@@ -933,11 +915,10 @@ int kda_attn_tree(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t dk, int3
 
 namespace {
 
-// A call on pools and tables: sizes checked, pools and table in the overlap
-// check (the pools where the call has them).
+// A call on pools and tables: its sizes checked.
 int cache_args(int32_t Hkv, int32_t dk, int32_t dv, int32_t x_dtype, void* k_cache, void* v_cache, int32_t num_pages,
                int32_t page_size, int32_t* page_table, int32_t slots, int32_t max_pages, int32_t* lens, int32_t* refs,
-               SpanList& sp, kda::CacheArgs& a) {
+               kda::CacheArgs& a) {
     int shift = 0;
     int st = check_cache(num_pages, page_size, slots, max_pages, shift);
     if (st != KDA_OK) return st;
@@ -947,12 +928,13 @@ int cache_args(int32_t Hkv, int32_t dk, int32_t dv, int32_t x_dtype, void* k_cac
         return fail(KDA_ERR_UNSUPPORTED, "dk=%d, dv=%d: attention takes dk = dv = 16, 32, 64, 128 or dk = 192, dv = 128", dk, dv);
     if (static_cast<int64_t>(Hkv) * dk * static_cast<int64_t>(dsize(x_dtype)) >= (1 << 25))
         return fail(KDA_ERR_UNSUPPORTED, "Hkv=%d, dk=%d: a token's row of %zu bytes is not below 2^25", Hkv, dk, Hkv * dk * dsize(x_dtype));
-    const size_t rows = static_cast<size_t>(num_pages) * Hkv * page_size;
-    sp.push_back({"k_cache", k_cache, rows * dk * dsize(x_dtype), true});
-    sp.push_back({"v_cache", v_cache, rows * dv * dsize(x_dtype), true});
-    sp.push_back({"page_table", page_table, table_bytes(slots, max_pages), true, 4});
     a = kda::CacheArgs{Hkv, dk, dv, num_pages, shift, slots, max_pages, static_cast<kda::DT>(x_dtype), k_cache, v_cache, page_table, lens, refs};
     return KDA_OK;
+}
+
+// Bytes of a pool of rows of d elements.
+size_t pool_bytes(const kda::CacheArgs& c, int d) {
+    return (static_cast<size_t>(c.pages) * c.Hkv << c.page_shift) * d * dsize(static_cast<int32_t>(c.x));
 }
 
 }  // namespace
@@ -973,20 +955,20 @@ int kda_cache_append(int64_t T_tot, int32_t N, const int32_t* cu_seqlens, int64_
     if (src_rows < 0 || src_rows >= (int64_t(1) << 31)) return fail(KDA_ERR_INVALID_ARGUMENT, "src_rows=%lld out of range [0, 2^31)", (long long)src_rows);
     if (rows == nullptr && src_rows < T_tot)
         return fail(KDA_ERR_INVALID_ARGUMENT, "rows is NULL but src_rows=%lld is below T_tot=%lld", (long long)src_rows, (long long)T_tot);
-    SpanList sp;
     kda::CacheArgs c;
     int st = cache_args(Hkv, dk, dv, x_dtype, k_cache, v_cache, num_pages, page_size, const_cast<int32_t*>(page_table), slots,
-                        max_pages, const_cast<int32_t*>(lens), nullptr, sp, c);
+                        max_pages, const_cast<int32_t*>(lens), nullptr, c);
     if (st != KDA_OK) return st;
     if (T_tot == 0) return ok();
     const size_t xs = dsize(x_dtype);
-    sp.back().writes = false;  // the table is read
-    sp.push_back({"lens", lens, static_cast<size_t>(slots) * 4, false, 4});
-    sp.push_back({"k_new", k_new, static_cast<size_t>(src_rows) * Hkv * dk * xs, false});
-    sp.push_back({"v_new", v_new, static_cast<size_t>(src_rows) * Hkv * dv * xs, false});
-    sp.push_back({"cu_seqlens", cu_seqlens, cu_seqlens ? (static_cast<size_t>(N) + 1) * 4 : 0, false, 4});
-    sp.push_back({"rows", rows, rows ? static_cast<size_t>(T_tot) * 4 : 0, false, 4});
-    sp.push_back({"slot_indices", slot_indices, slot_indices ? static_cast<size_t>(N) * 4 : 0, false, 4});
+    const Span sp[] = {
+        {"k_cache", k_cache, pool_bytes(c, dk), true}, {"v_cache", v_cache, pool_bytes(c, dv), true},
+        {"page_table", page_table, table_bytes(slots, max_pages), false, 4}, {"lens", lens, static_cast<size_t>(slots) * 4, false, 4},
+        {"k_new", k_new, static_cast<size_t>(src_rows) * Hkv * dk * xs, false}, {"v_new", v_new, static_cast<size_t>(src_rows) * Hkv * dv * xs, false},
+        {"cu_seqlens", cu_seqlens, cu_seqlens ? (static_cast<size_t>(N) + 1) * 4 : 0, false, 4},
+        {"rows", rows, rows ? static_cast<size_t>(T_tot) * 4 : 0, false, 4},
+        {"slot_indices", slot_indices, slot_indices ? static_cast<size_t>(N) * 4 : 0, false, 4},
+    };
     st = check_spans(sp);
     if (st != KDA_OK) return st;
     hipStream_t s = static_cast<hipStream_t>(stream);
@@ -1010,7 +992,7 @@ int kda_cache_free(int32_t n, const int32_t* slot_list, int32_t num_pages, int32
     st = check_entries(n);
     if (st != KDA_OK) return st;
     if (n == 0) return ok();
-    const SpanList sp = {
+    const Span sp[] = {
         {"slot_list", slot_list, static_cast<size_t>(n) * 4, false, 4}, {"page_table", page_table, table_bytes(slots, max_pages), true, 4},
         {"lens", lens, static_cast<size_t>(slots) * 4, true, 4}, {"refs", refs, static_cast<size_t>(num_pages) * 4, true, 4},
     };
@@ -1027,19 +1009,21 @@ int kda_cache_fork(int32_t n, const int32_t* src, const int32_t* dst, int32_t Hk
                    int32_t x_dtype, void* k_cache, void* v_cache, int32_t num_pages, int32_t page_size,
                    int32_t* page_table, int32_t slots, int32_t max_pages, int32_t* lens, int32_t* refs,
                    int32_t* status, void* workspace, size_t workspace_bytes, void* stream) {
-    SpanList sp;
     kda::CacheArgs c;
-    int st = cache_args(Hkv, dk, dv, x_dtype, k_cache, v_cache, num_pages, page_size, page_table, slots, max_pages, lens, refs, sp, c);
+    int st = cache_args(Hkv, dk, dv, x_dtype, k_cache, v_cache, num_pages, page_size, page_table, slots, max_pages, lens, refs, c);
     if (st != KDA_OK) return st;
     st = check_entries(n);
     if (st != KDA_OK) return st;
     if (n == 0) return ok();
-    sp.push_back({"lens", lens, static_cast<size_t>(slots) * 4, true, 4});
-    sp.push_back({"refs", refs, static_cast<size_t>(num_pages) * 4, true, 4});
-    sp.push_back({"src", src, static_cast<size_t>(n) * 4, false, 4});
-    sp.push_back({"dst", dst, static_cast<size_t>(n) * 4, false, 4});
-    sp.push_back({"status", status, status ? static_cast<size_t>(n) * 4 : 0, true, 4});
-    st = check_workspace("kda_cache_fork", workspace_bytes, kda_cache_workspace_bytes(num_pages, slots, n), workspace, sp);
+    const size_t need = kda_cache_workspace_bytes(num_pages, slots, n);
+    const Span sp[] = {
+        {"k_cache", k_cache, pool_bytes(c, dk), true}, {"v_cache", v_cache, pool_bytes(c, dv), true},
+        {"page_table", page_table, table_bytes(slots, max_pages), true, 4}, {"lens", lens, static_cast<size_t>(slots) * 4, true, 4},
+        {"refs", refs, static_cast<size_t>(num_pages) * 4, true, 4}, {"src", src, static_cast<size_t>(n) * 4, false, 4},
+        {"dst", dst, static_cast<size_t>(n) * 4, false, 4}, {"status", status, status ? static_cast<size_t>(n) * 4 : 0, true, 4},
+        {"workspace", workspace, need, true},
+    };
+    st = check_workspace("kda_cache_fork", workspace_bytes, need, workspace);
     if (st == KDA_OK) st = check_spans(sp);
     if (st != KDA_OK) return st;
     const hipError_t e = kda::launch_cache_fork(c, n, src, dst, status, workspace, static_cast<hipStream_t>(stream));
@@ -1056,12 +1040,14 @@ int kda_cache_reserve(int32_t n, const int32_t* slot_list, const int32_t* new_le
     st = check_entries(n);
     if (st != KDA_OK) return st;
     if (n == 0) return ok();
-    SpanList sp = {
+    const size_t need = kda_cache_workspace_bytes(num_pages, slots, n);
+    const Span sp[] = {
         {"slot_list", slot_list, static_cast<size_t>(n) * 4, false, 4}, {"new_lens", new_lens, static_cast<size_t>(n) * 4, false, 4},
         {"page_table", page_table, table_bytes(slots, max_pages), true, 4}, {"lens", lens, static_cast<size_t>(slots) * 4, false, 4},
         {"refs", refs, static_cast<size_t>(num_pages) * 4, true, 4}, {"status", status, status ? static_cast<size_t>(n) * 4 : 0, true, 4},
+        {"workspace", workspace, need, true},
     };
-    st = check_workspace("kda_cache_reserve", workspace_bytes, kda_cache_workspace_bytes(num_pages, slots, n), workspace, sp);
+    st = check_workspace("kda_cache_reserve", workspace_bytes, need, workspace);
     if (st == KDA_OK) st = check_spans(sp);
     if (st != KDA_OK) return st;
     kda::CacheArgs c{};
@@ -1075,13 +1061,16 @@ int kda_cache_reserve(int32_t n, const int32_t* slot_list, const int32_t* new_le
 int kda_cache_compact(int32_t Hkv, int32_t dk, int32_t dv, int32_t x_dtype, void* k_cache, void* v_cache,
                       int32_t num_pages, int32_t page_size, int32_t* page_table, int32_t slots, int32_t max_pages,
                       int32_t* refs, int32_t* live, void* workspace, size_t workspace_bytes, void* stream) {
-    SpanList sp;
     kda::CacheArgs c;
-    int st = cache_args(Hkv, dk, dv, x_dtype, k_cache, v_cache, num_pages, page_size, page_table, slots, max_pages, nullptr, refs, sp, c);
+    int st = cache_args(Hkv, dk, dv, x_dtype, k_cache, v_cache, num_pages, page_size, page_table, slots, max_pages, nullptr, refs, c);
     if (st != KDA_OK) return st;
-    sp.push_back({"refs", refs, static_cast<size_t>(num_pages) * 4, true, 4});
-    sp.push_back({"live", live, 4, true, 4});
-    st = check_workspace("kda_cache_compact", workspace_bytes, kda_cache_workspace_bytes(num_pages, slots, 0), workspace, sp);
+    const size_t need = kda_cache_workspace_bytes(num_pages, slots, 0);
+    const Span sp[] = {
+        {"k_cache", k_cache, pool_bytes(c, dk), true}, {"v_cache", v_cache, pool_bytes(c, dv), true},
+        {"page_table", page_table, table_bytes(slots, max_pages), true, 4}, {"refs", refs, static_cast<size_t>(num_pages) * 4, true, 4},
+        {"live", live, 4, true, 4}, {"workspace", workspace, need, true},
+    };
+    st = check_workspace("kda_cache_compact", workspace_bytes, need, workspace);
     if (st == KDA_OK) st = check_spans(sp);
     if (st != KDA_OK) return st;
     const hipError_t e = kda::launch_cache_compact(c, live, workspace, static_cast<hipStream_t>(stream));
@@ -1097,7 +1086,7 @@ int kda_cache_copy(void* pool, int64_t row_bytes, int32_t rows, const int32_t* s
     if (rows > 0 && row_bytes > (int64_t(1) << 46) / rows)
         return fail(KDA_ERR_INVALID_ARGUMENT, "row_bytes=%lld x rows=%d is out of range", (long long)row_bytes, rows);
     if (n == 0 || row_bytes == 0 || rows == 0) return ok();
-    const SpanList sp = {
+    const Span sp[] = {
         {"pool", pool, static_cast<size_t>(row_bytes) * rows, true}, {"src", src, static_cast<size_t>(n) * 4, false, 4},
         {"dst", dst, static_cast<size_t>(n) * 4, false, 4},
     };
