@@ -448,8 +448,9 @@ __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV>::kWaves), (sizeof(T) == 
 // Joins the parts, kWaves waves to a row: thread s of the row weighs part s,
 // then the row's half waves take the parts in turn, four channels a lane, and
 // their sums are added in LDS.  Many rows of few parts take a wave each (16,384
-// rows of 4 parts: 15.5 us, with four waves each 33 us); few rows of many parts
-// four (128 rows of 128 parts: 9 us, with one wave each 59 us).
+// rows of 2 parts: 15 us, with four waves each 29 us; 4,096 of 16: 8 against
+// 12); few rows of many parts four (512 rows of 32 parts: 7 us, with one wave
+// each 8.3; 128 of 64: 7.3 against 11.5).
 constexpr int kJoinThreads = 256;
 constexpr int kFewParts = 16;
 static_assert(kMaxSplits <= kJoinThreads && kFewParts <= 64, "a thread per part");
@@ -543,11 +544,15 @@ TreePlan tree_plan(int B, int T, int H, int Hkv, int64_t max_ctx) {
     p.blocks = static_cast<int>((rows + 31) / 32);
     const int64_t units = static_cast<int64_t>(B) * Hkv * p.blocks;
     const int64_t tiles = (max_ctx + kKeys - 1) / kKeys + (T + kKeys - 1) / kKeys;
-    // Two workgroups fit a CU.  The parts of one sequence are equally long:
-    // one round of them (262,144 tokens: 193 us and 8 us to join them, against
-    // 198 and 9 us in two rounds).  Sequences differ, and two rounds let the
-    // short ones fill up behind the long (64 of up to 8,000 tokens: 219 us
-    // against 239 us in one).
+    // Of bf16 at up to 128 channels two workgroups fit a CU.  The parts of one
+    // sequence are equally long: one round of them (262,144 tokens: 193 us and
+    // 8 us to join them, against 198 and 9 us in two rounds).  Sequences differ,
+    // and two rounds let the short ones fill up behind the long (64 of up to
+    // 8,000 tokens: 219 us against 239 us in one).  The other forms fit a CU
+    // once and take the same numbers, in twice the rounds: 32 sequences of up
+    // to 8,000 tokens 366 us in fp32 at 192 channels and 119 in bf16, with half
+    // as many parts 433 and 124; one of 100,000 tokens 289 and 100, with half
+    // as many 284 and 96.
     const int64_t want = B == 1 ? kWantUnitsOfOne : kWantUnits;
     int64_t s = (want + units - 1) / units;
     if (s > tiles / 8) s = tiles / 8;  // two tiles a wave at least

@@ -442,7 +442,9 @@ int kda_spec_verify(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv,
  *    dk = 192 with dv = 128 (else KDA_ERR_UNSUPPORTED).
  *  - Types: x_dtype (fp32 or bf16) for every tensor without another type.
  *    Scores, softmax statistics and sums are fp32; with bf16 the weights are
- *    rounded to bf16 for their product with the values.
+ *    rounded to bf16 for their product with the values, and in the gradients
+ *    also the scores' gradients (for their products with q and k) and the gated
+ *    output gradient dy * sigmoid(z).  With fp32 nothing is rounded to less.
  *  - scale multiplies q . k; positive and finite.
  *  - out_gate: NULL, or logits z of out's shape: out = o * sigmoid(z).
  *  - A row that attends nothing gets 0, and -infinity as its lse.  A row that
