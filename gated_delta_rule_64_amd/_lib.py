@@ -75,6 +75,19 @@ PROTOTYPES.update({
     "kda_cache_reserve": (ctypes.c_int, [_i32, _vp, _vp, _i32, _i32] + _TABLE + [_vp] * 3 + _WORK),
     "kda_cache_compact": (ctypes.c_int, [_i32] * 4 + _POOLS + _TABLE + [_vp, _vp] + _WORK),
     "kda_cache_copy": (ctypes.c_int, [_vp, _i64, _i32, _vp, _vp, _i32, _vp]),
+    "kda_attn_window_prefill": (ctypes.c_int, [_i64, _i32, _i32, _i32, _i32, _vp, _i32, _i32, _f32, _i32, _i32] + [_vp] * 6 + [_vp]),
+    "kda_attn_window_backward_workspace_bytes": (_sz, [_i64] + [_i32] * 9),
+    "kda_attn_window_backward_max_workspace_bytes": (_sz, [_i64] + [_i32] * 8),
+    "kda_attn_window_prefill_backward": (ctypes.c_int, [_i64, _i32, _i32, _i32, _i32, _vp, _i32, _i32, _f32, _i32, _i32] +
+                                         [_vp] * 11 + _WORK),
+    "kda_attn_window_tree_workspace_bytes": (_sz, [_i32] * 7 + [_i64, _i32, _i32]),
+    "kda_attn_window_tree_max_workspace_bytes": (_sz, [_i32] * 7 + [_i64, _i32, _i32]),
+    "kda_attn_window_tree": (ctypes.c_int, [_i32] * 7 + [_f32, _i32, _i32] + [_vp] * 5 + _POOLS + _TABLE + [_vp] * 4 + _WORK),
+    "kda_cache_weigh_workspace_bytes": (_sz, [_i64, _i32, _i32, _i32, _i64]),
+    "kda_cache_weigh": (ctypes.c_int, [_i64, _i32, _vp, _i64, _vp] + [_i32] * 4 + [_f32, _i32, _i32, _vp, _vp, _vp, _i32, _i32] + _TABLE +
+                        [_vp] * 3 + _WORK),
+    "kda_cache_evict_workspace_bytes": (_sz, [_i32, _i32]),
+    "kda_cache_evict": (ctypes.c_int, [_i32, _vp] + [_i32] * 7 + _POOLS + _TABLE + [_vp] * 5 + _WORK),
 })
 
 

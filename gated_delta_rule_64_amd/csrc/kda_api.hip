@@ -769,15 +769,40 @@ int check_workspace(const char* call, size_t have, size_t need, const void* p) {
     return KDA_OK;
 }
 
-}  // namespace
+// What a row attends of the tokens before it: all, or with kda_attn_window_* the
+// last `window` and the first `sinks`.
+struct View {
+    bool bounded;
+    int32_t window, sinks;
+    const char* call(const char* whole, const char* of_window) const { return bounded ? of_window : whole; }
+};
+constexpr View kWhole{false, 0, 0};
 
-extern "C" {
+constexpr int64_t kMostWindowed = int64_t(1) << 30;  // places and windows add up in 32 bits
 
-int kda_attn_prefill(int64_t T_tot, int32_t H, int32_t Hkv, int32_t dk, int32_t dv, const int32_t* cu_seqlens,
+// tokens: as many as a sequence of the call can have.
+int check_view(const View& view, int64_t tokens, const char* name) {
+    if (!view.bounded) return KDA_OK;
+    if (view.window < 1) return fail(KDA_ERR_INVALID_ARGUMENT, "window=%d must be >= 1", view.window);
+    if (view.sinks < 0) return fail(KDA_ERR_INVALID_ARGUMENT, "sinks=%d is negative", view.sinks);
+    if (tokens >= kMostWindowed) return fail(KDA_ERR_UNSUPPORTED, "%s=%lld is not below 2^30 with a window", name, (long long)tokens);
+    return KDA_OK;
+}
+
+size_t backward_need(int64_t T, int32_t N, int32_t H, int32_t Hkv, int32_t dk, int32_t dv, int32_t x_dtype, bool gate, const View& view) {
+    return kda::attn_backward_workspace_bytes(T, N, H, Hkv, dk, dv, static_cast<kda::DT>(x_dtype), gate, view.window, view.sinks);
+}
+
+size_t tree_need(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t dv, int64_t max_context, const View& view) {
+    return kda::attn_tree_workspace_bytes(B, T, H, Hkv, dv, view.bounded ? kda::window_reach(max_context, view.window, view.sinks) : max_context);
+}
+
+int attn_prefill_impl(const View& view, int64_t T_tot, int32_t H, int32_t Hkv, int32_t dk, int32_t dv, const int32_t* cu_seqlens,
                      int32_t N, int32_t x_dtype, float scale, const void* q, const void* k, const void* v,
                      const void* out_gate, void* out, float* lse, void* stream) {
     int st = check_heads(H, Hkv, dk, dv, x_dtype, scale);
     if (st == KDA_OK) st = check_packed(T_tot, N, cu_seqlens, H);
+    if (st == KDA_OK) st = check_view(view, T_tot, "T_tot");
     if (st != KDA_OK) return st;
     const size_t xs = dsize(x_dtype), T = static_cast<size_t>(T_tot);
     const Span sp[] = {
@@ -791,10 +816,111 @@ int kda_attn_prefill(int64_t T_tot, int32_t H, int32_t Hkv, int32_t dk, int32_t 
     hipStream_t s = static_cast<hipStream_t>(stream);
     st = debug_check_cu_within(cu_seqlens, N, T_tot, s);
     if (st != KDA_OK) return st;
-    const kda::AttnArgs a{T_tot, H, Hkv, dk, dv, N, cu_seqlens, static_cast<kda::DT>(x_dtype), scale, q, k, v, out_gate, out, lse};
+    const kda::AttnArgs a{T_tot, H, Hkv, dk, dv, N, cu_seqlens, static_cast<kda::DT>(x_dtype), scale, q, k, v, out_gate, out, lse,
+                          view.window, view.sinks};
     const hipError_t e = kda::launch_attn_prefill(a, s);
     if (e != hipSuccess) return hip_fail(e, "attention prefill launch");
     return ok();
+}
+
+int attn_backward_impl(const View& view, int64_t T_tot, int32_t H, int32_t Hkv, int32_t dk, int32_t dv,
+                              const int32_t* cu_seqlens, int32_t N, int32_t x_dtype, float scale, const void* q,
+                              const void* k, const void* v, const void* out_gate, const void* out, const float* lse,
+                              const void* dy, void* grad_q, void* grad_k, void* grad_v, void* grad_out_gate,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+    int st = check_heads(H, Hkv, dk, dv, x_dtype, scale);
+    if (st == KDA_OK) st = check_packed(T_tot, N, cu_seqlens, 2 * static_cast<int64_t>(H));
+    if (st == KDA_OK) st = check_view(view, T_tot, "T_tot");
+    if (st != KDA_OK) return st;
+    if (T_tot * H >= 16 * kMostGroups)  // the kernel of the rows takes 16 a workgroup
+        return fail(KDA_ERR_UNSUPPORTED, "T_tot=%lld, H=%d: rows for more than 2^24 workgroups", (long long)T_tot, H);
+    if ((out_gate != nullptr) != (grad_out_gate != nullptr) && T_tot > 0)
+        return fail(KDA_ERR_INVALID_ARGUMENT, "grad_out_gate is required exactly when out_gate is given");
+    const size_t xs = dsize(x_dtype), T = static_cast<size_t>(T_tot);
+    const size_t need = backward_need(T_tot, N, H, Hkv, dk, dv, x_dtype, out_gate != nullptr, view);
+    const Span sp[] = {
+        {"q", q, T * H * dk * xs, false}, {"k", k, T * Hkv * dk * xs, false}, {"v", v, T * Hkv * dv * xs, false},
+        {"out_gate", out_gate, out_gate ? T * H * dv * xs : 0, false}, {"out", out, T * H * dv * xs, false},
+        {"lse", lse, T * H * 4, false, 4}, {"dy", dy, T * H * dv * xs, false},
+        {"cu_seqlens", cu_seqlens, cu_seqlens ? (static_cast<size_t>(N) + 1) * 4 : 0, false, 4},
+        {"grad_q", grad_q, T * H * dk * xs, true}, {"grad_k", grad_k, T * Hkv * dk * xs, true},
+        {"grad_v", grad_v, T * Hkv * dv * xs, true}, {"grad_out_gate", grad_out_gate, grad_out_gate ? T * H * dv * xs : 0, true},
+        {"workspace", workspace, need, true},
+    };
+    st = check_workspace(view.call("kda_attn_prefill_backward", "kda_attn_window_prefill_backward"), workspace_bytes, need, workspace);
+    if (st == KDA_OK) st = check_spans(sp);
+    if (st != KDA_OK) return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    st = debug_check_cu_within(cu_seqlens, N, T_tot, s);
+    if (st != KDA_OK) return st;
+    kda::AttnBackwardArgs a{};
+    a.f = kda::AttnArgs{T_tot, H, Hkv, dk, dv, N, cu_seqlens, static_cast<kda::DT>(x_dtype), scale, q, k, v, out_gate,
+                        const_cast<void*>(out), const_cast<float*>(lse), view.window, view.sinks};
+    a.dy = dy; a.dq = grad_q; a.dk = grad_k; a.dv = grad_v; a.dz = grad_out_gate; a.ws = workspace;
+    const hipError_t e = kda::launch_attn_prefill_backward(a, s);
+    if (e != hipSuccess) return hip_fail(e, "attention backward launch");
+    return ok();
+}
+
+int attn_tree_impl(const View& view, int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t dk, int32_t dv, int32_t x_dtype, float scale,
+                  const void* q, const void* k_new, const void* v_new, const int64_t* tree_mask, const void* out_gate,
+                  const void* k_cache, const void* v_cache, int32_t num_pages, int32_t page_size,
+                  const int32_t* page_table, int32_t slots, int32_t max_pages, const int32_t* lens,
+                  const int32_t* slot_indices, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                  void* stream) {
+    int st = check_heads(H, Hkv, dk, dv, x_dtype, scale);
+    int shift = 0;
+    if (st == KDA_OK) st = check_cache(num_pages, page_size, slots, max_pages, shift);
+    if (st == KDA_OK) st = check_view(view, static_cast<int64_t>(max_pages) << shift, "max_pages x page_size");
+    if (st != KDA_OK) return st;
+    if (B < 0) return fail(KDA_ERR_INVALID_ARGUMENT, "B=%d is negative", B);
+    if (T < 0 || T > kda::kTreeMaxTokens) return fail(KDA_ERR_INVALID_ARGUMENT, "T=%d out of range [0, %d]", T, kda::kTreeMaxTokens);
+    if (slot_indices == nullptr && B != slots && B > 0)
+        return fail(KDA_ERR_INVALID_ARGUMENT, "slot_indices is NULL but slots=%d is not B=%d", slots, B);
+    if (static_cast<int64_t>(B) * T * H >= (int64_t(1) << 30))
+        return fail(KDA_ERR_UNSUPPORTED, "B x T x H = %lld rows are not below 2^30", static_cast<long long>(B) * T * H);
+    if (kda::attn_tree_groups(B, T, H, Hkv) >= kMostGroups)
+        return fail(KDA_ERR_UNSUPPORTED, "B=%d, T=%d, H=%d, Hkv=%d: %lld workgroups are not below 2^24", B, T, H, Hkv,
+                    static_cast<long long>(kda::attn_tree_groups(B, T, H, Hkv)));
+    const size_t xs = dsize(x_dtype), BT = static_cast<size_t>(B) * T;
+    const size_t page = static_cast<size_t>(num_pages) * Hkv * page_size;
+    const bool any = BT > 0;
+    const size_t need = tree_need(B, T, H, Hkv, dv, static_cast<int64_t>(max_pages) << shift, view);
+    const Span sp[] = {
+        {"q", q, BT * H * dk * xs, false}, {"k_new", k_new, BT * Hkv * dk * xs, false}, {"v_new", v_new, BT * Hkv * dv * xs, false},
+        {"tree_mask", tree_mask, tree_mask ? BT * 8 : 0, false, 8}, {"out_gate", out_gate, out_gate ? BT * H * dv * xs : 0, false},
+        {"k_cache", k_cache, any ? page * dk * xs : 0, false}, {"v_cache", v_cache, any ? page * dv * xs : 0, false},
+        {"page_table", page_table, any ? table_bytes(slots, max_pages) : 0, false, 4},
+        {"lens", lens, any ? static_cast<size_t>(slots) * 4 : 0, false, 4},
+        {"slot_indices", slot_indices, slot_indices ? static_cast<size_t>(B) * 4 : 0, false, 4},
+        {"out", out, BT * H * dv * xs, true}, {"lse", lse, lse ? BT * H * 4 : 0, true, 4},
+        {"workspace", workspace, need, true},
+    };
+    st = check_workspace(view.call("kda_attn_tree", "kda_attn_window_tree"), workspace_bytes, need, workspace);
+    if (st == KDA_OK) st = check_spans(sp);
+    if (st != KDA_OK) return st;
+    kda::TreeArgs a{B, T, H, Hkv, dk, dv, static_cast<kda::DT>(x_dtype), scale, q, k_new, v_new, out_gate, tree_mask,
+                    k_cache, v_cache, num_pages, shift, page_table, slots, max_pages, lens, slot_indices, out, lse, workspace,
+                    view.window, view.sinks};
+    const hipError_t e = kda::launch_attn_tree(a, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(e, "tree attention launch");
+    return ok();
+}
+
+}  // namespace
+
+extern "C" {
+
+int kda_attn_prefill(int64_t T_tot, int32_t H, int32_t Hkv, int32_t dk, int32_t dv, const int32_t* cu_seqlens,
+                     int32_t N, int32_t x_dtype, float scale, const void* q, const void* k, const void* v,
+                     const void* out_gate, void* out, float* lse, void* stream) {
+    return attn_prefill_impl(kWhole, T_tot, H, Hkv, dk, dv, cu_seqlens, N, x_dtype, scale, q, k, v, out_gate, out, lse, stream);
+}
+
+int kda_attn_window_prefill(int64_t T_tot, int32_t H, int32_t Hkv, int32_t dk, int32_t dv, const int32_t* cu_seqlens,
+                            int32_t N, int32_t x_dtype, float scale, int32_t window, int32_t sinks, const void* q,
+                            const void* k, const void* v, const void* out_gate, void* out, float* lse, void* stream) {
+    return attn_prefill_impl(View{true, window, sinks}, T_tot, H, Hkv, dk, dv, cu_seqlens, N, x_dtype, scale, q, k, v, out_gate, out, lse, stream);
 }
 
 size_t kda_attn_backward_workspace_bytes(int64_t T_tot, int32_t N, int32_t H, int32_t Hkv, int32_t dk, int32_t dv,
@@ -816,37 +942,36 @@ int kda_attn_prefill_backward(int64_t T_tot, int32_t H, int32_t Hkv, int32_t dk,
                               const void* k, const void* v, const void* out_gate, const void* out, const float* lse,
                               const void* dy, void* grad_q, void* grad_k, void* grad_v, void* grad_out_gate,
                               void* workspace, size_t workspace_bytes, void* stream) {
-    int st = check_heads(H, Hkv, dk, dv, x_dtype, scale);
-    if (st == KDA_OK) st = check_packed(T_tot, N, cu_seqlens, 2 * static_cast<int64_t>(H));
-    if (st != KDA_OK) return st;
-    if (T_tot * H >= 16 * kMostGroups)  // the kernel of the rows takes 16 a workgroup
-        return fail(KDA_ERR_UNSUPPORTED, "T_tot=%lld, H=%d: rows for more than 2^24 workgroups", (long long)T_tot, H);
-    if ((out_gate != nullptr) != (grad_out_gate != nullptr) && T_tot > 0)
-        return fail(KDA_ERR_INVALID_ARGUMENT, "grad_out_gate is required exactly when out_gate is given");
-    const size_t xs = dsize(x_dtype), T = static_cast<size_t>(T_tot);
-    const size_t need = kda_attn_backward_workspace_bytes(T_tot, N, H, Hkv, dk, dv, x_dtype, out_gate != nullptr);
-    const Span sp[] = {
-        {"q", q, T * H * dk * xs, false}, {"k", k, T * Hkv * dk * xs, false}, {"v", v, T * Hkv * dv * xs, false},
-        {"out_gate", out_gate, out_gate ? T * H * dv * xs : 0, false}, {"out", out, T * H * dv * xs, false},
-        {"lse", lse, T * H * 4, false, 4}, {"dy", dy, T * H * dv * xs, false},
-        {"cu_seqlens", cu_seqlens, cu_seqlens ? (static_cast<size_t>(N) + 1) * 4 : 0, false, 4},
-        {"grad_q", grad_q, T * H * dk * xs, true}, {"grad_k", grad_k, T * Hkv * dk * xs, true},
-        {"grad_v", grad_v, T * Hkv * dv * xs, true}, {"grad_out_gate", grad_out_gate, grad_out_gate ? T * H * dv * xs : 0, true},
-        {"workspace", workspace, need, true},
-    };
-    st = check_workspace("kda_attn_prefill_backward", workspace_bytes, need, workspace);
-    if (st == KDA_OK) st = check_spans(sp);
-    if (st != KDA_OK) return st;
-    hipStream_t s = static_cast<hipStream_t>(stream);
-    st = debug_check_cu_within(cu_seqlens, N, T_tot, s);
-    if (st != KDA_OK) return st;
-    kda::AttnBackwardArgs a{};
-    a.f = kda::AttnArgs{T_tot, H, Hkv, dk, dv, N, cu_seqlens, static_cast<kda::DT>(x_dtype), scale, q, k, v, out_gate,
-                        const_cast<void*>(out), const_cast<float*>(lse)};
-    a.dy = dy; a.dq = grad_q; a.dk = grad_k; a.dv = grad_v; a.dz = grad_out_gate; a.ws = workspace;
-    const hipError_t e = kda::launch_attn_prefill_backward(a, s);
-    if (e != hipSuccess) return hip_fail(e, "attention backward launch");
-    return ok();
+    return attn_backward_impl(kWhole, T_tot, H, Hkv, dk, dv, cu_seqlens, N, x_dtype, scale, q, k, v, out_gate, out, lse, dy, grad_q, grad_k,
+                              grad_v, grad_out_gate, workspace, workspace_bytes, stream);
+}
+
+namespace {
+bool window_sizes(int64_t T, int32_t N, int32_t H, int32_t Hkv, int32_t dk, int32_t dv, int32_t x_dtype, int32_t window, int32_t sinks) {
+    return T >= 0 && T < kMostWindowed && N >= 1 && H >= 1 && H <= 65535 && Hkv >= 1 && H % Hkv == 0 && kda::attn_head_sizes(dk, dv) &&
+           valid_dtype(x_dtype) && window >= 1 && sinks >= 0;
+}
+}  // namespace
+
+size_t kda_attn_window_backward_workspace_bytes(int64_t T_tot, int32_t N, int32_t H, int32_t Hkv, int32_t dk, int32_t dv,
+                                                int32_t x_dtype, int32_t with_gate, int32_t window, int32_t sinks) {
+    if (!window_sizes(T_tot, N, H, Hkv, dk, dv, x_dtype, window, sinks)) return 0;
+    return backward_need(T_tot, N, H, Hkv, dk, dv, x_dtype, with_gate != 0, View{true, window, sinks});
+}
+
+size_t kda_attn_window_backward_max_workspace_bytes(int64_t max_T_tot, int32_t H, int32_t Hkv, int32_t dk, int32_t dv,
+                                                    int32_t x_dtype, int32_t with_gate, int32_t window, int32_t sinks) {
+    if (!window_sizes(max_T_tot, 1, H, Hkv, dk, dv, x_dtype, window, sinks)) return 0;
+    return kda::attn_backward_max_workspace_bytes(max_T_tot, H, Hkv, dk, dv, static_cast<kda::DT>(x_dtype), with_gate != 0, window, sinks);
+}
+
+int kda_attn_window_prefill_backward(int64_t T_tot, int32_t H, int32_t Hkv, int32_t dk, int32_t dv,
+                                     const int32_t* cu_seqlens, int32_t N, int32_t x_dtype, float scale, int32_t window,
+                                     int32_t sinks, const void* q, const void* k, const void* v, const void* out_gate,
+                                     const void* out, const float* lse, const void* dy, void* grad_q, void* grad_k,
+                                     void* grad_v, void* grad_out_gate, void* workspace, size_t workspace_bytes, void* stream) {
+    return attn_backward_impl(View{true, window, sinks}, T_tot, H, Hkv, dk, dv, cu_seqlens, N, x_dtype, scale, q, k, v, out_gate, out, lse, dy,
+                              grad_q, grad_k, grad_v, grad_out_gate, workspace, workspace_bytes, stream);
 }
 
 namespace {
@@ -874,41 +999,31 @@ int kda_attn_tree(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t dk, int3
                   const int32_t* page_table, int32_t slots, int32_t max_pages, const int32_t* lens,
                   const int32_t* slot_indices, void* out, float* lse, void* workspace, size_t workspace_bytes,
                   void* stream) {
-    int st = check_heads(H, Hkv, dk, dv, x_dtype, scale);
-    int shift = 0;
-    if (st == KDA_OK) st = check_cache(num_pages, page_size, slots, max_pages, shift);
-    if (st != KDA_OK) return st;
-    if (B < 0) return fail(KDA_ERR_INVALID_ARGUMENT, "B=%d is negative", B);
-    if (T < 0 || T > kda::kTreeMaxTokens) return fail(KDA_ERR_INVALID_ARGUMENT, "T=%d out of range [0, %d]", T, kda::kTreeMaxTokens);
-    if (slot_indices == nullptr && B != slots && B > 0)
-        return fail(KDA_ERR_INVALID_ARGUMENT, "slot_indices is NULL but slots=%d is not B=%d", slots, B);
-    if (static_cast<int64_t>(B) * T * H >= (int64_t(1) << 30))
-        return fail(KDA_ERR_UNSUPPORTED, "B x T x H = %lld rows are not below 2^30", static_cast<long long>(B) * T * H);
-    if (kda::attn_tree_groups(B, T, H, Hkv) >= kMostGroups)
-        return fail(KDA_ERR_UNSUPPORTED, "B=%d, T=%d, H=%d, Hkv=%d: %lld workgroups are not below 2^24", B, T, H, Hkv,
-                    static_cast<long long>(kda::attn_tree_groups(B, T, H, Hkv)));
-    const size_t xs = dsize(x_dtype), BT = static_cast<size_t>(B) * T;
-    const size_t page = static_cast<size_t>(num_pages) * Hkv * page_size;
-    const bool any = BT > 0;
-    const size_t need = kda_attn_tree_workspace_bytes(B, T, H, Hkv, dk, dv, x_dtype, static_cast<int64_t>(max_pages) << shift);
-    const Span sp[] = {
-        {"q", q, BT * H * dk * xs, false}, {"k_new", k_new, BT * Hkv * dk * xs, false}, {"v_new", v_new, BT * Hkv * dv * xs, false},
-        {"tree_mask", tree_mask, tree_mask ? BT * 8 : 0, false, 8}, {"out_gate", out_gate, out_gate ? BT * H * dv * xs : 0, false},
-        {"k_cache", k_cache, any ? page * dk * xs : 0, false}, {"v_cache", v_cache, any ? page * dv * xs : 0, false},
-        {"page_table", page_table, any ? table_bytes(slots, max_pages) : 0, false, 4},
-        {"lens", lens, any ? static_cast<size_t>(slots) * 4 : 0, false, 4},
-        {"slot_indices", slot_indices, slot_indices ? static_cast<size_t>(B) * 4 : 0, false, 4},
-        {"out", out, BT * H * dv * xs, true}, {"lse", lse, lse ? BT * H * 4 : 0, true, 4},
-        {"workspace", workspace, need, true},
-    };
-    st = check_workspace("kda_attn_tree", workspace_bytes, need, workspace);
-    if (st == KDA_OK) st = check_spans(sp);
-    if (st != KDA_OK) return st;
-    kda::TreeArgs a{B, T, H, Hkv, dk, dv, static_cast<kda::DT>(x_dtype), scale, q, k_new, v_new, out_gate, tree_mask,
-                    k_cache, v_cache, num_pages, shift, page_table, slots, max_pages, lens, slot_indices, out, lse, workspace};
-    const hipError_t e = kda::launch_attn_tree(a, static_cast<hipStream_t>(stream));
-    if (e != hipSuccess) return hip_fail(e, "tree attention launch");
-    return ok();
+    return attn_tree_impl(kWhole, B, T, H, Hkv, dk, dv, x_dtype, scale, q, k_new, v_new, tree_mask, out_gate, k_cache, v_cache, num_pages,
+                          page_size, page_table, slots, max_pages, lens, slot_indices, out, lse, workspace, workspace_bytes, stream);
+}
+
+size_t kda_attn_window_tree_workspace_bytes(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t dk, int32_t dv,
+                                            int32_t x_dtype, int64_t max_context, int32_t window, int32_t sinks) {
+    if (!tree_sizes(B, T, H, Hkv, dk, dv, x_dtype, max_context) || max_context >= kMostWindowed || window < 1 || sinks < 0) return 0;
+    return tree_need(B, T, H, Hkv, dv, max_context, View{true, window, sinks});
+}
+
+size_t kda_attn_window_tree_max_workspace_bytes(int32_t max_B, int32_t max_T, int32_t H, int32_t Hkv, int32_t dk, int32_t dv,
+                                                int32_t x_dtype, int64_t max_context, int32_t window, int32_t sinks) {
+    if (!tree_sizes(max_B, max_T, H, Hkv, dk, dv, x_dtype, max_context) || max_context >= kMostWindowed || window < 1 || sinks < 0) return 0;
+    return kda::attn_tree_max_workspace_bytes(max_B, max_T, H, Hkv, dv, kda::window_reach(max_context, window, sinks));
+}
+
+int kda_attn_window_tree(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t dk, int32_t dv, int32_t x_dtype, float scale,
+                         int32_t window, int32_t sinks, const void* q, const void* k_new, const void* v_new,
+                         const int64_t* tree_mask, const void* out_gate, const void* k_cache, const void* v_cache,
+                         int32_t num_pages, int32_t page_size, const int32_t* page_table, int32_t slots, int32_t max_pages,
+                         const int32_t* lens, const int32_t* slot_indices, void* out, float* lse, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+    return attn_tree_impl(View{true, window, sinks}, B, T, H, Hkv, dk, dv, x_dtype, scale, q, k_new, v_new, tree_mask, out_gate, k_cache,
+                          v_cache, num_pages, page_size, page_table, slots, max_pages, lens, slot_indices, out, lse, workspace,
+                          workspace_bytes, stream);
 }
 
 }  // extern "C"
@@ -1097,6 +1212,103 @@ int kda_cache_copy(void* pool, int64_t row_bytes, int32_t rows, const int32_t* s
     if (st != KDA_OK) return st;
     const hipError_t e = kda::launch_cache_copy(pool, row_bytes, rows, src, dst, n, s);
     if (e != hipSuccess) return hip_fail(e, "cache copy launch");
+    return ok();
+}
+
+size_t kda_cache_weigh_workspace_bytes(int64_t T_tot, int32_t N, int32_t H, int32_t Hkv, int64_t max_context) {
+    if (T_tot < 0 || T_tot >= kMostWindowed || N < 1 || H < 1 || H > 65535 || Hkv < 1 || H % Hkv != 0 || max_context < 1 ||
+        max_context >= kMostWindowed)
+        return 0;
+    return kda::cache_weigh_workspace_bytes(T_tot, N, H, Hkv, max_context);
+}
+
+int kda_cache_weigh(int64_t T_tot, int32_t N, const int32_t* cu_seqlens, int64_t src_rows, const int32_t* rows, int32_t H,
+                    int32_t Hkv, int32_t dk, int32_t x_dtype, float scale, int32_t window, int32_t sinks, const void* q,
+                    const float* lse, const void* k_cache, int32_t num_pages, int32_t page_size, const int32_t* page_table,
+                    int32_t slots, int32_t max_pages, const int32_t* lens, const int32_t* slot_indices, float* weights,
+                    void* workspace, size_t workspace_bytes, void* stream) {
+    const int32_t dv = dk == 192 ? 128 : dk;
+    int st = check_heads(H, Hkv, dk, dv, x_dtype, scale);
+    if (st != KDA_OK) return st;
+    if (T_tot < 0 || T_tot >= (int64_t(1) << 31)) return fail(KDA_ERR_INVALID_ARGUMENT, "T_tot=%lld out of range [0, 2^31)", (long long)T_tot);
+    if (T_tot >= kMostWindowed) return fail(KDA_ERR_UNSUPPORTED, "T_tot=%lld is not below 2^30", (long long)T_tot);
+    if (N < 1) return fail(KDA_ERR_INVALID_ARGUMENT, "N=%d must be >= 1", N);
+    if (N >= kMostGroups / 2) return fail(KDA_ERR_UNSUPPORTED, "N=%d: the workgroups are not below 2^24", N);
+    if (cu_seqlens == nullptr && N != 1) return fail(KDA_ERR_INVALID_ARGUMENT, "cu_seqlens is NULL but N=%d", N);
+    if (slot_indices == nullptr && slots < N)
+        return fail(KDA_ERR_INVALID_ARGUMENT, "slot_indices is NULL but slots=%d is below N=%d", slots, N);
+    if (src_rows < 0 || src_rows >= (int64_t(1) << 31)) return fail(KDA_ERR_INVALID_ARGUMENT, "src_rows=%lld out of range [0, 2^31)", (long long)src_rows);
+    if (rows == nullptr && src_rows < T_tot)
+        return fail(KDA_ERR_INVALID_ARGUMENT, "rows is NULL but src_rows=%lld is below T_tot=%lld", (long long)src_rows, (long long)T_tot);
+    if (window < 0) return fail(KDA_ERR_INVALID_ARGUMENT, "window=%d is negative", window);
+    if (sinks < 0) return fail(KDA_ERR_INVALID_ARGUMENT, "sinks=%d is negative", sinks);
+    kda::CacheArgs c;
+    st = cache_args(Hkv, dk, dv, x_dtype, const_cast<void*>(k_cache), nullptr, num_pages, page_size, const_cast<int32_t*>(page_table), slots,
+                    max_pages, const_cast<int32_t*>(lens), nullptr, c);
+    if (st != KDA_OK) return st;
+    const int64_t most = static_cast<int64_t>(max_pages) << c.page_shift;
+    if (most >= kMostWindowed) return fail(KDA_ERR_UNSUPPORTED, "max_pages x page_size = %lld is not below 2^30", (long long)most);
+    if (T_tot == 0) return ok();
+    const size_t xs = dsize(x_dtype), need = kda_cache_weigh_workspace_bytes(T_tot, N, H, Hkv, most);
+    const Span sp[] = {
+        {"q", q, static_cast<size_t>(src_rows) * H * dk * xs, false}, {"lse", lse, static_cast<size_t>(src_rows) * H * 4, false, 4},
+        {"k_cache", k_cache, pool_bytes(c, dk), false}, {"page_table", page_table, table_bytes(slots, max_pages), false, 4},
+        {"lens", lens, static_cast<size_t>(slots) * 4, false, 4},
+        {"cu_seqlens", cu_seqlens, cu_seqlens ? (static_cast<size_t>(N) + 1) * 4 : 0, false, 4},
+        {"rows", rows, rows ? static_cast<size_t>(T_tot) * 4 : 0, false, 4},
+        {"slot_indices", slot_indices, slot_indices ? static_cast<size_t>(N) * 4 : 0, false, 4},
+        {"weights", weights, static_cast<size_t>(slots) * static_cast<size_t>(most) * 4, true, 4}, {"workspace", workspace, need, true},
+    };
+    st = check_workspace("kda_cache_weigh", workspace_bytes, need, workspace);
+    if (st == KDA_OK) st = check_spans(sp);
+    if (st != KDA_OK) return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    st = debug_check_cu_within(cu_seqlens, N, T_tot, s);
+    if (st != KDA_OK) return st;
+    const kda::WeighArgs a{T_tot, src_rows, N, H, cu_seqlens, rows, scale, window, sinks, q, lse, weights, slot_indices, workspace};
+    const hipError_t e = kda::launch_cache_weigh(c, a, s);
+    if (e != hipSuccess) return hip_fail(e, "cache weigh launch");
+    return ok();
+}
+
+size_t kda_cache_evict_workspace_bytes(int32_t n, int32_t keep) {
+    if (n < 0 || n >= kda::kMostEvicted || keep < 1 || keep >= kMostWindowed) return 0;
+    return kda::cache_evict_workspace_bytes(n, keep);
+}
+
+int kda_cache_evict(int32_t n, const int32_t* slot_list, int32_t keep, int32_t first, int32_t recent, int32_t Hkv, int32_t dk,
+                    int32_t dv, int32_t x_dtype, void* k_cache, void* v_cache, int32_t num_pages, int32_t page_size,
+                    int32_t* page_table, int32_t slots, int32_t max_pages, int32_t* lens, int32_t* refs, float* weights,
+                    int32_t* kept, int32_t* status, void* workspace, size_t workspace_bytes, void* stream) {
+    kda::CacheArgs c;
+    int st = cache_args(Hkv, dk, dv, x_dtype, k_cache, v_cache, num_pages, page_size, page_table, slots, max_pages, lens, refs, c);
+    if (st != KDA_OK) return st;
+    if (n < 0) return fail(KDA_ERR_INVALID_ARGUMENT, "n=%d is negative", n);
+    if (n >= kda::kMostEvicted) return fail(KDA_ERR_UNSUPPORTED, "n=%d entries are not below %d", n, kda::kMostEvicted);
+    if (Hkv >= (1 << 15)) return fail(KDA_ERR_UNSUPPORTED, "Hkv=%d is not below 2^15", Hkv);
+    if (keep < 1) return fail(KDA_ERR_INVALID_ARGUMENT, "keep=%d must be >= 1", keep);
+    if (first < 0) return fail(KDA_ERR_INVALID_ARGUMENT, "first=%d is negative", first);
+    if (recent < 0) return fail(KDA_ERR_INVALID_ARGUMENT, "recent=%d is negative", recent);
+    if (static_cast<int64_t>(first) + recent > keep)
+        return fail(KDA_ERR_INVALID_ARGUMENT, "first=%d and recent=%d are more than keep=%d", first, recent, keep);
+    const int64_t most = static_cast<int64_t>(max_pages) << c.page_shift;
+    if (most >= kMostWindowed) return fail(KDA_ERR_UNSUPPORTED, "max_pages x page_size = %lld is not below 2^30", (long long)most);
+    if (keep >= kMostWindowed) return fail(KDA_ERR_UNSUPPORTED, "keep=%d is not below 2^30", keep);
+    if (n == 0) return ok();
+    const size_t need = kda_cache_evict_workspace_bytes(n, keep), per = static_cast<size_t>(n) * 4;
+    const Span sp[] = {
+        {"k_cache", k_cache, pool_bytes(c, dk), true}, {"v_cache", v_cache, pool_bytes(c, dv), true},
+        {"page_table", page_table, table_bytes(slots, max_pages), true, 4}, {"lens", lens, static_cast<size_t>(slots) * 4, true, 4},
+        {"refs", refs, static_cast<size_t>(num_pages) * 4, true, 4}, {"slot_list", slot_list, per, false, 4},
+        {"weights", weights, static_cast<size_t>(slots) * static_cast<size_t>(most) * 4, true, 4}, {"kept", kept, kept ? per * keep : 0, true, 4},
+        {"status", status, status ? per : 0, true, 4}, {"workspace", workspace, need, true},
+    };
+    st = check_workspace("kda_cache_evict", workspace_bytes, need, workspace);
+    if (st == KDA_OK) st = check_spans(sp);
+    if (st != KDA_OK) return st;
+    const kda::EvictArgs a{n, keep, first, recent, slot_list, weights, kept, status, workspace};
+    const hipError_t e = kda::launch_cache_evict(c, a, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(e, "cache evict launch");
     return ok();
 }
 

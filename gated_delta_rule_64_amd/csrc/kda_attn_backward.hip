@@ -43,6 +43,7 @@ struct BwdK {
     int parts, q_parts;
     float* part;      // [parts][T, Hkv][dk + dv]
     float* q_part;    // [q_parts][T, H][dk]
+    int window, sinks;
 };
 
 // One row (token, head) per 16 lanes, so that a load takes whole lines of
@@ -121,7 +122,7 @@ struct DqSizes {
 // Query gradients: one workgroup per (tile of 128 queries, head, part of the
 // keys); a wave's queries, output gradients and sums stay in its registers, the
 // keys and values pass through LDS once for four waves.
-template <typename T, int DK, int DV>
+template <typename T, int DK, int DV, bool kWin>
 __device__ __forceinline__ void query_gradients(const BwdK& a, unsigned block, char* smem) {
     using Sz = DqSizes<T, DK, DV>;
     constexpr int kKeys = Sz::kKeys, kSub = kKeys / 32;
@@ -167,14 +168,17 @@ __device__ __forceinline__ void query_gradients(const BwdK& a, unsigned block, c
     rk.init_rows(c, half);
     rk.init_columns(lane);
     rv.init_rows(c, half);
-    const int64_t steps = (min(t.level * kRows + kRows, t.len) + kKeys - 1) / kKeys;  // keys [0, steps kKeys) are attended by some row
-    const int start = static_cast<int>(steps * part / a.q_parts) * kKeys;
-    const int last = static_cast<int>(steps * (part + 1) / a.q_parts) * kKeys;
+    const KeyWalk<kWin, kKeys> walk(t.level * kRows, t.len, a.window, a.sinks);
+    // tiles that some row attends
+    const int64_t steps = walk.before((min(t.level * kRows + kRows, t.len) + kKeys - 1) / kKeys * kKeys);
+    const int start = walk.nth(static_cast<int>(steps * part / a.q_parts));
+    const int last = walk.nth(static_cast<int>(steps * (part + 1) / a.q_parts));
     const T* kbase = static_cast<const T*>(a.k) + kvh * DK;
     const T* vbase = static_cast<const T*>(a.v) + kvh * DV;
     auto fetch = [&](int j0) {
-        ck.load(rows_of(kbase, t.start + j0, k_row, min(kKeys, t.len - j0)), k_row, tid);
-        cv.load(rows_of(vbase, t.start + j0, v_row, min(kKeys, t.len - j0)), v_row, tid);
+        const int there = walk.rows(j0);
+        ck.load(rows_of(kbase, t.start + j0, k_row, there), k_row, tid);
+        cv.load(rows_of(vbase, t.start + j0, v_row, there), v_row, tid);
     };
     auto put = [&](char* buf) {
         ck.store(buf, tid);
@@ -186,6 +190,9 @@ __device__ __forceinline__ void query_gradients(const BwdK& a, unsigned block, c
         for (int u = 0; u < kSub; ++u) {
             const int k0 = j0 + 32 * u;
             if (k0 > q0 + 31) break;
+            if constexpr (kWin) {
+                if (k0 + 32 <= walk.least(q0) && k0 >= walk.sinks) continue;
+            }
             f32x16 s{}, dp{};
 #pragma unroll
             for (int p = 0; p < kQPieces; ++p) {
@@ -200,6 +207,14 @@ __device__ __forceinline__ void query_gradients(const BwdK& a, unsigned block, c
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
                     if (8 * (r / 4) + r % 4 > most) s[r] = 0.f;
+            }
+            if constexpr (kWin) {
+                if (k0 < walk.least(q0 + 31) && k0 + 32 > walk.sinks) {  // keys before the row's window, but for the first ones
+                    const int least = opaque(walk.least(q0 + c) - k0 - 4 * half), sink = opaque(walk.sinks - k0 - 4 * half);
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (outside(8 * (r / 4) + r % 4, least, sink)) s[r] = 0.f;
+                }
             }
 #pragma unroll
             for (int p = 0; p < kP; ++p) {
@@ -217,16 +232,18 @@ __device__ __forceinline__ void query_gradients(const BwdK& a, unsigned block, c
         arrive(of);
         put(smem);
     }
-    for (int j0 = start; j0 < last; j0 += 2 * kKeys) {
+    for (int j0 = start; j0 < last;) {
+        const int j1 = walk.next(j0), j2 = walk.next(j1);
         tile_barrier();
-        if (j0 + kKeys < last) fetch(j0 + kKeys);
+        if (j1 < last) fetch(j1);
         work(smem, j0);
-        if (j0 + kKeys >= last) break;
+        if (j1 >= last) break;
         put(smem + Sz::kBuf);
         tile_barrier();
-        if (j0 + 2 * kKeys < last) fetch(j0 + 2 * kKeys);
-        work(smem + Sz::kBuf, j0 + kKeys);
-        if (j0 + 2 * kKeys < last) put(smem);
+        if (j2 < last) fetch(j2);
+        work(smem + Sz::kBuf, j1);
+        if (j2 < last) put(smem);
+        j0 = j2;
     }
     if (c >= rows) return;
     if (a.q_parts > 1)
@@ -255,7 +272,7 @@ struct DkvSizes {
 // the sequence of its steps of 32 queries, head by head of the group; the
 // parts cut it into equal pieces where there are few tiles, and their sums
 // (fp32) are added by attn_bwd_sum_kernel.
-template <typename T, int DK, int DV>
+template <typename T, int DK, int DV, bool kWin>
 __device__ __forceinline__ void key_gradients(const BwdK& a, unsigned block, char* smem) {
     using Sz = DkvSizes<T, DK, DV>;
     constexpr int kQ = Sz::kQ;
@@ -320,7 +337,12 @@ __device__ __forceinline__ void key_gradients(const BwdK& a, unsigned block, cha
     ro.init_rows(c, half);
     ro.init_columns(lane);
     uint2 stat{};
-    const int steps = (t.len - k_first + kQ - 1) / kQ;  // per head
+    // the queries that attend some key of the tile: [k_first, end)
+    int end = t.len;
+    if constexpr (kWin) {
+        if (k_first >= a.sinks) end = min(t.len, k_first + kRows - 1 + a.window);
+    }
+    const int steps = (end - k_first + kQ - 1) / kQ;  // per head
     const int64_t all = static_cast<int64_t>(steps) * G;
     int n = static_cast<int>(all * part / a.parts);
     const int n_end = static_cast<int>(all * (part + 1) / a.parts);
@@ -333,7 +355,7 @@ __device__ __forceinline__ void key_gradients(const BwdK& a, unsigned block, cha
         if (wave == 0)
             stat = buffer_load8(rows_of(a.stats + f_head, t.start + f_i0, a.H * 8, here), c * a.H * 8);
         f_i0 += kQ;
-        if (f_i0 >= t.len) {
+        if (f_i0 >= end) {
             f_i0 = k_first;
             ++f_head;
         }
@@ -345,8 +367,11 @@ __device__ __forceinline__ void key_gradients(const BwdK& a, unsigned block, cha
     };
     int i0 = f_i0 - kQ;  // the step worked on
     auto work = [&](const char* sQ) __attribute__((always_inline)) {
-        i0 = i0 + kQ < t.len ? i0 + kQ : k_first;
+        i0 = i0 + kQ < end ? i0 + kQ : k_first;
         if (i0 + kQ - 1 < k0) return;  // queries before this wave's keys
+        if constexpr (kWin) {
+            if (i0 - a.window > k0 + 30 && k0 >= a.sinks) return;  // and those that have left them behind
+        }
         const char* sO = sQ + kO;
         const f32x4* sStats = reinterpret_cast<const f32x4*>(sQ + kS);
         f32x16 s{}, dp{};
@@ -379,6 +404,14 @@ __device__ __forceinline__ void key_gradients(const BwdK& a, unsigned block, cha
 #pragma unroll
             for (int r = 0; r < 16; ++r)
                 if (8 * (r / 4) + r % 4 < least) s[r] = dp[r] = 0.f;
+        }
+        if constexpr (kWin) {
+            if (i0 + kQ > k0 + a.window && k0 + 32 > a.sinks) {  // queries whose window begins behind the key, unless it is a first one
+                const int most = opaque(k0 + c < a.sinks ? INT32_MAX : k0 + c + a.window - i0 - 4 * half);
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (8 * (r / 4) + r % 4 >= most) s[r] = dp[r] = 0.f;
+            }
         }
 #pragma unroll
         for (int p = 0; p < kP; ++p) {
@@ -426,11 +459,11 @@ __device__ __forceinline__ void key_gradients(const BwdK& a, unsigned block, cha
 // takes 55 + 59 us so).  Rows of up to 256 bytes leave registers for two
 // workgroups a CU (fp32 at 64 channels: 4,000 tokens 1,900 us, 2,180 with one;
 // the ragged batch of up to 1,000 tokens 301 us, 355 with one).
-template <typename T, int DK, int DV>
+template <typename T, int DK, int DV, bool kWin>
 __global__ __launch_bounds__(kThreads, (DK * sizeof(T) <= 256 ? 2 : 1)) void attn_bwd_kernel(BwdK a, unsigned key_groups) {
     extern __shared__ __align__(16) char smem[];
-    if (blockIdx.x < key_groups) key_gradients<T, DK, DV>(a, blockIdx.x, smem);
-    else query_gradients<T, DK, DV>(a, blockIdx.x - key_groups, smem);
+    if (blockIdx.x < key_groups) key_gradients<T, DK, DV, kWin>(a, blockIdx.x, smem);
+    else query_gradients<T, DK, DV, kWin>(a, blockIdx.x - key_groups, smem);
 }
 
 // Adds the parts in their order, four channels per thread: first the rows of
@@ -491,13 +524,15 @@ hipError_t allow_lds(F fn, int lds) {
     return hipFuncSetAttribute(reinterpret_cast<const void*>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
 }
 
-template <typename T, int DK, int DV>
+template <typename T, int DK, int DV, bool kWin>
 hipError_t launch_bwd(const AttnBackwardArgs& a, hipStream_t s) {
     const AttnArgs& f = a.f;
     BwdK k{};
     k.T = f.T; k.H = f.H; k.Hkv = f.Hkv; k.N = f.N; k.cu = f.cu;
     k.q = f.q; k.k = f.k; k.v = f.v; k.z = f.z; k.out = f.out; k.dy = a.dy; k.lse = f.lse;
     k.dq = a.dq; k.dk = a.dk; k.dv = a.dv; k.dz = a.dz; k.scale = f.scale;
+    k.window = static_cast<int>(f.window < f.T ? f.window : f.T);
+    k.sinks = static_cast<int>(f.sinks < f.T ? f.sinks : f.T);
     char* ws = static_cast<char*>(a.ws);
     k.stats = reinterpret_cast<float2*>(ws);
     ws += up256(static_cast<size_t>(f.T) * f.H * 8);
@@ -510,7 +545,7 @@ hipError_t launch_bwd(const AttnBackwardArgs& a, hipStream_t s) {
     if (k.parts > 1) ws += up256(static_cast<size_t>(k.parts) * f.T * f.Hkv * (DK + DV) * 4);
     k.q_part = reinterpret_cast<float*>(ws);
     constexpr int lds = DqSizes<T, DK, DV>::kLds > DkvSizes<T, DK, DV>::kLds ? DqSizes<T, DK, DV>::kLds : DkvSizes<T, DK, DV>::kLds;
-    hipError_t e = allow_lds(attn_bwd_kernel<T, DK, DV>, lds);
+    hipError_t e = allow_lds(attn_bwd_kernel<T, DK, DV, kWin>, lds);
     if (e != hipSuccess) return e;
     {
         LaunchTimer timer("attn_bwd_rows", s);
@@ -521,9 +556,9 @@ hipError_t launch_bwd(const AttnBackwardArgs& a, hipStream_t s) {
     if (e != hipSuccess) return e;
     const int64_t tiles = attn_tiles(f.T, f.N, kRows);
     {
-        LaunchTimer timer("attn_bwd", s);
+        LaunchTimer timer(kWin ? "attn_window_bwd" : "attn_bwd", s);
         const int64_t key_groups = tiles * f.Hkv * k.parts;
-        attn_bwd_kernel<T, DK, DV><<<dim3(static_cast<unsigned>(key_groups + tiles * f.H * k.q_parts)), dim3(kThreads), lds, s>>>(
+        attn_bwd_kernel<T, DK, DV, kWin><<<dim3(static_cast<unsigned>(key_groups + tiles * f.H * k.q_parts)), dim3(kThreads), lds, s>>>(
             k, static_cast<unsigned>(key_groups));
     }
     e = hipGetLastError();
@@ -540,7 +575,9 @@ hipError_t launch_bwd(const AttnBackwardArgs& a, hipStream_t s) {
 
 }  // namespace
 
-size_t attn_backward_workspace_bytes(int64_t T, int N, int H, int Hkv, int dk, int dv, DT x, bool gate) {
+size_t attn_backward_workspace_bytes(int64_t T, int N, int H, int Hkv, int dk, int dv, DT x, bool gate, int window, int sinks) {
+    (void)window;
+    (void)sinks;
     const size_t rows = static_cast<size_t>(T) * H;
     const BwdParts parts = bwd_parts(T, N, H, Hkv);
     return up256(rows * 8) + (gate ? up256(rows * dv * (x == DT::BF16 ? 2 : 4)) : 0) +
@@ -552,10 +589,10 @@ size_t attn_backward_workspace_bytes(int64_t T, int N, int H, int Hkv, int dk, i
 // sizes.  One sequence has the fewest tiles and so the most parts; of the
 // lengths of as many tiles the longest needs the most; from kKeyWant tiles on
 // there is one part.
-size_t attn_backward_max_workspace_bytes(int64_t T, int H, int Hkv, int dk, int dv, DT x, bool gate) {
-    size_t most = attn_backward_workspace_bytes(T, 1, H, Hkv, dk, dv, x, gate);
+size_t attn_backward_max_workspace_bytes(int64_t T, int H, int Hkv, int dk, int dv, DT x, bool gate, int window, int sinks) {
+    size_t most = attn_backward_workspace_bytes(T, 1, H, Hkv, dk, dv, x, gate, window, sinks);
     for (int64_t t = kRows - 1; t < T && t < static_cast<int64_t>(kKeyWant) * kRows; t += kRows) {
-        const size_t need = attn_backward_workspace_bytes(t, 1, H, Hkv, dk, dv, x, gate);
+        const size_t need = attn_backward_workspace_bytes(t, 1, H, Hkv, dk, dv, x, gate, window, sinks);
         most = need > most ? need : most;
     }
     return most;
@@ -564,7 +601,9 @@ size_t attn_backward_max_workspace_bytes(int64_t T, int H, int Hkv, int dk, int 
 hipError_t launch_attn_prefill_backward(const AttnBackwardArgs& a, hipStream_t s) {
     if (a.f.T == 0) return hipSuccess;
     return attn_dispatch(a.f.x, a.f.dk, a.f.dv, [&](auto t, auto dk, auto dv) {
-        return launch_bwd<typename decltype(t)::type, decltype(dk)::value, decltype(dv)::value>(a, s);
+        using X = typename decltype(t)::type;
+        constexpr int kDk = decltype(dk)::value, kDv = decltype(dv)::value;
+        return a.f.window > 0 ? launch_bwd<X, kDk, kDv, true>(a, s) : launch_bwd<X, kDk, kDv, false>(a, s);
     });
 }
 

@@ -248,6 +248,62 @@ __device__ __forceinline__ Tile find_tile(const int32_t* cu, int N, int64_t T, i
     return t;
 }
 
+// Whether a key is before a row's window and not among the first tokens (key,
+// least and sink from the same place on): one comparison, as 16 of two each
+// would hold more masks than there are scalar registers.
+__device__ __forceinline__ bool outside(int key, int least, int sink) { return ((key - least) & (sink - 1 - key)) < 0; }
+
+// The key tiles of kKeys that a tile of 128 query rows from q_first on attends,
+// in order: all up to its own last row, or with a window (kWin) those that hold
+// one of the sequence's first `sinks` tokens and those from the first row's
+// window on.  A tile is named by its first key, a multiple of kKeys.
+template <bool kWin, int kKeys>
+struct KeyWalk {
+    int len;
+    int window, sinks;      // below 2^30 each, as are len and q_first
+    int sink_end, win;      // the tiles before sink_end and from win on are walked
+    __device__ __forceinline__ KeyWalk(int q_first, int len_, int window_, int sinks_) : len(len_) {
+        if constexpr (kWin) {
+            window = window_;
+            sinks = sinks_;
+            sink_end = (sinks + kKeys - 1) / kKeys * kKeys;
+            win = max(0, q_first - window + 1) / kKeys * kKeys;
+        } else {
+            window = sinks = sink_end = win = 0;
+        }
+    }
+    __device__ __forceinline__ int next(int j0) const {
+        const int j = j0 + kKeys;
+        if constexpr (kWin) return j >= sink_end ? max(j, win) : j;
+        return j;
+    }
+    // Tiles that are walked before j0 (one that is walked itself, or the end)
+    __device__ __forceinline__ int before(int j0) const {
+        if constexpr (kWin) return j0 <= sink_end ? min(j0, sink_end) / kKeys : (j0 - max(win, sink_end) + sink_end) / kKeys;
+        return j0 / kKeys;
+    }
+    // The n-th of them
+    __device__ __forceinline__ int nth(int n) const {
+        if constexpr (kWin) return n * kKeys < sink_end ? n * kKeys : n * kKeys + max(win - sink_end, 0);
+        return n * kKeys;
+    }
+    // Rows of a tile that some row may attend; what is behind them reads as 0,
+    // so that a value that is not finite there meets no weight of 0.
+    __device__ __forceinline__ int rows(int j0) const {
+        if constexpr (kWin) return min(kKeys, (j0 < win ? sinks : len) - j0);
+        return min(kKeys, len - j0);
+    }
+    // The first token of row i's window (may be negative)
+    __device__ __forceinline__ int least(int i) const { return i - window + 1; }
+    // Whether the rows from q0 on have all left the tile behind them, and
+    // whether the window of one of the 32 from q0 on begins behind its first key
+    __device__ __forceinline__ bool passed(int j0, int q0) const {
+        if constexpr (kWin) return j0 + kKeys <= least(q0) && j0 >= sinks;
+        return false;
+    }
+    __device__ __forceinline__ bool edge(int j0, int q0) const { return kWin && j0 < least(q0 + 31) && j0 + kKeys > sinks; }
+};
+
 // A tile in LDS without padding: rows of kPieces 16-byte pieces, piece p of row
 // r stored in place p ^ turn(r).  LDS has 64 banks of 4 bytes, 16 pieces side
 // by side, and the turn is such that neither way of reading meets itself in a

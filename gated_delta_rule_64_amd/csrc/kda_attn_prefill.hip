@@ -39,6 +39,7 @@ struct FwdK {
     void* out;
     float* lse;
     float scale;
+    int window, sinks;
 };
 
 template <typename T, int DK, int DV>
@@ -49,7 +50,8 @@ struct FwdSizes {
     static constexpr int kLds = kTiles > kRows ? kTiles : kRows;  // the results pass through the tiles' space
 };
 
-template <typename T, int DK, int DV>
+// kWin: a row attends its last `window` tokens and the first `sinks` ones.
+template <typename T, int DK, int DV, bool kWin>
 __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void attn_fwd_kernel(FwdK a) {
     using Sz = FwdSizes<T, DK, DV>;
     constexpr int kKeys = Sz::kKeys, kSub = kKeys / 32;
@@ -93,9 +95,11 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void attn_fwd_k
     const int last = min(t.level * kQ + kQ, t.len);  // keys [0, last) are attended by some row
     const T* kbase = static_cast<const T*>(a.k) + kvh * DK;
     const T* vbase = static_cast<const T*>(a.v) + kvh * DV;
+    const KeyWalk<kWin, kKeys> walk(t.level * kQ, t.len, a.window, a.sinks);
     auto fetch = [&](int j0) {
-        ck.load(rows_of(kbase, t.start + j0, k_row, min(kKeys, t.len - j0)), k_row, tid);
-        cv.load(rows_of(vbase, t.start + j0, v_row, min(kKeys, t.len - j0)), v_row, tid);
+        const int rows = walk.rows(j0);
+        ck.load(rows_of(kbase, t.start + j0, k_row, rows), k_row, tid);
+        cv.load(rows_of(vbase, t.start + j0, v_row, rows), v_row, tid);
     };
     // Two tiles in LDS: while one is worked on, the next one's rows arrive in
     // registers and are stored behind it; one barrier a tile.
@@ -104,7 +108,7 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void attn_fwd_k
         cv.store(buf + kV, tid);
     };
     auto work = [&](const char* sK, int j0) __attribute__((always_inline)) {
-        if (j0 > q0 + 31) return;  // nothing of the tile is attended by this wave's rows
+        if (j0 > q0 + 31 || walk.passed(j0, q0)) return;  // nothing of the tile is attended by this wave's rows
         const char* sV = sK + kV;
         f32x16 s[kSub];
         // the wave that multiplies goes before the one that exponentiates
@@ -125,6 +129,16 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void attn_fwd_k
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
                     if (32 * u + 8 * (r / 4) + r % 4 > most) s[u][r] = -INFINITY;
+        }
+        if constexpr (kWin) {
+            if (walk.edge(j0, q0)) {  // keys before the row's window, but for the first ones
+                const int least = opaque(walk.least(q0 + c) - j0 - 4 * half), sink = opaque(walk.sinks - j0 - 4 * half);
+#pragma unroll
+                for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (outside(32 * u + 8 * (r / 4) + r % 4, least, sink)) s[u][r] = -INFINITY;
+            }
         }
         float top = s[0][0];
 #pragma unroll
@@ -168,19 +182,22 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void attn_fwd_k
                     acc[i] = mma<T>(rv.columns(sV + 32 * u * rv.kRow, i, p), b, acc[i]);
             }
     };
-    fetch(0);
+    int j0 = walk.next(-kKeys);
+    fetch(j0);
     arrive(qf);
     put(smem);
-    for (int j0 = 0; j0 < last; j0 += 2 * kKeys) {
+    while (j0 < last) {
         tile_barrier();
-        if (j0 + kKeys < last) fetch(j0 + kKeys);
+        const int j1 = walk.next(j0), j2 = walk.next(j1);
+        if (j1 < last) fetch(j1);
         work(smem, j0);
-        if (j0 + kKeys >= last) break;
+        if (j1 >= last) break;
         put(smem + Sz::kBuf);
         tile_barrier();
-        if (j0 + 2 * kKeys < last) fetch(j0 + 2 * kKeys);
-        work(smem + Sz::kBuf, j0 + kKeys);
-        if (j0 + 2 * kKeys < last) put(smem);
+        if (j2 < last) fetch(j2);
+        work(smem + Sz::kBuf, j1);
+        if (j2 < last) put(smem);
+        j0 = j2;
     }
 
     const int row = q0 + c;
@@ -216,17 +233,18 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void attn_fwd_k
     });
 }
 
-template <typename T, int DK, int DV>
+template <typename T, int DK, int DV, bool kWin>
 hipError_t launch_fwd(const AttnArgs& a, hipStream_t s) {
     constexpr int lds = FwdSizes<T, DK, DV>::kLds;
     static_assert(lds <= 160 * 1024, "one workgroup's LDS");
-    auto fn = attn_fwd_kernel<T, DK, DV>;
+    auto fn = attn_fwd_kernel<T, DK, DV, kWin>;
     if (lds > 64 * 1024) {
         const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
         if (e != hipSuccess) return e;
     }
-    const FwdK k{a.T, a.H, a.Hkv, a.N, a.cu, a.q, a.k, a.v, a.z, a.out, a.lse, a.scale};
-    LaunchTimer timer("attn_fwd", s);
+    const FwdK k{a.T, a.H, a.Hkv, a.N, a.cu, a.q, a.k, a.v, a.z, a.out, a.lse, a.scale,
+                 static_cast<int>(a.window < a.T ? a.window : a.T), static_cast<int>(a.sinks < a.T ? a.sinks : a.T)};
+    LaunchTimer timer(kWin ? "attn_window_fwd" : "attn_fwd", s);
     fn<<<dim3(static_cast<unsigned>(attn_tiles(a.T, a.N, kQ) * a.H)), dim3(kThreads), lds, s>>>(k);
     return hipGetLastError();
 }
@@ -236,7 +254,9 @@ hipError_t launch_fwd(const AttnArgs& a, hipStream_t s) {
 hipError_t launch_attn_prefill(const AttnArgs& a, hipStream_t s) {
     if (a.T == 0) return hipSuccess;
     return attn_dispatch(a.x, a.dk, a.dv, [&](auto t, auto dk, auto dv) {
-        return launch_fwd<typename decltype(t)::type, decltype(dk)::value, decltype(dv)::value>(a, s);
+        using X = typename decltype(t)::type;
+        constexpr int kDk = decltype(dk)::value, kDv = decltype(dv)::value;
+        return a.window > 0 ? launch_fwd<X, kDk, kDv, true>(a, s) : launch_fwd<X, kDk, kDv, false>(a, s);
     });
 }
 

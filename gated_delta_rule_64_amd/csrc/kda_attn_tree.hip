@@ -48,6 +48,7 @@ struct TreeK {
     float* stats;  // [splits][B, Hkv, T G][2]: maximum (raw scores), sum of weights
     int splits, blocks;  // workgroups per (sequence, key head): parts of the keys, blocks of rows
     int units;           // all but the blocks: sequences, key heads and parts
+    int window, sinks;
 };
 
 template <typename T, int DK, int DV>
@@ -111,7 +112,9 @@ __device__ __forceinline__ uint32_t take_odd(u32x4& x) {
     return any;
 }
 
-template <typename T, int DK, int DV>
+// kWin: of a row's tokens in order, the cached ones and then the drafts of its
+// mask word, the last `window` and the first `sinks` are attended.
+template <typename T, int DK, int DV, bool kWin>
 __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV>::kWaves), (sizeof(T) == 2 && DK <= 128 ? 2 : 1)) void attn_tree_kernel(TreeK a) {
     using Sz = TreeSizes<T, DK, DV>;
     constexpr int kE = sizeof(T);
@@ -156,7 +159,17 @@ __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV>::kWaves), (sizeof(T) == 
 #pragma unroll
     for (int i = 0; i < kVTiles; ++i) acc[i] = f32x16{};
 
-    const int ctx_tiles = (ctx + kKeys - 1) / kKeys, tiles = ctx_tiles + (a.T + kKeys - 1) / kKeys;
+    // The cache's tiles that some row reads: with a window those of the first
+    // tokens, sink_tiles of them, and those from `skip` tiles further on.
+    int ctx_tiles = (ctx + kKeys - 1) / kKeys, sink_tiles = ctx_tiles, skip = 0, low = 0, sinks = 0;
+    if constexpr (kWin) {
+        low = max(0, ctx - a.window);  // (a row of an empty mask word sees back to here)
+        sinks = min(a.sinks, ctx);
+        sink_tiles = (sinks + kKeys - 1) / kKeys;
+        skip = max(0, low / kKeys - sink_tiles);
+        ctx_tiles -= skip;
+    }
+    const int tiles = ctx_tiles + (a.T + kKeys - 1) / kKeys;
     const int each = (tiles + a.splits - 1) / a.splits;
     const int t_end = real ? min(tiles, (split + 1) * each) : 0;
     int tile = split * each + wave;
@@ -171,8 +184,24 @@ __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV>::kWaves), (sizeof(T) == 
 #pragma unroll
             for (int p = 0; p < kQPieces; ++p) qf[p] = *reinterpret_cast<const u32x4*>(q_row + p * 32);
         }
-        const uint64_t seen = a.mask != nullptr ? static_cast<uint64_t>(a.mask[static_cast<int64_t>(b) * a.T + token])
-                                                : ~0ull >> (63 - token);
+        uint64_t seen = a.mask != nullptr ? static_cast<uint64_t>(a.mask[static_cast<int64_t>(b) * a.T + token])
+                                          : ~0ull >> (63 - token);
+        int least = 0;  // the first cached token of the row's window
+        if constexpr (kWin) {
+            seen &= ~0ull >> (64 - a.T);
+            const int drafts = __popcll(seen);
+            least = ctx + drafts - a.window;
+            // a window of fewer tokens than the row's drafts: the first of them
+            // go, but for those among the sequence's first tokens
+            if (drafts > a.window) {
+                const int stay = max(0, a.sinks - ctx);
+                uint64_t rest = seen;
+                for (int n = 0; n < drafts - a.window; ++n) {
+                    if (n >= stay) seen &= ~(rest & -rest);
+                    rest &= rest - 1;
+                }
+            }
+        }
         const float sc = a.scale * kLog2e;
 
         // Half a tile: 16 rows of keys and of values, 16-byte pieces
@@ -190,12 +219,14 @@ __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV>::kWaves), (sizeof(T) == 
             int page[2], rows[2];  // rows that hold a token
         };
         const int in_page = (1 << a.page_shift) - 1;
+        auto real = [&](int n) __attribute__((always_inline)) { return kWin && n >= sink_tiles ? n + skip : n; };
         auto look_up = [&](int n) __attribute__((always_inline)) {
             Halves e;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                const int t0 = n * kKeys + 16 * x;
-                e.rows[x] = min(16, max(0, ctx - t0));
+                const int first = real(n) * kKeys, t0 = first + 16 * x;
+                // (a tile before every window: what is behind the first tokens reads as 0)
+                e.rows[x] = min(16, max(0, (kWin && first + kKeys <= low ? sinks : ctx) - t0));
                 // (clamped: a column behind the context is not looked at)
                 e.page[x] = entries[min(t0, ctx - 1) >> a.page_shift];
             }
@@ -205,7 +236,7 @@ __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV>::kWaves), (sizeof(T) == 
             const bool there = e.page[x] >= 0 && e.page[x] < a.pages;  // else its tokens are not attended
             e.rows[x] = there ? e.rows[x] : 0;
             const int64_t head = static_cast<int64_t>(there ? e.page[x] : 0) * a.Hkv + kvh;
-            const int64_t first = (head << a.page_shift) + ((n * kKeys + 16 * x) & in_page);
+            const int64_t first = (head << a.page_shift) + ((real(n) * kKeys + 16 * x) & in_page);
             const auto ks = rows_of(a.k_cache, first, kKRow, e.rows[x]);
             const auto vs = rows_of(a.v_cache, first, kVRow, e.rows[x]);
             const int to = kAhead ? x : 0;
@@ -278,6 +309,23 @@ __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV>::kWaves), (sizeof(T) == 
         };
         // register r of a score: key 8 (r / 4) + 4 half + r % 4 of the tile
 
+        // adds the values of a row of V that are not finite, where this lane's row attends it
+        // (four channels at a time: all at once would not fit beside the rows in flight)
+        auto add_odd = [&](const T* from, bool attended) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < kVTiles; ++i)
+#pragma unroll
+                for (int r4 = 0; r4 < 4; ++r4) {
+                    if (32 * i + 8 * r4 >= DV) continue;
+                    float v[4];
+                    ld4(from + 32 * i + 8 * r4 + 4 * half, v);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (attended && !(fabsf(v[e]) < INFINITY)) acc[i][4 * r4 + e] += v[e];
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+        };
+
         // the committed tokens: a tile's rows are in flight while the one
         // before is worked on, its table entries one tile earlier still
         const int c_end = min(t_end, ctx_tiles);
@@ -291,13 +339,26 @@ __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV>::kWaves), (sizeof(T) == 
             if constexpr (kKeep) arrive(qf);
             for (; tile < c_end; tile += kWaves) {
                 wave_lds_fence();
+                // where a window begins: the tile holds keys that some rows attend and others do not
+                const int t0 = real(tile) * kKeys;
+                const bool edge = kWin && t0 + kKeys > low && t0 - a.T < ctx - a.window && t0 + kKeys > sinks;
+                uint32_t odd = 0;
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     if constexpr (!kAhead) fetch_half(tile, now, x);
+                    if (edge) {
+#pragma unroll
+                        for (int i = 0; i < kVEach; ++i)
+                            if (kVPieces >= 64 || lane < kVPieces) odd |= take_odd<T>(vr[kAhead ? x : 0][i]);
+                    }
                     put_half(x);
                 }
                 const int n0 = now.rows[0], n1 = now.rows[1];
-                any |= n0 | n1;
+                const int page0 = now.page[0], page1 = now.page[1];
+                if constexpr (kWin)
+                    any |= (n0 > 0 && (t0 < sinks || t0 + n0 > least)) || (n1 > 0 && (t0 + 16 < sinks || t0 + 16 + n1 > least));
+                else
+                    any |= n0 | n1;
                 if (tile + kWaves < c_end) {
                     now = next;
                     if constexpr (kAhead) {
@@ -307,12 +368,29 @@ __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV>::kWaves), (sizeof(T) == 
                     if (tile + 2 * kWaves < c_end) next = look_up(tile + 2 * kWaves);
                 }
                 work([&](f32x16& s) __attribute__((always_inline)) {
+                    if (edge) {
+                        const int from = opaque(least - t0 - 4 * half), sink = opaque(sinks - t0 - 4 * half);
+#pragma unroll
+                        for (int r = 0; r < 16; ++r)
+                            if (outside(8 * (r / 4) + r % 4, from, sink)) s[r] = -INFINITY;
+                    }
                     if (n0 + n1 == kKeys) return;
                     const int lo = opaque(n0 - 4 * half), hi = opaque(n1 - 4 * half);
 #pragma unroll
                     for (int r = 0; r < 16; ++r)
                         if (8 * (r / 4) + r % 4 - (r >= 8 ? 16 : 0) >= (r >= 8 ? hi : lo)) s[r] = -INFINITY;
                 });
+                if constexpr (kWin) {
+                    // (rare) values that are not finite reach the rows that attend them
+                    if (__any(odd != 0)) {
+                        for (int key = 0; key < kKeys; ++key) {
+                            if ((key & 15) >= (key < 16 ? n0 : n1)) continue;
+                            const int64_t head = static_cast<int64_t>(key < 16 ? page0 : page1) * a.Hkv + kvh;
+                            const T* from = static_cast<const T*>(a.v_cache) + ((head << a.page_shift) + ((t0 + key) & in_page)) * DV;
+                            add_odd(from, t0 + key < sinks || t0 + key >= least);
+                        }
+                    }
+                }
             }
         }
         // the drafts: dense rows, a tile or two
@@ -355,16 +433,7 @@ __global__ __launch_bounds__((64 * TreeSizes<T, DK, DV>::kWaves), (sizeof(T) == 
             // (rare) such values reach the rows that attend them, as they are
             if (__any(odd != 0)) {
                 const T* from = reinterpret_cast<const T*>(vb);
-                for (int key = 0; key < kKeys && t0 + key < a.T; ++key, from += a.Hkv * DV) {
-#pragma unroll
-                    for (int i = 0; i < kVTiles; ++i)
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) {
-                            const int ch = 32 * i + 8 * (r / 4) + 4 * half + r % 4;
-                            const float v = ch < DV ? ld(from + ch) : 0.f;
-                            if ((bits >> key & 1) != 0 && !(fabsf(v) < INFINITY)) acc[i][r] += v;
-                        }
-                }
+                for (int key = 0; key < kKeys && t0 + key < a.T; ++key, from += a.Hkv * DV) add_odd(from, (bits >> key & 1) != 0);
             }
         }
     }
@@ -562,24 +631,25 @@ TreePlan tree_plan(int B, int T, int H, int Hkv, int64_t max_ctx) {
 
 size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
-template <typename T, int DK, int DV>
+template <typename T, int DK, int DV, bool kWin>
 hipError_t launch_tree(const TreeArgs& a, hipStream_t s) {
-    const TreePlan p = tree_plan(a.B, a.T, a.H, a.Hkv, static_cast<int64_t>(a.max_pages) << a.page_shift);
+    const int64_t max_ctx = static_cast<int64_t>(a.max_pages) << a.page_shift;
+    const TreePlan p = tree_plan(a.B, a.T, a.H, a.Hkv, kWin ? window_reach(max_ctx, a.window, a.sinks) : max_ctx);
     const size_t parts = static_cast<size_t>(p.splits) * a.B * a.T * a.H;
     float* part = static_cast<float*>(a.ws);
     float* stats = reinterpret_cast<float*>(static_cast<char*>(a.ws) + up256(parts * DV * 4));
     const TreeK k{a.B, a.T, a.H, a.Hkv, a.scale, a.q, a.k_new, a.v_new, a.z, a.mask, a.k_cache, a.v_cache,
                   a.pages, a.page_shift, a.table, a.slots, a.max_pages, a.lens, a.slot_indices, a.out, a.lse,
-                  part, stats, p.splits, p.blocks, a.B * a.Hkv * p.splits};
+                  part, stats, p.splits, p.blocks, a.B * a.Hkv * p.splits, a.window, a.sinks};
     using Sz = TreeSizes<T, DK, DV>;
     static_assert(Sz::kLds <= 160 * 1024, "one workgroup's LDS");
-    auto fn = attn_tree_kernel<T, DK, DV>;
+    auto fn = attn_tree_kernel<T, DK, DV, kWin>;
     if (Sz::kLds > 64 * 1024) {
         const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, Sz::kLds);
         if (e != hipSuccess) return e;
     }
     {
-        LaunchTimer timer("attn_tree", s);
+        LaunchTimer timer(kWin ? "attn_window_tree" : "attn_tree", s);
         const int64_t groups = static_cast<int64_t>((k.units + 7) / 8) * 8 * k.blocks;
         fn<<<dim3(static_cast<unsigned>(groups)), dim3(64 * Sz::kWaves), Sz::kLds, s>>>(k);
     }
@@ -621,7 +691,9 @@ size_t attn_tree_max_workspace_bytes(int B, int T, int H, int Hkv, int dv, int64
 hipError_t launch_attn_tree(const TreeArgs& a, hipStream_t s) {
     if (a.B == 0 || a.T == 0) return hipSuccess;
     return attn_dispatch(a.x, a.dk, a.dv, [&](auto t, auto dk, auto dv) {
-        return launch_tree<typename decltype(t)::type, decltype(dk)::value, decltype(dv)::value>(a, s);
+        using X = typename decltype(t)::type;
+        constexpr int kDk = decltype(dk)::value, kDv = decltype(dv)::value;
+        return a.window > 0 ? launch_tree<X, kDk, kDv, true>(a, s) : launch_tree<X, kDk, kDv, false>(a, s);
     });
 }
 

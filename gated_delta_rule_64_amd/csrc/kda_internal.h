@@ -146,6 +146,7 @@ struct AttnArgs {
     const void *q, *k, *v, *z;
     void* out;
     float* lse;
+    int window = 0, sinks = 0;  // window 0: every token before a row's own
 };
 struct AttnBackwardArgs {
     AttnArgs f;  // the forward call's arguments (out and lse are its results)
@@ -170,6 +171,7 @@ struct TreeArgs {
     void* out;
     float* lse;
     void* ws;
+    int window = 0, sinks = 0;  // window 0: the whole cache
 };
 
 // A paged cache: two pools, the slots' page table and lengths, the pages'
@@ -218,12 +220,47 @@ hipError_t attn_dispatch(DT x, int dk, int dv, F&& f) {
 }
 
 hipError_t launch_attn_prefill(const AttnArgs& a, hipStream_t s);
-size_t attn_backward_workspace_bytes(int64_t T, int N, int H, int Hkv, int dk, int dv, DT x, bool gate);
-size_t attn_backward_max_workspace_bytes(int64_t T, int H, int Hkv, int dk, int dv, DT x, bool gate);
+size_t attn_backward_workspace_bytes(int64_t T, int N, int H, int Hkv, int dk, int dv, DT x, bool gate, int window = 0, int sinks = 0);
+size_t attn_backward_max_workspace_bytes(int64_t T, int H, int Hkv, int dk, int dv, DT x, bool gate, int window = 0, int sinks = 0);
 hipError_t launch_attn_prefill_backward(const AttnBackwardArgs& a, hipStream_t s);
 size_t attn_tree_workspace_bytes(int B, int T, int H, int Hkv, int dv, int64_t max_ctx);
 size_t attn_tree_max_workspace_bytes(int B, int T, int H, int Hkv, int dv, int64_t max_ctx);
 hipError_t launch_attn_tree(const TreeArgs& a, hipStream_t s);
+
+// The tokens of a cache that a windowed row can read, of a context of at most
+// max_ctx: what the parts of a call go by.
+constexpr int64_t window_reach(int64_t max_ctx, int window, int sinks) {
+    const int64_t reach = static_cast<int64_t>(window) + sinks + 64;  // a tile at the window's start and at the sinks' end
+    return reach < max_ctx ? reach : max_ctx;
+}
+
+// Attention weights gathered per cached token: the queries of each sequence's
+// last tokens, their rows' lse.
+struct WeighArgs {
+    int64_t tokens, src_rows;
+    int N, H;
+    const int32_t *cu, *rows;  // cu NULL: one sequence; rows NULL: row t
+    float scale;
+    int window, sinks;  // window 0: none
+    const void* q;
+    const float* lse;
+    float* weights;  // [slots, max_pages << page_shift]
+    const int32_t* slot_indices;
+    void* ws;
+};
+size_t cache_weigh_workspace_bytes(int64_t tokens, int N, int H, int Hkv, int64_t max_ctx);
+hipError_t launch_cache_weigh(const CacheArgs& c, const WeighArgs& a, hipStream_t s);
+
+struct EvictArgs {
+    int n, keep, first, recent;
+    const int32_t* slot_list;
+    float* weights;
+    int32_t *kept, *status;  // either may be NULL
+    void* ws;
+};
+constexpr int kMostEvicted = 1 << 16;  // entries of a call
+size_t cache_evict_workspace_bytes(int n, int keep);
+hipError_t launch_cache_evict(const CacheArgs& c, const EvictArgs& a, hipStream_t s);
 
 hipError_t launch_cache_append(const CacheArgs& c, int64_t tokens, int N, const int32_t* cu, int64_t src_rows, const int32_t* rows,
                                const void* k_new, const void* v_new, const int32_t* slot_indices, hipStream_t s);

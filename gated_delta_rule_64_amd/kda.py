@@ -386,6 +386,65 @@ def kda_attn_prefill_backward(q, k, v, out, lse, dy, out_gate=None, cu_seqlens=N
     return g
 
 
+def _x_code(x_dtype):
+    if isinstance(x_dtype, torch.dtype):
+        return KDA_BF16 if x_dtype == torch.bfloat16 else KDA_F32
+    return x_dtype
+
+
+def kda_attn_window_prefill(q, k, v, window, sinks=0, out_gate=None, cu_seqlens=None, scale=None, out=None, lse=None):
+    """kda_attn_prefill with a sliding window: token i attends the tokens
+    j <= i with i - j < ``window`` or j < ``sinks``.  Returns (out [T,H,dv],
+    lse fp32 [T,H])."""
+    T, H, Hkv, dk, dv, N = _attn_shapes(q, k, v, out_gate, cu_seqlens)
+    dev = _device(q, k, v, out_gate, cu_seqlens, out, lse)
+    if out is None:
+        out = torch.empty((T, H, dv), dtype=q.dtype, device=dev)
+    else:
+        _shape("out", out, (T, H, dv), q.dtype)
+    if lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+    else:
+        _shape("lse", lse, (T, H), torch.float32)
+    _call(dev, "kda_attn_window_prefill", T, H, Hkv, dk, dv, _addr(cu_seqlens), N, _dtype_code(q),
+          dk ** -0.5 if scale is None else scale, window, sinks, _addr(q), _addr(k), _addr(v), _addr(out_gate), _addr(out),
+          _addr(lse))
+    return out, lse
+
+
+def kda_attn_window_backward_workspace_bytes(T_tot, N, H, Hkv, dk, dv, x_dtype, with_gate, window, sinks):
+    return int(lib().kda_attn_window_backward_workspace_bytes(T_tot, N, H, Hkv, dk, dv, _x_code(x_dtype), int(bool(with_gate)),
+                                                              window, sinks))
+
+
+def kda_attn_window_backward_max_workspace_bytes(max_T_tot, H, Hkv, dk, dv, x_dtype, with_gate, window, sinks):
+    """What every call of up to ``max_T_tot`` tokens with this window and these
+    sinks needs at most."""
+    return int(lib().kda_attn_window_backward_max_workspace_bytes(max_T_tot, H, Hkv, dk, dv, _x_code(x_dtype),
+                                                                  int(bool(with_gate)), window, sinks))
+
+
+def kda_attn_window_prefill_backward(q, k, v, out, lse, dy, window, sinks=0, out_gate=None, cu_seqlens=None, scale=None,
+                                     workspace=None):
+    """Gradients of kda_attn_window_prefill, as kda_attn_prefill_backward
+    returns them."""
+    T, H, Hkv, dk, dv, N = _attn_shapes(q, k, v, out_gate, cu_seqlens)
+    dev = _device(q, k, v, out, lse, dy, out_gate, cu_seqlens, workspace)
+    for name, t in (("out", out), ("dy", dy)):
+        _shape(name, t, (T, H, dv), q.dtype)
+    _shape("lse", lse, (T, H), torch.float32)
+    x = _dtype_code(q)
+    g = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v),
+         "dz": torch.empty_like(out_gate) if out_gate is not None else None}
+    need = kda_attn_window_backward_workspace_bytes(T, N, H, Hkv, dk, dv, x, out_gate is not None, window, sinks)
+    workspace = _workspace(workspace, need, dev)
+    _call(dev, "kda_attn_window_prefill_backward", T, H, Hkv, dk, dv, _addr(cu_seqlens), N, x,
+          dk ** -0.5 if scale is None else scale, window, sinks, _addr(q), _addr(k), _addr(v), _addr(out_gate), _addr(out),
+          _addr(lse), _addr(dy), _addr(g["dq"]), _addr(g["dk"]), _addr(g["dv"]), _addr(g["dz"]), _addr(workspace),
+          workspace.numel())
+    return g
+
+
 def _cache_shapes(k_cache, v_cache, page_table):
     """(num_pages, Hkv, page_size, dk, dv, slots, max_pages) of a cache."""
     pages, Hkv, page, dk = k_cache.shape
@@ -411,16 +470,10 @@ def kda_attn_tree_max_workspace_bytes(max_B, max_T, H, Hkv, dk, dv, x_dtype, max
     return int(lib().kda_attn_tree_max_workspace_bytes(max_B, max_T, H, Hkv, dk, dv, x_dtype, max_context))
 
 
-def kda_attn_tree(q, k_new, v_new, k_cache, v_cache, page_table, lens, tree_mask=None, out_gate=None,
-                  slot_indices=None, scale=None, workspace=None, out=None, lse=None):
-    """Drafted tokens q [B,T,H,dk] (T <= 64; T = 1 is plain decode) over the
-    paged cache and over each other: ``tree_mask`` int64 [B,T], bit j of word
-    t set where token t attends draft j (None: a chain).  k_new [B,T,Hkv,dk]
-    and v_new [B,T,Hkv,dv] are the drafts' own keys and values, not yet in the
-    cache.  Sequence b uses slot ``slot_indices[b]`` (None: b) of page_table
-    int32 [S,max_pages] and lens int32 [S]; an index outside [0, S) marks a
-    padding row, whose output is zero.  Returns (out [B,T,H,dv], lse fp32
-    [B,T,H])."""
+def _tree_call(name, need, view, q, k_new, v_new, k_cache, v_cache, page_table, lens, tree_mask, out_gate, slot_indices, scale,
+               workspace, out, lse):
+    """kda_attn_tree and, with ``view`` (window, sinks), kda_attn_window_tree;
+    ``need``: the call's workspace query."""
     B, T, H, dk = q.shape
     pages, Hkv, page, _, dv, slots, width = _cache_shapes(k_cache, v_cache, page_table)
     _shape("k_cache", k_cache, (pages, Hkv, page, dk), q.dtype)
@@ -444,12 +497,48 @@ def kda_attn_tree(q, k_new, v_new, k_cache, v_cache, page_table, lens, tree_mask
     else:
         _shape("lse", lse, (B, T, H), torch.float32)
     x = _dtype_code(q)
-    workspace = _workspace(workspace, kda_attn_tree_workspace_bytes(B, T, H, Hkv, dk, dv, x, width * page), dev)
-    _call(dev, "kda_attn_tree", B, T, H, Hkv, dk, dv, x, dk ** -0.5 if scale is None else scale,
+    workspace = _workspace(workspace, need(B, T, H, Hkv, dk, dv, x, width * page, *view), dev)
+    _call(dev, name, B, T, H, Hkv, dk, dv, x, dk ** -0.5 if scale is None else scale, *view,
           _addr(q), _addr(k_new), _addr(v_new), _addr(tree_mask), _addr(out_gate), _addr(k_cache), _addr(v_cache), pages, page,
           _addr(page_table), slots, width, _addr(lens), _addr(slot_indices), _addr(out), _addr(lse),
           _addr(workspace), workspace.numel())
     return out, lse
+
+
+def kda_attn_tree(q, k_new, v_new, k_cache, v_cache, page_table, lens, tree_mask=None, out_gate=None,
+                  slot_indices=None, scale=None, workspace=None, out=None, lse=None):
+    """Drafted tokens q [B,T,H,dk] (T <= 64; T = 1 is plain decode) over the
+    paged cache and over each other: ``tree_mask`` int64 [B,T], bit j of word
+    t set where token t attends draft j (None: a chain).  k_new [B,T,Hkv,dk]
+    and v_new [B,T,Hkv,dv] are the drafts' own keys and values, not yet in the
+    cache.  Sequence b uses slot ``slot_indices[b]`` (None: b) of page_table
+    int32 [S,max_pages] and lens int32 [S]; an index outside [0, S) marks a
+    padding row, whose output is zero.  Returns (out [B,T,H,dv], lse fp32
+    [B,T,H])."""
+    return _tree_call("kda_attn_tree", kda_attn_tree_workspace_bytes, (), q, k_new, v_new, k_cache, v_cache, page_table, lens,
+                      tree_mask, out_gate, slot_indices, scale, workspace, out, lse)
+
+
+def kda_attn_window_tree_workspace_bytes(B, T, H, Hkv, dk, dv, x_dtype, max_context, window, sinks):
+    """``max_context``: tokens that a page-table row can hold."""
+    return int(lib().kda_attn_window_tree_workspace_bytes(B, T, H, Hkv, dk, dv, _x_code(x_dtype), max_context, window, sinks))
+
+
+def kda_attn_window_tree_max_workspace_bytes(max_B, max_T, H, Hkv, dk, dv, x_dtype, max_context, window, sinks):
+    """What every call of up to ``max_B`` sequences of up to ``max_T`` tokens
+    with this window and these sinks needs at most."""
+    return int(lib().kda_attn_window_tree_max_workspace_bytes(max_B, max_T, H, Hkv, dk, dv, _x_code(x_dtype), max_context,
+                                                              window, sinks))
+
+
+def kda_attn_window_tree(q, k_new, v_new, k_cache, v_cache, page_table, lens, window, sinks=0, tree_mask=None, out_gate=None,
+                         slot_indices=None, scale=None, workspace=None, out=None, lse=None):
+    """kda_attn_tree with a sliding window: of a row's tokens in order, its
+    slot's and then the drafts of its mask word, the first ``sinks`` and the
+    last ``window`` are attended.  Returns (out [B,T,H,dv], lse fp32
+    [B,T,H])."""
+    return _tree_call("kda_attn_window_tree", kda_attn_window_tree_workspace_bytes, (window, sinks), q, k_new, v_new, k_cache,
+                      v_cache, page_table, lens, tree_mask, out_gate, slot_indices, scale, workspace, out, lse)
 
 
 def kda_cache_append(k_new, v_new, k_cache, v_cache, page_table, lens, cu_seqlens=None, rows=None, slot_indices=None):
@@ -565,6 +654,71 @@ def kda_cache_copy(pool, src, dst):
     row_bytes = pool.numel() // max(rows, 1) * pool.element_size()
     dev = _device(pool, src, dst)
     _call(dev, "kda_cache_copy", _addr(pool), row_bytes, rows, _addr(src), _addr(dst), n)
+
+
+def kda_cache_weigh_workspace_bytes(T_tot, N, H, Hkv, max_context):
+    """``max_context``: tokens that a page-table row can hold."""
+    return int(lib().kda_cache_weigh_workspace_bytes(T_tot, N, H, Hkv, max_context))
+
+
+def kda_cache_weigh(q, lse, k_cache, page_table, lens, weights, cu_seqlens=None, rows=None, slot_indices=None, window=0,
+                    sinks=0, scale=None, workspace=None):
+    """Adds the attention weights that each sequence's last tokens give to the
+    tokens of its slot to ``weights`` fp32 [S, max_pages * page]: sequence n's
+    queries cu_seqlens[n] .. cu_seqlens[n+1] - 1 of q [R,H,dk] and lse fp32
+    [R,H] (query t is row ``rows[t]``; None: row t) are the last tokens that
+    lens counts of slot ``slot_indices[n]`` (None: n).  ``window`` 0: a query
+    attends every token up to its own."""
+    R, H, dk = q.shape
+    pages, Hkv, page, _ = k_cache.shape
+    slots, width = page_table.shape
+    N = _n_seqs(cu_seqlens)
+    _shape("k_cache", k_cache, (pages, Hkv, page, dk), q.dtype)
+    _shape("lse", lse, (R, H), torch.float32)
+    _shape("page_table", page_table, (slots, width), torch.int32)
+    _shape("lens", lens, (slots,), torch.int32)
+    _shape("weights", weights, (slots, width * page), torch.float32)
+    T = R
+    if rows is not None:
+        T = rows.numel()
+        _shape("rows", rows, (T,), torch.int32)
+    if slot_indices is not None:
+        _shape("slot_indices", slot_indices, (N,), torch.int32)
+    dev = _device(q, lse, k_cache, page_table, lens, weights, cu_seqlens, rows, slot_indices, workspace)
+    workspace = _workspace(workspace, kda_cache_weigh_workspace_bytes(T, N, H, Hkv, width * page), dev)
+    _call(dev, "kda_cache_weigh", T, N, _addr(cu_seqlens), R, _addr(rows), H, Hkv, dk, _dtype_code(q),
+          dk ** -0.5 if scale is None else scale, window, sinks, _addr(q), _addr(lse), _addr(k_cache), pages, page,
+          _addr(page_table), slots, width, _addr(lens), _addr(slot_indices), _addr(weights), _addr(workspace),
+          workspace.numel())
+
+
+def kda_cache_evict_workspace_bytes(n, keep):
+    return int(lib().kda_cache_evict_workspace_bytes(n, keep))
+
+
+def kda_cache_evict(slot_list, keep, k_cache, v_cache, page_table, lens, refs, weights, first=0, recent=0, kept=None,
+                    status=None, workspace=None):
+    """Cuts the slots of ``slot_list`` (int32 [n]) down to ``keep`` tokens: the
+    first ``first``, the last ``recent`` and the heaviest between them by
+    ``weights`` fp32 [S, max_pages * page], moved to the front in their order.
+    Returns (kept int32 [n, keep]: the old places of what each slot holds now,
+    -1 behind; status int32 [n]: 0 done, 2 refused)."""
+    pages, Hkv, page, dk, dv, slots, width = _cache_shapes(k_cache, v_cache, page_table)
+    n = _slot_list("slot_list", slot_list)
+    _shape("lens", lens, (slots,), torch.int32)
+    _shape("refs", refs, (pages,), torch.int32)
+    _shape("weights", weights, (slots, width * page), torch.float32)
+    dev = _device(slot_list, k_cache, v_cache, page_table, lens, refs, weights, kept, status, workspace)
+    if kept is None:
+        kept = torch.empty((n, max(keep, 0)), dtype=torch.int32, device=dev)
+    else:
+        _shape("kept", kept, (n, keep), torch.int32)
+    status = _status(status, n, dev)
+    workspace = _workspace(workspace, kda_cache_evict_workspace_bytes(n, keep), dev)
+    _call(dev, "kda_cache_evict", n, _addr(slot_list), keep, first, recent, Hkv, dk, dv, _dtype_code(k_cache), _addr(k_cache),
+          _addr(v_cache), pages, page, _addr(page_table), slots, width, _addr(lens), _addr(refs), _addr(weights), _addr(kept),
+          _addr(status), _addr(workspace), workspace.numel())
+    return kept, status
 
 
 def kda_probe_peak(kind, blocks, iters=0, src=None, out=None):

@@ -512,6 +512,49 @@ int kda_attn_prefill_backward(int64_t T_tot, int32_t H, int32_t Hkv, int32_t dk,
                               void* stream);
 
 /*
+ * kda_attn_window_prefill, kda_attn_window_prefill_backward -- the same two
+ * calls for layers that see a bounded part of what is behind them: token i of
+ * a sequence attends its tokens j <= i with
+ *     i - j < window   or   j < sinks,
+ * the last `window` tokens, its own among them, and the sequence's first ones,
+ * which stay visible.  A window of the sequence's length or more is causal
+ * attention.  Work and time go by the pairs that are attended.
+ * Arguments: those of kda_attn_prefill and kda_attn_prefill_backward, and
+ *   window        >= 1;   sinks >= 0;
+ *   workspace     (gradients) sized by kda_attn_window_backward_workspace_bytes()
+ *                 with the call's sizes, window and sinks, or for every call of
+ *                 up to max_T_tot tokens in any number of sequences, with that
+ *                 window and those sinks, by
+ *                 kda_attn_window_backward_max_workspace_bytes().
+ * T_tot must be below 2^30, and the limits of the calls above hold
+ * (KDA_ERR_UNSUPPORTED otherwise).  A row that is not finite may also reach
+ * rows up to 190 tokens from those that attend it, and gradients of tokens as
+ * far from those that such rows attend.
+ */
+int kda_attn_window_prefill(int64_t T_tot, int32_t H, int32_t Hkv, int32_t dk, int32_t dv,
+                            const int32_t* cu_seqlens, int32_t N, int32_t x_dtype, float scale,
+                            int32_t window, int32_t sinks,
+                            const void* q, const void* k, const void* v,
+                            const void* out_gate,
+                            void* out, float* lse,
+                            void* stream);
+size_t kda_attn_window_backward_workspace_bytes(int64_t T_tot, int32_t N, int32_t H, int32_t Hkv,
+                                                int32_t dk, int32_t dv, int32_t x_dtype, int32_t with_gate,
+                                                int32_t window, int32_t sinks);
+size_t kda_attn_window_backward_max_workspace_bytes(int64_t max_T_tot, int32_t H, int32_t Hkv,
+                                                    int32_t dk, int32_t dv, int32_t x_dtype, int32_t with_gate,
+                                                    int32_t window, int32_t sinks);
+int kda_attn_window_prefill_backward(int64_t T_tot, int32_t H, int32_t Hkv, int32_t dk, int32_t dv,
+                                     const int32_t* cu_seqlens, int32_t N, int32_t x_dtype, float scale,
+                                     int32_t window, int32_t sinks,
+                                     const void* q, const void* k, const void* v,
+                                     const void* out_gate, const void* out, const float* lse,
+                                     const void* dy,
+                                     void* grad_q, void* grad_k, void* grad_v, void* grad_out_gate,
+                                     void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
+/*
  * A paged cache of keys and values.
  *   k_cache [num_pages, Hkv, page_size, dk], v_cache [num_pages, Hkv,
  *   page_size, dv]: the pools (x_dtype; page_size a power of two, 16 .. 1024);
@@ -569,6 +612,35 @@ int kda_attn_tree(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t dk, int3
                   void* out, float* lse,
                   void* workspace, size_t workspace_bytes,
                   void* stream);
+
+/*
+ * kda_attn_window_tree -- kda_attn_tree for such layers, over the same cache.
+ * The tokens of a row in order are the slot's lens[slot] tokens and then, by
+ * their number, the drafts of the row's mask word, n in all; the row attends
+ * those at places below `sinks` and from n - window on.  For a draft's own path
+ * from the context (its own bit included) that is the view of
+ * kda_attn_window_prefill.  A cached token whose entry names no page keeps its
+ * place and is not attended, so pages that no row will see again can go.
+ * Arguments: those of kda_attn_tree, and window >= 1, sinks >= 0; workspace by
+ * the two functions below.  max_pages x page_size must be below 2^30
+ * (KDA_ERR_UNSUPPORTED otherwise).
+ */
+size_t kda_attn_window_tree_workspace_bytes(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t dk,
+                                            int32_t dv, int32_t x_dtype, int64_t max_context,
+                                            int32_t window, int32_t sinks);
+size_t kda_attn_window_tree_max_workspace_bytes(int32_t max_B, int32_t max_T, int32_t H, int32_t Hkv,
+                                                int32_t dk, int32_t dv, int32_t x_dtype, int64_t max_context,
+                                                int32_t window, int32_t sinks);
+int kda_attn_window_tree(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t dk, int32_t dv,
+                         int32_t x_dtype, float scale, int32_t window, int32_t sinks,
+                         const void* q, const void* k_new, const void* v_new,
+                         const int64_t* tree_mask, const void* out_gate,
+                         const void* k_cache, const void* v_cache, int32_t num_pages, int32_t page_size,
+                         const int32_t* page_table, int32_t slots, int32_t max_pages,
+                         const int32_t* lens, const int32_t* slot_indices,
+                         void* out, float* lse,
+                         void* workspace, size_t workspace_bytes,
+                         void* stream);
 
 /*
  * kda_cache_append -- writes the keys and values of new tokens into pages.
@@ -665,6 +737,87 @@ int kda_cache_compact(int32_t Hkv, int32_t dk, int32_t dv, int32_t x_dtype,
                       void* workspace, size_t workspace_bytes, void* stream);
 int kda_cache_copy(void* pool, int64_t row_bytes, int32_t rows,
                    const int32_t* src, const int32_t* dst, int32_t n, void* stream);
+
+/*
+ * kda_cache_weigh -- how much attention each cached token gets: for a
+ * sequence's last tokens, whose queries are at hand, adds their attention
+ * weights to what the tokens of its slot have gathered,
+ *     weights[slot][j] += sum_i sum_h e^(scale q_ih . k_j - lse_ih),
+ * over the queries i that attend token j and all heads h.  Sequence n's
+ * queries t = cu_seqlens[n] .. cu_seqlens[n+1] - 1, c of them, are the last c
+ * tokens of its slot (they have been appended and lens counts them): the i-th
+ * stands at place p = lens[slot] - c + i and attends the places j <= p, with
+ * window > 0 those with p - j < window or j < sinks.  So one call serves a
+ * decode step, the accepted path of each draft tree (rows: b * T + the path's
+ * tokens, in order), the last tokens of a prompt or all of it.
+ * Arguments:
+ *   q [src_rows, H, dk], lse fp32 [src_rows, H]: the queries and what the
+ *                 attention call gave for them; rows int32 [T_tot] or NULL
+ *                 (query t is row t);
+ *   window        0 (every token up to the query's own) or as the attention
+ *                 call's, with its sinks;
+ *   weights       fp32 [slots, max_pages * page_size], added to; a slot's start
+ *                 at 0 with it.  kda_cache_copy forks rows of it;
+ *   slot_indices  NULL (sequence n uses slot n) or int32 [N], distinct where
+ *                 the sequences are not empty;
+ *   workspace     at least kda_cache_weigh_workspace_bytes() bytes for
+ *                 max_context = max_pages * page_size, 256-byte aligned;
+ *                 contents on entry are ignored.
+ * Products, exponentials and sums are fp32, in a fixed order: the same inputs
+ * give the same bits.  A weight is as right as its lse (see the gradients).
+ * Skipped: slots outside [0, slots), rows outside [0, src_rows), queries
+ * before the slot's first token, rows whose lse is not finite.  Tokens that no
+ * query attends and those whose entry names no page keep what they have.
+ * T_tot and max_pages x page_size must be below 2^30, N below 2^23
+ * (KDA_ERR_UNSUPPORTED otherwise).
+ */
+size_t kda_cache_weigh_workspace_bytes(int64_t T_tot, int32_t N, int32_t H, int32_t Hkv, int64_t max_context);
+int kda_cache_weigh(int64_t T_tot, int32_t N, const int32_t* cu_seqlens,
+                    int64_t src_rows, const int32_t* rows,
+                    int32_t H, int32_t Hkv, int32_t dk, int32_t x_dtype, float scale,
+                    int32_t window, int32_t sinks,
+                    const void* q, const float* lse,
+                    const void* k_cache, int32_t num_pages, int32_t page_size,
+                    const int32_t* page_table, int32_t slots, int32_t max_pages,
+                    const int32_t* lens, const int32_t* slot_indices,
+                    float* weights,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * kda_cache_evict -- cuts slots down to `keep` tokens.  Of a slot that holds
+ * more, the first `first` and the last `recent` tokens stay, and of those
+ * between them the keep - first - recent that have gathered the largest
+ * weights, the earlier of two that are equal (NaN is below every number).  They
+ * move to the front of the slot's pages in their order, rows of k_cache and
+ * v_cache and their weights; the weights behind them up to the old length
+ * become 0, the table's entries behind them -1 and their pages' counts drop by
+ * one each; lens becomes keep.  A slot of keep tokens or fewer is left alone.
+ * Arguments:
+ *   slot_list     int32 [n], n below 2^16 (KDA_ERR_UNSUPPORTED otherwise);
+ *   keep          >= 1;   first, recent >= 0, together at most keep;
+ *   weights       fp32 [slots, max_pages * page_size], as kda_cache_weigh;
+ *   kept          NULL or int32 [n, keep], written: the old places of the tokens
+ *                 that the slot holds now, rising, -1 behind them (a refused
+ *                 entry: all -1);
+ *   status        NULL or int32 [n], written: 0 done, 2 refused;
+ *   workspace     at least kda_cache_evict_workspace_bytes(n, keep) bytes,
+ *                 256-byte aligned; contents on entry are ignored.
+ * Refused, changing nothing: a slot outside [0, slots) or that an earlier entry
+ * names; a slot to be cut of which an entry within its length names no page;
+ * one where a page that would be written, or a last page that stays partly
+ * filled, has another entry that names it (refs above 1): pages of a shared
+ * prefix of at most `first` tokens stay shared.  max_pages x page_size must be below
+ * 2^30 and Hkv below 2^15 (KDA_ERR_UNSUPPORTED otherwise).
+ */
+size_t kda_cache_evict_workspace_bytes(int32_t n, int32_t keep);
+int kda_cache_evict(int32_t n, const int32_t* slot_list, int32_t keep, int32_t first, int32_t recent,
+                    int32_t Hkv, int32_t dk, int32_t dv, int32_t x_dtype,
+                    void* k_cache, void* v_cache, int32_t num_pages, int32_t page_size,
+                    int32_t* page_table, int32_t slots, int32_t max_pages,
+                    int32_t* lens, int32_t* refs,
+                    float* weights,
+                    int32_t* kept, int32_t* status,
+                    void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Kernel timing for profiling tools (not needed for normal use).

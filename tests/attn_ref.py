@@ -46,7 +46,16 @@ def causal(n, device):
     return torch.ones(n, n, dtype=torch.bool, device=device).tril()
 
 
-def prefill(q, k, v, z, lens, scale, dtype):
+def windowed(window, sinks):
+    """The view of a sliding window: the last `window` tokens and the first `sinks`."""
+    def view(n, device):
+        t = torch.arange(n, device=device)
+        d = t[:, None] - t
+        return (d >= 0) & ((d < window) | (t < sinks))
+    return view
+
+
+def prefill(q, k, v, z, lens, scale, dtype, view=causal):
     """Packed reference: (out, bound, lse, bound), rows behind the last sequence NaN."""
     T, H, _ = q.shape
     G, dv, u = H // k.shape[1], v.shape[2], UNIT[dtype]
@@ -60,7 +69,7 @@ def prefill(q, k, v, z, lens, scale, dtype):
         if n == 0:
             continue
         for h in range(H):
-            o, b, l, e, _, _ = softmax_rows(q[r, h], k[r, h // G], v[r, h // G], scale, causal(n, q.device), u)
+            o, b, l, e, _, _ = softmax_rows(q[r, h], k[r, h // G], v[r, h // G], scale, view(n, q.device), u)
             if z is not None:
                 g = torch.sigmoid(z[r, h])
                 o, b = o * g, b * g + o.abs() * g * 2.0 ** -20
@@ -69,7 +78,7 @@ def prefill(q, k, v, z, lens, scale, dtype):
     return out, bo, lse, bl
 
 
-def backward(q, k, v, z, dy, lens, scale, dtype):
+def backward(q, k, v, z, dy, lens, scale, dtype, view=causal):
     """Packed reference gradients {name: (value, bound)}."""
     T, H, dk = q.shape
     Hkv, dv, u = k.shape[1], v.shape[2], UNIT[dtype]
@@ -88,7 +97,7 @@ def backward(q, k, v, z, dy, lens, scale, dtype):
         fs = (n + 8) * F * 2 * max(1, G)
         for h in range(H):
             f = h // G
-            o, bo, _, _, p, eps = softmax_rows(q[r, h], k[r, f], v[r, f], scale, causal(n, dev), u)
+            o, bo, _, _, p, eps = softmax_rows(q[r, h], k[r, f], v[r, f], scale, view(n, dev), u)
             do = dy[r, h]
             if gated:
                 s = torch.sigmoid(z[r, h])
