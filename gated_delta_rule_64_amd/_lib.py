@@ -83,7 +83,7 @@ PROTOTYPES.update({
     "kda_attn_window_tree_workspace_bytes": (_sz, [_i32] * 7 + [_i64, _i32, _i32]),
     "kda_attn_window_tree_max_workspace_bytes": (_sz, [_i32] * 7 + [_i64, _i32, _i32]),
     "kda_attn_window_tree": (ctypes.c_int, [_i32] * 7 + [_f32, _i32, _i32] + [_vp] * 5 + _POOLS + _TABLE + [_vp] * 4 + _WORK),
-    "kda_cache_weigh_workspace_bytes": (_sz, [_i64, _i32, _i32, _i32, _i64]),
+    "kda_cache_weigh_workspace_bytes": (_sz, [_i64, _i32, _i32, _i32]),
     "kda_cache_weigh": (ctypes.c_int, [_i64, _i32, _vp, _i64, _vp] + [_i32] * 4 + [_f32, _i32, _i32, _vp, _vp, _vp, _i32, _i32] + _TABLE +
                         [_vp] * 3 + _WORK),
     "kda_cache_evict_workspace_bytes": (_sz, [_i32, _i32]),

@@ -778,14 +778,14 @@ struct View {
 };
 constexpr View kWhole{false, 0, 0};
 
-constexpr int64_t kMostWindowed = int64_t(1) << 30;  // places and windows add up in 32 bits
+constexpr int64_t kMostWindowed = int64_t(1) << 29;  // places, windows and first tokens add up in 32 bits
 
 // tokens: as many as a sequence of the call can have.
 int check_view(const View& view, int64_t tokens, const char* name) {
     if (!view.bounded) return KDA_OK;
     if (view.window < 1) return fail(KDA_ERR_INVALID_ARGUMENT, "window=%d must be >= 1", view.window);
     if (view.sinks < 0) return fail(KDA_ERR_INVALID_ARGUMENT, "sinks=%d is negative", view.sinks);
-    if (tokens >= kMostWindowed) return fail(KDA_ERR_UNSUPPORTED, "%s=%lld is not below 2^30 with a window", name, (long long)tokens);
+    if (tokens >= kMostWindowed) return fail(KDA_ERR_UNSUPPORTED, "%s=%lld is not below 2^29 with a window", name, (long long)tokens);
     return KDA_OK;
 }
 
@@ -1215,11 +1215,9 @@ int kda_cache_copy(void* pool, int64_t row_bytes, int32_t rows, const int32_t* s
     return ok();
 }
 
-size_t kda_cache_weigh_workspace_bytes(int64_t T_tot, int32_t N, int32_t H, int32_t Hkv, int64_t max_context) {
-    if (T_tot < 0 || T_tot >= kMostWindowed || N < 1 || H < 1 || H > 65535 || Hkv < 1 || H % Hkv != 0 || max_context < 1 ||
-        max_context >= kMostWindowed)
-        return 0;
-    return kda::cache_weigh_workspace_bytes(T_tot, N, H, Hkv, max_context);
+size_t kda_cache_weigh_workspace_bytes(int64_t T_tot, int32_t N, int32_t H, int32_t Hkv) {
+    if (T_tot < 0 || T_tot >= kMostWindowed || N < 1 || H < 1 || H > 65535 || Hkv < 1 || H % Hkv != 0) return 0;
+    return kda::cache_weigh_workspace_bytes(T_tot, N, H, Hkv);
 }
 
 int kda_cache_weigh(int64_t T_tot, int32_t N, const int32_t* cu_seqlens, int64_t src_rows, const int32_t* rows, int32_t H,
@@ -1231,7 +1229,7 @@ int kda_cache_weigh(int64_t T_tot, int32_t N, const int32_t* cu_seqlens, int64_t
     int st = check_heads(H, Hkv, dk, dv, x_dtype, scale);
     if (st != KDA_OK) return st;
     if (T_tot < 0 || T_tot >= (int64_t(1) << 31)) return fail(KDA_ERR_INVALID_ARGUMENT, "T_tot=%lld out of range [0, 2^31)", (long long)T_tot);
-    if (T_tot >= kMostWindowed) return fail(KDA_ERR_UNSUPPORTED, "T_tot=%lld is not below 2^30", (long long)T_tot);
+    if (T_tot >= kMostWindowed) return fail(KDA_ERR_UNSUPPORTED, "T_tot=%lld is not below 2^29", (long long)T_tot);
     if (N < 1) return fail(KDA_ERR_INVALID_ARGUMENT, "N=%d must be >= 1", N);
     if (N >= kMostGroups / 2) return fail(KDA_ERR_UNSUPPORTED, "N=%d: the workgroups are not below 2^24", N);
     if (cu_seqlens == nullptr && N != 1) return fail(KDA_ERR_INVALID_ARGUMENT, "cu_seqlens is NULL but N=%d", N);
@@ -1247,9 +1245,9 @@ int kda_cache_weigh(int64_t T_tot, int32_t N, const int32_t* cu_seqlens, int64_t
                     max_pages, const_cast<int32_t*>(lens), nullptr, c);
     if (st != KDA_OK) return st;
     const int64_t most = static_cast<int64_t>(max_pages) << c.page_shift;
-    if (most >= kMostWindowed) return fail(KDA_ERR_UNSUPPORTED, "max_pages x page_size = %lld is not below 2^30", (long long)most);
+    if (most >= kMostWindowed) return fail(KDA_ERR_UNSUPPORTED, "max_pages x page_size = %lld is not below 2^29", (long long)most);
     if (T_tot == 0) return ok();
-    const size_t xs = dsize(x_dtype), need = kda_cache_weigh_workspace_bytes(T_tot, N, H, Hkv, most);
+    const size_t xs = dsize(x_dtype), need = kda_cache_weigh_workspace_bytes(T_tot, N, H, Hkv);
     const Span sp[] = {
         {"q", q, static_cast<size_t>(src_rows) * H * dk * xs, false}, {"lse", lse, static_cast<size_t>(src_rows) * H * 4, false, 4},
         {"k_cache", k_cache, pool_bytes(c, dk), false}, {"page_table", page_table, table_bytes(slots, max_pages), false, 4},
@@ -1292,8 +1290,8 @@ int kda_cache_evict(int32_t n, const int32_t* slot_list, int32_t keep, int32_t f
     if (static_cast<int64_t>(first) + recent > keep)
         return fail(KDA_ERR_INVALID_ARGUMENT, "first=%d and recent=%d are more than keep=%d", first, recent, keep);
     const int64_t most = static_cast<int64_t>(max_pages) << c.page_shift;
-    if (most >= kMostWindowed) return fail(KDA_ERR_UNSUPPORTED, "max_pages x page_size = %lld is not below 2^30", (long long)most);
-    if (keep >= kMostWindowed) return fail(KDA_ERR_UNSUPPORTED, "keep=%d is not below 2^30", keep);
+    if (most >= kMostWindowed) return fail(KDA_ERR_UNSUPPORTED, "max_pages x page_size = %lld is not below 2^29", (long long)most);
+    if (keep >= kMostWindowed) return fail(KDA_ERR_UNSUPPORTED, "keep=%d is not below 2^29", keep);
     if (n == 0) return ok();
     const size_t need = kda_cache_evict_workspace_bytes(n, keep), per = static_cast<size_t>(n) * 4;
     const Span sp[] = {

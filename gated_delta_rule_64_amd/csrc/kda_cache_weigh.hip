@@ -5,10 +5,11 @@
 //   s_ijh = scale q_ih . k_j(h / G), over the keys j that query i attends
 //
 // lse is what the attention call gave, so the weights need no statistics of
-// their own: one pass over the keys, no values.  The scores are formed
-// transposed (S^T = K Q^T, 32 keys by 32 rows of queries and heads), so that a
-// lane's lse stays in one register and its 16 sums, one per key that it holds,
-// are added over the lanes once per tile of keys, not once per product.
+// their own: one pass over the keys, no values.
+//
+// Sequences of few queries (their rows of one key head, queries x heads of the
+// group, are at most 32) and of many are worked on in different ways, both in
+// one launch, since only the device knows a sequence's queries.
 #include "kda_attn_common.h"
 #include "kda_internal.h"
 #include "kda_profile.h"
@@ -20,142 +21,455 @@ using namespace attn;
 
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
-constexpr int kKeys = 32;  // keys of a tile
+constexpr int kRows = 32;  // rows of a product: queries of a head, or queries and heads of a group
 
 struct WeighK {
     CacheArgs c;
     WeighArgs a;
-    int splits;
+    int few_groups, many_groups;  // workgroups of a sequence, of either kind
+    int most_parts;               // that the work of a tile of the second kind may be cut into
+    float* part;                  // [N, many_groups][keys of a tile]
 };
 
 // Sequence n's queries and its slot's tokens; false: nothing to do.
 struct Weighed {
     int64_t first;  // its first query's index
     int count, slot, ctx;
+    int p_first;    // the first query's place; below 0: it has no token
 };
 __device__ __forceinline__ bool weighed(const WeighK& k, int n, Weighed& w) {
     seq_bounds(k.a.cu, n, k.a.tokens, w.first, w.count);
-    w.slot = k.a.slot_indices != nullptr ? k.a.slot_indices[n] : n;
-    if (w.count == 0 || w.slot < 0 || w.slot >= k.c.slots) return false;
-    const int64_t most = static_cast<int64_t>(k.c.max_pages) << k.c.page_shift;
-    const int len = k.c.lens[w.slot];
-    w.ctx = len < 0 ? 0 : static_cast<int>(len > most ? most : len);
-    w.slot = uniform(w.slot);
-    w.ctx = uniform(w.ctx);
     w.count = uniform(w.count);
     w.first = uniform64(w.first);
+    const int slot = k.a.slot_indices != nullptr ? k.a.slot_indices[n] : n;
+    w.slot = uniform(slot);
+    if (w.count == 0 || slot < 0 || slot >= k.c.slots || k.a.src_rows == 0) return false;
+    const int64_t most = static_cast<int64_t>(k.c.max_pages) << k.c.page_shift;
+    const int len = k.c.lens[slot];
+    w.ctx = uniform(len < 0 ? 0 : static_cast<int>(len > most ? most : len));
+    w.p_first = w.ctx - w.count;
     return w.ctx > 0;
 }
+// A sequence that the first kind takes, where it is launched.
+__device__ __forceinline__ bool few(const WeighK& k, const Weighed& w, int G) {
+    return k.few_groups > 0 && static_cast<int64_t>(w.count) * G <= kRows;
+}
 
-// One workgroup per (sequence, part of its tiles): the waves share out the
-// (key head, block of 32 rows) pairs of a tile, their sums are added in LDS.
+// The tiles of `keys` keys that some query attends, in order (the n-th begins at
+// key first(n)): those of the first tokens and those from the first query's
+// window on.
+struct Tiles {
+    int keys, sinks, sink_tiles, skip, count;
+    __device__ __forceinline__ Tiles(const WeighArgs& a, const Weighed& w, int keys_) : keys(keys_) {
+        const int low = a.window > 0 ? max(0, w.p_first - a.window + 1) : 0;
+        sinks = a.window > 0 ? min(a.sinks, w.ctx) : 0;
+        sink_tiles = (sinks + keys - 1) / keys;
+        skip = max(0, low / keys - sink_tiles);
+        count = (w.ctx + keys - 1) / keys - skip;
+    }
+    __device__ __forceinline__ int first(int n) const { return (n >= sink_tiles ? n + skip : n) * keys; }
+};
+
+// The row of place `pos` in head 0 of the pool, and whether it holds a token.
+__device__ __forceinline__ int64_t row_of(const WeighK& k, const Weighed& w, int pos, bool& there) {
+    const CacheArgs& c = k.c;
+    const int page = pos < w.ctx ? c.table[static_cast<int64_t>(w.slot) * c.max_pages + (pos >> c.page_shift)] : -1;
+    there = page >= 0 && page < c.pages;
+    return ((static_cast<int64_t>(there ? page : 0) * c.Hkv) << c.page_shift) + (there ? pos & ((1 << c.page_shift) - 1) : 0);
+}
+
+__device__ __forceinline__ float* weight_of(const WeighK& k, const Weighed& w, int pos) {
+    return k.a.weights + ((static_cast<int64_t>(w.slot) * k.c.max_pages) << k.c.page_shift) + pos;
+}
+
+// What a key has gathered: a sum that is NaN comes from a key that is not
+// finite.  A row that attends such a key has an lse that is not finite (and
+// weighs nothing) or no weight there.
+__device__ __forceinline__ float gathered(float x) { return x == x ? x : 0.f; }
+
+// Few queries: bound by reading the keys.  Scores transposed (S^T = K Q^T, 32
+// keys by the group's rows), a lane's row and its lse the same for every tile,
+// its 16 sums added over the lanes once per tile.  A wave takes its own tiles,
+// all heads of one after another (or shares a tile's heads with the others of
+// its workgroup, where there are few tiles), the next head's keys in flight
+// while one is worked on.
 template <typename T, int DK>
-__global__ __launch_bounds__(kThreads) void cache_weigh_kernel(WeighK k) {
-    constexpr int kQPieces = DK / (2 * Elem<T>::kPer16);
+__device__ __forceinline__ void weigh_few(const WeighK& k, unsigned block, float (*sums)[32]) {
+    constexpr int kKeys = 32;
+    constexpr int kPieces = DK / (2 * Elem<T>::kPer16);
     constexpr int kRow = DK * static_cast<int>(sizeof(T));
-    __shared__ float sums[kWaves][kKeys];
     const CacheArgs& c = k.c;
     const WeighArgs& a = k.a;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int col = lane & 31, half = lane >> 5;
-    const int n = blockIdx.x / k.splits, split = blockIdx.x % k.splits;
+    const int n = block / k.few_groups, group = block % k.few_groups;
     Weighed w;
     if (!weighed(k, n, w)) return;
     const int G = a.H / c.Hkv;
-    const int64_t rows = static_cast<int64_t>(w.count) * G;  // of a key head
-    const int p_first = w.ctx - w.count;  // the first query's place; below 0: it has no token
-    const int low = a.window > 0 ? max(0, p_first - a.window + 1) : 0;
-    const int sinks = a.window > 0 ? min(a.sinks, w.ctx) : 0;
-    const int sink_tiles = (sinks + kKeys - 1) / kKeys, skip = max(0, low / kKeys - sink_tiles);
-    const int tiles = (w.ctx + kKeys - 1) / kKeys - skip;
-    const int blocks = static_cast<int>((rows + 31) / 32);
-    const int64_t items = static_cast<int64_t>(blocks) * c.Hkv;
-    const int32_t* table = c.table + static_cast<int64_t>(w.slot) * c.max_pages;
+    if (!few(k, w, G)) return;
+    const Tiles tiles(a, w, kKeys);
+    // this lane's row: a query and a head of the group
+    const int rows = w.count * G, r = min(col, rows - 1);
+    const int64_t t = w.first + r / G, src = a.rows != nullptr ? a.rows[t] : t;
+    const int p_here = max(w.p_first + r / G, -1);
+    const bool on = col < rows && p_here >= 0 && src >= 0 && src < a.src_rows;
+    const int64_t q_at = (on ? src : 0) * a.H + r % G;  // of key head 0
+    const char* q_row = static_cast<const char*>(a.q) + q_at * kRow + half * 16;
+    const float* lse_at = a.lse + q_at;
     const float sc = a.scale * kLog2e;
-    for (int tile = split; tile < tiles; tile += k.splits) {
-        const int first = (tile >= sink_tiles ? tile + skip : tile) * kKeys;
-        // the row of this lane's key
-        const int pos = first + col;
-        const int page = pos < w.ctx ? table[pos >> c.page_shift] : -1;
-        const bool there = page >= 0 && page < c.pages;
-        const int64_t at = ((static_cast<int64_t>(there ? page : 0) * c.Hkv) << c.page_shift) + (pos & ((1 << c.page_shift) - 1));
-        f32x16 acc{};
-        u32x4 kf[kQPieces];
-        int kvh = -1;
-        for (int64_t item = items * wave / kWaves; item < items * (wave + 1) / kWaves; ++item) {
-            const int f = static_cast<int>(item / blocks), block = static_cast<int>(item % blocks);
-            if (f != kvh) {
-                kvh = f;
-                const char* from = static_cast<const char*>(c.k_cache) + (at + (static_cast<int64_t>(kvh) << c.page_shift)) * kRow + half * 16;
+    // Where there are few tiles, waves share one and take equal runs of its heads.
+    const int64_t all = static_cast<int64_t>(tiles.count) * a.N;
+    const int share = all >= 4096 || c.Hkv < 2 ? 1 : all >= 2048 || c.Hkv < 4 ? 2 : 4;
+    const int member = wave % share, team = wave / share, teams = kWaves / share;
+    const int f0 = c.Hkv * member / share, f1 = c.Hkv * (member + 1) / share;
+    struct Item {
+        u32x4 key[kPieces], q[kPieces];
+        float lse;
+    };
+    const char* pool = static_cast<const char*>(c.k_cache);
+    auto load = [&](Item& x, int64_t at, int f) __attribute__((always_inline)) {
+        const char* from = pool + (at + (static_cast<int64_t>(f) << c.page_shift)) * kRow + half * 16;
+        const char* q = q_row + static_cast<int64_t>(f) * G * kRow;
+        x.lse = lse_at[static_cast<int64_t>(f) * G];
 #pragma unroll
-                for (int p = 0; p < kQPieces; ++p) kf[p] = there ? *reinterpret_cast<const u32x4*>(from + p * 32) : u32x4{};
-            }
-            // this lane's row: a query and a head
-            const int64_t r = static_cast<int64_t>(block) * 32 + col;
-            const int token = static_cast<int>(min(r, rows - 1) / G), h = kvh * G + static_cast<int>(min(r, rows - 1) % G);
-            const int64_t t = w.first + token;
-            const int64_t src = a.rows != nullptr ? a.rows[t] : t;
-            const int p_here = max(p_first + token, -1);
-            bool on = r < rows && p_here >= 0 && src >= 0 && src < a.src_rows;
-            const int64_t q_at = (on ? src : 0) * a.H + h;
-            const float lse = on ? a.lse[q_at] : 0.f;
-            on = on && fabsf(lse) < INFINITY;  // a row that attends nothing, or a broken one, weighs nothing
-            const char* q_row = static_cast<const char*>(a.q) + q_at * kRow + half * 16;
-            f32x16 s{};
+        for (int p = 0; p < kPieces; ++p) x.q[p] = *reinterpret_cast<const u32x4*>(q + p * 32);
 #pragma unroll
-            for (int p = 0; p < kQPieces; ++p) {
-                const u32x4 q = on ? *reinterpret_cast<const u32x4*>(q_row + p * 32) : u32x4{};
-                s = mma<T>(kf[p], q, s);
-            }
-            const float lse2 = lse * kLog2e;
-            const int most = on ? p_here - first - 4 * half : INT32_MIN;
-            const int least = a.window > 0 ? p_here - a.window + 1 - first - 4 * half : INT32_MIN, sink = sinks - first - 4 * half;
+        for (int p = 0; p < kPieces; ++p) x.key[p] = *reinterpret_cast<const u32x4*>(from + p * 32);
+    };
+    f32x16 acc{};
+    auto work = [&](const Item& x, int first) __attribute__((always_inline)) {
+        f32x16 s{};
 #pragma unroll
-            for (int x = 0; x < 16; ++x) {
-                const int key = 8 * (x / 4) + x % 4;
-                const float e = __builtin_amdgcn_exp2f(fmaf(s[x], sc, -lse2));
-                acc[x] += key <= most && (key >= least || key < sink) ? e : 0.f;
+        for (int p = 0; p < kPieces; ++p) s = mma<T>(x.key[p], x.q[p], s);
+        const bool good = on && fabsf(x.lse) < INFINITY;  // a row that attends nothing, or a broken one, weighs nothing
+        const float lse2 = x.lse * kLog2e;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] = good ? __builtin_amdgcn_exp2f(fmaf(s[i], sc, -lse2)) : 0.f;
+        if (first + kKeys - 1 > w.p_first || (a.window > 0 && first < w.ctx - a.window && first + kKeys > tiles.sinks)) {
+            const int most = opaque(p_here - first - 4 * half);
+            const int least = opaque(a.window > 0 ? p_here - a.window + 1 - first - 4 * half : INT32_MIN / 2);
+            const int sink = opaque(tiles.sinks - first - 4 * half);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int key = 8 * (i / 4) + i % 4;
+                if (key > most || outside(key, least, sink)) s[i] = 0.f;
             }
         }
-        // over the lanes of a half: the rows of queries
+        acc += s;
+    };
+    auto finish = [&](int first, bool there) __attribute__((always_inline)) {
+        // over the lanes of a half; key 8 (i / 4) + 4 half + i % 4
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
-            float v = row_ror_add<1>(acc[x]);
+        for (int i = 0; i < 16; ++i) {
+            float v = row_ror_add<1>(acc[i]);
             v = row_ror_add<2>(v);
             v = row_ror_add<4>(v);
             v = xor16_add(row_ror_add<8>(v));
-            if (col == 0) sums[wave][8 * (x / 4) + 4 * half + x % 4] = v;
+            if (col == 0) sums[wave][8 * (i / 4) + 4 * half + i % 4] = v;
         }
-        __syncthreads();
-        if (threadIdx.x < kKeys && there) {  // (thread j holds key j's place)
+        acc = f32x16{};
+        if (share > 1) __syncthreads();
+        else wave_lds_fence();
+        if (member == 0 && half == 0 && there) {
             float v = 0.f;
-#pragma unroll
-            for (int x = 0; x < kWaves; ++x) v += sums[x][threadIdx.x];
-            a.weights[(static_cast<int64_t>(w.slot) * c.max_pages << c.page_shift) + pos] += v;
+            for (int x = 0; x < share; ++x) v += sums[wave + x][col];
+            *weight_of(k, w, first + col) += gathered(v);
         }
-        __syncthreads();
+        if (share > 1) __syncthreads();
+        else wave_lds_fence();
+    };
+    // every wave of a workgroup takes as many turns (they meet where they share)
+    const int stride = k.few_groups * teams;
+    const int turns = (tiles.count - group * teams + stride - 1) / stride;
+    if (turns <= 0) return;
+    int tile = group * teams + team;
+    auto look = [&](int tile, bool& there) { return row_of(k, w, tile < tiles.count ? tiles.first(tile) + col : w.ctx, there); };
+    bool there, next_there = false;
+    int64_t at = look(tile, there), next_at = 0;
+    Item x, y;
+    load(x, at, f0);
+    for (int turn = 0; turn < turns; ++turn) {
+        const int first = tile < tiles.count ? tiles.first(tile) : 0;
+        next_at = look(tile + stride, next_there);
+        int f = f0;
+        for (; f + 1 < f1; f += 2) {
+            load(y, at, f + 1);
+            work(x, first);
+            if (f + 2 < f1) load(x, at, f + 2);
+            else load(x, next_at, f0);
+            work(y, first);
+        }
+        if (f < f1) {
+            load(y, next_at, f0);
+            work(x, first);
+            x = y;
+        }
+        finish(first, there);
+        tile += stride;
+        at = next_at;
+        there = next_there;
     }
 }
 
-constexpr int kWantGroups = 2048;
+template <typename T, int DK>
+struct ManySizes {
+    static constexpr int kSub = sizeof(T) == 2 ? 2 : 1;  // blocks of 32 keys of a wave, in its registers
+    static constexpr int kKeys = kWaves * 32 * kSub;
+    static constexpr int kTile = kRows * DK * static_cast<int>(sizeof(T));
+    static constexpr int kBuf = kTile + kRows * 4;  // rows of queries and their lse
+};
+
+// How a sequence's tiles go to its workgroups: a tile each in turn, or, where
+// there are fewer tiles, several to a tile, that take equal parts of its work.
+struct Shares {
+    int parts;
+    __device__ __forceinline__ Shares(const WeighK& k, int tiles)
+        : parts(tiles >= k.many_groups ? 1 : min(k.many_groups / max(tiles, 1), k.most_parts)) {}
+};
+
+// Many queries: bound by the products and exponentials.  One workgroup per
+// (sequence, tile of keys, part): a wave's keys stay in its registers, the
+// queries of a head pass through LDS 32 at a time, once for four waves.  S =
+// Q K^T, so that a lane holds one key's scores and one sum.  The tile's work is
+// the sequence of its steps of 32 queries, head by head.
+template <typename T, int DK>
+__device__ __forceinline__ void weigh_many(const WeighK& k, unsigned block, char* smem) {
+    using Sz = ManySizes<T, DK>;
+    constexpr int kSub = Sz::kSub, kKeys = Sz::kKeys;
+    constexpr int kPieces = DK / (2 * Elem<T>::kPer16);
+    constexpr int kRow = DK * static_cast<int>(sizeof(T)), kRowPieces = kRow / 16;
+    constexpr int kEach = (kRows * kRowPieces + kThreads - 1) / kThreads;
+    const CacheArgs& c = k.c;
+    const WeighArgs& a = k.a;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int col = lane & 31, half = lane >> 5;
+    const int n = block / k.many_groups, group = block % k.many_groups;
+    Weighed w;
+    if (!weighed(k, n, w)) return;
+    const int G = a.H / c.Hkv;
+    if (few(k, w, G)) return;
+    const Tiles tiles(a, w, kKeys);
+    const int parts = Shares(k, tiles.count).parts, part = group % parts;
+    for (int tile = group / parts; tile < tiles.count; tile += k.many_groups / parts) {
+        const int k_first = tiles.first(tile), k0 = k_first + wave * 32 * kSub;
+        // the queries that attend some key of the tile
+        const int i_low = max(0, k_first - w.p_first);
+        int i_end = w.count;
+        if (a.window > 0 && k_first >= tiles.sinks) i_end = static_cast<int>(min<int64_t>(i_end, static_cast<int64_t>(k_first) + kKeys - 1 + a.window - w.p_first));
+        const int steps = max(0, (i_end - i_low + kRows - 1) / kRows);
+        const int64_t all = static_cast<int64_t>(steps) * a.H;
+        int64_t s_now = all * part / parts;
+        const int64_t s_end = all * (part + 1) / parts;
+
+        int64_t at[kSub];
+        bool there[kSub];
+        u32x4 key[kSub][kPieces];
+        float acc[kSub];
+#pragma unroll
+        for (int u = 0; u < kSub; ++u) {
+            at[u] = row_of(k, w, k0 + 32 * u + col, there[u]);
+            acc[u] = 0.f;
+        }
+        const float sc = a.scale * kLog2e;
+        TileRead<T, DK> rq;
+        rq.init_rows(col, half);
+
+        // the step to fetch, and the one worked on
+        int f_head = s_now < s_end ? static_cast<int>(s_now / steps) : 0, f_i = i_low + (s_now < s_end ? static_cast<int>(s_now % steps) * kRows : 0);
+        int head = f_head, i0 = f_i, kvh = -1;
+        u32x4 qr[kEach];
+        float lse_r = 0.f;
+        int src[kEach], lse_src = 0;  // rows of the next step to fetch
+        auto row_at = [&](int i) {  // query i's row in q, -1: none
+            if (i >= i_end) return -1;
+            const int64_t t = w.first + i;
+            const int64_t r = a.rows != nullptr ? a.rows[t] : t;
+            return r >= 0 && r < a.src_rows && w.p_first + i >= 0 ? static_cast<int>(r) : -1;
+        };
+        auto look = [&]() {
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) src[i] = row_at(f_i + (tid + i * kThreads) / kRowPieces);
+            if (tid < kRows) lse_src = row_at(f_i + tid);
+        };
+        auto fetch = [&]() __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                const int p = tid + i * kThreads;
+                if (kRows * kRowPieces % kThreads == 0 || p < kRows * kRowPieces) {
+                    qr[i] = u32x4{};
+                    if (src[i] >= 0)
+                        qr[i] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(a.q) + (static_cast<int64_t>(src[i]) * a.H + f_head) * kRow +
+                                                                p % kRowPieces * 16);
+                }
+            }
+            if (tid < kRows) lse_r = lse_src >= 0 ? a.lse[static_cast<int64_t>(lse_src) * a.H + f_head] : INFINITY;
+            f_i += kRows;
+            if (f_i >= i_low + steps * kRows) {
+                f_i = i_low;
+                ++f_head;
+            }
+            look();
+        };
+        auto put = [&](char* buf) __attribute__((always_inline)) {
+            // a row that is not there, attends nothing or is broken: e^(0 - infinity)
+            const bool none = tid < kRows && !(fabsf(lse_r) < INFINITY);
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                const int p = tid + i * kThreads, row = p / kRowPieces;
+                if (kRows * kRowPieces % kThreads == 0 || p < kRows * kRowPieces)
+                    *reinterpret_cast<u32x4*>(buf + row * kRow + (p % kRowPieces ^ turn<kRowPieces>(row)) * 16) = qr[i];
+            }
+            if (tid < kRows) reinterpret_cast<float*>(buf + Sz::kTile)[tid] = none ? INFINITY : lse_r * kLog2e;
+        };
+        auto work = [&](const char* sQ) __attribute__((always_inline)) {
+            const f32x4* lse2 = reinterpret_cast<const f32x4*>(sQ + Sz::kTile);
+            const int f = head / G;
+            if (f != kvh) {
+                kvh = uniform(f);
+#pragma unroll
+                for (int u = 0; u < kSub; ++u) {
+                    const char* from = static_cast<const char*>(c.k_cache) + (at[u] + (static_cast<int64_t>(kvh) << c.page_shift)) * kRow + half * 16;
+#pragma unroll
+                    for (int p = 0; p < kPieces; ++p) key[u][p] = *reinterpret_cast<const u32x4*>(from + p * 32);
+                }
+            }
+            const int p0 = w.p_first + i0;  // the first row's place
+            f32x16 s[kSub];
+#pragma unroll
+            for (int u = 0; u < kSub; ++u) s[u] = f32x16{};
+#pragma unroll
+            for (int p = 0; p < kPieces; ++p) {
+                const u32x4 q = rq.rows(sQ, p);
+#pragma unroll
+                for (int u = 0; u < kSub; ++u) s[u] = mma<T>(q, key[u][p], s[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < kSub; ++u) {
+                const int key0 = k0 + 32 * u;
+                // register r: the query at place p0 + 8 (r / 4) + 4 half + r % 4; key key0 + col
+#pragma unroll
+                for (int r4 = 0; r4 < 4; ++r4) {
+                    const f32x4 l = lse2[2 * r4 + half];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[u][4 * r4 + e] = __builtin_amdgcn_exp2f(fmaf(s[u][4 * r4 + e], sc, -l[e]));
+                }
+                if (p0 < key0 + 31 || (a.window > 0 && p0 + kRows > key0 + a.window && key0 + 32 > tiles.sinks)) {
+                    const int least = opaque(key0 + col - p0 - 4 * half);
+                    const int most = opaque(a.window > 0 && key0 + col >= tiles.sinks ? key0 + col + a.window - p0 - 4 * half : INT32_MAX);
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (8 * (r / 4) + r % 4 < least || 8 * (r / 4) + r % 4 >= most) s[u][r] = 0.f;
+                }
+                float sum = 0.f;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) sum += s[u][r];
+                acc[u] += sum;
+            }
+            i0 += kRows;
+            if (i0 >= i_low + steps * kRows) {
+                i0 = i_low;
+                ++head;
+            }
+        };
+        if (s_now < s_end) {
+            look();
+            fetch();
+            put(smem);
+        }
+        for (; s_now < s_end; s_now += 2) {
+            tile_barrier();
+            if (s_now + 1 < s_end) fetch();
+            work(smem);
+            if (s_now + 1 >= s_end) break;
+            put(smem + Sz::kBuf);
+            tile_barrier();
+            if (s_now + 2 < s_end) fetch();
+            work(smem + Sz::kBuf);
+            if (s_now + 2 < s_end) put(smem);
+        }
+#pragma unroll
+        for (int u = 0; u < kSub; ++u) {
+            const float x = gathered(xor32_add(acc[u]));
+            if (half != 0) continue;
+            if (parts > 1)
+                k.part[(static_cast<int64_t>(n) * k.many_groups + group) * kKeys + wave * 32 * kSub + 32 * u + col] = x;
+            else if (there[u])
+                *weight_of(k, w, k0 + 32 * u + col) += x;
+        }
+        tile_barrier();  // the next tile's first queries go where this one's were
+    }
+}
+
+template <typename T, int DK>
+__global__ __launch_bounds__(kThreads, (DK * sizeof(T) <= 256 ? 2 : 1)) void cache_weigh_kernel(WeighK k) {
+    __shared__ __align__(16) char smem[2 * ManySizes<T, DK>::kBuf];
+    const unsigned many = static_cast<unsigned>(k.a.N) * k.many_groups;
+    if (blockIdx.x < many) weigh_many<T, DK>(k, blockIdx.x, smem);
+    else weigh_few<T, DK>(k, blockIdx.x - many, reinterpret_cast<float(*)[32]>(smem));
+}
+
+// Adds the parts in their order, a key per thread.
+template <int kKeys>
+__global__ __launch_bounds__(kKeys) void cache_weigh_sum_kernel(WeighK k) {
+    const int n = blockIdx.x / k.many_groups, tile = blockIdx.x % k.many_groups;
+    Weighed w;
+    if (!weighed(k, n, w) || few(k, w, k.a.H / k.c.Hkv)) return;
+    const Tiles tiles(k.a, w, kKeys);
+    const int parts = Shares(k, tiles.count).parts;
+    if (parts == 1 || tile >= tiles.count) return;
+    const int pos = tiles.first(tile) + threadIdx.x;
+    bool there;
+    row_of(k, w, pos, there);
+    if (!there) return;
+    const float* from = k.part + (static_cast<int64_t>(n) * k.many_groups + tile * parts) * kKeys + threadIdx.x;
+    float sum = 0.f;
+    for (int p = 0; p < parts; ++p) sum += from[p * kKeys];
+    *weight_of(k, w, pos) += sum;
+}
+
+// Workgroups of a call, where it has that much work.
+constexpr int kFewWant = 2048, kManyWant = 1024, kMostParts = 64;
+
+int per_sequence(int64_t want, int64_t N) { return static_cast<int>((want + N - 1) / N); }
+
+// Sequences of few queries, as far as the host can tell: a decode step.  What
+// may be others among them is not cut into parts then.
+bool mostly_few(int64_t tokens, int64_t N, int G) { return tokens * G <= kRows * N; }
 
 template <typename T, int DK>
 hipError_t launch_weigh(const CacheArgs& c, const WeighArgs& a, hipStream_t s) {
+    constexpr int kKeys = ManySizes<T, DK>::kKeys;
     const int64_t max_ctx = static_cast<int64_t>(c.max_pages) << c.page_shift;
-    int64_t reach = max_ctx;
-    if (a.window > 0) reach = window_reach(max_ctx, a.window, a.sinks) + a.tokens;
-    if (reach > max_ctx) reach = max_ctx;
-    const int64_t tiles = (reach + kKeys - 1) / kKeys, want = (kWantGroups + a.N - 1) / a.N;
-    WeighK k{c, a, static_cast<int>(tiles < want ? tiles : want)};
-    if (k.a.window >= max_ctx) k.a.window = 0;  // it holds every token
-    LaunchTimer timer("cache_weigh", s);
-    cache_weigh_kernel<T, DK><<<dim3(static_cast<unsigned>(static_cast<int64_t>(a.N) * k.splits)), dim3(kThreads), 0, s>>>(k);
+    const int G = a.H / c.Hkv;
+    WeighK k{};
+    k.c = c;
+    k.a = a;
+    if (a.window >= max_ctx) k.a.window = 0;  // it holds every token
+    const bool any_many = a.tokens * G > kRows, cut = !mostly_few(a.tokens, a.N, G);
+    if (any_many) {
+        k.many_groups = per_sequence(kManyWant, a.N);
+        k.most_parts = !cut ? 1 : a.H < kMostParts ? a.H : kMostParts;
+        k.part = static_cast<float*>(a.ws);
+    }
+    if (!any_many || a.N > 1) k.few_groups = per_sequence(kFewWant, a.N);
+    {
+        LaunchTimer timer("cache_weigh", s);
+        const int64_t groups = static_cast<int64_t>(a.N) * (k.many_groups + k.few_groups);
+        cache_weigh_kernel<T, DK><<<dim3(static_cast<unsigned>(groups)), dim3(kThreads), 0, s>>>(k);
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !cut || k.many_groups <= 1) return e;
+    LaunchTimer timer("cache_weigh_sum", s);
+    cache_weigh_sum_kernel<kKeys><<<dim3(static_cast<unsigned>(a.N * k.many_groups)), dim3(kKeys), 0, s>>>(k);
     return hipGetLastError();
 }
 
 }  // namespace
 
-size_t cache_weigh_workspace_bytes(int64_t, int, int, int, int64_t) { return 0; }
+size_t cache_weigh_workspace_bytes(int64_t tokens, int N, int H, int Hkv) {
+    if (mostly_few(tokens, N, H / Hkv)) return 0;
+    return static_cast<size_t>(N) * per_sequence(kManyWant, N) * 256 * 4;  // a tile has 256 keys at most
+}
 
 hipError_t launch_cache_weigh(const CacheArgs& c, const WeighArgs& a, hipStream_t s) {
     if (a.tokens == 0) return hipSuccess;

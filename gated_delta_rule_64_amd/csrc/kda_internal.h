@@ -248,7 +248,7 @@ struct WeighArgs {
     const int32_t* slot_indices;
     void* ws;
 };
-size_t cache_weigh_workspace_bytes(int64_t tokens, int N, int H, int Hkv, int64_t max_ctx);
+size_t cache_weigh_workspace_bytes(int64_t tokens, int N, int H, int Hkv);
 hipError_t launch_cache_weigh(const CacheArgs& c, const WeighArgs& a, hipStream_t s);
 
 struct EvictArgs {

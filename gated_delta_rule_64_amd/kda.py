@@ -656,9 +656,8 @@ def kda_cache_copy(pool, src, dst):
     _call(dev, "kda_cache_copy", _addr(pool), row_bytes, rows, _addr(src), _addr(dst), n)
 
 
-def kda_cache_weigh_workspace_bytes(T_tot, N, H, Hkv, max_context):
-    """``max_context``: tokens that a page-table row can hold."""
-    return int(lib().kda_cache_weigh_workspace_bytes(T_tot, N, H, Hkv, max_context))
+def kda_cache_weigh_workspace_bytes(T_tot, N, H, Hkv):
+    return int(lib().kda_cache_weigh_workspace_bytes(T_tot, N, H, Hkv))
 
 
 def kda_cache_weigh(q, lse, k_cache, page_table, lens, weights, cu_seqlens=None, rows=None, slot_indices=None, window=0,
@@ -685,7 +684,7 @@ def kda_cache_weigh(q, lse, k_cache, page_table, lens, weights, cu_seqlens=None,
     if slot_indices is not None:
         _shape("slot_indices", slot_indices, (N,), torch.int32)
     dev = _device(q, lse, k_cache, page_table, lens, weights, cu_seqlens, rows, slot_indices, workspace)
-    workspace = _workspace(workspace, kda_cache_weigh_workspace_bytes(T, N, H, Hkv, width * page), dev)
+    workspace = _workspace(workspace, kda_cache_weigh_workspace_bytes(T, N, H, Hkv), dev)
     _call(dev, "kda_cache_weigh", T, N, _addr(cu_seqlens), R, _addr(rows), H, Hkv, dk, _dtype_code(q),
           dk ** -0.5 if scale is None else scale, window, sinks, _addr(q), _addr(lse), _addr(k_cache), pages, page,
           _addr(page_table), slots, width, _addr(lens), _addr(slot_indices), _addr(weights), _addr(workspace),

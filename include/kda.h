@@ -526,7 +526,7 @@ int kda_attn_prefill_backward(int64_t T_tot, int32_t H, int32_t Hkv, int32_t dk,
  *                 up to max_T_tot tokens in any number of sequences, with that
  *                 window and those sinks, by
  *                 kda_attn_window_backward_max_workspace_bytes().
- * T_tot must be below 2^30, and the limits of the calls above hold
+ * T_tot must be below 2^29, and the limits of the calls above hold
  * (KDA_ERR_UNSUPPORTED otherwise).  A row that is not finite may also reach
  * rows up to 190 tokens from those that attend it, and gradients of tokens as
  * far from those that such rows attend.
@@ -622,7 +622,7 @@ int kda_attn_tree(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t dk, int3
  * kda_attn_window_prefill.  A cached token whose entry names no page keeps its
  * place and is not attended, so pages that no row will see again can go.
  * Arguments: those of kda_attn_tree, and window >= 1, sinks >= 0; workspace by
- * the two functions below.  max_pages x page_size must be below 2^30
+ * the two functions below.  max_pages x page_size must be below 2^29
  * (KDA_ERR_UNSUPPORTED otherwise).
  */
 size_t kda_attn_window_tree_workspace_bytes(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t dk,
@@ -760,18 +760,19 @@ int kda_cache_copy(void* pool, int64_t row_bytes, int32_t rows,
  *                 at 0 with it.  kda_cache_copy forks rows of it;
  *   slot_indices  NULL (sequence n uses slot n) or int32 [N], distinct where
  *                 the sequences are not empty;
- *   workspace     at least kda_cache_weigh_workspace_bytes() bytes for
- *                 max_context = max_pages * page_size, 256-byte aligned;
- *                 contents on entry are ignored.
+ *   workspace     at least kda_cache_weigh_workspace_bytes() bytes, 256-byte
+ *                 aligned; contents on entry are ignored ((1,024 + N) KiB hold
+ *                 every call of up to N sequences).
  * Products, exponentials and sums are fp32, in a fixed order: the same inputs
  * give the same bits.  A weight is as right as its lse (see the gradients).
  * Skipped: slots outside [0, slots), rows outside [0, src_rows), queries
- * before the slot's first token, rows whose lse is not finite.  Tokens that no
+ * before the slot's first token, rows whose lse is not finite; a key that is not
+ * finite gathers nothing.  Tokens that no
  * query attends and those whose entry names no page keep what they have.
- * T_tot and max_pages x page_size must be below 2^30, N below 2^23
+ * T_tot and max_pages x page_size must be below 2^29, N below 2^23
  * (KDA_ERR_UNSUPPORTED otherwise).
  */
-size_t kda_cache_weigh_workspace_bytes(int64_t T_tot, int32_t N, int32_t H, int32_t Hkv, int64_t max_context);
+size_t kda_cache_weigh_workspace_bytes(int64_t T_tot, int32_t N, int32_t H, int32_t Hkv);
 int kda_cache_weigh(int64_t T_tot, int32_t N, const int32_t* cu_seqlens,
                     int64_t src_rows, const int32_t* rows,
                     int32_t H, int32_t Hkv, int32_t dk, int32_t x_dtype, float scale,
@@ -807,7 +808,7 @@ int kda_cache_weigh(int64_t T_tot, int32_t N, const int32_t* cu_seqlens,
  * one where a page that would be written, or a last page that stays partly
  * filled, has another entry that names it (refs above 1): pages of a shared
  * prefix of at most `first` tokens stay shared.  max_pages x page_size must be below
- * 2^30 and Hkv below 2^15 (KDA_ERR_UNSUPPORTED otherwise).
+ * 2^29 and Hkv below 2^15 (KDA_ERR_UNSUPPORTED otherwise).
  */
 size_t kda_cache_evict_workspace_bytes(int32_t n, int32_t keep);
 int kda_cache_evict(int32_t n, const int32_t* slot_list, int32_t keep, int32_t first, int32_t recent,

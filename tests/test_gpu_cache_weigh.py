@@ -242,8 +242,8 @@ def test_same_bits_twice_and_streams(K):
 @pytest.mark.parametrize("count", [2, 150])
 def test_captured_and_replayed(K, count):
     x = _setup(13, [700, 300], [count, 1], 8, 2, 64, 64, torch.bfloat16)
-    n, lens = x["weights"].shape[1], x["lens"].clone()
-    ws = torch.empty(max(256, K.kda_cache_weigh_workspace_bytes(count + 1, 2, 8, 2, n)), dtype=torch.uint8, device="cuda")
+    lens = x["lens"].clone()
+    ws = torch.empty(max(256, K.kda_cache_weigh_workspace_bytes(count + 1, 2, 8, 2)), dtype=torch.uint8, device="cuda")
     w = x["weights"].clone()
 
     def step(to):

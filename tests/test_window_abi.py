@@ -68,7 +68,7 @@ WINDOWS = [(dict(window=0), BAD, "window=0"), (dict(window=-5), BAD, "window=-5"
 
 
 @pytest.mark.parametrize("kw,status,word", HEAD_REFUSALS + WINDOWS + [
-    (dict(T=-1), BAD, "T_tot"), (dict(T=2**31), BAD, "T_tot"), (dict(T=2**30, H=1, Hkv=1, dk=16, dv=16), UNSUP, "2^30"), (dict(N=0), BAD, "N=0"),
+    (dict(T=-1), BAD, "T_tot"), (dict(T=2**31), BAD, "T_tot"), (dict(T=2**29, H=1, Hkv=1, dk=16, dv=16), UNSUP, "2^29"), (dict(N=0), BAD, "N=0"),
     (dict(N=2), BAD, "cu_seqlens"), (dict(q=None), BAD, "q is NULL"), (dict(v=FAKE + 2 * M + 8), BAD, "aligned"),
     (dict(T=1 << 28, H=8, Hkv=1, dk=16, dv=16), UNSUP, "workgroups")])
 def test_prefill_refuses(lib, kw, status, word):
@@ -86,18 +86,20 @@ def test_backward_refuses(lib, kw, status, word):
 
 @pytest.mark.parametrize("kw,status,word", HEAD_REFUSALS + WINDOWS + CACHE_REFUSALS + PAGE_REFUSALS[:-1] + [
     (dict(T=65), BAD, "T=65"), (dict(B=-1), BAD, "B=-1"), (dict(slots=5), BAD, "slot_indices"), (dict(kc=None), BAD, "k_cache is NULL"),
-    (dict(width=1 << 20, page=1024), UNSUP, "2^30"), (dict(width=600, window=9000, ws_bytes=64), SMALL, "kda_attn_window_tree")])
+    (dict(width=1 << 19, page=1024), UNSUP, "2^29"), (dict(width=600, window=9000, ws_bytes=64), SMALL, "kda_attn_window_tree")])
 def test_tree_refuses(lib, kw, status, word):
     assert tree(lib, **kw) == status
     assert word in detail(lib)
 
 
 @pytest.mark.parametrize("kw,status,word", [r for r in HEAD_REFUSALS if "dv" not in r[0]] + WINDOWS[1:] + CACHE_REFUSALS + PAGE_REFUSALS[:-1] + [
-    (dict(dk=96), UNSUP, "dk=96"), (dict(T=-1), BAD, "T_tot"), (dict(T=1 << 30, R=1 << 30), UNSUP, "2^30"), (dict(N=0), BAD, "N=0"),
+    (dict(dk=96), UNSUP, "dk=96"), (dict(T=-1), BAD, "T_tot"), (dict(T=1 << 29, R=1 << 29), UNSUP, "2^29"), (dict(N=0), BAD, "N=0"),
     (dict(N=2), BAD, "cu_seqlens"), (dict(R=7), BAD, "src_rows"), (dict(R=-1), BAD, "src_rows"), (dict(N=3, cu=FAKE + 9 * M), BAD, "slots=2"),
     (dict(N=1 << 23, cu=FAKE + (1 << 38), idx=FAKE + (1 << 39)), UNSUP, "workgroups"), (dict(q=None), BAD, "q is NULL"),
     (dict(lse=None), BAD, "lse is NULL"), (dict(w=None), BAD, "weights is NULL"), (dict(w=FAKE + 5 * M + 2), BAD, "aligned"),
-    (dict(rows=FAKE + 30 * M + 2), BAD, "aligned"), (dict(width=1 << 20, page=1024), UNSUP, "2^30")])
+    (dict(rows=FAKE + 30 * M + 2), BAD, "aligned"), (dict(width=1 << 19, page=1024), UNSUP, "2^29"),
+    (dict(N=1, T=4096, R=4096, H=32, Hkv=8, width=64, page=64, pages=64, ws_bytes=0), SMALL, "kda_cache_weigh"),
+    (dict(N=1, T=4096, R=4096, H=32, Hkv=8, width=64, page=64, pages=64, ws=None), BAD, "256-byte")])
 def test_weigh_refuses(lib, kw, status, word):
     assert weigh(lib, **kw) == status
     assert word in detail(lib)
@@ -106,9 +108,9 @@ def test_weigh_refuses(lib, kw, status, word):
 @pytest.mark.parametrize("kw,status,word", CACHE_REFUSALS + PAGE_REFUSALS[:-1] + [
     (dict(n=-1), BAD, "n=-1"), (dict(n=1 << 16), UNSUP, "entries"), (dict(keep=0), BAD, "keep=0"), (dict(keep=-3), BAD, "keep=-3"),
     (dict(first=-1), BAD, "first=-1"), (dict(recent=-1), BAD, "recent=-1"), (dict(first=17), BAD, "more than keep"),
-    (dict(first=2**31 - 1, recent=2**31 - 1), BAD, "more than keep"), (dict(keep=1 << 30), UNSUP, "keep="), (dict(Hkv=0), BAD, "Hkv"),
+    (dict(first=2**31 - 1, recent=2**31 - 1), BAD, "more than keep"), (dict(keep=1 << 29), UNSUP, "keep="), (dict(Hkv=0), BAD, "Hkv"),
     (dict(Hkv=1 << 15, dk=16, dv=16), UNSUP, "Hkv="), (dict(dk=48, dv=48), UNSUP, "dk=48"), (dict(x=3), BAD, "x_dtype"),
-    (dict(width=1 << 20, page=1024), UNSUP, "2^30"), (dict(list=None), BAD, "slot_list is NULL"), (dict(refs=None), BAD, "refs is NULL"),
+    (dict(width=1 << 19, page=1024), UNSUP, "2^29"), (dict(list=None), BAD, "slot_list is NULL"), (dict(refs=None), BAD, "refs is NULL"),
     (dict(w=None), BAD, "weights is NULL"), (dict(kept=FAKE + 20 * M + 2), BAD, "aligned"), (dict(ws_bytes=64), SMALL, "kda_cache_evict"),
     (dict(ws=None), BAD, "256-byte")])
 def test_evict_refuses(lib, kw, status, word):
@@ -131,7 +133,7 @@ CALLS = {
     "prefill": (prefill, dict(N=2), "q k v z cu", "out lse"),
     "backward": (backward, dict(N=2, ws=WS), "q k v z out lse dy cu", "gq gk gv gz ws"),
     "tree": (tree, dict(width=600, window=9000, ws=WS), "q k v mask z kc vc table lens idx", "out lse ws"),
-    "weigh": (weigh, BIG, "q lse kc table lens cu rows idx", "w"),
+    "weigh": (weigh, BIG, "q lse kc table lens cu rows idx", "w ws"),
     "evict": (evict, dict(ws=WS), "list", "kc vc table lens refs w kept status ws"),
 }
 
@@ -178,15 +180,23 @@ def test_workspaces_of_gradients(T, window, sinks, H, Hkv, dk, dv, x, gate):
     assert T == 0 or most > 0
 
 
+@pytest.mark.parametrize("H,Hkv", [(32, 8), (1, 1), (64, 1)])
+def test_workspaces_of_weights(H, Hkv):
+    """(1,024 + N) KiB hold every call of N sequences."""
+    for N in (1, 2, 3, 7, 300, 1000, 1023, 1024, 1025, 5000):
+        need = max(kda.kda_cache_weigh_workspace_bytes(T, N, H, Hkv) for T in (0, 1, N, 40 * N, 1 << 20))
+        assert 0 < need <= (1024 + N) * 1024
+
+
 def test_bad_sizes_need_nothing():
     good = (8, 8, 64, 64, BF16)
     assert kda.kda_attn_window_backward_workspace_bytes(100, 1, *good, 0, 0, 0) == 0
-    assert kda.kda_attn_window_backward_workspace_bytes(1 << 30, 1, *good, 0, 5, 0) == 0
+    assert kda.kda_attn_window_backward_workspace_bytes(1 << 29, 1, *good, 0, 5, 0) == 0
     assert kda.kda_attn_window_backward_max_workspace_bytes(100, *good, 0, 5, -1) == 0
-    assert kda.kda_attn_window_tree_workspace_bytes(1, 1, *good, 1 << 30, 5, 0) == 0
+    assert kda.kda_attn_window_tree_workspace_bytes(1, 1, *good, 1 << 29, 5, 0) == 0
     assert kda.kda_attn_window_tree_max_workspace_bytes(1, 1, *good, 1 << 16, 0, 0) == 0
     for bad in A.HEAD_REFUSALS[:1]:
-        assert kda.kda_cache_weigh_workspace_bytes(8, 1, bad[0]["H"], 1, 4096) == 0
-    assert kda.kda_cache_weigh_workspace_bytes(8, 0, 8, 8, 4096) == kda.kda_cache_weigh_workspace_bytes(8, 1, 8, 3, 4096) == 0
+        assert kda.kda_cache_weigh_workspace_bytes(8, 1, bad[0]["H"], 1) == 0
+    assert kda.kda_cache_weigh_workspace_bytes(8, 0, 8, 8) == kda.kda_cache_weigh_workspace_bytes(8, 1, 8, 3) == 0
     assert kda.kda_cache_evict_workspace_bytes(1 << 16, 8) == kda.kda_cache_evict_workspace_bytes(4, 0) == 0
     assert kda.kda_cache_evict_workspace_bytes(4, 100) >= 4 * 100 * 4
