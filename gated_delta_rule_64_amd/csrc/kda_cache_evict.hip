@@ -5,7 +5,8 @@
 // in the tokens' order.  They then move to the front in that order: token d
 // goes to a place that is not behind its own, so whoever walks them in order
 // can move them where they are, as long as a step's reads come before its
-// writes.
+// writes.  What a later step reads is behind all that an earlier one writes, so
+// that its reads need not wait for those writes.
 #include "kda_common.h"
 #include "kda_internal.h"
 #include "kda_profile.h"
@@ -20,14 +21,16 @@ struct EvictK {
     CacheArgs c;
     EvictArgs a;
     int32_t* list;  // [n, keep]: places of the tokens that stay
+    int64_t* from;  // [n, keep]: their rows in head 0 of the pools
     int32_t* plan;  // [n]: the first token that changes its place (-1: nothing to do)
+    int splits;     // workgroups that share a head's rows, each some of the channels
 };
 
 __device__ __forceinline__ bool names_page(int32_t e, int pages) { return e >= 0 && e < pages; }
 
-// A barrier behind loads whose places other threads write after it: every wave
-// waits until its loads have arrived.
-__device__ __forceinline__ void loaded_barrier() {
+// A barrier behind loads whose places other threads write after it, or behind
+// stores that they read: every wave waits until its own are done.
+__device__ __forceinline__ void done_barrier() {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
 }
@@ -39,21 +42,20 @@ __device__ __forceinline__ uint32_t order_of(float w) {
     return b >> 31 ? ~b : b | 0x80000000u;
 }
 
-template <typename I>
-__device__ __forceinline__ I block_scan(I x, I* sums, I& total) {
+__device__ __forceinline__ uint64_t block_scan(uint64_t x, uint64_t* sums, uint64_t& total) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    I inc = x;
+    uint64_t inc = x;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
-        const I y = __shfl_up(inc, o);
+        const uint64_t y = __shfl_up(inc, o);
         if (lane >= o) inc += y;
     }
     if (lane == 63) sums[wave] = inc;
     __syncthreads();
-    I before = 0, all = 0;
+    uint64_t before = 0, all = 0;
 #pragma unroll
     for (int w = 0; w < kPlan / 64; ++w) {
-        const I s = sums[w];
+        const uint64_t s = sums[w];
         before += w < wave ? s : 0;
         all += s;
     }
@@ -62,9 +64,14 @@ __device__ __forceinline__ I block_scan(I x, I* sums, I& total) {
     return before + inc - x;
 }
 
-// One workgroup per entry: checks it, finds what stays, moves its weights.
+// One workgroup per entry: checks it, finds what stays, moves its weights.  A
+// slot of up to kStep tokens is read once and its orders stay in registers; the
+// digits are counted in LDS.  Bound by the length of its chain of barriers.
+constexpr int kPer = 8;  // neighbouring tokens of a thread
+constexpr int kStep = kPlan * kPer;
+
 __global__ __launch_bounds__(kPlan) void cache_evict_plan_kernel(EvictK k) {
-    __shared__ int hist[256];
+    __shared__ int hist[4][256];
     __shared__ uint64_t sums[kPlan / 64];
     __shared__ int s_first, s_bad, s_digit, s_left;
     const CacheArgs& c = k.c;
@@ -72,32 +79,59 @@ __global__ __launch_bounds__(kPlan) void cache_evict_plan_kernel(EvictK k) {
     const int i = blockIdx.x, tid = threadIdx.x;
     const int slot = a.slot_list[i];
     int32_t* list = k.list + static_cast<int64_t>(i) * a.keep;
+    int64_t* rows = k.from + static_cast<int64_t>(i) * a.keep;
     int32_t* kept = a.kept != nullptr ? a.kept + static_cast<int64_t>(i) * a.keep : nullptr;
+    const bool real = slot >= 0 && slot < c.slots;
+    const int64_t most = static_cast<int64_t>(c.max_pages) << c.page_shift;
+    const int stored = real ? c.lens[slot] : 0;
+    const int len = stored < 0 ? 0 : static_cast<int>(stored > most ? most : stored);
+    const int32_t* table = c.table + static_cast<int64_t>(real ? slot : 0) * c.max_pages;
+    float* w = a.weights + ((static_cast<int64_t>(real ? slot : 0) * c.max_pages) << c.page_shift);
+    const int mask = (1 << c.page_shift) - 1;
+
+    uint32_t order[kPer];
+    const int steps = (len + kStep - 1) / kStep;
+    auto read = [&](int step) __attribute__((always_inline)) {
+        const int p = step * kStep + tid * kPer;
+        if (p + kPer <= len) {  // a slot's weights begin at a multiple of 64 bytes from the first slot's
+            const uint4* from = reinterpret_cast<const uint4*>(w + p);
+            float x[kPer];
+            if ((reinterpret_cast<uintptr_t>(w) & 15) == 0) {
+#pragma unroll
+                for (int e = 0; e < kPer / 4; ++e) {
+                    const uint4 v = from[e];
+                    x[4 * e] = __uint_as_float(v.x), x[4 * e + 1] = __uint_as_float(v.y);
+                    x[4 * e + 2] = __uint_as_float(v.z), x[4 * e + 3] = __uint_as_float(v.w);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) x[e] = w[p + e];
+            }
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) order[e] = order_of(x[e]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) order[e] = p + e < len ? order_of(w[p + e]) : 0;
+        }
+    };
+    const bool cut = len > a.keep;
+    if (cut) read(0);
+
+    // an earlier entry that names the slot has it; every token of a slot that is cut has a page
     if (tid == 0) {
-        s_bad = slot < 0 || slot >= c.slots;
-        s_first = INT32_MAX;
+        s_bad = !real;
+        s_first = a.keep;
     }
+    if (tid < 256) hist[0][tid] = hist[1][tid] = hist[2][tid] = hist[3][tid] = 0;
     __syncthreads();
-    // an earlier entry that names the slot has it
     for (int j = tid; j < i; j += kPlan)
         if (a.slot_list[j] == slot) s_bad = 1;
-    __syncthreads();
-    bool bad = s_bad != 0;
-    int len = 0;
-    const int32_t* table = nullptr;
-    if (!bad) {
-        const int64_t most = static_cast<int64_t>(c.max_pages) << c.page_shift;
-        const int n = c.lens[slot];
-        len = n < 0 ? 0 : static_cast<int>(n > most ? most : n);
-        table = c.table + static_cast<int64_t>(slot) * c.max_pages;
-    }
-    const bool cut = !bad && len > a.keep;
-    if (cut) {  // every token has a page
-        for (int j = tid; j < (len + (1 << c.page_shift) - 1) >> c.page_shift; j += kPlan)
+    if (cut) {
+        for (int j = tid; j < (len + mask) >> c.page_shift; j += kPlan)
             if (!names_page(table[j], c.pages)) s_bad = 1;
     }
     __syncthreads();
-    bad = s_bad != 0;
+    const bool bad = s_bad != 0;
     if (bad || !cut) {
         if (kept != nullptr)
             for (int d = tid; d < a.keep; d += kPlan) kept[d] = !bad && d < len ? d : -1;
@@ -107,25 +141,43 @@ __global__ __launch_bounds__(kPlan) void cache_evict_plan_kernel(EvictK k) {
         }
         return;
     }
-    float* w = a.weights + (static_cast<int64_t>(slot) * c.max_pages << c.page_shift);
     // the places between the first and the most recent ones, of which `left` stay
     const int from = a.first, to = len - a.recent;
+    const bool some = a.keep > a.first + a.recent;
     int left = a.keep - a.first - a.recent;
     uint32_t known = 0;
-    if (left > 0) {
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            for (int b = tid; b < 256; b += kPlan) hist[b] = 0;
-            __syncthreads();
-            for (int p = from + tid; p < to; p += kPlan) {
-                const uint32_t o = order_of(w[p]);
-                if (shift == 24 || o >> (shift + 8) == known >> (shift + 8)) atomicAdd(&hist[o >> shift & 255], 1);
+    if (some) {
+#pragma unroll
+        for (int digit = 0; digit < 4; ++digit) {
+            const int shift = 24 - 8 * digit;
+            for (int step = 0; step < steps; ++step) {
+                if (steps > 1) read(step);
+                const int p = step * kStep + tid * kPer;
+#pragma unroll
+                for (int e = 0; e < kPer; ++e)
+                    if (p + e >= from && p + e < to && (digit == 0 || order[e] >> (shift + 8) == known >> (shift + 8)))
+                        atomicAdd(&hist[digit][order[e] >> shift & 255], 1);
             }
             __syncthreads();
-            if (tid == 0) {
-                int rest = left, b = 255;
-                while (b > 0 && hist[b] < rest) rest -= hist[b--];
-                s_digit = b;
-                s_left = rest;
+            if (tid < 64) {  // one wave: four bins a lane, the largest first
+                int n[4], mine = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mine += n[e] = hist[digit][255 - 4 * tid - e];
+                int before = mine;
+#pragma unroll
+                for (int o = 1; o < 64; o <<= 1) {
+                    const int y = __shfl_up(before, o);
+                    if (tid >= o) before += y;
+                }
+                before -= mine;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (before < left && left <= before + n[e]) {
+                        s_digit = 255 - 4 * tid - e;
+                        s_left = left - before;
+                    }
+                    before += n[e];
+                }
             }
             __syncthreads();
             known |= static_cast<uint32_t>(s_digit) << shift;
@@ -133,33 +185,43 @@ __global__ __launch_bounds__(kPlan) void cache_evict_plan_kernel(EvictK k) {
         }
     }
     // `left` of those whose order is `known` stay, the first ones, and all above it
-    const bool some = a.keep > a.first + a.recent;
     uint64_t before = 0;  // above it or protected (high half), equal to it (low half)
-    for (int p0 = 0; p0 < len; p0 += kPlan) {
-        const int p = p0 + tid;
-        uint64_t x = 0;
-        if (p < len) {
-            if (p < from || p >= to) {
-                x = 1ull << 32;
-            } else if (some) {
-                const uint32_t o = order_of(w[p]);
-                x = o > known ? 1ull << 32 : o == known ? 1 : 0;
-            }
+    for (int step = 0; step < steps; ++step) {
+        if (steps > 1) read(step);
+        const int p0 = step * kStep + tid * kPer;
+        uint32_t above = 0, equal = 0;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+            const int p = p0 + e;
+            if (p >= len) continue;
+            if (p < from || p >= to || (some && order[e] > known)) above |= 1u << e;
+            else if (some && order[e] == known) equal |= 1u << e;
         }
         uint64_t total;
-        const uint64_t at = before + block_scan(x, sums, total);
+        const uint64_t at = before + block_scan(static_cast<uint64_t>(__popc(above)) << 32 | __popc(equal), sums, total);
         before += total;
-        const int eq = static_cast<int>(at & 0xffffffffu);
-        if (x >> 32 || (x && eq < left)) {
-            const int d = static_cast<int>(at >> 32) + min(eq, left);
-            list[d] = p;
-            if (kept != nullptr) kept[d] = p;
-            if (d != p) atomicMin(&s_first, d);
+        int up = static_cast<int>(at >> 32), eq = static_cast<int>(at & 0xffffffffu);
+        int gone = a.keep;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+            const int p = p0 + e;
+            const bool is_up = above >> e & 1, is_eq = equal >> e & 1;
+            if (is_up || (is_eq && eq < left)) {
+                const int d = up + min(eq, left);
+                list[d] = p;
+                rows[d] = ((static_cast<int64_t>(table[p >> c.page_shift]) * c.Hkv) << c.page_shift) + (p & mask);
+                if (kept != nullptr) kept[d] = p;
+            } else if (p < len) {
+                gone = min(gone, p);
+            }
+            up += is_up;
+            eq += is_eq;
         }
+        // tokens before the first one that goes keep their places
+        if (gone < a.keep) atomicMin(&s_first, gone);
     }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the list is read by other threads
-    __syncthreads();
-    const int d0 = min(s_first, a.keep);  // (a cut slot whose last tokens go keeps its places)
+    done_barrier();  // the list is read by other threads
+    const int d0 = s_first;
     // A page that is written must be this slot's alone, and so must a partly
     // filled last one, which the slot's next tokens are written to.
     for (int j = (d0 >> c.page_shift) + tid; j <= (a.keep - 1) >> c.page_shift; j += kPlan)
@@ -178,65 +240,92 @@ __global__ __launch_bounds__(kPlan) void cache_evict_plan_kernel(EvictK k) {
         k.plan[i] = d0;
         if (a.status != nullptr) a.status[i] = 0;
     }
-    for (int e0 = d0; e0 < a.keep; e0 += kPlan) {
-        const int d = e0 + tid;
-        const float x = d < a.keep ? w[__hip_atomic_load(list + d, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)] : 0.f;
-        loaded_barrier();
-        if (d < a.keep) w[d] = x;
+    constexpr int kAtOnce = 4;
+    for (int e0 = d0; e0 < a.keep; e0 += kAtOnce * kPlan) {
+        float x[kAtOnce];
+#pragma unroll
+        for (int e = 0; e < kAtOnce; ++e) {
+            const int d = e0 + e * kPlan + tid;
+            x[e] = d < a.keep ? w[__hip_atomic_load(list + d, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)] : 0.f;
+        }
+        done_barrier();
+#pragma unroll
+        for (int e = 0; e < kAtOnce; ++e) {
+            const int d = e0 + e * kPlan + tid;
+            if (d < a.keep) w[d] = x[e];
+        }
     }
     __syncthreads();
     for (int p = a.keep + tid; p < len; p += kPlan) w[p] = 0.f;
 }
 
-// One workgroup per (entry, key head, keys or values): its rows in order, a
-// step's reads before its writes.  What a later step reads is behind all that
-// an earlier one writes.
+// One workgroup per (entry, key head, keys or values, part of the channels): its
+// rows in order, a step's rows in flight while the one before is written.  The
+// last workgroup of an entry gives the pages behind back and sets the length
+// (the others read neither those entries nor the counts).
+constexpr int kRowsEach = 8;  // rows of a thread in a step
+
 __global__ __launch_bounds__(kMove) void cache_evict_move_kernel(EvictK k) {
     const CacheArgs& c = k.c;
-    const int i = blockIdx.x, d0 = k.plan[i];
+    const int i = blockIdx.x, d0 = k.plan[i], keep = k.a.keep;
     if (d0 < 0) return;
-    const int keep = k.a.keep, kvh = blockIdx.y >> 1, e = c.x == DT::BF16 ? 2 : 4;
-    const bool is_k = (blockIdx.y & 1) == 0;
-    const int pieces = (is_k ? c.dk : c.dv) * e / 16;
-    uint4* pool = static_cast<uint4*>(is_k ? c.k_cache : c.v_cache);
-    const int32_t* table = c.table + static_cast<int64_t>(k.a.slot_list[i]) * c.max_pages;
-    const int32_t* list = k.list + static_cast<int64_t>(i) * keep;
-    const int mask = (1 << c.page_shift) - 1;
-    auto row = [&](int p) {
-        return (((static_cast<int64_t>(table[p >> c.page_shift]) * c.Hkv + kvh) << c.page_shift) + (p & mask)) * pieces;
-    };
-    const int64_t all = static_cast<int64_t>(keep - d0) * pieces;
-    constexpr int kEach = 4;
-    for (int64_t x0 = 0; x0 < all; x0 += kMove * kEach) {
-        uint4 r[kEach];
-#pragma unroll
-        for (int x = 0; x < kEach; ++x) {
-            const int64_t at = x0 + x * kMove + threadIdx.x;
-            if (at < all) r[x] = pool[row(list[d0 + at / pieces]) + at % pieces];
-        }
-        loaded_barrier();
-#pragma unroll
-        for (int x = 0; x < kEach; ++x) {
-            const int64_t at = x0 + x * kMove + threadIdx.x;
-            if (at < all) pool[row(static_cast<int>(d0 + at / pieces)) + at % pieces] = r[x];
-        }
-    }
-}
-
-// The pages behind are given back, the length is set.
-__global__ __launch_bounds__(kMove) void cache_evict_finish_kernel(EvictK k) {
-    const CacheArgs& c = k.c;
-    const int i = blockIdx.x;
-    if (k.plan[i] < 0) return;
     const int slot = k.a.slot_list[i];
     int32_t* table = c.table + static_cast<int64_t>(slot) * c.max_pages;
-    for (int j = ((k.a.keep + (1 << c.page_shift) - 1) >> c.page_shift) + threadIdx.x; j < c.max_pages; j += kMove) {
-        const int page = table[j];
-        if (page == -1) continue;
-        table[j] = -1;
-        if (names_page(page, c.pages)) atomicSub(c.refs + page, 1);
+    if (blockIdx.y == gridDim.y - 1) {
+        for (int j = ((keep + (1 << c.page_shift) - 1) >> c.page_shift) + threadIdx.x; j < c.max_pages; j += kMove) {
+            const int page = table[j];
+            if (page == -1) continue;
+            table[j] = -1;
+            if (names_page(page, c.pages)) atomicSub(c.refs + page, 1);
+        }
+        if (threadIdx.x == 0) c.lens[slot] = keep;
+        return;
     }
-    if (threadIdx.x == 0) c.lens[slot] = k.a.keep;
+    const int share = blockIdx.y % k.splits, unit = blockIdx.y / k.splits;
+    const int kvh = unit >> 1, e = c.x == DT::BF16 ? 2 : 4;
+    const int pieces = ((unit & 1) == 0 ? c.dk : c.dv) * e / 16;
+    const int mine = pieces / k.splits, at_once = kMove / mine;  // pieces of a row, rows of a step of one each
+    const int row = threadIdx.x / mine;
+    const bool on = row < at_once;
+    uint4* pool = static_cast<uint4*>((unit & 1) == 0 ? c.k_cache : c.v_cache) + share * mine + threadIdx.x % mine;
+    const int64_t* from = k.from + static_cast<int64_t>(i) * keep;
+    const int64_t head = static_cast<int64_t>(kvh) << c.page_shift;
+    const int mask = (1 << c.page_shift) - 1, step = at_once * kRowsEach;
+    struct Step {
+        uint4 r[kRowsEach];
+        int page[kRowsEach];  // that they go to
+    };
+    auto load = [&](Step& x, int d) __attribute__((always_inline)) {
+        int64_t at[kRowsEach];
+#pragma unroll
+        for (int n = 0; n < kRowsEach; ++n) {
+            const int to = min(d + n * at_once + row, keep - 1);
+            at[n] = from[to];
+            x.page[n] = table[to >> c.page_shift];
+        }
+#pragma unroll
+        for (int n = 0; n < kRowsEach; ++n) x.r[n] = pool[(at[n] + head) * pieces];
+    };
+    // The rows of a step have arrived in every wave before any of its places is written.
+    auto store = [&](Step& x, int d) __attribute__((always_inline)) {
+#pragma unroll
+        for (int n = 0; n < kRowsEach; ++n) asm volatile("" : "+v"(x.r[n].x), "+v"(x.r[n].y), "+v"(x.r[n].z), "+v"(x.r[n].w));
+        lds_barrier();
+#pragma unroll
+        for (int n = 0; n < kRowsEach; ++n) {
+            const int to = d + n * at_once + row;
+            if (on && to < keep) pool[(((static_cast<int64_t>(x.page[n]) * c.Hkv) << c.page_shift) + head + (to & mask)) * pieces] = x.r[n];
+        }
+    };
+    Step a, b;
+    load(a, d0);
+    for (int d = d0; d < keep; d += 2 * step) {
+        load(b, d + step);
+        store(a, d);
+        if (d + step >= keep) break;
+        load(a, d + 2 * step);
+        store(b, d + step);
+    }
 }
 
 size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -244,27 +333,31 @@ size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 }  // namespace
 
 size_t cache_evict_workspace_bytes(int n, int keep) {
-    return up256(static_cast<size_t>(n) * keep * 4) + up256(static_cast<size_t>(n) * 4);
+    const size_t all = static_cast<size_t>(n) * keep;
+    return up256(all * 4) + up256(all * 8) + up256(static_cast<size_t>(n) * 4);
 }
 
 hipError_t launch_cache_evict(const CacheArgs& c, const EvictArgs& a, hipStream_t s) {
     if (a.n == 0) return hipSuccess;
+    const size_t all = static_cast<size_t>(a.n) * a.keep;
     char* ws = static_cast<char*>(a.ws);
-    EvictK k{c, a, reinterpret_cast<int32_t*>(ws), reinterpret_cast<int32_t*>(ws + up256(static_cast<size_t>(a.n) * a.keep * 4))};
+    EvictK k{c, a, nullptr, nullptr, nullptr, 1};
+    k.list = reinterpret_cast<int32_t*>(ws);
+    ws += up256(all * 4);
+    k.from = reinterpret_cast<int64_t*>(ws);
+    ws += up256(all * 8);
+    k.plan = reinterpret_cast<int32_t*>(ws);
     {
         LaunchTimer timer("cache_evict_plan", s);
         cache_evict_plan_kernel<<<dim3(a.n), dim3(kPlan), 0, s>>>(k);
     }
-    hipError_t e = hipGetLastError();
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    {
-        LaunchTimer timer("cache_evict_move", s);
-        cache_evict_move_kernel<<<dim3(a.n, 2 * c.Hkv), dim3(kMove), 0, s>>>(k);
-    }
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    LaunchTimer timer("cache_evict_finish", s);
-    cache_evict_finish_kernel<<<dim3(a.n), dim3(kMove), 0, s>>>(k);
+    // few workgroups: each takes fewer channels of more rows, 64 bytes of a row at least
+    const int row = (c.dk < c.dv ? c.dk : c.dv) * (c.x == DT::BF16 ? 2 : 4);
+    while (k.splits < 4 && static_cast<int64_t>(a.n) * 2 * c.Hkv * k.splits < 512 && row / (2 * k.splits) >= 64) k.splits *= 2;
+    LaunchTimer timer("cache_evict_move", s);
+    cache_evict_move_kernel<<<dim3(a.n, 2 * c.Hkv * k.splits + 1), dim3(kMove), 0, s>>>(k);
     return hipGetLastError();
 }
 
