@@ -829,7 +829,7 @@ int attn_backward_impl(const View& view, int64_t T_tot, int32_t H, int32_t Hkv, 
                               const void* dy, void* grad_q, void* grad_k, void* grad_v, void* grad_out_gate,
                               void* workspace, size_t workspace_bytes, void* stream) {
     int st = check_heads(H, Hkv, dk, dv, x_dtype, scale);
-    if (st == KDA_OK) st = check_packed(T_tot, N, cu_seqlens, 2 * static_cast<int64_t>(H));
+    if (st == KDA_OK) st = check_packed(T_tot, N, cu_seqlens, (view.bounded ? 4 : 2) * static_cast<int64_t>(H));  // key and query tiles, and at most as many again
     if (st == KDA_OK) st = check_view(view, T_tot, "T_tot");
     if (st != KDA_OK) return st;
     if (T_tot * H >= 16 * kMostGroups)  // the kernel of the rows takes 16 a workgroup

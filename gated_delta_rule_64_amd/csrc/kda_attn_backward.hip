@@ -44,7 +44,46 @@ struct BwdK {
     float* part;      // [parts][T, Hkv][dk + dv]
     float* q_part;    // [q_parts][T, H][dk]
     int window, sinks;
+    // With a window: the first tokens' far queries, worked on apart (far_parts 0: not).
+    int far_tiles, far_parts;
+    int64_t far_buckets;
+    float* far;       // [1 + far_parts][far_buckets, sinks, Hkv][dk + dv]
 };
+
+// The kernel's arguments (its only parameter but for numbers), read again: the
+// compiler loads all of them at the start and would keep those that only the
+// results need in scalar registers that the loop has no room for.
+__device__ __forceinline__ BwdK again() {
+    typedef const __attribute__((address_space(4))) BwdK* Args;
+    uint64_t at = reinterpret_cast<uint64_t>(__builtin_amdgcn_kernarg_segment_ptr());
+    asm volatile("" : "+s"(at));
+    const Args from = reinterpret_cast<Args>(at);
+    BwdK a;
+    __builtin_memcpy(&a, from, sizeof(a));
+    return a;
+}
+
+// The first tokens of a sequence are attended by every token of it, the others
+// by window + 127 of their tile at most: a tile of first tokens would be many
+// times as long as the rest.  So it takes as many queries as the others do, and
+// those behind, from far_from() on, go to workgroups of their own, in parts.
+// Only sequences of reach() tokens or more have such queries.  There is at most
+// one that begins in each bucket of so many tokens, the one that holds the
+// bucket's last token.
+__device__ __forceinline__ int reach(const BwdK& a) { return a.window + kRows; }
+template <int kQ>
+__device__ __forceinline__ int far_from(const BwdK& a, int k_first, int len) {
+    return k_first + (min(len - k_first, kRows - 1 + a.window) + kQ - 1) / kQ * kQ;
+}
+__device__ __forceinline__ bool far_sequence(const BwdK& a, int64_t bucket, int64_t& start, int& len) {
+    const int64_t token = (bucket + 1) * reach(a) - 1;
+    seq_bounds(a.cu, a.cu == nullptr ? 0 : find_seq(a.cu, a.N, token), a.T, start, len);
+    return start >= bucket * reach(a) && start <= token && token < start + len && len >= reach(a);
+}
+// A row's place in the far sums.
+__device__ __forceinline__ float* far_row(const BwdK& a, int slot, int64_t bucket, int key, int kvh, int width) {
+    return a.far + (((slot * a.far_buckets + bucket) * a.sinks + key) * a.Hkv + kvh) * width;
+}
 
 // One row (token, head) per 16 lanes, so that a load takes whole lines of
 // neighbouring rows.  Bound by memory: 131,072 rows of 128, 68 MB, in 15 us
@@ -246,10 +285,11 @@ __device__ __forceinline__ void query_gradients(const BwdK& a, unsigned block, c
         j0 = j2;
     }
     if (c >= rows) return;
-    if (a.q_parts > 1)
-        store_rows<float, DK>(a.q_part + (static_cast<int64_t>(part) * a.T * a.H + at) * DK, acc, a.scale, half);
+    const BwdK b = kWin ? again() : a;
+    if (b.q_parts > 1)
+        store_rows<float, DK>(b.q_part + (static_cast<int64_t>(part) * b.T * b.H + at) * DK, acc, b.scale, half);
     else
-        store_rows<T, DK>(static_cast<T*>(a.dq) + at * DK, acc, a.scale, half);
+        store_rows<T, DK>(static_cast<T*>(b.dq) + at * DK, acc, b.scale, half);
 }
 
 template <typename T, int DK, int DV>
@@ -272,7 +312,7 @@ struct DkvSizes {
 // the sequence of its steps of 32 queries, head by head of the group; the
 // parts cut it into equal pieces where there are few tiles, and their sums
 // (fp32) are added by attn_bwd_sum_kernel.
-template <typename T, int DK, int DV, bool kWin>
+template <typename T, int DK, int DV, bool kWin, bool kFar>
 __device__ __forceinline__ void key_gradients(const BwdK& a, unsigned block, char* smem) {
     using Sz = DkvSizes<T, DK, DV>;
     constexpr int kQ = Sz::kQ;
@@ -285,13 +325,30 @@ __device__ __forceinline__ void key_gradients(const BwdK& a, unsigned block, cha
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int c = lane & 31, half = lane >> 5;
     const int G = a.H / a.Hkv;
-    const int64_t rank = block / (a.Hkv * a.parts);
-    const int slot = block % (a.Hkv * a.parts);
-    const int kvh = slot % a.Hkv, part = slot / a.Hkv;
-    const Tile t = find_tile<kRows>(a.cu, a.N, a.T, rank);
-    if (!t.there) return;
-    // the first keys of a sequence have the most queries: levels from the end
-    const int k_first = (t.tiles - 1 - t.level) * kRows;
+    int kvh, part, parts, k_first;
+    int64_t bucket = 0;
+    Tile t;
+    if constexpr (kFar) {
+        parts = a.far_parts;
+        part = block % parts;
+        kvh = block / parts % a.Hkv;
+        k_first = static_cast<int>(block / (parts * a.Hkv) % a.far_tiles) * kRows;
+        bucket = block / (parts * a.Hkv) / a.far_tiles;
+        if (!far_sequence(a, bucket, t.start, t.len)) return;
+        t.len = uniform(t.len);
+        t.start = uniform64(t.start);
+        if (far_from<kQ>(a, k_first, t.len) >= t.len) return;
+    } else {
+        const int64_t rank = block / (a.Hkv * a.parts);
+        const int slot = block % (a.Hkv * a.parts);
+        parts = a.parts;
+        kvh = slot % a.Hkv;
+        part = slot / a.Hkv;
+        t = find_tile<kRows>(a.cu, a.N, a.T, rank);
+        if (!t.there) return;
+        // the first keys of a sequence have the most queries: levels from the end
+        k_first = (t.tiles - 1 - t.level) * kRows;
+    }
     const int k0 = k_first + wave * 32;
     const int rows = min(32, t.len - k0);
 
@@ -337,16 +394,17 @@ __device__ __forceinline__ void key_gradients(const BwdK& a, unsigned block, cha
     ro.init_rows(c, half);
     ro.init_columns(lane);
     uint2 stat{};
-    // the queries that attend some key of the tile: [k_first, end)
-    int end = t.len;
-    if constexpr (kWin) {
-        if (k_first >= a.sinks) end = min(t.len, k_first + kRows - 1 + a.window);
+    // the queries that attend some key of the tile, and this workgroup's share of them: [i_first, end)
+    int i_first = k_first, end = t.len;
+    if constexpr (kFar) i_first = far_from<kQ>(a, k_first, t.len);
+    else if constexpr (kWin) {
+        if (k_first >= a.sinks || a.far_parts > 0) end = min(t.len, k_first + kRows - 1 + a.window);
     }
-    const int steps = (end - k_first + kQ - 1) / kQ;  // per head
+    const int steps = (end - i_first + kQ - 1) / kQ;  // per head
     const int64_t all = static_cast<int64_t>(steps) * G;
-    int n = static_cast<int>(all * part / a.parts);
-    const int n_end = static_cast<int>(all * (part + 1) / a.parts);
-    int f_head = uniform(kvh * G + n / steps), f_i0 = uniform(k_first + n % steps * kQ);  // the next step to fetch
+    int n = static_cast<int>(all * part / parts);
+    const int n_end = static_cast<int>(all * (part + 1) / parts);
+    int f_head = uniform(kvh * G + n / steps), f_i0 = uniform(i_first + n % steps * kQ);  // the next step to fetch
     auto fetch = [&]() __attribute__((always_inline)) {
         const int here = min(kQ, t.len - f_i0);
         cq.load(rows_of(static_cast<const T*>(a.q) + f_head * DK, t.start + f_i0, q_row, here), q_row, tid);
@@ -356,7 +414,7 @@ __device__ __forceinline__ void key_gradients(const BwdK& a, unsigned block, cha
             stat = buffer_load8(rows_of(a.stats + f_head, t.start + f_i0, a.H * 8, here), c * a.H * 8);
         f_i0 += kQ;
         if (f_i0 >= end) {
-            f_i0 = k_first;
+            f_i0 = i_first;
             ++f_head;
         }
     };
@@ -367,7 +425,7 @@ __device__ __forceinline__ void key_gradients(const BwdK& a, unsigned block, cha
     };
     int i0 = f_i0 - kQ;  // the step worked on
     auto work = [&](const char* sQ) __attribute__((always_inline)) {
-        i0 = i0 + kQ < end ? i0 + kQ : k_first;
+        i0 = i0 + kQ < end ? i0 + kQ : i_first;
         if (i0 + kQ - 1 < k0) return;  // queries before this wave's keys
         if constexpr (kWin) {
             if (i0 - a.window > k0 + 30 && k0 >= a.sinks) return;  // and those that have left them behind
@@ -440,15 +498,32 @@ __device__ __forceinline__ void key_gradients(const BwdK& a, unsigned block, cha
         work(smem + Sz::kBuf);
         if (n + 2 < n_end) put(smem);
     }
-    if (c < rows) {
-        const int64_t at = (t.start + k0 + c) * a.Hkv + kvh;
-        if (a.parts > 1) {
-            float* to = a.part + (static_cast<int64_t>(part) * a.T * a.Hkv + at) * (DK + DV);
+    if constexpr (kFar) {
+        if (c < rows && k0 + c < a.sinks) {
+            float* to = far_row(a, 1 + part, bucket, k0 + c, kvh, DK + DV);
             store_rows<float, DK>(to, gk, a.scale, half);
             store_rows<float, DV>(to + DK, gv, 1.f, half);
+        }
+        return;
+    }
+    const BwdK b = kWin ? again() : a;
+    if (kWin && b.parts == 1 && b.far_parts > 0 && k_first < b.sinks && far_from<kQ>(b, k_first, t.len) < t.len) {
+        if (c < rows && k0 + c < b.sinks) {
+            float* to = far_row(b, 0, t.start / reach(b), k0 + c, kvh, DK + DV);
+            store_rows<float, DK>(to, gk, b.scale, half);
+            store_rows<float, DV>(to + DK, gv, 1.f, half);
+            return;
+        }
+    }
+    if (c < rows) {
+        const int64_t at = (t.start + k0 + c) * b.Hkv + kvh;
+        if (b.parts > 1) {
+            float* to = b.part + (static_cast<int64_t>(part) * b.T * b.Hkv + at) * (DK + DV);
+            store_rows<float, DK>(to, gk, b.scale, half);
+            store_rows<float, DV>(to + DK, gv, 1.f, half);
         } else {
-            store_rows<T, DK>(static_cast<T*>(a.dk) + at * DK, gk, a.scale, half);
-            store_rows<T, DV>(static_cast<T*>(a.dv) + at * DV, gv, 1.f, half);
+            store_rows<T, DK>(static_cast<T*>(b.dk) + at * DK, gk, b.scale, half);
+            store_rows<T, DV>(static_cast<T*>(b.dv) + at * DV, gv, 1.f, half);
         }
     }
 }
@@ -460,10 +535,15 @@ __device__ __forceinline__ void key_gradients(const BwdK& a, unsigned block, cha
 // workgroups a CU (fp32 at 64 channels: 4,000 tokens 1,900 us, 2,180 with one;
 // the ragged batch of up to 1,000 tokens 301 us, 355 with one).
 template <typename T, int DK, int DV, bool kWin>
-__global__ __launch_bounds__(kThreads, (DK * sizeof(T) <= 256 ? 2 : 1)) void attn_bwd_kernel(BwdK a, unsigned key_groups) {
+__global__ __launch_bounds__(kThreads, (DK * sizeof(T) <= 256 ? 2 : 1)) void attn_bwd_kernel(BwdK a, unsigned key_groups, unsigned far_groups) {
     extern __shared__ __align__(16) char smem[];
-    if (blockIdx.x < key_groups) key_gradients<T, DK, DV, kWin>(a, blockIdx.x, smem);
-    else query_gradients<T, DK, DV, kWin>(a, blockIdx.x - key_groups, smem);
+    unsigned block = blockIdx.x;
+    if constexpr (kWin) {
+        if (block < far_groups) return key_gradients<T, DK, DV, true, true>(a, block, smem);
+        block -= far_groups;
+    }
+    if (block < key_groups) key_gradients<T, DK, DV, kWin, false>(a, block, smem);
+    else query_gradients<T, DK, DV, kWin>(a, block - key_groups, smem);
 }
 
 // Adds the parts in their order, four channels per thread: first the rows of
@@ -499,6 +579,37 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_sum_kernel(BwdK a) {
     st4(static_cast<T*>(a.dq) + i * 4, sum);
 }
 
+// The first tokens' gradients: what their own tile's workgroups summed, then the
+// far parts in their order.
+template <typename T, int DK, int DV>
+__global__ __launch_bounds__(kThreads) void attn_bwd_far_sum_kernel(BwdK a) {
+    constexpr int kKv = (DK + DV) / 4;
+    int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    const int ch = static_cast<int>(i % kKv) * 4;
+    i /= kKv;
+    const int kvh = static_cast<int>(i % a.Hkv);
+    i /= a.Hkv;
+    const int key = static_cast<int>(i % a.sinks);
+    const int64_t bucket = i / a.sinks;
+    int64_t start;
+    int len;
+    if (bucket >= a.far_buckets || !far_sequence(a, bucket, start, len)) return;
+    if (far_from<DkvSizes<T, DK, DV>::kQ>(a, key / kRows * kRows, len) >= len) return;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    auto add = [&](const float* from) {
+        float x[4];
+        ld4(from + ch, x);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[e] += x[e];
+    };
+    const int64_t row = (start + key) * a.Hkv + kvh;
+    if (a.parts > 1)
+        for (int p = 0; p < a.parts; ++p) add(a.part + (p * a.T * a.Hkv + row) * (DK + DV));
+    for (int p = a.parts > 1 ? 1 : 0; p <= a.far_parts; ++p) add(far_row(a, p, bucket, key, kvh, DK + DV));
+    if (ch < DK) st4(static_cast<T*>(a.dk) + row * DK + ch, sum);
+    else st4(static_cast<T*>(a.dv) + row * DV + ch - DK, sum);
+}
+
 // Into how many parts the work of a tile is cut: key tiles so that their
 // workgroups, which differ in length, fill the chip several times; query tiles
 // where they and the key tiles' together leave it half empty.
@@ -514,6 +625,31 @@ BwdParts bwd_parts(int64_t T, int N, int H, int Hkv) {
         return static_cast<int>(p < 1 ? 1 : p > most ? most : p);
     };
     return {parts(kKeyWant, keys, kMostParts), parts(kQueryWant, queries, kMostParts / 2)};
+}
+
+// The far queries' workgroups.  More first tokens than a tile's reach are
+// balanced as they are.  Parts as long as the other workgroups', as far as their
+// sums stay few (kFarRows rows of all heads).
+constexpr int kMostFarParts = 64;
+constexpr int64_t kFarRows = 16384, kFarGroups = 65536;
+struct FarPlan {
+    int64_t buckets = 0;
+    int tiles = 0, parts = 0;
+    int64_t rows(int sinks) const { return buckets * sinks; }
+};
+FarPlan far_plan(int64_t T, int Hkv, int window, int sinks, int near_parts) {
+    FarPlan p;
+    const int64_t reach = static_cast<int64_t>(window) + kRows;
+    if (window < 1 || sinks < 1 || sinks > reach || T < reach) return p;
+    p.buckets = T / reach;
+    p.tiles = (sinks + kRows - 1) / kRows;
+    int64_t parts = ((T - reach) * near_parts + reach - 1) / reach;
+    const int64_t groups = p.buckets * p.tiles * Hkv, rows = p.rows(sinks);
+    if (parts > kMostFarParts) parts = kMostFarParts;
+    if (parts * groups > kFarGroups) parts = kFarGroups / groups;
+    if (parts * rows > kFarRows) parts = kFarRows / rows;
+    p.parts = static_cast<int>(parts < 1 ? 1 : parts);
+    return p;
 }
 
 size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -544,6 +680,14 @@ hipError_t launch_bwd(const AttnBackwardArgs& a, hipStream_t s) {
     k.part = reinterpret_cast<float*>(ws);
     if (k.parts > 1) ws += up256(static_cast<size_t>(k.parts) * f.T * f.Hkv * (DK + DV) * 4);
     k.q_part = reinterpret_cast<float*>(ws);
+    if (k.q_parts > 1) ws += up256(static_cast<size_t>(k.q_parts) * f.T * f.H * DK * 4);
+    if constexpr (kWin) {
+        const FarPlan far = far_plan(f.T, f.Hkv, k.window, k.sinks, k.parts);
+        k.far_buckets = far.buckets;
+        k.far_tiles = far.tiles;
+        k.far_parts = far.parts;
+        k.far = reinterpret_cast<float*>(ws);
+    }
     constexpr int lds = DqSizes<T, DK, DV>::kLds > DkvSizes<T, DK, DV>::kLds ? DqSizes<T, DK, DV>::kLds : DkvSizes<T, DK, DV>::kLds;
     hipError_t e = allow_lds(attn_bwd_kernel<T, DK, DV, kWin>, lds);
     if (e != hipSuccess) return e;
@@ -557,9 +701,9 @@ hipError_t launch_bwd(const AttnBackwardArgs& a, hipStream_t s) {
     const int64_t tiles = attn_tiles(f.T, f.N, kRows);
     {
         LaunchTimer timer(kWin ? "attn_window_bwd" : "attn_bwd", s);
-        const int64_t key_groups = tiles * f.Hkv * k.parts;
-        attn_bwd_kernel<T, DK, DV, kWin><<<dim3(static_cast<unsigned>(key_groups + tiles * f.H * k.q_parts)), dim3(kThreads), lds, s>>>(
-            k, static_cast<unsigned>(key_groups));
+        const int64_t key_groups = tiles * f.Hkv * k.parts, far_groups = k.far_buckets * k.far_tiles * f.Hkv * k.far_parts;
+        attn_bwd_kernel<T, DK, DV, kWin><<<dim3(static_cast<unsigned>(far_groups + key_groups + tiles * f.H * k.q_parts)), dim3(kThreads), lds, s>>>(
+            k, static_cast<unsigned>(key_groups), static_cast<unsigned>(far_groups));
     }
     e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -570,32 +714,43 @@ hipError_t launch_bwd(const AttnBackwardArgs& a, hipStream_t s) {
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
+    if constexpr (kWin) {
+        if (k.far_parts > 0) {
+            LaunchTimer timer("attn_window_bwd_far_sum", s);
+            const int64_t threads = k.far_buckets * k.sinks * f.Hkv * ((DK + DV) / 4);
+            attn_bwd_far_sum_kernel<T, DK, DV><<<dim3(static_cast<unsigned>((threads + kThreads - 1) / kThreads)), dim3(kThreads), 0, s>>>(k);
+        }
+    }
     return hipGetLastError();
 }
 
 }  // namespace
 
 size_t attn_backward_workspace_bytes(int64_t T, int N, int H, int Hkv, int dk, int dv, DT x, bool gate, int window, int sinks) {
-    (void)window;
-    (void)sinks;
     const size_t rows = static_cast<size_t>(T) * H;
     const BwdParts parts = bwd_parts(T, N, H, Hkv);
+    const FarPlan far = far_plan(T, Hkv, window, sinks, parts.key);
     return up256(rows * 8) + (gate ? up256(rows * dv * (x == DT::BF16 ? 2 : 4)) : 0) +
            (parts.key > 1 ? up256(static_cast<size_t>(parts.key) * T * Hkv * (dk + dv) * 4) : 0) +
-           (parts.query > 1 ? up256(static_cast<size_t>(parts.query) * rows * dk * 4) : 0);
+           (parts.query > 1 ? up256(static_cast<size_t>(parts.query) * rows * dk * 4) : 0) +
+           (far.parts > 0 ? up256(static_cast<size_t>(1 + far.parts) * far.rows(sinks) * Hkv * (dk + dv) * 4) : 0);
 }
 
 // More tokens have fewer parts, so what a call needs does not rise with its
 // sizes.  One sequence has the fewest tiles and so the most parts; of the
 // lengths of as many tiles the longest needs the most; from kKeyWant tiles on
-// there is one part.
+// there is one part.  The far sums' parts fall as their rows rise: p parts of r
+// rows are at most kMostFarParts r and at most kFarRows or r.
 size_t attn_backward_max_workspace_bytes(int64_t T, int H, int Hkv, int dk, int dv, DT x, bool gate, int window, int sinks) {
-    size_t most = attn_backward_workspace_bytes(T, 1, H, Hkv, dk, dv, x, gate, window, sinks);
+    size_t most = attn_backward_workspace_bytes(T, 1, H, Hkv, dk, dv, x, gate, 0, 0);
     for (int64_t t = kRows - 1; t < T && t < static_cast<int64_t>(kKeyWant) * kRows; t += kRows) {
-        const size_t need = attn_backward_workspace_bytes(t, 1, H, Hkv, dk, dv, x, gate, window, sinks);
+        const size_t need = attn_backward_workspace_bytes(t, 1, H, Hkv, dk, dv, x, gate, 0, 0);
         most = need > most ? need : most;
     }
-    return most;
+    const FarPlan far = far_plan(T, Hkv, window, sinks, 1);
+    if (far.parts == 0) return most;
+    const int64_t rows = far.rows(sinks), parts = rows > kFarRows ? rows : rows * kMostFarParts < kFarRows ? rows * kMostFarParts : kFarRows;
+    return most + up256(static_cast<size_t>(rows + parts) * Hkv * (dk + dv) * 4);
 }
 
 hipError_t launch_attn_prefill_backward(const AttnBackwardArgs& a, hipStream_t s) {

@@ -526,8 +526,9 @@ int kda_attn_prefill_backward(int64_t T_tot, int32_t H, int32_t Hkv, int32_t dk,
  *                 up to max_T_tot tokens in any number of sequences, with that
  *                 window and those sinks, by
  *                 kda_attn_window_backward_max_workspace_bytes().
- * T_tot must be below 2^29, and the limits of the calls above hold
- * (KDA_ERR_UNSUPPORTED otherwise).  A row that is not finite may also reach
+ * T_tot must be below 2^29, for the gradients H x (T_tot/128 + min(N, T_tot))
+ * below 2^22, and the limits of the calls above hold (KDA_ERR_UNSUPPORTED
+ * otherwise).  A row that is not finite may also reach
  * rows up to 190 tokens from those that attend it, and gradients of tokens as
  * far from those that such rows attend.
  */

@@ -98,6 +98,26 @@ def test_longer_sequences(K, window, sinks):
     _check(K, x, lens, window, sinks, torch.bfloat16)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("window,sinks", [(40, 3), (90, 140), (3, 131), (200, 1)])
+def test_first_tokens_of_many_long_sequences(K, window, sinks, dtype):
+    """Their far queries are worked on apart: sequences that begin anywhere, of
+    just the lengths at which there are some, between short and empty ones."""
+    reach = window + 128
+    lens = [reach - 1, 0, reach, 5, reach + 1, 700, 130, reach + 33, 1, 1100, reach - 1, 257]
+    print(f"first tokens {window} {sinks} {dtype}", flush=True)
+    x = _inputs(window, lens, 2, 1, 32, 32, TYPES[dtype], True, spare=9)
+    _check(K, x, lens, window, sinks, TYPES[dtype])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_first_tokens_where_tiles_are_not_cut(K, dtype):
+    """So many key tiles that none is cut into parts; the far queries are."""
+    lens = [2500, 129, 2100]
+    x = _inputs(17, lens, 32, 32, 16, 16, TYPES[dtype], False)
+    _check(K, x, lens, 100, 5, TYPES[dtype])
+
+
 def test_many_sequences(K):
     lens = [(i * 37) % 19 for i in range(150)] + [300] + [(i * 11) % 7 for i in range(70)]
     x = _inputs(6, lens, 2, 2, 32, 32, torch.float32, False)
