@@ -546,41 +546,72 @@ __global__ __launch_bounds__(kThreads, (DK * sizeof(T) <= 256 ? 2 : 1)) void att
     else query_gradients<T, DK, DV, kWin>(a, block - key_groups, smem);
 }
 
+// Adds four channels of `parts` rows `step` apart, in their order, eight in flight.
+__device__ __forceinline__ void add_parts(const float* from, int64_t step, int parts, float (&sum)[4]) {
+    constexpr int kEach = 8;
+    for (int p0 = 0; p0 < parts; p0 += kEach) {
+        float x[kEach][4];
+#pragma unroll
+        for (int p = 0; p < kEach; ++p)
+            if (p0 + p < parts) ld4(from + (p0 + p) * step, x[p]);
+#pragma unroll
+        for (int p = 0; p < kEach; ++p)
+            if (p0 + p < parts) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum[e] += x[p][e];
+            }
+    }
+}
+
+template <typename T, int DK, int DV>
+__device__ __forceinline__ void store_sum(const BwdK& a, int64_t row, int ch, const float (&sum)[4]) {
+    if (ch < DK) st4(static_cast<T*>(a.dk) + row * DK + ch, sum);
+    else st4(static_cast<T*>(a.dv) + row * DV + ch - DK, sum);
+}
+
+// Adds what far queries gave to a first token; false: there are none.
+template <typename T, int DK, int DV>
+__device__ __forceinline__ bool add_far(const BwdK& a, int64_t bucket, int key, int len, int kvh, int ch, int first, float (&sum)[4]) {
+    if (far_from<DkvSizes<T, DK, DV>::kQ>(a, key / kRows * kRows, len) >= len) return false;
+    const int64_t step = a.far_buckets * a.sinks * a.Hkv * (DK + DV);
+    add_parts(far_row(a, first, bucket, key, kvh, DK + DV) + ch, step, 1 + a.far_parts - first, sum);
+    return true;
+}
+
 // Adds the parts in their order, four channels per thread: first the rows of
 // the key heads (dk and dv together), then those of the query heads.  Bound by
 // memory: four parts of 4,096 tokens of 8 heads, 151 MB, in 23 us (6.6 TB/s,
 // a part of it from the caches).
-template <typename T, int DK, int DV>
+template <typename T, int DK, int DV, bool kWin>
 __global__ __launch_bounds__(kThreads) void attn_bwd_sum_kernel(BwdK a) {
     constexpr int kKv = (DK + DV) / 4, kQ = DK / 4;
     const int64_t tokens = a.cu == nullptr ? a.T : min(static_cast<int64_t>(max(a.cu[a.N], 0)), a.T);
     const int64_t kv_all = a.parts > 1 ? tokens * a.Hkv * kKv : 0, q_all = a.q_parts > 1 ? tokens * a.H * kQ : 0;
     int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    auto add = [&](const float* from, int64_t step, int parts, float (&sum)[4]) {
-        for (int p = 0; p < parts; ++p) {
-            float x[4];
-            ld4(from + p * step, x);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sum[e] += x[e];
-        }
-    };
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
     if (i < kv_all) {
         const int64_t row = i / kKv;
         const int ch = static_cast<int>(i % kKv) * 4;
-        add(a.part + row * (DK + DV) + ch, a.T * a.Hkv * (DK + DV), a.parts, sum);
-        if (ch < DK) st4(static_cast<T*>(a.dk) + row * DK + ch, sum);
-        else st4(static_cast<T*>(a.dv) + row * DV + ch - DK, sum);
+        add_parts(a.part + row * (DK + DV) + ch, a.T * a.Hkv * (DK + DV), a.parts, sum);
+        if (kWin && a.far_parts > 0) {
+            const int64_t token = row / a.Hkv;
+            int64_t start;
+            int len;
+            seq_bounds(a.cu, a.cu == nullptr ? 0 : find_seq(a.cu, a.N, token), a.T, start, len);
+            if (token - start < a.sinks && len >= reach(a))
+                add_far<T, DK, DV>(a, start / reach(a), static_cast<int>(token - start), len, static_cast<int>(row % a.Hkv), ch, 1, sum);
+        }
+        store_sum<T, DK, DV>(a, row, ch, sum);
         return;
     }
     i -= kv_all;
     if (i >= q_all) return;
-    add(a.q_part + i * 4, a.T * a.H * DK, a.q_parts, sum);
+    add_parts(a.q_part + i * 4, a.T * a.H * DK, a.q_parts, sum);
     st4(static_cast<T*>(a.dq) + i * 4, sum);
 }
 
-// The first tokens' gradients: what their own tile's workgroups summed, then the
-// far parts in their order.
+// The first tokens' gradients where no tile is cut into parts: what their own
+// tile's workgroup summed, then the far parts.
 template <typename T, int DK, int DV>
 __global__ __launch_bounds__(kThreads) void attn_bwd_far_sum_kernel(BwdK a) {
     constexpr int kKv = (DK + DV) / 4;
@@ -594,37 +625,28 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_far_sum_kernel(BwdK a) {
     int64_t start;
     int len;
     if (bucket >= a.far_buckets || !far_sequence(a, bucket, start, len)) return;
-    if (far_from<DkvSizes<T, DK, DV>::kQ>(a, key / kRows * kRows, len) >= len) return;
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
-    auto add = [&](const float* from) {
-        float x[4];
-        ld4(from + ch, x);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sum[e] += x[e];
-    };
-    const int64_t row = (start + key) * a.Hkv + kvh;
-    if (a.parts > 1)
-        for (int p = 0; p < a.parts; ++p) add(a.part + (p * a.T * a.Hkv + row) * (DK + DV));
-    for (int p = a.parts > 1 ? 1 : 0; p <= a.far_parts; ++p) add(far_row(a, p, bucket, key, kvh, DK + DV));
-    if (ch < DK) st4(static_cast<T*>(a.dk) + row * DK + ch, sum);
-    else st4(static_cast<T*>(a.dv) + row * DV + ch - DK, sum);
+    if (add_far<T, DK, DV>(a, bucket, key, len, kvh, ch, 0, sum)) store_sum<T, DK, DV>(a, (start + key) * a.Hkv + kvh, ch, sum);
 }
 
 // Into how many parts the work of a tile is cut: key tiles so that their
 // workgroups, which differ in length, fill the chip several times; query tiles
 // where they and the key tiles' together leave it half empty.
 constexpr int kKeyWant = 1024, kQueryWant = 384;  // workgroups below which tiles are cut
+// With a window the workgroups of key tiles are equally long but for a
+// sequence's last ones.
+constexpr int kKeyWantWindow = 512;
 struct BwdParts {
     int key, query;
 };
-BwdParts bwd_parts(int64_t T, int N, int H, int Hkv) {
+BwdParts bwd_parts(int64_t T, int N, int H, int Hkv, int window) {
     const int64_t tiles = attn_tiles(T, N, kRows), keys = tiles * Hkv, queries = tiles * H;
     if (tiles == 0) return {1, 1};
     auto parts = [](int64_t want, int64_t units, int64_t most) {
         const int64_t p = (want + units - 1) / units;
         return static_cast<int>(p < 1 ? 1 : p > most ? most : p);
     };
-    return {parts(kKeyWant, keys, kMostParts), parts(kQueryWant, queries, kMostParts / 2)};
+    return {parts(window > 0 ? kKeyWantWindow : kKeyWant, keys, kMostParts), parts(kQueryWant, queries, kMostParts / 2)};
 }
 
 // The far queries' workgroups.  More first tokens than a tile's reach are
@@ -674,7 +696,7 @@ hipError_t launch_bwd(const AttnBackwardArgs& a, hipStream_t s) {
     ws += up256(static_cast<size_t>(f.T) * f.H * 8);
     k.dog = f.z != nullptr ? static_cast<void*>(ws) : const_cast<void*>(a.dy);
     if (f.z != nullptr) ws += up256(static_cast<size_t>(f.T) * f.H * DV * sizeof(T));
-    const BwdParts parts = bwd_parts(f.T, f.N, f.H, f.Hkv);
+    const BwdParts parts = bwd_parts(f.T, f.N, f.H, f.Hkv, f.window);
     k.parts = parts.key;
     k.q_parts = parts.query;
     k.part = reinterpret_cast<float*>(ws);
@@ -710,12 +732,12 @@ hipError_t launch_bwd(const AttnBackwardArgs& a, hipStream_t s) {
     if (k.parts > 1 || k.q_parts > 1) {
         LaunchTimer timer("attn_bwd_sum", s);
         const int64_t threads = (k.parts > 1 ? f.T * f.Hkv * ((DK + DV) / 4) : 0) + (k.q_parts > 1 ? f.T * f.H * (DK / 4) : 0);
-        attn_bwd_sum_kernel<T, DK, DV><<<dim3(static_cast<unsigned>((threads + kThreads - 1) / kThreads)), dim3(kThreads), 0, s>>>(k);
+        attn_bwd_sum_kernel<T, DK, DV, kWin><<<dim3(static_cast<unsigned>((threads + kThreads - 1) / kThreads)), dim3(kThreads), 0, s>>>(k);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     if constexpr (kWin) {
-        if (k.far_parts > 0) {
+        if (k.far_parts > 0 && k.parts == 1) {
             LaunchTimer timer("attn_window_bwd_far_sum", s);
             const int64_t threads = k.far_buckets * k.sinks * f.Hkv * ((DK + DV) / 4);
             attn_bwd_far_sum_kernel<T, DK, DV><<<dim3(static_cast<unsigned>((threads + kThreads - 1) / kThreads)), dim3(kThreads), 0, s>>>(k);
@@ -728,7 +750,7 @@ hipError_t launch_bwd(const AttnBackwardArgs& a, hipStream_t s) {
 
 size_t attn_backward_workspace_bytes(int64_t T, int N, int H, int Hkv, int dk, int dv, DT x, bool gate, int window, int sinks) {
     const size_t rows = static_cast<size_t>(T) * H;
-    const BwdParts parts = bwd_parts(T, N, H, Hkv);
+    const BwdParts parts = bwd_parts(T, N, H, Hkv, window);
     const FarPlan far = far_plan(T, Hkv, window, sinks, parts.key);
     return up256(rows * 8) + (gate ? up256(rows * dv * (x == DT::BF16 ? 2 : 4)) : 0) +
            (parts.key > 1 ? up256(static_cast<size_t>(parts.key) * T * Hkv * (dk + dv) * 4) : 0) +
@@ -742,9 +764,9 @@ size_t attn_backward_workspace_bytes(int64_t T, int N, int H, int Hkv, int dk, i
 // there is one part.  The far sums' parts fall as their rows rise: p parts of r
 // rows are at most kMostFarParts r and at most kFarRows or r.
 size_t attn_backward_max_workspace_bytes(int64_t T, int H, int Hkv, int dk, int dv, DT x, bool gate, int window, int sinks) {
-    size_t most = attn_backward_workspace_bytes(T, 1, H, Hkv, dk, dv, x, gate, 0, 0);
+    size_t most = attn_backward_workspace_bytes(T, 1, H, Hkv, dk, dv, x, gate, window, 0);
     for (int64_t t = kRows - 1; t < T && t < static_cast<int64_t>(kKeyWant) * kRows; t += kRows) {
-        const size_t need = attn_backward_workspace_bytes(t, 1, H, Hkv, dk, dv, x, gate, 0, 0);
+        const size_t need = attn_backward_workspace_bytes(t, 1, H, Hkv, dk, dv, x, gate, window, 0);
         most = need > most ? need : most;
     }
     const FarPlan far = far_plan(T, Hkv, window, sinks, 1);
