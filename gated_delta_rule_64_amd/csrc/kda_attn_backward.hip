@@ -159,9 +159,9 @@ struct DqSizes {
 };
 
 // Query gradients: one workgroup per (tile of 128 queries, head, part of the
-// keys); a wave's queries, output gradients and sums stay in its registers, the
+// keys), or of 32 queries of four heads that share their keys (as the prefill); a wave's queries, output gradients and sums stay in its registers, the
 // keys and values pass through LDS once for four waves.
-template <typename T, int DK, int DV, bool kWin>
+template <typename T, int DK, int DV, bool kWin, int kTileRows>
 __device__ __forceinline__ void query_gradients(const BwdK& a, unsigned block, char* smem) {
     using Sz = DqSizes<T, DK, DV>;
     constexpr int kKeys = Sz::kKeys, kSub = kKeys / 32;
@@ -173,12 +173,14 @@ __device__ __forceinline__ void query_gradients(const BwdK& a, unsigned block, c
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int c = lane & 31, half = lane >> 5;
     const int G = a.H / a.Hkv;
-    const int64_t rank = block / (a.H * a.q_parts);
-    const int slot = block % (a.H * a.q_parts) / a.q_parts, part = block % a.q_parts;
-    const int kvh = slot % a.Hkv, h = kvh * G + slot / a.Hkv;
-    const Tile t = find_tile<kRows>(a.cu, a.N, a.T, rank);
+    constexpr int kHeads = kRows / kTileRows;
+    const int slots = a.H / kHeads * a.q_parts;
+    const int64_t rank = block / slots;
+    const int slot = block % slots / a.q_parts, part = block % a.q_parts;
+    const int kvh = slot % a.Hkv, h = kvh * G + slot / a.Hkv * kHeads + (kHeads > 1 ? wave : 0);
+    const Tile t = find_tile<kTileRows>(a.cu, a.N, a.T, rank);
     if (!t.there) return;
-    const int q0 = t.level * kRows + wave * 32;
+    const int q0 = t.level * kTileRows + (kHeads > 1 ? 0 : wave * 32);
     const int rows = min(32, t.len - q0);
 
     const int q_row = a.H * DK * static_cast<int>(sizeof(T)), o_row = a.H * DV * static_cast<int>(sizeof(T));
@@ -207,9 +209,9 @@ __device__ __forceinline__ void query_gradients(const BwdK& a, unsigned block, c
     rk.init_rows(c, half);
     rk.init_columns(lane);
     rv.init_rows(c, half);
-    const KeyWalk<kWin, kKeys> walk(t.level * kRows, t.len, a.window, a.sinks);
+    const KeyWalk<kWin, kKeys> walk(t.level * kTileRows, t.len, a.window, a.sinks);
     // tiles that some row attends
-    const int64_t steps = walk.before((min(t.level * kRows + kRows, t.len) + kKeys - 1) / kKeys * kKeys);
+    const int64_t steps = walk.before((min(t.level * kTileRows + kTileRows, t.len) + kKeys - 1) / kKeys * kKeys);
     const int start = walk.nth(static_cast<int>(steps * part / a.q_parts));
     const int last = walk.nth(static_cast<int>(steps * (part + 1) / a.q_parts));
     const T* kbase = static_cast<const T*>(a.k) + kvh * DK;
@@ -534,7 +536,7 @@ __device__ __forceinline__ void key_gradients(const BwdK& a, unsigned block, cha
 // takes 55 + 59 us so).  Rows of up to 256 bytes leave registers for two
 // workgroups a CU (fp32 at 64 channels: 4,000 tokens 1,900 us, 2,180 with one;
 // the ragged batch of up to 1,000 tokens 301 us, 355 with one).
-template <typename T, int DK, int DV, bool kWin>
+template <typename T, int DK, int DV, bool kWin, int kTileRows>
 __global__ __launch_bounds__(kThreads, (DK * sizeof(T) <= 256 ? 2 : 1)) void attn_bwd_kernel(BwdK a, unsigned key_groups, unsigned far_groups) {
     extern __shared__ __align__(16) char smem[];
     unsigned block = blockIdx.x;
@@ -543,7 +545,7 @@ __global__ __launch_bounds__(kThreads, (DK * sizeof(T) <= 256 ? 2 : 1)) void att
         block -= far_groups;
     }
     if (block < key_groups) key_gradients<T, DK, DV, kWin, false>(a, block, smem);
-    else query_gradients<T, DK, DV, kWin>(a, block - key_groups, smem);
+    else query_gradients<T, DK, DV, kWin, kTileRows>(a, block - key_groups, smem);
 }
 
 // Adds four channels of `parts` rows `step` apart, in their order, eight in flight.
@@ -682,7 +684,7 @@ hipError_t allow_lds(F fn, int lds) {
     return hipFuncSetAttribute(reinterpret_cast<const void*>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
 }
 
-template <typename T, int DK, int DV, bool kWin>
+template <typename T, int DK, int DV, bool kWin, int kTileRows>
 hipError_t launch_bwd(const AttnBackwardArgs& a, hipStream_t s) {
     const AttnArgs& f = a.f;
     BwdK k{};
@@ -711,7 +713,7 @@ hipError_t launch_bwd(const AttnBackwardArgs& a, hipStream_t s) {
         k.far = reinterpret_cast<float*>(ws);
     }
     constexpr int lds = DqSizes<T, DK, DV>::kLds > DkvSizes<T, DK, DV>::kLds ? DqSizes<T, DK, DV>::kLds : DkvSizes<T, DK, DV>::kLds;
-    hipError_t e = allow_lds(attn_bwd_kernel<T, DK, DV, kWin>, lds);
+    hipError_t e = allow_lds(attn_bwd_kernel<T, DK, DV, kWin, kTileRows>, lds);
     if (e != hipSuccess) return e;
     {
         LaunchTimer timer("attn_bwd_rows", s);
@@ -724,7 +726,8 @@ hipError_t launch_bwd(const AttnBackwardArgs& a, hipStream_t s) {
     {
         LaunchTimer timer(kWin ? "attn_window_bwd" : "attn_bwd", s);
         const int64_t key_groups = tiles * f.Hkv * k.parts, far_groups = k.far_buckets * k.far_tiles * f.Hkv * k.far_parts;
-        attn_bwd_kernel<T, DK, DV, kWin><<<dim3(static_cast<unsigned>(far_groups + key_groups + tiles * f.H * k.q_parts)), dim3(kThreads), lds, s>>>(
+        const int64_t query_groups = attn_tiles(f.T, f.N, kTileRows) * (f.H / (kRows / kTileRows)) * k.q_parts;
+        attn_bwd_kernel<T, DK, DV, kWin, kTileRows><<<dim3(static_cast<unsigned>(far_groups + key_groups + query_groups)), dim3(kThreads), lds, s>>>(
             k, static_cast<unsigned>(key_groups), static_cast<unsigned>(far_groups));
     }
     e = hipGetLastError();
@@ -780,7 +783,8 @@ hipError_t launch_attn_prefill_backward(const AttnBackwardArgs& a, hipStream_t s
     return attn_dispatch(a.f.x, a.f.dk, a.f.dv, [&](auto t, auto dk, auto dv) {
         using X = typename decltype(t)::type;
         constexpr int kDk = decltype(dk)::value, kDv = decltype(dv)::value;
-        return a.f.window > 0 ? launch_bwd<X, kDk, kDv, true>(a, s) : launch_bwd<X, kDk, kDv, false>(a, s);
+        if (a.f.window > 0 && a.f.H / a.f.Hkv % 4 == 0) return launch_bwd<X, kDk, kDv, true, 32>(a, s);
+        return a.f.window > 0 ? launch_bwd<X, kDk, kDv, true, kRows>(a, s) : launch_bwd<X, kDk, kDv, false, kRows>(a, s);
     });
 }
 

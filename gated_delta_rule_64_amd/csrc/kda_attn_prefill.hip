@@ -46,12 +46,14 @@ template <typename T, int DK, int DV>
 struct FwdSizes {
     static constexpr int kKeys = DK > 128 || (sizeof(T) == 4 && DK > 64) ? 32 : 64;  // keys of a tile
     static constexpr int kBuf = kKeys * (DK + DV) * static_cast<int>(sizeof(T));
-    static constexpr int kTiles = 2 * kBuf + tr_slack(DV), kRows = kWaves * 32 * DV * 4;
-    static constexpr int kLds = kTiles > kRows ? kTiles : kRows;  // the results pass through the tiles' space
+    static constexpr int kTiles = 2 * kBuf + tr_slack(DV), kOut = kWaves * 32 * DV * 4;
+    static constexpr int kLds = kTiles > kOut ? kTiles : kOut;  // the results pass through the tiles' space
 };
 
 // kWin: a row attends its last `window` tokens and the first `sinks` ones.
-template <typename T, int DK, int DV, bool kWin>
+// kRows: rows of a workgroup's heads, 128 of one head or 32 of four that share
+// their keys (a wave's 32 rows then have no other rows' keys to wait for).
+template <typename T, int DK, int DV, bool kWin, int kRows>
 __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void attn_fwd_kernel(FwdK a) {
     using Sz = FwdSizes<T, DK, DV>;
     constexpr int kKeys = Sz::kKeys, kSub = kKeys / 32;
@@ -64,12 +66,14 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void attn_fwd_k
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int c = lane & 31, half = lane >> 5;
     const int G = a.H / a.Hkv;
-    const int64_t rank = blockIdx.x / a.H;
-    const int slot = blockIdx.x % a.H;
-    const int kvh = slot % a.Hkv, h = kvh * G + slot / a.Hkv;
-    const Tile t = find_tile<kQ>(a.cu, a.N, a.T, rank);
+    constexpr int kHeads = kQ / kRows;
+    const int slots = a.H / kHeads;
+    const int64_t rank = blockIdx.x / slots;
+    const int slot = blockIdx.x % slots;
+    const int kvh = slot % a.Hkv, h = kvh * G + slot / a.Hkv * kHeads + (kHeads > 1 ? wave : 0);
+    const Tile t = find_tile<kRows>(a.cu, a.N, a.T, rank);
     if (!t.there) return;
-    const int q0 = t.level * kQ + wave * 32;  // this wave's first row, in the sequence
+    const int q0 = t.level * kRows + (kHeads > 1 ? 0 : wave * 32);  // this wave's first row, in the sequence
 
     const int q_row = a.H * DK * static_cast<int>(sizeof(T));
     const int k_row = a.Hkv * DK * static_cast<int>(sizeof(T)), v_row = a.Hkv * DV * static_cast<int>(sizeof(T));
@@ -92,10 +96,10 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void attn_fwd_k
     TileRead<T, DV> rv;
     rk.init_rows(c, half);
     rv.init_columns(lane);
-    const int last = min(t.level * kQ + kQ, t.len);  // keys [0, last) are attended by some row
+    const int last = min(t.level * kRows + kRows, t.len);  // keys [0, last) are attended by some row
     const T* kbase = static_cast<const T*>(a.k) + kvh * DK;
     const T* vbase = static_cast<const T*>(a.v) + kvh * DV;
-    const KeyWalk<kWin, kKeys> walk(t.level * kQ, t.len, a.window, a.sinks);
+    const KeyWalk<kWin, kKeys> walk(t.level * kRows, t.len, a.window, a.sinks);
     auto fetch = [&](int j0) {
         const int rows = walk.rows(j0);
         ck.load(rows_of(kbase, t.start + j0, k_row, rows), k_row, tid);
@@ -233,11 +237,11 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void attn_fwd_k
     });
 }
 
-template <typename T, int DK, int DV, bool kWin>
+template <typename T, int DK, int DV, bool kWin, int kRows>
 hipError_t launch_fwd(const AttnArgs& a, hipStream_t s) {
     constexpr int lds = FwdSizes<T, DK, DV>::kLds;
     static_assert(lds <= 160 * 1024, "one workgroup's LDS");
-    auto fn = attn_fwd_kernel<T, DK, DV, kWin>;
+    auto fn = attn_fwd_kernel<T, DK, DV, kWin, kRows>;
     if (lds > 64 * 1024) {
         const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
         if (e != hipSuccess) return e;
@@ -245,7 +249,7 @@ hipError_t launch_fwd(const AttnArgs& a, hipStream_t s) {
     const FwdK k{a.T, a.H, a.Hkv, a.N, a.cu, a.q, a.k, a.v, a.z, a.out, a.lse, a.scale,
                  static_cast<int>(a.window < a.T ? a.window : a.T), static_cast<int>(a.sinks < a.T ? a.sinks : a.T)};
     LaunchTimer timer(kWin ? "attn_window_fwd" : "attn_fwd", s);
-    fn<<<dim3(static_cast<unsigned>(attn_tiles(a.T, a.N, kQ) * a.H)), dim3(kThreads), lds, s>>>(k);
+    fn<<<dim3(static_cast<unsigned>(attn_tiles(a.T, a.N, kRows) * (a.H / (kQ / kRows)))), dim3(kThreads), lds, s>>>(k);
     return hipGetLastError();
 }
 
@@ -256,7 +260,8 @@ hipError_t launch_attn_prefill(const AttnArgs& a, hipStream_t s) {
     return attn_dispatch(a.x, a.dk, a.dv, [&](auto t, auto dk, auto dv) {
         using X = typename decltype(t)::type;
         constexpr int kDk = decltype(dk)::value, kDv = decltype(dv)::value;
-        return a.window > 0 ? launch_fwd<X, kDk, kDv, true>(a, s) : launch_fwd<X, kDk, kDv, false>(a, s);
+        if (a.window > 0 && a.H / a.Hkv % 4 == 0) return launch_fwd<X, kDk, kDv, true, 32>(a, s);
+        return a.window > 0 ? launch_fwd<X, kDk, kDv, true, kQ>(a, s) : launch_fwd<X, kDk, kDv, false, kQ>(a, s);
     });
 }
 
