@@ -87,21 +87,33 @@ __device__ __forceinline__ float* weight_of(const WeighK& k, const Weighed& w, i
 // weighs nothing) or no weight there.
 __device__ __forceinline__ float gathered(float x) { return x == x ? x : 0.f; }
 
+template <typename T, int DK>
+struct FewSizes {
+    static constexpr int kKeys = 32;  // of a tile
+    static constexpr int kTile = kKeys * DK * static_cast<int>(sizeof(T));
+    static constexpr int kLds = kWaves * (kTile + kKeys * 4);  // a wave's keys, its sums
+};
+
 // Few queries: bound by reading the keys.  Scores transposed (S^T = K Q^T, 32
 // keys by the group's rows), a lane's row and its lse the same for every tile,
 // its 16 sums added over the lanes once per tile.  A wave takes its own tiles,
 // all heads of one after another (or shares a tile's heads with the others of
-// its workgroup, where there are few tiles), the next head's keys in flight
-// while one is worked on.
+// its workgroup, where there are few tiles).  Keys are read by whole rows, the
+// next head's in flight while one is worked on, and laid out in LDS for the
+// product.
 template <typename T, int DK>
-__device__ __forceinline__ void weigh_few(const WeighK& k, unsigned block, float (*sums)[32]) {
-    constexpr int kKeys = 32;
+__device__ __forceinline__ void weigh_few(const WeighK& k, unsigned block, char* smem) {
+    using Sz = FewSizes<T, DK>;
+    constexpr int kKeys = Sz::kKeys;
     constexpr int kPieces = DK / (2 * Elem<T>::kPer16);
-    constexpr int kRow = DK * static_cast<int>(sizeof(T));
+    constexpr int kRow = DK * static_cast<int>(sizeof(T)), kRowPieces = kRow / 16;
+    constexpr int kHalf = 16 * kRowPieces, kEach = (kHalf + 63) / 64;  // 16-byte pieces of 16 rows, of a lane
     const CacheArgs& c = k.c;
     const WeighArgs& a = k.a;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int col = lane & 31, half = lane >> 5;
+    char* sK = smem + wave * Sz::kTile;
+    float(*sums)[kKeys] = reinterpret_cast<float(*)[kKeys]>(smem + kWaves * Sz::kTile);
     const int n = block / k.few_groups, group = block % k.few_groups;
     Weighed w;
     if (!weighed(k, n, w)) return;
@@ -122,25 +134,70 @@ __device__ __forceinline__ void weigh_few(const WeighK& k, unsigned block, float
     const int share = all >= 4096 || c.Hkv < 2 ? 1 : all >= 2048 || c.Hkv < 4 ? 2 : 4;
     const int member = wave % share, team = wave / share, teams = kWaves / share;
     const int f0 = c.Hkv * member / share, f1 = c.Hkv * (member + 1) / share;
-    struct Item {
-        u32x4 key[kPieces], q[kPieces];
+
+    // A tile's halves of 16 rows, each in one page
+    typedef const __attribute__((address_space(4))) int32_t* scalar_ints;
+    const scalar_ints entries = (scalar_ints)(c.table + static_cast<int64_t>(w.slot) * c.max_pages);
+    struct Place {
+        int page[2], rows[2];  // rows that hold a token
+    };
+    auto look = [&](int tile) __attribute__((always_inline)) {
+        Place x;
+        const int first = tile < tiles.count ? tiles.first(tile) : w.ctx;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int p = first + 16 * h;
+            const int page = entries[min(p, w.ctx - 1) >> c.page_shift];
+            const bool there = page >= 0 && page < c.pages;
+            x.rows[h] = there ? min(16, max(0, w.ctx - p)) : 0;
+            x.page[h] = there ? page : 0;
+        }
+        return x;
+    };
+    u32x4 kr[2][kEach];
+    struct Queries {
+        u32x4 q[kPieces];
         float lse;
     };
-    const char* pool = static_cast<const char*>(c.k_cache);
-    auto load = [&](Item& x, int64_t at, int f) __attribute__((always_inline)) {
-        const char* from = pool + (at + (static_cast<int64_t>(f) << c.page_shift)) * kRow + half * 16;
+    // fp32 rows leave no registers for the next head's: read from the caches when they are used
+    constexpr bool kAhead = sizeof(T) == 2;
+    auto load_q = [&](Queries& x, int f) __attribute__((always_inline)) {
         const char* q = q_row + static_cast<int64_t>(f) * G * kRow;
         x.lse = lse_at[static_cast<int64_t>(f) * G];
 #pragma unroll
         for (int p = 0; p < kPieces; ++p) x.q[p] = *reinterpret_cast<const u32x4*>(q + p * 32);
+    };
+    const int mask = (1 << c.page_shift) - 1;
+    auto load_k = [&](const Place& x, int tile, int f) __attribute__((always_inline)) {
+        const int first = tile < tiles.count ? tiles.first(tile) : 0;
 #pragma unroll
-        for (int p = 0; p < kPieces; ++p) x.key[p] = *reinterpret_cast<const u32x4*>(from + p * 32);
+        for (int h = 0; h < 2; ++h) {
+            const int64_t row = ((static_cast<int64_t>(x.page[h]) * c.Hkv + f) << c.page_shift) + ((first + 16 * h) & mask);
+            const auto from = rows_of(c.k_cache, row, kRow, x.rows[h]);
+#pragma unroll
+            for (int i = 0; i < kEach; ++i)
+                if (kHalf >= 64 || lane < kHalf) kr[h][i] = buffer_load16(from, (lane + 64 * i) * 16);
+        }
+    };
+    TileRead<T, DK> rk;
+    rk.init_rows(col, half);
+    auto put = [&]() __attribute__((always_inline)) {
+        wave_lds_fence();
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                const int p = lane + 64 * i, row = 16 * h + p / kRowPieces;
+                if (kHalf >= 64 || lane < kHalf)
+                    *reinterpret_cast<u32x4*>(sK + row * kRow + (p % kRowPieces ^ turn<kRowPieces>(row)) * 16) = kr[h][i];
+            }
+        wave_lds_fence();
     };
     f32x16 acc{};
-    auto work = [&](const Item& x, int first) __attribute__((always_inline)) {
+    auto work = [&](const Queries& x, int first) __attribute__((always_inline)) {
         f32x16 s{};
 #pragma unroll
-        for (int p = 0; p < kPieces; ++p) s = mma<T>(x.key[p], x.q[p], s);
+        for (int p = 0; p < kPieces; ++p) s = mma<T>(rk.rows(sK, p), x.q[p], s);
         const bool good = on && fabsf(x.lse) < INFINITY;  // a row that attends nothing, or a broken one, weighs nothing
         const float lse2 = x.lse * kLog2e;
 #pragma unroll
@@ -157,7 +214,7 @@ __device__ __forceinline__ void weigh_few(const WeighK& k, unsigned block, float
         }
         acc += s;
     };
-    auto finish = [&](int first, bool there) __attribute__((always_inline)) {
+    auto finish = [&](int first, const Place& x) __attribute__((always_inline)) {
         // over the lanes of a half; key 8 (i / 4) + 4 half + i % 4
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -170,9 +227,9 @@ __device__ __forceinline__ void weigh_few(const WeighK& k, unsigned block, float
         acc = f32x16{};
         if (share > 1) __syncthreads();
         else wave_lds_fence();
-        if (member == 0 && half == 0 && there) {
+        if (member == 0 && half == 0 && (col & 15) < (col < 16 ? x.rows[0] : x.rows[1])) {
             float v = 0.f;
-            for (int x = 0; x < share; ++x) v += sums[wave + x][col];
+            for (int m = 0; m < share; ++m) v += sums[wave + m][col];
             *weight_of(k, w, first + col) += gathered(v);
         }
         if (share > 1) __syncthreads();
@@ -183,41 +240,27 @@ __device__ __forceinline__ void weigh_few(const WeighK& k, unsigned block, float
     const int turns = (tiles.count - group * teams + stride - 1) / stride;
     if (turns <= 0) return;
     int tile = group * teams + team;
-    auto look = [&](int tile, bool& there) { return row_of(k, w, tile < tiles.count ? tiles.first(tile) + col : w.ctx, there); };
-    bool there, next_there = false;
-    int64_t at = look(tile, there), next_at = 0;
-    Item x, y;
-    load(x, at, f0);
+    Place here = look(tile), next = look(tile + stride);
+    Queries x, y;
+    if constexpr (kAhead) load_q(x, f0);
+    load_k(here, tile, f0);
     for (int turn = 0; turn < turns; ++turn) {
         const int first = tile < tiles.count ? tiles.first(tile) : 0;
-        next_at = look(tile + stride, next_there);
-        int f = f0;
-        for (; f + 1 < f1; f += 2) {
-            load(y, at, f + 1);
+        for (int f = f0; f < f1; ++f) {
+            put();
+            if constexpr (kAhead) load_q(y, f + 1 < f1 ? f + 1 : f0);
+            else load_q(x, f);
+            if (f + 1 < f1) load_k(here, tile, f + 1);
+            else load_k(next, tile + stride, f0);
             work(x, first);
-            if (f + 2 < f1) load(x, at, f + 2);
-            else load(x, next_at, f0);
-            work(y, first);
+            if constexpr (kAhead) x = y;
         }
-        if (f < f1) {
-            load(y, next_at, f0);
-            work(x, first);
-            x = y;
-        }
-        finish(first, there);
+        finish(first, here);
         tile += stride;
-        at = next_at;
-        there = next_there;
+        here = next;
+        if (turn + 2 < turns) next = look(tile + stride);
     }
 }
-
-template <typename T, int DK>
-struct ManySizes {
-    static constexpr int kSub = sizeof(T) == 2 ? 2 : 1;  // blocks of 32 keys of a wave, in its registers
-    static constexpr int kKeys = kWaves * 32 * kSub;
-    static constexpr int kTile = kRows * DK * static_cast<int>(sizeof(T));
-    static constexpr int kBuf = kTile + kRows * 4;  // rows of queries and their lse
-};
 
 // How a sequence's tiles go to its workgroups: a tile each in turn, or, where
 // there are fewer tiles, several to a tile, that take equal parts of its work.
@@ -225,6 +268,14 @@ struct Shares {
     int parts;
     __device__ __forceinline__ Shares(const WeighK& k, int tiles)
         : parts(tiles >= k.many_groups ? 1 : min(k.many_groups / max(tiles, 1), k.most_parts)) {}
+};
+
+template <typename T, int DK>
+struct ManySizes {
+    static constexpr int kSub = sizeof(T) == 2 ? 2 : 1;  // blocks of 32 keys of a wave, in its registers
+    static constexpr int kKeys = kWaves * 32 * kSub;
+    static constexpr int kTile = kRows * DK * static_cast<int>(sizeof(T));
+    static constexpr int kBuf = kTile + kRows * 4;  // rows of queries and their lse
 };
 
 // Many queries: bound by the products and exponentials.  One workgroup per
@@ -402,10 +453,10 @@ __device__ __forceinline__ void weigh_many(const WeighK& k, unsigned block, char
 
 template <typename T, int DK>
 __global__ __launch_bounds__(kThreads, (DK * sizeof(T) <= 256 ? 2 : 1)) void cache_weigh_kernel(WeighK k) {
-    __shared__ __align__(16) char smem[2 * ManySizes<T, DK>::kBuf];
+    extern __shared__ __align__(16) char smem[];
     const unsigned many = static_cast<unsigned>(k.a.N) * k.many_groups;
     if (blockIdx.x < many) weigh_many<T, DK>(k, blockIdx.x, smem);
-    else weigh_few<T, DK>(k, blockIdx.x - many, reinterpret_cast<float(*)[32]>(smem));
+    else weigh_few<T, DK>(k, blockIdx.x - many, smem);
 }
 
 // Adds the parts in their order, a key per thread.
@@ -452,10 +503,16 @@ hipError_t launch_weigh(const CacheArgs& c, const WeighArgs& a, hipStream_t s) {
         k.part = static_cast<float*>(a.ws);
     }
     if (!any_many || a.N > 1) k.few_groups = per_sequence(kFewWant, a.N);
+    constexpr int few_lds = FewSizes<T, DK>::kLds, many_lds = 2 * ManySizes<T, DK>::kBuf;
+    const int lds = k.few_groups > 0 && few_lds > many_lds ? few_lds : many_lds;
+    if (few_lds > 64 * 1024) {
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(cache_weigh_kernel<T, DK>), hipFuncAttributeMaxDynamicSharedMemorySize, few_lds);
+        if (e != hipSuccess) return e;
+    }
     {
         LaunchTimer timer("cache_weigh", s);
         const int64_t groups = static_cast<int64_t>(a.N) * (k.many_groups + k.few_groups);
-        cache_weigh_kernel<T, DK><<<dim3(static_cast<unsigned>(groups)), dim3(kThreads), 0, s>>>(k);
+        cache_weigh_kernel<T, DK><<<dim3(static_cast<unsigned>(groups)), dim3(kThreads), lds, s>>>(k);
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !cut || k.many_groups <= 1) return e;
