@@ -7,9 +7,10 @@
 // lse is what the attention call gave, so the weights need no statistics of
 // their own: one pass over the keys, no values.
 //
-// Sequences of few queries (their rows of one key head, queries x heads of the
-// group, are at most 32) and of many are worked on in different ways, both in
-// one launch, since only the device knows a sequence's queries.
+// Two kernels: one for few queries a sequence (a decode step, accepted drafts),
+// one for many (the last tokens of prompts, whole prompts).  Either is right for
+// any number; the host chooses by the average, as only the device knows a
+// sequence's own.
 #include "kda_attn_common.h"
 #include "kda_internal.h"
 #include "kda_profile.h"
@@ -26,9 +27,9 @@ constexpr int kRows = 32;  // rows of a product: queries of a head, or queries a
 struct WeighK {
     CacheArgs c;
     WeighArgs a;
-    int few_groups, many_groups;  // workgroups of a sequence, of either kind
-    int most_parts;               // that the work of a tile of the second kind may be cut into
-    float* part;                  // [N, many_groups][keys of a tile]
+    int groups;      // workgroups of a sequence
+    int most_parts;  // many queries: that the work of a tile may be cut into
+    float* part;     // [N, groups][keys of a tile]
 };
 
 // Sequence n's queries and its slot's tokens; false: nothing to do.
@@ -49,10 +50,6 @@ __device__ __forceinline__ bool weighed(const WeighK& k, int n, Weighed& w) {
     w.ctx = uniform(len < 0 ? 0 : static_cast<int>(len > most ? most : len));
     w.p_first = w.ctx - w.count;
     return w.ctx > 0;
-}
-// A sequence that the first kind takes, where it is launched.
-__device__ __forceinline__ bool few(const WeighK& k, const Weighed& w, int G) {
-    return k.few_groups > 0 && static_cast<int64_t>(w.count) * G <= kRows;
 }
 
 // The tiles of `keys` keys that some query attends, in order (the n-th begins at
@@ -91,7 +88,10 @@ template <typename T, int DK>
 struct FewSizes {
     static constexpr int kKeys = 32;  // of a tile
     static constexpr int kTile = kKeys * DK * static_cast<int>(sizeof(T));
-    static constexpr int kLds = kWaves * (kTile + kKeys * 4);  // a wave's keys, its sums
+    static constexpr int kRow = DK * static_cast<int>(sizeof(T));
+    static constexpr int kQueries = 16384 / kRow > kRows ? 16384 / kRow : kRows;  // rows of queries that LDS holds
+    static constexpr int kSums = kWaves * kTile, kQ = kSums + kWaves * kKeys * 4, kLse = kQ + kQueries * kRow;
+    static constexpr int kLds = kLse + kQueries * 4;
 };
 
 // Few queries: bound by reading the keys.  Scores transposed (S^T = K Q^T, 32
@@ -100,9 +100,12 @@ struct FewSizes {
 // all heads of one after another (or shares a tile's heads with the others of
 // its workgroup, where there are few tiles).  Keys are read by whole rows, the
 // next head's in flight while one is worked on, and laid out in LDS for the
-// product.
+// product.  So are the queries, of as many heads as fit, once for all tiles (read
+// from the caches for every tile and head they took more of the L1 than the
+// keys: a decode step of 256 sequences 259 us).
 template <typename T, int DK>
-__device__ __forceinline__ void weigh_few(const WeighK& k, unsigned block, char* smem) {
+__global__ __launch_bounds__(kThreads, (DK * sizeof(T) <= 256 ? 3 : 1)) void cache_weigh_few_kernel(WeighK k) {
+    extern __shared__ __align__(16) char smem[];
     using Sz = FewSizes<T, DK>;
     constexpr int kKeys = Sz::kKeys;
     constexpr int kPieces = DK / (2 * Elem<T>::kPer16);
@@ -113,152 +116,160 @@ __device__ __forceinline__ void weigh_few(const WeighK& k, unsigned block, char*
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int col = lane & 31, half = lane >> 5;
     char* sK = smem + wave * Sz::kTile;
-    float(*sums)[kKeys] = reinterpret_cast<float(*)[kKeys]>(smem + kWaves * Sz::kTile);
-    const int n = block / k.few_groups, group = block % k.few_groups;
+    float(*sums)[kKeys] = reinterpret_cast<float(*)[kKeys]>(smem + Sz::kSums);
+    char* sQ = smem + Sz::kQ;
+    float* sLse = reinterpret_cast<float*>(smem + Sz::kLse);
+    const int n = blockIdx.x / k.groups, group = blockIdx.x % k.groups;
     Weighed w;
     if (!weighed(k, n, w)) return;
     const int G = a.H / c.Hkv;
-    if (!few(k, w, G)) return;
     const Tiles tiles(a, w, kKeys);
-    // this lane's row: a query and a head of the group
-    const int rows = w.count * G, r = min(col, rows - 1);
-    const int64_t t = w.first + r / G, src = a.rows != nullptr ? a.rows[t] : t;
-    const int p_here = max(w.p_first + r / G, -1);
-    const bool on = col < rows && p_here >= 0 && src >= 0 && src < a.src_rows;
-    const int64_t q_at = (on ? src : 0) * a.H + r % G;  // of key head 0
-    const char* q_row = static_cast<const char*>(a.q) + q_at * kRow + half * 16;
-    const float* lse_at = a.lse + q_at;
     const float sc = a.scale * kLog2e;
     // Where there are few tiles, waves share one and take equal runs of its heads.
     const int64_t all = static_cast<int64_t>(tiles.count) * a.N;
     const int share = all >= 4096 || c.Hkv < 2 ? 1 : all >= 2048 || c.Hkv < 4 ? 2 : 4;
     const int member = wave % share, team = wave / share, teams = kWaves / share;
-    const int f0 = c.Hkv * member / share, f1 = c.Hkv * (member + 1) / share;
-
-    // A tile's halves of 16 rows, each in one page
-    typedef const __attribute__((address_space(4))) int32_t* scalar_ints;
-    const scalar_ints entries = (scalar_ints)(c.table + static_cast<int64_t>(w.slot) * c.max_pages);
-    struct Place {
-        int page[2], rows[2];  // rows that hold a token
-    };
-    auto look = [&](int tile) __attribute__((always_inline)) {
-        Place x;
-        const int first = tile < tiles.count ? tiles.first(tile) : w.ctx;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int p = first + 16 * h;
-            const int page = entries[min(p, w.ctx - 1) >> c.page_shift];
-            const bool there = page >= 0 && page < c.pages;
-            x.rows[h] = there ? min(16, max(0, w.ctx - p)) : 0;
-            x.page[h] = there ? page : 0;
-        }
-        return x;
-    };
-    u32x4 kr[2][kEach];
-    struct Queries {
-        u32x4 q[kPieces];
-        float lse;
-    };
-    // fp32 rows leave no registers for the next head's: read from the caches when they are used
-    constexpr bool kAhead = sizeof(T) == 2;
-    auto load_q = [&](Queries& x, int f) __attribute__((always_inline)) {
-        const char* q = q_row + static_cast<int64_t>(f) * G * kRow;
-        x.lse = lse_at[static_cast<int64_t>(f) * G];
-#pragma unroll
-        for (int p = 0; p < kPieces; ++p) x.q[p] = *reinterpret_cast<const u32x4*>(q + p * 32);
-    };
-    const int mask = (1 << c.page_shift) - 1;
-    auto load_k = [&](const Place& x, int tile, int f) __attribute__((always_inline)) {
-        const int first = tile < tiles.count ? tiles.first(tile) : 0;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int64_t row = ((static_cast<int64_t>(x.page[h]) * c.Hkv + f) << c.page_shift) + ((first + 16 * h) & mask);
-            const auto from = rows_of(c.k_cache, row, kRow, x.rows[h]);
-#pragma unroll
-            for (int i = 0; i < kEach; ++i)
-                if (kHalf >= 64 || lane < kHalf) kr[h][i] = buffer_load16(from, (lane + 64 * i) * 16);
-        }
-    };
-    TileRead<T, DK> rk;
-    rk.init_rows(col, half);
-    auto put = [&]() __attribute__((always_inline)) {
-        wave_lds_fence();
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < kEach; ++i) {
-                const int p = lane + 64 * i, row = 16 * h + p / kRowPieces;
-                if (kHalf >= 64 || lane < kHalf)
-                    *reinterpret_cast<u32x4*>(sK + row * kRow + (p % kRowPieces ^ turn<kRowPieces>(row)) * 16) = kr[h][i];
-            }
-        wave_lds_fence();
-    };
-    f32x16 acc{};
-    auto work = [&](const Queries& x, int first) __attribute__((always_inline)) {
-        f32x16 s{};
-#pragma unroll
-        for (int p = 0; p < kPieces; ++p) s = mma<T>(rk.rows(sK, p), x.q[p], s);
-        const bool good = on && fabsf(x.lse) < INFINITY;  // a row that attends nothing, or a broken one, weighs nothing
-        const float lse2 = x.lse * kLog2e;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] = good ? __builtin_amdgcn_exp2f(fmaf(s[i], sc, -lse2)) : 0.f;
-        if (first + kKeys - 1 > w.p_first || (a.window > 0 && first < w.ctx - a.window && first + kKeys > tiles.sinks)) {
-            const int most = opaque(p_here - first - 4 * half);
-            const int least = opaque(a.window > 0 ? p_here - a.window + 1 - first - 4 * half : INT32_MIN / 2);
-            const int sink = opaque(tiles.sinks - first - 4 * half);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int key = 8 * (i / 4) + i % 4;
-                if (key > most || outside(key, least, sink)) s[i] = 0.f;
-            }
-        }
-        acc += s;
-    };
-    auto finish = [&](int first, const Place& x) __attribute__((always_inline)) {
-        // over the lanes of a half; key 8 (i / 4) + 4 half + i % 4
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float v = row_ror_add<1>(acc[i]);
-            v = row_ror_add<2>(v);
-            v = row_ror_add<4>(v);
-            v = xor16_add(row_ror_add<8>(v));
-            if (col == 0) sums[wave][8 * (i / 4) + 4 * half + i % 4] = v;
-        }
-        acc = f32x16{};
-        if (share > 1) __syncthreads();
-        else wave_lds_fence();
-        if (member == 0 && half == 0 && (col & 15) < (col < 16 ? x.rows[0] : x.rows[1])) {
-            float v = 0.f;
-            for (int m = 0; m < share; ++m) v += sums[wave + m][col];
-            *weight_of(k, w, first + col) += gathered(v);
-        }
-        if (share > 1) __syncthreads();
-        else wave_lds_fence();
-    };
     // every wave of a workgroup takes as many turns (they meet where they share)
-    const int stride = k.few_groups * teams;
+    const int stride = k.groups * teams;
     const int turns = (tiles.count - group * teams + stride - 1) / stride;
     if (turns <= 0) return;
-    int tile = group * teams + team;
-    Place here = look(tile), next = look(tile + stride);
-    Queries x, y;
-    if constexpr (kAhead) load_q(x, f0);
-    load_k(here, tile, f0);
-    for (int turn = 0; turn < turns; ++turn) {
-        const int first = tile < tiles.count ? tiles.first(tile) : 0;
-        for (int f = f0; f < f1; ++f) {
-            put();
-            if constexpr (kAhead) load_q(y, f + 1 < f1 ? f + 1 : f0);
-            else load_q(x, f);
-            if (f + 1 < f1) load_k(here, tile, f + 1);
-            else load_k(next, tile + stride, f0);
-            work(x, first);
-            if constexpr (kAhead) x = y;
+
+    // 32 rows at a time: all of them in the calls that this kernel is for
+    const int64_t rows = static_cast<int64_t>(w.count) * G;
+    for (int64_t r0 = 0; r0 < rows; r0 += kRows) {
+        // this lane's row: a query and a head of the group
+        const int64_t r = min(r0 + col, rows - 1);
+        const int64_t t = w.first + r / G, src = a.rows != nullptr ? a.rows[t] : t;
+        const int p_here = max(w.p_first + static_cast<int>(r / G), -1);
+        const bool on = r0 + col < rows && p_here >= 0 && src >= 0 && src < a.src_rows;
+
+        // A tile's halves of 16 rows, each in one page
+        typedef const __attribute__((address_space(4))) int32_t* scalar_ints;
+        const scalar_ints entries = (scalar_ints)(c.table + static_cast<int64_t>(w.slot) * c.max_pages);
+        struct Place {
+            int page[2], rows[2];  // rows that hold a token
+        };
+        auto look = [&](int tile) __attribute__((always_inline)) {
+            Place x;
+            const int first = tile < tiles.count ? tiles.first(tile) : w.ctx;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int p = first + 16 * h;
+                const int page = entries[min(p, w.ctx - 1) >> c.page_shift];
+                const bool there = page >= 0 && page < c.pages;
+                x.rows[h] = there ? min(16, max(0, w.ctx - p)) : 0;
+                x.page[h] = there ? page : 0;
+            }
+            return x;
+        };
+        u32x4 kr[2][kEach];
+        const int here_rows = static_cast<int>(min<int64_t>(kRows, rows - r0)), my_row = min(col, here_rows - 1);
+        TileRead<T, DK> rq;
+        rq.init_rows(my_row, half);
+        const int mask = (1 << c.page_shift) - 1;
+        auto load_k = [&](const Place& x, int tile, int f) __attribute__((always_inline)) {
+            const int first = tile < tiles.count ? tiles.first(tile) : 0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t row = ((static_cast<int64_t>(x.page[h]) * c.Hkv + min(f, c.Hkv - 1)) << c.page_shift) + ((first + 16 * h) & mask);
+                const auto from = rows_of(c.k_cache, row, kRow, x.rows[h]);
+#pragma unroll
+                for (int i = 0; i < kEach; ++i)
+                    if (kHalf >= 64 || lane < kHalf) kr[h][i] = buffer_load16(from, (lane + 64 * i) * 16);
+            }
+        };
+        TileRead<T, DK> rk;
+        rk.init_rows(col, half);
+        auto put = [&]() __attribute__((always_inline)) {
+            wave_lds_fence();
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < kEach; ++i) {
+                    const int p = lane + 64 * i, row = 16 * h + p / kRowPieces;
+                    if (kHalf >= 64 || lane < kHalf)
+                        *reinterpret_cast<u32x4*>(sK + row * kRow + (p % kRowPieces ^ turn<kRowPieces>(row)) * 16) = kr[h][i];
+                }
+            wave_lds_fence();
+        };
+        f32x16 acc{};
+        auto work = [&](int f, int first) __attribute__((always_inline)) {  // f: the head's place among those in LDS
+            f32x16 s{};
+            const char* at = sQ + f * here_rows * kRow;
+            const float lse = sLse[f * here_rows + my_row];
+#pragma unroll
+            for (int p = 0; p < kPieces; ++p) s = mma<T>(rk.rows(sK, p), rq.rows(at, p), s);
+            const bool good = on && fabsf(lse) < INFINITY;  // a row that attends nothing, or a broken one, weighs nothing
+            const float lse2 = lse * kLog2e;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[i] = good ? __builtin_amdgcn_exp2f(fmaf(s[i], sc, -lse2)) : 0.f;
+            if (first + kKeys - 1 > w.p_first || (a.window > 0 && first < w.ctx - a.window && first + kKeys > tiles.sinks)) {
+                const int most = opaque(p_here - first - 4 * half);
+                const int least = opaque(a.window > 0 ? p_here - a.window + 1 - first - 4 * half : INT32_MIN / 2);
+                const int sink = opaque(tiles.sinks - first - 4 * half);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int key = 8 * (i / 4) + i % 4;
+                    if (key > most || outside(key, least, sink)) s[i] = 0.f;
+                }
+            }
+            acc += s;
+        };
+        // the place that this lane writes when a tile is done, and what stands there
+        auto mine = [&](const Place& x) { return member == 0 && half == 0 && (col & 15) < (col < 16 ? x.rows[0] : x.rows[1]); };
+        auto finish = [&](int first, const Place& x, float had) __attribute__((always_inline)) {
+            // over the lanes of a half; key 8 (i / 4) + 4 half + i % 4
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float v = row_ror_add<1>(acc[i]);
+                v = row_ror_add<2>(v);
+                v = row_ror_add<4>(v);
+                v = xor16_add(row_ror_add<8>(v));
+                if (col == 0) sums[wave][8 * (i / 4) + 4 * half + i % 4] = v;
+            }
+            acc = f32x16{};
+            if (share > 1) __syncthreads();
+            else wave_lds_fence();
+            if (mine(x)) {
+                float v = 0.f;
+                for (int m = 0; m < share; ++m) v += sums[wave + m][col];
+                *weight_of(k, w, first + col) = had + gathered(v);
+            }
+            if (share > 1) __syncthreads();
+            else wave_lds_fence();
+        };
+        const int at_once = Sz::kQueries / here_rows;  // heads whose queries LDS holds
+        for (int g0 = 0; g0 < c.Hkv; g0 += at_once) {
+            const int heads = min(at_once, c.Hkv - g0);
+            __syncthreads();  // (the queries before these are done with)
+            for (int x = threadIdx.x; x < here_rows * heads * kRowPieces; x += kThreads) {
+                const int piece = x % kRowPieces, to = x / kRowPieces, row = to % here_rows, f = g0 + to / here_rows;
+                const int64_t ri = r0 + row, ti = w.first + ri / G, si = a.rows != nullptr ? a.rows[ti] : ti;
+                const int64_t from = (si >= 0 && si < a.src_rows ? si : 0) * a.H + f * G + ri % G;
+                *reinterpret_cast<u32x4*>(sQ + to * kRow + (piece ^ turn<kRowPieces>(row)) * 16) =
+                    *reinterpret_cast<const u32x4*>(static_cast<const char*>(a.q) + from * kRow + piece * 16);
+                if (piece == 0) sLse[to] = a.lse[from];
+            }
+            __syncthreads();
+            const int f0 = g0 + heads * member / share, f1 = g0 + heads * (member + 1) / share;
+            int tile = group * teams + team;
+            Place here = look(tile), next = look(tile + stride);
+            load_k(here, tile, f0);
+            for (int turn = 0; turn < turns; ++turn) {
+                const int first = tile < tiles.count ? tiles.first(tile) : 0;
+                const float had = mine(here) ? *weight_of(k, w, first + col) : 0.f;
+                for (int f = f0; f < f1; ++f) {
+                    put();
+                    if (f + 1 < f1) load_k(here, tile, f + 1);
+                    else load_k(next, tile + stride, f0);
+                    work(f - g0, first);
+                }
+                finish(first, here, had);
+                tile += stride;
+                here = next;
+                if (turn + 2 < turns) next = look(tile + stride);
+            }
         }
-        finish(first, here);
-        tile += stride;
-        here = next;
-        if (turn + 2 < turns) next = look(tile + stride);
     }
 }
 
@@ -267,7 +278,7 @@ __device__ __forceinline__ void weigh_few(const WeighK& k, unsigned block, char*
 struct Shares {
     int parts;
     __device__ __forceinline__ Shares(const WeighK& k, int tiles)
-        : parts(tiles >= k.many_groups ? 1 : min(k.many_groups / max(tiles, 1), k.most_parts)) {}
+        : parts(tiles >= k.groups ? 1 : min(k.groups / max(tiles, 1), k.most_parts)) {}
 };
 
 template <typename T, int DK>
@@ -284,7 +295,8 @@ struct ManySizes {
 // Q K^T, so that a lane holds one key's scores and one sum.  The tile's work is
 // the sequence of its steps of 32 queries, head by head.
 template <typename T, int DK>
-__device__ __forceinline__ void weigh_many(const WeighK& k, unsigned block, char* smem) {
+__global__ __launch_bounds__(kThreads, (DK * sizeof(T) <= 256 ? 2 : 1)) void cache_weigh_many_kernel(WeighK k) {
+    __shared__ __align__(16) char smem[2 * ManySizes<T, DK>::kBuf];
     using Sz = ManySizes<T, DK>;
     constexpr int kSub = Sz::kSub, kKeys = Sz::kKeys;
     constexpr int kPieces = DK / (2 * Elem<T>::kPer16);
@@ -294,14 +306,13 @@ __device__ __forceinline__ void weigh_many(const WeighK& k, unsigned block, char
     const WeighArgs& a = k.a;
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int col = lane & 31, half = lane >> 5;
-    const int n = block / k.many_groups, group = block % k.many_groups;
+    const int n = blockIdx.x / k.groups, group = blockIdx.x % k.groups;
     Weighed w;
     if (!weighed(k, n, w)) return;
     const int G = a.H / c.Hkv;
-    if (few(k, w, G)) return;
     const Tiles tiles(a, w, kKeys);
     const int parts = Shares(k, tiles.count).parts, part = group % parts;
-    for (int tile = group / parts; tile < tiles.count; tile += k.many_groups / parts) {
+    for (int tile = group / parts; tile < tiles.count; tile += k.groups / parts) {
         const int k_first = tiles.first(tile), k0 = k_first + wave * 32 * kSub;
         // the queries that attend some key of the tile
         const int i_low = max(0, k_first - w.p_first);
@@ -443,7 +454,7 @@ __device__ __forceinline__ void weigh_many(const WeighK& k, unsigned block, char
             const float x = gathered(xor32_add(acc[u]));
             if (half != 0) continue;
             if (parts > 1)
-                k.part[(static_cast<int64_t>(n) * k.many_groups + group) * kKeys + wave * 32 * kSub + 32 * u + col] = x;
+                k.part[(static_cast<int64_t>(n) * k.groups + group) * kKeys + wave * 32 * kSub + 32 * u + col] = x;
             else if (there[u])
                 *weight_of(k, w, k0 + 32 * u + col) += x;
         }
@@ -451,20 +462,12 @@ __device__ __forceinline__ void weigh_many(const WeighK& k, unsigned block, char
     }
 }
 
-template <typename T, int DK>
-__global__ __launch_bounds__(kThreads, (DK * sizeof(T) <= 256 ? 2 : 1)) void cache_weigh_kernel(WeighK k) {
-    extern __shared__ __align__(16) char smem[];
-    const unsigned many = static_cast<unsigned>(k.a.N) * k.many_groups;
-    if (blockIdx.x < many) weigh_many<T, DK>(k, blockIdx.x, smem);
-    else weigh_few<T, DK>(k, blockIdx.x - many, smem);
-}
-
 // Adds the parts in their order, a key per thread.
 template <int kKeys>
 __global__ __launch_bounds__(kKeys) void cache_weigh_sum_kernel(WeighK k) {
-    const int n = blockIdx.x / k.many_groups, tile = blockIdx.x % k.many_groups;
+    const int n = blockIdx.x / k.groups, tile = blockIdx.x % k.groups;
     Weighed w;
-    if (!weighed(k, n, w) || few(k, w, k.a.H / k.c.Hkv)) return;
+    if (!weighed(k, n, w)) return;
     const Tiles tiles(k.a, w, kKeys);
     const int parts = Shares(k, tiles.count).parts;
     if (parts == 1 || tile >= tiles.count) return;
@@ -472,59 +475,59 @@ __global__ __launch_bounds__(kKeys) void cache_weigh_sum_kernel(WeighK k) {
     bool there;
     row_of(k, w, pos, there);
     if (!there) return;
-    const float* from = k.part + (static_cast<int64_t>(n) * k.many_groups + tile * parts) * kKeys + threadIdx.x;
+    const float* from = k.part + (static_cast<int64_t>(n) * k.groups + tile * parts) * kKeys + threadIdx.x;
     float sum = 0.f;
     for (int p = 0; p < parts; ++p) sum += from[p * kKeys];
     *weight_of(k, w, pos) += sum;
 }
 
 // Workgroups of a call, where it has that much work.
-constexpr int kFewWant = 2048, kManyWant = 1024, kMostParts = 64;
+constexpr int kFewWant = 4096, kManyWant = 1024, kMostParts = 64;
 
 int per_sequence(int64_t want, int64_t N) { return static_cast<int>((want + N - 1) / N); }
 
-// Sequences of few queries, as far as the host can tell: a decode step.  What
-// may be others among them is not cut into parts then.
-bool mostly_few(int64_t tokens, int64_t N, int G) { return tokens * G <= kRows * N; }
+// Few queries: their rows of one key head are 32 on the average at most.
+bool few_queries(int64_t tokens, int64_t N, int G) { return tokens * G <= kRows * N; }
 
 template <typename T, int DK>
 hipError_t launch_weigh(const CacheArgs& c, const WeighArgs& a, hipStream_t s) {
-    constexpr int kKeys = ManySizes<T, DK>::kKeys;
     const int64_t max_ctx = static_cast<int64_t>(c.max_pages) << c.page_shift;
-    const int G = a.H / c.Hkv;
     WeighK k{};
     k.c = c;
     k.a = a;
     if (a.window >= max_ctx) k.a.window = 0;  // it holds every token
-    const bool any_many = a.tokens * G > kRows, cut = !mostly_few(a.tokens, a.N, G);
-    if (any_many) {
-        k.many_groups = per_sequence(kManyWant, a.N);
-        k.most_parts = !cut ? 1 : a.H < kMostParts ? a.H : kMostParts;
-        k.part = static_cast<float*>(a.ws);
+    if (few_queries(a.tokens, a.N, a.H / c.Hkv)) {
+        k.groups = per_sequence(kFewWant, a.N);
+        constexpr int lds = FewSizes<T, DK>::kLds;
+        auto fn = cache_weigh_few_kernel<T, DK>;
+        if (lds > 64 * 1024) {
+            const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+            if (e != hipSuccess) return e;
+        }
+        LaunchTimer timer("cache_weigh_few", s);
+        fn<<<dim3(static_cast<unsigned>(static_cast<int64_t>(a.N) * k.groups)), dim3(kThreads), lds, s>>>(k);
+        return hipGetLastError();
     }
-    if (!any_many || a.N > 1) k.few_groups = per_sequence(kFewWant, a.N);
-    constexpr int few_lds = FewSizes<T, DK>::kLds, many_lds = 2 * ManySizes<T, DK>::kBuf;
-    const int lds = k.few_groups > 0 && few_lds > many_lds ? few_lds : many_lds;
-    if (few_lds > 64 * 1024) {
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(cache_weigh_kernel<T, DK>), hipFuncAttributeMaxDynamicSharedMemorySize, few_lds);
-        if (e != hipSuccess) return e;
-    }
+    constexpr int kKeys = ManySizes<T, DK>::kKeys;
+    k.groups = per_sequence(kManyWant, a.N);
+    k.most_parts = a.H < kMostParts ? a.H : kMostParts;
+    k.part = static_cast<float*>(a.ws);
+    const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(a.N) * k.groups));
     {
-        LaunchTimer timer("cache_weigh", s);
-        const int64_t groups = static_cast<int64_t>(a.N) * (k.many_groups + k.few_groups);
-        cache_weigh_kernel<T, DK><<<dim3(static_cast<unsigned>(groups)), dim3(kThreads), lds, s>>>(k);
+        LaunchTimer timer("cache_weigh_many", s);
+        cache_weigh_many_kernel<T, DK><<<grid, dim3(kThreads), 0, s>>>(k);
     }
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !cut || k.many_groups <= 1) return e;
+    if (e != hipSuccess || k.groups == 1) return e;
     LaunchTimer timer("cache_weigh_sum", s);
-    cache_weigh_sum_kernel<kKeys><<<dim3(static_cast<unsigned>(a.N * k.many_groups)), dim3(kKeys), 0, s>>>(k);
+    cache_weigh_sum_kernel<kKeys><<<grid, dim3(kKeys), 0, s>>>(k);
     return hipGetLastError();
 }
 
 }  // namespace
 
 size_t cache_weigh_workspace_bytes(int64_t tokens, int N, int H, int Hkv) {
-    if (mostly_few(tokens, N, H / Hkv)) return 0;
+    if (few_queries(tokens, N, H / Hkv)) return 0;
     return static_cast<size_t>(N) * per_sequence(kManyWant, N) * 256 * 4;  // a tile has 256 keys at most
 }
 
