@@ -291,17 +291,20 @@ struct ManySizes {
 
 // Many queries: bound by the products and exponentials.  One workgroup per
 // (sequence, tile of keys, part): a wave's keys stay in its registers, the
-// queries of a head pass through LDS 32 at a time, once for four waves.  S =
-// Q K^T, so that a lane holds one key's scores and one sum.  The tile's work is
-// the sequence of its steps of 32 queries, head by head.
-template <typename T, int DK>
+// queries of a head pass through LDS, once for four waves, two steps in flight
+// (a step is shorter than a load takes).  S = Q K^T, so that a lane holds one
+// key's scores and one sum.  The tile's work is the sequence of its steps, head
+// by head.
+// kPicked: the queries' rows are named by a list.
+template <typename T, int DK, bool kPicked>
 __global__ __launch_bounds__(kThreads, (DK * sizeof(T) <= 256 ? 2 : 1)) void cache_weigh_many_kernel(WeighK k) {
     __shared__ __align__(16) char smem[2 * ManySizes<T, DK>::kBuf];
     using Sz = ManySizes<T, DK>;
     constexpr int kSub = Sz::kSub, kKeys = Sz::kKeys;
     constexpr int kPieces = DK / (2 * Elem<T>::kPer16);
     constexpr int kRow = DK * static_cast<int>(sizeof(T)), kRowPieces = kRow / 16;
-    constexpr int kEach = (kRows * kRowPieces + kThreads - 1) / kThreads;
+    constexpr int kPiecesOfStep = kRows * kRowPieces, kEach = (kPiecesOfStep + kThreads - 1) / kThreads;
+    constexpr bool kFull = kPiecesOfStep % kThreads == 0;
     const CacheArgs& c = k.c;
     const WeighArgs& a = k.a;
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
@@ -312,6 +315,16 @@ __global__ __launch_bounds__(kThreads, (DK * sizeof(T) <= 256 ? 2 : 1)) void cac
     const int G = a.H / c.Hkv;
     const Tiles tiles(a, w, kKeys);
     const int parts = Shares(k, tiles.count).parts, part = group % parts;
+    // this thread's pieces of a step: where they come from and go to
+    const int q_row = a.H * kRow;
+    int row_in[kEach], piece_in[kEach], put_at[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int p = tid + i * kThreads;
+        row_in[i] = p / kRowPieces;
+        piece_in[i] = p % kRowPieces;
+        put_at[i] = row_in[i] * kRow + (piece_in[i] ^ turn<kRowPieces>(row_in[i])) * 16;
+    }
     for (int tile = group / parts; tile < tiles.count; tile += k.groups / parts) {
         const int k_first = tiles.first(tile), k0 = k_first + wave * 32 * kSub;
         // the queries that attend some key of the tile
@@ -337,55 +350,69 @@ __global__ __launch_bounds__(kThreads, (DK * sizeof(T) <= 256 ? 2 : 1)) void cac
         rq.init_rows(col, half);
 
         // the step to fetch, and the one worked on
-        int f_head = s_now < s_end ? static_cast<int>(s_now / steps) : 0, f_i = i_low + (s_now < s_end ? static_cast<int>(s_now % steps) * kRows : 0);
+        int f_head = uniform(s_now < s_end ? static_cast<int>(s_now / steps) : 0);
+        int f_i = uniform(i_low + (s_now < s_end ? static_cast<int>(s_now % steps) * kRows : 0));
         int head = f_head, i0 = f_i, kvh = -1;
-        u32x4 qr[kEach];
-        float lse_r = 0.f;
-        int src[kEach], lse_src = 0;  // rows of the next step to fetch
-        auto row_at = [&](int i) {  // query i's row in q, -1: none
-            if (i >= i_end) return -1;
-            const int64_t t = w.first + i;
-            const int64_t r = a.rows != nullptr ? a.rows[t] : t;
-            return r >= 0 && r < a.src_rows && w.p_first + i >= 0 ? static_cast<int>(r) : -1;
+        struct Step {
+            u32x4 q[kEach];
+            float of[kEach], lse;  // the lse of the pieces' rows, and of row `col`
+            bool there;            // row `col` is one
         };
-        auto look = [&]() {
+        // (behind the last step it reads nothing, but in no branch: a wait for the
+        // step before would be one for this one too)
+        int64_t s_fetch = s_now;
+        auto fetch = [&](Step& x) __attribute__((always_inline)) {
+            const int here = s_fetch < s_end ? min(kRows, i_end - f_i) : 0;
+            ++s_fetch;
+            if constexpr (!kPicked) {  // what is behind the last row reads as 0
+                const auto q = rows_of(static_cast<const T*>(a.q) + f_head * DK, w.first + f_i, q_row, here);
+                const auto l = rows_of(a.lse + f_head, w.first + f_i, a.H * 4, here);
 #pragma unroll
-            for (int i = 0; i < kEach; ++i) src[i] = row_at(f_i + (tid + i * kThreads) / kRowPieces);
-            if (tid < kRows) lse_src = row_at(f_i + tid);
-        };
-        auto fetch = [&]() __attribute__((always_inline)) {
+                for (int i = 0; i < kEach; ++i)
+                    if (kFull || tid + i * kThreads < kPiecesOfStep) {
+                        x.q[i] = buffer_load16(q, row_in[i] * q_row + piece_in[i] * 16);
+                        x.of[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(l, row_in[i] * a.H * 4, 0, 0));
+                    }
+                x.lse = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(l, col * a.H * 4, 0, 0));
+                x.there = col < here;
+            } else {
+                auto row_at = [&](int i) {  // query i's row in q and lse; the first one of the tensor for none
+                    const int64_t r = i < here ? a.rows[w.first + f_i + i] : -1;
+                    return (r >= 0 && r < a.src_rows ? r : 0) * a.H + min(f_head, a.H - 1);
+                };
 #pragma unroll
-            for (int i = 0; i < kEach; ++i) {
-                const int p = tid + i * kThreads;
-                if (kRows * kRowPieces % kThreads == 0 || p < kRows * kRowPieces) {
-                    qr[i] = u32x4{};
-                    if (src[i] >= 0)
-                        qr[i] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(a.q) + (static_cast<int64_t>(src[i]) * a.H + f_head) * kRow +
-                                                                p % kRowPieces * 16);
-                }
+                for (int i = 0; i < kEach; ++i)
+                    if (kFull || tid + i * kThreads < kPiecesOfStep) {
+                        const int64_t r = row_at(row_in[i]);
+                        x.q[i] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(a.q) + r * kRow + piece_in[i] * 16);
+                        x.of[i] = a.lse[r];
+                    }
+                const int64_t r = col < here ? a.rows[w.first + f_i + col] : -1;
+                x.there = r >= 0 && r < a.src_rows;
+                x.lse = a.lse[(x.there ? r : 0) * a.H + min(f_head, a.H - 1)];
             }
-            if (tid < kRows) lse_r = lse_src >= 0 ? a.lse[static_cast<int64_t>(lse_src) * a.H + f_head] : INFINITY;
             f_i += kRows;
             if (f_i >= i_low + steps * kRows) {
                 f_i = i_low;
                 ++f_head;
             }
-            look();
         };
-        auto put = [&](char* buf) __attribute__((always_inline)) {
-            // a row that is not there, attends nothing or is broken: e^(0 - infinity)
-            const bool none = tid < kRows && !(fabsf(lse_r) < INFINITY);
+        // A row that is not there, attends nothing or is broken: e^(0 - infinity).
+        auto put = [&](char* buf, const Step& x) __attribute__((always_inline)) {
 #pragma unroll
-            for (int i = 0; i < kEach; ++i) {
-                const int p = tid + i * kThreads, row = p / kRowPieces;
-                if (kRows * kRowPieces % kThreads == 0 || p < kRows * kRowPieces)
-                    *reinterpret_cast<u32x4*>(buf + row * kRow + (p % kRowPieces ^ turn<kRowPieces>(row)) * 16) = qr[i];
-            }
-            if (tid < kRows) reinterpret_cast<float*>(buf + Sz::kTile)[tid] = none ? INFINITY : lse_r * kLog2e;
+            for (int i = 0; i < kEach; ++i)
+                if (kFull || tid + i * kThreads < kPiecesOfStep)
+                    *reinterpret_cast<u32x4*>(buf + put_at[i]) = fabsf(x.of[i]) < INFINITY ? x.q[i] : u32x4{};
+            if (tid < kRows) reinterpret_cast<float*>(buf + Sz::kTile)[col] = x.there && fabsf(x.lse) < INFINITY ? x.lse * kLog2e : INFINITY;
         };
         auto work = [&](const char* sQ) __attribute__((always_inline)) {
             const f32x4* lse2 = reinterpret_cast<const f32x4*>(sQ + Sz::kTile);
-            const int f = head / G;
+            const int f = head / G, p0 = w.p_first + i0;  // the first row's place
+            i0 += kRows;
+            if (i0 >= i_low + steps * kRows) {
+                i0 = i_low;
+                ++head;
+            }
             if (f != kvh) {
                 kvh = uniform(f);
 #pragma unroll
@@ -394,17 +421,22 @@ __global__ __launch_bounds__(kThreads, (DK * sizeof(T) <= 256 ? 2 : 1)) void cac
 #pragma unroll
                     for (int p = 0; p < kPieces; ++p) key[u][p] = *reinterpret_cast<const u32x4*>(from + p * 32);
                 }
+                // waited for here: at their use, every step would wait for the queries in flight
+#pragma unroll
+                for (int u = 0; u < kSub; ++u) arrive(key[u]);
             }
-            const int p0 = w.p_first + i0;  // the first row's place
+            if (p0 + kRows <= k0) return;  // queries before this wave's keys
             f32x16 s[kSub];
 #pragma unroll
             for (int u = 0; u < kSub; ++u) s[u] = f32x16{};
+            __builtin_amdgcn_s_setprio(1);
 #pragma unroll
             for (int p = 0; p < kPieces; ++p) {
                 const u32x4 q = rq.rows(sQ, p);
 #pragma unroll
                 for (int u = 0; u < kSub; ++u) s[u] = mma<T>(q, key[u][p], s[u]);
             }
+            __builtin_amdgcn_s_setprio(0);
 #pragma unroll
             for (int u = 0; u < kSub; ++u) {
                 const int key0 = k0 + 32 * u;
@@ -427,27 +459,21 @@ __global__ __launch_bounds__(kThreads, (DK * sizeof(T) <= 256 ? 2 : 1)) void cac
                 for (int r = 0; r < 16; ++r) sum += s[u][r];
                 acc[u] += sum;
             }
-            i0 += kRows;
-            if (i0 >= i_low + steps * kRows) {
-                i0 = i_low;
-                ++head;
-            }
         };
-        if (s_now < s_end) {
-            look();
-            fetch();
-            put(smem);
-        }
+        Step x, y;
+        fetch(x);
+        fetch(y);
+        put(smem, x);
         for (; s_now < s_end; s_now += 2) {
             tile_barrier();
-            if (s_now + 1 < s_end) fetch();
+            fetch(x);
             work(smem);
             if (s_now + 1 >= s_end) break;
-            put(smem + Sz::kBuf);
+            put(smem + Sz::kBuf, y);
             tile_barrier();
-            if (s_now + 2 < s_end) fetch();
+            fetch(y);
             work(smem + Sz::kBuf);
-            if (s_now + 2 < s_end) put(smem);
+            put(smem, x);
         }
 #pragma unroll
         for (int u = 0; u < kSub; ++u) {
@@ -515,7 +541,8 @@ hipError_t launch_weigh(const CacheArgs& c, const WeighArgs& a, hipStream_t s) {
     const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(a.N) * k.groups));
     {
         LaunchTimer timer("cache_weigh_many", s);
-        cache_weigh_many_kernel<T, DK><<<grid, dim3(kThreads), 0, s>>>(k);
+        if (a.rows != nullptr) cache_weigh_many_kernel<T, DK, true><<<grid, dim3(kThreads), 0, s>>>(k);
+        else cache_weigh_many_kernel<T, DK, false><<<grid, dim3(kThreads), 0, s>>>(k);
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || k.groups == 1) return e;

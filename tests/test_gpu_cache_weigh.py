@@ -179,6 +179,33 @@ def test_what_is_skipped(K):
         assert torch.equal(_call(K, y), want)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("counts", [[3, 2], [90, 33]])
+def test_broken_rows_and_keys(K, counts, dtype):
+    """A query that is not finite has an lse that is not: it weighs nothing and
+    the rows beside it are as before.  A key that is not finite gathers nothing."""
+    x = _setup(41, [200, 64], counts, 4, 2, 64, 16, TYPES[dtype])
+    want, g = _call(K, x), x["pick_list"]
+    y = dict(x, q=x["q"].clone(), lse=x["lse"].clone())
+    y["lse"][g[1], 2] = math.nan
+    clean = _call(K, y)
+    for value in (math.nan, math.inf, -math.inf):
+        y["q"][g[1], 2, 5] = value
+        assert torch.equal(_call(K, y), clean), value
+    assert not torch.equal(clean, want)
+    # every row of the heads over a broken key attends it: none of them weighs anything
+    z = dict(x, kc=x["kc"].clone(), lse=x["lse"].clone())
+    page, n = int(x["table"][int(x["rows"][0]), 2]), counts[0]
+    z["kc"][page, 1, 3, 7] = math.nan
+    z["lse"][g[:n], 2:] = math.nan
+    got = _call(K, z)
+    y = dict(x, lse=z["lse"])
+    want, bound = _want(y, 0, 0)
+    slot, place = int(x["rows"][0]), 35
+    assert float((got[slot, place].double() - want[slot, place]).abs()) <= float(bound[slot, place])
+    R.check("weights", got, want, bound + 1e-30)
+
+
 def test_lengths_past_the_table(K):
     x = _setup(6, [64, 32], [2, 3], 2, 2, 64, 16, torch.float32, width=4)
     want = _call(K, x)
