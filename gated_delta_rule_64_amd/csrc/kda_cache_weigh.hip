@@ -426,27 +426,26 @@ __global__ __launch_bounds__(kThreads, (DK * sizeof(T) <= 256 ? 2 : 1)) void cac
                 for (int u = 0; u < kSub; ++u) arrive(key[u]);
             }
             if (p0 + kRows <= k0) return;  // queries before this wave's keys
+            // one half's products, then the other's, then all exponentials without a branch between:
+            // the first half's run beside the other half's products (8,000 tokens 331 to 315 us)
             f32x16 s[kSub];
 #pragma unroll
             for (int u = 0; u < kSub; ++u) s[u] = f32x16{};
-            __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-            for (int p = 0; p < kPieces; ++p) {
-                const u32x4 q = rq.rows(sQ, p);
+            for (int u = 0; u < kSub; ++u)
 #pragma unroll
-                for (int u = 0; u < kSub; ++u) s[u] = mma<T>(q, key[u][p], s[u]);
-            }
-            __builtin_amdgcn_s_setprio(0);
+                for (int p = 0; p < kPieces; ++p) s[u] = mma<T>(rq.rows(sQ, p), key[u][p], s[u]);
+            f32x4 l4[4];
+#pragma unroll
+            for (int r4 = 0; r4 < 4; ++r4) l4[r4] = lse2[2 * r4 + half];
+#pragma unroll
+            for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[u][r] = __builtin_amdgcn_exp2f(fmaf(s[u][r], sc, -l4[r / 4][r % 4]));
 #pragma unroll
             for (int u = 0; u < kSub; ++u) {
                 const int key0 = k0 + 32 * u;
                 // register r: the query at place p0 + 8 (r / 4) + 4 half + r % 4; key key0 + col
-#pragma unroll
-                for (int r4 = 0; r4 < 4; ++r4) {
-                    const f32x4 l = lse2[2 * r4 + half];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[u][4 * r4 + e] = __builtin_amdgcn_exp2f(fmaf(s[u][4 * r4 + e], sc, -l[e]));
-                }
                 if (p0 < key0 + 31 || (a.window > 0 && p0 + kRows > key0 + a.window && key0 + 32 > tiles.sinks)) {
                     const int least = opaque(key0 + col - p0 - 4 * half);
                     const int most = opaque(a.window > 0 && key0 + col >= tiles.sinks ? key0 + col + a.window - p0 - 4 * half : INT32_MAX);
