@@ -794,7 +794,7 @@ size_t backward_need(int64_t T, int32_t N, int32_t H, int32_t Hkv, int32_t dk, i
 }
 
 size_t tree_need(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t dv, int64_t max_context, const View& view) {
-    return kda::attn_tree_workspace_bytes(B, T, H, Hkv, dv, view.bounded ? kda::window_reach(max_context, view.window, view.sinks) : max_context);
+    return kda::attn_tree_workspace_bytes(B, T, H, Hkv, dv, max_context, view.window, view.sinks);
 }
 
 int attn_prefill_impl(const View& view, int64_t T_tot, int32_t H, int32_t Hkv, int32_t dk, int32_t dv, const int32_t* cu_seqlens,
@@ -1012,7 +1012,7 @@ size_t kda_attn_window_tree_workspace_bytes(int32_t B, int32_t T, int32_t H, int
 size_t kda_attn_window_tree_max_workspace_bytes(int32_t max_B, int32_t max_T, int32_t H, int32_t Hkv, int32_t dk, int32_t dv,
                                                 int32_t x_dtype, int64_t max_context, int32_t window, int32_t sinks) {
     if (!tree_sizes(max_B, max_T, H, Hkv, dk, dv, x_dtype, max_context) || max_context >= kMostWindowed || window < 1 || sinks < 0) return 0;
-    return kda::attn_tree_max_workspace_bytes(max_B, max_T, H, Hkv, dv, kda::window_reach(max_context, window, sinks));
+    return kda::attn_tree_max_workspace_bytes(max_B, max_T, H, Hkv, dv, max_context, window, sinks);
 }
 
 int kda_attn_window_tree(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t dk, int32_t dv, int32_t x_dtype, float scale,

@@ -607,7 +607,16 @@ struct TreePlan {
     int blocks, splits;
 };
 constexpr int kWantUnits = 1024, kWantUnitsOfOne = 512;  // workgroups below which a call is split
-TreePlan tree_plan(int B, int T, int H, int Hkv, int64_t max_ctx) {
+
+// The tokens of a cache that a windowed row can read, of a context of at most
+// max_ctx: what the parts of a call go by.
+int64_t window_reach(int64_t max_ctx, int window, int sinks) {
+    const int64_t reach = static_cast<int64_t>(window) + sinks + 64;  // a tile at the window's start and at the sinks' end
+    return window > 0 && reach < max_ctx ? reach : max_ctx;
+}
+
+// even: the sequences read equally much.
+TreePlan tree_plan(int B, int T, int H, int Hkv, int64_t max_ctx, bool even) {
     const int64_t rows = static_cast<int64_t>(T) * (H / Hkv);
     TreePlan p;
     p.blocks = static_cast<int>((rows + 31) / 32);
@@ -622,7 +631,11 @@ TreePlan tree_plan(int B, int T, int H, int Hkv, int64_t max_ctx) {
     // to 8,000 tokens 366 us in fp32 at 192 channels and 119 in bf16, with half
     // as many parts 433 and 124; one of 100,000 tokens 289 and 100, with half
     // as many 284 and 96.
-    const int64_t want = B == 1 ? kWantUnitsOfOne : kWantUnits;
+    // A window shorter than the contexts evens them out: one round (32 trees of
+    // 16 under a window of 2,000, 75 us in two rounds with their join, 61 in one
+    // without; fp32 270 against 243 us; a window of 7,000 of at most 8,000 tokens
+    // 134 against 130).
+    const int64_t want = B == 1 || even ? kWantUnitsOfOne : kWantUnits;
     int64_t s = (want + units - 1) / units;
     if (s > tiles / 8) s = tiles / 8;  // two tiles a wave at least
     p.splits = static_cast<int>(s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s);
@@ -634,7 +647,8 @@ size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 template <typename T, int DK, int DV, bool kWin>
 hipError_t launch_tree(const TreeArgs& a, hipStream_t s) {
     const int64_t max_ctx = static_cast<int64_t>(a.max_pages) << a.page_shift;
-    const TreePlan p = tree_plan(a.B, a.T, a.H, a.Hkv, kWin ? window_reach(max_ctx, a.window, a.sinks) : max_ctx);
+    const int64_t reach = window_reach(max_ctx, a.window, a.sinks);
+    const TreePlan p = tree_plan(a.B, a.T, a.H, a.Hkv, reach, reach < max_ctx);
     const size_t parts = static_cast<size_t>(p.splits) * a.B * a.T * a.H;
     float* part = static_cast<float*>(a.ws);
     float* stats = reinterpret_cast<float*>(static_cast<char*>(a.ws) + up256(parts * DV * 4));
@@ -666,22 +680,30 @@ hipError_t launch_tree(const TreeArgs& a, hipStream_t s) {
 
 }  // namespace
 
-size_t attn_tree_workspace_bytes(int B, int T, int H, int Hkv, int dv, int64_t max_ctx) {
-    if (B == 0 || T == 0) return 0;
-    const TreePlan p = tree_plan(B, T, H, Hkv, max_ctx);
+namespace {
+size_t parts_bytes(const TreePlan& p, int B, int T, int H, int dv) {
     if (p.splits == 1) return 0;
     const size_t parts = static_cast<size_t>(p.splits) * B * T * H;
     return up256(parts * dv * 4) + up256(parts * 8);
 }
+}  // namespace
+
+size_t attn_tree_workspace_bytes(int B, int T, int H, int Hkv, int dv, int64_t max_ctx, int window, int sinks) {
+    if (B == 0 || T == 0) return 0;
+    const int64_t reach = window_reach(max_ctx, window, sinks);
+    return parts_bytes(tree_plan(B, T, H, Hkv, reach, reach < max_ctx), B, T, H, dv);
+}
 
 // More sequences or tokens have fewer parts of more rows, so what a call needs
-// does not rise with its sizes: all that are split are tried.
-size_t attn_tree_max_workspace_bytes(int B, int T, int H, int Hkv, int dv, int64_t max_ctx) {
+// does not rise with its sizes: all that are split are tried.  Nor with its
+// contexts under a window: those no longer than it are cut into more parts.
+size_t attn_tree_max_workspace_bytes(int B, int T, int H, int Hkv, int dv, int64_t max_ctx, int window, int sinks) {
+    const int64_t reach = window_reach(max_ctx, window, sinks);
     size_t most = 0;
     for (int t = 1; t <= T; ++t) {
         const int64_t units = static_cast<int64_t>(Hkv) * ((static_cast<int64_t>(t) * (H / Hkv) + 31) / 32);  // of a sequence
         for (int b = 1; b <= B && b * units < kWantUnits; ++b) {
-            const size_t need = attn_tree_workspace_bytes(b, t, H, Hkv, dv, max_ctx);
+            const size_t need = parts_bytes(tree_plan(b, t, H, Hkv, reach, false), b, t, H, dv);
             most = need > most ? need : most;
         }
     }

@@ -223,16 +223,9 @@ hipError_t launch_attn_prefill(const AttnArgs& a, hipStream_t s);
 size_t attn_backward_workspace_bytes(int64_t T, int N, int H, int Hkv, int dk, int dv, DT x, bool gate, int window = 0, int sinks = 0);
 size_t attn_backward_max_workspace_bytes(int64_t T, int H, int Hkv, int dk, int dv, DT x, bool gate, int window = 0, int sinks = 0);
 hipError_t launch_attn_prefill_backward(const AttnBackwardArgs& a, hipStream_t s);
-size_t attn_tree_workspace_bytes(int B, int T, int H, int Hkv, int dv, int64_t max_ctx);
-size_t attn_tree_max_workspace_bytes(int B, int T, int H, int Hkv, int dv, int64_t max_ctx);
+size_t attn_tree_workspace_bytes(int B, int T, int H, int Hkv, int dv, int64_t max_ctx, int window = 0, int sinks = 0);
+size_t attn_tree_max_workspace_bytes(int B, int T, int H, int Hkv, int dv, int64_t max_ctx, int window = 0, int sinks = 0);
 hipError_t launch_attn_tree(const TreeArgs& a, hipStream_t s);
-
-// The tokens of a cache that a windowed row can read, of a context of at most
-// max_ctx: what the parts of a call go by.
-constexpr int64_t window_reach(int64_t max_ctx, int window, int sinks) {
-    const int64_t reach = static_cast<int64_t>(window) + sinks + 64;  // a tile at the window's start and at the sinks' end
-    return reach < max_ctx ? reach : max_ctx;
-}
 
 // Attention weights gathered per cached token: the queries of each sequence's
 // last tokens, their rows' lse.

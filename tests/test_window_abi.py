@@ -160,8 +160,10 @@ BF16, F32 = 1, 0
 @pytest.mark.parametrize("B,T,context", [(256, 1, 4096), (20, 9, 8192), (1, 1, 64)])
 def test_workspaces_of_trees(B, T, context, window, sinks, H, Hkv, dk, dv, x):
     most = kda.kda_attn_window_tree_max_workspace_bytes(B, T, H, Hkv, dk, dv, x, context, window, sinks)
+    # (a context that the window holds just so, with a tile at its start and one at the sinks' end, is cut into the most parts)
+    contexts = (0, context // 2, context - 1, context, min(context, window + sinks + 64))
     every = [kda.kda_attn_window_tree_workspace_bytes(b, t, H, Hkv, dk, dv, x, c, window, sinks)
-             for b in range(B + 1) for t in range(T + 1) for c in (0, context // 2, context - 1, context)]
+             for b in range(B + 1) for t in range(T + 1) for c in contexts]
     assert max(every) == most
     if window >= context:
         assert most == kda.kda_attn_tree_max_workspace_bytes(B, T, H, Hkv, dk, dv, x, context)
