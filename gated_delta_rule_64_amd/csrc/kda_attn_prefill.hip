@@ -186,22 +186,20 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void attn_fwd_k
                     acc[i] = mma<T>(rv.columns(sV + 32 * u * rv.kRow, i, p), b, acc[i]);
             }
     };
-    int j0 = walk.next(-kKeys);
-    fetch(j0);
+    const int begin = walk.next(-kKeys);
+    fetch(begin);
     arrive(qf);
     put(smem);
-    while (j0 < last) {
+    for (int j0 = begin; j0 < last; j0 = walk.next(walk.next(j0))) {
         tile_barrier();
-        const int j1 = walk.next(j0), j2 = walk.next(j1);
-        if (j1 < last) fetch(j1);
+        if (walk.next(j0) < last) fetch(walk.next(j0));
         work(smem, j0);
-        if (j1 >= last) break;
+        if (walk.next(j0) >= last) break;
         put(smem + Sz::kBuf);
         tile_barrier();
-        if (j2 < last) fetch(j2);
-        work(smem + Sz::kBuf, j1);
-        if (j2 < last) put(smem);
-        j0 = j2;
+        if (walk.next(walk.next(j0)) < last) fetch(walk.next(walk.next(j0)));
+        work(smem + Sz::kBuf, walk.next(j0));
+        if (walk.next(walk.next(j0)) < last) put(smem);
     }
 
     const int row = q0 + c;
