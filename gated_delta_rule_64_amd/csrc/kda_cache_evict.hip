@@ -22,7 +22,7 @@ struct EvictK {
     EvictArgs a;
     int32_t* list;  // [n, keep]: places of the tokens that stay
     int64_t* from;  // [n, keep]: their rows in head 0 of the pools
-    int32_t* plan;  // [n]: the first token that changes its place (-1: nothing to do)
+    int32_t* plan;  // [n][2]: the first token that changes its place (-1: nothing to do), how many there were
     int splits;     // workgroups that share a head's rows, each some of the channels
 };
 
@@ -64,14 +64,18 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t x, uint64_t* sums, uint6
     return before + inc - x;
 }
 
-// One workgroup per entry: checks it, finds what stays, moves its weights.  A
-// slot of up to kStep tokens is read once and its orders stay in registers; the
-// digits are counted in LDS.  Bound by the length of its chain of barriers.
+// One workgroup per entry: checks it, finds what stays.  The digits (of 11, 11
+// and 10 bits: many bins, so that weights of one size do not wait for each other)
+// are counted in LDS.  A slot of up to kStep tokens is read once and its orders
+// stay in registers: bound by the length of its chain of barriers.  A longer one
+// is read once per digit, the next step's weights in flight.
 constexpr int kPer = 8;  // neighbouring tokens of a thread
 constexpr int kStep = kPlan * kPer;
+constexpr int kDigits = 3, kBins = 2048;
+static_assert(kBins == 2 * kPlan, "two bins a thread");
 
 __global__ __launch_bounds__(kPlan) void cache_evict_plan_kernel(EvictK k) {
-    __shared__ int hist[4][256];
+    __shared__ int hist[kDigits][kBins], stay[kStep];
     __shared__ uint64_t sums[kPlan / 64];
     __shared__ int s_first, s_bad, s_digit, s_left;
     const CacheArgs& c = k.c;
@@ -86,43 +90,42 @@ __global__ __launch_bounds__(kPlan) void cache_evict_plan_kernel(EvictK k) {
     const int stored = real ? c.lens[slot] : 0;
     const int len = stored < 0 ? 0 : static_cast<int>(stored > most ? most : stored);
     const int32_t* table = c.table + static_cast<int64_t>(real ? slot : 0) * c.max_pages;
-    float* w = a.weights + ((static_cast<int64_t>(real ? slot : 0) * c.max_pages) << c.page_shift);
+    const float* w = a.weights + ((static_cast<int64_t>(real ? slot : 0) * c.max_pages) << c.page_shift);
     const int mask = (1 << c.page_shift) - 1;
 
     uint32_t order[kPer];
+    float next[kPer];
     const int steps = (len + kStep - 1) / kStep;
-    auto read = [&](int step) __attribute__((always_inline)) {
+    const bool whole = (reinterpret_cast<uintptr_t>(w) & 15) == 0;
+    auto fetch = [&](int step) __attribute__((always_inline)) {  // behind the last token 0, which nothing looks at
         const int p = step * kStep + tid * kPer;
-        if (p + kPer <= len) {  // a slot's weights begin at a multiple of 64 bytes from the first slot's
-            const uint4* from = reinterpret_cast<const uint4*>(w + p);
-            float x[kPer];
-            if ((reinterpret_cast<uintptr_t>(w) & 15) == 0) {
+        if (whole && p + kPer <= len) {
 #pragma unroll
-                for (int e = 0; e < kPer / 4; ++e) {
-                    const uint4 v = from[e];
-                    x[4 * e] = __uint_as_float(v.x), x[4 * e + 1] = __uint_as_float(v.y);
-                    x[4 * e + 2] = __uint_as_float(v.z), x[4 * e + 3] = __uint_as_float(v.w);
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < kPer; ++e) x[e] = w[p + e];
+            for (int e = 0; e < kPer / 4; ++e) {
+                const float4 v = reinterpret_cast<const float4*>(w + p)[e];
+                next[4 * e] = v.x, next[4 * e + 1] = v.y, next[4 * e + 2] = v.z, next[4 * e + 3] = v.w;
             }
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) order[e] = order_of(x[e]);
         } else {
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) order[e] = p + e < len ? order_of(w[p + e]) : 0;
+            for (int e = 0; e < kPer; ++e) next[e] = p + e < len ? w[p + e] : 0.f;
         }
     };
+    // the orders of a step, the next one's weights on their way (behind the last the first one's again)
+    auto take = [&](int step) __attribute__((always_inline)) {
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) order[e] = order_of(next[e]);
+        if (steps > 1) fetch(step + 1 < steps ? step + 1 : 0);
+    };
     const bool cut = len > a.keep;
-    if (cut) read(0);
+    if (cut) fetch(0);
 
     // an earlier entry that names the slot has it; every token of a slot that is cut has a page
     if (tid == 0) {
         s_bad = !real;
         s_first = a.keep;
     }
-    if (tid < 256) hist[0][tid] = hist[1][tid] = hist[2][tid] = hist[3][tid] = 0;
+#pragma unroll
+    for (int d = 0; d < kDigits; ++d) hist[d][tid] = hist[d][kPlan + tid] = 0;
     __syncthreads();
     for (int j = tid; j < i; j += kPlan)
         if (a.slot_list[j] == slot) s_bad = 1;
@@ -136,7 +139,7 @@ __global__ __launch_bounds__(kPlan) void cache_evict_plan_kernel(EvictK k) {
         if (kept != nullptr)
             for (int d = tid; d < a.keep; d += kPlan) kept[d] = !bad && d < len ? d : -1;
         if (tid == 0) {
-            k.plan[i] = -1;
+            k.plan[2 * i] = -1;
             if (a.status != nullptr) a.status[i] = bad ? 2 : 0;
         }
         return;
@@ -148,46 +151,37 @@ __global__ __launch_bounds__(kPlan) void cache_evict_plan_kernel(EvictK k) {
     uint32_t known = 0;
     if (some) {
 #pragma unroll
-        for (int digit = 0; digit < 4; ++digit) {
-            const int shift = 24 - 8 * digit;
+        for (int digit = 0; digit < kDigits; ++digit) {
+            constexpr int kShift[kDigits] = {21, 10, 0}, kWidth[kDigits] = {11, 11, 10};
+            const int shift = kShift[digit], bins = 1 << kWidth[digit];
             for (int step = 0; step < steps; ++step) {
-                if (steps > 1) read(step);
+                take(step);
                 const int p = step * kStep + tid * kPer;
 #pragma unroll
                 for (int e = 0; e < kPer; ++e)
-                    if (p + e >= from && p + e < to && (digit == 0 || order[e] >> (shift + 8) == known >> (shift + 8)))
-                        atomicAdd(&hist[digit][order[e] >> shift & 255], 1);
+                    if (p + e >= from && p + e < to && (digit == 0 || order[e] >> (shift + kWidth[digit]) == known >> (shift + kWidth[digit])))
+                        atomicAdd(&hist[digit][order[e] >> shift & (bins - 1)], 1);
             }
             __syncthreads();
-            if (tid < 64) {  // one wave: four bins a lane, the largest first
-                int n[4], mine = 0;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) mine += n[e] = hist[digit][255 - 4 * tid - e];
-                int before = mine;
-#pragma unroll
-                for (int o = 1; o < 64; o <<= 1) {
-                    const int y = __shfl_up(before, o);
-                    if (tid >= o) before += y;
-                }
-                before -= mine;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (before < left && left <= before + n[e]) {
-                        s_digit = 255 - 4 * tid - e;
-                        s_left = left - before;
-                    }
-                    before += n[e];
-                }
+            // two bins a thread, the largest first
+            const int n0 = hist[digit][kBins - 1 - 2 * tid], n1 = hist[digit][kBins - 2 - 2 * tid];
+            uint64_t total;
+            const int before = static_cast<int>(block_scan(static_cast<uint64_t>(n0 + n1), sums, total));
+            if (before < left && left <= before + n0 + n1) {
+                const bool second = left > before + n0;
+                s_digit = kBins - 1 - 2 * tid - second;
+                s_left = left - before - (second ? n0 : 0);
             }
             __syncthreads();
             known |= static_cast<uint32_t>(s_digit) << shift;
             left = s_left;
         }
     }
-    // `left` of those whose order is `known` stay, the first ones, and all above it
-    uint64_t before = 0;  // above it or protected (high half), equal to it (low half)
+    // `left` of those whose order is `known` stay, the first ones, and all above
+    // it.  A step's are gathered in LDS and written from there side by side.
+    int up_before = 0, eq_before = 0;  // above it or protected, equal to it
     for (int step = 0; step < steps; ++step) {
-        if (steps > 1) read(step);
+        take(step);
         const int p0 = step * kStep + tid * kPer;
         uint32_t above = 0, equal = 0;
 #pragma unroll
@@ -198,27 +192,31 @@ __global__ __launch_bounds__(kPlan) void cache_evict_plan_kernel(EvictK k) {
             else if (some && order[e] == known) equal |= 1u << e;
         }
         uint64_t total;
-        const uint64_t at = before + block_scan(static_cast<uint64_t>(__popc(above)) << 32 | __popc(equal), sums, total);
-        before += total;
-        int up = static_cast<int>(at >> 32), eq = static_cast<int>(at & 0xffffffffu);
-        int gone = a.keep;
+        const uint64_t at = block_scan(static_cast<uint64_t>(__popc(above)) << 32 | __popc(equal), sums, total);
+        const int base = up_before + min(eq_before, left);
+        int up = up_before + static_cast<int>(at >> 32), eq = eq_before + static_cast<int>(at & 0xffffffffu);
 #pragma unroll
         for (int e = 0; e < kPer; ++e) {
-            const int p = p0 + e;
             const bool is_up = above >> e & 1, is_eq = equal >> e & 1;
-            if (is_up || (is_eq && eq < left)) {
-                const int d = up + min(eq, left);
-                list[d] = p;
-                rows[d] = ((static_cast<int64_t>(table[p >> c.page_shift]) * c.Hkv) << c.page_shift) + (p & mask);
-                if (kept != nullptr) kept[d] = p;
-            } else if (p < len) {
-                gone = min(gone, p);
-            }
+            if (is_up || (is_eq && eq < left)) stay[up + min(eq, left) - base] = p0 + e;
             up += is_up;
             eq += is_eq;
         }
-        // tokens before the first one that goes keep their places
-        if (gone < a.keep) atomicMin(&s_first, gone);
+        up_before += static_cast<int>(total >> 32);
+        eq_before += static_cast<int>(total & 0xffffffffu);
+        __syncthreads();
+        const int count = up_before + min(eq_before, left) - base;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+            const int x = tid + e * kPlan, d = base + x;
+            if (x >= count) break;
+            const int p = stay[x];
+            list[d] = p;
+            rows[d] = ((static_cast<int64_t>(table[p >> c.page_shift]) * c.Hkv) << c.page_shift) + (p & mask);
+            if (kept != nullptr) kept[d] = p;
+            // tokens before the first one that goes keep their places
+            if (p != d && (x == 0 || stay[x - 1] == d - 1)) atomicMin(&s_first, d);
+        }
     }
     done_barrier();  // the list is read by other threads
     const int d0 = s_first;
@@ -231,43 +229,64 @@ __global__ __launch_bounds__(kPlan) void cache_evict_plan_kernel(EvictK k) {
         if (kept != nullptr)
             for (int d = tid; d < a.keep; d += kPlan) kept[d] = -1;
         if (tid == 0) {
-            k.plan[i] = -1;
+            k.plan[2 * i] = -1;
             if (a.status != nullptr) a.status[i] = 2;
         }
         return;
     }
     if (tid == 0) {
-        k.plan[i] = d0;
+        k.plan[2 * i] = d0;
+        k.plan[2 * i + 1] = len;
         if (a.status != nullptr) a.status[i] = 0;
     }
-    constexpr int kAtOnce = 4;
-    for (int e0 = d0; e0 < a.keep; e0 += kAtOnce * kPlan) {
-        float x[kAtOnce];
-#pragma unroll
-        for (int e = 0; e < kAtOnce; ++e) {
-            const int d = e0 + e * kPlan + tid;
-            x[e] = d < a.keep ? w[__hip_atomic_load(list + d, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)] : 0.f;
-        }
-        done_barrier();
-#pragma unroll
-        for (int e = 0; e < kAtOnce; ++e) {
-            const int d = e0 + e * kPlan + tid;
-            if (d < a.keep) w[d] = x[e];
-        }
-    }
-    __syncthreads();
-    for (int p = a.keep + tid; p < len; p += kPlan) w[p] = 0.f;
 }
 
 // One workgroup per (entry, key head, keys or values, part of the channels): its
-// rows in order, a step's rows in flight while the one before is written.  The
-// last workgroup of an entry gives the pages behind back and sets the length
-// (the others read neither those entries nor the counts).
+// rows in order, a step's rows in flight while the one before is written.  One
+// workgroup more of an entry moves its weights in the same way, and one gives
+// the pages behind back and sets the length (the others read neither those
+// entries, nor the counts, nor the length).
 constexpr int kRowsEach = 8;  // rows of a thread in a step
+
+__device__ __forceinline__ void move_weights(const EvictK& k, int i, int slot, int d0) {
+    const int keep = k.a.keep, len = k.plan[2 * i + 1], tid = threadIdx.x;
+    const int32_t* list = k.list + static_cast<int64_t>(i) * keep;
+    float* w = k.a.weights + ((static_cast<int64_t>(slot) * k.c.max_pages) << k.c.page_shift);
+    constexpr int kEach = 8, kStep = kMove * kEach;
+    struct Step {
+        float x[kEach];
+    };
+    auto load = [&](Step& s, int d) __attribute__((always_inline)) {
+        int at[kEach];
+#pragma unroll
+        for (int n = 0; n < kEach; ++n) at[n] = list[min(d + n * kMove + tid, keep - 1)];
+#pragma unroll
+        for (int n = 0; n < kEach; ++n) s.x[n] = w[at[n]];
+    };
+    auto store = [&](Step& s, int d) __attribute__((always_inline)) {
+#pragma unroll
+        for (int n = 0; n < kEach; ++n) asm volatile("" : "+v"(s.x[n]));
+        lds_barrier();
+#pragma unroll
+        for (int n = 0; n < kEach; ++n)
+            if (d + n * kMove + tid < keep) w[d + n * kMove + tid] = s.x[n];
+    };
+    Step a, b;
+    load(a, d0);
+    for (int d = d0; d < keep; d += 2 * kStep) {
+        load(b, d + kStep);
+        store(a, d);
+        if (d + kStep >= keep) break;
+        load(a, d + 2 * kStep);
+        store(b, d + kStep);
+    }
+    done_barrier();  // the last loads
+    for (int p = keep + tid; p < len; p += kMove) w[p] = 0.f;
+}
 
 __global__ __launch_bounds__(kMove) void cache_evict_move_kernel(EvictK k) {
     const CacheArgs& c = k.c;
-    const int i = blockIdx.x, d0 = k.plan[i], keep = k.a.keep;
+    const int i = blockIdx.x, d0 = k.plan[2 * i], keep = k.a.keep;
     if (d0 < 0) return;
     const int slot = k.a.slot_list[i];
     int32_t* table = c.table + static_cast<int64_t>(slot) * c.max_pages;
@@ -281,6 +300,7 @@ __global__ __launch_bounds__(kMove) void cache_evict_move_kernel(EvictK k) {
         if (threadIdx.x == 0) c.lens[slot] = keep;
         return;
     }
+    if (blockIdx.y == gridDim.y - 2) return move_weights(k, i, slot, d0);
     const int share = blockIdx.y % k.splits, unit = blockIdx.y / k.splits;
     const int kvh = unit >> 1, e = c.x == DT::BF16 ? 2 : 4;
     const int pieces = ((unit & 1) == 0 ? c.dk : c.dv) * e / 16;
@@ -334,7 +354,7 @@ size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 size_t cache_evict_workspace_bytes(int n, int keep) {
     const size_t all = static_cast<size_t>(n) * keep;
-    return up256(all * 4) + up256(all * 8) + up256(static_cast<size_t>(n) * 4);
+    return up256(all * 4) + up256(all * 8) + up256(static_cast<size_t>(n) * 8);
 }
 
 hipError_t launch_cache_evict(const CacheArgs& c, const EvictArgs& a, hipStream_t s) {
@@ -357,7 +377,7 @@ hipError_t launch_cache_evict(const CacheArgs& c, const EvictArgs& a, hipStream_
     const int row = (c.dk < c.dv ? c.dk : c.dv) * (c.x == DT::BF16 ? 2 : 4);
     while (k.splits < 4 && static_cast<int64_t>(a.n) * 2 * c.Hkv * k.splits < 512 && row / (2 * k.splits) >= 64) k.splits *= 2;
     LaunchTimer timer("cache_evict_move", s);
-    cache_evict_move_kernel<<<dim3(a.n, 2 * c.Hkv * k.splits + 1), dim3(kMove), 0, s>>>(k);
+    cache_evict_move_kernel<<<dim3(a.n, 2 * c.Hkv * k.splits + 2), dim3(kMove), 0, s>>>(k);
     return hipGetLastError();
 }
 
