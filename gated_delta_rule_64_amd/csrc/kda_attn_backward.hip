@@ -635,20 +635,35 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_far_sum_kernel(BwdK a) {
 // workgroups, which differ in length, fill the chip several times; query tiles
 // where they and the key tiles' together leave it half empty.
 constexpr int kKeyWant = 1024, kQueryWant = 384;  // workgroups below which tiles are cut
-// With a window the workgroups of key tiles are equally long but for a
-// sequence's last ones.
-constexpr int kKeyWantWindow = 512;
 struct BwdParts {
     int key, query;
 };
-BwdParts bwd_parts(int64_t T, int N, int H, int Hkv, int window) {
+// With a window the workgroups of key tiles are equally long but for a sequence's
+// last ones, and short: about one round of them, none of fewer than kLeast of its
+// steps (32 queries of a key tile, 32 keys of a query tile).  fp32, whose steps
+// are four times as long, is cut finer.  bf16 (8 heads over 2, six sequences of
+// up to 500 tokens): 8 key parts 38 us, 3 parts 30; 4,096 tokens of 4 heads under
+// a window of 1,024: 62 us, for 512 workgroups 79; 16 sequences of up to 800
+// tokens 140 and 157.  fp32: the same six sequences 62 us, of 8 steps at least 84,
+// of 2 as long; 3 sequences of 4 heads of 128 104 us, of 2 steps at least 119.
+constexpr int kKeyWantWindow = 256, kKeyWantWindowF32 = 512, kQueryWantWindow = 256;
+constexpr int kLeastSteps = 8, kLeastKeyStepsF32 = 4, kLeastQueryStepsF32 = 2;
+
+BwdParts bwd_parts(int64_t T, int N, int H, int Hkv, DT x, int window) {
     const int64_t tiles = attn_tiles(T, N, kRows), keys = tiles * Hkv, queries = tiles * H;
     if (tiles == 0) return {1, 1};
     auto parts = [](int64_t want, int64_t units, int64_t most) {
         const int64_t p = (want + units - 1) / units;
-        return static_cast<int>(p < 1 ? 1 : p > most ? most : p);
+        return static_cast<int>(p < 1 || most < 1 ? 1 : p > most ? most : p);
     };
-    return {parts(window > 0 ? kKeyWantWindow : kKeyWant, keys, kMostParts), parts(kQueryWant, queries, kMostParts / 2)};
+    if (window < 1) return {parts(kKeyWant, keys, kMostParts), parts(kQueryWant, queries, kMostParts / 2)};
+    auto least = [](int64_t a, int64_t b) { return a < b ? a : b; };
+    const bool four = heads_share(H, Hkv), wide = x == DT::F32;
+    const int64_t rows = four ? 32 : kRows, seen = least(window, T);
+    const int64_t key_steps = (seen + kRows + 31) / 32 * (H / Hkv), query_steps = (seen + rows + 31) / 32;
+    const int64_t units = four ? attn_tiles(T, N, 32) * (H / 4) : queries;
+    return {parts(wide ? kKeyWantWindowF32 : kKeyWantWindow, keys, least(kMostParts, key_steps / (wide ? kLeastKeyStepsF32 : kLeastSteps))),
+            parts(kQueryWantWindow, units, least(kMostParts / 2, query_steps / (wide ? kLeastQueryStepsF32 : kLeastSteps)))};
 }
 
 // The far queries' workgroups.  More first tokens than a tile's reach are
@@ -698,7 +713,7 @@ hipError_t launch_bwd(const AttnBackwardArgs& a, hipStream_t s) {
     ws += up256(static_cast<size_t>(f.T) * f.H * 8);
     k.dog = f.z != nullptr ? static_cast<void*>(ws) : const_cast<void*>(a.dy);
     if (f.z != nullptr) ws += up256(static_cast<size_t>(f.T) * f.H * DV * sizeof(T));
-    const BwdParts parts = bwd_parts(f.T, f.N, f.H, f.Hkv, f.window);
+    const BwdParts parts = bwd_parts(f.T, f.N, f.H, f.Hkv, f.x, f.window);
     k.parts = parts.key;
     k.q_parts = parts.query;
     k.part = reinterpret_cast<float*>(ws);
@@ -753,7 +768,7 @@ hipError_t launch_bwd(const AttnBackwardArgs& a, hipStream_t s) {
 
 size_t attn_backward_workspace_bytes(int64_t T, int N, int H, int Hkv, int dk, int dv, DT x, bool gate, int window, int sinks) {
     const size_t rows = static_cast<size_t>(T) * H;
-    const BwdParts parts = bwd_parts(T, N, H, Hkv, window);
+    const BwdParts parts = bwd_parts(T, N, H, Hkv, x, window);
     const FarPlan far = far_plan(T, Hkv, window, sinks, parts.key);
     return up256(rows * 8) + (gate ? up256(rows * dv * (x == DT::BF16 ? 2 : 4)) : 0) +
            (parts.key > 1 ? up256(static_cast<size_t>(parts.key) * T * Hkv * (dk + dv) * 4) : 0) +
@@ -762,13 +777,14 @@ size_t attn_backward_workspace_bytes(int64_t T, int N, int H, int Hkv, int dk, i
 }
 
 // More tokens have fewer parts, so what a call needs does not rise with its
-// sizes.  One sequence has the fewest tiles and so the most parts; of the
-// lengths of as many tiles the longest needs the most; from kKeyWant tiles on
+// sizes (but for a window's, as far as it holds them all).  One sequence has the
+// fewest tiles and so the most parts; of the lengths of as many tiles, of 32 rows
+// or 128, the longest needs the most; from kKeyWant tiles on
 // there is one part.  The far sums' parts fall as their rows rise: p parts of r
 // rows are at most kMostFarParts r and at most kFarRows or r.
 size_t attn_backward_max_workspace_bytes(int64_t T, int H, int Hkv, int dk, int dv, DT x, bool gate, int window, int sinks) {
     size_t most = attn_backward_workspace_bytes(T, 1, H, Hkv, dk, dv, x, gate, window, 0);
-    for (int64_t t = kRows - 1; t < T && t < static_cast<int64_t>(kKeyWant) * kRows; t += kRows) {
+    for (int64_t t = 31; t < T && t < static_cast<int64_t>(kKeyWant) * kRows; t += 32) {
         const size_t need = attn_backward_workspace_bytes(t, 1, H, Hkv, dk, dv, x, gate, window, 0);
         most = need > most ? need : most;
     }
@@ -783,7 +799,7 @@ hipError_t launch_attn_prefill_backward(const AttnBackwardArgs& a, hipStream_t s
     return attn_dispatch(a.f.x, a.f.dk, a.f.dv, [&](auto t, auto dk, auto dv) {
         using X = typename decltype(t)::type;
         constexpr int kDk = decltype(dk)::value, kDv = decltype(dv)::value;
-        if (a.f.window > 0 && a.f.H / a.f.Hkv % 4 == 0) return launch_bwd<X, kDk, kDv, true, 32>(a, s);
+        if (a.f.window > 0 && heads_share(a.f.H, a.f.Hkv)) return launch_bwd<X, kDk, kDv, true, 32>(a, s);
         return a.f.window > 0 ? launch_bwd<X, kDk, kDv, true, kRows>(a, s) : launch_bwd<X, kDk, kDv, false, kRows>(a, s);
     });
 }

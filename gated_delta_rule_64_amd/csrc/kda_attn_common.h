@@ -253,6 +253,9 @@ __device__ __forceinline__ Tile find_tile(const int32_t* cu, int N, int64_t T, i
 // would hold more masks than there are scalar registers.
 __device__ __forceinline__ bool outside(int key, int least, int sink) { return ((key - least) & (sink - 1 - key)) < 0; }
 
+// Whether a windowed workgroup takes 32 rows of four heads of a group, not 128 of one.
+inline bool heads_share(int H, int Hkv) { return H / Hkv % 4 == 0; }
+
 // The key tiles of kKeys that a tile of 128 query rows from q_first on attends,
 // in order: all up to its own last row, or with a window (kWin) those that hold
 // one of the sequence's first `sinks` tokens and those from the first row's

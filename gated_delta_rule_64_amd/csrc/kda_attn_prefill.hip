@@ -258,7 +258,7 @@ hipError_t launch_attn_prefill(const AttnArgs& a, hipStream_t s) {
     return attn_dispatch(a.x, a.dk, a.dv, [&](auto t, auto dk, auto dv) {
         using X = typename decltype(t)::type;
         constexpr int kDk = decltype(dk)::value, kDv = decltype(dv)::value;
-        if (a.window > 0 && a.H / a.Hkv % 4 == 0) return launch_fwd<X, kDk, kDv, true, 32>(a, s);
+        if (a.window > 0 && heads_share(a.H, a.Hkv)) return launch_fwd<X, kDk, kDv, true, 32>(a, s);
         return a.window > 0 ? launch_fwd<X, kDk, kDv, true, kQ>(a, s) : launch_fwd<X, kDk, kDv, false, kQ>(a, s);
     });
 }
