@@ -499,10 +499,17 @@ __global__ __launch_bounds__(kKeys) void cache_weigh_sum_kernel(WeighK k) {
     const int pos = tiles.first(tile) + threadIdx.x;
     bool there;
     row_of(k, w, pos, there);
-    if (!there) return;
     const float* from = k.part + (static_cast<int64_t>(n) * k.groups + tile * parts) * kKeys + threadIdx.x;
     float sum = 0.f;
-    for (int p = 0; p < parts; ++p) sum += from[p * kKeys];
+    constexpr int kEach = 8;  // in flight (one after the other, up to 64 of them, 11 us)
+    for (int p0 = 0; p0 < parts; p0 += kEach) {
+        float x[kEach];
+#pragma unroll
+        for (int p = 0; p < kEach; ++p) x[p] = p0 + p < parts ? from[(p0 + p) * kKeys] : 0.f;
+#pragma unroll
+        for (int p = 0; p < kEach; ++p) sum += x[p];
+    }
+    if (!there) return;
     *weight_of(k, w, pos) += sum;
 }
 
