@@ -28,7 +28,6 @@ struct WeighK {
     CacheArgs c;
     WeighArgs a;
     int groups;      // workgroups of a sequence
-    int most_parts;  // many queries: that the work of a tile may be cut into
     float* part;     // [N, groups][keys of a tile]
 };
 
@@ -273,12 +272,14 @@ __global__ __launch_bounds__(kThreads, (DK * sizeof(T) <= 256 ? 3 : 1)) void cac
     }
 }
 
+constexpr int kMostParts = 64;
+
 // How a sequence's tiles go to its workgroups: a tile each in turn, or, where
 // there are fewer tiles, several to a tile, that take equal parts of its work.
 struct Shares {
     int parts;
     __device__ __forceinline__ Shares(const WeighK& k, int tiles)
-        : parts(tiles >= k.groups ? 1 : min(k.groups / max(tiles, 1), k.most_parts)) {}
+        : parts(tiles >= k.groups ? 1 : min(k.groups / max(tiles, 1), kMostParts)) {}
 };
 
 template <typename T, int DK>
@@ -513,10 +514,23 @@ __global__ __launch_bounds__(kKeys) void cache_weigh_sum_kernel(WeighK k) {
     *weight_of(k, w, pos) += sum;
 }
 
-// Workgroups of a call, where it has that much work.
-constexpr int kFewWant = 4096, kManyWant = 1024, kMostParts = 64;
+// Workgroups of a call.  The host knows how many tiles a table row can hold, not
+// how many there are: workgroups without work cost, where few fit a CU, most of a
+// short call (43 fp32 sequences of up to 20 tokens, 32 heads of 128: 215 us with
+// 4,096 of them, 35 with one per tile of the table).
+// Few queries: three workgroups a CU up to 50 KB of LDS (a decode step of 256
+// sequences 263 us by events, with 2,048 workgroups 270); else one or two (the
+// step in fp32 692 us, with 4,096 workgroups 775).
+// Many queries: a prompt of 8,000 tokens 392 us by events, with 512 workgroups 607
+// (the tiles differ), with 2,048 the last 64 tokens of 8 prompts 61 us for 56.
+// Parts of a tile: 8,000 tokens of 4 heads 59 us, with a part per head 222.
+constexpr int kFewWant = 4096, kFewWantWide = 1024, kManyWant = 1024;
 
-int per_sequence(int64_t want, int64_t N) { return static_cast<int>((want + N - 1) / N); }
+// of a sequence that has work for `most` at most
+int per_sequence(int64_t want, int64_t N, int64_t most) {
+    const int64_t p = (want + N - 1) / N;
+    return static_cast<int>(p < most ? p : most < 1 ? 1 : most);
+}
 
 // Few queries: their rows of one key head are 32 on the average at most.
 bool few_queries(int64_t tokens, int64_t N, int G) { return tokens * G <= kRows * N; }
@@ -524,13 +538,14 @@ bool few_queries(int64_t tokens, int64_t N, int G) { return tokens * G <= kRows 
 template <typename T, int DK>
 hipError_t launch_weigh(const CacheArgs& c, const WeighArgs& a, hipStream_t s) {
     const int64_t max_ctx = static_cast<int64_t>(c.max_pages) << c.page_shift;
+    auto tiles_of = [&](int keys) { return (max_ctx + keys - 1) / keys; };
     WeighK k{};
     k.c = c;
     k.a = a;
     if (a.window >= max_ctx) k.a.window = 0;  // it holds every token
     if (few_queries(a.tokens, a.N, a.H / c.Hkv)) {
-        k.groups = per_sequence(kFewWant, a.N);
         constexpr int lds = FewSizes<T, DK>::kLds;
+        k.groups = per_sequence(3 * lds > 160 * 1024 ? kFewWantWide : kFewWant, a.N, tiles_of(FewSizes<T, DK>::kKeys));
         auto fn = cache_weigh_few_kernel<T, DK>;
         if (lds > 64 * 1024) {
             const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
@@ -541,8 +556,7 @@ hipError_t launch_weigh(const CacheArgs& c, const WeighArgs& a, hipStream_t s) {
         return hipGetLastError();
     }
     constexpr int kKeys = ManySizes<T, DK>::kKeys;
-    k.groups = per_sequence(kManyWant, a.N);
-    k.most_parts = a.H < kMostParts ? a.H : kMostParts;
+    k.groups = per_sequence(kManyWant, a.N, kMostParts * tiles_of(kKeys));
     k.part = static_cast<float*>(a.ws);
     const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(a.N) * k.groups));
     {
@@ -561,7 +575,7 @@ hipError_t launch_weigh(const CacheArgs& c, const WeighArgs& a, hipStream_t s) {
 
 size_t cache_weigh_workspace_bytes(int64_t tokens, int N, int H, int Hkv) {
     if (few_queries(tokens, N, H / Hkv)) return 0;
-    return static_cast<size_t>(N) * per_sequence(kManyWant, N) * 256 * 4;  // a tile has 256 keys at most
+    return static_cast<size_t>(N) * per_sequence(kManyWant, N, kManyWant) * 256 * 4;  // a tile has 256 keys at most
 }
 
 hipError_t launch_cache_weigh(const CacheArgs& c, const WeighArgs& a, hipStream_t s) {
