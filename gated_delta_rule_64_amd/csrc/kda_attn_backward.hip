@@ -67,18 +67,28 @@ __device__ __forceinline__ BwdK again() {
 // by window + 127 of their tile at most: a tile of first tokens would be many
 // times as long as the rest.  So it takes as many queries as the others do, and
 // those behind, from far_from() on, go to workgroups of their own, in parts.
-// Only sequences of reach() tokens or more have such queries.  There is at most
-// one that begins in each bucket of so many tokens, the one that holds the
-// bucket's last token.
+// Only sequences of reach() tokens or more have such queries: a bucket for each
+// sequence, or, where that is fewer, one for each reach() tokens, in which at most
+// one of them begins, the one that holds the bucket's last token.
 __device__ __forceinline__ int reach(const BwdK& a) { return a.window + kRows; }
 template <int kQ>
 __device__ __forceinline__ int far_from(const BwdK& a, int k_first, int len) {
     return k_first + (min(len - k_first, kRows - 1 + a.window) + kQ - 1) / kQ * kQ;
 }
+__device__ __forceinline__ bool far_by_sequence(const BwdK& a) { return a.N <= a.far_buckets; }
 __device__ __forceinline__ bool far_sequence(const BwdK& a, int64_t bucket, int64_t& start, int& len) {
+    if (far_by_sequence(a)) {
+        seq_bounds(a.cu, static_cast<int>(bucket), a.T, start, len);
+        return len >= reach(a);
+    }
     const int64_t token = (bucket + 1) * reach(a) - 1;
     seq_bounds(a.cu, a.cu == nullptr ? 0 : find_seq(a.cu, a.N, token), a.T, start, len);
     return start >= bucket * reach(a) && start <= token && token < start + len && len >= reach(a);
+}
+// The bucket of the sequence that begins at `start`.
+__device__ __forceinline__ int64_t far_bucket(const BwdK& a, int64_t start) {
+    if (!far_by_sequence(a)) return start / reach(a);
+    return a.cu == nullptr ? 0 : find_seq(a.cu, a.N, start);
 }
 // A row's place in the far sums.
 __device__ __forceinline__ float* far_row(const BwdK& a, int slot, int64_t bucket, int key, int kvh, int width) {
@@ -511,7 +521,7 @@ __device__ __forceinline__ void key_gradients(const BwdK& a, unsigned block, cha
     const BwdK b = kWin ? again() : a;
     if (kWin && b.parts == 1 && b.far_parts > 0 && k_first < b.sinks && far_from<kQ>(b, k_first, t.len) < t.len) {
         if (c < rows && k0 + c < b.sinks) {
-            float* to = far_row(b, 0, t.start / reach(b), k0 + c, kvh, DK + DV);
+            float* to = far_row(b, 0, far_bucket(b, t.start), k0 + c, kvh, DK + DV);
             store_rows<float, DK>(to, gk, b.scale, half);
             store_rows<float, DV>(to + DK, gv, 1.f, half);
             return;
@@ -601,7 +611,7 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_sum_kernel(BwdK a) {
             int len;
             seq_bounds(a.cu, a.cu == nullptr ? 0 : find_seq(a.cu, a.N, token), a.T, start, len);
             if (token - start < a.sinks && len >= reach(a))
-                add_far<T, DK, DV>(a, start / reach(a), static_cast<int>(token - start), len, static_cast<int>(row % a.Hkv), ch, 1, sum);
+                add_far<T, DK, DV>(a, far_bucket(a, start), static_cast<int>(token - start), len, static_cast<int>(row % a.Hkv), ch, 1, sum);
         }
         store_sum<T, DK, DV>(a, row, ch, sum);
         return;
@@ -676,11 +686,11 @@ struct FarPlan {
     int tiles = 0, parts = 0;
     int64_t rows(int sinks) const { return buckets * sinks; }
 };
-FarPlan far_plan(int64_t T, int Hkv, int window, int sinks, int near_parts) {
+FarPlan far_plan(int64_t T, int64_t N, int Hkv, int window, int sinks, int near_parts) {
     FarPlan p;
     const int64_t reach = static_cast<int64_t>(window) + kRows;
     if (window < 1 || sinks < 1 || sinks > reach || T < reach) return p;
-    p.buckets = T / reach;
+    p.buckets = T / reach < N ? T / reach : N;
     p.tiles = (sinks + kRows - 1) / kRows;
     int64_t parts = ((T - reach) * near_parts + reach - 1) / reach;
     const int64_t groups = p.buckets * p.tiles * Hkv, rows = p.rows(sinks);
@@ -721,7 +731,7 @@ hipError_t launch_bwd(const AttnBackwardArgs& a, hipStream_t s) {
     k.q_part = reinterpret_cast<float*>(ws);
     if (k.q_parts > 1) ws += up256(static_cast<size_t>(k.q_parts) * f.T * f.H * DK * 4);
     if constexpr (kWin) {
-        const FarPlan far = far_plan(f.T, f.Hkv, k.window, k.sinks, k.parts);
+        const FarPlan far = far_plan(f.T, f.N, f.Hkv, k.window, k.sinks, k.parts);
         k.far_buckets = far.buckets;
         k.far_tiles = far.tiles;
         k.far_parts = far.parts;
@@ -769,7 +779,7 @@ hipError_t launch_bwd(const AttnBackwardArgs& a, hipStream_t s) {
 size_t attn_backward_workspace_bytes(int64_t T, int N, int H, int Hkv, int dk, int dv, DT x, bool gate, int window, int sinks) {
     const size_t rows = static_cast<size_t>(T) * H;
     const BwdParts parts = bwd_parts(T, N, H, Hkv, x, window);
-    const FarPlan far = far_plan(T, Hkv, window, sinks, parts.key);
+    const FarPlan far = far_plan(T, N, Hkv, window, sinks, parts.key);
     return up256(rows * 8) + (gate ? up256(rows * dv * (x == DT::BF16 ? 2 : 4)) : 0) +
            (parts.key > 1 ? up256(static_cast<size_t>(parts.key) * T * Hkv * (dk + dv) * 4) : 0) +
            (parts.query > 1 ? up256(static_cast<size_t>(parts.query) * rows * dk * 4) : 0) +
@@ -788,7 +798,7 @@ size_t attn_backward_max_workspace_bytes(int64_t T, int H, int Hkv, int dk, int 
         const size_t need = attn_backward_workspace_bytes(t, 1, H, Hkv, dk, dv, x, gate, window, 0);
         most = need > most ? need : most;
     }
-    const FarPlan far = far_plan(T, Hkv, window, sinks, 1);
+    const FarPlan far = far_plan(T, T, Hkv, window, sinks, 1);
     if (far.parts == 0) return most;
     const int64_t rows = far.rows(sinks), parts = rows > kFarRows ? rows : rows * kMostFarParts < kFarRows ? rows * kMostFarParts : kFarRows;
     return most + up256(static_cast<size_t>(rows + parts) * Hkv * (dk + dv) * 4);

@@ -111,6 +111,18 @@ def test_first_tokens_of_many_long_sequences(K, window, sinks, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_first_tokens_of_long_sequences_among_many_short_ones(K, dtype):
+    """More sequences than could have far queries."""
+    reach = 40 + 128
+    short = [i % 4 for i in range(12)]
+    lens = [*short, reach, *short, reach + 33, reach - 1, *short, 700, 2]
+    assert len(lens) > sum(lens) // reach
+    print(f"first tokens, many short {dtype}", flush=True)
+    x = _inputs(23, lens, 4, 2, 32, 32, TYPES[dtype], False, spare=3)
+    _check(K, x, lens, 40, 35, TYPES[dtype])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_first_tokens_where_tiles_are_not_cut(K, dtype):
     """So many key tiles that none is cut into parts; the far queries are."""
     lens = [2500, 129, 2100]
