@@ -136,6 +136,32 @@ def test_longer_slots(K, n, keep, page):
     _check(K, x, list(x["slot"]), keep, min(4, keep), min(keep - min(4, keep), 100))
 
 
+@pytest.mark.parametrize("kind", ["random", "few values", "odd"])
+@pytest.mark.parametrize("lens,keep,first,recent", [([8192, 8193, 100], 100, 4, 7), ([20000, 16385], 16384, 0, 0), ([25000], 9000, 8200, 500),
+                                                    ([16390, 8200], 8192, 3, 8189), ([40000], 1, 0, 0)])
+def test_slots_of_several_steps(K, lens, keep, first, recent, kind):
+    """More tokens than a planning workgroup holds at once."""
+    print(f"evict steps {lens} {keep} {kind}", flush=True)
+    x = _cache(len(lens) + keep, lens, 64, Hkv=1, kind=kind)
+    assert _check(K, x, x["slot"], keep, first, recent) == [0] * len(lens)
+
+
+@pytest.mark.parametrize("n", [50, 20000])
+def test_weights_that_begin_anywhere(K, n):
+    x = _cache(n, [n, 33], 16, kind="few values")
+    flat = torch.empty(x["weights"].numel() + 1, device="cuda")[1:]
+    flat.copy_(x["weights"].flatten())
+    x["weights"] = flat.view(x["weights"].shape)
+    assert x["weights"].data_ptr() % 16 == 4
+    assert _check(K, x, x["slot"], 29, 2, 3) == [0, 0]
+
+
+def test_as_many_heads_as_there_can_be(K):
+    x = _cache(77, [40], 16, Hkv=(1 << 15) - 1, dtype=torch.bfloat16, spare=0)
+    print("evict 32767 heads", flush=True)
+    assert _check(K, x, x["slot"], 17, 1, 2) == [0]
+
+
 @pytest.mark.parametrize("order", ["rising", "falling"])
 def test_ordered_weights(K, order):
     """Only the last stay (every row moves as far as it can), or only the first
