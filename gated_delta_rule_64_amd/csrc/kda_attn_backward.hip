@@ -17,6 +17,15 @@
 // TFLOP/s on five products (940 to 980 on the seven), matrix cores 51 % of the
 // cycles, waits 30 %.  Six ragged fp32 sequences of up to 500 tokens, 8 heads of
 // 64 over 2: 70 us, bound by the length of a workgroup's chain of fp32 products.
+//
+// With a window a key tile has the queries up to its last key's window, and
+// queries of 32 rows of four heads share a workgroup where the group allows it.
+// What later queries give to the first tokens is summed apart (far queries,
+// below), else the first tile would be as long as the sequence: 8,192 tokens
+// under a window of 1,024, 849 us with it in one piece, 520 to 535 now (floor 233;
+// 610 TFLOP/s on five products, matrix cores 44 %, vector units 31 %, waits 38 %).
+// The six fp32 sequences under a window of 100: 61 us (49 of them the gradients,
+// matrix cores 25 %; chains of 3 to 5 steps of 4 us each and their starts).
 #include "kda_attn_common.h"
 #include "kda_internal.h"
 #include "kda_profile.h"

@@ -18,6 +18,16 @@
 // 192/128 channels, gated: 326 to 341 us, 650 to 680 TFLOP/s, matrix cores 36 %,
 // waits 28 %: such a batch also moves 0.69 GB (125 us), of which the queries, the
 // gate and the results are not under the products (without a gate: 22 us less).
+//
+// With a window (and first tokens that stay visible) the same walk over fewer
+// tiles: those of the first tokens, then those from the first row's window on;
+// only tiles at a window's start are masked.  Four heads of a group and 32 rows
+// of them share a workgroup where the group allows it, so that all its waves need
+// the same keys: 16,384 tokens under a window of 4,096, 1,050 to 980 us (floor
+// 693; 980 TFLOP/s of what is attended, 1,050 of what is formed).  The twelve
+// prompts under a window of 512: 238 us (floor 135, memory; matrix cores 26 %,
+// vector units 38 %, waits 34 %): 18 tiles of 32 keys a workgroup do not cover
+// its queries, gate and results.  64 tokens: 9.5 us, the host's side of a call.
 #include "kda_attn_common.h"
 #include "kda_internal.h"
 #include "kda_profile.h"

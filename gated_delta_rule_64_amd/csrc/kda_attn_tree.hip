@@ -18,6 +18,13 @@
 // 6.3 that a streaming read reaches); trees of 16 over 32 ragged sequences take
 // 136 us with their join, 1.07 times the traffic; a chain of 4 over 262,144
 // tokens 191 us (5.6 TB/s).
+//
+// With a window only the tiles that hold a first token or one of some row's
+// window are walked; those where a window begins are masked per row, and values
+// there that are not finite are taken out and given to the rows that attend them.
+// The decode step under a window of 1,024: 1.08 GB in 192 us (5.6 TB/s); the trees
+// under one of 2,000: 61 us for 244 MB (4.0 TB/s; a workgroup's start and the join
+// of its waves are a fourth of its time).
 #include <cfloat>
 
 #include "kda_attn_common.h"

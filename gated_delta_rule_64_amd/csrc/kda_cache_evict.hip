@@ -7,6 +7,10 @@
 // can move them where they are, as long as a step's reads come before its
 // writes.  What a later step reads is behind all that an earlier one writes, so
 // that its reads need not wait for those writes.
+//
+// 64 slots of 500 to 8,000 tokens cut to 2,048 (8 heads of 128, bf16): 205 us, of
+// which the plan takes 15 and the rows 183 (0.86 GB, 4.8 TB/s, of the 5.1 that a
+// large copy reaches); one of 5,000 cut to 1,024: 28 us, of which the plan takes 13.
 #include "kda_common.h"
 #include "kda_internal.h"
 #include "kda_profile.h"
@@ -68,7 +72,8 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t x, uint64_t* sums, uint6
 // and 10 bits: many bins, so that weights of one size do not wait for each other)
 // are counted in LDS.  A slot of up to kStep tokens is read once and its orders
 // stay in registers: bound by the length of its chain of barriers.  A longer one
-// is read once per digit, the next step's weights in flight.
+// is read once per digit, the next step's weights in flight: 100,000 tokens in 92
+// us, 1.7 us a step and digit.
 constexpr int kPer = 8;  // neighbouring tokens of a thread
 constexpr int kStep = kPlan * kPer;
 constexpr int kDigits = 3, kBins = 2048;

@@ -11,6 +11,11 @@
 // one for many (the last tokens of prompts, whole prompts).  Either is right for
 // any number; the host chooses by the average, as only the device knows a
 // sequence's own.
+//
+// bf16, 32 heads of 128 over 8: a decode step's 256 queries over 1,024 to 4,096
+// tokens each read 1.33 GB in 243 us (5.5 TB/s); all of a prompt of 8,000 tokens
+// 306 us (860 TFLOP/s of the 1,390 that a large product reaches; floor 189), the
+// last 64 tokens of 8 prompts 50 us (floor 14).
 #include "kda_attn_common.h"
 #include "kda_internal.h"
 #include "kda_profile.h"
@@ -290,7 +295,10 @@ struct ManySizes {
     static constexpr int kBuf = kTile + kRows * 4;  // rows of queries and their lse
 };
 
-// Many queries: bound by the products and exponentials.  One workgroup per
+// Many queries: bound by the products and exponentials (8,000 tokens: matrix cores
+// 34 % of the cycles, vector units 44 %, waits 21 %; a wave's step of 64 keys by 32
+// queries has 16 products of 32 cycles and 32 exponentials of 8, each with a
+// multiply-add and an addition of 4).  One workgroup per
 // (sequence, tile of keys, part): a wave's keys stay in its registers, the
 // queries of a head pass through LDS, once for four waves, two steps in flight
 // (a step is shorter than a load takes).  S = Q K^T, so that a lane holds one
