@@ -22,8 +22,8 @@
 // queries of 32 rows of four heads share a workgroup where the group allows it.
 // What later queries give to the first tokens is summed apart (far queries,
 // below), else the first tile would be as long as the sequence: 8,192 tokens
-// under a window of 1,024, 849 us with it in one piece, 520 to 535 now (floor 233;
-// 610 TFLOP/s on five products, matrix cores 44 %, vector units 31 %, waits 38 %).
+// under a window of 1,024, 849 us with it in one piece, 517 to 524 now (floor 233;
+// 620 TFLOP/s on five products, matrix cores 44 %, vector units 31 %, waits 38 %).
 // The six fp32 sequences under a window of 100: 61 us (49 of them the gradients,
 // matrix cores 25 %; chains of 3 to 5 steps of 4 us each and their starts).
 #include "kda_attn_common.h"
@@ -425,7 +425,14 @@ __device__ __forceinline__ void key_gradients(const BwdK& a, unsigned block, cha
     const int64_t all = static_cast<int64_t>(steps) * G;
     int n = static_cast<int>(all * part / parts);
     const int n_end = static_cast<int>(all * (part + 1) / parts);
-    int f_head = uniform(kvh * G + n / steps), f_i0 = uniform(i_first + n % steps * kQ);  // the next step to fetch
+    // With a window and a tile in one piece: each head's steps begin where the
+    // other tiles' do, modulo their number, so that the tiles that need the same
+    // queries read them at about the same time (8,192 tokens under a window of
+    // 1,024: 0.57 GB read from memory for 1.48, 530 to 521 us).
+    int i_start = i_first;
+    if constexpr (kWin && !kFar)
+        if (parts == 1) i_start = uniform(i_first + (steps - k_first / kQ % steps) % steps * kQ);
+    int f_head = uniform(kvh * G + n / steps), f_i0 = uniform(i_start + n % steps * kQ);  // the next step to fetch
     auto fetch = [&]() __attribute__((always_inline)) {
         const int here = min(kQ, t.len - f_i0);
         cq.load(rows_of(static_cast<const T*>(a.q) + f_head * DK, t.start + f_i0, q_row, here), q_row, tid);
@@ -434,7 +441,10 @@ __device__ __forceinline__ void key_gradients(const BwdK& a, unsigned block, cha
         if (wave == 0)
             stat = buffer_load8(rows_of(a.stats + f_head, t.start + f_i0, a.H * 8, here), c * a.H * 8);
         f_i0 += kQ;
-        if (f_i0 >= end) {
+        if constexpr (kWin && !kFar) {
+            if (f_i0 >= end) f_i0 = i_first;
+            if (f_i0 == i_start) ++f_head;
+        } else if (f_i0 >= end) {
             f_i0 = i_first;
             ++f_head;
         }
