@@ -83,9 +83,10 @@ __device__ __forceinline__ float* weight_of(const WeighK& k, const Weighed& w, i
     return k.a.weights + ((static_cast<int64_t>(w.slot) * k.c.max_pages) << k.c.page_shift) + pos;
 }
 
-// What a key has gathered: a sum that is NaN comes from a key that is not
+// What a key has gathered: a sum that is NaN comes from a head's key that is not
 // finite.  A row that attends such a key has an lse that is not finite (and
-// weighs nothing) or no weight there.
+// weighs nothing) or no weight there.  Where many queries are, whose broken rows
+// read as 0, it is taken for a step of one head, so that the others' stay.
 __device__ __forceinline__ float gathered(float x) { return x == x ? x : 0.f; }
 
 template <typename T, int DK>
@@ -465,7 +466,7 @@ __global__ __launch_bounds__(kThreads, (DK * sizeof(T) <= 256 ? 2 : 1)) void cac
                 float sum = 0.f;
 #pragma unroll
                 for (int r = 0; r < 16; ++r) sum += s[u][r];
-                acc[u] += sum;
+                acc[u] += gathered(sum);
             }
         };
         Step x, y;
@@ -485,7 +486,7 @@ __global__ __launch_bounds__(kThreads, (DK * sizeof(T) <= 256 ? 2 : 1)) void cac
         }
 #pragma unroll
         for (int u = 0; u < kSub; ++u) {
-            const float x = gathered(xor32_add(acc[u]));
+            const float x = xor32_add(acc[u]);
             if (half != 0) continue;
             if (parts > 1)
                 k.part[(static_cast<int64_t>(n) * k.groups + group) * kKeys + wave * 32 * kSub + 32 * u + col] = x;

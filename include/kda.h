@@ -767,9 +767,9 @@ int kda_cache_copy(void* pool, int64_t row_bytes, int32_t rows,
  * Products, exponentials and sums are fp32, in a fixed order: the same inputs
  * give the same bits.  A weight is as right as its lse (see the gradients).
  * Skipped: slots outside [0, slots), rows outside [0, src_rows), queries
- * before the slot's first token, rows whose lse is not finite; a key that is not
- * finite gathers nothing.  Tokens that no
- * query attends and those whose entry names no page keep what they have.
+ * before the slot's first token, rows whose lse is not finite; a head's key that
+ * is not finite gathers nothing from that head's queries.  Tokens that no query
+ * attends and those whose entry names no page keep what they have.
  * T_tot and max_pages x page_size must be below 2^29, N below 2^23
  * (KDA_ERR_UNSUPPORTED otherwise).
  */

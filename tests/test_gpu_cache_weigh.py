@@ -206,6 +206,20 @@ def test_broken_rows_and_keys(K, counts, dtype):
     R.check("weights", got, want, bound + 1e-30)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_broken_head_of_a_key(K, dtype):
+    """A key that is not finite in one head still gathers what the other heads'
+    queries give, also where one workgroup takes all heads of a tile."""
+    x = _setup(43, [600] + [0] * 299, [160] + [0] * 299, 128, 2, 16, 16, TYPES[dtype])
+    slot, place, page = int(x["rows"][0]), 35, 16
+    x["kc"][int(x["table"][slot, place // page]), 1, place % page, 7] = math.nan
+    x["lse"][x["pick_list"], 64:] = math.nan
+    want, bound = _want(x, 0, 0)
+    got = _call(K, x)
+    assert float(want[slot, place] - x["weights"][slot, place]) > 8 * float(bound[slot, place])
+    R.check("weights", got, want, bound + 1e-30)
+
+
 def test_lengths_past_the_table(K):
     x = _setup(6, [64, 32], [2, 3], 2, 2, 64, 16, torch.float32, width=4)
     want = _call(K, x)
