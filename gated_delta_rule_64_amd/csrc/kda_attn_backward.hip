@@ -722,6 +722,30 @@ FarPlan far_plan(int64_t T, int64_t N, int Hkv, int window, int sinks, int near_
 
 size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
+// How a call is cut, and where its workspace holds what: the launch and the
+// queries all go by this one.  A window and first tokens of more than there are
+// tokens count as that many, so that calls of the same view have the same plan.
+struct BwdPlan {
+    int window, sinks;
+    BwdParts parts;
+    FarPlan far;
+    size_t dog, part, q_part, far_sums, bytes;  // (the statistics come first)
+};
+BwdPlan bwd_plan(int64_t T, int N, int H, int Hkv, int dk, int dv, DT x, bool gate, int window, int sinks) {
+    BwdPlan p;
+    p.window = static_cast<int>(window < T ? window : T);
+    p.sinks = static_cast<int>(sinks < T ? sinks : T);
+    p.parts = bwd_parts(T, N, H, Hkv, x, p.window);
+    p.far = far_plan(T, N, Hkv, p.window, p.sinks, p.parts.key);
+    const size_t rows = static_cast<size_t>(T) * H, kv = static_cast<size_t>(Hkv) * (dk + dv) * 4;
+    p.dog = up256(rows * 8);
+    p.part = p.dog + (gate ? up256(rows * dv * (x == DT::BF16 ? 2 : 4)) : 0);
+    p.q_part = p.part + (p.parts.key > 1 ? up256(p.parts.key * T * kv) : 0);
+    p.far_sums = p.q_part + (p.parts.query > 1 ? up256(p.parts.query * rows * dk * 4) : 0);
+    p.bytes = p.far_sums + (p.far.parts > 0 ? up256((1 + p.far.parts) * p.far.rows(p.sinks) * kv) : 0);
+    return p;
+}
+
 template <typename F>
 hipError_t allow_lds(F fn, int lds) {
     if (lds <= 64 * 1024) return hipSuccess;
@@ -735,26 +759,21 @@ hipError_t launch_bwd(const AttnBackwardArgs& a, hipStream_t s) {
     k.T = f.T; k.H = f.H; k.Hkv = f.Hkv; k.N = f.N; k.cu = f.cu;
     k.q = f.q; k.k = f.k; k.v = f.v; k.z = f.z; k.out = f.out; k.dy = a.dy; k.lse = f.lse;
     k.dq = a.dq; k.dk = a.dk; k.dv = a.dv; k.dz = a.dz; k.scale = f.scale;
-    k.window = static_cast<int>(f.window < f.T ? f.window : f.T);
-    k.sinks = static_cast<int>(f.sinks < f.T ? f.sinks : f.T);
+    const BwdPlan p = bwd_plan(f.T, f.N, f.H, f.Hkv, DK, DV, f.x, f.z != nullptr, f.window, f.sinks);
+    k.window = p.window;
+    k.sinks = p.sinks;
     char* ws = static_cast<char*>(a.ws);
     k.stats = reinterpret_cast<float2*>(ws);
-    ws += up256(static_cast<size_t>(f.T) * f.H * 8);
-    k.dog = f.z != nullptr ? static_cast<void*>(ws) : const_cast<void*>(a.dy);
-    if (f.z != nullptr) ws += up256(static_cast<size_t>(f.T) * f.H * DV * sizeof(T));
-    const BwdParts parts = bwd_parts(f.T, f.N, f.H, f.Hkv, f.x, f.window);
-    k.parts = parts.key;
-    k.q_parts = parts.query;
-    k.part = reinterpret_cast<float*>(ws);
-    if (k.parts > 1) ws += up256(static_cast<size_t>(k.parts) * f.T * f.Hkv * (DK + DV) * 4);
-    k.q_part = reinterpret_cast<float*>(ws);
-    if (k.q_parts > 1) ws += up256(static_cast<size_t>(k.q_parts) * f.T * f.H * DK * 4);
+    k.dog = f.z != nullptr ? static_cast<void*>(ws + p.dog) : const_cast<void*>(a.dy);
+    k.parts = p.parts.key;
+    k.q_parts = p.parts.query;
+    k.part = reinterpret_cast<float*>(ws + p.part);
+    k.q_part = reinterpret_cast<float*>(ws + p.q_part);
     if constexpr (kWin) {
-        const FarPlan far = far_plan(f.T, f.N, f.Hkv, k.window, k.sinks, k.parts);
-        k.far_buckets = far.buckets;
-        k.far_tiles = far.tiles;
-        k.far_parts = far.parts;
-        k.far = reinterpret_cast<float*>(ws);
+        k.far_buckets = p.far.buckets;
+        k.far_tiles = p.far.tiles;
+        k.far_parts = p.far.parts;
+        k.far = reinterpret_cast<float*>(ws + p.far_sums);
     }
     constexpr int lds = DqSizes<T, DK, DV>::kLds > DkvSizes<T, DK, DV>::kLds ? DqSizes<T, DK, DV>::kLds : DkvSizes<T, DK, DV>::kLds;
     hipError_t e = allow_lds(attn_bwd_kernel<T, DK, DV, kWin, kTileRows>, lds);
@@ -796,13 +815,7 @@ hipError_t launch_bwd(const AttnBackwardArgs& a, hipStream_t s) {
 }  // namespace
 
 size_t attn_backward_workspace_bytes(int64_t T, int N, int H, int Hkv, int dk, int dv, DT x, bool gate, int window, int sinks) {
-    const size_t rows = static_cast<size_t>(T) * H;
-    const BwdParts parts = bwd_parts(T, N, H, Hkv, x, window);
-    const FarPlan far = far_plan(T, N, Hkv, window, sinks, parts.key);
-    return up256(rows * 8) + (gate ? up256(rows * dv * (x == DT::BF16 ? 2 : 4)) : 0) +
-           (parts.key > 1 ? up256(static_cast<size_t>(parts.key) * T * Hkv * (dk + dv) * 4) : 0) +
-           (parts.query > 1 ? up256(static_cast<size_t>(parts.query) * rows * dk * 4) : 0) +
-           (far.parts > 0 ? up256(static_cast<size_t>(1 + far.parts) * far.rows(sinks) * Hkv * (dk + dv) * 4) : 0);
+    return bwd_plan(T, N, H, Hkv, dk, dv, x, gate, window, sinks).bytes;
 }
 
 // More tokens have fewer parts, so what a call needs does not rise with its
@@ -810,16 +823,19 @@ size_t attn_backward_workspace_bytes(int64_t T, int N, int H, int Hkv, int dk, i
 // fewest tiles and so the most parts; of the lengths of as many tiles, of 32 rows
 // or 128, the longest needs the most; from kKeyWant tiles on
 // there is one part.  The far sums' parts fall as their rows rise: p parts of r
-// rows are at most kMostFarParts r and at most kFarRows or r.
+// rows are at most kMostFarParts r and at most kFarRows or r.  Of more first
+// tokens than a tile's reach, the call of just that many tokens alone has far
+// sums, in one part.
 size_t attn_backward_max_workspace_bytes(int64_t T, int H, int Hkv, int dk, int dv, DT x, bool gate, int window, int sinks) {
     size_t most = attn_backward_workspace_bytes(T, 1, H, Hkv, dk, dv, x, gate, window, 0);
     for (int64_t t = 31; t < T && t < static_cast<int64_t>(kKeyWant) * kRows; t += 32) {
         const size_t need = attn_backward_workspace_bytes(t, 1, H, Hkv, dk, dv, x, gate, window, 0);
         most = need > most ? need : most;
     }
-    const FarPlan far = far_plan(T, T, Hkv, window, sinks, 1);
-    if (far.parts == 0) return most;
-    const int64_t rows = far.rows(sinks), parts = rows > kFarRows ? rows : rows * kMostFarParts < kFarRows ? rows * kMostFarParts : kFarRows;
+    const int64_t reach = static_cast<int64_t>(window) + kRows;
+    if (window < 1 || sinks < 1 || T < reach) return most;
+    const int64_t rows = sinks > reach ? reach : T / reach * sinks;
+    const int64_t parts = sinks > reach || rows > kFarRows ? rows : rows * kMostFarParts < kFarRows ? rows * kMostFarParts : kFarRows;
     return most + up256(static_cast<size_t>(rows + parts) * Hkv * (dk + dv) * 4);
 }
 

@@ -111,6 +111,25 @@ def test_first_tokens_of_many_long_sequences(K, window, sinks, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("H,Hkv", [(2, 2), (4, 1)])
+@pytest.mark.parametrize("lens,window,sinks", [([161], 33, 162), ([129], 1, 1000), ([0, 161, 0], 33, 2 ** 31 - 1), ([161], 33, 161), ([192], 64, 193),
+                                               ([225], 97, 226), ([162], 33, 162), ([160], 33, 162), ([70, 91], 33, 162)])
+def test_more_first_tokens_than_tokens(K, lens, window, sinks, H, Hkv, dtype):
+    """At the lengths at which first tokens begin to have far queries.  What is
+    around a workspace of just the size asked for stays as it was."""
+    print(f"first tokens {lens} {window} {sinks} {H}/{Hkv} {dtype}", flush=True)
+    x = _inputs(window + sum(lens), lens, H, Hkv, 64, 64, TYPES[dtype], False)
+    out, lse, g = _check(K, x, lens, window, sinks, TYPES[dtype])
+    need = K.kda_attn_window_backward_workspace_bytes(sum(lens), len(lens), H, Hkv, 64, 64, TYPES[dtype], False, window, sinks)
+    around = 1 << 20
+    room = torch.full((need + 2 * around,), 0xa5, dtype=torch.uint8, device="cuda")
+    got = _backward(K, x, lens, window, sinks, out, lse, workspace=room[around:around + need])
+    torch.cuda.synchronize()
+    assert bool((room[:around] == 0xa5).all()) and bool((room[around + need:] == 0xa5).all())
+    assert all(torch.equal(got[n], g[n]) for n in ("dq", "dk", "dv"))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_first_tokens_of_long_sequences_among_many_short_ones(K, dtype):
     """More sequences than could have far queries."""
     reach = 40 + 128

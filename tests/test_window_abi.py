@@ -182,6 +182,26 @@ def test_workspaces_of_gradients(T, window, sinks, H, Hkv, dk, dv, x, gate):
     assert T == 0 or most > 0
 
 
+@pytest.mark.parametrize("H,Hkv,dk,dv,x,gate", [(8, 2, 128, 128, F32, 0), (4, 1, 128, 128, BF16, 1), (32, 8, 16, 16, BF16, 0), (2, 2, 192, 128, F32, 1)])
+@pytest.mark.parametrize("window", [1, 2, 33, 64, 65, 512, 513])
+def test_first_tokens_past_the_sequences_end(window, H, Hkv, dk, dv, x, gate):
+    """More first tokens than there are, and a window of more, are the call of
+    just as many: it needs as much, also at the lengths at which first tokens begin
+    to have queries that are worked on apart."""
+    reach = window + 128
+    need = lambda t, n, w, s: kda.kda_attn_window_backward_workspace_bytes(t, n, H, Hkv, dk, dv, x, gate, w, s)  # noqa: E731
+    for T in (window - 1, window, window + 1, reach - 1, reach, reach + 1, 2 * reach):
+        if T == 0:
+            continue
+        for sinks in (T - 1, T, T + 1, reach - 1, reach, reach + 1, T + 200, 2 ** 31 - 1):
+            for N in (1, 2, 5):
+                assert need(T, N, window, sinks) == need(T, N, min(window, T), min(sinks, T)), (T, N, sinks)
+    for sinks in range(reach - 2, reach + 203, 3):
+        for T in (reach - 1, reach, reach + 1, 2 * reach):
+            most = kda.kda_attn_window_backward_max_workspace_bytes(T, H, Hkv, dk, dv, x, gate, window, sinks)
+            assert max(need(t, n, window, sinks) for t in range(1, T + 1) for n in (1, 3)) <= most, (T, sinks)
+
+
 @pytest.mark.parametrize("H,Hkv", [(32, 8), (1, 1), (64, 1)])
 def test_workspaces_of_weights(H, Hkv):
     """(1,024 + N) KiB hold every call of N sequences."""
