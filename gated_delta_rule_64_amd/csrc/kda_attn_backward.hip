@@ -700,16 +700,23 @@ BwdParts bwd_parts(int64_t T, int N, int H, int Hkv, DT x, int window) {
 // sums stay few (kFarRows rows of all heads).
 constexpr int kMostFarParts = 64;
 constexpr int64_t kFarRows = 16384, kFarGroups = 65536;
+// Rows whose sums one launch adds, four channels a thread: below 2^32 threads.
+// Calls of more (first tokens of a tile's reach in millions of tokens, whose tiles
+// are many) are balanced as they are too.
+int64_t most_far_rows(int Hkv, int width) { return ((int64_t(1) << 32) - kThreads) / (static_cast<int64_t>(Hkv) * (width / 4)); }
 struct FarPlan {
     int64_t buckets = 0;
     int tiles = 0, parts = 0;
     int64_t rows(int sinks) const { return buckets * sinks; }
 };
-FarPlan far_plan(int64_t T, int64_t N, int Hkv, int window, int sinks, int near_parts) {
+// width: channels of a key and a value.
+FarPlan far_plan(int64_t T, int64_t N, int Hkv, int width, int window, int sinks, int near_parts) {
     FarPlan p;
     const int64_t reach = static_cast<int64_t>(window) + kRows;
     if (window < 1 || sinks < 1 || sinks > reach || T < reach) return p;
-    p.buckets = T / reach < N ? T / reach : N;
+    const int64_t buckets = T / reach < N ? T / reach : N;
+    if (buckets * sinks > most_far_rows(Hkv, width)) return p;
+    p.buckets = buckets;
     p.tiles = (sinks + kRows - 1) / kRows;
     int64_t parts = ((T - reach) * near_parts + reach - 1) / reach;
     const int64_t groups = p.buckets * p.tiles * Hkv, rows = p.rows(sinks);
@@ -736,7 +743,7 @@ BwdPlan bwd_plan(int64_t T, int N, int H, int Hkv, int dk, int dv, DT x, bool ga
     p.window = static_cast<int>(window < T ? window : T);
     p.sinks = static_cast<int>(sinks < T ? sinks : T);
     p.parts = bwd_parts(T, N, H, Hkv, x, p.window);
-    p.far = far_plan(T, N, Hkv, p.window, p.sinks, p.parts.key);
+    p.far = far_plan(T, N, Hkv, dk + dv, p.window, p.sinks, p.parts.key);
     const size_t rows = static_cast<size_t>(T) * H, kv = static_cast<size_t>(Hkv) * (dk + dv) * 4;
     p.dog = up256(rows * 8);
     p.part = p.dog + (gate ? up256(rows * dv * (x == DT::BF16 ? 2 : 4)) : 0);
@@ -834,7 +841,8 @@ size_t attn_backward_max_workspace_bytes(int64_t T, int H, int Hkv, int dk, int 
     }
     const int64_t reach = static_cast<int64_t>(window) + kRows;
     if (window < 1 || sinks < 1 || T < reach) return most;
-    const int64_t rows = sinks > reach ? reach : T / reach * sinks;
+    int64_t rows = sinks > reach ? reach : T / reach * sinks;
+    if (rows > most_far_rows(Hkv, dk + dv)) rows = most_far_rows(Hkv, dk + dv);
     const int64_t parts = sinks > reach || rows > kFarRows ? rows : rows * kMostFarParts < kFarRows ? rows * kMostFarParts : kFarRows;
     return most + up256(static_cast<size_t>(rows + parts) * Hkv * (dk + dv) * 4);
 }

@@ -202,6 +202,24 @@ def test_first_tokens_past_the_sequences_end(window, H, Hkv, dk, dv, x, gate):
             assert max(need(t, n, window, sinks) for t in range(1, T + 1) for n in (1, 3)) <= most, (T, sinks)
 
 
+def test_far_sums_of_more_threads_than_a_launch_takes():
+    """2^32 threads and more are no launch: such a call, allowed by its limits, goes
+    without sums of far queries, and the largest workspace holds the calls below."""
+    window, sinks = 10000, 10000
+    for H, Hkv, dk, dv in ((32, 32, 128, 128), (32, 32, 192, 128), (64, 32, 128, 128)):
+        need = lambda t, n, s: kda.kda_attn_window_backward_workspace_bytes(t, n, H, Hkv, dk, dv, BF16, 0, window, s)  # noqa: E731
+        reach, width = window + 128, Hkv * (dk + dv)
+        most = (2**32 - 256) // (width // 4) // sinks  # sequences whose sums are few enough
+        T = (2**28 - 1) // H
+        assert T // reach > most
+        for n in (most + 1, T // reach, 2 * T // reach):
+            assert need(T, n, sinks) == need(T, n, 0), n
+        sums = need(T, most, sinks) - need(T, most, 0)
+        assert sums == 2 * most * sinks * width * 4
+        top = kda.kda_attn_window_backward_max_workspace_bytes(T, H, Hkv, dk, dv, BF16, 0, window, sinks)
+        assert max(need(t, n, sinks) for t in (T, T // 2, (most + 1) * reach - 1) for n in (1, most, most + 1, T // reach)) <= top
+
+
 @pytest.mark.parametrize("H,Hkv", [(32, 8), (1, 1), (64, 1)])
 def test_workspaces_of_weights(H, Hkv):
     """(1,024 + N) KiB hold every call of N sequences."""
