@@ -367,6 +367,7 @@ __global__ __launch_bounds__(kThreads, (DK * sizeof(T) <= 256 ? 2 : 1)) void cac
             u32x4 q[kEach];
             float of[kEach], lse;  // the lse of the pieces' rows, and of row `col`
             bool there;            // row `col` is one
+            uint32_t named;        // of the pieces' rows, a bit each
         };
         // (behind the last step it reads nothing, but in no branch: a wait for the
         // step before would be one for this one too)
@@ -385,15 +386,21 @@ __global__ __launch_bounds__(kThreads, (DK * sizeof(T) <= 256 ? 2 : 1)) void cac
                     }
                 x.lse = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(l, col * a.H * 4, 0, 0));
                 x.there = col < here;
+                x.named = ~0u;
             } else {
-                auto row_at = [&](int i) {  // query i's row in q and lse; the first one of the tensor for none
+                // query i's row in q and lse; the tensor's first one for none, which is not to be looked at
+                auto row_at = [&](int i, bool& named) {
                     const int64_t r = i < here ? a.rows[w.first + f_i + i] : -1;
-                    return (r >= 0 && r < a.src_rows ? r : 0) * a.H + min(f_head, a.H - 1);
+                    named = r >= 0 && r < a.src_rows;
+                    return (named ? r : 0) * a.H + min(f_head, a.H - 1);
                 };
+                x.named = 0;
 #pragma unroll
                 for (int i = 0; i < kEach; ++i)
                     if (kFull || tid + i * kThreads < kPiecesOfStep) {
-                        const int64_t r = row_at(row_in[i]);
+                        bool named;
+                        const int64_t r = row_at(row_in[i], named);
+                        x.named |= static_cast<uint32_t>(named) << i;
                         x.q[i] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(a.q) + r * kRow + piece_in[i] * 16);
                         x.of[i] = a.lse[r];
                     }
@@ -412,7 +419,7 @@ __global__ __launch_bounds__(kThreads, (DK * sizeof(T) <= 256 ? 2 : 1)) void cac
 #pragma unroll
             for (int i = 0; i < kEach; ++i)
                 if (kFull || tid + i * kThreads < kPiecesOfStep)
-                    *reinterpret_cast<u32x4*>(buf + put_at[i]) = fabsf(x.of[i]) < INFINITY ? x.q[i] : u32x4{};
+                    *reinterpret_cast<u32x4*>(buf + put_at[i]) = (x.named >> i & 1) != 0 && fabsf(x.of[i]) < INFINITY ? x.q[i] : u32x4{};
             if (tid < kRows) reinterpret_cast<float*>(buf + Sz::kTile)[col] = x.there && fabsf(x.lse) < INFINITY ? x.lse * kLog2e : INFINITY;
         };
         auto work = [&](const char* sQ) __attribute__((always_inline)) {

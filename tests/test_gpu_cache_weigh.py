@@ -207,6 +207,32 @@ def test_broken_rows_and_keys(K, counts, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("counts", [[3, 2], [33, 70]])
+def test_rows_that_no_query_names(K, counts, dtype):
+    """What a source holds beside the queries (rows that no attention call wrote)
+    is nothing to them, nor to a row of the list that is not there."""
+    x = _setup(57, [200, 90], counts, 4, 2, 64, 16, TYPES[dtype], pick=True)
+    x["lse"][x["pick_list"][1]] = math.nan
+    rest = [r for r in range(x["q"].shape[0]) if r not in x["pick_list"]]
+    assert rest[0] < 3
+    order = [rest[0]] + [r for r in range(x["q"].shape[0]) if r != rest[0]]  # such a row is the first one
+    x["pick_list"] = [order.index(r) for r in x["pick_list"]]
+    x.update(q=x["q"][order].contiguous(), lse=x["lse"][order].contiguous(),
+             pick=torch.tensor(x["pick_list"], dtype=torch.int32, device="cuda"))
+    want = _check(K, x)
+    rest = [r for r in range(x["q"].shape[0]) if r not in x["pick_list"]]
+    assert rest[0] == 0
+    for value in (math.nan, math.inf, 1e30):
+        y = dict(x, q=x["q"].clone(), lse=x["lse"].clone())
+        y["q"][rest], y["lse"][rest] = value, 0.0
+        assert torch.equal(_call(K, y), want), value
+        for bad in (-1, x["q"].shape[0]):
+            y["pick"] = x["pick"].clone()
+            y["pick"][1] = bad
+            assert torch.equal(_call(K, y), want), (value, bad)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_broken_head_of_a_key(K, dtype):
     """A key that is not finite in one head still gathers what the other heads'
     queries give, also where one workgroup takes all heads of a tile."""
