@@ -32,8 +32,8 @@ struct EvictK {
 
 __device__ __forceinline__ bool names_page(int32_t e, int pages) { return e >= 0 && e < pages; }
 
-// A barrier behind loads whose places other threads write after it, or behind
-// stores that they read: every wave waits until its own are done.
+// A barrier behind loads whose places other threads write after it: every wave
+// waits until its own are done.
 __device__ __forceinline__ void done_barrier() {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
@@ -228,7 +228,7 @@ __global__ __launch_bounds__(kPlan) void cache_evict_plan_kernel(EvictK k) {
             if (p != d && (x == 0 || stay[x - 1] == d - 1)) atomicMin(&s_first, d);
         }
     }
-    done_barrier();  // the list is read by other threads
+    __syncthreads();  // s_first is whole (the list is for the next launch)
     const int d0 = s_first;
     // A page that is written must be this slot's alone, and so must a partly
     // filled last one, which the slot's next tokens are written to.
