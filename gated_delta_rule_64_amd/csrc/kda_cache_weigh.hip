@@ -83,11 +83,12 @@ __device__ __forceinline__ float* weight_of(const WeighK& k, const Weighed& w, i
     return k.a.weights + ((static_cast<int64_t>(w.slot) * k.c.max_pages) << k.c.page_shift) + pos;
 }
 
-// What a key has gathered: a sum that is NaN comes from a head's key that is not
-// finite.  A row that attends such a key has an lse that is not finite (and
-// weighs nothing) or no weight there.  Where many queries are, whose broken rows
-// read as 0, it is taken for a step of one head, so that the others' stay.
-__device__ __forceinline__ float gathered(float x) { return x == x ? x : 0.f; }
+// What a key gathers: weights, or sums of one head's, that are NaN or infinite come
+// from that head's key not being finite.  A row that attends such a key has an lse
+// that is not finite (and weighs nothing) or no weight there, unless its lse is of
+// a window that the key is not in.  Where many queries are, whose broken rows read
+// as 0, it is taken for a step of one head, so that the others' stay.
+__device__ __forceinline__ float gathered(float x) { return x < INFINITY ? x : 0.f; }
 
 template <typename T, int DK>
 struct FewSizes {
@@ -205,9 +206,9 @@ __global__ __launch_bounds__(kThreads, (DK * sizeof(T) <= 256 ? 3 : 1)) void cac
 #pragma unroll
             for (int p = 0; p < kPieces; ++p) s = mma<T>(rk.rows(sK, p), rq.rows(at, p), s);
             const bool good = on && fabsf(lse) < INFINITY;  // a row that attends nothing, or a broken one, weighs nothing
-            const float lse2 = lse * kLog2e;
+            const float lse2 = good ? lse * kLog2e : INFINITY;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[i] = good ? __builtin_amdgcn_exp2f(fmaf(s[i], sc, -lse2)) : 0.f;
+            for (int i = 0; i < 16; ++i) s[i] = gathered(__builtin_amdgcn_exp2f(fmaf(s[i], sc, -lse2)));
             if (first + kKeys - 1 > w.p_first || (a.window > 0 && first < w.ctx - a.window && first + kKeys > tiles.sinks)) {
                 const int most = opaque(p_here - first - 4 * half);
                 const int least = opaque(a.window > 0 ? p_here - a.window + 1 - first - 4 * half : INT32_MIN / 2);
@@ -238,7 +239,7 @@ __global__ __launch_bounds__(kThreads, (DK * sizeof(T) <= 256 ? 3 : 1)) void cac
             if (mine(x)) {
                 float v = 0.f;
                 for (int m = 0; m < share; ++m) v += sums[wave + m][col];
-                *weight_of(k, w, first + col) = had + gathered(v);
+                *weight_of(k, w, first + col) = had + v;
             }
             if (share > 1) __syncthreads();
             else wave_lds_fence();

@@ -246,6 +246,26 @@ def test_broken_head_of_a_key(K, dtype):
     R.check("weights", got, want, bound + 1e-30)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("counts", [[1, 2], [90, 33]])
+def test_broken_key_that_no_lse_knows_of(K, counts, dtype):
+    """Weighed without the window that their lse is of, queries meet a key that is
+    not finite: it gathers nothing of that head, and all that the others give."""
+    x = _setup(47, [300, 64], counts, 8, 2, 64, 16, TYPES[dtype], window=40)
+    slot, place, page = int(x["rows"][0]), 35, 16
+    at = int(x["table"][slot, place // page]), 1, place % page, 7
+    want, bound = _want(x, 0, 0)
+    y = dict(x, lse=x["lse"].clone())
+    y["lse"][:, 4:] = math.nan
+    others, near = _want(y, 0, 0)
+    want[slot, place], bound[slot, place] = others[slot, place], near[slot, place]
+    assert float(others[slot, place] - x["weights"][slot, place]) > 8 * float(near[slot, place])
+    for value in (math.nan, math.inf, -math.inf):
+        y = dict(x, kc=x["kc"].clone())
+        y["kc"][at] = value
+        R.check(f"weights {value}", _call(K, y), want, bound + 1e-30)
+
+
 def test_lengths_past_the_table(K):
     x = _setup(6, [64, 32], [2, 3], 2, 2, 64, 16, torch.float32, width=4)
     want = _call(K, x)
