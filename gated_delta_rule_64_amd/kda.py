@@ -667,7 +667,8 @@ def kda_cache_weigh(q, lse, k_cache, page_table, lens, weights, cu_seqlens=None,
     queries cu_seqlens[n] .. cu_seqlens[n+1] - 1 of q [R,H,dk] and lse fp32
     [R,H] (query t is row ``rows[t]``; None: row t) are the last tokens that
     lens counts of slot ``slot_indices[n]`` (None: n).  ``window`` 0: a query
-    attends every token up to its own."""
+    attends every token up to its own.  Decode steps and prompts are faster in
+    calls of their own."""
     R, H, dk = q.shape
     pages, Hkv, page, _ = k_cache.shape
     slots, width = page_table.shape

@@ -750,7 +750,11 @@ int kda_cache_copy(void* pool, int64_t row_bytes, int32_t rows,
  * stands at place p = lens[slot] - c + i and attends the places j <= p, with
  * window > 0 those with p - j < window or j < sinks.  So one call serves a
  * decode step, the accepted path of each draft tree (rows: b * T + the path's
- * tokens, in order), the last tokens of a prompt or all of it.
+ * tokens, in order), the last tokens of a prompt or all of it.  A call takes one
+ * of two forms by the average, T_tot (H / Hkv) / N rows of a key head up to 32 or
+ * above.  Either is right for any batch, but a prompt beside decode steps belongs
+ * in a call of its own: 300 steps and 2,000 tokens of a prompt take 10 ms in one
+ * call and 0.3 ms in two.
  * Arguments:
  *   q [src_rows, H, dk], lse fp32 [src_rows, H]: the queries and what the
  *                 attention call gave for them; rows int32 [T_tot] or NULL
