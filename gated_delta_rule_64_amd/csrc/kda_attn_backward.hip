@@ -22,10 +22,10 @@
 // queries of 32 rows of four heads share a workgroup where the group allows it.
 // What later queries give to the first tokens is summed apart (far queries,
 // below), else the first tile would be as long as the sequence: 8,192 tokens
-// under a window of 1,024, 849 us with it in one piece, 517 to 524 now (floor 233;
-// 620 TFLOP/s on five products, matrix cores 44 %, vector units 31 %, waits 38 %).
-// The six fp32 sequences under a window of 100: 61 us (49 of them the gradients,
-// matrix cores 25 %; chains of 3 to 5 steps of 4 us each and their starts).
+// under a window of 1,024, 849 us with it in one piece, 517 to 531 now (floor 233;
+// 610 to 625 TFLOP/s on five products, matrix cores 44 %, vector units 30 %, waits 38 %).
+// The six fp32 sequences under a window of 100: 60 us (47 of them the gradients,
+// matrix cores 26 %; chains of 3 to 5 steps of 4 us each and their starts).
 #include "kda_attn_common.h"
 #include "kda_internal.h"
 #include "kda_profile.h"

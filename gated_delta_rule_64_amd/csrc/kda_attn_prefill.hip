@@ -23,9 +23,9 @@
 // tiles: those of the first tokens, then those from the first row's window on;
 // only tiles at a window's start are masked.  Four heads of a group and 32 rows
 // of them share a workgroup where the group allows it, so that all its waves need
-// the same keys: 16,384 tokens under a window of 4,096, 1,050 to 980 us (floor
-// 693; 980 TFLOP/s of what is attended, 1,050 of what is formed).  The twelve
-// prompts under a window of 512: 238 us (floor 135, memory; matrix cores 26 %,
+// the same keys: 16,384 tokens under a window of 4,096, 1,050 to 980 us (by the
+// card 973 to 1,033, floor 693; 930 to 990 TFLOP/s of what is attended).  The twelve
+// prompts under a window of 512: 237 to 242 us (floor 135, memory; matrix cores 26 %,
 // vector units 38 %, waits 34 %): 18 tiles of 32 keys a workgroup do not cover
 // its queries, gate and results.  64 tokens: 9.5 us, the host's side of a call.
 #include "kda_attn_common.h"

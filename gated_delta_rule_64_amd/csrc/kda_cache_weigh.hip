@@ -13,9 +13,9 @@
 // sequence's own.
 //
 // bf16, 32 heads of 128 over 8: a decode step's 256 queries over 1,024 to 4,096
-// tokens each read 1.33 GB in 243 us (5.5 TB/s); all of a prompt of 8,000 tokens
-// 306 us (860 TFLOP/s of the 1,390 that a large product reaches; floor 189), the
-// last 64 tokens of 8 prompts 50 us (floor 14).
+// tokens each read 1.33 GB in 244 us (5.5 TB/s); all of a prompt of 8,000 tokens
+// 306 to 325 us by the card (810 to 860 TFLOP/s of the 1,390 that a large product
+// reaches; floor 189), the last 64 tokens of 8 prompts 50 us (floor 14).
 #include "kda_attn_common.h"
 #include "kda_internal.h"
 #include "kda_profile.h"
@@ -298,7 +298,7 @@ struct ManySizes {
 };
 
 // Many queries: bound by the products and exponentials (8,000 tokens: matrix cores
-// 34 % of the cycles, vector units 44 %, waits 21 %; a wave's step of 64 keys by 32
+// 34 % of the cycles, vector units 46 %, waits 24 %; a wave's step of 64 keys by 32
 // queries has 16 products of 32 cycles and 32 exponentials of 8, each with a
 // multiply-add and an addition of 4).  One workgroup per
 // (sequence, tile of keys, part): a wave's keys stay in its registers, the
@@ -306,7 +306,7 @@ struct ManySizes {
 // (a step is shorter than a load takes).  S = Q K^T, so that a lane holds one
 // key's scores and one sum.  The tile's work is the sequence of its steps, head
 // by head.
-// kPicked: the queries' rows are named by a list.
+// kPicked: the queries' rows are named by a list (64 of each of 8 prompts: 59 us).
 template <typename T, int DK, bool kPicked>
 __global__ __launch_bounds__(kThreads, (DK * sizeof(T) <= 256 ? 2 : 1)) void cache_weigh_many_kernel(WeighK k) {
     __shared__ __align__(16) char smem[2 * ManySizes<T, DK>::kBuf];
